@@ -22,6 +22,11 @@
  * moe_layer_forward runs all four on one stream; moe_prefill_forward_host
  * runs it over a sequence of chunks held in host memory.
  *
+ * Beside the routed experts stand the operators that feed the layer and join
+ * its result: moe_linear (router logits, dense projections, the residual
+ * add) and moe_route (logits to ids, w, counts and the balance and z losses),
+ * with their gradients moe_linear_grad and moe_route_grad.
+ *
  * Conventions shared by every call
  *  - Tensors are caller-owned DEVICE pointers, row-major and contiguous
  *    (moe_prefill_forward_host alone takes host buffers for x, ids, w, y).
@@ -71,9 +76,21 @@ extern "C" {
 struct CUstream_st;
 typedef struct CUstream_st *moe_stream_t;
 
-/* dtype of 16-bit activation rows */
+/* dtype of 16-bit activation rows; MOE_DT_F32 only where a call names it */
 #define MOE_DT_BF16 0
 #define MOE_DT_F16 1
+#define MOE_DT_F32 2
+
+/* activation of moe_linear */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2      /* z / (1 + e^-z) */
+#define MOE_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define MOE_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+
+/* score of moe_route */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
 
 /* return codes */
 #define MOE_OK 0
@@ -92,6 +109,8 @@ typedef struct CUstream_st *moe_stream_t;
                                      that expert was skipped by the FFN */
 #define MOE_STATUS_TIMEOUT 8u     /* a pipeline wait inside a GEMM ran out its
                                      time limit (about 2 s); the kernel stopped */
+#define MOE_STATUS_BAD_LOGIT 16u  /* a NaN or +inf logit of a token that takes part:
+                                     that expert was treated as closed (-inf) */
 
 /* limits */
 #define MOE_MAX_EXPERTS 4096
@@ -503,6 +522,116 @@ MOE_API int moe_read_status(const void *ws, moe_stream_t stream, uint32_t *statu
 MOE_API int moe_selftest_wait_limit(const void *xs, const void *Wg, const void *Wu,
                                     const int32_t *offsets, int E, int d, int f, int64_t cap,
                                     void *H, uint32_t *status, int cta, moe_stream_t stream);
+
+/*
+ * moe_linear -- a dense projection with bias, activation and residual.
+ *
+ *   z[t][n] = sum_i x[t][i] W[n][i] + bias[n]     (16-bit operands, fp32 sums)
+ *   y[t][n] = act(z[t][n]) + residual[t][n]       (fp32, rounded once to y's type)
+ *   pre[t][n] = z[t][n] in dtype                  (what the gradient needs)
+ * in   x         dtype [T, K], rows ldx elements apart
+ * in   W         dtype [N, K]  contiguous (each output feature's weights in a row)
+ * in   bias      fp32 [N] or NULL
+ * in   residual  y_dtype [T, N], rows ldr elements apart, or NULL
+ * out  pre       dtype [T, N] contiguous, or NULL
+ * out  y         y_dtype [T, N], rows ldy elements apart
+ * in   status    uint32* device word to OR MOE_STATUS_TIMEOUT into, or NULL
+ * dtype is MOE_DT_BF16 or MOE_DT_F16, y_dtype that same type or MOE_DT_F32.
+ * T >= 0, N >= 1 (any), K a positive multiple of 8; ldx >= K a multiple of 8;
+ * ldr, ldy >= N; T, K, N < 2^31.  x and W 16-byte aligned, the others aligned
+ * to their element.  residual may be y itself (same ldr and ldy): each element
+ * is read before it is written, by the same thread.  No other operands may
+ * overlap.  A fixed order of every sum: results are deterministic.
+ */
+MOE_API int moe_linear(const void *x, int64_t ldx, const void *W, const float *bias,
+                       const void *residual, int64_t ldr, int dtype, int act, int T, int K,
+                       int N, void *pre, void *y, int64_t ldy, int y_dtype, uint32_t *status,
+                       moe_stream_t stream);
+
+/*
+ * moe_linear_grad -- the gradients of moe_linear from dy (the residual's is
+ * dy itself).
+ *
+ *   dP[t][n] = dy[t][n] act'(pre[t][n])           (fp32)
+ *   dx[t][i] = sum_n dP[t][n] W[n][i]
+ *   dW[n][i] = sum_t dP[t][n] x[t][i]
+ *   db[n]    = sum_t dP[t][n]
+ * The two products take dP as an operand of type dtype: unless it is dy
+ * itself (act none, dy of type dtype) it is rounded to dtype once.  db is
+ * summed from the fp32 values.  relu'(0) = 0.
+ * in   x, W, pre as in moe_linear (pre may be NULL for MOE_ACT_NONE)
+ * in   dy        dy_dtype [T, N], rows lddy elements apart (dtype or MOE_DT_F32)
+ * out  dx        dtype [T, K] contiguous, or NULL
+ * out  dW        dw_dtype [N, K] contiguous, or NULL (dtype or MOE_DT_F32)
+ * out  db        fp32 [N], or NULL
+ * ws             moe_linear_grad_workspace_bytes(T, N) bytes, 256-byte aligned
+ * With T = 0, dW and db are zero.  W may be NULL without dx, x without dW.
+ */
+MOE_API size_t moe_linear_grad_workspace_bytes(int T, int N);
+MOE_API int moe_linear_grad(const void *x, int64_t ldx, const void *W, const void *pre,
+                            const void *dy, int64_t lddy, int dy_dtype, int dtype, int act, int T,
+                            int K, int N, void *dx, void *dW, int dw_dtype, float *db, void *ws,
+                            size_t ws_bytes, uint32_t *status, moe_stream_t stream);
+
+/*
+ * moe_route -- the router: logits to the top-k experts of each token, their
+ * weights, and (for the losses that balance the experts) per-expert counts,
+ * mean probabilities, the balance loss and the z loss.
+ *
+ * An expert is open to a token unless its logit is -inf (NaN and +inf logits
+ * are treated as -inf and set MOE_STATUS_BAD_LOGIT).  A token takes part if
+ * mask (when given) is nonzero for it and at least one expert is open; the
+ * logits of tokens with mask 0 are not looked at.  For a token with logits l,
+ * over its open experts:
+ *   score s_e = softmax(l)_e, or sigmoid(l_e)
+ *   p_e       = s_e / sum s          (the softmax itself; 0 for closed experts)
+ *   chosen    = the k open experts with the largest key, in descending order,
+ *               ties to the lowest id; key = l_e without bias (the same order
+ *               as s_e), s_e + bias[e] with it.  Slots left over (fewer than k
+ *               open experts, or a token that takes no part): id -1, weight 0.
+ *   w_j       = scale * s_j / (sum of s over the chosen)   (norm != 0)
+ *             = scale * s_j                                (norm == 0)
+ * and with n the number of tokens that take part, counts[e] the tokens that
+ * chose e and f_e = counts[e] / (n k):
+ *   prob[e]   = sum_t p_{t,e} / n
+ *   loss[0]   = E * sum_e f_e prob[e]             (balance)
+ *   loss[1]   = sum_t (log sum_e e^{l_{t,e}})^2 / n        (z)
+ * (0 when n = 0).
+ * in   logits  l_dtype [T, E], rows ld elements apart (any MOE_DT_*)
+ * in   bias    fp32 [E] or NULL (a selection bias: the weights do not see it)
+ * in   mask    uint8 [T] or NULL
+ * out  ids     int32 [T, k], w fp32 [T, k]      what moe_plan takes
+ * out  counts  int32 [E+1]  counts, then n; or NULL
+ * out  prob    fp32 [E] or NULL;  loss fp32 [2] or NULL
+ * ws           moe_route_workspace_bytes(T, E) bytes, 256-byte aligned; its
+ *              status word is set by every call (moe_read_status)
+ * T >= 0, 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E, MOE_MAX_TOPK), ld >= E,
+ * T*k < 2^31.  All sums in a fixed order: results are deterministic.
+ */
+MOE_API size_t moe_route_workspace_bytes(int T, int E);
+MOE_API int moe_route(const void *logits, int64_t ld, int l_dtype, const float *bias,
+                      const uint8_t *mask, int T, int E, int k, int score, int norm, float scale,
+                      int32_t *ids, float *w, int32_t *counts, float *prob, float *loss, void *ws,
+                      size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_route_grad -- gradient of moe_route's w and losses with respect to the
+ * logits (the choice of experts and the counts are constants, as usual).
+ *
+ *   G = sum dw_{t,j} w_{t,j} + dloss[0] loss[0] + dloss[1] loss[1]
+ *   dlogits[t][e] = dG / dl_{t,e}   (0 for closed experts and tokens that take no part)
+ * in   logits, mask, score, norm, scale  as given to moe_route
+ * in   ids     int32 [T, k] as moe_route wrote them (distinct within a token; a
+ *              slot whose id is outside [0, E) or closed has no weight)
+ * in   counts  int32 [E+1] from moe_route, or NULL (then dloss is not looked at)
+ * in   dw      fp32 [T, k] or NULL (zeros)
+ * in   dloss   fp32 [2] device memory, or NULL (zeros)
+ * out  dlogits l_dtype [T, E], rows ldd elements apart
+ */
+MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const uint8_t *mask,
+                           const int32_t *ids, const int32_t *counts, const float *dw,
+                           const float *dloss, int T, int E, int k, int score, int norm,
+                           float scale, void *dlogits, int64_t ldd, moe_stream_t stream);
 
 /* Human-readable text of a return code. */
 MOE_API const char *moe_status_str(int code);

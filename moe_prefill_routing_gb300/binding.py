@@ -23,7 +23,10 @@ MOE_OK = 0
 MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_CAPACITY, MOE_ERR_WORKSPACE = -1, -2, -3, -4
 MOE_ERR_ALIGN, MOE_ERR_CUDA, MOE_ERR_DTYPE = -5, -6, -7
 STATUS_BAD_ID, STATUS_OVERFLOW, STATUS_BAD_OFFSETS, STATUS_TIMEOUT = 1, 2, 4, 8
-DT_BF16, DT_F16 = 0, 1
+STATUS_BAD_LOGIT = 16
+DT_BF16, DT_F16, DT_F32 = 0, 1, 2
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
 WS_FIELDS = ["status", "bcnt", "offsets", "counts", "srt_tok", "srt_w", "pos", "tile_expert",
              "xs", "H", "Ys", "total"]
 
@@ -105,6 +108,23 @@ _SIGS = {
                                           C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int,
                                           C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_size_t,
                                           C.c_void_p]),
+    "moe_linear": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                             C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p,
+                             C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p]),
+    "moe_linear_grad_workspace_bytes": (C.c_size_t, [C.c_int] * 2),
+    "moe_linear_grad": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                  C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                                  C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
+                                  C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "moe_route_workspace_bytes": (C.c_size_t, [C.c_int] * 2),
+    "moe_route": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p, C.c_int,
+                            C.c_int, C.c_int, C.c_int, C.c_int, C.c_float, C.c_void_p,
+                            C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                            C.c_size_t, C.c_void_p]),
+    "moe_route_grad": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p,
+                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
+                                 C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_int64,
+                                 C.c_void_p]),
     "moe_read_status": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
     "moe_selftest_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                           C.c_int, C.c_int, C.c_int, C.c_int64, C.c_void_p,
@@ -575,6 +595,194 @@ def layer_forward_mxfp4(x, ids, w, Wg: Mxfp4, Wu: Mxfp4, Wd: Mxfp4, tm: int, y=N
                                            _ptr(y), _ptr(ws), ws.numel(), _stream(dev))
     _check("moe_layer_forward_mxfp4", rc)
     return y
+
+
+# ---- router and dense projections ------------------------------------------
+
+_DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
+
+
+def _dtype(t) -> int:
+    c = _DTYPES.get(t if isinstance(t, torch.dtype) else t.dtype)
+    if c is None:
+        raise ValueError(f"unsupported dtype {t if isinstance(t, torch.dtype) else t.dtype}")
+    return c
+
+
+def _rows(t, name: str, shape, dtypes) -> tuple:
+    """(address, elements between rows) of a 2-D tensor whose rows are
+    contiguous and may lie further apart than their length."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: unexpected dtype {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    if rows <= 1:
+        return t.data_ptr(), (cols + 7) // 8 * 8
+    return t.data_ptr(), t.stride(0)
+
+
+def _flat(t, name: str, shape, dtypes):
+    """Address of an optional contiguous tensor of the given shape and type."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: unexpected dtype {t.dtype}")
+    return _ptr(t)
+
+
+def _name(table: dict, key: str, what: str) -> int:
+    if key not in table:
+        raise ValueError(f"{what}: one of {', '.join(table)}; got {key!r}")
+    return table[key]
+
+
+_F32 = (torch.float32,)
+_F16S = (torch.bfloat16, torch.float16)
+
+
+def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pre=None, y=None,
+           status=None):
+    """moe_linear: y = act(x W^T + bias) + residual.
+
+    x [T, K] and W [N, K] of one 16-bit type, bias fp32 [N], residual and y
+    [T, N] of ``out_dtype`` (x's type by default, or float32); the rows of x,
+    residual and y may lie further apart than their length.  ``pre`` (an
+    output, x's type, [T, N]) receives x W^T + bias for ``linear_grad``.
+    ``residual`` may be ``y``."""
+    T, K = x.shape
+    N = W.shape[0]
+    if y is None:
+        y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
+    elif out_dtype is not None and y.dtype != out_dtype:
+        raise ValueError(f"y: expected {out_dtype}, got {y.dtype}")
+    xp, ldx = _rows(x, "x", (T, K), _F16S)
+    yp, ldy = _rows(y, "y", (T, N), (x.dtype, torch.float32))
+    rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", (T, N), (y.dtype,))
+    with torch.cuda.device(x.device):
+        rc = lib().moe_linear(xp, ldx, _flat(W, "W", (N, K), (x.dtype,)),
+                              _flat(bias, "bias", (N,), _F32), rp, ldr, _dtype(x),
+                              _name(ACTS, act, "act"), T, K, N,
+                              _flat(pre, "pre", (T, N), (x.dtype,)), yp, ldy, _dtype(y),
+                              _ptr(status), _stream(x.device))
+    _check("moe_linear", rc)
+    return y
+
+
+def linear_grad_workspace_bytes(T: int, N: int) -> int:
+    return int(lib().moe_linear_grad_workspace_bytes(T, N))
+
+
+def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), dw_dtype=None,
+                dx=None, dW=None, db=None, ws=None, status=None):
+    """moe_linear_grad: (dx, dW, db) from dy [T, N] (x's type or float32).
+
+    ``pre`` is what ``linear`` left there (not needed for act "none").
+    ``need`` says which of dx [T, K], dW [N, K] (``dw_dtype``: W's type or
+    float32) and db fp32 [N] to compute; the others come back as None."""
+    T, K = x.shape
+    N = W.shape[0]
+    dev = x.device
+    if need[0] and dx is None:
+        dx = torch.empty((T, K), dtype=x.dtype, device=dev)
+    if need[1] and dW is None:
+        dW = torch.empty((N, K), dtype=dw_dtype or x.dtype, device=dev)
+    if need[2] and db is None:
+        db = torch.empty(N, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty(linear_grad_workspace_bytes(T, N), dtype=torch.uint8, device=dev)
+    xp, ldx = _rows(x, "x", (T, K), _F16S)
+    dyp, lddy = _rows(dy, "dy", (T, N), (x.dtype, torch.float32))
+    if dW is not None and dw_dtype is not None and dW.dtype != dw_dtype:
+        raise ValueError(f"dW: expected {dw_dtype}, got {dW.dtype}")
+    with torch.cuda.device(dev):
+        rc = lib().moe_linear_grad(
+            xp, ldx, _flat(W, "W", (N, K), (x.dtype,)), _flat(pre, "pre", (T, N), (x.dtype,)),
+            dyp, lddy, _dtype(dy), _dtype(x), _name(ACTS, act, "act"), T, K, N,
+            _flat(dx, "dx", (T, K), (x.dtype,)),
+            _flat(dW, "dW", (N, K), (x.dtype, torch.float32)),
+            _dtype(x if dW is None else dW), _flat(db, "db", (N,), _F32), _ptr(ws), ws.numel(),
+            _ptr(status), _stream(dev))
+    _check("moe_linear_grad", rc)
+    return dx, dW, db
+
+
+def route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().moe_route_workspace_bytes(T, E))
+
+
+def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bool = True,
+          scale: float = 1.0, stats: bool = True, out: dict | None = None, ws=None) -> dict:
+    """moe_route: the top-k experts of each token from logits [T, E].
+
+    Returns ids int32 [T, k] and w fp32 [T, k] (what ``plan`` and
+    ``layer_forward`` take) and, with ``stats``, counts int32 [E+1] (the
+    last: tokens that take part), prob fp32 [E] and loss fp32 [2] (balance,
+    z); and the workspace ``ws`` (status word at byte 0).  bias fp32 [E] is
+    added to the scores for the choice alone; mask [T] (bool or uint8) is 0
+    for padding.  ``out`` may hold some of the outputs."""
+    T, E = logits.shape
+    dev = logits.device
+    o = dict(out or {})
+    if "ids" not in o:
+        o["ids"] = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if "w" not in o:
+        o["w"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+    if stats:
+        if "counts" not in o:
+            o["counts"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        if "prob" not in o:
+            o["prob"] = torch.empty(E, dtype=torch.float32, device=dev)
+        if "loss" not in o:
+            o["loss"] = torch.empty(2, dtype=torch.float32, device=dev)
+    o["ws"] = ws if ws is not None else torch.empty(route_workspace_bytes(T, E),
+                                                    dtype=torch.uint8, device=dev)
+    lp, ld = _rows(logits, "logits", (T, E), tuple(_DTYPES))
+    get = o.get if stats else (lambda n: None)
+    with torch.cuda.device(dev):
+        rc = lib().moe_route(lp, ld, _dtype(logits), _flat(bias, "bias", (E,), _F32),
+                             _flat(mask, "mask", (T,), (torch.bool, torch.uint8)), T, E, k,
+                             _name(SCORES, score, "score"), int(norm), scale,
+                             _flat(o["ids"], "ids", (T, k), (torch.int32,)),
+                             _flat(o["w"], "w", (T, k), _F32),
+                             _flat(get("counts"), "counts", (E + 1,), (torch.int32,)),
+                             _flat(get("prob"), "prob", (E,), _F32),
+                             _flat(get("loss"), "loss", (2,), _F32), _ptr(o["ws"]),
+                             o["ws"].numel(), _stream(dev))
+    _check("moe_route", rc)
+    return o
+
+
+def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: str = "softmax",
+               norm: bool = True, scale: float = 1.0, dlogits=None):
+    """moe_route_grad: the gradient with respect to the logits of
+    sum(dw * w) + dloss . loss, with ids and counts from ``route`` and its
+    mask, score, norm and scale.  dw fp32 [T, k], dloss fp32 [2] (a device
+    tensor); either may be None."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    dev = logits.device
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    lp, ld = _rows(logits, "logits", (T, E), tuple(_DTYPES))
+    dp, ldd = _rows(dlogits, "dlogits", (T, E), (logits.dtype,))
+    with torch.cuda.device(dev):
+        rc = lib().moe_route_grad(lp, ld, _dtype(logits),
+                                  _flat(mask, "mask", (T,), (torch.bool, torch.uint8)),
+                                  _flat(ids, "ids", (T, k), (torch.int32,)),
+                                  _flat(counts, "counts", (E + 1,), (torch.int32,)),
+                                  _flat(dw, "dw", (T, k), _F32),
+                                  _flat(dloss, "dloss", (2,), _F32), T, E, k,
+                                  _name(SCORES, score, "score"), int(norm), scale, dp, ldd,
+                                  _stream(dev))
+    _check("moe_route_grad", rc)
+    return dlogits
 
 
 def selftest_wait_limit(xs, Wg, Wu, offsets, cap: int, status, cta: int = 0, H=None):

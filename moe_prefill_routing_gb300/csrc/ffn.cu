@@ -60,10 +60,6 @@
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 namespace moe {
 namespace {
 
@@ -960,33 +956,17 @@ __global__ void __launch_bounds__(Cfg<WM>::kThreadsK, 1)
 
 // ---- host: tensor maps ------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-cudaError_t get_encoder()
-{
-    std::call_once(g_encode_once, [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    });
-    return g_encode ? cudaSuccess : cudaErrorNotSupported;
-}
-
 // bf16 (or, with `u8`, byte) tensor map, 128-byte swizzle unless `plain`;
 // dims innermost first.
 cudaError_t encode_bf16(CUtensorMap *m, const void *base, uint32_t rank, const cuuint64_t *dims,
                         const cuuint64_t *strides_bytes, const cuuint32_t *box, bool plain = false,
                         bool u8 = false)
 {
-    cudaError_t err = get_encoder();
-    if (err != cudaSuccess)
-        return err;
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode)
+        return cudaErrorNotSupported;
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = g_encode(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+    const CUresult r = encode(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                 rank, const_cast<void *>(base),
                                 dims, strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 plain ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,

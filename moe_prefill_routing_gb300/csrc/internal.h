@@ -1,6 +1,7 @@
 // Internal interface between the C ABI (api.cu) and the kernel files.
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -128,6 +129,9 @@ cudaError_t launch_ffn_down_mxfp4(const void *H, const uint8_t *Wd, const uint8_
 // Streaming multiprocessors of the current device (cached per device).
 int device_sm_count();
 
+// The driver's tensor-map encoder (null if the driver lacks it).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 // Raise a kernel's dynamic shared-memory limit once per device.
 cudaError_t ensure_smem_limit(const void *kernel, int slot, size_t bytes);
 
@@ -166,6 +170,8 @@ enum SmemSlot {
     kSlotDownNative,
     kSlotGateUpMx4,
     kSlotDownMx4,
+    kSlotLinear0,  // the dense products: forward, dx, dW
+    kSlotLinear2 = kSlotLinear0 + 2,
     kSlotCount
 };
 
