@@ -598,7 +598,7 @@ MOE_API int moe_linear_grad(const void *x, int64_t ldx, const void *W, const voi
  *   loss[1]   = sum_t (log sum_e e^{l_{t,e}})^2 / n        (z)
  * (0 when n = 0).
  * in   logits  l_dtype [T, E], rows ld elements apart (any MOE_DT_*)
- * in   bias    fp32 [E] or NULL (a selection bias: the weights do not see it)
+ * in   bias    fp32 [E], finite, or NULL (a selection bias: the weights do not see it)
  * in   mask    uint8 [T] or NULL
  * out  ids     int32 [T, k], w fp32 [T, k]      what moe_plan takes
  * out  counts  int32 [E+1]  counts, then n; or NULL
