@@ -626,7 +626,7 @@ MOE_API int moe_route(const void *logits, int64_t ld, int l_dtype, const float *
  * in   counts  int32 [E+1] from moe_route, or NULL (then dloss is not looked at)
  * in   dw      fp32 [T, k] or NULL (zeros)
  * in   dloss   fp32 [2] device memory, or NULL (zeros)
- * out  dlogits l_dtype [T, E], rows ldd elements apart
+ * out  dlogits l_dtype [T, E], rows ldd elements apart; may be logits itself (ldd = ld)
  */
 MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const uint8_t *mask,
                            const int32_t *ids, const int32_t *counts, const float *dw,

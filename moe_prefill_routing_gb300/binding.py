@@ -598,53 +598,66 @@ def layer_forward_mxfp4(x, ids, w, Wg: Mxfp4, Wu: Mxfp4, Wd: Mxfp4, tm: int, y=N
 
 
 # ---- router and dense projections ------------------------------------------
+#
+# Calls of a few microseconds on the GPU: the checks below are written to cost
+# well under a microsecond each, and outputs made here are not checked again.
 
 _DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
+_16 = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _dtype(t) -> int:
-    c = _DTYPES.get(t if isinstance(t, torch.dtype) else t.dtype)
-    if c is None:
-        raise ValueError(f"unsupported dtype {t if isinstance(t, torch.dtype) else t.dtype}")
-    return c
+def _launch(name: str, dev, *args):
+    """The library's entry point `name` with the device's current stream, the
+    device being current."""
+    fn = getattr(_lib or lib(), name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev.index))
+    if rc != MOE_OK:
+        raise MoeError(name, rc)
 
 
-def _rows(t, name: str, shape, dtypes) -> tuple:
-    """(address, elements between rows) of a 2-D tensor whose rows are
-    contiguous and may lie further apart than their length."""
-    if tuple(t.shape) != tuple(shape):
+def _refuse(t, name: str, shape, dtypes):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: unexpected dtype {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: expected contiguous rows")
-    if rows <= 1:
-        return t.data_ptr(), (cols + 7) // 8 * 8
-    return t.data_ptr(), t.stride(0)
+    raise ValueError(f"{name}: expected a contiguous tensor"
+                     if len(shape) < 2 else f"{name}: expected contiguous rows")
 
 
-def _flat(t, name: str, shape, dtypes):
-    """Address of an optional contiguous tensor of the given shape and type."""
+def _flat(t, name: str, shape, *dtypes):
+    """Address of a contiguous tensor of the given shape and type; None stays."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: unexpected dtype {t.dtype}")
-    return _ptr(t)
+    if (t.shape != shape or t.dtype not in dtypes or not t.is_cuda
+            or not t.is_contiguous()):
+        _refuse(t, name, shape, dtypes)
+    return t.data_ptr()
+
+
+def _ld(t, name: str, shape, dtypes) -> int:
+    """Elements between the rows of a 2-D tensor whose rows are contiguous and
+    may lie further apart than their length."""
+    if t.shape != shape or t.dtype not in dtypes or not t.is_cuda:
+        _refuse(t, name, shape, dtypes)
+    rows, cols = shape
+    step, one = t.stride()
+    if one != 1 and cols > 1:
+        _refuse(t, name, shape, dtypes)
+    return step if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _name(table: dict, key: str, what: str) -> int:
-    if key not in table:
+    c = table.get(key)
+    if c is None:
         raise ValueError(f"{what}: one of {', '.join(table)}; got {key!r}")
-    return table[key]
-
-
-_F32 = (torch.float32,)
-_F16S = (torch.bfloat16, torch.float16)
+    return c
 
 
 def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pre=None, y=None,
@@ -658,25 +671,29 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
     ``residual`` may be ``y``."""
     T, K = x.shape
     N = W.shape[0]
+    dt = x.dtype
+    dev = x.device
+    ldx = _ld(x, "x", (T, K), _16)
     if y is None:
-        y = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
+        y = torch.empty((T, N), dtype=out_dtype or dt, device=dev)
+        ldy = N
+        if y.dtype is not dt and y.dtype is not torch.float32:
+            raise ValueError(f"out_dtype: unexpected dtype {y.dtype}")
     elif out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"y: expected {out_dtype}, got {y.dtype}")
-    xp, ldx = _rows(x, "x", (T, K), _F16S)
-    yp, ldy = _rows(y, "y", (T, N), (x.dtype, torch.float32))
-    rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", (T, N), (y.dtype,))
-    with torch.cuda.device(x.device):
-        rc = lib().moe_linear(xp, ldx, _flat(W, "W", (N, K), (x.dtype,)),
-                              _flat(bias, "bias", (N,), _F32), rp, ldr, _dtype(x),
-                              _name(ACTS, act, "act"), T, K, N,
-                              _flat(pre, "pre", (T, N), (x.dtype,)), yp, ldy, _dtype(y),
-                              _ptr(status), _stream(x.device))
-    _check("moe_linear", rc)
+    else:
+        ldy = _ld(y, "y", (T, N), (dt, torch.float32))
+    ldr = 0 if residual is None else _ld(residual, "residual", (T, N), (y.dtype,))
+    _launch("moe_linear", dev, x.data_ptr(), ldx, _flat(W, "W", (N, K), dt),
+            _flat(bias, "bias", (N,), torch.float32),
+            None if residual is None else residual.data_ptr(), ldr, _16[dt],
+            _name(ACTS, act, "act"), T, K, N, _flat(pre, "pre", (T, N), dt), y.data_ptr(), ldy,
+            _DTYPES[y.dtype], _ptr(status))
     return y
 
 
 def linear_grad_workspace_bytes(T: int, N: int) -> int:
-    return int(lib().moe_linear_grad_workspace_bytes(T, N))
+    return int((_lib or lib()).moe_linear_grad_workspace_bytes(T, N))
 
 
 def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), dw_dtype=None,
@@ -685,36 +702,35 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
 
     ``pre`` is what ``linear`` left there (not needed for act "none").
     ``need`` says which of dx [T, K], dW [N, K] (``dw_dtype``: W's type or
-    float32) and db fp32 [N] to compute; the others come back as None."""
+    float32) and db fp32 [N] to compute; the others come back as None unless
+    they are passed in."""
     T, K = x.shape
     N = W.shape[0]
+    dt = x.dtype
     dev = x.device
+    ldx = _ld(x, "x", (T, K), _16)
+    lddy = _ld(dy, "dy", (T, N), (dt, torch.float32))
     if need[0] and dx is None:
-        dx = torch.empty((T, K), dtype=x.dtype, device=dev)
+        dx = torch.empty((T, K), dtype=dt, device=dev)
     if need[1] and dW is None:
-        dW = torch.empty((N, K), dtype=dw_dtype or x.dtype, device=dev)
+        dW = torch.empty((N, K), dtype=dw_dtype or dt, device=dev)
+    elif dW is not None and dw_dtype is not None and dW.dtype != dw_dtype:
+        raise ValueError(f"dW: expected {dw_dtype}, got {dW.dtype}")
     if need[2] and db is None:
         db = torch.empty(N, dtype=torch.float32, device=dev)
     if ws is None:
         ws = torch.empty(linear_grad_workspace_bytes(T, N), dtype=torch.uint8, device=dev)
-    xp, ldx = _rows(x, "x", (T, K), _F16S)
-    dyp, lddy = _rows(dy, "dy", (T, N), (x.dtype, torch.float32))
-    if dW is not None and dw_dtype is not None and dW.dtype != dw_dtype:
-        raise ValueError(f"dW: expected {dw_dtype}, got {dW.dtype}")
-    with torch.cuda.device(dev):
-        rc = lib().moe_linear_grad(
-            xp, ldx, _flat(W, "W", (N, K), (x.dtype,)), _flat(pre, "pre", (T, N), (x.dtype,)),
-            dyp, lddy, _dtype(dy), _dtype(x), _name(ACTS, act, "act"), T, K, N,
-            _flat(dx, "dx", (T, K), (x.dtype,)),
-            _flat(dW, "dW", (N, K), (x.dtype, torch.float32)),
-            _dtype(x if dW is None else dW), _flat(db, "db", (N,), _F32), _ptr(ws), ws.numel(),
-            _ptr(status), _stream(dev))
-    _check("moe_linear_grad", rc)
+    _launch("moe_linear_grad", dev, x.data_ptr(), ldx, _flat(W, "W", (N, K), dt),
+            _flat(pre, "pre", (T, N), dt), dy.data_ptr(), lddy, _DTYPES[dy.dtype], _16[dt],
+            _name(ACTS, act, "act"), T, K, N, _flat(dx, "dx", (T, K), dt),
+            _flat(dW, "dW", (N, K), dt, torch.float32),
+            _DTYPES[dt if dW is None else dW.dtype], _flat(db, "db", (N,), torch.float32),
+            _ptr(ws), ws.numel(), _ptr(status))
     return dx, dW, db
 
 
 def route_workspace_bytes(T: int, E: int) -> int:
-    return int(lib().moe_route_workspace_bytes(T, E))
+    return int((_lib or lib()).moe_route_workspace_bytes(T, E))
 
 
 def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bool = True,
@@ -729,33 +745,30 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
     for padding.  ``out`` may hold some of the outputs."""
     T, E = logits.shape
     dev = logits.device
-    o = dict(out or {})
-    if "ids" not in o:
-        o["ids"] = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if "w" not in o:
-        o["w"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ld = _ld(logits, "logits", (T, E), _DTYPES)
+    o = {} if out is None else dict(out)
+
+    def output(name, shape, dtype):
+        t = o.get(name)
+        if t is not None:
+            return _flat(t, name, shape, dtype)
+        t = o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        return t.data_ptr()
+
+    ids, w = output("ids", (T, k), torch.int32), output("w", (T, k), torch.float32)
+    counts = prob = loss = None
     if stats:
-        if "counts" not in o:
-            o["counts"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        if "prob" not in o:
-            o["prob"] = torch.empty(E, dtype=torch.float32, device=dev)
-        if "loss" not in o:
-            o["loss"] = torch.empty(2, dtype=torch.float32, device=dev)
-    o["ws"] = ws if ws is not None else torch.empty(route_workspace_bytes(T, E),
-                                                    dtype=torch.uint8, device=dev)
-    lp, ld = _rows(logits, "logits", (T, E), tuple(_DTYPES))
-    get = o.get if stats else (lambda n: None)
-    with torch.cuda.device(dev):
-        rc = lib().moe_route(lp, ld, _dtype(logits), _flat(bias, "bias", (E,), _F32),
-                             _flat(mask, "mask", (T,), (torch.bool, torch.uint8)), T, E, k,
-                             _name(SCORES, score, "score"), int(norm), scale,
-                             _flat(o["ids"], "ids", (T, k), (torch.int32,)),
-                             _flat(o["w"], "w", (T, k), _F32),
-                             _flat(get("counts"), "counts", (E + 1,), (torch.int32,)),
-                             _flat(get("prob"), "prob", (E,), _F32),
-                             _flat(get("loss"), "loss", (2,), _F32), _ptr(o["ws"]),
-                             o["ws"].numel(), _stream(dev))
-    _check("moe_route", rc)
+        counts = output("counts", (E + 1,), torch.int32)
+        prob = output("prob", (E,), torch.float32)
+        loss = output("loss", (2,), torch.float32)
+    if ws is None:
+        ws = torch.empty(route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+    o["ws"] = ws
+    _launch("moe_route", dev, logits.data_ptr(), ld, _DTYPES[logits.dtype],
+            _flat(bias, "bias", (E,), torch.float32),
+            _flat(mask, "mask", (T,), torch.bool, torch.uint8), T, E, k,
+            _name(SCORES, score, "score"), norm, scale, ids, w, counts, prob, loss, _ptr(ws),
+            ws.numel())
     return o
 
 
@@ -764,24 +777,23 @@ def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: 
     """moe_route_grad: the gradient with respect to the logits of
     sum(dw * w) + dloss . loss, with ids and counts from ``route`` and its
     mask, score, norm and scale.  dw fp32 [T, k], dloss fp32 [2] (a device
-    tensor); either may be None."""
+    tensor); either may be None.  ``dlogits`` may be ``logits``."""
     T, E = logits.shape
     k = ids.shape[1]
+    dt = logits.dtype
     dev = logits.device
+    ld = _ld(logits, "logits", (T, E), _DTYPES)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    lp, ld = _rows(logits, "logits", (T, E), tuple(_DTYPES))
-    dp, ldd = _rows(dlogits, "dlogits", (T, E), (logits.dtype,))
-    with torch.cuda.device(dev):
-        rc = lib().moe_route_grad(lp, ld, _dtype(logits),
-                                  _flat(mask, "mask", (T,), (torch.bool, torch.uint8)),
-                                  _flat(ids, "ids", (T, k), (torch.int32,)),
-                                  _flat(counts, "counts", (E + 1,), (torch.int32,)),
-                                  _flat(dw, "dw", (T, k), _F32),
-                                  _flat(dloss, "dloss", (2,), _F32), T, E, k,
-                                  _name(SCORES, score, "score"), int(norm), scale, dp, ldd,
-                                  _stream(dev))
-    _check("moe_route_grad", rc)
+        dlogits = torch.empty((T, E), dtype=dt, device=dev)
+        ldd = E
+    else:
+        ldd = _ld(dlogits, "dlogits", (T, E), (dt,))
+    _launch("moe_route_grad", dev, logits.data_ptr(), ld, _DTYPES[dt],
+            _flat(mask, "mask", (T,), torch.bool, torch.uint8),
+            _flat(ids, "ids", (T, k), torch.int32),
+            _flat(counts, "counts", (E + 1,), torch.int32),
+            _flat(dw, "dw", (T, k), torch.float32), _flat(dloss, "dloss", (2,), torch.float32),
+            T, E, k, _name(SCORES, score, "score"), norm, scale, dlogits.data_ptr(), ldd)
     return dlogits
 
 

@@ -172,6 +172,8 @@ enum SmemSlot {
     kSlotDownMx4,
     kSlotLinear0,  // the dense products: forward, dx, dW
     kSlotLinear2 = kSlotLinear0 + 2,
+    kSlotLinearPair0,  // the same on CTA pairs
+    kSlotLinearPair2 = kSlotLinearPair0 + 2,
     kSlotCount
 };
 

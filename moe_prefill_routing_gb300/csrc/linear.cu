@@ -26,6 +26,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -80,20 +81,44 @@ __device__ __forceinline__ float gelu_u(float z)
     return 0.7978845608028654f * (z + 0.044715f * z * z * z);
 }
 
-__device__ __forceinline__ float act_of(float z, int act)
+template <int ACT>
+__device__ __forceinline__ float act_t(float z)
+{
+    if constexpr (ACT == MOE_ACT_RELU)
+        return z < 0.0f ? 0.0f : z;  // a NaN stays one
+    else if constexpr (ACT == MOE_ACT_SILU)
+        return __fdividef(z, 1.0f + __expf(-z));
+    else if constexpr (ACT == MOE_ACT_GELU)
+        return 0.5f * z * erfcf(z * -0.7071067811865476f);
+    else if constexpr (ACT == MOE_ACT_GELU_TANH)
+        return __fdividef(z, 1.0f + __expf(-2.0f * gelu_u(z)));
+    else
+        return z;
+}
+
+// f(integral_constant<int, act>)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
 {
     switch (act) {
     case MOE_ACT_RELU:
-        return z < 0.0f ? 0.0f : z;  // a NaN stays one
+        return f(std::integral_constant<int, MOE_ACT_RELU>());
     case MOE_ACT_SILU:
-        return __fdividef(z, 1.0f + __expf(-z));
+        return f(std::integral_constant<int, MOE_ACT_SILU>());
     case MOE_ACT_GELU:
-        return 0.5f * z * erfcf(z * -0.7071067811865476f);
+        return f(std::integral_constant<int, MOE_ACT_GELU>());
     case MOE_ACT_GELU_TANH:
-        return __fdividef(z, 1.0f + __expf(-2.0f * gelu_u(z)));
+        return f(std::integral_constant<int, MOE_ACT_GELU_TANH>());
     default:
-        return z;
+        return f(std::integral_constant<int, MOE_ACT_NONE>());
     }
+}
+
+__device__ __forceinline__ float act_of(float z, int act)
+{
+    float y;
+    with_act(act, [&](auto a) { y = act_t<decltype(a)::value>(z); });
+    return y;
 }
 
 __device__ __forceinline__ float act_grad(float z, int act)
@@ -368,6 +393,273 @@ __global__ void __launch_bounds__(kLinThreads)
     cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
+// ---- large products: pairs of CTAs ---------------------------------------------
+//
+// Tiles of 256 (m) x bn (n): one tcgen05.mma of a CTA pair per 16 of r, each
+// CTA loading its 128 rows of A and half the rows of B, so a stage of
+// 64 r costs each SM 32 KB of loads (bn = 256) for 512 cycles of MMA; the
+// same tile on one SM would load 64 KB.  Pairs walk the tiles
+// (persistent); two accumulators in tensor memory let the eight epilogue
+// warps work on one tile while the MMAs fill the other.  Neighbouring lanes
+// are neighbouring outputs, so the epilogue stores straight from registers,
+// 64 or 128 contiguous bytes per warp and column.
+constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairStages = 7;
+
+struct PairCtrl {
+    uint64_t full[kPairStages];
+    uint64_t empty[kPairStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// 32 columns of a tile for one lane (output feature m): registers -> epilogue
+// -> global.  `n` columns exist from the first one's row on.
+template <int ACT>
+__device__ __forceinline__ void pair_columns(const LinArgs &p, const uint32_t (&r)[32], int64_t row,
+                                             int m, float bias, int n)
+{
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        v[j] = __uint_as_float(r[j]) + bias;
+    if (p.pre) {
+        uint16_t *o = static_cast<uint16_t *>(p.pre) + row * p.ldp + m;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n)
+                o[int64_t(j) * p.ldp] = to16(v[j], p.f16);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        v[j] = act_t<ACT>(v[j]);
+    if (p.residual) {
+        if (p.out_f32) {
+            const float *a = static_cast<const float *>(p.residual) + row * p.ldr + m;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < n)
+                    v[j] += a[int64_t(j) * p.ldr];
+        } else {
+            const uint16_t *a = static_cast<const uint16_t *>(p.residual) + row * p.ldr + m;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < n)
+                    v[j] += from16(a[int64_t(j) * p.ldr], p.f16);
+        }
+    }
+    if (p.out_f32) {
+        float *o = static_cast<float *>(p.out) + row * p.ldo + m;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n)
+                o[int64_t(j) * p.ldo] = v[j];
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(p.out) + row * p.ldo + m;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n)
+                o[int64_t(j) * p.ldo] = to16(v[j], p.f16);
+    }
+}
+
+template <bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_b, const LinArgs p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    // the same offset in both CTAs: dynamic shared memory starts at the same address
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    __shared__ PairCtrl ctl;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int bn = p.bn, half = bn / 2, S = p.stages;
+    const uint32_t stage_bytes = kLinATile + uint32_t(half) * (LK * 2);
+    const uint32_t tmem_cols = 2u * uint32_t(bn);
+    const int nk = (p.R + LK - 1) / LK;
+    const int n_nt = (p.N + bn - 1) / bn;
+    const int64_t tiles = int64_t(p.n_mt) * n_nt;
+    const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    volatile int *abort_flag = &ctl.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.acc_full[b], 1);
+            mbar_init(&ctl.acc_empty[b], 2 * kPairEpiWarps);  // both CTAs' warps
+        }
+        ctl.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&map_a);
+        prefetch_tmap(&map_b);
+    }
+    if (warp == 1)
+        tmem_alloc_pair(&ctl.tmem_base, tmem_cols);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // the other CTA's barriers are initialised
+    tc_fence_after_sync();
+    const uint32_t tmem_base = ctl.tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // Tiles in blocks of 16 n tiles, n fastest: the pairs running at one time
+    // share few rows of both operands.
+    auto tile_at = [&](int64_t t, int &m0, int &n0) {
+        const int64_t block = int64_t(16) * p.n_mt;
+        const int b = int(t / block);
+        const int wide = min(16, n_nt - 16 * b);
+        const int64_t u = t - b * block;
+        m0 = int(u / wide) * (2 * LM);
+        n0 = (16 * b + int(u % wide)) * bn;
+    };
+
+    if (warp == 0 && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < tiles; t += step) {
+            int m0, n0;
+            tile_at(t, m0, n0);
+            m0 += int(rank) * LM;
+            n0 += int(rank) * half;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
+                    mbar_arrive_expect_tx(&ctl.full[stage], 2 * stage_bytes);
+                const uint32_t fb = dsmem_addr(&ctl.full[stage], 0);
+                uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
+                const int k0 = kb * LK;
+                if (A_MN) {
+                    tma_load_2d_pair(sa, &map_a, fb, m0, k0);
+                    tma_load_2d_pair(sa + 8192, &map_a, fb, m0 + 64, k0);
+                } else {
+                    tma_load_2d_pair(sa, &map_a, fb, k0, m0);
+                }
+                if (B_MN) {
+                    for (int c = 0; c < half; c += 64)
+                        tma_load_2d_pair(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
+                } else {
+                    tma_load_2d_pair(sb, &map_b, fb, k0, n0);
+                }
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every stage released: this CTA's copies have landed and been read
+        for (int i = 0; ok && i < S; ++i) {
+            ok = mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag);
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {  // stopped: copies in flight take microseconds; give them a millisecond
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000u) {
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, aphase = 0;
+        uint32_t idesc = idesc_bf16_f32(2 * LM, uint32_t(bn), A_MN, B_MN);
+        if (p.f16)
+            idesc &= ~((7u << 7) | (7u << 10));
+        bool ok = true;
+        for (int64_t t = first; ok && t < tiles; t += step) {
+            if (!mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag))
+                break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + uint32_t(buf * bn);
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!mbar_wait(&ctl.full[stage], phase, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t sa = smem_u32(smem + stage * stage_bytes), sb = sa + kLinATile;
+#pragma unroll
+                for (int kk = 0; kk < LK / 16; ++kk) {
+                    const uint64_t da = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024)
+                                             : smem_desc_sw128(sa + kk * 32, 16, 1024);
+                    const uint64_t db = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024)
+                                             : smem_desc_sw128(sb + kk * 32, 16, 1024);
+                    tc_mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
+                }
+                tc_commit_pair(&ctl.empty[stage]);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok)
+                break;
+            tc_commit_pair(&ctl.acc_full[buf]);
+            if (++buf == 2) {
+                buf = 0;
+                aphase ^= 1u;
+            }
+        }
+        // (the epilogue warps of both CTAs wait for every accumulator, so the
+        // MMAs are done when the cluster meets below)
+    } else if (warp >= 2) {
+        const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant, half of the columns
+        int buf = 0;
+        uint32_t aphase = 0;
+        for (int64_t t = first; t < tiles; t += step) {
+            int m0, n0;
+            tile_at(t, m0, n0);
+            const int m = m0 + int(rank) * LM + q * 32 + int(lane);
+            const float bias = p.bias && m < p.M ? p.bias[m] : 0.0f;
+            bool ok = mbar_wait(&ctl.acc_full[buf], aphase, abort_flag);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            tc_fence_after_sync();
+            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * bn);
+            with_act(p.act, [&](auto act) {
+                for (int c = part * half; c < (part + 1) * half; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t0 + uint32_t(c), r);
+                    tmem_ld_wait();
+                    const int n = min(32, p.N - (n0 + c));
+                    if (m < p.M && n > 0)
+                        pair_columns<decltype(act)::value>(p, r, int64_t(n0) + c, m, bias, n);
+                    __syncwarp();
+                }
+            });
+            tc_fence_before_sync();
+            if (lane == 0)
+                mbar_arrive_cluster(dsmem_addr(&ctl.acc_empty[buf], 0));
+            if (++buf == 2) {
+                buf = 0;
+                aphase ^= 1u;
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && ctl.abort_flag && p.status)
+        atomicOr(p.status, MOE_STATUS_TIMEOUT);
+    cluster_sync();  // both CTAs are done with each other's shared memory and barriers
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, tmem_cols);
+    }
+}
+
 // ---- dP and db ---------------------------------------------------------------
 
 constexpr int kGradThreads = 256;
@@ -470,16 +762,57 @@ struct Operand {
     int64_t rows, cols, ld;  // as stored: cols contiguous
 };
 
+cudaError_t launch_clustered(const void *kern, unsigned grid, unsigned cluster, unsigned threads,
+                             size_t smem, cudaStream_t s, void **args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
 // D[m][n] = sum_r A[m][r] B[n][r]; a.M, a.N, a.R and the epilogue fields are
 // set, the tiling is chosen here.
 template <bool A_MN, bool B_MN>
 cudaError_t launch_linear(const Operand &A, const Operand &B, LinArgs a, cudaStream_t s)
 {
+    constexpr int which = B_MN ? 2 : A_MN ? 1 : 0;
     const int sms = device_sm_count();
+    const int nk = (a.R + LK - 1) / LK;
+    CUtensorMap ma, mb;
+    const int64_t pair_tiles = int64_t((a.M + 2 * LM - 1) / (2 * LM)) * ((a.N + 255) / 256);
+    if (pair_tiles >= sms / 2) {  // at least one tile for every pair of SMs
+        a.bn = 256;
+        a.n_mt = (a.M + 2 * LM - 1) / (2 * LM);
+        a.split = 1;
+        a.stages = kPairStages;
+        const size_t smem = 1024 + size_t(a.stages) * (kLinATile + a.bn / 2 * LK * 2);
+        cudaError_t e = lin_map(&ma, A.p, A.rows, A.cols, A.ld, A_MN ? LK : LM, a.f16);
+        if (e == cudaSuccess)
+            e = lin_map(&mb, B.p, B.rows, B.cols, B.ld, B_MN ? LK : a.bn / 2, a.f16);
+        const void *kern = reinterpret_cast<const void *>(k_linear_pair<A_MN, B_MN>);
+        if (e == cudaSuccess)
+            e = ensure_smem_limit(kern, kSlotLinearPair0 + which, smem);
+        if (e != cudaSuccess)
+            return e;
+        void *args[] = {&ma, &mb, &a};
+        return launch_clustered(kern, unsigned(std::min<int64_t>(pair_tiles, sms / 2)) * 2, 2,
+                                kPairThreads, smem, s, args);
+    }
     a.bn = a.N <= 16 ? 16 : a.N <= 32 ? 32 : a.N <= 64 ? 64 : 128;
     a.n_mt = (a.M + LM - 1) / LM;
     const int64_t tiles = int64_t(a.n_mt) * ((a.N + a.bn - 1) / a.bn);
-    const int nk = (a.R + LK - 1) / LK;
     // split the reduction while that still adds CTAs (two fit an SM) and
     // leaves each at least four stages
     a.split = 1;
@@ -491,34 +824,17 @@ cudaError_t launch_linear(const Operand &A, const Operand &B, LinArgs a, cudaStr
     a.stages = std::min<int>(kLinMaxStages, 96 * 1024 / stage);
     const size_t ring = size_t(a.stages) * stage;
     const size_t smem = 1024 + std::max(ring, size_t(a.bn) * LM * 4);
-
-    CUtensorMap ma, mb;
     cudaError_t e = lin_map(&ma, A.p, A.rows, A.cols, A.ld, A_MN ? LK : LM, a.f16);
+    if (e == cudaSuccess)
+        e = lin_map(&mb, B.p, B.rows, B.cols, B.ld, B_MN ? LK : a.bn, a.f16);
+    const void *kern = reinterpret_cast<const void *>(k_linear<A_MN, B_MN>);
+    if (e == cudaSuccess)
+        e = ensure_smem_limit(kern, kSlotLinear0 + which, 112 * 1024);
     if (e != cudaSuccess)
         return e;
-    e = lin_map(&mb, B.p, B.rows, B.cols, B.ld, B_MN ? LK : a.bn, a.f16);
-    if (e != cudaSuccess)
-        return e;
-    auto kern = k_linear<A_MN, B_MN>;
-    e = ensure_smem_limit(reinterpret_cast<const void *>(kern),
-                          kSlotLinear0 + (B_MN ? 2 : A_MN ? 1 : 0), 112 * 1024);
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(tiles * a.split));
-    cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(a.split);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+    void *args[] = {&ma, &mb, &a};
+    return launch_clustered(kern, unsigned(tiles * a.split), unsigned(a.split), kLinThreads, smem, s,
+                            args);
 }
 
 inline bool aligned(const void *p, uintptr_t a)

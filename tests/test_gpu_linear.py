@@ -87,6 +87,17 @@ def test_linear_large_tiles():
     _check_linear(2050, 256, 2600, "gelu_tanh", torch.bfloat16, torch.bfloat16)
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("out", [torch.float16, torch.float32])
+def test_linear_256_wide_tiles(act, out):
+    # enough 256 x 256 tiles for pairs of CTAs, with odd edges and short reductions
+    _check_linear(2321, 72, 2309, act, torch.float16, out, pad=40)
+
+
+def test_linear_256_wide_tiles_long_reduction():
+    _check_linear(2304, 4104, 2304, "none", torch.bfloat16, torch.bfloat16, bias=False, res=False)
+
+
 def test_linear_adds_into_its_output():
     x = _rand(1, 40, 320).to("cuda", torch.bfloat16)
     W = _rand(2, 90, 320, amp=0.05).to("cuda", torch.bfloat16)
@@ -181,6 +192,11 @@ def test_linear_grad_epilogues(act, dy_dtype):
 
 def test_linear_grad_large_tiles():
     _check_grad(1500, 520, 1300, "silu", torch.bfloat16, torch.bfloat16, torch.bfloat16)
+
+
+def test_linear_grad_256_wide_tiles():
+    _check_grad(2300, 2312, 2201, "gelu", torch.bfloat16, torch.bfloat16, torch.bfloat16, pad=8)
+    _check_grad(1000, 4104, 2600, "none", torch.float16, torch.float16, torch.float32)
 
 
 def test_linear_grad_computes_what_is_asked():
