@@ -2,21 +2,22 @@
 // staged by TMA: moe_linear (bias, activation and residual in the epilogue)
 // and its gradients.
 //
-// All three products have one form: D[m][n] = sum_r A[m][r] B[n][r], stored at
-// out[n * ldo + m], with the output's contiguous dimension as the MMA's M:
+// All three products have one form: out[i][j] = sum_r X[i][r] Y[j][r], j the
+// output's contiguous dimension:
 //
-//   y  [t][n] : m = n (output feature), n = t, r = i.  A = W  (r contiguous), B = x  (r contiguous)
-//   dx [t][i] : m = i, n = t, r = n.                   A = W  (m contiguous), B = dP (r contiguous)
-//   dW [n][i] : m = i, n = n, r = t.                   A = x  (m contiguous), B = dP (n contiguous)
+//   y  [t][n] : i = t, j = n (output feature), r = i.  X = x  (r contiguous), Y = W (r contiguous)
+//   dx [t][i] : i = t, j = i, r = n.                   X = dP (r contiguous), Y = W (j contiguous)
+//   dW [n][i] : i = n, j = i, r = t.                   X = dP (i contiguous), Y = x (j contiguous)
 //
-// A few tokens therefore fill only the MMA's N (16 columns at least) while
-// its M = 128 rows are always weights, and neighbouring lanes of the
-// accumulator are neighbouring output elements.
+// k_linear, for few rows or few tiles: Y is the MMA's A operand (M = 128),
+// so that a few tokens fill only the MMA's N (16 columns at least) and the
+// weights stream through whole tiles.  k_linear_pair, for the rest: 256 x bn
+// tiles on pairs of CTAs, rows as M.
 //
-// A tile's reduction is split over the Z CTAs of a thread-block cluster when
-// there are fewer tiles than SMs; each leaves its fp32 accumulator in its
-// own shared memory and the cluster adds them in rank order through
-// distributed shared memory (results are deterministic).
+// Either way a tile's reduction can be split over the CTAs of a thread-block
+// cluster when there are fewer tiles than SMs; each leaves its fp32
+// accumulator in its own shared memory and the cluster adds them in rank
+// order through distributed shared memory (results are deterministic).
 #include "../../include/moe_prefill.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -46,10 +47,10 @@ struct LinArgs {
     void *out;
     uint32_t *status;
     int64_t ldr, ldo, ldp;
-    int M, N, R;
+    int M, N, R;  // k_linear: M = j, N = i; k_linear_pair: M = i, N = j
     int bn, stages, split, n_mt;
     int f16, out_f32, act;
-    int vec_out, vec_res, vec_pre;  // four neighbouring elements are one aligned access
+    int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
 };
 
 struct LinCtrl {
@@ -75,10 +76,29 @@ __device__ __forceinline__ float4 dsmem_ld4(uint32_t a)
     return v;
 }
 
-// sqrt(2/pi) (z + 0.044715 z^3); (1 + tanh u) / 2 is 1 / (1 + e^-2u)
-__device__ __forceinline__ float gelu_u(float z)
+// 1 / (1 + e^-x): exponential and reciprocal by one special-function
+// instruction each (2 units in the last place, and the rounding of
+// x log2(e)); e^-x past 2^126 gives 0, where the true value is below 2^-126.
+__device__ __forceinline__ float sigmoid_ftz(float x)
 {
-    return 0.7978845608028654f * (z + 0.044715f * z * z * z);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+__device__ __forceinline__ void dsmem_st4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                          uint32_t w)
+{
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y),
+                 "r"(z), "r"(w)
+                 : "memory");
+}
+
+// sqrt(2/pi) (z + 0.044715 z^3) times two; (1 + tanh u) / 2 is 1 / (1 + e^-2u)
+__device__ __forceinline__ float gelu_2u(float z)
+{
+    return z * (1.5957691216057308f + 0.07135481627260025f * z * z);
 }
 
 template <int ACT>
@@ -87,11 +107,11 @@ __device__ __forceinline__ float act_t(float z)
     if constexpr (ACT == MOE_ACT_RELU)
         return z < 0.0f ? 0.0f : z;  // a NaN stays one
     else if constexpr (ACT == MOE_ACT_SILU)
-        return __fdividef(z, 1.0f + __expf(-z));
+        return z * sigmoid_ftz(z);
     else if constexpr (ACT == MOE_ACT_GELU)
         return 0.5f * z * erfcf(z * -0.7071067811865476f);
     else if constexpr (ACT == MOE_ACT_GELU_TANH)
-        return __fdividef(z, 1.0f + __expf(-2.0f * gelu_u(z)));
+        return z * sigmoid_ftz(gelu_2u(z));
     else
         return z;
 }
@@ -114,31 +134,22 @@ __device__ __forceinline__ void with_act(int act, F f)
     }
 }
 
-__device__ __forceinline__ float act_of(float z, int act)
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z)
 {
-    float y;
-    with_act(act, [&](auto a) { y = act_t<decltype(a)::value>(z); });
-    return y;
-}
-
-__device__ __forceinline__ float act_grad(float z, int act)
-{
-    switch (act) {
-    case MOE_ACT_RELU:
+    if constexpr (ACT == MOE_ACT_RELU) {
         return z > 0.0f ? 1.0f : 0.0f;
-    case MOE_ACT_SILU: {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+    } else if constexpr (ACT == MOE_ACT_SILU) {
+        const float s = sigmoid_ftz(z);
         return s * (1.0f + z * (1.0f - s));
-    }
-    case MOE_ACT_GELU:
+    } else if constexpr (ACT == MOE_ACT_GELU) {
         return 0.5f * erfcf(z * -0.7071067811865476f) +
                0.3989422804014327f * z * __expf(-0.5f * z * z);
-    case MOE_ACT_GELU_TANH: {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-2.0f * gelu_u(z)));
-        const float du = 0.7978845608028654f * (1.0f + 3.0f * 0.044715f * z * z);
-        return s + z * 2.0f * s * (1.0f - s) * du;
-    }
-    default:
+    } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
+        const float s = sigmoid_ftz(gelu_2u(z));
+        const float du2 = 1.5957691216057308f + 3.0f * 0.07135481627260025f * z * z;
+        return s + z * s * (1.0f - s) * du2;
+    } else {
         return 1.0f;
     }
 }
@@ -199,6 +210,47 @@ __device__ __forceinline__ void store4(const float (&v)[4], void *p, int64_t at,
         }
 }
 
+// The epilogue, after the bias, of four neighbouring outputs (the first `left`
+// exist) in each of R rows, `by` apart (those less than `rows` ahead exist).
+template <int R>
+__device__ __forceinline__ void finish_rows(const LinArgs &p, float (&v)[R][4], int64_t row, int by,
+                                            int rows, int col, int left)
+{
+    if (p.pre) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i * by < rows)
+                store4(v[i], p.pre, (row + i * by) * p.ldp + col, left, 0, p.f16, p.vec_pre);
+    }
+    float a[R][4];
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i * by < rows)
+                load4(a[i], p.residual, (row + i * by) * p.ldr + col, left, p.out_f32, p.f16,
+                      p.vec_res);
+    }
+    if (p.act != MOE_ACT_NONE)
+        with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = act_t<decltype(act)::value>(v[i][j]);
+        });
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[i][j] += i * by < rows ? a[i][j] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i * by < rows)
+            store4(v[i], p.out, (row + i * by) * p.ldo + col, left, p.out_f32, p.f16, p.vec_out);
+}
+
 // Bounded wait of the stop path.
 __device__ __forceinline__ void lin_drain(uint64_t *bar, uint32_t parity)
 {
@@ -252,31 +304,34 @@ __global__ void __launch_bounds__(kLinThreads)
     pdl_wait();
     pdl_launch_dependents();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0, issued = 0, issued_par = 0;
+        const bool one = elect_one();
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag)) {
-                ok = false;
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
+            if (!ok)
                 break;
+            if (one) {
+                uint64_t *fb = &ctl.full[stage];
+                mbar_arrive_expect_tx(fb, stage_bytes);
+                uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
+                const int k0 = kb * LK;
+                if (A_MN) {  // 64 m x 64 r boxes, m contiguous
+                    tma_load_2d(sa, &map_a, fb, m0, k0);
+                    tma_load_2d(sa + 8192, &map_a, fb, m0 + 64, k0);
+                } else {
+                    tma_load_2d(sa, &map_a, fb, k0, m0);
+                }
+                if (B_MN) {
+                    for (int c = 0; c < bn; c += 64)
+                        tma_load_2d(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
+                } else {
+                    tma_load_2d(sb, &map_b, fb, k0, n0);
+                }
             }
-            uint64_t *fb = &ctl.full[stage];
-            mbar_arrive_expect_tx(fb, stage_bytes);
-            uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
-            const int k0 = kb * LK;
-            if (A_MN) {  // 64 m x 64 r boxes, m contiguous
-                tma_load_2d(sa, &map_a, fb, m0, k0);
-                tma_load_2d(sa + 8192, &map_a, fb, m0 + 64, k0);
-            } else {
-                tma_load_2d(sa, &map_a, fb, k0, m0);
-            }
-            if (B_MN) {
-                for (int c = 0; c < bn; c += 64)
-                    tma_load_2d(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
-            } else {
-                tma_load_2d(sb, &map_b, fb, k0, n0);
-            }
+            __syncwarp();
             issued |= 1u << stage;
             issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
             if (++stage == S) {
@@ -288,34 +343,40 @@ __global__ void __launch_bounds__(kLinThreads)
             for (int s = 0; s < S; ++s)
                 if ((issued >> s) & 1u)
                     lin_drain(&ctl.full[s], (issued_par >> s) & 1u);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
+        // the whole warp walks the loop and one lane issues, so that
+        // descriptors and addresses stay warp-uniform
         int stage = 0;
         uint32_t phase = 0;
         uint32_t idesc = idesc_bf16_f32(LM, uint32_t(bn), A_MN, B_MN);
         if (p.f16)
             idesc &= ~((7u << 7) | (7u << 10));  // f16 operands: format 0
+        const uint32_t sa = smem_u32(smem), sb = sa + kLinATile;
+        // r contiguous: 16 of them are 32 bytes inside the 128-byte row; m or n
+        // contiguous: 16 rows of 128 bytes, 64-element chunks 8 KB apart
+        const uint64_t da0 = A_MN ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
+        const uint64_t db0 = B_MN ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
+        const bool one = elect_one();
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&ctl.full[stage], phase, abort_flag))
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag)))
                 break;
             tc_fence_after_sync();
-            const uint32_t sa = smem_u32(smem + stage * stage_bytes), sb = sa + kLinATile;
+            if (one) {
+                const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
 #pragma unroll
-            for (int kk = 0; kk < LK / 16; ++kk) {
-                // r contiguous: 16 of them are 32 bytes inside the 128-byte row;
-                // m or n contiguous: 16 rows of 128 bytes, 64-element chunks 8 KB apart
-                const uint64_t da = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024)
-                                         : smem_desc_sw128(sa + kk * 32, 16, 1024);
-                const uint64_t db = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024)
-                                         : smem_desc_sw128(sb + kk * 32, 16, 1024);
-                tc_mma_f16(tmem_base, da, db, idesc, kb != kb0 || kk != 0);
+                for (int kk = 0; kk < LK / 16; ++kk)
+                    tc_mma_f16(tmem_base, da0 + off + kk * (A_MN ? 128 : 2),
+                               db0 + off + kk * (B_MN ? 128 : 2), idesc, kb != kb0 || kk != 0);
+                tc_commit(&ctl.empty[stage]);
             }
-            tc_commit(&ctl.empty[stage]);
+            __syncwarp();
             if (++stage == S) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
-        tc_commit(&ctl.done);  // arrives once every MMA issued here has completed
+        if (one)
+            tc_commit(&ctl.done);  // arrives once every MMA issued here has completed
     }
     __syncwarp();
 
@@ -361,33 +422,17 @@ __global__ void __launch_bounds__(kLinThreads)
         const int left = min(4, p.M - (m0 + m));
         if (left <= 0)
             continue;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int r = 0; r < p.split; ++r) {
-            const float4 o = dsmem_ld4(dsmem_addr(acc + n * LM + m, r));
-            v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
-        }
-        const int64_t row = n0 + n;
-        if (p.bias) {
+        float v[1][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left)
-                    v[i] += p.bias[m0 + m + i];
-        }
-        if (p.pre)
-            store4(v, p.pre, row * p.ldp + m0 + m, left, 0, p.f16, p.vec_pre);
-        if (p.act != MOE_ACT_NONE) {
+        for (int i = 0; i < 4; ++i)
+            v[0][i] = p.bias && i < left ? p.bias[m0 + m + i] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = act_of(v[i], p.act);
-        }
-        if (p.residual) {
-            float a[4];
-            load4(a, p.residual, row * p.ldr + m0 + m, left, p.out_f32, p.f16, p.vec_res);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] += a[i];
-        }
-        store4(v, p.out, row * p.ldo + m0 + m, left, p.out_f32, p.f16, p.vec_out);
+        for (int r = 0; r < kLinMaxSplit; ++r)
+            if (r < p.split) {
+                const float4 o = dsmem_ld4(dsmem_addr(acc + n * LM + m, r));
+                v[0][0] += o.x, v[0][1] += o.y, v[0][2] += o.z, v[0][3] += o.w;
+            }
+        finish_rows<1>(p, v, n0 + n, 1, 1, m0 + m, left);
     }
     __syncwarp();
     cluster_sync();  // no CTA leaves while its shared memory is read
@@ -395,17 +440,23 @@ __global__ void __launch_bounds__(kLinThreads)
 
 // ---- large products: pairs of CTAs ---------------------------------------------
 //
-// Tiles of 256 (m) x bn (n): one tcgen05.mma of a CTA pair per 16 of r, each
-// CTA loading its 128 rows of A and half the rows of B, so a stage of
-// 64 r costs each SM 32 KB of loads (bn = 256) for 512 cycles of MMA; the
-// same tile on one SM would load 64 KB.  Pairs walk the tiles
-// (persistent); two accumulators in tensor memory let the eight epilogue
-// warps work on one tile while the MMAs fill the other.  Neighbouring lanes
-// are neighbouring outputs, so the epilogue stores straight from registers,
-// 64 or 128 contiguous bytes per warp and column.
+// out[m * ldo + n] = sum_r A[m][r] B[n][r] in tiles of 256 (m) x bn (n): one
+// tcgen05.mma of a CTA pair per 16 of r, each CTA loading its 128 rows of A
+// and half the rows of B.  A stage of 64 r costs each SM 32 KB of loads
+// (bn = 256) for 512 cycles of MMA; the same tile on one SM would load 48.
+// Pairs walk the tiles (persistent); two accumulators in tensor memory let
+// eight epilogue warps work on one tile while the MMAs fill the other.  An
+// epilogue warp takes 32 rows x 32 columns at a time through 4 KB of shared
+// memory, so that global accesses are whole row pieces of 64 or 128 bytes;
+// the next 32 columns are read from tensor memory (about 330 cycles) ahead.
+//
+// split > 1: a cluster of `split` pairs shares one tile's reduction.
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairEpiWarps = 8;
-constexpr int kPairStages = 7;
+constexpr int kPairSub = 2;     // 64-r halves of a stage
+constexpr int kPairStages = 3;
+constexpr uint32_t kPairStg = 4096;  // staging of one epilogue warp
+constexpr int kPairMaxSplit = 4;     // a cluster of eight CTAs
 
 struct PairCtrl {
     uint64_t full[kPairStages];
@@ -416,54 +467,168 @@ struct PairCtrl {
     int abort_flag;
 };
 
-// 32 columns of a tile for one lane (output feature m): registers -> epilogue
-// -> global.  `n` columns exist from the first one's row on.
-template <int ACT>
-__device__ __forceinline__ void pair_columns(const LinArgs &p, const uint32_t (&r)[32], int64_t row,
-                                             int m, float bias, int n)
+__host__ __device__ __forceinline__ uint32_t pair_sub_bytes(int bn, bool b_mn)
 {
-    float v[32];
+    const int half = bn / 2;
+    return kLinATile + uint32_t(b_mn ? (half + 63) / 64 * 64 : half) * (LK * 2);
+}
+
+// A warp's staging tile: 32 rows of 32 elements E, in 16-byte pieces; piece c
+// of row r sits where eight rows' same pieces fall into different banks.
+template <typename E>
+__device__ __forceinline__ uint4 *stg_at(uint8_t *stg, int r, int c)
+{
+    constexpr int kPieces = 2 * int(sizeof(E));  // 4 (16-bit) or 8 of a row
+    const int x = sizeof(E) == 4 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+    return reinterpret_cast<uint4 *>(stg) + r * kPieces + x;
+}
+
+// Moves the tile to (STORE) or from rows [0, rows) x columns [0, cols) of a
+// matrix with ld elements between rows.  vec: 16-byte pieces are aligned;
+// otherwise, or where columns end inside the tile, element by element.
+template <bool STORE, typename E>
+__device__ __forceinline__ void stg_move(uint8_t *stg, E *p, int64_t ld, int rows, int cols,
+                                         bool vec)
+{
+    constexpr int kPieces = 2 * int(sizeof(E)), kPer = 16 / int(sizeof(E));
+    constexpr int kRows = 32 / kPieces;  // rows a warp moves at once
+    const int lane = threadIdx.x & 31;
+    if (vec && cols == 32) {
+        const int r0 = lane / kPieces, c = lane % kPieces;
+        E *q = p + int64_t(r0) * ld + c * kPer;
+        uint4 v[kPieces];
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        v[j] = __uint_as_float(r[j]) + bias;
-    if (p.pre) {
-        uint16_t *o = static_cast<uint16_t *>(p.pre) + row * p.ldp + m;
+        for (int i = 0; i < kPieces; ++i) {
+            if (STORE)
+                v[i] = *stg_at<E>(stg, r0 + i * kRows, c);
+            else if (r0 + i * kRows < rows)
+                v[i] = *reinterpret_cast<const uint4 *>(q + int64_t(i * kRows) * ld);
+        }
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < n)
-                o[int64_t(j) * p.ldp] = to16(v[j], p.f16);
+        for (int i = 0; i < kPieces; ++i) {
+            if (!STORE)
+                *stg_at<E>(stg, r0 + i * kRows, c) = v[i];
+            else if (r0 + i * kRows < rows)
+                *reinterpret_cast<uint4 *>(q + int64_t(i * kRows) * ld) = v[i];
+        }
+        return;
     }
+    if (lane < cols)
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            E *at = reinterpret_cast<E *>(stg_at<E>(stg, r, lane / kPer)) + lane % kPer;
+            if (STORE)
+                p[int64_t(r) * ld + lane] = *at;
+            else
+                *at = p[int64_t(r) * ld + lane];
+        }
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, int f16)
+{
+    if (f16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t v, int f16)
+{
+    if (f16)
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// 32 rows (lane = row) x 32 columns -> 16-bit rows, by way of the staging tile.
+__device__ __forceinline__ void emit16(uint8_t *stg, const float (&v)[32], uint16_t *out,
+                                       int64_t ld, int rows, int cols, int f16, bool vec)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        v[j] = act_t<ACT>(v[j]);
-    if (p.residual) {
-        if (p.out_f32) {
-            const float *a = static_cast<const float *>(p.residual) + row * p.ldr + m;
+    for (int c = 0; c < 4; ++c)
+        *stg_at<uint16_t>(stg, lane, c) = make_uint4(
+            pack16(v[8 * c], v[8 * c + 1], f16), pack16(v[8 * c + 2], v[8 * c + 3], f16),
+            pack16(v[8 * c + 4], v[8 * c + 5], f16), pack16(v[8 * c + 6], v[8 * c + 7], f16));
+    __syncwarp();
+    stg_move<true>(stg, out, ld, rows, cols, vec);
+}
+
+// The epilogue of 32 rows x 32 columns: bias, pre, activation, residual, output.
+// `bias`: lane j holds column j's; every lane takes all of them, by way of
+// the staging tile.
+__device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float (&v)[32],
+                                           float bias, int64_t m0, int n0, int rows, int cols)
+{
+    const int lane = threadIdx.x & 31;
+    if (p.bias) {
+        __syncwarp();
+        reinterpret_cast<float *>(stg)[lane] = bias;
+        __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < n)
-                    v[j] += a[int64_t(j) * p.ldr];
-        } else {
-            const uint16_t *a = static_cast<const uint16_t *>(p.residual) + row * p.ldr + m;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < n)
-                    v[j] += from16(a[int64_t(j) * p.ldr], p.f16);
+        for (int j = 0; j < 32; j += 4) {
+            const float4 b = *reinterpret_cast<const float4 *>(stg + 4 * j);
+            v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
         }
     }
-    if (p.out_f32) {
-        float *o = static_cast<float *>(p.out) + row * p.ldo + m;
+    if (p.pre)
+        emit16(stg, v, static_cast<uint16_t *>(p.pre) + m0 * p.ldp + n0, p.ldp, rows, cols, p.f16,
+               p.vec_pre);
+    if (p.act != MOE_ACT_NONE)
+        with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < n)
-                o[int64_t(j) * p.ldo] = v[j];
-    } else {
-        uint16_t *o = static_cast<uint16_t *>(p.out) + row * p.ldo + m;
+            for (int j = 0; j < 32; ++j)
+                v[j] = act_t<decltype(act)::value>(v[j]);
+        });
+    if (p.residual) {
+        __syncwarp();
+        if (p.out_f32) {
+            stg_move<false>(stg,
+                            const_cast<float *>(static_cast<const float *>(p.residual)) +
+                                m0 * p.ldr + n0,
+                            p.ldr, rows, cols, p.vec_res);
+            __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < n)
-                o[int64_t(j) * p.ldo] = to16(v[j], p.f16);
+            for (int c = 0; c < 8; ++c) {
+                const uint4 q = *stg_at<float>(stg, lane, c);
+                v[4 * c] += __uint_as_float(q.x), v[4 * c + 1] += __uint_as_float(q.y);
+                v[4 * c + 2] += __uint_as_float(q.z), v[4 * c + 3] += __uint_as_float(q.w);
+            }
+        } else {
+            stg_move<false>(stg,
+                            const_cast<uint16_t *>(static_cast<const uint16_t *>(p.residual)) +
+                                m0 * p.ldr + n0,
+                            p.ldr, rows, cols, p.vec_res);
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 q = *stg_at<uint16_t>(stg, lane, c);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack16(w[i], p.f16);
+                    v[8 * c + 2 * i] += f.x;
+                    v[8 * c + 2 * i + 1] += f.y;
+                }
+            }
+        }
     }
+    if (!p.out_f32) {
+        emit16(stg, v, static_cast<uint16_t *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols, p.f16,
+               p.vec_out);
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *stg_at<float>(stg, lane, c) =
+            make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+    __syncwarp();
+    stg_move<true>(stg, static_cast<float *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols,
+                   p.vec_out);
 }
 
 template <bool A_MN, bool B_MN>
@@ -472,20 +637,24 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                   const __grid_constant__ CUtensorMap map_b, const LinArgs p)
 {
     extern __shared__ uint8_t smem_raw[];
-    // the same offset in both CTAs: dynamic shared memory starts at the same address
+    // the same offset in every CTA: dynamic shared memory starts at the same address
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
     __shared__ PairCtrl ctl;
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t rank = crank & 1u, lead = crank & ~1u;  // place in the pair, its even CTA
+    const int z = int(crank >> 1), Z = p.split;
     const int bn = p.bn, half = bn / 2, S = p.stages;
-    const uint32_t stage_bytes = kLinATile + uint32_t(half) * (LK * 2);
-    const uint32_t tmem_cols = 2u * uint32_t(bn);
+    const uint32_t sub_bytes = pair_sub_bytes(bn, B_MN);
+    uint8_t *stg = smem + S * kPairSub * sub_bytes;
+    const uint32_t tmem_cols = bn <= 64 ? 128u : bn <= 128 ? 256u : 512u;  // two accumulators
     const int nk = (p.R + LK - 1) / LK;
+    const int kb0 = int(int64_t(nk) * z / Z), kb1 = int(int64_t(nk) * (z + 1) / Z);
     const int n_nt = (p.N + bn - 1) / bn;
     const int64_t tiles = int64_t(p.n_mt) * n_nt;
-    const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int64_t first = blockIdx.x / (2 * Z), step = gridDim.x / (2 * Z);
     volatile int *abort_flag = &ctl.abort_flag;
 
     if (threadIdx.x == 0) {
@@ -502,58 +671,70 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         prefetch_tmap(&map_a);
         prefetch_tmap(&map_b);
     }
+    __syncwarp();
+    cluster_arrive();
     if (warp == 1)
         tmem_alloc_pair(&ctl.tmem_base, tmem_cols);
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync();  // the other CTA's barriers are initialised
+    cluster_wait();  // the other CTAs' barriers are initialised
     tc_fence_after_sync();
     const uint32_t tmem_base = ctl.tmem_base;
     pdl_wait();
     pdl_launch_dependents();
 
-    // Tiles in blocks of 16 n tiles, n fastest: the pairs running at one time
+    // Tiles in blocks of 16 m tiles, m fastest: the pairs running at one time
     // share few rows of both operands.
     auto tile_at = [&](int64_t t, int &m0, int &n0) {
-        const int64_t block = int64_t(16) * p.n_mt;
+        const int64_t block = int64_t(16) * n_nt;
         const int b = int(t / block);
-        const int wide = min(16, n_nt - 16 * b);
+        const int tall = min(16, p.n_mt - 16 * b);
         const int64_t u = t - b * block;
-        m0 = int(u / wide) * (2 * LM);
-        n0 = (16 * b + int(u % wide)) * bn;
+        n0 = int(u / tall) * bn;
+        m0 = (16 * b + int(u % tall)) * (2 * LM);
     };
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0;
+        const bool one = elect_one();
         bool ok = true;
         for (int64_t t = first; ok && t < tiles; t += step) {
             int m0, n0;
             tile_at(t, m0, n0);
             m0 += int(rank) * LM;
             n0 += int(rank) * half;
-            for (int kb = 0; kb < nk; ++kb) {
-                if (!mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag)) {
-                    ok = false;
+            for (int kb = kb0; kb < kb1; kb += kPairSub) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
+                if (!ok)
                     break;
+                if (one) {
+                    const int subs = min(kPairSub, kb1 - kb);
+                    if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
+                        mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(2 * subs) * sub_bytes);
+                    const uint32_t fb = dsmem_addr(&ctl.full[stage], lead);
+#pragma unroll
+                    for (int h = 0; h < kPairSub; ++h) {
+                        if (h >= subs)
+                            break;
+                        uint8_t *sa = smem + (stage * kPairSub + h) * sub_bytes;
+                        uint8_t *sb = sa + kLinATile;
+                        const int k0 = (kb + h) * LK;
+                        if (A_MN) {  // 64 m x 64 r boxes, m contiguous
+                            tma_load_2d_pair(sa, &map_a, fb, m0, k0);
+                            tma_load_2d_pair(sa + 8192, &map_a, fb, m0 + 64, k0);
+                        } else {
+                            tma_load_2d_pair(sa, &map_a, fb, k0, m0);
+                        }
+                        if (B_MN) {
+                            for (int c = 0; c < half; c += 64)
+                                tma_load_2d_pair(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
+                        } else {
+                            tma_load_2d_pair(sb, &map_b, fb, k0, n0);
+                        }
+                    }
                 }
-                if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
-                    mbar_arrive_expect_tx(&ctl.full[stage], 2 * stage_bytes);
-                const uint32_t fb = dsmem_addr(&ctl.full[stage], 0);
-                uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
-                const int k0 = kb * LK;
-                if (A_MN) {
-                    tma_load_2d_pair(sa, &map_a, fb, m0, k0);
-                    tma_load_2d_pair(sa + 8192, &map_a, fb, m0 + 64, k0);
-                } else {
-                    tma_load_2d_pair(sa, &map_a, fb, k0, m0);
-                }
-                if (B_MN) {
-                    for (int c = 0; c < half; c += 64)
-                        tma_load_2d_pair(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
-                } else {
-                    tma_load_2d_pair(sb, &map_b, fb, k0, n0);
-                }
+                __syncwarp();
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1u;
@@ -562,7 +743,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         // every stage released: this CTA's copies have landed and been read
         for (int i = 0; ok && i < S; ++i) {
-            ok = mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag);
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
             if (++stage == S) {
                 stage = 0;
                 phase ^= 1u;
@@ -573,34 +754,46 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             while (globaltimer_ns() - t0 < 1000000u) {
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        // The whole warp walks the loop and one lane issues, so that
+        // descriptors and addresses stay warp-uniform.
         int stage = 0, buf = 0;
         uint32_t phase = 0, aphase = 0;
         uint32_t idesc = idesc_bf16_f32(2 * LM, uint32_t(bn), A_MN, B_MN);
         if (p.f16)
             idesc &= ~((7u << 7) | (7u << 10));
+        const uint32_t sa = smem_u32(smem), sb = sa + kLinATile;
+        const uint64_t da0 = A_MN ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
+        const uint64_t db0 = B_MN ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
+        const bool one = elect_one();
         bool ok = true;
         for (int64_t t = first; ok && t < tiles; t += step) {
-            if (!mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag))
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
+            if (!ok)
                 break;
             tc_fence_after_sync();
             const uint32_t d = tmem_base + uint32_t(buf * bn);
-            for (int kb = 0; kb < nk; ++kb) {
-                if (!mbar_wait(&ctl.full[stage], phase, abort_flag)) {
-                    ok = false;
+            for (int kb = kb0; kb < kb1; kb += kPairSub) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+                if (!ok)
                     break;
-                }
                 tc_fence_after_sync();
-                const uint32_t sa = smem_u32(smem + stage * stage_bytes), sb = sa + kLinATile;
+                if (one) {
 #pragma unroll
-                for (int kk = 0; kk < LK / 16; ++kk) {
-                    const uint64_t da = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024)
-                                             : smem_desc_sw128(sa + kk * 32, 16, 1024);
-                    const uint64_t db = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024)
-                                             : smem_desc_sw128(sb + kk * 32, 16, 1024);
-                    tc_mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
+                    for (int h = 0; h < kPairSub; ++h) {
+                        const uint64_t off =
+                            uint64_t(uint32_t(stage * kPairSub + h) * (sub_bytes >> 4));
+                        if (kb + h < kb1) {
+#pragma unroll
+                            for (int kk = 0; kk < LK / 16; ++kk)
+                                tc_mma_f16_pair(d, da0 + off + kk * (A_MN ? 128 : 2),
+                                                db0 + off + kk * (B_MN ? 128 : 2), idesc,
+                                                kb != kb0 || (h | kk) != 0);
+                        }
+                    }
+                    tc_commit_pair(&ctl.empty[stage], uint16_t(3u << lead));
                 }
-                tc_commit_pair(&ctl.empty[stage]);
+                __syncwarp();
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1u;
@@ -608,7 +801,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             if (!ok)
                 break;
-            tc_commit_pair(&ctl.acc_full[buf]);
+            if (one)
+                tc_commit_pair(&ctl.acc_full[buf], uint16_t(3u << lead));
+            __syncwarp();
             if (++buf == 2) {
                 buf = 0;
                 aphase ^= 1u;
@@ -616,44 +811,129 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         // (the epilogue warps of both CTAs wait for every accumulator, so the
         // MMAs are done when the cluster meets below)
-    } else if (warp >= 2) {
-        const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant, half of the columns
+    } else if (warp >= 2 && Z == 1) {
+        const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant; even or odd chunks
+        uint8_t *mine = stg + (warp - 2) * kPairStg;
         int buf = 0;
         uint32_t aphase = 0;
         for (int64_t t = first; t < tiles; t += step) {
             int m0, n0;
             tile_at(t, m0, n0);
-            const int m = m0 + int(rank) * LM + q * 32 + int(lane);
-            const float bias = p.bias && m < p.M ? p.bias[m] : 0.0f;
-            bool ok = mbar_wait(&ctl.acc_full[buf], aphase, abort_flag);
+            const int64_t row = int64_t(m0) + int(rank) * LM + q * 32;
+            const int rows = int(min(int64_t(32), p.M - row)), width = min(bn, p.N - n0);
+            auto bias_of = [&](int c) {
+                return p.bias && c + int(lane) < width ? p.bias[n0 + c + int(lane)] : 0.0f;
+            };
+            float bias = bias_of(part * 32);
+            const bool ok = mbar_wait(&ctl.acc_full[buf], aphase, abort_flag);
             if (!__all_sync(0xffffffffu, ok))
                 break;
             tc_fence_after_sync();
             const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * bn);
-            with_act(p.act, [&](auto act) {
-                for (int c = part * half; c < (part + 1) * half; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(t0 + uint32_t(c), r);
+            if (rows > 0 && part * 32 < width) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(t0 + uint32_t(part * 32), r);
+#pragma unroll 1
+                for (int c = part * 32; c < width; c += 64) {
+                    float v[32];
                     tmem_ld_wait();
-                    const int n = min(32, p.N - (n0 + c));
-                    if (m < p.M && n > 0)
-                        pair_columns<decltype(act)::value>(p, r, int64_t(n0) + c, m, bias, n);
-                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __uint_as_float(r[j]);
+                    const float now = bias;
+                    if (c + 64 < width) {
+                        tmem_ld_32x32b_x32(t0 + uint32_t(c) + 64, r);
+                        bias = bias_of(c + 64);
+                    }
+                    pair_chunk(p, mine, v, now, row, n0 + c, rows, min(32, width - c));
                 }
-            });
+            }
             tc_fence_before_sync();
+            __syncwarp();
             if (lane == 0)
-                mbar_arrive_cluster(dsmem_addr(&ctl.acc_empty[buf], 0));
+                mbar_arrive_cluster(dsmem_addr(&ctl.acc_empty[buf], lead));
             if (++buf == 2) {
                 buf = 0;
                 aphase ^= 1u;
             }
         }
     }
+    __syncwarp();
+    if (Z > 1) {
+        // One tile per cluster; each pair has summed its share of r.  CTA z
+        // of the Z that hold the same rows finishes 128 / Z of them: every
+        // CTA sends it its sums of those rows (into memory beside the ring,
+        // which may still be in use there), and it adds them in rank order.
+        int m0, n0;
+        tile_at(first, m0, n0);
+        float *acc = reinterpret_cast<float *>(stg);  // [Z][128 / Z][pitch]
+        const int pitch = bn + 4, slice = LM / Z;     // float4 rows, conflict-free
+        // what a thread finishes: four neighbouring columns, always the same, of
+        // every `by`-th row
+        const int quads = bn / 4, t = int(threadIdx.x), by = kPairThreads / quads;
+        const int n = t % quads * 4, left = min(4, p.N - (n0 + n));
+        float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                bias[i] = i < left ? p.bias[n0 + n + i] : 0.0f;
+        }
+        if (warp >= 2) {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[0], 0, abort_flag));
+            const int q = warp & 3, part = (warp - 2) >> 2, m = q * 32 + int(lane);
+            tc_fence_after_sync();
+            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(part * bn / 2);
+            const uint32_t to = dsmem_addr(acc + (z * slice + m % slice) * pitch + part * bn / 2,
+                                           2 * uint32_t(m / slice) + rank);
+            uint32_t r[2][32] = {};
+            if (ok) {
+                tmem_ld_32x32b_x32(t0, r[0]);
+                if (bn > 64)
+                    tmem_ld_32x32b_x32(t0 + 32, r[1]);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)
+                if (j < 32 || bn > 64)
+                    dsmem_st4(to + j * 4, r[j >> 5][j & 31], r[j >> 5][(j & 31) + 1],
+                              r[j >> 5][(j & 31) + 2], r[j >> 5][(j & 31) + 3]);
+            tc_fence_before_sync();
+        }
+        __syncwarp();
+        cluster_sync();
+        m0 += int(rank) * LM + z * slice;
+        const int rows = min(slice, p.M - m0);
+        if (left > 0) {
+            constexpr int kBatch = 4;
+#pragma unroll 1
+            for (int m = t / quads; m < rows; m += kBatch * by) {
+                float v[kBatch][4];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[i][j] = 0.0f;
+                    const float *a = acc + min(m + i * by, slice - 1) * pitch + n;
+#pragma unroll
+                    for (int r = 0; r < kPairMaxSplit; ++r)
+                        if (r < Z) {
+                            const float4 o =
+                                *reinterpret_cast<const float4 *>(a + r * slice * pitch);
+                            v[i][0] += o.x, v[i][1] += o.y, v[i][2] += o.z, v[i][3] += o.w;
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[i][j] += bias[j];
+                }
+                finish_rows<kBatch>(p, v, int64_t(m0) + m, by, rows - m, n0 + n, left);
+            }
+        }
+        __syncwarp();
+    }
     __syncthreads();
     if (threadIdx.x == 0 && ctl.abort_flag && p.status)
         atomicOr(p.status, MOE_STATUS_TIMEOUT);
-    cluster_sync();  // both CTAs are done with each other's shared memory and barriers
+    cluster_sync();  // the CTAs are done with each other's shared memory and barriers
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem_base, tmem_cols);
@@ -663,7 +943,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---- dP and db ---------------------------------------------------------------
 
 constexpr int kGradThreads = 256;
-constexpr int kGradCols = 128;      // columns of a CTA: 32 lanes x 4
+constexpr int kGradGroups = 8;       // rows of a CTA side by side, one per warp
+constexpr int kGradCols = 256;       // columns of a CTA: 32 lanes x 8
+constexpr int kGradUnroll = 4;       // rows of a warp in flight
 constexpr int kGradMaxChunks = 128;  // rows of partial column sums
 
 struct GradArgs {
@@ -672,68 +954,170 @@ struct GradArgs {
     float *part;      // [chunks][N] or null
     int64_t lddy, lddp;
     int T, N, rows;   // rows per chunk
-    int dy_f32, f16, act;
-    int vec_dy, vec_pre;
+    int f16, act;
+    int vec;          // 16-byte accesses of dy and pre are aligned
 };
 
-// dP = dy act'(pre), and the column sums of one chunk of rows: eight rows at
-// a time, four columns a thread; the eight row groups are added in order.
-__global__ void __launch_bounds__(kGradThreads) k_act_grad(const GradArgs p)
+// Eight neighbouring elements, the first `n` of which exist.
+template <bool F32>
+struct Eight {
+    uint4 q[F32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void *p, int64_t at, int n, bool vec)
+    {
+        if (vec && n == 8) {
+            const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) +
+                                                             at * (F32 ? 4 : 2));
+            q[0] = v[0];
+            if (F32)
+                q[F32 ? 1 : 0] = v[1];
+            return;
+        }
+        uint32_t w[F32 ? 8 : 4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {
+                if (F32)
+                    w[F32 ? i : 0] = static_cast<const uint32_t *>(p)[at + i];
+                else
+                    w[i >> 1] |= uint32_t(static_cast<const uint16_t *>(p)[at + i])
+                                 << (16 * (i & 1));
+            }
+        q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (F32)
+            q[F32 ? 1 : 0] = make_uint4(w[F32 ? 4 : 0], w[F32 ? 5 : 0], w[F32 ? 6 : 0], w[F32 ? 7 : 0]);
+    }
+
+    __device__ __forceinline__ void to(float (&v)[8], int f16) const
+    {
+        const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+        if constexpr (F32) {
+            const uint32_t u[4] = {q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = __uint_as_float(w[i]);
+                v[i + 4] = __uint_as_float(u[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack16(w[i], f16);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
+
+// dP = dy act'(pre), and the column sums of one chunk of rows.  A warp takes
+// every eighth row of the chunk, eight columns a lane, four rows' loads in
+// flight; the warps' sums are added in order.  Bound by memory: dy and pre
+// are read and dP written once.
+template <int ACT, bool F32>
+__global__ void __launch_bounds__(kGradThreads) k_act_grad(GradArgs p)
 {
-    __shared__ float red[8][kGradCols];
+    __shared__ float red[kGradGroups][kGradCols];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int c = blockIdx.x * kGradCols + lane * 4;
-    const int left = min(4, p.N - c);
+    const int c = blockIdx.x * kGradCols + lane * 8;
+    const int left = min(8, p.N - c);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = int64_t(blockIdx.y) * p.rows;
     const int64_t t1 = min(int64_t(p.T), t0 + p.rows);
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[8] = {};
     if (left > 0)
-        for (int64_t t = t0 + g; t < t1; t += 8) {
-            float d[4];
-            load4(d, p.dy, t * p.lddy + c, left, p.dy_f32, p.f16, p.vec_dy);
-            if (p.act != MOE_ACT_NONE) {
-                float z[4];
-                load4(z, p.pre, t * p.N + c, left, 0, p.f16, p.vec_pre);
+        for (int64_t t = t0 + g; t < t1; t += kGradGroups * kGradUnroll) {
+            Eight<F32> dy[kGradUnroll];
+            Eight<false> pre[kGradUnroll];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    d[i] *= act_grad(z[i], p.act);
+            for (int u = 0; u < kGradUnroll; ++u) {
+                const int64_t r = t + u * kGradGroups;
+                if (r < t1) {
+                    dy[u].load(p.dy, r * p.lddy + c, left, p.vec);
+                    if (ACT != MOE_ACT_NONE)
+                        pre[u].load(p.pre, r * p.N + c, left, p.vec);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s[i] += d[i];
-            if (p.dp)  // lddp is a multiple of 8 and c of 4
-                store4(d, p.dp, t * p.lddp + c, left, 0, p.f16, true);
+            for (int u = 0; u < kGradUnroll; ++u) {
+                const int64_t r = t + u * kGradGroups;
+                if (r >= t1)
+                    break;
+                float d[8];
+                dy[u].to(d, p.f16);
+                if (ACT != MOE_ACT_NONE) {
+                    float z[8];
+                    pre[u].to(z, p.f16);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[i] *= act_grad<ACT>(z[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s[i] += i < left ? d[i] : 0.0f;
+                if (p.dp) {  // lddp is a multiple of 8: whole vectors, past N too
+                    *reinterpret_cast<uint4 *>(p.dp + r * p.lddp + c) =
+                        make_uint4(pack16(d[0], d[1], p.f16), pack16(d[2], d[3], p.f16),
+                                   pack16(d[4], d[5], p.f16), pack16(d[6], d[7], p.f16));
+                }
+            }
         }
     if (!p.part)
         return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        red[g][lane * 4 + i] = s[i];
+    for (int i = 0; i < 8; ++i)
+        red[g][lane * 8 + i] = s[i];
     __syncthreads();
     const int col = blockIdx.x * kGradCols + threadIdx.x;
-    if (threadIdx.x < kGradCols && col < p.N) {
+    if (col < p.N) {
         float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kGradGroups; ++i)
             v += red[i][threadIdx.x];
         p.part[int64_t(blockIdx.y) * p.N + col] = v;
     }
 }
 
+// db: the chunks' column sums; a CTA takes 32 columns, its warps every eighth
+// chunk, added in order.
 __global__ void __launch_bounds__(kGradThreads)
     k_col_sum(const float *part, int chunks, int N, float *db)
 {
+    __shared__ float red[kGradGroups][32];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     pdl_wait();
     pdl_launch_dependents();
-    const int c = blockIdx.x * kGradThreads + threadIdx.x;
-    if (c >= N)
-        return;
     float v = 0.0f;
-    for (int i = 0; i < chunks; ++i)
-        v += part[int64_t(i) * N + c];
-    db[c] = v;
+    if (c < N) {
+#pragma unroll 8
+        for (int i = g; i < chunks; i += kGradGroups)
+            v += part[int64_t(i) * N + c];
+    }
+    red[g][lane] = v;
+    __syncthreads();
+    if (g == 0 && c < N) {
+#pragma unroll
+        for (int i = 1; i < kGradGroups; ++i)
+            v += red[i][lane];
+        db[c] = v;
+    }
+}
+
+void (*act_grad_kernel(int act, bool f32))(GradArgs)
+{
+    switch (act) {
+    case MOE_ACT_RELU:
+        return f32 ? k_act_grad<MOE_ACT_RELU, true> : k_act_grad<MOE_ACT_RELU, false>;
+    case MOE_ACT_SILU:
+        return f32 ? k_act_grad<MOE_ACT_SILU, true> : k_act_grad<MOE_ACT_SILU, false>;
+    case MOE_ACT_GELU:
+        return f32 ? k_act_grad<MOE_ACT_GELU, true> : k_act_grad<MOE_ACT_GELU, false>;
+    case MOE_ACT_GELU_TANH:
+        return f32 ? k_act_grad<MOE_ACT_GELU_TANH, true> : k_act_grad<MOE_ACT_GELU_TANH, false>;
+    default:
+        return f32 ? k_act_grad<MOE_ACT_NONE, true> : k_act_grad<MOE_ACT_NONE, false>;
+    }
 }
 
 // ---- host ---------------------------------------------------------------------
@@ -782,37 +1166,89 @@ cudaError_t launch_clustered(const void *kern, unsigned grid, unsigned cluster, 
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
-// D[m][n] = sum_r A[m][r] B[n][r]; a.M, a.N, a.R and the epilogue fields are
-// set, the tiling is chosen here.
-template <bool A_MN, bool B_MN>
-cudaError_t launch_linear(const Operand &A, const Operand &B, LinArgs a, cudaStream_t s)
+// Tiling of a product, chosen by estimated SM cycles.
+struct Tiling {
+    bool pair;
+    int bn, split;
+};
+
+// What k_linear_pair is estimated to take.  Per 64 of r a tile of 256 x bn
+// costs 2 bn cycles of MMA, or the time its operands take to arrive (16 KB
+// and 128 bytes a row of B, at about 85 bytes a cycle as measured).  A tile's
+// epilogue (about 1200 cycles per 64 columns) hides behind the next tile's
+// MMAs, except the last one's; starting takes about 5000 cycles, and adding
+// the parts of a split tile about as long again.
+double pair_cycles(int64_t tiles, int pairs, int bn, int split, int nk, bool col_mn)
 {
-    constexpr int which = B_MN ? 2 : A_MN ? 1 : 0;
+    const int half = col_mn ? (bn / 2 + 63) / 64 * 64 : bn / 2;
+    const double step = std::max(2.0 * bn, (16384.0 + 128.0 * half) / 85.0);
+    const double main = step * ((nk + split - 1) / split), epi = 1200.0 * ((bn + 63) / 64);
+    if (split > 1)
+        return 10000.0 + main;
+    const int64_t waves = (tiles + pairs - 1) / pairs;
+    return 5000.0 + std::max(main, epi) * double(waves - 1) + main + epi;
+}
+
+Tiling choose_tiling(int64_t rows, int64_t cols, int nk, int sms, bool col_mn)
+{
+    Tiling t{false, 0, 1};
+    if (rows <= 128)
+        return t;
+    double best = 0.0;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const int64_t tiles = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
+        for (int z = 1; z <= kPairMaxSplit; z *= 2) {
+            // a split tile needs room for the parts beside the ring
+            if (z > 1 && (nk / z < 4 || tiles * z > sms / 2 || (bn != 64 && bn != 128)))
+                break;
+            const double c = pair_cycles(tiles, sms / 2, bn, z, nk, col_mn);
+            if (!t.pair || c < best) {
+                t = Tiling{true, bn, z};
+                best = c;
+            }
+        }
+    }
+    return t;
+}
+
+// out[i][j] = sum_r X[i][r] Y[j][r]; a's epilogue fields are set.
+template <bool X_MN, bool Y_MN>
+cudaError_t launch_linear(const Operand &X, const Operand &Y, int rows, int cols, int R, LinArgs a,
+                          cudaStream_t s)
+{
+    constexpr int which = X_MN ? 2 : Y_MN ? 1 : 0;
     const int sms = device_sm_count();
-    const int nk = (a.R + LK - 1) / LK;
+    const int nk = (R + LK - 1) / LK;
+    a.R = R;
     CUtensorMap ma, mb;
-    const int64_t pair_tiles = int64_t((a.M + 2 * LM - 1) / (2 * LM)) * ((a.N + 255) / 256);
-    if (pair_tiles >= sms / 2) {  // at least one tile for every pair of SMs
-        a.bn = 256;
-        a.n_mt = (a.M + 2 * LM - 1) / (2 * LM);
-        a.split = 1;
+    void *args[] = {&ma, &mb, &a};
+    const Tiling t = choose_tiling(rows, cols, nk, sms, Y_MN);
+    if (t.pair) {
+        a.M = rows, a.N = cols;
+        a.bn = t.bn, a.split = t.split;
+        a.n_mt = (rows + 2 * LM - 1) / (2 * LM);
         a.stages = kPairStages;
-        const size_t smem = 1024 + size_t(a.stages) * (kLinATile + a.bn / 2 * LK * 2);
-        cudaError_t e = lin_map(&ma, A.p, A.rows, A.cols, A.ld, A_MN ? LK : LM, a.f16);
+        const int64_t tiles = int64_t(a.n_mt) * ((cols + a.bn - 1) / a.bn);
+        const size_t smem =
+            1024 + size_t(a.stages) * kPairSub * pair_sub_bytes(a.bn, Y_MN) +
+            (a.split > 1 ? size_t(LM) * (a.bn + 4) * 4 : size_t(kPairEpiWarps) * kPairStg);
+        cudaError_t e = lin_map(&ma, X.p, X.rows, X.cols, X.ld, X_MN ? LK : LM, a.f16);
         if (e == cudaSuccess)
-            e = lin_map(&mb, B.p, B.rows, B.cols, B.ld, B_MN ? LK : a.bn / 2, a.f16);
-        const void *kern = reinterpret_cast<const void *>(k_linear_pair<A_MN, B_MN>);
+            e = lin_map(&mb, Y.p, Y.rows, Y.cols, Y.ld, Y_MN ? LK : a.bn / 2, a.f16);
+        const void *kern = reinterpret_cast<const void *>(k_linear_pair<X_MN, Y_MN>);
         if (e == cudaSuccess)
-            e = ensure_smem_limit(kern, kSlotLinearPair0 + which, smem);
+            e = ensure_smem_limit(kern, kSlotLinearPair0 + which, 226 * 1024);
         if (e != cudaSuccess)
             return e;
-        void *args[] = {&ma, &mb, &a};
-        return launch_clustered(kern, unsigned(std::min<int64_t>(pair_tiles, sms / 2)) * 2, 2,
+        const int64_t clusters =
+            a.split > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, sms / 2));
+        return launch_clustered(kern, unsigned(clusters * 2 * a.split), unsigned(2 * a.split),
                                 kPairThreads, smem, s, args);
     }
-    a.bn = a.N <= 16 ? 16 : a.N <= 32 ? 32 : a.N <= 64 ? 64 : 128;
-    a.n_mt = (a.M + LM - 1) / LM;
-    const int64_t tiles = int64_t(a.n_mt) * ((a.N + a.bn - 1) / a.bn);
+    a.M = cols, a.N = rows;
+    a.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    a.n_mt = (cols + LM - 1) / LM;
+    const int64_t tiles = int64_t(a.n_mt) * ((rows + a.bn - 1) / a.bn);
     // split the reduction while that still adds CTAs (two fit an SM) and
     // leaves each at least four stages
     a.split = 1;
@@ -820,19 +1256,18 @@ cudaError_t launch_linear(const Operand &A, const Operand &B, LinArgs a, cudaStr
         a.split *= 2;
     if (tiles * a.split > INT_MAX)
         return cudaErrorInvalidValue;
-    const uint32_t stage = kLinATile + lin_b_tile(a.bn, B_MN);
+    const uint32_t stage = kLinATile + lin_b_tile(a.bn, X_MN);
     a.stages = std::min<int>(kLinMaxStages, 96 * 1024 / stage);
     const size_t ring = size_t(a.stages) * stage;
     const size_t smem = 1024 + std::max(ring, size_t(a.bn) * LM * 4);
-    cudaError_t e = lin_map(&ma, A.p, A.rows, A.cols, A.ld, A_MN ? LK : LM, a.f16);
+    cudaError_t e = lin_map(&ma, Y.p, Y.rows, Y.cols, Y.ld, Y_MN ? LK : LM, a.f16);
     if (e == cudaSuccess)
-        e = lin_map(&mb, B.p, B.rows, B.cols, B.ld, B_MN ? LK : a.bn, a.f16);
-    const void *kern = reinterpret_cast<const void *>(k_linear<A_MN, B_MN>);
+        e = lin_map(&mb, X.p, X.rows, X.cols, X.ld, X_MN ? LK : a.bn, a.f16);
+    const void *kern = reinterpret_cast<const void *>(k_linear<Y_MN, X_MN>);
     if (e == cudaSuccess)
         e = ensure_smem_limit(kern, kSlotLinear0 + which, 112 * 1024);
     if (e != cudaSuccess)
         return e;
-    void *args[] = {&ma, &mb, &a};
     return launch_clustered(kern, unsigned(tiles * a.split), unsigned(a.split), kLinThreads, smem, s,
                             args);
 }
@@ -847,10 +1282,10 @@ inline size_t align256(size_t b)
     return (b + 255) & ~size_t(255);
 }
 
-// whether groups of four elements of rows `ld` apart are aligned accesses
-inline int vec4(const void *p, int64_t ld, int size)
+// whether 16-byte pieces of rows `ld` apart are aligned accesses (so are groups of four)
+inline int vec16(const void *p, int64_t ld, int size)
 {
-    return ld % 4 == 0 && aligned(p, 4 * size);
+    return ld * size % 16 == 0 && aligned(p, 16);
 }
 
 inline bool is16(int dtype)
@@ -887,11 +1322,10 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
     a.out = y;
     a.status = status;
     a.ldr = ldr, a.ldo = ldy, a.ldp = N;
-    a.M = N, a.N = T, a.R = K;
     a.f16 = dtype == MOE_DT_F16, a.out_f32 = y_dtype == MOE_DT_F32, a.act = act;
-    a.vec_out = vec4(y, ldy, ysize), a.vec_res = vec4(residual, ldr, ysize);
-    a.vec_pre = vec4(pre, N, 2);
-    return launch_linear<false, false>({W, N, K, K}, {x, T, K, ldx}, a,
+    a.vec_out = vec16(y, ldy, ysize), a.vec_res = vec16(residual, ldr, ysize);
+    a.vec_pre = vec16(pre, N, 2);
+    return launch_linear<false, false>({x, T, K, ldx}, {W, N, K, K}, T, N, K, a,
                                        reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
@@ -944,6 +1378,7 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     // dy is the products' operand as it is
     const bool direct =
         act == MOE_ACT_NONE && dy_dtype == dtype && lddy % 8 == 0 && aligned(dy, 16);
+    int chunks = 0;
     if (db || (products && !direct)) {
         GradArgs g = {};
         g.dy = dy, g.pre = pre;
@@ -951,18 +1386,15 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
         g.part = db ? part : nullptr;
         g.lddy = lddy, g.lddp = ldp;
         g.T = T, g.N = N;
-        g.dy_f32 = dy_dtype == MOE_DT_F32, g.f16 = dtype == MOE_DT_F16, g.act = act;
-        g.vec_dy = vec4(dy, lddy, dysize), g.vec_pre = vec4(pre, N, 2);
+        g.f16 = dtype == MOE_DT_F16, g.act = act;
+        g.vec = vec16(dy, lddy, dysize) && (act == MOE_ACT_NONE || vec16(pre, N, 2));
         const int cb = (N + kGradCols - 1) / kGradCols;
-        int chunks = std::max(1, std::min({(T + 31) / 32, 8 * device_sm_count() / cb,
-                                           kGradMaxChunks}));
+        // about eight CTAs an SM, each with at least one round of rows
+        chunks = std::max(1, std::min({(T + 31) / 32, 8 * device_sm_count() / cb, kGradMaxChunks}));
         g.rows = (T + chunks - 1) / chunks;
         chunks = (T + g.rows - 1) / g.rows;
-        if (launch_pdl(k_act_grad, dim3(cb, chunks), dim3(kGradThreads), 0, s, g) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        if (db && launch_pdl(k_col_sum, dim3((N + kGradThreads - 1) / kGradThreads),
-                             dim3(kGradThreads), 0, s, static_cast<const float *>(part), chunks,
-                             N, db) != cudaSuccess)
+        if (launch_pdl(act_grad_kernel(act, dy_dtype == MOE_DT_F32), dim3(cb, chunks),
+                       dim3(kGradThreads), 0, s, g) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     const Operand P = direct ? Operand{dy, T, N, lddy} : Operand{dp, T, N, ldp};
@@ -973,18 +1405,19 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     a.ldo = K;
     if (dx) {
         a.out = dx;
-        a.M = K, a.N = T, a.R = N;
-        a.vec_out = vec4(dx, K, 2);
-        if (launch_linear<true, false>({W, N, K, K}, P, a, s) != cudaSuccess)
+        a.vec_out = vec16(dx, K, 2);
+        if (launch_linear<false, true>(P, {W, N, K, K}, T, K, N, a, s) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     if (dW) {
         a.out = dW;
         a.out_f32 = dw_dtype == MOE_DT_F32;
-        a.M = K, a.N = N, a.R = T;
-        a.vec_out = vec4(dW, K, dwsize);
-        if (launch_linear<true, true>({x, T, K, ldx}, P, a, s) != cudaSuccess)
+        a.vec_out = vec16(dW, K, dwsize);
+        if (launch_linear<true, true>(P, {x, T, K, ldx}, N, K, T, a, s) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
+    if (db && launch_pdl(k_col_sum, dim3((N + 31) / 32), dim3(kGradThreads), 0, s,
+                         static_cast<const float *>(part), chunks, N, db) != cudaSuccess)
+        return MOE_ERR_CUDA;
     return MOE_OK;
 }

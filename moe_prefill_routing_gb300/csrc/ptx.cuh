@@ -30,6 +30,20 @@ __device__ __forceinline__ uint32_t lanemask_lt()
     return m;
 }
 
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---- programmatic dependent launch -----------------------------------------
 
 // Blocks until the preceding kernel in the stream has completed and its
@@ -59,6 +73,17 @@ __device__ __forceinline__ uint32_t cluster_nctarank()
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
+}
+
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Every thread of every CTA of the cluster; orders memory at cluster scope.
@@ -357,16 +382,14 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                  : "memory");
 }
 
-// Arrives once on `bar` of both CTAs when what this thread issued completes.
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar)
+// Arrives once on `bar` of each CTA in `ctas` (a bit per rank of the cluster)
+// when what this thread issued completes.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar, uint16_t ctas)
 {
     asm volatile(
-        "{\n"
-        ".reg .b16 m;\n"
-        "mov.b16 m, 3;\n"
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-        ".b64 [%0], m;\n"
-        "}\n" ::"r"(smem_u32(bar))
+        ".b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(ctas)
         : "memory");
 }
 
@@ -387,6 +410,16 @@ __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t a_desc
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// 32 lanes x 8 consecutive 32-bit columns, as below.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
                  : "memory");
 }
 
