@@ -599,57 +599,63 @@ def layer_forward_mxfp4(x, ids, w, Wg: Mxfp4, Wu: Mxfp4, Wd: Mxfp4, tm: int, y=N
 
 # ---- router and dense projections ------------------------------------------
 #
-# Calls of a few microseconds on the GPU: the checks below are written to cost
-# well under a microsecond each, and outputs made here are not checked again.
+# Calls of a few microseconds on the GPU, so what Python does per call counts:
+# checks are single comparisons, and outputs made here are not checked again.
 
 _DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
 _16 = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_MASK = (torch.bool, torch.uint8)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_fns: dict = {}
 
 
 def _launch(name: str, dev, *args):
     """The library's entry point `name` with the device's current stream, the
     device being current."""
-    fn = getattr(_lib or lib(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(dev.index))
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev.index))
-    if rc != MOE_OK:
+            rc = fn(*args, _raw_stream(i))
+    if rc:
         raise MoeError(name, rc)
 
 
-def _refuse(t, name: str, shape, dtypes):
+def _refuse(t, name: str, shape, dtypes, dev):
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: unexpected dtype {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
     raise ValueError(f"{name}: expected a contiguous tensor"
-                     if len(shape) < 2 else f"{name}: expected contiguous rows")
+                     if t.dim() < 2 or t.stride(1) == 1 else f"{name}: expected contiguous rows")
 
 
-def _flat(t, name: str, shape, *dtypes):
-    """Address of a contiguous tensor of the given shape and type; None stays."""
-    if t is None:
-        return None
-    if (t.shape != shape or t.dtype not in dtypes or not t.is_cuda
-            or not t.is_contiguous()):
-        _refuse(t, name, shape, dtypes)
+def _flat(t, name: str, shape, dtypes, dev):
+    """Address of a contiguous tensor of the given shape and type on dev."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
+        _refuse(t, name, shape, dtypes, dev)
     return t.data_ptr()
 
 
-def _ld(t, name: str, shape, dtypes) -> int:
+def _ld(t, name: str, shape, dtypes, dev) -> int:
     """Elements between the rows of a 2-D tensor whose rows are contiguous and
     may lie further apart than their length."""
-    if t.shape != shape or t.dtype not in dtypes or not t.is_cuda:
-        _refuse(t, name, shape, dtypes)
-    rows, cols = shape
+    if t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_cuda:
+        _refuse(t, name, shape, dtypes, dev)
     step, one = t.stride()
+    rows, cols = shape
     if one != 1 and cols > 1:
-        _refuse(t, name, shape, dtypes)
+        _refuse(t, name, shape, dtypes, dev)
     return step if rows > 1 else (cols + 7) // 8 * 8
 
 
@@ -673,27 +679,31 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
     N = W.shape[0]
     dt = x.dtype
     dev = x.device
-    ldx = _ld(x, "x", (T, K), _16)
+    ldx = _ld(x, "x", (T, K), _16, dev)
+    wp = _flat(W, "W", (N, K), (dt,), dev)
     if y is None:
         y = torch.empty((T, N), dtype=out_dtype or dt, device=dev)
         ldy = N
-        if y.dtype is not dt and y.dtype is not torch.float32:
-            raise ValueError(f"out_dtype: unexpected dtype {y.dtype}")
+        if out_dtype is not None and out_dtype != dt and out_dtype != torch.float32:
+            raise ValueError(f"out_dtype: unexpected dtype {out_dtype}")
     elif out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"y: expected {out_dtype}, got {y.dtype}")
     else:
-        ldy = _ld(y, "y", (T, N), (dt, torch.float32))
-    ldr = 0 if residual is None else _ld(residual, "residual", (T, N), (y.dtype,))
-    _launch("moe_linear", dev, x.data_ptr(), ldx, _flat(W, "W", (N, K), dt),
-            _flat(bias, "bias", (N,), torch.float32),
-            None if residual is None else residual.data_ptr(), ldr, _16[dt],
-            _name(ACTS, act, "act"), T, K, N, _flat(pre, "pre", (T, N), dt), y.data_ptr(), ldy,
-            _DTYPES[y.dtype], _ptr(status))
+        ldy = _ld(y, "y", (T, N), (dt, torch.float32), dev)
+    rp, ldr = None, 0
+    if residual is not None:
+        ldr = _ld(residual, "residual", (T, N), (y.dtype,), dev)
+        rp = residual.data_ptr()
+    _launch("moe_linear", dev, x.data_ptr(), ldx, wp,
+            None if bias is None else _flat(bias, "bias", (N,), _F32, dev), rp, ldr, _16[dt],
+            _name(ACTS, act, "act"), T, K, N,
+            None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev), y.data_ptr(), ldy,
+            _DTYPES[y.dtype], None if status is None else _ptr(status))
     return y
 
 
 def linear_grad_workspace_bytes(T: int, N: int) -> int:
-    return int((_lib or lib()).moe_linear_grad_workspace_bytes(T, N))
+    return int(lib().moe_linear_grad_workspace_bytes(T, N))
 
 
 def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), dw_dtype=None,
@@ -708,29 +718,41 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
     N = W.shape[0]
     dt = x.dtype
     dev = x.device
-    ldx = _ld(x, "x", (T, K), _16)
-    lddy = _ld(dy, "dy", (T, N), (dt, torch.float32))
-    if need[0] and dx is None:
-        dx = torch.empty((T, K), dtype=dt, device=dev)
-    if need[1] and dW is None:
-        dW = torch.empty((N, K), dtype=dw_dtype or dt, device=dev)
-    elif dW is not None and dw_dtype is not None and dW.dtype != dw_dtype:
+    ldx = _ld(x, "x", (T, K), _16, dev)
+    wp = _flat(W, "W", (N, K), (dt,), dev)
+    lddy = _ld(dy, "dy", (T, N), (dt, torch.float32), dev)
+    if dW is not None and dw_dtype is not None and dW.dtype != dw_dtype:
         raise ValueError(f"dW: expected {dw_dtype}, got {dW.dtype}")
-    if need[2] and db is None:
+    dxp = dWp = dbp = None
+    dw_code = _16[dt]
+    if dx is not None:
+        dxp = _flat(dx, "dx", (T, K), (dt,), dev)
+    elif need[0]:
+        dx = torch.empty((T, K), dtype=dt, device=dev)
+        dxp = dx.data_ptr()
+    if dW is not None:
+        dWp = _flat(dW, "dW", (N, K), (dt, torch.float32), dev)
+        dw_code = _DTYPES[dW.dtype]
+    elif need[1]:
+        dW = torch.empty((N, K), dtype=dw_dtype or dt, device=dev)
+        dWp = dW.data_ptr()
+        dw_code = _DTYPES.get(dW.dtype, -1)
+    if db is not None:
+        dbp = _flat(db, "db", (N,), _F32, dev)
+    elif need[2]:
         db = torch.empty(N, dtype=torch.float32, device=dev)
+        dbp = db.data_ptr()
     if ws is None:
         ws = torch.empty(linear_grad_workspace_bytes(T, N), dtype=torch.uint8, device=dev)
-    _launch("moe_linear_grad", dev, x.data_ptr(), ldx, _flat(W, "W", (N, K), dt),
-            _flat(pre, "pre", (T, N), dt), dy.data_ptr(), lddy, _DTYPES[dy.dtype], _16[dt],
-            _name(ACTS, act, "act"), T, K, N, _flat(dx, "dx", (T, K), dt),
-            _flat(dW, "dW", (N, K), dt, torch.float32),
-            _DTYPES[dt if dW is None else dW.dtype], _flat(db, "db", (N,), torch.float32),
-            _ptr(ws), ws.numel(), _ptr(status))
+    _launch("moe_linear_grad", dev, x.data_ptr(), ldx, wp,
+            None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev), dy.data_ptr(), lddy,
+            _DTYPES[dy.dtype], _16[dt], _name(ACTS, act, "act"), T, K, N, dxp, dWp, dw_code, dbp,
+            _ptr(ws), ws.numel(), None if status is None else _ptr(status))
     return dx, dW, db
 
 
 def route_workspace_bytes(T: int, E: int) -> int:
-    return int((_lib or lib()).moe_route_workspace_bytes(T, E))
+    return int(lib().moe_route_workspace_bytes(T, E))
 
 
 def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bool = True,
@@ -745,30 +767,37 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
     for padding.  ``out`` may hold some of the outputs."""
     T, E = logits.shape
     dev = logits.device
-    ld = _ld(logits, "logits", (T, E), _DTYPES)
-    o = {} if out is None else dict(out)
-
-    def output(name, shape, dtype):
-        t = o.get(name)
-        if t is not None:
-            return _flat(t, name, shape, dtype)
-        t = o[name] = torch.empty(shape, dtype=dtype, device=dev)
-        return t.data_ptr()
-
-    ids, w = output("ids", (T, k), torch.int32), output("w", (T, k), torch.float32)
-    counts = prob = loss = None
-    if stats:
-        counts = output("counts", (E + 1,), torch.int32)
-        prob = output("prob", (E,), torch.float32)
-        loss = output("loss", (2,), torch.float32)
+    ld = _ld(logits, "logits", (T, E), _DTYPES, dev)
     if ws is None:
         ws = torch.empty(route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
-    o["ws"] = ws
+    cp = pp = sp = None
+    if out is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        o = {"ids": ids, "w": w, "ws": ws}
+        ip, wp = ids.data_ptr(), w.data_ptr()
+        if stats:
+            counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+            prob = torch.empty(E, dtype=torch.float32, device=dev)
+            loss = torch.empty(2, dtype=torch.float32, device=dev)
+            o["counts"], o["prob"], o["loss"] = counts, prob, loss
+            cp, pp, sp = counts.data_ptr(), prob.data_ptr(), loss.data_ptr()
+    else:
+        o = dict(out, ws=ws)
+
+        def output(name, shape, dtypes):
+            if o.get(name) is None:
+                o[name] = torch.empty(shape, dtype=dtypes[0], device=dev)
+            return _flat(o[name], name, shape, dtypes, dev)
+
+        ip, wp = output("ids", (T, k), _I32), output("w", (T, k), _F32)
+        if stats:
+            cp, pp = output("counts", (E + 1,), _I32), output("prob", (E,), _F32)
+            sp = output("loss", (2,), _F32)
     _launch("moe_route", dev, logits.data_ptr(), ld, _DTYPES[logits.dtype],
-            _flat(bias, "bias", (E,), torch.float32),
-            _flat(mask, "mask", (T,), torch.bool, torch.uint8), T, E, k,
-            _name(SCORES, score, "score"), norm, scale, ids, w, counts, prob, loss, _ptr(ws),
-            ws.numel())
+            None if bias is None else _flat(bias, "bias", (E,), _F32, dev),
+            None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, E, k,
+            _name(SCORES, score, "score"), norm, scale, ip, wp, cp, pp, sp, _ptr(ws), ws.numel())
     return o
 
 
@@ -782,18 +811,19 @@ def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: 
     k = ids.shape[1]
     dt = logits.dtype
     dev = logits.device
-    ld = _ld(logits, "logits", (T, E), _DTYPES)
+    ld = _ld(logits, "logits", (T, E), _DTYPES, dev)
+    ip = _flat(ids, "ids", (T, k), _I32, dev)
     if dlogits is None:
         dlogits = torch.empty((T, E), dtype=dt, device=dev)
         ldd = E
     else:
-        ldd = _ld(dlogits, "dlogits", (T, E), (dt,))
+        ldd = _ld(dlogits, "dlogits", (T, E), (dt,), dev)
     _launch("moe_route_grad", dev, logits.data_ptr(), ld, _DTYPES[dt],
-            _flat(mask, "mask", (T,), torch.bool, torch.uint8),
-            _flat(ids, "ids", (T, k), torch.int32),
-            _flat(counts, "counts", (E + 1,), torch.int32),
-            _flat(dw, "dw", (T, k), torch.float32), _flat(dloss, "dloss", (2,), torch.float32),
-            T, E, k, _name(SCORES, score, "score"), norm, scale, dlogits.data_ptr(), ldd)
+            None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), ip,
+            None if counts is None else _flat(counts, "counts", (E + 1,), _I32, dev),
+            None if dw is None else _flat(dw, "dw", (T, k), _F32, dev),
+            None if dloss is None else _flat(dloss, "dloss", (2,), _F32, dev), T, E, k,
+            _name(SCORES, score, "score"), norm, scale, dlogits.data_ptr(), ldd)
     return dlogits
 
 

@@ -170,10 +170,8 @@ enum SmemSlot {
     kSlotDownNative,
     kSlotGateUpMx4,
     kSlotDownMx4,
-    kSlotLinear0,  // the dense products: forward, dx, dW
-    kSlotLinear2 = kSlotLinear0 + 2,
-    kSlotLinearPair0,  // the same on CTA pairs
-    kSlotLinearPair2 = kSlotLinearPair0 + 2,
+    kSlotLinear,
+    kSlotLinearPair,
     kSlotCount
 };
 

@@ -47,7 +47,8 @@ struct LinArgs {
     void *out;
     uint32_t *status;
     int64_t ldr, ldo, ldp;
-    int M, N, R;  // k_linear: M = j, N = i; k_linear_pair: M = i, N = j
+    int M, N, R;     // k_linear: M = j, N = i; k_linear_pair: M = i, N = j
+    int a_mn, b_mn;  // the operand's m (n) is contiguous, not its r
     int bn, stages, split, n_mt;
     int f16, out_f32, act;
     int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
@@ -61,7 +62,7 @@ struct LinCtrl {
     int abort_flag;
 };
 
-__host__ __device__ __forceinline__ uint32_t lin_b_tile(int bn, bool b_mn)
+__host__ __device__ __forceinline__ uint32_t lin_b_tile(int bn, int b_mn)
 {
     return uint32_t(b_mn && bn < 64 ? 64 : bn) * LK * 2;
 }
@@ -260,7 +261,6 @@ __device__ __forceinline__ void lin_drain(uint64_t *bar, uint32_t parity)
             return;
 }
 
-template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kLinThreads)
     k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const LinArgs p)
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kLinThreads)
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
     const int bn = p.bn, S = p.stages;
-    const uint32_t b_bytes = lin_b_tile(bn, B_MN);
+    const uint32_t b_bytes = lin_b_tile(bn, p.b_mn);
     const uint32_t stage_bytes = kLinATile + b_bytes;
     const uint32_t z = cluster_ctarank();
     const int tile = int(blockIdx.x) / p.split;
@@ -318,13 +318,13 @@ __global__ void __launch_bounds__(kLinThreads)
                 mbar_arrive_expect_tx(fb, stage_bytes);
                 uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
                 const int k0 = kb * LK;
-                if (A_MN) {  // 64 m x 64 r boxes, m contiguous
+                if (p.a_mn) {  // 64 m x 64 r boxes, m contiguous
                     tma_load_2d(sa, &map_a, fb, m0, k0);
                     tma_load_2d(sa + 8192, &map_a, fb, m0 + 64, k0);
                 } else {
                     tma_load_2d(sa, &map_a, fb, k0, m0);
                 }
-                if (B_MN) {
+                if (p.b_mn) {
                     for (int c = 0; c < bn; c += 64)
                         tma_load_2d(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
                 } else {
@@ -348,14 +348,14 @@ __global__ void __launch_bounds__(kLinThreads)
         // descriptors and addresses stay warp-uniform
         int stage = 0;
         uint32_t phase = 0;
-        uint32_t idesc = idesc_bf16_f32(LM, uint32_t(bn), A_MN, B_MN);
+        uint32_t idesc = idesc_bf16_f32(LM, uint32_t(bn), p.a_mn, p.b_mn);
         if (p.f16)
             idesc &= ~((7u << 7) | (7u << 10));  // f16 operands: format 0
         const uint32_t sa = smem_u32(smem), sb = sa + kLinATile;
         // r contiguous: 16 of them are 32 bytes inside the 128-byte row; m or n
         // contiguous: 16 rows of 128 bytes, 64-element chunks 8 KB apart
-        const uint64_t da0 = A_MN ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
-        const uint64_t db0 = B_MN ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
+        const uint64_t da0 = p.a_mn ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
+        const uint64_t db0 = p.b_mn ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
         const bool one = elect_one();
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!__all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag)))
@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kLinThreads)
                 const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
 #pragma unroll
                 for (int kk = 0; kk < LK / 16; ++kk)
-                    tc_mma_f16(tmem_base, da0 + off + kk * (A_MN ? 128 : 2),
-                               db0 + off + kk * (B_MN ? 128 : 2), idesc, kb != kb0 || kk != 0);
+                    tc_mma_f16(tmem_base, da0 + off + kk * (p.a_mn ? 128 : 2),
+                               db0 + off + kk * (p.b_mn ? 128 : 2), idesc, kb != kb0 || kk != 0);
                 tc_commit(&ctl.empty[stage]);
             }
             __syncwarp();
@@ -451,6 +451,9 @@ __global__ void __launch_bounds__(kLinThreads)
 // the next 32 columns are read from tensor memory (about 330 cycles) ahead.
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
+//
+// A launch takes one product or two (dx and dW): two short launches would
+// each leave SMs idle in their last round and pay the start twice.
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairSub = 2;     // 64-r halves of a stage
@@ -467,10 +470,27 @@ struct PairCtrl {
     int abort_flag;
 };
 
-__host__ __device__ __forceinline__ uint32_t pair_sub_bytes(int bn, bool b_mn)
+struct PairArgs {
+    CUtensorMap a[2], b[2];
+    LinArgs p[2];
+    int tiles[2];       // 0 for an absent second product
+    int bn;             // the larger of the two
+    uint32_t sub_bytes; // of shared memory for 64 r of both operands
+    // Pair q of the grid's first takes tiles q, q + pairs, ... of product 0;
+    // the `extra` pairs that get one more of them take at most `shared`
+    // tiles of product 1, the others what is left.
+    int shared;
+    // sums of `chunks` rows of partial column sums, or null
+    const float *part;
+    float *db;
+    int chunks, db_n;
+};
+
+// What one CTA loads of B per 64 r.
+__host__ __device__ __forceinline__ uint32_t pair_b_bytes(int bn, int b_mn)
 {
     const int half = bn / 2;
-    return kLinATile + uint32_t(b_mn ? (half + 63) / 64 * 64 : half) * (LK * 2);
+    return uint32_t(b_mn ? (half + 63) / 64 * 64 : half) * (LK * 2);
 }
 
 // A warp's staging tile: 32 rows of 32 elements E, in 16-byte pieces; piece c
@@ -631,10 +651,8 @@ __device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float
                    p.vec_out);
 }
 
-template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    k_linear_pair(const __grid_constant__ CUtensorMap map_a,
-                  const __grid_constant__ CUtensorMap map_b, const LinArgs p)
+    k_linear_pair(const __grid_constant__ PairArgs g)
 {
     extern __shared__ uint8_t smem_raw[];
     // the same offset in every CTA: dynamic shared memory starts at the same address
@@ -645,16 +663,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
     const uint32_t rank = crank & 1u, lead = crank & ~1u;  // place in the pair, its even CTA
-    const int z = int(crank >> 1), Z = p.split;
-    const int bn = p.bn, half = bn / 2, S = p.stages;
-    const uint32_t sub_bytes = pair_sub_bytes(bn, B_MN);
+    const int z = int(crank >> 1), Z = g.p[0].split;
+    constexpr int S = kPairStages;
+    const uint32_t sub_bytes = g.sub_bytes;
     uint8_t *stg = smem + S * kPairSub * sub_bytes;
-    const uint32_t tmem_cols = bn <= 64 ? 128u : bn <= 128 ? 256u : 512u;  // two accumulators
-    const int nk = (p.R + LK - 1) / LK;
-    const int kb0 = int(int64_t(nk) * z / Z), kb1 = int(int64_t(nk) * (z + 1) / Z);
-    const int n_nt = (p.N + bn - 1) / bn;
-    const int64_t tiles = int64_t(p.n_mt) * n_nt;
-    const int64_t first = blockIdx.x / (2 * Z), step = gridDim.x / (2 * Z);
+    const uint32_t tmem_cols = g.bn <= 64 ? 128u : g.bn <= 128 ? 256u : 512u;  // two accumulators
     volatile int *abort_flag = &ctl.abort_flag;
 
     if (threadIdx.x == 0) {
@@ -668,8 +681,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         ctl.abort_flag = 0;
         fence_mbar_init();
-        prefetch_tmap(&map_a);
-        prefetch_tmap(&map_b);
+        for (int i = 0; i < (g.tiles[1] ? 2 : 1); ++i) {
+            prefetch_tmap(&g.a[i]);
+            prefetch_tmap(&g.b[i]);
+        }
     }
     __syncwarp();
     cluster_arrive();
@@ -683,35 +698,60 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // Tiles in blocks of 16 m tiles, m fastest: the pairs running at one time
-    // share few rows of both operands.
-    auto tile_at = [&](int64_t t, int &m0, int &n0) {
-        const int64_t block = int64_t(16) * n_nt;
-        const int b = int(t / block);
-        const int tall = min(16, p.n_mt - 16 * b);
-        const int64_t u = t - b * block;
-        n0 = int(u / tall) * bn;
-        m0 = (16 * b + int(u % tall)) * (2 * LM);
+    // The pair's i-th tile: its product and its place there; false past the
+    // last.  Tiles of a product are numbered in blocks of 16 m tiles, m
+    // fastest: the pairs running at one time share few rows of both operands.
+    const int pairs = int(gridDim.x) / (2 * Z), pair = int(blockIdx.x) / (2 * Z);
+    struct Tile {
+        int which, m0, n0, nk0, nk1;
     };
+    auto tile_at = [&](int i, Tile &o) {
+        const int extra = g.tiles[0] % pairs;
+        const int mine = g.tiles[0] / pairs + (pair < extra ? 1 : 0);
+        int t;
+        o.which = i < mine ? 0 : 1;
+        if (i < mine) {
+            t = pair + i * pairs;
+        } else {
+            const int j = i - mine;
+            if (j >= g.shared && pair < extra)
+                return false;
+            t = j < g.shared ? j * pairs + pair
+                             : g.shared * pairs + (j - g.shared) * (pairs - extra) + pair - extra;
+            if (t >= g.tiles[1])
+                return false;
+        }
+        const LinArgs &p = g.p[o.which];
+        const int n_nt = (p.N + p.bn - 1) / p.bn, block = 16 * n_nt;
+        const int b = t / block, tall = min(16, p.n_mt - 16 * b), u = t - b * block;
+        o.n0 = u / tall * p.bn;
+        o.m0 = (16 * b + u % tall) * (2 * LM);
+        const int nk = (p.R + LK - 1) / LK;
+        o.nk0 = int(int64_t(nk) * z / Z);
+        o.nk1 = int(int64_t(nk) * (z + 1) / Z);
+        return true;
+    };
+    Tile w;
 
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0;
         const bool one = elect_one();
         bool ok = true;
-        for (int64_t t = first; ok && t < tiles; t += step) {
-            int m0, n0;
-            tile_at(t, m0, n0);
-            m0 += int(rank) * LM;
-            n0 += int(rank) * half;
-            for (int kb = kb0; kb < kb1; kb += kPairSub) {
+        for (int i = 0; ok && tile_at(i, w); ++i) {
+            const LinArgs &p = g.p[w.which];
+            const CUtensorMap *map_a = &g.a[w.which], *map_b = &g.b[w.which];
+            const int a_mn = p.a_mn, b_mn = p.b_mn, half = p.bn / 2;
+            const uint32_t tx = 2 * (kLinATile + pair_b_bytes(p.bn, b_mn));
+            const int m0 = w.m0 + int(rank) * LM, n0 = w.n0 + int(rank) * half;
+            for (int kb = w.nk0; kb < w.nk1; kb += kPairSub) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
                 if (!ok)
                     break;
                 if (one) {
-                    const int subs = min(kPairSub, kb1 - kb);
+                    const int subs = min(kPairSub, w.nk1 - kb);
                     if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
-                        mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(2 * subs) * sub_bytes);
+                        mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(subs) * tx);
                     const uint32_t fb = dsmem_addr(&ctl.full[stage], lead);
 #pragma unroll
                     for (int h = 0; h < kPairSub; ++h) {
@@ -720,17 +760,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         uint8_t *sa = smem + (stage * kPairSub + h) * sub_bytes;
                         uint8_t *sb = sa + kLinATile;
                         const int k0 = (kb + h) * LK;
-                        if (A_MN) {  // 64 m x 64 r boxes, m contiguous
-                            tma_load_2d_pair(sa, &map_a, fb, m0, k0);
-                            tma_load_2d_pair(sa + 8192, &map_a, fb, m0 + 64, k0);
+                        if (a_mn) {  // 64 m x 64 r boxes, m contiguous
+                            tma_load_2d_pair(sa, map_a, fb, m0, k0);
+                            tma_load_2d_pair(sa + 8192, map_a, fb, m0 + 64, k0);
                         } else {
-                            tma_load_2d_pair(sa, &map_a, fb, k0, m0);
+                            tma_load_2d_pair(sa, map_a, fb, k0, m0);
                         }
-                        if (B_MN) {
+                        if (b_mn) {
                             for (int c = 0; c < half; c += 64)
-                                tma_load_2d_pair(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
+                                tma_load_2d_pair(sb + c * (LK * 2), map_b, fb, n0 + c, k0);
                         } else {
-                            tma_load_2d_pair(sb, &map_b, fb, k0, n0);
+                            tma_load_2d_pair(sb, map_b, fb, k0, n0);
                         }
                     }
                 }
@@ -756,24 +796,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         // The whole warp walks the loop and one lane issues, so that
-        // descriptors and addresses stay warp-uniform.
+        // descriptors and addresses stay warp-uniform (issued from inside an
+        // `if (lane == 0)` loop, a stage of four MMAs took about 690 cycles
+        // where the tensor core needs 512).
         int stage = 0, buf = 0;
         uint32_t phase = 0, aphase = 0;
-        uint32_t idesc = idesc_bf16_f32(2 * LM, uint32_t(bn), A_MN, B_MN);
-        if (p.f16)
-            idesc &= ~((7u << 7) | (7u << 10));
         const uint32_t sa = smem_u32(smem), sb = sa + kLinATile;
-        const uint64_t da0 = A_MN ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
-        const uint64_t db0 = B_MN ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
         const bool one = elect_one();
         bool ok = true;
-        for (int64_t t = first; ok && t < tiles; t += step) {
+        for (int i = 0; ok && tile_at(i, w); ++i) {
+            const LinArgs &p = g.p[w.which];
+            uint32_t idesc =
+                idesc_bf16_f32(2 * LM, uint32_t(p.bn), uint32_t(p.a_mn), uint32_t(p.b_mn));
+            if (p.f16)
+                idesc &= ~((7u << 7) | (7u << 10));
+            const uint64_t da0 = smem_desc_sw128(sa, p.a_mn ? 8192 : 16, 1024);
+            const uint64_t db0 = smem_desc_sw128(sb, p.b_mn ? 8192 : 16, 1024);
+            const uint32_t ia = p.a_mn ? 128 : 2, ib = p.b_mn ? 128 : 2;
             ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
             if (!ok)
                 break;
             tc_fence_after_sync();
-            const uint32_t d = tmem_base + uint32_t(buf * bn);
-            for (int kb = kb0; kb < kb1; kb += kPairSub) {
+            const uint32_t d = tmem_base + uint32_t(buf * g.bn);
+            for (int kb = w.nk0; kb < w.nk1; kb += kPairSub) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
                 if (!ok)
                     break;
@@ -781,14 +826,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (one) {
 #pragma unroll
                     for (int h = 0; h < kPairSub; ++h) {
-                        const uint64_t off =
-                            uint64_t(uint32_t(stage * kPairSub + h) * (sub_bytes >> 4));
-                        if (kb + h < kb1) {
+                        const uint32_t off = uint32_t(stage * kPairSub + h) * (sub_bytes >> 4);
+                        if (kb + h < w.nk1) {
 #pragma unroll
-                            for (int kk = 0; kk < LK / 16; ++kk)
-                                tc_mma_f16_pair(d, da0 + off + kk * (A_MN ? 128 : 2),
-                                                db0 + off + kk * (B_MN ? 128 : 2), idesc,
-                                                kb != kb0 || (h | kk) != 0);
+                            for (uint32_t kk = 0; kk < LK / 16; ++kk)
+                                tc_mma_f16_pair(d, da0 + (off + kk * ia), db0 + (off + kk * ib),
+                                                idesc, kb != w.nk0 || h != 0 || kk != 0);
                         }
                     }
                     tc_commit_pair(&ctl.empty[stage], uint16_t(3u << lead));
@@ -811,16 +854,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         // (the epilogue warps of both CTAs wait for every accumulator, so the
         // MMAs are done when the cluster meets below)
-    } else if (warp >= 2 && Z == 1) {
+    } else if (warp >= 2) {
+        if (g.db) {  // while the first tile is on its way
+            const int threads = 32 * kPairEpiWarps;
+            for (int c = int(blockIdx.x) * threads + int(threadIdx.x) - 64; c < g.db_n;
+                 c += int(gridDim.x) * threads) {
+                float v = 0.0f;
+#pragma unroll 8
+                for (int i = 0; i < g.chunks; ++i)
+                    v += g.part[int64_t(i) * g.db_n + c];
+                g.db[c] = v;
+            }
+            __syncwarp();
+        }
         const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant; even or odd chunks
         uint8_t *mine = stg + (warp - 2) * kPairStg;
         int buf = 0;
         uint32_t aphase = 0;
-        for (int64_t t = first; t < tiles; t += step) {
-            int m0, n0;
-            tile_at(t, m0, n0);
-            const int64_t row = int64_t(m0) + int(rank) * LM + q * 32;
-            const int rows = int(min(int64_t(32), p.M - row)), width = min(bn, p.N - n0);
+        for (int i = 0; Z == 1 && tile_at(i, w); ++i) {
+            const LinArgs &p = g.p[w.which];
+            const int n0 = w.n0;
+            const int64_t row = int64_t(w.m0) + int(rank) * LM + q * 32;
+            const int rows = int(min(int64_t(32), p.M - row)), width = min(p.bn, p.N - n0);
             auto bias_of = [&](int c) {
                 return p.bias && c + int(lane) < width ? p.bias[n0 + c + int(lane)] : 0.0f;
             };
@@ -829,7 +884,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (!__all_sync(0xffffffffu, ok))
                 break;
             tc_fence_after_sync();
-            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * bn);
+            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * g.bn);
             if (rows > 0 && part * 32 < width) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t0 + uint32_t(part * 32), r);
@@ -864,8 +919,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // of the Z that hold the same rows finishes 128 / Z of them: every
         // CTA sends it its sums of those rows (into memory beside the ring,
         // which may still be in use there), and it adds them in rank order.
-        int m0, n0;
-        tile_at(first, m0, n0);
+        const LinArgs &p = g.p[0];
+        tile_at(0, w);
+        const int bn = p.bn, n0 = w.n0;
         float *acc = reinterpret_cast<float *>(stg);  // [Z][128 / Z][pitch]
         const int pitch = bn + 4, slice = LM / Z;     // float4 rows, conflict-free
         // what a thread finishes: four neighbouring columns, always the same, of
@@ -901,7 +957,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
         cluster_sync();
-        m0 += int(rank) * LM + z * slice;
+        const int m0 = w.m0 + int(rank) * LM + z * slice;
         const int rows = min(slice, p.M - m0);
         if (left > 0) {
             constexpr int kBatch = 4;
@@ -931,8 +987,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     }
     __syncthreads();
-    if (threadIdx.x == 0 && ctl.abort_flag && p.status)
-        atomicOr(p.status, MOE_STATUS_TIMEOUT);
+    if (threadIdx.x == 0 && ctl.abort_flag && g.p[0].status)
+        atomicOr(g.p[0].status, MOE_STATUS_TIMEOUT);
     cluster_sync();  // the CTAs are done with each other's shared memory and barriers
     if (warp == 1) {
         tc_fence_after_sync();
@@ -1122,29 +1178,28 @@ void (*act_grad_kernel(int act, bool f32))(GradArgs)
 
 // ---- host ---------------------------------------------------------------------
 
-// 16-bit matrix [rows, cols], cols contiguous, rows ld elements apart, read in
-// boxes of 64 columns x box_rows rows with the 128-byte swizzle.
-cudaError_t lin_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                    int box_rows, int f16)
+// A 16-bit matrix as stored: rows x cols, cols contiguous, rows ld elements apart.
+struct Operand {
+    const void *p;
+    int64_t rows, cols, ld;
+};
+
+// Its tensor map: boxes of 64 columns x box_rows rows with the 128-byte swizzle.
+cudaError_t lin_map(CUtensorMap *m, const Operand &o, int box_rows, int f16)
 {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode)
         return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+    const cuuint64_t dims[2] = {cuuint64_t(o.cols), cuuint64_t(o.rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(o.ld) * 2};
     const cuuint32_t box[2] = {LK, cuuint32_t(box_rows)}, estr[2] = {1, 1};
     const CUresult r =
         encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-               const_cast<void *>(base), dims, strides, box, estr,
+               const_cast<void *>(o.p), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-
-struct Operand {
-    const void *p;
-    int64_t rows, cols, ld;  // as stored: cols contiguous
-};
 
 cudaError_t launch_clustered(const void *kern, unsigned grid, unsigned cluster, unsigned threads,
                              size_t smem, cudaStream_t s, void **args)
@@ -1166,44 +1221,53 @@ cudaError_t launch_clustered(const void *kern, unsigned grid, unsigned cluster, 
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+// out[i][j] = sum_r X[i][r] Y[j][r], with a's epilogue fields.
+struct Product {
+    Operand X, Y;
+    bool x_mn, y_mn;  // i (j) is contiguous, not r
+    int rows, cols, R;
+    LinArgs a;
+};
+
 // Tiling of a product, chosen by estimated SM cycles.
 struct Tiling {
     bool pair;
     int bn, split;
+    int64_t tiles;
+    double tile_cycles;
 };
 
-// What k_linear_pair is estimated to take.  Per 64 of r a tile of 256 x bn
-// costs 2 bn cycles of MMA, or the time its operands take to arrive (16 KB
-// and 128 bytes a row of B, at about 85 bytes a cycle as measured).  A tile's
-// epilogue (about 1200 cycles per 64 columns) hides behind the next tile's
-// MMAs, except the last one's; starting takes about 5000 cycles, and adding
-// the parts of a split tile about as long again.
-double pair_cycles(int64_t tiles, int pairs, int bn, int split, int nk, bool col_mn)
+// What a tile of k_linear_pair takes per 64 of r, from times at bn = 64 ...
+// 256 (4096 x 2816 x 11264: 144 us at 256, 154 at 192, 183 at 128).
+double pair_step(int bn, bool y_mn)
 {
-    const int half = col_mn ? (bn / 2 + 63) / 64 * 64 : bn / 2;
-    const double step = std::max(2.0 * bn, (16384.0 + 128.0 * half) / 85.0);
-    const double main = step * ((nk + split - 1) / split), epi = 1200.0 * ((bn + 63) / 64);
-    if (split > 1)
-        return 10000.0 + main;
-    const int64_t waves = (tiles + pairs - 1) / pairs;
-    return 5000.0 + std::max(main, epi) * double(waves - 1) + main + epi;
+    return 200.0 + 1.65 * (2.0 * pair_b_bytes(bn, y_mn) / (LK * 2));
 }
 
-Tiling choose_tiling(int64_t rows, int64_t cols, int nk, int sms, bool col_mn)
+// A tile's epilogue (about 1500 cycles per 64 columns) hides behind the next
+// tile's MMAs, except the last one's; starting takes about 5000 cycles, and
+// joining the parts of a split tile about 8000.
+Tiling choose_tiling(const Product &q, int sms)
 {
-    Tiling t{false, 0, 1};
-    if (rows <= 128)
+    Tiling t{false, 0, 1, 0, 0.0};
+    if (q.rows <= 128)
         return t;
+    const int nk = (q.R + LK - 1) / LK, pairs = std::max(1, sms / 2);
     double best = 0.0;
     for (int bn = 256; bn >= 64; bn -= 32) {
-        const int64_t tiles = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
+        const int64_t tiles =
+            ((int64_t(q.rows) + 255) / 256) * ((int64_t(q.cols) + bn - 1) / bn);
         for (int z = 1; z <= kPairMaxSplit; z *= 2) {
             // a split tile needs room for the parts beside the ring
-            if (z > 1 && (nk / z < 4 || tiles * z > sms / 2 || (bn != 64 && bn != 128)))
+            if (z > 1 && (nk / z < 4 || tiles * z > pairs || (bn != 64 && bn != 128)))
                 break;
-            const double c = pair_cycles(tiles, sms / 2, bn, z, nk, col_mn);
+            const double main = pair_step(bn, q.y_mn) * ((nk + z - 1) / z);
+            const double epi = 1500.0 * ((bn + 63) / 64);
+            const int64_t waves = (tiles + pairs - 1) / pairs;
+            const double c = 5000.0 + main + (z > 1 ? 8000.0 : epi) +
+                             double(waves - 1) * std::max(main, epi);
             if (!t.pair || c < best) {
-                t = Tiling{true, bn, z};
+                t = Tiling{true, bn, z, tiles, std::max(main, epi)};
                 best = c;
             }
         }
@@ -1211,44 +1275,15 @@ Tiling choose_tiling(int64_t rows, int64_t cols, int nk, int sms, bool col_mn)
     return t;
 }
 
-// out[i][j] = sum_r X[i][r] Y[j][r]; a's epilogue fields are set.
-template <bool X_MN, bool Y_MN>
-cudaError_t launch_linear(const Operand &X, const Operand &Y, int rows, int cols, int R, LinArgs a,
-                          cudaStream_t s)
+cudaError_t launch_small(const Product &q, cudaStream_t s)
 {
-    constexpr int which = X_MN ? 2 : Y_MN ? 1 : 0;
-    const int sms = device_sm_count();
-    const int nk = (R + LK - 1) / LK;
-    a.R = R;
-    CUtensorMap ma, mb;
-    void *args[] = {&ma, &mb, &a};
-    const Tiling t = choose_tiling(rows, cols, nk, sms, Y_MN);
-    if (t.pair) {
-        a.M = rows, a.N = cols;
-        a.bn = t.bn, a.split = t.split;
-        a.n_mt = (rows + 2 * LM - 1) / (2 * LM);
-        a.stages = kPairStages;
-        const int64_t tiles = int64_t(a.n_mt) * ((cols + a.bn - 1) / a.bn);
-        const size_t smem =
-            1024 + size_t(a.stages) * kPairSub * pair_sub_bytes(a.bn, Y_MN) +
-            (a.split > 1 ? size_t(LM) * (a.bn + 4) * 4 : size_t(kPairEpiWarps) * kPairStg);
-        cudaError_t e = lin_map(&ma, X.p, X.rows, X.cols, X.ld, X_MN ? LK : LM, a.f16);
-        if (e == cudaSuccess)
-            e = lin_map(&mb, Y.p, Y.rows, Y.cols, Y.ld, Y_MN ? LK : a.bn / 2, a.f16);
-        const void *kern = reinterpret_cast<const void *>(k_linear_pair<X_MN, Y_MN>);
-        if (e == cudaSuccess)
-            e = ensure_smem_limit(kern, kSlotLinearPair0 + which, 226 * 1024);
-        if (e != cudaSuccess)
-            return e;
-        const int64_t clusters =
-            a.split > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, sms / 2));
-        return launch_clustered(kern, unsigned(clusters * 2 * a.split), unsigned(2 * a.split),
-                                kPairThreads, smem, s, args);
-    }
-    a.M = cols, a.N = rows;
-    a.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    a.n_mt = (cols + LM - 1) / LM;
-    const int64_t tiles = int64_t(a.n_mt) * ((rows + a.bn - 1) / a.bn);
+    const int sms = device_sm_count(), nk = (q.R + LK - 1) / LK;
+    LinArgs a = q.a;
+    a.M = q.cols, a.N = q.rows, a.R = q.R;
+    a.a_mn = q.y_mn, a.b_mn = q.x_mn;
+    a.bn = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
+    a.n_mt = (q.cols + LM - 1) / LM;
+    const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.rows) + a.bn - 1) / a.bn);
     // split the reduction while that still adds CTAs (two fit an SM) and
     // leaves each at least four stages
     a.split = 1;
@@ -1256,20 +1291,106 @@ cudaError_t launch_linear(const Operand &X, const Operand &Y, int rows, int cols
         a.split *= 2;
     if (tiles * a.split > INT_MAX)
         return cudaErrorInvalidValue;
-    const uint32_t stage = kLinATile + lin_b_tile(a.bn, X_MN);
+    const uint32_t stage = kLinATile + lin_b_tile(a.bn, a.b_mn);
     a.stages = std::min<int>(kLinMaxStages, 96 * 1024 / stage);
-    const size_t ring = size_t(a.stages) * stage;
-    const size_t smem = 1024 + std::max(ring, size_t(a.bn) * LM * 4);
-    cudaError_t e = lin_map(&ma, Y.p, Y.rows, Y.cols, Y.ld, Y_MN ? LK : LM, a.f16);
+    const size_t smem =
+        1024 + std::max(size_t(a.stages) * stage, size_t(a.bn) * LM * 4);
+    CUtensorMap ma, mb;
+    cudaError_t e = lin_map(&ma, q.Y, q.y_mn ? LK : LM, a.f16);
     if (e == cudaSuccess)
-        e = lin_map(&mb, X.p, X.rows, X.cols, X.ld, X_MN ? LK : a.bn, a.f16);
-    const void *kern = reinterpret_cast<const void *>(k_linear<Y_MN, X_MN>);
+        e = lin_map(&mb, q.X, q.x_mn ? LK : a.bn, a.f16);
+    const void *kern = reinterpret_cast<const void *>(k_linear);
     if (e == cudaSuccess)
-        e = ensure_smem_limit(kern, kSlotLinear0 + which, 112 * 1024);
+        e = ensure_smem_limit(kern, kSlotLinear, 112 * 1024);
     if (e != cudaSuccess)
         return e;
+    void *args[] = {&ma, &mb, &a};
     return launch_clustered(kern, unsigned(tiles * a.split), unsigned(a.split), kLinThreads, smem, s,
                             args);
+}
+
+struct ColSums {
+    const float *part;
+    float *db;
+    int chunks, n;
+};
+
+// One or two products in one launch; both unsplit if two.
+cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const ColSums &sums,
+                         cudaStream_t s)
+{
+    const int sms = device_sm_count(), pairs = std::max(1, sms / 2);
+    PairArgs g = {};
+    g.part = sums.part, g.db = sums.db, g.chunks = sums.chunks, g.db_n = sums.n;
+    for (int i = 0; i < count; ++i) {
+        if (t[i].tiles > INT_MAX / 2)
+            return cudaErrorInvalidValue;
+        LinArgs &a = g.p[i];
+        a = q[i].a;
+        a.M = q[i].rows, a.N = q[i].cols, a.R = q[i].R;
+        a.a_mn = q[i].x_mn, a.b_mn = q[i].y_mn;
+        a.bn = t[i].bn, a.split = t[i].split;
+        a.n_mt = int((int64_t(a.M) + 2 * LM - 1) / (2 * LM));
+        g.tiles[i] = int(t[i].tiles);
+        g.bn = std::max(g.bn, a.bn);
+        g.sub_bytes = std::max(g.sub_bytes, kLinATile + pair_b_bytes(a.bn, a.b_mn));
+        cudaError_t e = lin_map(&g.a[i], q[i].X, q[i].x_mn ? LK : LM, a.f16);
+        if (e == cudaSuccess)
+            e = lin_map(&g.b[i], q[i].Y, q[i].y_mn ? LK : a.bn / 2, a.f16);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int split = t[0].split;
+    int clusters = g.tiles[0];
+    if (split == 1) {
+        clusters = int(std::min<int64_t>(int64_t(g.tiles[0]) + g.tiles[1], pairs));
+        // the most of product 1's tiles that a pair with one more of product
+        // 0's takes: what evens out the pairs' times
+        const int extra = g.tiles[0] % clusters, others = clusters - extra;
+        const double lead = extra ? t[0].tile_cycles / std::max(1.0, t[1].tile_cycles) : 0.0;
+        const double each = (g.tiles[1] - lead * others) / clusters;
+        g.shared = extra ? std::max(0, int(each + 0.5))
+                         : (g.tiles[1] + clusters - 1) / clusters;
+    }
+    const size_t smem = 1024 + size_t(kPairStages) * kPairSub * g.sub_bytes +
+                        (split > 1 ? size_t(LM) * (g.bn + 4) * 4 : size_t(kPairEpiWarps) * kPairStg);
+    const void *kern = reinterpret_cast<const void *>(k_linear_pair);
+    const cudaError_t e = ensure_smem_limit(kern, kSlotLinearPair, 226 * 1024);
+    if (e != cudaSuccess)
+        return e;
+    void *args[] = {&g};
+    return launch_clustered(kern, unsigned(clusters * 2 * split), unsigned(2 * split), kPairThreads,
+                            smem, s, args);
+}
+
+// The products (the one with the longer reduction first) and the column sums,
+// if any.
+cudaError_t launch_products(Product *q, int count, ColSums sums, cudaStream_t s)
+{
+    const int sms = device_sm_count();
+    if (count == 2 && q[1].R > q[0].R)
+        std::swap(q[0], q[1]);
+    Tiling t[2] = {};
+    for (int i = 0; i < count; ++i)
+        t[i] = choose_tiling(q[i], sms);
+    cudaError_t e = cudaSuccess;
+    if (count == 2 && t[0].pair && t[1].pair && t[0].split == 1 && t[1].split == 1) {
+        e = launch_pairs(q, t, 2, sums, s);
+        sums.db = nullptr;
+    } else {
+        for (int i = 0; i < count && e == cudaSuccess; ++i) {
+            if (t[i].pair) {
+                e = launch_pairs(q + i, t + i, 1, sums, s);
+                sums.db = nullptr;
+            } else {
+                e = launch_small(q[i], s);
+            }
+        }
+    }
+    if (e == cudaSuccess && sums.db)
+        e = launch_pdl(k_col_sum, dim3((sums.n + 31) / 32), dim3(kGradThreads), 0, s, sums.part,
+                       sums.chunks, sums.n, sums.db);
+    return e;
 }
 
 inline bool aligned(const void *p, uintptr_t a)
@@ -1325,8 +1446,8 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
     a.f16 = dtype == MOE_DT_F16, a.out_f32 = y_dtype == MOE_DT_F32, a.act = act;
     a.vec_out = vec16(y, ldy, ysize), a.vec_res = vec16(residual, ldr, ysize);
     a.vec_pre = vec16(pre, N, 2);
-    return launch_linear<false, false>({x, T, K, ldx}, {W, N, K, K}, T, N, K, a,
-                                       reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    Product q{{x, T, K, ldx}, {W, N, K, K}, false, false, T, N, K, a};
+    return launch_products(&q, 1, ColSums{}, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -1403,21 +1524,20 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     a.f16 = dtype == MOE_DT_F16;
     a.act = MOE_ACT_NONE;
     a.ldo = K;
+    Product q[2];
+    int count = 0;
     if (dx) {
         a.out = dx;
         a.vec_out = vec16(dx, K, 2);
-        if (launch_linear<false, true>(P, {W, N, K, K}, T, K, N, a, s) != cudaSuccess)
-            return MOE_ERR_CUDA;
+        q[count++] = Product{P, {W, N, K, K}, false, true, T, K, N, a};
     }
     if (dW) {
         a.out = dW;
         a.out_f32 = dw_dtype == MOE_DT_F32;
         a.vec_out = vec16(dW, K, dwsize);
-        if (launch_linear<true, true>(P, {x, T, K, ldx}, N, K, T, a, s) != cudaSuccess)
-            return MOE_ERR_CUDA;
+        q[count++] = Product{P, {x, T, K, ldx}, true, true, N, K, T, a};
     }
-    if (db && launch_pdl(k_col_sum, dim3((N + 31) / 32), dim3(kGradThreads), 0, s,
-                         static_cast<const float *>(part), chunks, N, db) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return MOE_OK;
+    return launch_products(q, count, ColSums{part, db, chunks, N}, s) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
