@@ -445,20 +445,24 @@ __global__ void __launch_bounds__(kLinThreads)
 // and half the rows of B.  A stage of 64 r costs each SM 32 KB of loads
 // (bn = 256) for 512 cycles of MMA; the same tile on one SM would load 48.
 // Pairs walk the tiles (persistent); two accumulators in tensor memory let
-// eight epilogue warps work on one tile while the MMAs fill the other.  An
-// epilogue warp takes 32 rows x 32 columns at a time through 4 KB of shared
+// four epilogue warps work on one tile while the MMAs fill the other.  An
+// epilogue warp takes 32 rows x 32 columns at a time through shared
 // memory, so that global accesses are whole row pieces of 64 or 128 bytes;
 // the next 32 columns are read from tensor memory (about 330 cycles) ahead.
+// Eight epilogue warps, at 168 registers a thread instead of 255, measured
+// 172 us instead of 159 for 4096 x 2816 x 11264 with GELU and pre.
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
 //
 // A launch takes one product or two (dx and dW): two short launches would
 // each leave SMs idle in their last round and pay the start twice.
-constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
-constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 192;  // producer, MMA, four epilogue warps
+constexpr int kPairEpiWarps = 4;
 constexpr int kPairSub = 2;     // 64-r halves of a stage
 constexpr int kPairStages = 3;
-constexpr uint32_t kPairStg = 4096;  // staging of one epilogue warp
+// staging of one epilogue warp: output (and residual), pre, bias
+constexpr uint32_t kPairStgPre = 4096, kPairStgBias = kPairStgPre + 2048;
+constexpr uint32_t kPairStg = kPairStgBias + 128;
 constexpr int kPairMaxSplit = 4;     // a cluster of eight CTAs
 
 struct PairCtrl {
@@ -503,6 +507,22 @@ __device__ __forceinline__ uint4 *stg_at(uint8_t *stg, int r, int c)
     return reinterpret_cast<uint4 *>(stg) + r * kPieces + x;
 }
 
+template <bool STORE, typename E>
+__device__ __noinline__ void stg_move_by_element(uint8_t *stg, E *p, int64_t ld, int rows, int cols)
+{
+    constexpr int kPer = 16 / int(sizeof(E));
+    const int lane = threadIdx.x & 31;
+    if (lane < cols)
+#pragma unroll 16
+        for (int r = 0; r < rows; ++r) {
+            E *at = reinterpret_cast<E *>(stg_at<E>(stg, r, lane / kPer)) + lane % kPer;
+            if (STORE)
+                p[int64_t(r) * ld + lane] = *at;
+            else
+                *at = p[int64_t(r) * ld + lane];
+        }
+}
+
 // Moves the tile to (STORE) or from rows [0, rows) x columns [0, cols) of a
 // matrix with ld elements between rows.  vec: 16-byte pieces are aligned;
 // otherwise, or where columns end inside the tile, element by element.
@@ -533,15 +553,7 @@ __device__ __forceinline__ void stg_move(uint8_t *stg, E *p, int64_t ld, int row
         }
         return;
     }
-    if (lane < cols)
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r) {
-            E *at = reinterpret_cast<E *>(stg_at<E>(stg, r, lane / kPer)) + lane % kPer;
-            if (STORE)
-                p[int64_t(r) * ld + lane] = *at;
-            else
-                *at = p[int64_t(r) * ld + lane];
-        }
+    stg_move_by_element<STORE>(stg, p, ld, rows, cols);
 }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int f16)
@@ -561,67 +573,66 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int f16)
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// 32 rows (lane = row) x 32 columns -> 16-bit rows, by way of the staging tile.
-__device__ __forceinline__ void emit16(uint8_t *stg, const float (&v)[32], uint16_t *out,
-                                       int64_t ld, int rows, int cols, int f16, bool vec)
+// The residual's 32 rows x `cols` columns into the staging tile.
+__device__ __forceinline__ void stage_residual(const LinArgs &p, uint8_t *stg, int64_t m0, int n0,
+                                               int rows, int cols)
+{
+    void *r = const_cast<void *>(p.residual);
+    if (p.out_f32)
+        stg_move<false>(stg, static_cast<float *>(r) + m0 * p.ldr + n0, p.ldr, rows, cols,
+                        p.vec_res);
+    else
+        stg_move<false>(stg, static_cast<uint16_t *>(r) + m0 * p.ldr + n0, p.ldr, rows, cols,
+                        p.vec_res);
+}
+
+__device__ __forceinline__ void stage16(uint8_t *stg, const float (&v)[32], int f16)
 {
     const int lane = threadIdx.x & 31;
-    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c)
         *stg_at<uint16_t>(stg, lane, c) = make_uint4(
             pack16(v[8 * c], v[8 * c + 1], f16), pack16(v[8 * c + 2], v[8 * c + 3], f16),
             pack16(v[8 * c + 4], v[8 * c + 5], f16), pack16(v[8 * c + 6], v[8 * c + 7], f16));
-    __syncwarp();
-    stg_move<true>(stg, out, ld, rows, cols, vec);
 }
 
-// The epilogue of 32 rows x 32 columns: bias, pre, activation, residual, output.
-// `bias`: lane j holds column j's; every lane takes all of them, by way of
-// the staging tile.
+// The epilogue of 32 rows (lane = row) x 32 columns: bias, pre, activation,
+// residual, output.  `bias`: lane j holds column j's; every lane takes all of
+// them from shared memory.  The residual is there already.
 __device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float (&v)[32],
                                            float bias, int64_t m0, int n0, int rows, int cols)
 {
     const int lane = threadIdx.x & 31;
     if (p.bias) {
-        __syncwarp();
-        reinterpret_cast<float *>(stg)[lane] = bias;
+        float *b = reinterpret_cast<float *>(stg + kPairStgBias);
+        b[lane] = bias;
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-            const float4 b = *reinterpret_cast<const float4 *>(stg + 4 * j);
-            v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+            const float4 q = *reinterpret_cast<const float4 *>(b + j);
+            v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
         }
     }
     if (p.pre)
-        emit16(stg, v, static_cast<uint16_t *>(p.pre) + m0 * p.ldp + n0, p.ldp, rows, cols, p.f16,
-               p.vec_pre);
+        stage16(stg + kPairStgPre, v, p.f16);
     if (p.act != MOE_ACT_NONE)
         with_act(p.act, [&](auto act) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 v[j] = act_t<decltype(act)::value>(v[j]);
         });
-    if (p.residual) {
-        __syncwarp();
-        if (p.out_f32) {
-            stg_move<false>(stg,
-                            const_cast<float *>(static_cast<const float *>(p.residual)) +
-                                m0 * p.ldr + n0,
-                            p.ldr, rows, cols, p.vec_res);
-            __syncwarp();
+    if (p.out_f32) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint4 q = *stg_at<float>(stg, lane, c);
-                v[4 * c] += __uint_as_float(q.x), v[4 * c + 1] += __uint_as_float(q.y);
-                v[4 * c + 2] += __uint_as_float(q.z), v[4 * c + 3] += __uint_as_float(q.w);
+        for (int c = 0; c < 8; ++c) {
+            float4 *at = reinterpret_cast<float4 *>(stg_at<float>(stg, lane, c));
+            if (p.residual) {
+                const float4 q = *at;
+                v[4 * c] += q.x, v[4 * c + 1] += q.y, v[4 * c + 2] += q.z, v[4 * c + 3] += q.w;
             }
-        } else {
-            stg_move<false>(stg,
-                            const_cast<uint16_t *>(static_cast<const uint16_t *>(p.residual)) +
-                                m0 * p.ldr + n0,
-                            p.ldr, rows, cols, p.vec_res);
-            __syncwarp();
+            *at = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+    } else {
+        if (p.residual) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint4 q = *stg_at<uint16_t>(stg, lane, c);
@@ -634,21 +645,19 @@ __device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float
                 }
             }
         }
-    }
-    if (!p.out_f32) {
-        emit16(stg, v, static_cast<uint16_t *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols, p.f16,
-               p.vec_out);
-        return;
+        stage16(stg, v, p.f16);
     }
     __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        *stg_at<float>(stg, lane, c) =
-            make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+    if (p.pre)
+        stg_move<true>(stg + kPairStgPre, static_cast<uint16_t *>(p.pre) + m0 * p.ldp + n0, p.ldp,
+                       rows, cols, p.vec_pre);
+    if (p.out_f32)
+        stg_move<true>(stg, static_cast<float *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols,
+                       p.vec_out);
+    else
+        stg_move<true>(stg, static_cast<uint16_t *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols,
+                       p.vec_out);
     __syncwarp();
-    stg_move<true>(stg, static_cast<float *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols,
-                   p.vec_out);
 }
 
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -867,7 +876,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         }
-        const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant; even or odd chunks
+        const int q = warp & 3;  // TMEM lane quadrant
         uint8_t *mine = stg + (warp - 2) * kPairStg;
         int buf = 0;
         uint32_t aphase = 0;
@@ -879,30 +888,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             auto bias_of = [&](int c) {
                 return p.bias && c + int(lane) < width ? p.bias[n0 + c + int(lane)] : 0.0f;
             };
-            float bias = bias_of(part * 32);
-            const bool ok = mbar_wait(&ctl.acc_full[buf], aphase, abort_flag);
-            if (!__all_sync(0xffffffffu, ok))
-                break;
-            tc_fence_after_sync();
+            float bias = bias_of(0);
             const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * g.bn);
-            if (rows > 0 && part * 32 < width) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(t0 + uint32_t(part * 32), r);
+            bool ok = true;
+            uint32_t r[32];
 #pragma unroll 1
-                for (int c = part * 32; c < width; c += 64) {
-                    float v[32];
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = __uint_as_float(r[j]);
-                    const float now = bias;
-                    if (c + 64 < width) {
-                        tmem_ld_32x32b_x32(t0 + uint32_t(c) + 64, r);
-                        bias = bias_of(c + 64);
-                    }
-                    pair_chunk(p, mine, v, now, row, n0 + c, rows, min(32, width - c));
+            for (int c = 0; ok && (c == 0 || (rows > 0 && c < width)); c += 32) {
+                if (p.residual && rows > 0)
+                    stage_residual(p, mine, row, n0 + c, rows, min(32, width - c));
+                __syncwarp();
+                if (c == 0) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
+                    if (!ok || rows <= 0)
+                        break;
+                    tc_fence_after_sync();
+                    tmem_ld_32x32b_x32(t0, r);
                 }
+                float v[32];
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = __uint_as_float(r[j]);
+                const float now = bias;
+                if (c + 32 < width) {
+                    tmem_ld_32x32b_x32(t0 + uint32_t(c) + 32, r);
+                    bias = bias_of(c + 32);
+                }
+                pair_chunk(p, mine, v, now, row, n0 + c, rows, min(32, width - c));
             }
+            if (!ok)
+                break;
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
@@ -936,23 +952,24 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (warp >= 2) {
             const bool ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[0], 0, abort_flag));
-            const int q = warp & 3, part = (warp - 2) >> 2, m = q * 32 + int(lane);
+            const int q = warp & 3, m = q * 32 + int(lane);
             tc_fence_after_sync();
-            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(part * bn / 2);
-            const uint32_t to = dsmem_addr(acc + (z * slice + m % slice) * pitch + part * bn / 2,
-                                           2 * uint32_t(m / slice) + rank);
-            uint32_t r[2][32] = {};
-            if (ok) {
-                tmem_ld_32x32b_x32(t0, r[0]);
-                if (bn > 64)
-                    tmem_ld_32x32b_x32(t0 + 32, r[1]);
-                tmem_ld_wait();
-            }
+            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16);
+            const uint32_t to =
+                dsmem_addr(acc + (z * slice + m % slice) * pitch, 2 * uint32_t(m / slice) + rank);
+#pragma unroll 1
+            for (int c = 0; c < bn; c += 64) {
+                uint32_t r[2][32] = {};
+                if (ok) {
+                    tmem_ld_32x32b_x32(t0 + uint32_t(c), r[0]);
+                    tmem_ld_32x32b_x32(t0 + uint32_t(c) + 32, r[1]);
+                    tmem_ld_wait();
+                }
 #pragma unroll
-            for (int j = 0; j < 64; j += 4)
-                if (j < 32 || bn > 64)
-                    dsmem_st4(to + j * 4, r[j >> 5][j & 31], r[j >> 5][(j & 31) + 1],
+                for (int j = 0; j < 64; j += 4)
+                    dsmem_st4(to + (c + j) * 4, r[j >> 5][j & 31], r[j >> 5][(j & 31) + 1],
                               r[j >> 5][(j & 31) + 2], r[j >> 5][(j & 31) + 3]);
+            }
             tc_fence_before_sync();
         }
         __syncwarp();
@@ -1001,7 +1018,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 constexpr int kGradThreads = 256;
 constexpr int kGradGroups = 8;       // rows of a CTA side by side, one per warp
 constexpr int kGradCols = 256;       // columns of a CTA: 32 lanes x 8
-constexpr int kGradUnroll = 4;       // rows of a warp in flight
+constexpr int kGradUnroll = 2;       // rows of a warp in flight
 constexpr int kGradMaxChunks = 128;  // rows of partial column sums
 
 struct GradArgs {
@@ -1066,11 +1083,12 @@ struct Eight {
 };
 
 // dP = dy act'(pre), and the column sums of one chunk of rows.  A warp takes
-// every eighth row of the chunk, eight columns a lane, four rows' loads in
+// every eighth row of the chunk, eight columns a lane, two rows' loads in
 // flight; the warps' sums are added in order.  Bound by memory: dy and pre
-// are read and dP written once.
+// are read and dP written once.  Four CTAs an SM with two rows in flight
+// each measured 51 us on 4096 x 11264 (5.4 TB/s), two CTAs with four rows 58.
 template <int ACT, bool F32>
-__global__ void __launch_bounds__(kGradThreads) k_act_grad(GradArgs p)
+__global__ void __launch_bounds__(kGradThreads, 4) k_act_grad(GradArgs p)
 {
     __shared__ float red[kGradGroups][kGradCols];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
