@@ -67,16 +67,6 @@ __host__ __device__ __forceinline__ uint32_t lin_b_tile(int bn, int b_mn)
     return uint32_t(b_mn && bn < 64 ? 64 : bn) * LK * 2;
 }
 
-__device__ __forceinline__ float4 dsmem_ld4(uint32_t a)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-
 // 1 / (1 + e^-x): exponential and reciprocal by one special-function
 // instruction each (2 units in the last place, and the rounding of
 // x log2(e)); e^-x past 2^126 gives 0, where the true value is below 2^-126.
@@ -293,6 +283,8 @@ __global__ void __launch_bounds__(kLinThreads)
         prefetch_tmap(&map_a);
         prefetch_tmap(&map_b);
     }
+    __syncwarp();
+    cluster_arrive();
     if (warp == 1) {
         tmem_alloc(&ctl.tmem_base, tmem_cols);
         tmem_relinquish();
@@ -378,31 +370,82 @@ __global__ void __launch_bounds__(kLinThreads)
         if (one)
             tc_commit(&ctl.done);  // arrives once every MMA issued here has completed
     }
-    __syncwarp();
-
-    // accumulator -> own shared memory, fp32 [n][m] (the ring is free: every
-    // copy has been consumed by an MMA and every MMA has completed)
-    float *acc = reinterpret_cast<float *>(smem);
-    bool done = mbar_wait(&ctl.done, 0, abort_flag);
-    if (!done)  // stopped: the MMAs in flight still read shared and write tensor memory
-        lin_drain(&ctl.done, 0);
-    done = __syncthreads_and(done);  // the producer's copies have landed, also when stopped
+    // CTA z of the cluster finishes 128 / Z of the tile's m: every CTA sends it
+    // its sums of those, and it adds them in rank order.  They go beside the
+    // ring, which may still be in use there, or (128 columns) into the ring
+    // once every CTA is done with it.
+    const bool beside = bn < LM;
+    float *acc = reinterpret_cast<float *>(smem + (beside ? S * stage_bytes : 0u));
+    const int slice = LM / p.split, pitch = bn + 4;  // acc: [Z][128 / Z][pitch]
+    const int cols = min(bn, p.N - n0);
+    // what a thread finishes: four neighbouring m, always the same, of every `by`-th n
+    const int quads = slice / 4, by = kLinThreads / quads;
+    const int mq = int(threadIdx.x) % quads * 4, at = m0 + int(z) * slice + mq;
+    const int left = min(4, p.M - at);
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bias[i] = p.bias && i < left ? p.bias[at + i] : 0.0f;
+    bool done = false;
     if (warp >= 2) {
-        const int m = (warp & 3) * 32 + int(lane);
+        done = mbar_wait(&ctl.done, 0, abort_flag);
+        if (!done)  // stopped: the MMAs in flight still read shared and write tensor memory
+            lin_drain(&ctl.done, 0);
+        done = __all_sync(0xffffffffu, done) && kb1 > kb0;
+    }
+    __syncwarp();
+    cluster_wait();  // every CTA of the cluster has started
+    if (!beside)
+        cluster_sync();
+    if (warp >= 2) {
         tc_fence_after_sync();
+        const int m = (warp & 3) * 32 + int(lane);
         const uint32_t t0 = tmem_base + (uint32_t(warp & 3) << 21);
-        const int cols = min(bn, (p.N - n0 + 15) & ~15);
+        const uint32_t to = dsmem_addr(acc + (int(z) * slice + m % slice) * pitch, m / slice);
+#pragma unroll 1
         for (int c = 0; c < cols; c += 16) {
-            uint32_t r[16];
-            if (kb1 > kb0 && done) {
+            uint32_t r[16] = {};
+            if (done) {
                 tmem_ld_32x32b_x16(t0 + uint32_t(c), r);
                 tmem_ld_wait();
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                acc[(c + j) * LM + m] = kb1 > kb0 && done ? __uint_as_float(r[j]) : 0.0f;
+            for (int j = 0; j < 16; j += 4)
+                dsmem_st4(to + uint32_t(c + j) * 4, r[j], r[j + 1], r[j + 2], r[j + 3]);
         }
         tc_fence_before_sync();
+    }
+    __syncwarp();
+    cluster_sync();
+    // R rows at a time; one where that is all there is (less code to fetch
+    // counts in a call of a few microseconds: 4.3 against 4.9 us for one token)
+    auto finish = [&](auto count) {
+        constexpr int R = decltype(count)::value;
+#pragma unroll 1
+        for (int n = int(threadIdx.x) / quads; n < cols; n += R * by) {
+            float v[R][4];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = bias[j];
+                if (i == 0 || n + i * by < cols) {
+                    const float *a = acc + mq * pitch + n + i * by;
+                    for (int r = 0; r < p.split; ++r, a += slice * pitch) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[i][j] += a[j * pitch];
+                    }
+                }
+            }
+            finish_rows<R>(p, v, n0 + n, by, cols - n, at, left);
+        }
+    };
+    if (left > 0) {
+        if (cols <= by)
+            finish(std::integral_constant<int, 1>());
+        else
+            finish(std::integral_constant<int, 4>());
     }
     __syncthreads();
     if (warp == 1) {
@@ -411,31 +454,6 @@ __global__ void __launch_bounds__(kLinThreads)
     }
     if (threadIdx.x == 0 && ctl.abort_flag && p.status)
         atomicOr(p.status, MOE_STATUS_TIMEOUT);
-    __syncwarp();
-    cluster_sync();
-
-    // the cluster shares the tile's elements, four neighbouring m at a time
-    const int cols = min(bn, p.N - n0);
-    const uint32_t step = uint32_t(p.split) * kLinThreads;
-    for (uint32_t q = z * kLinThreads + threadIdx.x; q < uint32_t(cols) * (LM / 4); q += step) {
-        const int n = int(q / (LM / 4)), m = int(q % (LM / 4)) * 4;
-        const int left = min(4, p.M - (m0 + m));
-        if (left <= 0)
-            continue;
-        float v[1][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[0][i] = p.bias && i < left ? p.bias[m0 + m + i] : 0.0f;
-#pragma unroll
-        for (int r = 0; r < kLinMaxSplit; ++r)
-            if (r < p.split) {
-                const float4 o = dsmem_ld4(dsmem_addr(acc + n * LM + m, r));
-                v[0][0] += o.x, v[0][1] += o.y, v[0][2] += o.z, v[0][3] += o.w;
-            }
-        finish_rows<1>(p, v, n0 + n, 1, 1, m0 + m, left);
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
 // ---- large products: pairs of CTAs ---------------------------------------------
@@ -1302,17 +1320,18 @@ cudaError_t launch_small(const Product &q, cudaStream_t s)
     a.bn = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
     a.n_mt = (q.cols + LM - 1) / LM;
     const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.rows) + a.bn - 1) / a.bn);
-    // split the reduction while that still adds CTAs (two fit an SM) and
-    // leaves each at least four stages
+    // split the reduction while the CTAs still fit at once and each has at
+    // least four stages
     a.split = 1;
     while (a.split < kLinMaxSplit && tiles * a.split * 2 <= 2 * sms && nk / (a.split * 2) >= 4)
         a.split *= 2;
     if (tiles * a.split > INT_MAX)
         return cudaErrorInvalidValue;
     const uint32_t stage = kLinATile + lin_b_tile(a.bn, a.b_mn);
-    a.stages = std::min<int>(kLinMaxStages, 96 * 1024 / stage);
-    const size_t smem =
-        1024 + std::max(size_t(a.stages) * stage, size_t(a.bn) * LM * 4);
+    // two CTAs an SM; the parts beside the ring, or in it at 128 columns
+    const uint32_t parts = a.bn < LM ? uint32_t(LM) * (a.bn + 4) * 4 : 0;
+    a.stages = std::min<int>(kLinMaxStages, (110 * 1024 - parts) / stage);
+    const size_t smem = 1024 + size_t(a.stages) * stage + parts;
     CUtensorMap ma, mb;
     cudaError_t e = lin_map(&ma, q.Y, q.y_mn ? LK : LM, a.f16);
     if (e == cudaSuccess)
