@@ -39,16 +39,22 @@ struct RouteArgs {
 };
 
 // Dynamic shared memory: the CTA's counts, then per group the experts under
-// choice (id, logit, key; 32 at least) or, once its tokens are done, its
-// probability sums.
+// choice (id and logit; for k <= 32 also key and id as one number, 32 of each
+// and a spare) or, once its tokens are done, its probability sums.
 __host__ __device__ inline int sel_slots(int k)
 {
-    return k > 32 ? k : 32;
+    return k > 32 ? (k + 3) & ~3 : 36;
+}
+
+__host__ __device__ inline int group_words(int k, int E)
+{
+    const int sel = (k > 32 ? 2 : 4) * sel_slots(k);
+    return sel > E ? sel : (E + 3) & ~3;
 }
 
 size_t route_smem(int E, int k, int W)
 {
-    return size_t(E) * 4 + size_t(kRouteWarps / W) * std::max(3 * sel_slots(k), E) * 4;
+    return size_t((E + 3) & ~3) * 4 + size_t(kRouteWarps / W) * group_words(k, E) * 4;
 }
 
 // Sum over the CTA in a fixed order; every thread gets it.
@@ -77,21 +83,21 @@ __device__ __forceinline__ X cta_sum(X v, X *red)
 __device__ __forceinline__ uint32_t warp_threshold(uint32_t own, uint32_t kmax, int k)
 {
     uint32_t t = kmax;
+#pragma unroll 4
     for (int j = 1; j < k; ++j) {
         own = own == t ? kTaken : own;
         t = __reduce_max_sync(kFull, own);
-        if (t <= kClosed)
-            return kClosed + 1;
     }
-    return t;
+    return max(t, kClosed + 1);
 }
 
 // One token per group of W warps at a time; a lane holds V of its logits.
 //
 // Choosing (a warp, k <= 32): keys at or above warp_threshold are collected
 // in shared memory, k of them at least and rarely more than a few extra (512
-// experts: 12 for k = 10); each lane takes one and counts how many precede
-// it, which is its slot.  With more than 32 (ties, or one lane holding most),
+// experts: 12 for k = 10), each with its expert as one 64-bit number that
+// orders them (key, then the lower expert); each lane takes one and counts
+// how many are larger, which is its slot.  With more than 32 (ties, or one lane holding most),
 // k > 32, or a CTA per token: k rounds of the group's largest key, whose
 // holder drops it and looks for its next best.
 template <typename L, int V, int W, int C, bool BIAS>
@@ -107,9 +113,10 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
     __shared__ uint32_t s_flags;
     const int g = threadIdx.x / G, lane = threadIdx.x % G;
     int *cnt = reinterpret_cast<int *>(smem);
-    int *sel_e = cnt + p.E + g * 3 * sel_slots(p.k);
+    float *ps = reinterpret_cast<float *>(cnt + ((p.E + 3) & ~3)) + g * group_words(p.k, p.E);
+    uint64_t *sel_o = reinterpret_cast<uint64_t *>(ps);  // key, then ~expert
+    int *sel_e = reinterpret_cast<int *>(sel_o + (p.k > 32 ? 0 : sel_slots(p.k)));
     float *sel_l = reinterpret_cast<float *>(sel_e + sel_slots(p.k));
-    uint32_t *sel_k = reinterpret_cast<uint32_t *>(sel_l + sel_slots(p.k));
     Group<W> gr{red};
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
         cnt[e] = 0;
@@ -120,23 +127,28 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
     pdl_launch_dependents();
 
     const L *logits = static_cast<const L *>(p.logits);
-    float acc[V];
+    float acc[V], bias[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+        const int e = expert_of<C, G>(lane, i);
         acc[i] = 0.0f;
-    const bool need_p = p.stats || (!p.norm && !p.sigmoid) || (BIAS && !p.sigmoid);
+        bias[i] = BIAS && e < p.E ? p.bias[e] : 0.0f;
+    }
+    const bool need_p = p.stats || (!p.norm && !p.sigmoid) || BIAS;
     bool bad = false;
     int live = 0;
     float zsum = 0.0f;
 
-    for (int64_t t = int64_t(blockIdx.x) * kGroups + g; t < p.T;
-         t += int64_t(gridDim.x) * kGroups) {
-        int32_t *ids = p.ids + t * p.k;
-        float *w = p.w + t * p.k;
+    int64_t t = int64_t(blockIdx.x) * kGroups + g;
+    const int64_t step = int64_t(gridDim.x) * kGroups;
+    const L *row = logits + t * p.ld;
+    int32_t *ids = p.ids + t * p.k;
+    float *w = p.w + t * p.k;
+    for (; t < p.T; t += step, row += step * p.ld, ids += step * p.k, w += step * p.k) {
         float l[V];
         uint32_t key[V], own = kClosed, kmax = kClosed;
         if (!p.mask || p.mask[t]) {
-            load_row<L, V, C, G>(l, logits + t * p.ld, lane, p.E, p.f16);
+            load_row<L, V, C, G>(l, row, lane, p.E, p.f16);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (!(l[i] < INFINITY)) {  // NaN or +inf: closed, and reported
@@ -185,22 +197,17 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
                 for (int i = 0; i < V; ++i)
                     acc[i] += s[i] * inv;
             }
-            if (BIAS && !p.sigmoid) {
+            if (BIAS) {
+                const float mul = p.sigmoid ? exp_ftz(c) : inv;  // s to scores
+                own = kClosed;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
+                for (int i = 0; i < V; ++i) {
                     if (l[i] > -INFINITY)
-                        key[i] = key_of(s[i] * inv + p.bias[expert_of<C, G>(lane, i)]);
+                        key[i] = key_of(s[i] * mul + bias[i]);
+                    own = max(own, key[i]);
+                }
+                kmax = gr.largest(own);
             }
-        }
-        if (BIAS) {
-            own = kClosed;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (p.sigmoid && l[i] > -INFINITY)
-                    key[i] = key_of(sig_scaled(l[i], 0.0f) + p.bias[expert_of<C, G>(lane, i)]);
-                own = max(own, key[i]);
-            }
-            kmax = gr.largest(own);
         }
         ++live;
 
@@ -227,25 +234,25 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (key[i] >= th) {
-                        sel_e[at] = expert_of<C, G>(lane, i);
-                        sel_l[at] = l[i];
+                        const int e = expert_of<C, G>(lane, i);
+                        sel_o[at] = uint64_t(key[i]) << 32 | uint32_t(~e);
                         if (BIAS)
-                            sel_k[at] = key[i];
+                            sel_l[at] = l[i];
                         ++at;
                     }
+                if (lane == 0)
+                    sel_o[all] = 0;  // the loop below takes two at a time
                 __syncwarp();
-                uint32_t kk = 0;
-                if (lane < all) {
-                    id = sel_e[lane];
-                    lid = sel_l[lane];
-                    kk = BIAS ? sel_k[lane] : key_of(lid);
+                const uint64_t o = lane < all ? sel_o[lane] : ~0ull;
+                id = ~int(uint32_t(o));
+                lid = BIAS ? sel_l[min(lane, 31)] : of_key(uint32_t(o >> 32));
+                slot = 0;
+                for (int j = 0; j < all; j += 2) {
+                    const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sel_o + j);
+                    slot += q.x > o;
+                    slot += q.y > o;
                 }
-                slot = lane < all ? 0 : 32;
-                for (int j = 0; j < all; ++j) {
-                    const uint32_t kj = __shfl_sync(kFull, kk, j);
-                    const int ej = __shfl_sync(kFull, id, j);
-                    slot += kj > kk || (kj == kk && ej < id);
-                }
+                slot = lane < all ? slot : p.k;
                 n = min(all, p.k);
             }
         }
@@ -332,13 +339,12 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
         s_z[g] = zsum;
     }
     __syncthreads();
-    float *ps = reinterpret_cast<float *>(cnt + p.E);  // [groups][E]
     if (p.stats) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = expert_of<C, G>(lane, i);
             if (e < p.E)
-                ps[g * p.E + e] = acc[i];
+                ps[e] = acc[i];
         }
         __syncthreads();
     }
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
         float s = 0.0f;
 #pragma unroll
         for (int q = 0; q < kGroups; ++q)
-            s += ps[q * p.E + e];
+            s += ps[(q - g) * group_words(p.k, p.E) + e];
         if (alone) {
             const float pr = s / nt;
             dot += float(cnt[e]) / (nt * float(p.k)) * pr;

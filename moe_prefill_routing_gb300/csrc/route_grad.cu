@@ -38,7 +38,7 @@ struct RouteGradArgs {
 
 // J: slots of a lane (k <= 32 W J).
 template <typename L, int V, int W, int C, int J>
-__global__ void __launch_bounds__(kGradThreads) k_route_grad(const RouteGradArgs p)
+__global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 4) k_route_grad(const RouteGradArgs p)
 {
     constexpr int G = 32 * W;
     constexpr int kGroups = kGradWarps / W;

@@ -92,7 +92,7 @@ def _check(T, E, k, seed=0, dtype=torch.float32, score="softmax", norm=True, sca
 @pytest.mark.parametrize("T,E,k", [
     (1, 1, 1), (1, 512, 10), (3, 2, 2), (5, 31, 4), (8, 32, 1), (9, 33, 33), (64, 64, 6),
     (100, 65, 8), (33, 128, 8), (40, 129, 16), (257, 256, 8), (50, 300, 64), (130, 512, 10),
-    (20, 513, 10), (12, 1000, 33), (9, 1025, 8), (6, 4096, 256)])
+    (40, 512, 256), (40, 500, 40), (20, 513, 10), (12, 1000, 33), (9, 1025, 8), (6, 4096, 256)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_shapes(T, E, k, score):
     _check(T, E, k, score=score)
