@@ -604,7 +604,8 @@ MOE_API int moe_linear_grad(const void *x, int64_t ldx, const void *W, const voi
  * out  counts  int32 [E+1]  counts, then n; or NULL
  * out  prob    fp32 [E] or NULL;  loss fp32 [2] or NULL
  * ws           moe_route_workspace_bytes(T, E) bytes, 256-byte aligned; its
- *              status word is set by every call (moe_read_status)
+ *              status word is set by every call (moe_read_status).  NULL, if
+ *              counts, prob and loss are: then no status is kept
  * T >= 0, 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E, MOE_MAX_TOPK), ld >= E,
  * T*k < 2^31.  All sums in a fixed order: results are deterministic.
  */

@@ -762,19 +762,20 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
     Returns ids int32 [T, k] and w fp32 [T, k] (what ``plan`` and
     ``layer_forward`` take) and, with ``stats``, counts int32 [E+1] (the
     last: tokens that take part), prob fp32 [E] and loss fp32 [2] (balance,
-    z); and the workspace ``ws`` (status word at byte 0).  bias fp32 [E] is
+    z), and the workspace ``ws`` (status word at byte 0; without ``stats``
+    only if one is passed in, and no status is kept otherwise).  bias fp32 [E] is
     added to the scores for the choice alone; mask [T] (bool or uint8) is 0
     for padding.  ``out`` may hold some of the outputs."""
     T, E = logits.shape
     dev = logits.device
     ld = _ld(logits, "logits", (T, E), _DTYPES, dev)
-    if ws is None:
+    if ws is None and stats:
         ws = torch.empty(route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
     cp = pp = sp = None
     if out is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        o = {"ids": ids, "w": w, "ws": ws}
+        o = {"ids": ids, "w": w}
         ip, wp = ids.data_ptr(), w.data_ptr()
         if stats:
             counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
@@ -783,7 +784,7 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
             o["counts"], o["prob"], o["loss"] = counts, prob, loss
             cp, pp, sp = counts.data_ptr(), prob.data_ptr(), loss.data_ptr()
     else:
-        o = dict(out, ws=ws)
+        o = dict(out)
 
         def output(name, shape, dtypes):
             if o.get(name) is None:
@@ -794,10 +795,13 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
         if stats:
             cp, pp = output("counts", (E + 1,), _I32), output("prob", (E,), _F32)
             sp = output("loss", (2,), _F32)
+    if ws is not None:
+        o["ws"] = ws
     _launch("moe_route", dev, logits.data_ptr(), ld, _DTYPES[logits.dtype],
             None if bias is None else _flat(bias, "bias", (E,), _F32, dev),
             None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, E, k,
-            _name(SCORES, score, "score"), norm, scale, ip, wp, cp, pp, sp, _ptr(ws), ws.numel())
+            _name(SCORES, score, "score"), norm, scale, ip, wp, cp, pp, sp,
+            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
     return o
 
 

@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
             p.part_count[int64_t(blockIdx.x) * p.E + e] = cnt[e];
         }
     }
+    if (!p.status)  // nobody asked for more than ids and weights
+        return;
     if (!alone) {
         if (threadIdx.x == 0)
             p.part_scal[blockIdx.x] =
@@ -517,9 +519,10 @@ extern "C" int moe_route(const void *logits, int64_t ld, int l_dtype, const floa
     const int rc = check_sizes(l_dtype, T, E, k, ld, score);
     if (rc != MOE_OK)
         return rc;
-    if (!ws || (T > 0 && (!logits || !ids || !w)))
+    const int stats = counts || prob || loss;
+    if ((stats && !ws) || (T > 0 && (!logits || !ids || !w)))
         return MOE_ERR_NULL;
-    if (ws_bytes < moe_route_workspace_bytes(T, E))
+    if (ws && ws_bytes < moe_route_workspace_bytes(T, E))
         return MOE_ERR_WORKSPACE;
     if (!aligned(logits, size_of(l_dtype)) || !aligned(bias, 4) || !aligned(ids, 4) ||
         !aligned(w, 4) || !aligned(counts, 4) || !aligned(prob, 4) || !aligned(loss, 4) ||
@@ -530,14 +533,16 @@ extern "C" int moe_route(const void *logits, int64_t ld, int l_dtype, const floa
     uint8_t *b = static_cast<uint8_t *>(ws);
     RouteArgs a = {};
     a.logits = logits, a.bias = bias, a.mask = mask, a.ids = ids, a.w = w;
-    a.part_scal = reinterpret_cast<float4 *>(b + 256);
-    a.part_prob = reinterpret_cast<float *>(b + 256 + align256(rows * sizeof(float4)));
-    a.part_count = reinterpret_cast<int32_t *>(a.part_prob + rows * E);
+    if (ws) {
+        a.part_scal = reinterpret_cast<float4 *>(b + 256);
+        a.part_prob = reinterpret_cast<float *>(b + 256 + align256(rows * sizeof(float4)));
+        a.part_count = reinterpret_cast<int32_t *>(a.part_prob + rows * E);
+    }
     a.status = reinterpret_cast<uint32_t *>(ws);
     a.counts = counts, a.prob = prob, a.loss = loss;
     a.ld = ld, a.T = T, a.E = E, a.k = k;
     a.sigmoid = score == MOE_SCORE_SIGMOID, a.norm = norm != 0;
-    a.stats = counts || prob || loss, a.f16 = l_dtype == MOE_DT_F16;
+    a.stats = stats, a.f16 = l_dtype == MOE_DT_F16;
     a.scale = scale;
     const int size = size_of(l_dtype);
     int grid = 1;
@@ -552,7 +557,7 @@ extern "C" int moe_route(const void *logits, int64_t ld, int l_dtype, const floa
             auto kern = bias ? k_route<L, V, W, C, true> : k_route<L, V, W, C, false>;
             return launch_pdl(kern, dim3(grid), dim3(kRouteThreads), route_smem(E, k, W), s, a);
         });
-    if (e == cudaSuccess && grid > 1) {
+    if (e == cudaSuccess && grid > 1 && ws) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kFinalCtas);
         cfg.blockDim = dim3(kFinalThreads);

@@ -91,6 +91,14 @@ __device__ __forceinline__ int expert_of(int lane, int i)
 template <int BYTES>
 struct Vec;
 template <>
+struct Vec<2> {
+    using type = uint16_t;
+};
+template <>
+struct Vec<4> {
+    using type = uint32_t;
+};
+template <>
 struct Vec<8> {
     using type = uint2;
 };
@@ -99,24 +107,19 @@ struct Vec<16> {
     using type = uint4;
 };
 
-// A lane's V logits of a row (-inf past E).  C > 1: E, the distance of rows
-// and the base are multiples of C elements.
+// A lane's V logits of a row as they are stored.  C > 1: E, the distance of
+// rows and the base are multiples of C elements.
 template <typename L, int V, int C, int G>
-__device__ __forceinline__ void load_row(float (&l)[V], const L *row, int lane, int E, int f16)
-{
-    if constexpr (C == 1) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + G * i;
-            l[i] = e < E ? to_f(row[e], f16) : -INFINITY;
-        }
-    } else {
-        using Q = typename Vec<C * int(sizeof(L))>::type;
-        static_assert(V % C == 0, "whole vectors");
-        union {
-            Q q;
-            L v[C];
-        } u[V / C];
+struct RawRow {
+    using Q = typename Vec<C * int(sizeof(L))>::type;
+    static_assert(V % C == 0, "whole accesses");
+    union {
+        Q q;
+        L v[C];
+    } u[V / C];
+
+    __device__ __forceinline__ void load(const L *row, int lane, int E)
+    {
 #pragma unroll
         for (int i = 0; i < V / C; ++i) {
             const int e = expert_of<C, G>(lane, i * C);
@@ -124,10 +127,23 @@ __device__ __forceinline__ void load_row(float (&l)[V], const L *row, int lane, 
             if (e < E)
                 u[i].q = *reinterpret_cast<const Q *>(row + e);
         }
+    }
+
+    // as floats, -inf past E
+    __device__ __forceinline__ void to(float (&l)[V], int lane, int E, int f16) const
+    {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             l[i] = expert_of<C, G>(lane, i) < E ? to_f(u[i / C].v[i % C], f16) : -INFINITY;
     }
+};
+
+template <typename L, int V, int C, int G>
+__device__ __forceinline__ void load_row(float (&l)[V], const L *row, int lane, int E, int f16)
+{
+    RawRow<L, V, C, G> raw;
+    raw.load(row, lane, E);
+    raw.to(l, lane, E, f16);
 }
 
 template <typename L, int V, int C, int G>

@@ -10,8 +10,9 @@
 //   no norm, sigmoid:  da_j += s_j scale dw_j
 //   sigmoid:           dl_e  = da_e sigmoid(-l_e)      (a = log sigmoid(l))
 //   z:                 dl_e += 2 g1 lse softmax(l)_e / n
-// One pass: a token's row is read once, its gradient written once; the
-// weights' part is k values a token, set out by expert in shared memory.
+// One pass: a token's row is read once (a token ahead), its gradient written
+// once; the weights' part is k values a token, set out by expert in shared
+// memory.
 #include "route.cuh"
 
 namespace moe {
@@ -36,16 +37,35 @@ struct RouteGradArgs {
     float scale;
 };
 
+// Sums of N values over a group; every lane gets them.
+template <int N, int W>
+__device__ __forceinline__ void sum_all(float (&v)[N], Group<W> &gr)
+{
+    if constexpr (W == 1) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] += __shfl_xor_sync(kFull, v[i], o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = gr.sum(v[i]);
+    }
+}
+
 // J: slots of a lane (k <= 32 W J).
 template <typename L, int V, int W, int C, int J>
-__global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 4) k_route_grad(const RouteGradArgs p)
+__global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 3)
+    k_route_grad(const RouteGradArgs p)
 {
     constexpr int G = 32 * W;
     constexpr int kGroups = kGradWarps / W;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint2 red[2][W];
     const int g = threadIdx.x / G, lane = threadIdx.x % G;
-    float *dsel = reinterpret_cast<float *>(smem) + size_t(g) * p.E;  // by expert; zeros
+    const int E4 = (p.E + 3) & ~3;
+    float *dsel = reinterpret_cast<float *>(smem) + size_t(g) * E4;  // by expert; zeros
     Group<W> gr{red};
     for (int e = lane; e < p.E; e += G)
         dsel[e] = 0.0f;
@@ -53,7 +73,6 @@ __global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 4) k_rout
     pdl_wait();
     pdl_launch_dependents();
 
-    const L *logits = static_cast<const L *>(p.logits);
     float cf[V], gz = 0.0f;
     const bool aux = p.counts && p.dloss;
     {
@@ -70,38 +89,51 @@ __global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 4) k_rout
         }
     }
 
-    for (int64_t t = int64_t(blockIdx.x) * kGroups + g; t < p.T;
-         t += int64_t(gridDim.x) * kGroups) {
-        L *orow = static_cast<L *>(p.dlogits) + t * p.ldd;
-        const L *row = logits + t * p.ld;
-        float l[V];
-        uint32_t kmax = kClosed;
-        int id[J];         // the lane's slots: expert (-1: none), its logit, scale dw
-        float v[J], d[J];
-        if (!p.mask || p.mask[t]) {
+    // what a token's gradient is made from, loaded one token ahead
+    RawRow<L, V, C, G> raw;
+    int id[J];    // the lane's slots: expert (-1: none) and scale dw
+    float d[J];
+    bool on;
+    int64_t t = int64_t(blockIdx.x) * kGroups + g;
+    const int64_t step = int64_t(gridDim.x) * kGroups;
+    const L *row = static_cast<const L *>(p.logits) + t * p.ld;
+    L *orow = static_cast<L *>(p.dlogits) + t * p.ldd;
+    auto fetch = [&](int64_t at, const L *from) {
+        on = !p.mask || p.mask[at];
+        raw.load(from, lane, p.E);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int at = lane + G * j;
-                id[j] = p.dw && at < p.k ? p.ids[t * p.k + at] : -1;
-                d[j] = p.dw && at < p.k ? p.scale * p.dw[t * p.k + at] : 0.0f;
-            }
-            load_row<L, V, C, G>(l, row, lane, p.E, p.f16);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                v[j] = uint32_t(id[j]) < uint32_t(p.E) ? to_f(row[id[j]], p.f16) : -INFINITY;
-                if (!(v[j] < INFINITY))
-                    v[j] = -INFINITY;
-            }
-            float own = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (!(l[i] < INFINITY))
-                    l[i] = -INFINITY;
-                own = fmaxf(own, l[i]);
-            }
-            kmax = gr.largest(key_of(own));
+        for (int j = 0; j < J; ++j) {
+            const int slot = lane + G * j;
+            id[j] = p.dw && slot < p.k ? p.ids[at * p.k + slot] : -1;
+            d[j] = p.dw && slot < p.k ? p.scale * p.dw[at * p.k + slot] : 0.0f;
         }
-        if (kmax == kClosed) {
+    };
+    if (t < p.T)
+        fetch(t, row);
+    for (; t < p.T; t += step, row += step * p.ld, orow += step * p.ldd) {
+        float l[V], v[J], dj[J];
+        int e[J];
+        raw.to(l, lane, p.E, p.f16);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            e[j] = on ? id[j] : -1;
+            dj[j] = d[j];
+            // the slot's logit (read again: this lane need not hold it)
+            v[j] = uint32_t(e[j]) < uint32_t(p.E) ? to_f(row[e[j]], p.f16) : -INFINITY;
+            if (!(v[j] < INFINITY))
+                v[j] = -INFINITY;
+        }
+        float own = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!(l[i] < INFINITY))
+                l[i] = -INFINITY;
+            own = fmaxf(own, l[i]);
+        }
+        const uint32_t kmax = on ? gr.largest(key_of(own)) : kClosed;
+        if (t + step < p.T)
+            fetch(t + step, row + step * p.ld);
+        if (kmax == kClosed) {  // takes no part
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 l[i] = 0.0f;
@@ -110,11 +142,13 @@ __global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 4) k_rout
         }
         const float m = of_key(kmax);
         const float c = p.sigmoid ? fminf(m, 0.0f) : 0.0f;
-        float s[V], sum = 0.0f, sume = 0.0f, pc = 0.0f;
+        float s[V];
+        enum { kS, kP, kQ, kD, kE, kSums };  // sums: s, s c, q, q dw, e^(l-m)
+        float sums[kSums] = {};
         if (p.sigmoid) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                sume += exp_ftz(l[i] - m);
+                sums[kE] += exp_ftz(l[i] - m);
                 s[i] = sig_scaled(l[i], c);
             }
         } else {
@@ -124,72 +158,92 @@ __global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 4) k_rout
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            sum += s[i];
-            pc += s[i] * cf[i];
+            sums[kS] += s[i];
+            sums[kP] += s[i] * cf[i];
         }
-
-        // the chosen experts' scores
-        float q[J], sq = 0.0f, sd = 0.0f;
-        if (p.dw) {
-            float ms = m, cs = 0.0f;  // no norm: the scores themselves
-            if (p.norm) {
-                uint32_t own = kClosed;
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    own = max(own, key_of(v[j]));
-                ms = of_key(gr.largest(own));  // -inf where no slot has weight
-                cs = fminf(ms, 0.0f);
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                q[j] = v[j] == -INFINITY ? 0.0f
-                       : p.sigmoid       ? sig_scaled(v[j], cs)
-                                         : exp_ftz(v[j] - ms);
-                sq += q[j];
-                sd += q[j] * d[j];
-            }
-        }
-        sum = gr.sum(sum);
-        const float inv = rcp_ftz(sum);
-        pc = aux ? gr.sum(pc) * inv : 0.0f;
-        sume = !p.sigmoid ? sum : aux ? gr.sum(sume) : 1.0f;
-        float dot = 0.0f;  // no norm, softmax: sum s scale dw
-        if (p.dw) {
-            float mul = 1.0f, mean = 0.0f;
-            if (p.norm) {
-                sq = gr.sum(sq);
-                mul = sq > 0.0f ? rcp_ftz(sq) : 0.0f;
-                mean = gr.sum(sd) * mul;
-            } else if (!p.sigmoid) {
-                mul = inv;
-                dot = gr.sum(sd) * inv;
-            }
+        // the chosen experts' scores: over their own maximum, or as they are
+        float q[J], ms = m, cs = 0.0f;
+        if (p.dw && p.norm) {
+            uint32_t o = kClosed;
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                if (v[j] > -INFINITY)
-                    dsel[id[j]] = q[j] * mul * (d[j] - mean);
+                o = max(o, key_of(v[j]));
+            ms = of_key(gr.largest(o));  // -inf where no slot has weight
+            cs = fminf(ms, 0.0f);
         }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            q[j] = v[j] == -INFINITY ? 0.0f
+                   : p.sigmoid       ? sig_scaled(v[j], cs)
+                                     : exp_ftz(v[j] - ms);
+            sums[kQ] += q[j];
+            sums[kD] += q[j] * dj[j];
+        }
+        if (p.sigmoid) {
+            sum_all(sums, gr);
+        } else if (aux && p.dw) {
+            float four[4] = {sums[kS], sums[kP], sums[kQ], sums[kD]};
+            sum_all(four, gr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sums[i] = four[i];
+        } else {  // without counts or without dw two of them are 0
+            float three[3] = {sums[kS], aux ? sums[kP] : sums[kQ], sums[kD]};
+            sum_all(three, gr);
+            sums[kS] = three[0];
+            (aux ? sums[kP] : sums[kQ]) = three[1];
+            sums[kD] = three[2];
+        }
+        const float inv = rcp_ftz(sums[kS]);
+        const float sume = p.sigmoid ? sums[kE] : sums[kS];
+        float mul = p.sigmoid ? 1.0f : inv, mean = 0.0f, base = sums[kP] * inv;
+        if (p.norm) {
+            mul = sums[kQ] > 0.0f ? rcp_ftz(sums[kQ]) : 0.0f;
+            mean = sums[kD] * mul;
+        } else if (!p.sigmoid) {
+            base += sums[kD] * inv;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (v[j] > -INFINITY)
+                dsel[e[j]] = q[j] * mul * (dj[j] - mean);
         gr.sync();
         const float zc = gz * (m + __logf(sume)) * rcp_ftz(sume);
-        const float base = pc + dot;
+        float ds[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = expert_of<C, G>(lane, i);
-            float o = s[i] * inv * (cf[i] - base) + (e < p.E ? dsel[e] : 0.0f);
-            if (p.sigmoid)
-                o = o * rcp_ftz(1.0f + exp_ftz(l[i])) + zc * exp_ftz(l[i] - m);
-            else
-                o += zc * s[i];
-            l[i] = l[i] > -INFINITY ? o : 0.0f;
+        for (int i = 0; i < V; i += C) {
+            const int x = expert_of<C, G>(lane, i);
+            if constexpr (C >= 4) {
+#pragma unroll
+                for (int h = 0; h < C; h += 4) {
+                    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (x < p.E)
+                        f = *reinterpret_cast<const float4 *>(dsel + x + h);
+                    ds[i + h] = f.x, ds[i + h + 1] = f.y, ds[i + h + 2] = f.z, ds[i + h + 3] = f.w;
+                }
+            } else {
+                ds[i] = x < p.E ? dsel[x] : 0.0f;
+            }
+        }
+        if (p.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float da = s[i] * inv * (cf[i] - base) + ds[i];
+                const float o = da * rcp_ftz(1.0f + exp_ftz(l[i])) + zc * exp_ftz(l[i] - m);
+                l[i] = l[i] > -INFINITY ? o : 0.0f;
+            }
+        } else {  // s, ds and with them the gradient are 0 for closed experts
+            const float z0 = zc - inv * base;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                l[i] = s[i] * (inv * cf[i] + z0) + ds[i];
         }
         store_row<L, V, C, G>(l, orow, lane, p.E, p.f16);
         gr.sync();
-        if (p.dw) {
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (v[j] > -INFINITY)
-                    dsel[id[j]] = 0.0f;
-        }
+        for (int j = 0; j < J; ++j)
+            if (v[j] > -INFINITY)
+                dsel[e[j]] = 0.0f;
         gr.sync();
     }
 }
@@ -236,7 +290,7 @@ extern "C" int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const
             auto kern = W > 1 || k <= 32 ? k_route_grad<L, V, W, C, 1>
                                          : k_route_grad<L, V, W, C, W == 1 ? 8 : 1>;
             return launch_pdl(kern, dim3(grid), dim3(kGradThreads),
-                              size_t(per) * E * 4, reinterpret_cast<cudaStream_t>(stream), a);
+                              size_t(per) * ((E + 3) & ~3) * 4, reinterpret_cast<cudaStream_t>(stream), a);
         });
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -161,6 +161,9 @@ def test_route_reports_logits_that_are_no_numbers():
     ref = R.route(l.double().numpy(), 5)
     r = B.route(l.cuda(), 5)
     assert B.read_status(r["ws"]) == B.STATUS_BAD_LOGIT
+    lean = B.route(l.cuda(), 5, stats=False, ws=torch.empty_like(r["ws"]))
+    assert B.read_status(lean["ws"]) == B.STATUS_BAD_LOGIT and "ws" not in B.route(
+        l.cuda(), 5, stats=False)
     assert np.array_equal(r["ids"].cpu().numpy(), ref["ids"])
     ok = B.route(_logits(50, 96, 4).cuda(), 5, ws=r["ws"])
     assert B.read_status(ok["ws"]) == 0

@@ -40,6 +40,14 @@ def test_linear(lib, kw, rc):
     assert _call(lib.moe_linear, LIN, LIN_OK, **kw) == getattr(B, "MOE_ERR_" + rc)
 
 
+def test_route_needs_a_workspace_for_statistics(lib):
+    none = dict(counts=None, prob=None, loss=None)
+    for name in none:
+        kw = {**none, name: FAKE, "ws": None}
+        assert _call(lib.moe_route, ROUTE, ROUTE_OK, **kw) == B.MOE_ERR_NULL
+    assert _call(lib.moe_route, ROUTE, ROUTE_OK, **none, ws_bytes=8) == B.MOE_ERR_WORKSPACE
+
+
 def test_linear_without_tokens_does_nothing(lib):
     assert _call(lib.moe_linear, LIN, LIN_OK, T=0, x=None, y=None) == B.MOE_OK
 
