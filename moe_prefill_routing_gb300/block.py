@@ -1,0 +1,88 @@
+"""A whole mixture-of-experts block on the library: router, routed experts, a
+dense expert beside them and the residual; and a training step of the router.
+
+    python -m moe_prefill_routing_gb300.block      # needs a GB300
+
+``MoeBlock.forward`` is what a model runs per layer (a prefill chunk or a few
+decoded tokens); ``MoeBlock.train_router`` takes one gradient step that
+balances the experts, the experts' weights fixed.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+
+class MoeBlock:
+    """out = x + experts(x) + down(gelu(up(x))), the experts chosen by a router.
+
+    Wr [E, d] are the router's weights and ``layer`` a binding.MoeLayer over
+    the E experts; ``up`` [h, d] and ``down`` [d, h] the dense expert, or None.
+    ``score``, ``norm``, ``scale`` and the per-expert selection ``bias`` are
+    moe_route's."""
+
+    def __init__(self, layer: B.MoeLayer, Wr, k: int, up=None, down=None, bias=None,
+                 score: str = "softmax", norm: bool = True, scale: float = 1.0):
+        self.layer, self.Wr, self.k = layer, Wr, k
+        self.up, self.down, self.bias = up, down, bias
+        self.how = dict(score=score, norm=norm, scale=scale)
+
+    def route(self, x, mask=None, stats: bool = False) -> dict:
+        """The router alone: its fp32 logits and what ``binding.route`` returns."""
+        logits = B.linear(x, self.Wr, out_dtype=torch.float32)
+        r = B.route(logits, self.k, bias=self.bias, mask=mask, stats=stats, **self.how)
+        r["logits"] = logits
+        return r
+
+    def forward(self, x, mask=None):
+        r = self.route(x, mask)
+        y = self.layer.forward(x, r["ids"], r["w"])
+        # the residual stream rides on the dense expert's down projection, or
+        # is added to the experts' sum as it is
+        if self.up is None:
+            return y.add_(x)
+        h = B.linear(x, self.up, act="gelu_tanh")
+        return B.linear(h, self.down, residual=y.add_(x), y=y)
+
+    def train_router(self, x, lr: float, balance: float = 1e-2, z: float = 1e-3, dw=None,
+                     mask=None):
+        """One SGD step on Wr for balance * (balance loss) + z * (z loss) (and,
+        with ``dw`` [T, k], the loss whose gradient with respect to the
+        routing weights it is).  Returns (losses [2], dx): the losses before
+        the step and the gradient with respect to x."""
+        r = self.route(x, mask, stats=True)
+        dloss = torch.tensor([balance, z], dtype=torch.float32, device=x.device)
+        dlogits = B.route_grad(r["logits"], r["ids"], r["counts"], dw=dw, dloss=dloss, mask=mask,
+                               **self.how)
+        dx, dWr, _ = B.linear_grad(x, self.Wr, dlogits, need=(True, True, False),
+                                   dw_dtype=torch.float32)
+        self.Wr.copy_(self.Wr.float() - lr * dWr)
+        return r["loss"], dx
+
+
+def main():
+    torch.manual_seed(0)
+    T, d, E, k, f, h = 512, 256, 32, 4, 128, 512
+    dev, bf = "cuda", torch.bfloat16
+
+    def randn(*shape, amp=1.0):
+        return (amp * torch.randn(*shape, device=dev)).to(bf)
+
+    layer = B.MoeLayer(randn(E, d, f, amp=0.05), randn(E, d, f, amp=0.05),
+                       randn(E, f, d, amp=0.05))
+    # a router that prefers some experts
+    Wr = randn(E, d, amp=0.03) + randn(E, 1, amp=0.02)
+    block = MoeBlock(layer, Wr, k, up=randn(h, d, amp=0.05), down=randn(d, h, amp=0.05))
+    x = randn(T, d) + 0.3
+    print("block output", tuple(block.forward(x).shape))
+    for step in range(60):
+        loss, _ = block.train_router(x, lr=0.05, balance=1.0, z=1e-2)
+        if step % 10 == 0 or step == 59:
+            counts = block.route(x, stats=True)["counts"][:E]
+            print(f"step {step:2d}: balance loss {float(loss[0]):.4f}  z loss {float(loss[1]):.3f}"
+                  f"  tokens of the busiest expert {int(counts.max())} (mean {T * k // E})")
+
+
+if __name__ == "__main__":
+    main()
