@@ -40,6 +40,13 @@ constexpr int kLinMaxStages = 8;
 constexpr int kLinMaxSplit = 8;  // portable cluster size
 constexpr uint64_t kLinDrainNs = 200000000ull;
 
+// The tensor core adds each product of 16 r to its fp32 accumulator with
+// truncation, so a sum drifts by about 1.6e-8 of itself per addition (2.7e-6
+// measured for r = 2560).  That is nothing beside a 16-bit output's rounding;
+// an fp32 output's sums are cut into chains of kChain steps of 64 r (32
+// additions, 5e-7) that are added outside the tensor core.
+constexpr int kChain = 8;
+
 struct LinArgs {
     const float *bias;
     const void *residual;
@@ -50,6 +57,7 @@ struct LinArgs {
     int M, N, R;     // k_linear: M = j, N = i; k_linear_pair: M = i, N = j
     int a_mn, b_mn;  // the operand's m (n) is contiguous, not its r
     int bn, stages, split, n_mt;
+    int chain;       // steps of 64 r that one accumulator sums, see kChain
     int f16, out_f32, act;
     int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
 };
@@ -86,6 +94,26 @@ __device__ __forceinline__ void dsmem_st4(uint32_t a, uint32_t x, uint32_t y, ui
                  : "memory");
 }
 
+// (Phi(z), e^(-z^2/2)), Phi the normal distribution function, from
+// erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), x >= 0: formula
+// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions, off
+// by 1.5e-7 at most (Phi by half of that).  The library's erfc is more exact
+// than any output here needs and takes registers that the epilogue lacks.
+__device__ __forceinline__ float2 normal_cdf(float z)
+{
+    const float x = fabsf(z) * 0.7071067811865476f;
+    float t, e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(1.0f + 0.3275911f * x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * -0.7213475204444817f));
+    float q = 1.061405429f;
+    q = q * t - 1.453152027f;
+    q = q * t + 1.421413741f;
+    q = q * t - 0.284496736f;
+    q = q * t + 0.254829592f;
+    q = 0.5f * q * t * e;
+    return make_float2(z > 0.0f ? 1.0f - q : q, e);
+}
+
 // sqrt(2/pi) (z + 0.044715 z^3) times two; (1 + tanh u) / 2 is 1 / (1 + e^-2u)
 __device__ __forceinline__ float gelu_2u(float z)
 {
@@ -100,7 +128,7 @@ __device__ __forceinline__ float act_t(float z)
     else if constexpr (ACT == MOE_ACT_SILU)
         return z * sigmoid_ftz(z);
     else if constexpr (ACT == MOE_ACT_GELU)
-        return 0.5f * z * erfcf(z * -0.7071067811865476f);
+        return z * normal_cdf(z).x;
     else if constexpr (ACT == MOE_ACT_GELU_TANH)
         return z * sigmoid_ftz(gelu_2u(z));
     else
@@ -134,8 +162,8 @@ __device__ __forceinline__ float act_grad(float z)
         const float s = sigmoid_ftz(z);
         return s * (1.0f + z * (1.0f - s));
     } else if constexpr (ACT == MOE_ACT_GELU) {
-        return 0.5f * erfcf(z * -0.7071067811865476f) +
-               0.3989422804014327f * z * __expf(-0.5f * z * z);
+        const float2 c = normal_cdf(z);
+        return c.x + 0.3989422804014327f * z * c.y;
     } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
         const float s = sigmoid_ftz(gelu_2u(z));
         const float du2 = 1.5957691216057308f + 3.0f * 0.07135481627260025f * z * z;
@@ -269,7 +297,11 @@ __global__ void __launch_bounds__(kLinThreads)
     const int m0 = (tile % p.n_mt) * LM, n0 = (tile / p.n_mt) * bn;
     const int nk = (p.R + LK - 1) / LK;
     const int kb0 = int(int64_t(nk) * z / p.split), kb1 = int(int64_t(nk) * (z + 1) / p.split);
-    const uint32_t tmem_cols = bn < 32 ? 32u : uint32_t(bn);
+    // chains of p.chain steps, each in an accumulator of its own
+    const int accs = max(1, (kb1 - kb0 + p.chain - 1) / p.chain);
+    uint32_t tmem_cols = 32;
+    while (tmem_cols < uint32_t(accs * bn))
+        tmem_cols *= 2;
     volatile int *abort_flag = &ctl.abort_flag;
 
     if (threadIdx.x == 0) {
@@ -349,6 +381,8 @@ __global__ void __launch_bounds__(kLinThreads)
         const uint64_t da0 = p.a_mn ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
         const uint64_t db0 = p.b_mn ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
         const bool one = elect_one();
+        uint32_t d = tmem_base;
+        int left = p.chain;
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!__all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag)))
                 break;
@@ -357,9 +391,14 @@ __global__ void __launch_bounds__(kLinThreads)
                 const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
 #pragma unroll
                 for (int kk = 0; kk < LK / 16; ++kk)
-                    tc_mma_f16(tmem_base, da0 + off + kk * (p.a_mn ? 128 : 2),
-                               db0 + off + kk * (p.b_mn ? 128 : 2), idesc, kb != kb0 || kk != 0);
+                    tc_mma_f16(d, da0 + off + kk * (p.a_mn ? 128 : 2),
+                               db0 + off + kk * (p.b_mn ? 128 : 2), idesc,
+                               left != p.chain || kk != 0);
                 tc_commit(&ctl.empty[stage]);
+            }
+            if (--left == 0) {
+                left = p.chain;
+                d += uint32_t(bn);
             }
             __syncwarp();
             if (++stage == S) {
@@ -408,6 +447,15 @@ __global__ void __launch_bounds__(kLinThreads)
             if (done) {
                 tmem_ld_32x32b_x16(t0 + uint32_t(c), r);
                 tmem_ld_wait();
+#pragma unroll 1
+                for (int i = 1; i < accs; ++i) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(t0 + uint32_t(i * bn + c), o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
+                }
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
@@ -497,6 +545,7 @@ struct PairArgs {
     LinArgs p[2];
     int tiles[2];       // 0 for an absent second product
     int bn;             // the larger of the two
+    int cut;            // chains are cut (an fp32 output)
     uint32_t sub_bytes; // of shared memory for 64 r of both operands
     // Pair q of the grid's first takes tiles q, q + pairs, ... of product 0;
     // the `extra` pairs that get one more of them take at most `shared`
@@ -678,6 +727,28 @@ __device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float
     __syncwarp();
 }
 
+// Adds (or, first, copies) `width` columns of an accumulator to the sum of the
+// earlier chains; whole warp, its 32 lanes of tensor memory.  Not inlined: the
+// epilogue's registers are its loop's.
+__device__ __noinline__ void add_chain(uint32_t acc, uint32_t sum, int width, bool add)
+{
+#pragma unroll 1
+    for (int c = 0; c < width; c += 32) {
+        uint32_t r[32], o[32];
+        tmem_ld_32x32b_x32(acc + uint32_t(c), r);
+        if (add)
+            tmem_ld_32x32b_x32(sum + uint32_t(c), o);
+        tmem_ld_wait();
+        if (add) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
+        }
+        tmem_st_32x32b_x32(sum + uint32_t(c), r);
+    }
+    tmem_st_wait();
+}
+
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ PairArgs g)
 {
@@ -694,7 +765,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr int S = kPairStages;
     const uint32_t sub_bytes = g.sub_bytes;
     uint8_t *stg = smem + S * kPairSub * sub_bytes;
-    const uint32_t tmem_cols = g.bn <= 64 ? 128u : g.bn <= 128 ? 256u : 512u;  // two accumulators
+    // two accumulators and, where chains are cut, the sum of the earlier ones
+    const uint32_t tmem_need = uint32_t(g.bn) * (g.cut ? 3 : 2);
+    const uint32_t tmem_cols = tmem_need <= 128 ? 128u : tmem_need <= 256 ? 256u : 512u;
     volatile int *abort_flag = &ctl.abort_flag;
 
     if (threadIdx.x == 0) {
@@ -840,12 +913,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint64_t da0 = smem_desc_sw128(sa, p.a_mn ? 8192 : 16, 1024);
             const uint64_t db0 = smem_desc_sw128(sb, p.b_mn ? 8192 : 16, 1024);
             const uint32_t ia = p.a_mn ? 128 : 2, ib = p.b_mn ? 128 : 2;
-            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
-            if (!ok)
-                break;
-            tc_fence_after_sync();
-            const uint32_t d = tmem_base + uint32_t(buf * g.bn);
+            uint32_t d = 0;
+            int left = 0;  // steps to go in this chain
             for (int kb = w.nk0; kb < w.nk1; kb += kPairSub) {
+                const bool start = left == 0;
+                if (start) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
+                    if (!ok)
+                        break;
+                    d = tmem_base + uint32_t(buf * g.bn);
+                    left = p.chain;
+                }
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
                 if (!ok)
                     break;
@@ -858,7 +937,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                             for (uint32_t kk = 0; kk < LK / 16; ++kk)
                                 tc_mma_f16_pair(d, da0 + (off + kk * ia), db0 + (off + kk * ib),
-                                                idesc, kb != w.nk0 || h != 0 || kk != 0);
+                                                idesc, !start || h != 0 || kk != 0);
                         }
                     }
                     tc_commit_pair(&ctl.empty[stage], uint16_t(3u << lead));
@@ -868,15 +947,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     stage = 0;
                     phase ^= 1u;
                 }
-            }
-            if (!ok)
-                break;
-            if (one)
-                tc_commit_pair(&ctl.acc_full[buf], uint16_t(3u << lead));
-            __syncwarp();
-            if (++buf == 2) {
-                buf = 0;
-                aphase ^= 1u;
+                left -= kPairSub;
+                if (left <= 0 || kb + kPairSub >= w.nk1) {  // the chain is complete
+                    left = 0;
+                    if (one)
+                        tc_commit_pair(&ctl.acc_full[buf], uint16_t(3u << lead));
+                    __syncwarp();
+                    if (++buf == 2) {
+                        buf = 0;
+                        aphase ^= 1u;
+                    }
+                }
             }
         }
         // (the epilogue warps of both CTAs wait for every accumulator, so the
@@ -907,8 +988,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 return p.bias && c + int(lane) < width ? p.bias[n0 + c + int(lane)] : 0.0f;
             };
             float bias = bias_of(0);
-            const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(buf * g.bn);
+            const uint32_t lanes = tmem_base + (uint32_t(q * 32) << 16);
+            auto release = [&] {  // this accumulator has been read
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(dsmem_addr(&ctl.acc_empty[buf], lead));
+                if (++buf == 2) {
+                    buf = 0;
+                    aphase ^= 1u;
+                }
+            };
             bool ok = true;
+            // a sum cut into chains is put together in tensor memory
+            int chains = (w.nk1 - w.nk0 + p.chain - 1) / p.chain;
+            const bool cut = chains > 1;
+            const uint32_t t1 = lanes + uint32_t(2 * g.bn);
+            for (bool sum = false; cut && chains > 0; --chains, sum = true) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                const uint32_t t0 = lanes + uint32_t(buf * g.bn);
+                add_chain(t0, t1, width, sum);
+                release();
+            }
+            const uint32_t t0 = cut ? t1 : lanes + uint32_t(buf * g.bn);
             uint32_t r[32];
 #pragma unroll 1
             for (int c = 0; ok && (c == 0 || (rows > 0 && c < width)); c += 32) {
@@ -916,8 +1021,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     stage_residual(p, mine, row, n0 + c, rows, min(32, width - c));
                 __syncwarp();
                 if (c == 0) {
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
+                    if (!cut)
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
                     if (!ok || rows <= 0)
                         break;
                     tc_fence_after_sync();
@@ -937,14 +1043,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             if (!ok)
                 break;
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(dsmem_addr(&ctl.acc_empty[buf], lead));
-            if (++buf == 2) {
-                buf = 0;
-                aphase ^= 1u;
-            }
+            if (!cut)
+                release();
         }
     }
     __syncwarp();
@@ -1283,20 +1383,24 @@ double pair_step(int bn, bool y_mn)
 // A tile's epilogue (about 1500 cycles per 64 columns) hides behind the next
 // tile's MMAs, except the last one's; starting takes about 5000 cycles, and
 // joining the parts of a split tile about 8000.
-Tiling choose_tiling(const Product &q, int sms)
+constexpr int kCutMaxBn = 160;  // three times as many columns fit tensor memory
+
+Tiling choose_tiling(const Product &q, int sms, int max_bn)
 {
     Tiling t{false, 0, 1, 0, 0.0};
     if (q.rows <= 128)
         return t;
     const int nk = (q.R + LK - 1) / LK, pairs = std::max(1, sms / 2);
     double best = 0.0;
-    for (int bn = 256; bn >= 64; bn -= 32) {
+    for (int bn = max_bn; bn >= 64; bn -= 32) {
         const int64_t tiles =
             ((int64_t(q.rows) + 255) / 256) * ((int64_t(q.cols) + bn - 1) / bn);
         for (int z = 1; z <= kPairMaxSplit; z *= 2) {
             // a split tile needs room for the parts beside the ring
             if (z > 1 && (nk / z < 4 || tiles * z > pairs || (bn != 64 && bn != 128)))
                 break;
+            if (z > 1 && q.a.out_f32 && (nk + z - 1) / z > kChain)
+                continue;  // its chains are not cut further
             const double main = pair_step(bn, q.y_mn) * ((nk + z - 1) / z);
             const double epi = 1500.0 * ((bn + 63) / 64);
             const int64_t waves = (tiles + pairs - 1) / pairs;
@@ -1311,20 +1415,29 @@ Tiling choose_tiling(const Product &q, int sms)
     return t;
 }
 
+constexpr int kSmallTmem = 256;
+
 cudaError_t launch_small(const Product &q, cudaStream_t s)
 {
     const int sms = device_sm_count(), nk = (q.R + LK - 1) / LK;
     LinArgs a = q.a;
     a.M = q.cols, a.N = q.rows, a.R = q.R;
     a.a_mn = q.y_mn, a.b_mn = q.x_mn;
-    a.bn = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
+    a.bn = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 || a.out_f32 ? 64 : 128;
     a.n_mt = (q.cols + LM - 1) / LM;
     const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.rows) + a.bn - 1) / a.bn);
     // split the reduction while the CTAs still fit at once and each has at
-    // least four stages
+    // least four stages, or until the chains of an fp32 output fit the 256
+    // columns of tensor memory that each of two CTAs has
+    const int fit = kSmallTmem / a.bn * kChain;
     a.split = 1;
-    while (a.split < kLinMaxSplit && tiles * a.split * 2 <= 2 * sms && nk / (a.split * 2) >= 4)
+    while (a.split < kLinMaxSplit &&
+           ((tiles * a.split * 2 <= 2 * sms && nk / (a.split * 2) >= 4) ||
+            (a.out_f32 && nk > fit * a.split)))
         a.split *= 2;
+    const int steps = (nk + a.split - 1) / a.split;
+    a.chain = !a.out_f32 ? std::max(steps, 1)
+                         : std::max(kChain, (steps + kSmallTmem / a.bn - 1) / (kSmallTmem / a.bn));
     if (tiles * a.split > INT_MAX)
         return cudaErrorInvalidValue;
     const uint32_t stage = kLinATile + lin_b_tile(a.bn, a.b_mn);
@@ -1368,6 +1481,9 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         a.a_mn = q[i].x_mn, a.b_mn = q[i].y_mn;
         a.bn = t[i].bn, a.split = t[i].split;
         a.n_mt = int((int64_t(a.M) + 2 * LM - 1) / (2 * LM));
+        const int nk = (a.R + LK - 1) / LK;
+        a.chain = a.out_f32 ? kChain : std::max(nk, 1);
+        g.cut |= a.split == 1 && nk > a.chain;
         g.tiles[i] = int(t[i].tiles);
         g.bn = std::max(g.bn, a.bn);
         g.sub_bytes = std::max(g.sub_bytes, kLinATile + pair_b_bytes(a.bn, a.b_mn));
@@ -1408,8 +1524,11 @@ cudaError_t launch_products(Product *q, int count, ColSums sums, cudaStream_t s)
     if (count == 2 && q[1].R > q[0].R)
         std::swap(q[0], q[1]);
     Tiling t[2] = {};
+    bool f32 = false;
     for (int i = 0; i < count; ++i)
-        t[i] = choose_tiling(q[i], sms);
+        f32 |= q[i].a.out_f32 != 0;
+    for (int i = 0; i < count; ++i)
+        t[i] = choose_tiling(q[i], sms, f32 ? kCutMaxBn : 256);
     cudaError_t e = cudaSuccess;
     if (count == 2 && t[0].pair && t[1].pair && t[0].split == 1 && t[1].split == 1) {
         e = launch_pairs(q, t, 2, sums, s);

@@ -82,6 +82,27 @@ def test_linear_epilogues(act, out):
     _check_linear(9, 1536, 300, act, torch.bfloat16, out, bias=False, res=False, pre=False)
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_values(act):
+    # every bf16 value from 2^-20 to 2^6, of both signs, through an identity
+    # product.  GELU's erf is a formula good to 1.5e-7, so its factor of z to
+    # half of that; the others' factors to a few units of 2^-24
+    bits = torch.arange(0x3580, 0x4280, dtype=torch.int32)
+    z = torch.cat([bits, bits | 0x8000]).to(torch.int16).view(torch.bfloat16)
+    z = z[:z.numel() // 16 * 16].reshape(-1, 16)
+    y = B.linear(z.cuda(), torch.eye(16, dtype=torch.bfloat16, device="cuda"), act=act,
+                 out_dtype=torch.float32)
+    ref = R.act(_f64(z), act)
+    assert np.all(np.abs(_f64(y) - ref) <= (0.75e-7 + 2.0 ** -21) * np.abs(_f64(z)))
+    one = torch.ones(z.shape, dtype=torch.float32, device="cuda")
+    _, _, db = B.linear_grad(z.cuda(), torch.eye(16, dtype=torch.bfloat16, device="cuda"), one[:1]
+                             .expand(z.shape).contiguous(), pre=z.cuda(), act=act,
+                             need=(False, False, True))
+    want = R.act_grad(_f64(z), act).sum(0)
+    assert np.all(np.abs(_f64(db) - want) <= (0.75e-7 + 2.0 ** -20) * np.maximum(
+        1.0, np.abs(_f64(z))).sum(0))
+
+
 def test_linear_large_tiles():
     # more tiles than CTAs fit at once, ragged in both directions
     _check_linear(2050, 256, 2600, "gelu_tanh", torch.bfloat16, torch.bfloat16)
