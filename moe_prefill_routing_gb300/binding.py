@@ -608,23 +608,7 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _MASK = (torch.bool, torch.uint8)
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_fns: dict = {}
-
-
-def _launch(name: str, dev, *args):
-    """The library's entry point `name` with the device's current stream, the
-    device being current."""
-    fn = _fns.get(name)
-    if fn is None:
-        fn = _fns[name] = getattr(lib(), name)
-    i = dev.index
-    if i == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(i))
-    if rc:
-        raise MoeError(name, rc)
+_current_device = torch.cuda.current_device
 
 
 def _refuse(t, name: str, shape, dtypes, dev):
@@ -659,11 +643,8 @@ def _ld(t, name: str, shape, dtypes, dev) -> int:
     return step if rows > 1 else (cols + 7) // 8 * 8
 
 
-def _name(table: dict, key: str, what: str) -> int:
-    c = table.get(key)
-    if c is None:
-        raise ValueError(f"{what}: one of {', '.join(table)}; got {key!r}")
-    return c
+def _unknown(table: dict, key: str, what: str):
+    raise ValueError(f"{what}: one of {', '.join(table)}; got {key!r}")
 
 
 def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pre=None, y=None,
@@ -680,12 +661,18 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
     dt = x.dtype
     dev = x.device
     ldx = _ld(x, "x", (T, K), _16, dev)
-    wp = _flat(W, "W", (N, K), (dt,), dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return linear(x, W, bias, residual, act, out_dtype, pre, y, status)
+    if W.shape[1] != K or W.dtype is not dt or W.device != dev or not W.is_contiguous():
+        _refuse(W, "W", (N, K), (dt,), dev)
     if y is None:
-        y = torch.empty((T, N), dtype=out_dtype or dt, device=dev)
-        ldy = N
-        if out_dtype is not None and out_dtype != dt and out_dtype != torch.float32:
+        if out_dtype is None:
+            out_dtype = dt
+        elif out_dtype is not dt and out_dtype is not torch.float32:
             raise ValueError(f"out_dtype: unexpected dtype {out_dtype}")
+        y = torch.empty((T, N), dtype=out_dtype, device=dev)
+        ldy = N
     elif out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"y: expected {out_dtype}, got {y.dtype}")
     else:
@@ -694,16 +681,19 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
     if residual is not None:
         ldr = _ld(residual, "residual", (T, N), (y.dtype,), dev)
         rp = residual.data_ptr()
-    _launch("moe_linear", dev, x.data_ptr(), ldx, wp,
-            None if bias is None else _flat(bias, "bias", (N,), _F32, dev), rp, ldr, _16[dt],
-            _name(ACTS, act, "act"), T, K, N,
-            None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev), y.data_ptr(), ldy,
-            _DTYPES[y.dtype], None if status is None else _ptr(status))
+    rc = (_lib or lib()).moe_linear(
+        x.data_ptr(), ldx, W.data_ptr(),
+        None if bias is None else _flat(bias, "bias", (N,), _F32, dev), rp, ldr, _16[dt],
+        ACTS[act] if act in ACTS else _unknown(ACTS, act, "act"), T, K, N,
+        None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev), y.data_ptr(), ldy,
+        _DTYPES[y.dtype], None if status is None else _ptr(status), _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_linear", rc)
     return y
 
 
 def linear_grad_workspace_bytes(T: int, N: int) -> int:
-    return int(lib().moe_linear_grad_workspace_bytes(T, N))
+    return int((_lib or lib()).moe_linear_grad_workspace_bytes(T, N))
 
 
 def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), dw_dtype=None,
@@ -719,6 +709,9 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
     dt = x.dtype
     dev = x.device
     ldx = _ld(x, "x", (T, K), _16, dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return linear_grad(x, W, dy, pre, act, need, dw_dtype, dx, dW, db, ws, status)
     wp = _flat(W, "W", (N, K), (dt,), dev)
     lddy = _ld(dy, "dy", (T, N), (dt, torch.float32), dev)
     if dW is not None and dw_dtype is not None and dW.dtype != dw_dtype:
@@ -744,15 +737,21 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
         dbp = db.data_ptr()
     if ws is None:
         ws = torch.empty(linear_grad_workspace_bytes(T, N), dtype=torch.uint8, device=dev)
-    _launch("moe_linear_grad", dev, x.data_ptr(), ldx, wp,
-            None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev), dy.data_ptr(), lddy,
-            _DTYPES[dy.dtype], _16[dt], _name(ACTS, act, "act"), T, K, N, dxp, dWp, dw_code, dbp,
-            _ptr(ws), ws.numel(), None if status is None else _ptr(status))
+    else:
+        _ptr(ws)
+    rc = (_lib or lib()).moe_linear_grad(
+        x.data_ptr(), ldx, wp, None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev),
+        dy.data_ptr(), lddy, _DTYPES[dy.dtype], _16[dt],
+        ACTS[act] if act in ACTS else _unknown(ACTS, act, "act"), T, K, N, dxp, dWp, dw_code, dbp,
+        ws.data_ptr(), ws.numel(), None if status is None else _ptr(status),
+        _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_linear_grad", rc)
     return dx, dW, db
 
 
 def route_workspace_bytes(T: int, E: int) -> int:
-    return int(lib().moe_route_workspace_bytes(T, E))
+    return int((_lib or lib()).moe_route_workspace_bytes(T, E))
 
 
 def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bool = True,
@@ -769,6 +768,9 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
     T, E = logits.shape
     dev = logits.device
     ld = _ld(logits, "logits", (T, E), _DTYPES, dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return route(logits, k, bias, mask, score, norm, scale, stats, out, ws)
     if ws is None and stats:
         ws = torch.empty(route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
     cp = pp = sp = None
@@ -797,11 +799,15 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
             sp = output("loss", (2,), _F32)
     if ws is not None:
         o["ws"] = ws
-    _launch("moe_route", dev, logits.data_ptr(), ld, _DTYPES[logits.dtype],
-            None if bias is None else _flat(bias, "bias", (E,), _F32, dev),
-            None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, E, k,
-            _name(SCORES, score, "score"), norm, scale, ip, wp, cp, pp, sp,
-            None if ws is None else _ptr(ws), 0 if ws is None else ws.numel())
+    rc = (_lib or lib()).moe_route(
+        logits.data_ptr(), ld, _DTYPES[logits.dtype],
+        None if bias is None else _flat(bias, "bias", (E,), _F32, dev),
+        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, E, k,
+        SCORES[score] if score in SCORES else _unknown(SCORES, score, "score"), norm, scale, ip,
+        wp, cp, pp, sp, None if ws is None else _ptr(ws), 0 if ws is None else ws.numel(),
+        _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_route", rc)
     return o
 
 
@@ -816,18 +822,25 @@ def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: 
     dt = logits.dtype
     dev = logits.device
     ld = _ld(logits, "logits", (T, E), _DTYPES, dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return route_grad(logits, ids, counts, dw, dloss, mask, score, norm, scale, dlogits)
     ip = _flat(ids, "ids", (T, k), _I32, dev)
     if dlogits is None:
         dlogits = torch.empty((T, E), dtype=dt, device=dev)
         ldd = E
     else:
         ldd = _ld(dlogits, "dlogits", (T, E), (dt,), dev)
-    _launch("moe_route_grad", dev, logits.data_ptr(), ld, _DTYPES[dt],
-            None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), ip,
-            None if counts is None else _flat(counts, "counts", (E + 1,), _I32, dev),
-            None if dw is None else _flat(dw, "dw", (T, k), _F32, dev),
-            None if dloss is None else _flat(dloss, "dloss", (2,), _F32, dev), T, E, k,
-            _name(SCORES, score, "score"), norm, scale, dlogits.data_ptr(), ldd)
+    rc = (_lib or lib()).moe_route_grad(
+        logits.data_ptr(), ld, _DTYPES[dt],
+        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), ip,
+        None if counts is None else _flat(counts, "counts", (E + 1,), _I32, dev),
+        None if dw is None else _flat(dw, "dw", (T, k), _F32, dev),
+        None if dloss is None else _flat(dloss, "dloss", (2,), _F32, dev), T, E, k,
+        SCORES[score] if score in SCORES else _unknown(SCORES, score, "score"), norm, scale,
+        dlogits.data_ptr(), ldd, _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_route_grad", rc)
     return dlogits
 
 

@@ -1159,9 +1159,9 @@ struct Eight {
         if (vec && n == 8) {
             const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) +
                                                              at * (F32 ? 4 : 2));
-            q[0] = v[0];
+            q[0] = __ldcs(v);  // read once: leave the cache to dP
             if (F32)
-                q[F32 ? 1 : 0] = v[1];
+                q[F32 ? 1 : 0] = __ldcs(v + 1);
             return;
         }
         uint32_t w[F32 ? 8 : 4] = {};
