@@ -511,24 +511,21 @@ __global__ void __launch_bounds__(kLinThreads)
 // and half the rows of B.  A stage of 64 r costs each SM 32 KB of loads
 // (bn = 256) for 512 cycles of MMA; the same tile on one SM would load 48.
 // Pairs walk the tiles (persistent); two accumulators in tensor memory let
-// four epilogue warps work on one tile while the MMAs fill the other.  An
-// epilogue warp takes 32 rows x 32 columns at a time through shared
-// memory, so that global accesses are whole row pieces of 64 or 128 bytes;
-// the next 32 columns are read from tensor memory (about 330 cycles) ahead.
-// Eight epilogue warps, at 168 registers a thread instead of 255, measured
-// 172 us instead of 159 for 4096 x 2816 x 11264 with GELU and pre.
+// eight epilogue warps work on one tile while the MMAs fill the other.  An
+// epilogue warp takes 32 rows x 32 columns at a time: tensor memory (read
+// about 330 cycles ahead) -> registers -> one of its two slots of shared
+// memory -> one TMA store.  (Row pieces stored from registers by way of shared
+// memory took 1700 cycles for those 32 columns.)
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
 //
 // A launch takes one product or two (dx and dW): two short launches would
 // each leave SMs idle in their last round and pay the start twice.
-constexpr int kPairThreads = 192;  // producer, MMA, four epilogue warps
-constexpr int kPairEpiWarps = 4;
+constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairParts = kPairEpiWarps / 4;  // warps that share 32 rows
 constexpr int kPairSub = 2;     // 64-r halves of a stage
 constexpr int kPairStages = 3;
-// staging of one epilogue warp: output (and residual), pre, bias
-constexpr uint32_t kPairStgPre = 4096, kPairStgBias = kPairStgPre + 2048;
-constexpr uint32_t kPairStg = kPairStgBias + 128;
 constexpr int kPairMaxSplit = 4;     // a cluster of eight CTAs
 
 struct PairCtrl {
@@ -541,12 +538,13 @@ struct PairCtrl {
 };
 
 struct PairArgs {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[2], b[2], out[2], pre;
     LinArgs p[2];
     int tiles[2];       // 0 for an absent second product
     int bn;             // the larger of the two
     int cut;            // chains are cut (an fp32 output)
     uint32_t sub_bytes; // of shared memory for 64 r of both operands
+    uint32_t slot;      // bytes of one slot of an epilogue warp
     // Pair q of the grid's first takes tiles q, q + pairs, ... of product 0;
     // the `extra` pairs that get one more of them take at most `shared`
     // tiles of product 1, the others what is left.
@@ -564,25 +562,28 @@ __host__ __device__ __forceinline__ uint32_t pair_b_bytes(int bn, int b_mn)
     return uint32_t(b_mn ? (half + 63) / 64 * 64 : half) * (LK * 2);
 }
 
-// A warp's staging tile: 32 rows of 32 elements E, in 16-byte pieces; piece c
-// of row r sits where eight rows' same pieces fall into different banks.
+// A slot: 32 rows of 32 elements E, in 16-byte pieces laid out as the 64-byte
+// (16-bit) or 128-byte (fp32) swizzle of a TMA copy has them, which also puts
+// eight rows' same pieces into different banks.
 template <typename E>
-__device__ __forceinline__ uint4 *stg_at(uint8_t *stg, int r, int c)
+__device__ __forceinline__ uint4 *slot_at(uint8_t *slot, int r, int c)
 {
     constexpr int kPieces = 2 * int(sizeof(E));  // 4 (16-bit) or 8 of a row
     const int x = sizeof(E) == 4 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-    return reinterpret_cast<uint4 *>(stg) + r * kPieces + x;
+    return reinterpret_cast<uint4 *>(slot) + r * kPieces + x;
 }
 
+// Element by element, where 16-byte pieces are not aligned: rows [0, rows) x
+// columns [0, cols) of a matrix with ld elements between rows.
 template <bool STORE, typename E>
-__device__ __noinline__ void stg_move_by_element(uint8_t *stg, E *p, int64_t ld, int rows, int cols)
+__device__ __noinline__ void move_by_element(uint8_t *slot, E *p, int64_t ld, int rows, int cols)
 {
     constexpr int kPer = 16 / int(sizeof(E));
     const int lane = threadIdx.x & 31;
     if (lane < cols)
 #pragma unroll 16
         for (int r = 0; r < rows; ++r) {
-            E *at = reinterpret_cast<E *>(stg_at<E>(stg, r, lane / kPer)) + lane % kPer;
+            E *at = reinterpret_cast<E *>(slot_at<E>(slot, r, lane / kPer)) + lane % kPer;
             if (STORE)
                 p[int64_t(r) * ld + lane] = *at;
             else
@@ -590,37 +591,50 @@ __device__ __noinline__ void stg_move_by_element(uint8_t *stg, E *p, int64_t ld,
         }
 }
 
-// Moves the tile to (STORE) or from rows [0, rows) x columns [0, cols) of a
-// matrix with ld elements between rows.  vec: 16-byte pieces are aligned;
-// otherwise, or where columns end inside the tile, element by element.
-template <bool STORE, typename E>
-__device__ __forceinline__ void stg_move(uint8_t *stg, E *p, int64_t ld, int rows, int cols,
-                                         bool vec)
+// The residual's 32 rows x `cols` columns into a slot.
+template <typename E>
+__device__ __forceinline__ void load_slot(uint8_t *slot, const void *residual, int64_t at,
+                                          int64_t ld, int rows, int cols, bool vec)
 {
     constexpr int kPieces = 2 * int(sizeof(E)), kPer = 16 / int(sizeof(E));
     constexpr int kRows = 32 / kPieces;  // rows a warp moves at once
     const int lane = threadIdx.x & 31;
+    E *p = static_cast<E *>(const_cast<void *>(residual)) + at;
     if (vec && cols == 32) {
         const int r0 = lane / kPieces, c = lane % kPieces;
-        E *q = p + int64_t(r0) * ld + c * kPer;
+        const E *q = p + int64_t(r0) * ld + c * kPer;
         uint4 v[kPieces];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if (STORE)
-                v[i] = *stg_at<E>(stg, r0 + i * kRows, c);
-            else if (r0 + i * kRows < rows)
+        for (int i = 0; i < kPieces; ++i)
+            if (r0 + i * kRows < rows)
                 v[i] = *reinterpret_cast<const uint4 *>(q + int64_t(i * kRows) * ld);
-        }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if (!STORE)
-                *stg_at<E>(stg, r0 + i * kRows, c) = v[i];
-            else if (r0 + i * kRows < rows)
-                *reinterpret_cast<uint4 *>(q + int64_t(i * kRows) * ld) = v[i];
-        }
-        return;
+        for (int i = 0; i < kPieces; ++i)
+            *slot_at<E>(slot, r0 + i * kRows, c) = v[i];
+    } else {
+        move_by_element<false>(slot, p, ld, rows, cols);
     }
-    stg_move_by_element<STORE>(stg, p, ld, rows, cols);
+}
+
+// A written slot to the output: one TMA store (which leaves out what is past
+// the matrix), or element by element.
+template <typename E>
+__device__ __forceinline__ void store_slot(uint8_t *slot, const CUtensorMap *map, void *out,
+                                           int64_t m0, int n0, int64_t ld, int rows, int cols,
+                                           bool vec)
+{
+    if (vec) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            tma_store_2d(map, slot, n0, int(m0));
+            bulk_commit();
+        }
+    } else {
+        __syncwarp();
+        move_by_element<true>(slot, static_cast<E *>(out) + m0 * ld + n0, ld, rows, cols);
+        __syncwarp();
+    }
 }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int f16)
@@ -640,69 +654,88 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int f16)
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// The residual's 32 rows x `cols` columns into the staging tile.
-__device__ __forceinline__ void stage_residual(const LinArgs &p, uint8_t *stg, int64_t m0, int n0,
-                                               int rows, int cols)
-{
-    void *r = const_cast<void *>(p.residual);
-    if (p.out_f32)
-        stg_move<false>(stg, static_cast<float *>(r) + m0 * p.ldr + n0, p.ldr, rows, cols,
-                        p.vec_res);
-    else
-        stg_move<false>(stg, static_cast<uint16_t *>(r) + m0 * p.ldr + n0, p.ldr, rows, cols,
-                        p.vec_res);
-}
-
-__device__ __forceinline__ void stage16(uint8_t *stg, const float (&v)[32], int f16)
+__device__ __forceinline__ void fill16(uint8_t *slot, const float (&v)[32], int f16)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-        *stg_at<uint16_t>(stg, lane, c) = make_uint4(
+        *slot_at<uint16_t>(slot, lane, c) = make_uint4(
             pack16(v[8 * c], v[8 * c + 1], f16), pack16(v[8 * c + 2], v[8 * c + 3], f16),
             pack16(v[8 * c + 4], v[8 * c + 5], f16), pack16(v[8 * c + 6], v[8 * c + 7], f16));
 }
 
+// One warp's memory for the epilogue: two slots, used in turn, and 32 floats
+// of bias.
+struct EpiMemory {
+    uint8_t *slots;
+    uint32_t bytes;  // of a slot
+    float *bias;
+    uint32_t turn;
+    bool strict;  // the last store may have been from the next slot
+
+    // The next slot, once the store that last read it is done with it: only
+    // the last store may still be reading, its own slot being the other one.
+    __device__ __forceinline__ uint8_t *take()
+    {
+        if ((threadIdx.x & 31) == 0) {
+            if (strict)
+                bulk_wait_read<0>();
+            else
+                bulk_wait_read<1>();
+        }
+        __syncwarp();
+        uint8_t *s = slots + (turn & 1u) * bytes;
+        ++turn;
+        return s;
+    }
+};
+
 // The epilogue of 32 rows (lane = row) x 32 columns: bias, pre, activation,
 // residual, output.  `bias`: lane j holds column j's; every lane takes all of
-// them from shared memory.  The residual is there already.
-__device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float (&v)[32],
+// them from shared memory.  `slot`: of the output; it holds the residual.
+__device__ __forceinline__ void pair_chunk(const PairArgs &g, const LinArgs &p, int which,
+                                           EpiMemory &mem, uint8_t *slot, float (&v)[32],
                                            float bias, int64_t m0, int n0, int rows, int cols)
 {
     const int lane = threadIdx.x & 31;
     if (p.bias) {
-        float *b = reinterpret_cast<float *>(stg + kPairStgBias);
-        b[lane] = bias;
+        mem.bias[lane] = bias;
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(b + j);
+            const float4 q = *reinterpret_cast<const float4 *>(mem.bias + j);
             v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
         }
     }
-    if (p.pre)
-        stage16(stg + kPairStgPre, v, p.f16);
+    if (p.pre) {
+        uint8_t *s = mem.take();
+        fill16(s, v, p.f16);
+        store_slot<uint16_t>(s, &g.pre, p.pre, m0, n0, p.ldp, rows, cols, p.vec_pre);
+    }
     if (p.act != MOE_ACT_NONE)
         with_act(p.act, [&](auto act) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 v[j] = act_t<decltype(act)::value>(v[j]);
         });
+    if (!p.residual)
+        slot = mem.take();
     if (p.out_f32) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            float4 *at = reinterpret_cast<float4 *>(stg_at<float>(stg, lane, c));
+            float4 *at = reinterpret_cast<float4 *>(slot_at<float>(slot, lane, c));
             if (p.residual) {
                 const float4 q = *at;
                 v[4 * c] += q.x, v[4 * c + 1] += q.y, v[4 * c + 2] += q.z, v[4 * c + 3] += q.w;
             }
             *at = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         }
+        store_slot<float>(slot, &g.out[which], p.out, m0, n0, p.ldo, rows, cols, p.vec_out);
     } else {
         if (p.residual) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint4 q = *stg_at<uint16_t>(stg, lane, c);
+                const uint4 q = *slot_at<uint16_t>(slot, lane, c);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -712,28 +745,18 @@ __device__ __forceinline__ void pair_chunk(const LinArgs &p, uint8_t *stg, float
                 }
             }
         }
-        stage16(stg, v, p.f16);
+        fill16(slot, v, p.f16);
+        store_slot<uint16_t>(slot, &g.out[which], p.out, m0, n0, p.ldo, rows, cols, p.vec_out);
     }
-    __syncwarp();
-    if (p.pre)
-        stg_move<true>(stg + kPairStgPre, static_cast<uint16_t *>(p.pre) + m0 * p.ldp + n0, p.ldp,
-                       rows, cols, p.vec_pre);
-    if (p.out_f32)
-        stg_move<true>(stg, static_cast<float *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols,
-                       p.vec_out);
-    else
-        stg_move<true>(stg, static_cast<uint16_t *>(p.out) + m0 * p.ldo + n0, p.ldo, rows, cols,
-                       p.vec_out);
-    __syncwarp();
 }
 
-// Adds (or, first, copies) `width` columns of an accumulator to the sum of the
-// earlier chains; whole warp, its 32 lanes of tensor memory.  Not inlined: the
+// Adds (or, first, copies) columns c .. c + 31, c + 64 .. of an accumulator to
+// the sum of the earlier chains; whole warp, its 32 lanes of tensor memory.  Not inlined: the
 // epilogue's registers are its loop's.
-__device__ __noinline__ void add_chain(uint32_t acc, uint32_t sum, int width, bool add)
+__device__ __noinline__ void add_chain(uint32_t acc, uint32_t sum, int c, int width, bool add)
 {
 #pragma unroll 1
-    for (int c = 0; c < width; c += 32) {
+    for (; c < width; c += 32 * kPairParts) {
         uint32_t r[32], o[32];
         tmem_ld_32x32b_x32(acc + uint32_t(c), r);
         if (add)
@@ -975,8 +998,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         }
-        const int q = warp & 3;  // TMEM lane quadrant
-        uint8_t *mine = stg + (warp - 2) * kPairStg;
+        const int q = warp & 3, part = (warp - 2) >> 2;  // TMEM lane quadrant; even or odd 32 columns
+        EpiMemory mem{stg + uint32_t(warp - 2) * 2 * g.slot, g.slot,
+                      reinterpret_cast<float *>(stg + kPairEpiWarps * 2 * g.slot) + (warp - 2) * 32,
+                      0, true};
         int buf = 0;
         uint32_t aphase = 0;
         for (int i = 0; Z == 1 && tile_at(i, w); ++i) {
@@ -987,7 +1012,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             auto bias_of = [&](int c) {
                 return p.bias && c + int(lane) < width ? p.bias[n0 + c + int(lane)] : 0.0f;
             };
-            float bias = bias_of(0);
+            float bias = bias_of(part * 32);
             const uint32_t lanes = tmem_base + (uint32_t(q * 32) << 16);
             auto release = [&] {  // this accumulator has been read
                 tc_fence_before_sync();
@@ -1010,24 +1035,38 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     break;
                 tc_fence_after_sync();
                 const uint32_t t0 = lanes + uint32_t(buf * g.bn);
-                add_chain(t0, t1, width, sum);
+                add_chain(t0, t1, part * 32, width, sum);
                 release();
             }
             const uint32_t t0 = cut ? t1 : lanes + uint32_t(buf * g.bn);
             uint32_t r[32];
+            const bool some = rows > 0 && part * 32 < width;
+            // the slots of pre and output do not alternate as their stores do: a
+            // residual takes the output's first, or one of the two needs no store
+            const bool mixed = p.pre && (p.residual || p.vec_pre != p.vec_out);
 #pragma unroll 1
-            for (int c = 0; ok && (c == 0 || (rows > 0 && c < width)); c += 32) {
-                if (p.residual && rows > 0)
-                    stage_residual(p, mine, row, n0 + c, rows, min(32, width - c));
+            for (int c = part * 32; c < p.bn; c += 32 * kPairParts) {
+                uint8_t *slot = nullptr;
+                mem.strict = mixed || c == part * 32;  // (another product before, perhaps)
+                if (p.residual && some) {
+                    slot = mem.take();
+                    const int64_t at = row * p.ldr + n0 + c;
+                    if (p.out_f32)
+                        load_slot<float>(slot, p.residual, at, p.ldr, rows, min(32, width - c),
+                                         p.vec_res);
+                    else
+                        load_slot<uint16_t>(slot, p.residual, at, p.ldr, rows, min(32, width - c),
+                                            p.vec_res);
+                }
                 __syncwarp();
-                if (c == 0) {
+                if (c == part * 32) {
                     if (!cut)
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
-                    if (!ok || rows <= 0)
+                    if (!ok || !some)
                         break;
                     tc_fence_after_sync();
-                    tmem_ld_32x32b_x32(t0, r);
+                    tmem_ld_32x32b_x32(t0 + uint32_t(c), r);
                 }
                 float v[32];
                 tmem_ld_wait();
@@ -1035,17 +1074,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int j = 0; j < 32; ++j)
                     v[j] = __uint_as_float(r[j]);
                 const float now = bias;
-                if (c + 32 < width) {
-                    tmem_ld_32x32b_x32(t0 + uint32_t(c) + 32, r);
-                    bias = bias_of(c + 32);
+                const int next = c + 32 * kPairParts;
+                if (next < width) {
+                    tmem_ld_32x32b_x32(t0 + uint32_t(next), r);
+                    bias = bias_of(next);
                 }
-                pair_chunk(p, mine, v, now, row, n0 + c, rows, min(32, width - c));
+                pair_chunk(g, p, w.which, mem, slot, v, now, row, n0 + c, rows,
+                           min(32, width - c));
+                if (next >= width)
+                    break;
             }
             if (!ok)
                 break;
             if (!cut)
                 release();
         }
+        if (lane == 0)
+            bulk_wait<0>();  // every store written before the CTA (and its memory) goes
     }
     __syncwarp();
     if (Z > 1) {
@@ -1070,13 +1115,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (warp >= 2) {
             const bool ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[0], 0, abort_flag));
-            const int q = warp & 3, m = q * 32 + int(lane);
+            const int q = warp & 3, part = (warp - 2) >> 2, m = q * 32 + int(lane);
             tc_fence_after_sync();
             const uint32_t t0 = tmem_base + (uint32_t(q * 32) << 16);
             const uint32_t to =
                 dsmem_addr(acc + (z * slice + m % slice) * pitch, 2 * uint32_t(m / slice) + rank);
 #pragma unroll 1
-            for (int c = 0; c < bn; c += 64) {
+            for (int c = part * 64; c < bn; c += 64 * kPairParts) {
                 uint32_t r[2][32] = {};
                 if (ok) {
                     tmem_ld_32x32b_x32(t0 + uint32_t(c), r[0]);
@@ -1337,6 +1382,27 @@ cudaError_t lin_map(CUtensorMap *m, const Operand &o, int box_rows, int f16)
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Outputs [rows, cols], rows ld elements apart, written 32 x 32 from a slot.
+cudaError_t out_map(CUtensorMap *m, void *out, int64_t rows, int64_t cols, int64_t ld, int f32,
+                    int f16)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+    const CUresult r =
+        encode(m,
+               f32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+               : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_clustered(const void *kern, unsigned grid, unsigned cluster, unsigned threads,
                              size_t smem, cudaStream_t s, void **args)
 {
@@ -1490,8 +1556,14 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         cudaError_t e = lin_map(&g.a[i], q[i].X, q[i].x_mn ? LK : LM, a.f16);
         if (e == cudaSuccess)
             e = lin_map(&g.b[i], q[i].Y, q[i].y_mn ? LK : a.bn / 2, a.f16);
+        // outputs by TMA where their rows are aligned (a split tile's are not)
+        if (e == cudaSuccess && a.vec_out && a.split == 1)
+            e = out_map(&g.out[i], a.out, a.M, a.N, a.ldo, a.out_f32, a.f16);
+        if (e == cudaSuccess && a.pre && a.vec_pre && a.split == 1)
+            e = out_map(&g.pre, a.pre, a.M, a.N, a.ldp, 0, a.f16);
         if (e != cudaSuccess)
             return e;
+        g.slot = std::max(g.slot, a.out_f32 ? 4096u : 2048u);
     }
     const int split = t[0].split;
     int clusters = g.tiles[0];
@@ -1506,7 +1578,8 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
                          : (g.tiles[1] + clusters - 1) / clusters;
     }
     const size_t smem = 1024 + size_t(kPairStages) * kPairSub * g.sub_bytes +
-                        (split > 1 ? size_t(LM) * (g.bn + 4) * 4 : size_t(kPairEpiWarps) * kPairStg);
+                        (split > 1 ? size_t(LM) * (g.bn + 4) * 4
+                                   : size_t(kPairEpiWarps) * (2 * g.slot + 128));
     const void *kern = reinterpret_cast<const void *>(k_linear_pair);
     const cudaError_t e = ensure_smem_limit(kern, kSlotLinearPair, 226 * 1024);
     if (e != cudaSuccess)
