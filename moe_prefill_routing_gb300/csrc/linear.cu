@@ -60,6 +60,22 @@ struct LinArgs {
     int chain;       // steps of 64 r that one accumulator sums, see kChain
     int f16, out_f32, act;
     int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
+    uint32_t flags;  // the epilogue's choices in one word, see EpiFlags
+};
+
+// What the epilogue of k_linear_pair asks for again and again, in a register:
+// a field of one of two products is a constant load at a run-time offset, and
+// a chain of branches on five of them took about 400 cycles.
+enum EpiFlags : uint32_t {
+    kEpiBias = 1,
+    kEpiPre = 2,
+    kEpiResidual = 4,
+    kEpiF32 = 8,
+    kEpiF16 = 16,
+    kEpiVecOut = 32,
+    kEpiVecRes = 64,
+    kEpiVecPre = 128,
+    kEpiAct = 256,  // times the activation
 };
 
 struct LinCtrl {
@@ -693,12 +709,13 @@ struct EpiMemory {
 // The epilogue of 32 rows (lane = row) x 32 columns: bias, pre, activation,
 // residual, output.  `bias`: lane j holds column j's; every lane takes all of
 // them from shared memory.  `slot`: of the output; it holds the residual.
-__device__ __forceinline__ void pair_chunk(const PairArgs &g, const LinArgs &p, int which,
+__device__ __forceinline__ void pair_chunk(const PairArgs &g, int which, uint32_t flags,
                                            EpiMemory &mem, uint8_t *slot, float (&v)[32],
                                            float bias, int64_t m0, int n0, int rows, int cols)
 {
     const int lane = threadIdx.x & 31;
-    if (p.bias) {
+    const int f16 = flags & kEpiF16;
+    if (flags & kEpiBias) {
         mem.bias[lane] = bias;
         __syncwarp();
 #pragma unroll
@@ -707,46 +724,50 @@ __device__ __forceinline__ void pair_chunk(const PairArgs &g, const LinArgs &p, 
             v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
         }
     }
-    if (p.pre) {
+    if (flags & kEpiPre) {
         uint8_t *s = mem.take();
-        fill16(s, v, p.f16);
-        store_slot<uint16_t>(s, &g.pre, p.pre, m0, n0, p.ldp, rows, cols, p.vec_pre);
+        fill16(s, v, f16);
+        store_slot<uint16_t>(s, &g.pre, g.p[which].pre, m0, n0, g.p[which].ldp, rows, cols,
+                             flags & kEpiVecPre);
     }
-    if (p.act != MOE_ACT_NONE)
-        with_act(p.act, [&](auto act) {
+    if (flags >= kEpiAct)
+        with_act(int(flags / kEpiAct), [&](auto act) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 v[j] = act_t<decltype(act)::value>(v[j]);
         });
-    if (!p.residual)
+    const bool residual = flags & kEpiResidual;
+    if (!residual)
         slot = mem.take();
-    if (p.out_f32) {
+    if (flags & kEpiF32) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             float4 *at = reinterpret_cast<float4 *>(slot_at<float>(slot, lane, c));
-            if (p.residual) {
+            if (residual) {
                 const float4 q = *at;
                 v[4 * c] += q.x, v[4 * c + 1] += q.y, v[4 * c + 2] += q.z, v[4 * c + 3] += q.w;
             }
             *at = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         }
-        store_slot<float>(slot, &g.out[which], p.out, m0, n0, p.ldo, rows, cols, p.vec_out);
+        store_slot<float>(slot, &g.out[which], g.p[which].out, m0, n0, g.p[which].ldo, rows, cols,
+                          flags & kEpiVecOut);
     } else {
-        if (p.residual) {
+        if (residual) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint4 q = *slot_at<uint16_t>(slot, lane, c);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack16(w[i], p.f16);
+                    const float2 f = unpack16(w[i], f16);
                     v[8 * c + 2 * i] += f.x;
                     v[8 * c + 2 * i + 1] += f.y;
                 }
             }
         }
-        fill16(slot, v, p.f16);
-        store_slot<uint16_t>(slot, &g.out[which], p.out, m0, n0, p.ldo, rows, cols, p.vec_out);
+        fill16(slot, v, f16);
+        store_slot<uint16_t>(slot, &g.out[which], g.p[which].out, m0, n0, g.p[which].ldo, rows,
+                             cols, flags & kEpiVecOut);
     }
 }
 
@@ -936,6 +957,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint64_t da0 = smem_desc_sw128(sa, p.a_mn ? 8192 : 16, 1024);
             const uint64_t db0 = smem_desc_sw128(sb, p.b_mn ? 8192 : 16, 1024);
             const uint32_t ia = p.a_mn ? 128 : 2, ib = p.b_mn ? 128 : 2;
+            const int chain = p.chain;
             uint32_t d = 0;
             int left = 0;  // steps to go in this chain
             for (int kb = w.nk0; kb < w.nk1; kb += kPairSub) {
@@ -946,7 +968,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (!ok)
                         break;
                     d = tmem_base + uint32_t(buf * g.bn);
-                    left = p.chain;
+                    left = chain;
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
                 if (!ok)
@@ -1006,11 +1028,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t aphase = 0;
         for (int i = 0; Z == 1 && tile_at(i, w); ++i) {
             const LinArgs &p = g.p[w.which];
-            const int n0 = w.n0;
+            const uint32_t flags = p.flags;
+            const int n0 = w.n0, chain = p.chain;
             const int64_t row = int64_t(w.m0) + int(rank) * LM + q * 32;
             const int rows = int(min(int64_t(32), p.M - row)), width = min(p.bn, p.N - n0);
+            const float *bias_at = flags & kEpiBias ? p.bias + n0 + lane : nullptr;
             auto bias_of = [&](int c) {
-                return p.bias && c + int(lane) < width ? p.bias[n0 + c + int(lane)] : 0.0f;
+                return bias_at && c + int(lane) < width ? bias_at[c] : 0.0f;
             };
             float bias = bias_of(part * 32);
             const uint32_t lanes = tmem_base + (uint32_t(q * 32) << 16);
@@ -1018,7 +1042,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(dsmem_addr(&ctl.acc_empty[buf], lead));
+                    mbar_arrive_cluster_relaxed(dsmem_addr(&ctl.acc_empty[buf], lead));
                 if (++buf == 2) {
                     buf = 0;
                     aphase ^= 1u;
@@ -1026,7 +1050,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             };
             bool ok = true;
             // a sum cut into chains is put together in tensor memory
-            int chains = (w.nk1 - w.nk0 + p.chain - 1) / p.chain;
+            int chains = (w.nk1 - w.nk0 + chain - 1) / chain;
             const bool cut = chains > 1;
             const uint32_t t1 = lanes + uint32_t(2 * g.bn);
             for (bool sum = false; cut && chains > 0; --chains, sum = true) {
@@ -1043,20 +1067,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const bool some = rows > 0 && part * 32 < width;
             // the slots of pre and output do not alternate as their stores do: a
             // residual takes the output's first, or one of the two needs no store
-            const bool mixed = p.pre && (p.residual || p.vec_pre != p.vec_out);
+            const bool mixed = (flags & kEpiPre) && ((flags & kEpiResidual) ||
+                                                     !(flags & kEpiVecPre) != !(flags & kEpiVecOut));
 #pragma unroll 1
-            for (int c = part * 32; c < p.bn; c += 32 * kPairParts) {
+            for (int c = part * 32; c == part * 32 || c < width; c += 32 * kPairParts) {
                 uint8_t *slot = nullptr;
                 mem.strict = mixed || c == part * 32;  // (another product before, perhaps)
-                if (p.residual && some) {
+                if ((flags & kEpiResidual) && some) {
                     slot = mem.take();
                     const int64_t at = row * p.ldr + n0 + c;
-                    if (p.out_f32)
+                    if (flags & kEpiF32)
                         load_slot<float>(slot, p.residual, at, p.ldr, rows, min(32, width - c),
-                                         p.vec_res);
+                                         flags & kEpiVecRes);
                     else
                         load_slot<uint16_t>(slot, p.residual, at, p.ldr, rows, min(32, width - c),
-                                            p.vec_res);
+                                            flags & kEpiVecRes);
                 }
                 __syncwarp();
                 if (c == part * 32) {
@@ -1079,10 +1104,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     tmem_ld_32x32b_x32(t0 + uint32_t(next), r);
                     bias = bias_of(next);
                 }
-                pair_chunk(g, p, w.which, mem, slot, v, now, row, n0 + c, rows,
+                pair_chunk(g, w.which, flags, mem, slot, v, now, row, n0 + c, rows,
                            min(32, width - c));
-                if (next >= width)
-                    break;
             }
             if (!ok)
                 break;
@@ -1547,6 +1570,11 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         a.a_mn = q[i].x_mn, a.b_mn = q[i].y_mn;
         a.bn = t[i].bn, a.split = t[i].split;
         a.n_mt = int((int64_t(a.M) + 2 * LM - 1) / (2 * LM));
+        a.flags = (a.bias ? kEpiBias : 0) | (a.pre ? kEpiPre : 0) |
+                  (a.residual ? kEpiResidual : 0) | (a.out_f32 ? kEpiF32 : 0) |
+                  (a.f16 ? kEpiF16 : 0) | (a.vec_out ? kEpiVecOut : 0) |
+                  (a.vec_res ? kEpiVecRes : 0) | (a.vec_pre ? kEpiVecPre : 0) |
+                  uint32_t(a.act) * kEpiAct;
         const int nk = (a.R + LK - 1) / LK;
         a.chain = a.out_f32 ? kChain : std::max(nk, 1);
         g.cut |= a.split == 1 && nk > a.chain;
