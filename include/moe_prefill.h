@@ -538,7 +538,7 @@ MOE_API int moe_selftest_wait_limit(const void *xs, const void *Wg, const void *
  * in   status    uint32* device word to OR MOE_STATUS_TIMEOUT into, or NULL
  * dtype is MOE_DT_BF16 or MOE_DT_F16, y_dtype that same type or MOE_DT_F32.
  * T >= 0, N >= 1 (any), K a positive multiple of 8; ldx >= K a multiple of 8;
- * ldr, ldy >= N; T, K, N < 2^31.  x and W 16-byte aligned, the others aligned
+ * ldr, ldy >= N; T, K, N <= 2^31 - 512.  x and W 16-byte aligned, the others aligned
  * to their element.  residual may be y itself (same ldr and ldy): each element
  * is read before it is written, by the same thread.  No other operands may
  * overlap.  A fixed order of every sum: results are deterministic.

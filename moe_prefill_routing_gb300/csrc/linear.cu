@@ -15,9 +15,9 @@
 // tiles on pairs of CTAs, rows as M.
 //
 // Either way a tile's reduction can be split over the CTAs of a thread-block
-// cluster when there are fewer tiles than SMs; each leaves its fp32
-// accumulator in its own shared memory and the cluster adds them in rank
-// order through distributed shared memory (results are deterministic).
+// cluster when there are fewer tiles than SMs: each CTA finishes a share of
+// the tile, to which the others send their fp32 sums through distributed
+// shared memory, and adds them in rank order (results are deterministic).
 #include "../../include/moe_prefill.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -182,7 +182,8 @@ __device__ __forceinline__ float act_grad(float z)
         return c.x + 0.3989422804014327f * z * c.y;
     } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
         const float s = sigmoid_ftz(gelu_2u(z));
-        const float du2 = 1.5957691216057308f + 3.0f * 0.07135481627260025f * z * z;
+        // (z^2 cut where s is 0 or 1 long since, lest 0 times infinity come out)
+        const float du2 = 1.5957691216057308f + 3.0f * 0.07135481627260025f * fminf(z * z, 1e8f);
         return s + z * s * (1.0f - s) * du2;
     } else {
         return 1.0f;
@@ -788,9 +789,9 @@ __device__ __noinline__ void add_chain(uint32_t acc, uint32_t sum, int c, int wi
             for (int j = 0; j < 32; ++j)
                 r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
         }
-        tmem_st_32x32b_x32(sum + uint32_t(c), r);
+        tmem_store_32x32b_x32(sum + uint32_t(c), r);
     }
-    tmem_st_wait();
+    tmem_store_wait();
 }
 
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -1010,8 +1011,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else if (warp >= 2) {
         if (g.db) {  // while the first tile is on its way
             const int threads = 32 * kPairEpiWarps;
-            for (int c = int(blockIdx.x) * threads + int(threadIdx.x) - 64; c < g.db_n;
-                 c += int(gridDim.x) * threads) {
+            for (int64_t c = int64_t(blockIdx.x) * threads + int(threadIdx.x) - 64; c < g.db_n;
+                 c += int64_t(gridDim.x) * threads) {
                 float v = 0.0f;
 #pragma unroll 8
                 for (int i = 0; i < g.chunks; ++i)
@@ -1666,6 +1667,14 @@ inline int vec16(const void *p, int64_t ld, int size)
     return ld * size % 16 == 0 && aligned(p, 16);
 }
 
+// (sizes rounded up to whole tiles stay below 2^31)
+inline bool sizes_ok(int T, int K, int N, int act)
+{
+    constexpr int kMost = INT_MAX - 511;
+    return T >= 0 && T <= kMost && K >= 1 && K <= kMost && K % 8 == 0 && N >= 1 && N <= kMost &&
+           act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH;
+}
+
 inline bool is16(int dtype)
 {
     return dtype == MOE_DT_BF16 || dtype == MOE_DT_F16;
@@ -1682,8 +1691,7 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
     using namespace moe;
     if (!is16(dtype) || (y_dtype != dtype && y_dtype != MOE_DT_F32))
         return MOE_ERR_DTYPE;
-    if (T < 0 || K < 1 || K % 8 != 0 || N < 1 || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH ||
-        ldx < K || ldx % 8 != 0 || ldy < N || (residual && ldr < N))
+    if (!sizes_ok(T, K, N, act) || ldx < K || ldx % 8 != 0 || ldy < N || (residual && ldr < N))
         return MOE_ERR_SHAPE;
     if (!W || (T > 0 && (!x || !y)))
         return MOE_ERR_NULL;
@@ -1711,7 +1719,7 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
 
 extern "C" size_t moe_linear_grad_workspace_bytes(int T, int N)
 {
-    if (T < 0 || N < 1)
+    if (!moe::sizes_ok(T, 8, N, MOE_ACT_NONE))
         return 0;
     const size_t ldp = (size_t(N) + 7) & ~size_t(7);
     return moe::align256(size_t(T) * ldp * 2) +
@@ -1727,8 +1735,7 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     if (!is16(dtype) || (dy_dtype != dtype && dy_dtype != MOE_DT_F32) ||
         (dw_dtype != dtype && dw_dtype != MOE_DT_F32))
         return MOE_ERR_DTYPE;
-    if (T < 0 || K < 1 || K % 8 != 0 || N < 1 || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH ||
-        lddy < N || (dW && (ldx < K || ldx % 8 != 0)))
+    if (!sizes_ok(T, K, N, act) || lddy < N || (dW && (ldx < K || ldx % 8 != 0)))
         return MOE_ERR_SHAPE;
     if (!ws || (dx && !W) ||
         (T > 0 && (!dy || (dW && !x) || (act != MOE_ACT_NONE && !pre))))

@@ -416,16 +416,6 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
                  : "memory");
 }
 
-// 32 lanes x 8 consecutive 32-bit columns, as below.
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-
 // 32 lanes x 32 consecutive 32-bit columns, as below.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -463,7 +453,7 @@ __device__ __forceinline__ void tmem_ld_wait()
 }
 
 // The other way: lane (quadrant base + i), columns [col, col+32).
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32])
+__device__ __forceinline__ void tmem_store_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -477,7 +467,7 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_wait()
+__device__ __forceinline__ void tmem_store_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }

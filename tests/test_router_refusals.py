@@ -30,7 +30,8 @@ LIN_OK = dict(x=FAKE, ldx=64, W=FAKE, bias=None, residual=None, ldr=0, dtype=0, 
     (dict(dtype=2), "DTYPE"), (dict(dtype=7), "DTYPE"), (dict(y_dtype=1), "DTYPE"),
     (dict(T=-1), "SHAPE"), (dict(K=0), "SHAPE"), (dict(K=60), "SHAPE"), (dict(N=0), "SHAPE"),
     (dict(act=5), "SHAPE"), (dict(act=-1), "SHAPE"), (dict(ldx=56), "SHAPE"),
-    (dict(ldx=68), "SHAPE"), (dict(ldy=9), "SHAPE"), (dict(residual=FAKE, ldr=9), "SHAPE"),
+    (dict(ldx=68), "SHAPE"), (dict(T=(1 << 31) - 511), "SHAPE"),
+    (dict(N=(1 << 31) - 1, ldy=1 << 31), "SHAPE"), (dict(ldy=9), "SHAPE"), (dict(residual=FAKE, ldr=9), "SHAPE"),
     (dict(x=None), "NULL"), (dict(W=None), "NULL"), (dict(y=None), "NULL"),
     (dict(x=FAKE + 8), "ALIGN"), (dict(W=FAKE + 2), "ALIGN"), (dict(y=FAKE + 1), "ALIGN"),
     (dict(y=FAKE + 2, y_dtype=2), "ALIGN"), (dict(bias=FAKE + 2), "ALIGN"),
