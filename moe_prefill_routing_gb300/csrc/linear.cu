@@ -110,24 +110,38 @@ __device__ __forceinline__ void dsmem_st4(uint32_t a, uint32_t x, uint32_t y, ui
                  : "memory");
 }
 
-// (Phi(z), e^(-z^2/2)), Phi the normal distribution function, from
+// Phi(z) and e^(-z^2/2), Phi the normal distribution function, from
 // erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), x >= 0: formula
 // 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions, off
 // by 1.5e-7 at most (Phi by half of that).  The library's erfc is more exact
 // than any output here needs and takes registers that the epilogue lacks.
-__device__ __forceinline__ float2 normal_cdf(float z)
+__device__ __forceinline__ float cdf_t(float z)  // 1 / t
 {
-    const float x = fabsf(z) * 0.7071067811865476f;
-    float t, e;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(1.0f + 0.3275911f * x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * -0.7213475204444817f));
+    return 1.0f + 0.3275911f * 0.7071067811865476f * fabsf(z);
+}
+
+__device__ __forceinline__ float cdf_e(float z)  // log2 of e^(-z^2/2)
+{
+    return z * z * -0.7213475204444817f;
+}
+
+__device__ __forceinline__ float cdf(float z, float t, float e)
+{
     float q = 1.061405429f;
     q = q * t - 1.453152027f;
     q = q * t + 1.421413741f;
     q = q * t - 0.284496736f;
     q = q * t + 0.254829592f;
     q = 0.5f * q * t * e;
-    return make_float2(z > 0.0f ? 1.0f - q : q, e);
+    return z > 0.0f ? 1.0f - q : q;
+}
+
+__device__ __forceinline__ float2 normal_cdf(float z)
+{
+    float t, e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(cdf_t(z)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(cdf_e(z)));
+    return make_float2(cdf(z, t, e), e);
 }
 
 // sqrt(2/pi) (z + 0.044715 z^3) times two; (1 + tanh u) / 2 is 1 / (1 + e^-2u)
@@ -149,6 +163,60 @@ __device__ __forceinline__ float act_t(float z)
         return z * sigmoid_ftz(gelu_2u(z));
     else
         return z;
+}
+
+template <int R>
+__device__ __forceinline__ void ex2_all(float (&x)[R])
+{
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x[i]));
+}
+
+template <int R>
+__device__ __forceinline__ void rcp_all(float (&x)[R])
+{
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+f"(x[i]));
+}
+
+// act_t of R values, each step for all of them in turn (volatile keeps that
+// order): left to the compiler, one value's chain followed another's and 32
+// values of a lane took 2300 cycles (GELU-tanh).
+template <int ACT, int R>
+__device__ __forceinline__ void act_all(float (&z)[R])
+{
+    if constexpr (ACT == MOE_ACT_SILU || ACT == MOE_ACT_GELU_TANH) {
+        float s[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            s[i] = (ACT == MOE_ACT_SILU ? z[i] : gelu_2u(z[i])) * -1.4426950408889634f;
+        ex2_all(s);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            s[i] += 1.0f;
+        rcp_all(s);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            z[i] *= s[i];
+    } else if constexpr (ACT == MOE_ACT_GELU) {
+        float t[R], e[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            t[i] = cdf_t(z[i]);
+            e[i] = cdf_e(z[i]);
+        }
+        rcp_all(t);
+        ex2_all(e);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            z[i] *= cdf(z[i], t[i], e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            z[i] = act_t<ACT>(z[i]);
+    }
 }
 
 // f(integral_constant<int, act>)
@@ -531,8 +599,15 @@ __global__ void __launch_bounds__(kLinThreads)
 // eight epilogue warps work on one tile while the MMAs fill the other.  An
 // epilogue warp takes 32 rows x 32 columns at a time: tensor memory (read
 // about 330 cycles ahead) -> registers -> one of its two slots of shared
-// memory -> one TMA store.  (Row pieces stored from registers by way of shared
-// memory took 1700 cycles for those 32 columns.)
+// memory -> one TMA store.  (Row pieces read back from shared memory and
+// stored by the warp took 1700 cycles for those 32 columns; each lane storing
+// its row from registers, 32 bytes at a time, takes 203 us where this takes
+// 168 below: 32 lines an instruction.)
+//
+// Bound by the tensor cores: 4096 x 2816 x 11264 with bias, GELU and pre
+// takes 157 - 170 us (1.53 - 1.65 PFLOP/s, on six GPUs), its MMAs alone 133;
+// the rest is what 184 MB of outputs take from the loads' shared memory and
+// L2 bandwidth, and the last of ten rounds of tiles, a quarter full.
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
 //
@@ -734,8 +809,16 @@ __device__ __forceinline__ void pair_chunk(const PairArgs &g, int which, uint32_
     if (flags >= kEpiAct)
         with_act(int(flags / kEpiAct), [&](auto act) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = act_t<decltype(act)::value>(v[j]);
+            for (int j = 0; j < 32; j += 8) {
+                float z[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    z[i] = v[j + i];
+                act_all<decltype(act)::value>(z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[j + i] = z[i];
+            }
         });
     const bool residual = flags & kEpiResidual;
     if (!residual)
