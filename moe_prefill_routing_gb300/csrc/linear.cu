@@ -91,13 +91,13 @@ __host__ __device__ __forceinline__ uint32_t lin_b_tile(int bn, int b_mn)
     return uint32_t(b_mn && bn < 64 ? 64 : bn) * LK * 2;
 }
 
-// 1 / (1 + e^-x): exponential and reciprocal by one special-function
-// instruction each (2 units in the last place, and the rounding of
-// x log2(e)); e^-x past 2^126 gives 0, where the true value is below 2^-126.
-__device__ __forceinline__ float sigmoid_ftz(float x)
+// 1 / (1 + 2^x): exponential and reciprocal by one special-function
+// instruction each (2 units in the last place); 2^x past 2^126 gives 0, where
+// the true value is below 2^-126.
+__device__ __forceinline__ float sigmoid_2(float x)
 {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
@@ -144,10 +144,19 @@ __device__ __forceinline__ float2 normal_cdf(float z)
     return make_float2(cdf(z, t, e), e);
 }
 
-// sqrt(2/pi) (z + 0.044715 z^3) times two; (1 + tanh u) / 2 is 1 / (1 + e^-2u)
-__device__ __forceinline__ float gelu_2u(float z)
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kTanh1 = 1.5957691216057308f;    // 2 sqrt(2/pi)
+constexpr float kTanh3 = 0.07135481627260025f;   // 2 sqrt(2/pi) 0.044715
+
+// Of SiLU and GELU-tanh, act(z) = z / (1 + 2^x): x.  (1 + tanh u) / 2 is
+// 1 / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3).
+template <int ACT>
+__device__ __forceinline__ float gate_x(float z)
 {
-    return z * (1.5957691216057308f + 0.07135481627260025f * z * z);
+    if constexpr (ACT == MOE_ACT_SILU)
+        return z * -kLog2E;
+    else
+        return z * (-kLog2E * kTanh1 - kLog2E * kTanh3 * (z * z));
 }
 
 template <int ACT>
@@ -155,12 +164,10 @@ __device__ __forceinline__ float act_t(float z)
 {
     if constexpr (ACT == MOE_ACT_RELU)
         return z < 0.0f ? 0.0f : z;  // a NaN stays one
-    else if constexpr (ACT == MOE_ACT_SILU)
-        return z * sigmoid_ftz(z);
+    else if constexpr (ACT == MOE_ACT_SILU || ACT == MOE_ACT_GELU_TANH)
+        return z * sigmoid_2(gate_x<ACT>(z));
     else if constexpr (ACT == MOE_ACT_GELU)
         return z * normal_cdf(z).x;
-    else if constexpr (ACT == MOE_ACT_GELU_TANH)
-        return z * sigmoid_ftz(gelu_2u(z));
     else
         return z;
 }
@@ -191,7 +198,7 @@ __device__ __forceinline__ void act_all(float (&z)[R])
         float s[R];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            s[i] = (ACT == MOE_ACT_SILU ? z[i] : gelu_2u(z[i])) * -1.4426950408889634f;
+            s[i] = gate_x<ACT>(z[i]);
         ex2_all(s);
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -243,15 +250,15 @@ __device__ __forceinline__ float act_grad(float z)
     if constexpr (ACT == MOE_ACT_RELU) {
         return z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (ACT == MOE_ACT_SILU) {
-        const float s = sigmoid_ftz(z);
+        const float s = sigmoid_2(gate_x<ACT>(z));
         return s * (1.0f + z * (1.0f - s));
     } else if constexpr (ACT == MOE_ACT_GELU) {
         const float2 c = normal_cdf(z);
         return c.x + 0.3989422804014327f * z * c.y;
     } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
-        const float s = sigmoid_ftz(gelu_2u(z));
+        const float s = sigmoid_2(gate_x<ACT>(z));
         // (z^2 cut where s is 0 or 1 long since, lest 0 times infinity come out)
-        const float du2 = 1.5957691216057308f + 3.0f * 0.07135481627260025f * fminf(z * z, 1e8f);
+        const float du2 = kTanh1 + 3.0f * kTanh3 * fminf(z * z, 1e8f);
         return s + z * s * (1.0f - s) * du2;
     } else {
         return 1.0f;
@@ -616,6 +623,7 @@ __global__ void __launch_bounds__(kLinThreads)
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairParts = kPairEpiWarps / 4;  // warps that share 32 rows
+constexpr int kCols = 16;       // columns that an epilogue warp works on at once
 constexpr int kPairSub = 2;     // 64-r halves of a stage
 constexpr int kPairStages = 3;
 constexpr int kPairMaxSplit = 4;     // a cluster of eight CTAs
@@ -746,16 +754,6 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int f16)
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-__device__ __forceinline__ void fill16(uint8_t *slot, const float (&v)[32], int f16)
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        *slot_at<uint16_t>(slot, lane, c) = make_uint4(
-            pack16(v[8 * c], v[8 * c + 1], f16), pack16(v[8 * c + 2], v[8 * c + 3], f16),
-            pack16(v[8 * c + 4], v[8 * c + 5], f16), pack16(v[8 * c + 6], v[8 * c + 7], f16));
-}
-
 // One warp's memory for the epilogue: two slots, used in turn, and 32 floats
 // of bias.
 struct EpiMemory {
@@ -782,76 +780,61 @@ struct EpiMemory {
     }
 };
 
-// The epilogue of 32 rows (lane = row) x 32 columns: bias, pre, activation,
-// residual, output.  `bias`: lane j holds column j's; every lane takes all of
-// them from shared memory.  `slot`: of the output; it holds the residual.
-__device__ __forceinline__ void pair_chunk(const PairArgs &g, int which, uint32_t flags,
-                                           EpiMemory &mem, uint8_t *slot, float (&v)[32],
-                                           float bias, int64_t m0, int n0, int rows, int cols)
+// A row's kCols 16-bit values, from column h of a slot on.
+__device__ __forceinline__ void put16(uint8_t *slot, int h, const float (&v)[kCols], int f16)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i)
+        *slot_at<uint16_t>(slot, lane, h / 8 + i) = make_uint4(
+            pack16(v[8 * i], v[8 * i + 1], f16), pack16(v[8 * i + 2], v[8 * i + 3], f16),
+            pack16(v[8 * i + 4], v[8 * i + 5], f16), pack16(v[8 * i + 6], v[8 * i + 7], f16));
+}
+
+// The epilogue of 32 rows (lane = row) x kCols columns, from column h of the
+// slots on: bias (`bias`: theirs), pre, activation, residual (in `slot`),
+// output.
+__device__ __forceinline__ void pair_cols(uint32_t flags, const float *bias, uint8_t *pre,
+                                          uint8_t *slot, int h, float (&v)[kCols])
 {
     const int lane = threadIdx.x & 31;
     const int f16 = flags & kEpiF16;
     if (flags & kEpiBias) {
-        mem.bias[lane] = bias;
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(mem.bias + j);
+        for (int j = 0; j < kCols; j += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(bias + j);
             v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
         }
     }
-    if (flags & kEpiPre) {
-        uint8_t *s = mem.take();
-        fill16(s, v, f16);
-        store_slot<uint16_t>(s, &g.pre, g.p[which].pre, m0, n0, g.p[which].ldp, rows, cols,
-                             flags & kEpiVecPre);
-    }
+    if (flags & kEpiPre)
+        put16(pre, h, v, f16);
     if (flags >= kEpiAct)
-        with_act(int(flags / kEpiAct), [&](auto act) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                float z[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    z[i] = v[j + i];
-                act_all<decltype(act)::value>(z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[j + i] = z[i];
-            }
-        });
-    const bool residual = flags & kEpiResidual;
-    if (!residual)
-        slot = mem.take();
+        with_act(int(flags / kEpiAct), [&](auto act) { act_all<decltype(act)::value>(v); });
     if (flags & kEpiF32) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            float4 *at = reinterpret_cast<float4 *>(slot_at<float>(slot, lane, c));
-            if (residual) {
+        for (int i = 0; i < kCols; i += 4) {
+            float4 *at = reinterpret_cast<float4 *>(slot_at<float>(slot, lane, (h + i) / 4));
+            if (flags & kEpiResidual) {
                 const float4 q = *at;
-                v[4 * c] += q.x, v[4 * c + 1] += q.y, v[4 * c + 2] += q.z, v[4 * c + 3] += q.w;
+                v[i] += q.x, v[i + 1] += q.y, v[i + 2] += q.z, v[i + 3] += q.w;
             }
-            *at = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            *at = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
-        store_slot<float>(slot, &g.out[which], g.p[which].out, m0, n0, g.p[which].ldo, rows, cols,
-                          flags & kEpiVecOut);
     } else {
-        if (residual) {
+        if (flags & kEpiResidual) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 q = *slot_at<uint16_t>(slot, lane, c);
+            for (int i = 0; i < kCols; i += 8) {
+                const uint4 q = *slot_at<uint16_t>(slot, lane, (h + i) / 8);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack16(w[i], f16);
-                    v[8 * c + 2 * i] += f.x;
-                    v[8 * c + 2 * i + 1] += f.y;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack16(w[j], f16);
+                    v[i + 2 * j] += f.x;
+                    v[i + 2 * j + 1] += f.y;
                 }
             }
         }
-        fill16(slot, v, f16);
-        store_slot<uint16_t>(slot, &g.out[which], g.p[which].out, m0, n0, g.p[which].ldo, rows,
-                             cols, flags & kEpiVecOut);
+        put16(slot, h, v, f16);
     }
 }
 
@@ -1147,26 +1130,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 release();
             }
             const uint32_t t0 = cut ? t1 : lanes + uint32_t(buf * g.bn);
-            uint32_t r[32];
+            uint32_t r[kCols];
             const bool some = rows > 0 && part * 32 < width;
-            // the slots of pre and output do not alternate as their stores do: a
-            // residual takes the output's first, or one of the two needs no store
-            const bool mixed = (flags & kEpiPre) && ((flags & kEpiResidual) ||
-                                                     !(flags & kEpiVecPre) != !(flags & kEpiVecOut));
 #pragma unroll 1
             for (int c = part * 32; c == part * 32 || c < width; c += 32 * kPairParts) {
-                uint8_t *slot = nullptr;
-                mem.strict = mixed || c == part * 32;  // (another product before, perhaps)
+                const int cols = min(32, width - c);
+                // (before a tile's first, another product's stores, perhaps)
+                mem.strict = (flags & kEpiPre) || c == part * 32;
+                uint8_t *slot = mem.take(), *pre = slot;
+                if (flags & kEpiPre)
+                    pre = mem.take();
                 if ((flags & kEpiResidual) && some) {
-                    slot = mem.take();
                     const int64_t at = row * p.ldr + n0 + c;
                     if (flags & kEpiF32)
-                        load_slot<float>(slot, p.residual, at, p.ldr, rows, min(32, width - c),
+                        load_slot<float>(slot, p.residual, at, p.ldr, rows, cols,
                                          flags & kEpiVecRes);
                     else
-                        load_slot<uint16_t>(slot, p.residual, at, p.ldr, rows, min(32, width - c),
+                        load_slot<uint16_t>(slot, p.residual, at, p.ldr, rows, cols,
                                             flags & kEpiVecRes);
                 }
+                if (flags & kEpiBias)
+                    mem.bias[lane] = bias;
                 __syncwarp();
                 if (c == part * 32) {
                     if (!cut)
@@ -1175,21 +1159,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (!ok || !some)
                         break;
                     tc_fence_after_sync();
-                    tmem_ld_32x32b_x32(t0 + uint32_t(c), r);
+                    tmem_ld_32x32b_x16(t0 + uint32_t(c), r);
                 }
-                float v[32];
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    v[j] = __uint_as_float(r[j]);
-                const float now = bias;
                 const int next = c + 32 * kPairParts;
-                if (next < width) {
-                    tmem_ld_32x32b_x32(t0 + uint32_t(next), r);
+                if (next < width)
                     bias = bias_of(next);
+#pragma unroll 1
+                for (int h = 0; h < 32; h += kCols) {
+                    float v[kCols];
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        v[j] = __uint_as_float(r[j]);
+                    const int ahead = h + kCols < 32 ? c + h + kCols : next;
+                    if (ahead < width)
+                        tmem_ld_32x32b_x16(t0 + uint32_t(ahead), r);
+                    pair_cols(flags, mem.bias + h, pre, slot, h, v);
                 }
-                pair_chunk(g, w.which, flags, mem, slot, v, now, row, n0 + c, rows,
-                           min(32, width - c));
+                if (flags & kEpiPre)
+                    store_slot<uint16_t>(pre, &g.pre, p.pre, row, n0 + c, p.ldp, rows, cols,
+                                         flags & kEpiVecPre);
+                if (flags & kEpiF32)
+                    store_slot<float>(slot, &g.out[w.which], p.out, row, n0 + c, p.ldo, rows, cols,
+                                      flags & kEpiVecOut);
+                else
+                    store_slot<uint16_t>(slot, &g.out[w.which], p.out, row, n0 + c, p.ldo, rows,
+                                         cols, flags & kEpiVecOut);
             }
             if (!ok)
                 break;
@@ -1297,7 +1292,6 @@ struct GradArgs {
     float *part;      // [chunks][N] or null
     int64_t lddy, lddp;
     int T, N, rows;   // rows per chunk
-    int f16, act;
     int vec;          // 16-byte accesses of dy and pre are aligned
 };
 
@@ -1357,7 +1351,7 @@ struct Eight {
 // flight; the warps' sums are added in order.  Bound by memory: dy and pre
 // are read and dP written once.  Four CTAs an SM with two rows in flight
 // each measured 51 us on 4096 x 11264 (5.4 TB/s), two CTAs with four rows 58.
-template <int ACT, bool F32>
+template <int ACT, bool F32, bool F16>
 __global__ void __launch_bounds__(kGradThreads, 4) k_act_grad(GradArgs p)
 {
     __shared__ float red[kGradGroups][kGradCols];
@@ -1388,21 +1382,21 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_act_grad(GradArgs p)
                 if (r >= t1)
                     break;
                 float d[8];
-                dy[u].to(d, p.f16);
+                dy[u].to(d, F16);
                 if (ACT != MOE_ACT_NONE) {
                     float z[8];
-                    pre[u].to(z, p.f16);
+                    pre[u].to(z, F16);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         d[i] *= act_grad<ACT>(z[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    s[i] += i < left ? d[i] : 0.0f;
+                    s[i] += d[i];  // 0 past N
                 if (p.dp) {  // lddp is a multiple of 8: whole vectors, past N too
                     *reinterpret_cast<uint4 *>(p.dp + r * p.lddp + c) =
-                        make_uint4(pack16(d[0], d[1], p.f16), pack16(d[2], d[3], p.f16),
-                                   pack16(d[4], d[5], p.f16), pack16(d[6], d[7], p.f16));
+                        make_uint4(pack16(d[0], d[1], F16), pack16(d[2], d[3], F16),
+                                   pack16(d[4], d[5], F16), pack16(d[6], d[7], F16));
                 }
             }
         }
@@ -1448,19 +1442,29 @@ __global__ void __launch_bounds__(kGradThreads)
     }
 }
 
-void (*act_grad_kernel(int act, bool f32))(GradArgs)
+using GradKernel = void (*)(GradArgs);
+
+template <int ACT>
+GradKernel act_grad_kernel(bool f32, bool f16)
+{
+    if (f32)
+        return f16 ? k_act_grad<ACT, true, true> : k_act_grad<ACT, true, false>;
+    return f16 ? k_act_grad<ACT, false, true> : k_act_grad<ACT, false, false>;
+}
+
+GradKernel act_grad_kernel(int act, bool f32, bool f16)
 {
     switch (act) {
     case MOE_ACT_RELU:
-        return f32 ? k_act_grad<MOE_ACT_RELU, true> : k_act_grad<MOE_ACT_RELU, false>;
+        return act_grad_kernel<MOE_ACT_RELU>(f32, f16);
     case MOE_ACT_SILU:
-        return f32 ? k_act_grad<MOE_ACT_SILU, true> : k_act_grad<MOE_ACT_SILU, false>;
+        return act_grad_kernel<MOE_ACT_SILU>(f32, f16);
     case MOE_ACT_GELU:
-        return f32 ? k_act_grad<MOE_ACT_GELU, true> : k_act_grad<MOE_ACT_GELU, false>;
+        return act_grad_kernel<MOE_ACT_GELU>(f32, f16);
     case MOE_ACT_GELU_TANH:
-        return f32 ? k_act_grad<MOE_ACT_GELU_TANH, true> : k_act_grad<MOE_ACT_GELU_TANH, false>;
+        return act_grad_kernel<MOE_ACT_GELU_TANH>(f32, f16);
     default:
-        return f32 ? k_act_grad<MOE_ACT_NONE, true> : k_act_grad<MOE_ACT_NONE, false>;
+        return act_grad_kernel<MOE_ACT_NONE>(f32, f16);
     }
 }
 
@@ -1854,15 +1858,15 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
         g.part = db ? part : nullptr;
         g.lddy = lddy, g.lddp = ldp;
         g.T = T, g.N = N;
-        g.f16 = dtype == MOE_DT_F16, g.act = act;
         g.vec = vec16(dy, lddy, dysize) && (act == MOE_ACT_NONE || vec16(pre, N, 2));
         const int cb = (N + kGradCols - 1) / kGradCols;
         // about eight CTAs an SM, each with at least one round of rows
         chunks = std::max(1, std::min({(T + 31) / 32, 8 * device_sm_count() / cb, kGradMaxChunks}));
         g.rows = (T + chunks - 1) / chunks;
         chunks = (T + g.rows - 1) / g.rows;
-        if (launch_pdl(act_grad_kernel(act, dy_dtype == MOE_DT_F32), dim3(cb, chunks),
-                       dim3(kGradThreads), 0, s, g) != cudaSuccess)
+        const GradKernel kern =
+            act_grad_kernel(act, dy_dtype == MOE_DT_F32, dtype == MOE_DT_F16);
+        if (launch_pdl(kern, dim3(cb, chunks), dim3(kGradThreads), 0, s, g) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     const Operand P = direct ? Operand{dy, T, N, lddy} : Operand{dp, T, N, ldp};
