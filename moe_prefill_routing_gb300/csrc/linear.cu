@@ -189,8 +189,8 @@ __device__ __forceinline__ void rcp_all(float (&x)[R])
 }
 
 // act_t of R values, each step for all of them in turn (volatile keeps that
-// order): left to the compiler, one value's chain followed another's and 32
-// values of a lane took 2300 cycles (GELU-tanh).
+// order): left to the compiler, one value's chain followed another's, and
+// 4096 x 2816 x 11264 with GELU-tanh took 168 us instead of 158.
 template <int ACT, int R>
 __device__ __forceinline__ void act_all(float (&z)[R])
 {
@@ -371,6 +371,16 @@ __device__ __forceinline__ void lin_drain(uint64_t *bar, uint32_t parity)
             return;
 }
 
+// ---- few rows --------------------------------------------------------------------
+//
+// Tiles of 128 of Y's rows x bn of X's (16 ... 128), one CTA each, or `split`
+// CTAs of a cluster that share the reduction: a few tokens against a weight
+// matrix have as many tiles as 128 divides its rows (20 for 2560), and only
+// all SMs together draw the memory's bandwidth.  Two CTAs fit an SM, 110 KB
+// of loads in flight each.  Bound by memory, and by a fixed 4 us of launch,
+// first loads, joining the parts and writing: 16 x 10240 x 2560 with a
+// residual takes 13.2 us (52.9 MB, 4.0 TB/s, 6 without the fixed part);
+// 1 x 2560 x 512, 4.4 us.
 __global__ void __launch_bounds__(kLinThreads)
     k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const LinArgs p)
@@ -604,17 +614,17 @@ __global__ void __launch_bounds__(kLinThreads)
 // (bn = 256) for 512 cycles of MMA; the same tile on one SM would load 48.
 // Pairs walk the tiles (persistent); two accumulators in tensor memory let
 // eight epilogue warps work on one tile while the MMAs fill the other.  An
-// epilogue warp takes 32 rows x 32 columns at a time: tensor memory (read
-// about 330 cycles ahead) -> registers -> one of its two slots of shared
-// memory -> one TMA store.  (Row pieces read back from shared memory and
-// stored by the warp took 1700 cycles for those 32 columns; each lane storing
-// its row from registers, 32 bytes at a time, takes 203 us where this takes
-// 168 below: 32 lines an instruction.)
+// epilogue warp takes 32 rows x 32 columns at a time, half of the columns in
+// one go: tensor memory (read one step ahead) -> registers -> one of its two
+// slots of shared memory -> one TMA store.  (On 4096 x 2816 x 11264 with GELU-tanh,
+// pre and bias: rows read back from shared memory and stored by the warp 220
+// us, each lane storing its row from registers, 32 bytes at a time, 203 us,
+// where TMA stores took 168: both put 8 to 32 lines into an instruction.)
 //
-// Bound by the tensor cores: 4096 x 2816 x 11264 with bias, GELU and pre
-// takes 157 - 170 us (1.53 - 1.65 PFLOP/s, on six GPUs), its MMAs alone 133;
-// the rest is what 184 MB of outputs take from the loads' shared memory and
-// L2 bandwidth, and the last of ten rounds of tiles, a quarter full.
+// Bound by the tensor cores: that product with GELU-tanh takes 157 - 161 us
+// (1.61 - 1.65 PFLOP/s, on several GPUs), without pre and activation 141 -
+// 150, its MMAs alone 133.  The rest is 184 MB of outputs, and the last of
+// ten rounds of tiles, a quarter full.
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
 //
@@ -623,7 +633,10 @@ __global__ void __launch_bounds__(kLinThreads)
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairParts = kPairEpiWarps / 4;  // warps that share 32 rows
-constexpr int kCols = 16;       // columns that an epilogue warp works on at once
+// Columns that an epilogue warp works on at once.  Fewer leave latencies bare,
+// more make the loop's code too long for the instruction caches: the product
+// above takes 166 us with 8, 161 with 16, 164 with 32 (on one GPU).
+constexpr int kCols = 16;
 constexpr int kPairSub = 2;     // 64-r halves of a stage
 constexpr int kPairStages = 3;
 constexpr int kPairMaxSplit = 4;     // a cluster of eight CTAs
@@ -1349,8 +1362,11 @@ struct Eight {
 // dP = dy act'(pre), and the column sums of one chunk of rows.  A warp takes
 // every eighth row of the chunk, eight columns a lane, two rows' loads in
 // flight; the warps' sums are added in order.  Bound by memory: dy and pre
-// are read and dP written once.  Four CTAs an SM with two rows in flight
-// each measured 51 us on 4096 x 11264 (5.4 TB/s), two CTAs with four rows 58.
+// are read and dP written once: 48 us for 4096 x 11264 (5.8 TB/s, 0.85 of a
+// copy's), at 26 instructions an element with six tenths of the issue slots
+// taken (58 with the 16-bit type chosen at run time, 32 instructions).  Four
+// CTAs an SM with two rows in flight each; two CTAs with four rows took a
+// seventh longer.
 template <int ACT, bool F32, bool F16>
 __global__ void __launch_bounds__(kGradThreads, 4) k_act_grad(GradArgs p)
 {
@@ -1557,7 +1573,7 @@ double pair_step(int bn, bool y_mn)
     return 200.0 + 1.65 * (2.0 * pair_b_bytes(bn, y_mn) / (LK * 2));
 }
 
-// A tile's epilogue (about 1500 cycles per 64 columns) hides behind the next
+// A tile's epilogue (counted as 1500 cycles per 64 columns) hides behind the next
 // tile's MMAs, except the last one's; starting takes about 5000 cycles, and
 // joining the parts of a split tile about 8000.
 constexpr int kCutMaxBn = 160;  // three times as many columns fit tensor memory
