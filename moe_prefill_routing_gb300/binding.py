@@ -7,6 +7,7 @@ is no fallback: if the library is missing or a call fails, this raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -608,7 +609,7 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _MASK = (torch.bool, torch.uint8)
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice  # of an initialised context: its tensors exist
 
 
 def _refuse(t, name: str, shape, dtypes, dev):
@@ -692,6 +693,7 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
     return y
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_grad_workspace_bytes(T: int, N: int) -> int:
     return int((_lib or lib()).moe_linear_grad_workspace_bytes(T, N))
 
@@ -750,6 +752,7 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
     return dx, dW, db
 
 
+@functools.lru_cache(maxsize=1024)
 def route_workspace_bytes(T: int, E: int) -> int:
     return int((_lib or lib()).moe_route_workspace_bytes(T, E))
 
