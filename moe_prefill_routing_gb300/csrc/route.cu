@@ -19,6 +19,10 @@ constexpr int kFinalCtas = 8;       // one cluster
 constexpr int kFinalThreads = 512;
 constexpr uint32_t kTaken = 0;  // key of an expert already chosen
 
+// CTAs that an SM holds at once, by registers; the grid is as many
+template <int V>
+constexpr int kRouteResident = V >= 16 ? 1 : 2;
+
 struct RouteArgs {
     const void *logits;
     const float *bias;     // may be null
@@ -108,7 +112,7 @@ __device__ __forceinline__ uint32_t warp_threshold(uint32_t own, uint32_t kmax, 
 // 2.4 us for one token.  (Two tokens a warp would halve the shuffles but
 // double the lane maxima's rounds, which one instruction each reduces.)
 template <typename L, int V, int W, int C, bool BIAS>
-__global__ void __launch_bounds__(kRouteThreads, V >= 16 ? 1 : 2) k_route(const RouteArgs p)
+__global__ void __launch_bounds__(kRouteThreads, kRouteResident<V>) k_route(const RouteArgs p)
 {
     constexpr int G = 32 * W;                 // threads of a group
     constexpr int kGroups = kRouteWarps / W;  // groups of the CTA
@@ -574,7 +578,8 @@ extern "C" int moe_route(const void *logits, int64_t ld, int l_dtype, const floa
             constexpr int V = decltype(v)::value, W = decltype(w)::value, C = decltype(c)::value;
             using L = decltype(l);
             const int per = kRouteWarps / W;
-            grid = std::max(1, std::min({(T - 1) / per + 1, 2 * device_sm_count(), kRouteMaxCtas}));
+            grid = std::max(1, std::min({(T - 1) / per + 1, kRouteResident<V> * device_sm_count(),
+                                         kRouteMaxCtas}));
             auto kern = bias ? k_route<L, V, W, C, true> : k_route<L, V, W, C, false>;
             return launch_pdl(kern, dim3(grid), dim3(kRouteThreads), route_smem(E, k, W), s, a);
         });

@@ -14,9 +14,9 @@
 // once; the weights' part is k values a token, set out by expert in shared
 // memory.
 //
-// 32768 tokens x 256 experts, bf16: 16.2 us, 2.2 TB/s of the 35.7 MB it moves;
-// bound by instructions (390 a token, six tenths of the issue slots; the rest
-// waits for loads and reductions).  2048 x 512, fp32: 3.6 us, launch and one
+// 32768 tokens x 256 experts, bf16: 13.9 us, 2.6 TB/s of the 35.7 MB it moves;
+// bound by instructions (370 a token, seven tenths of the issue slots; the rest
+// waits for loads and reductions).  2048 x 512, fp32: 3.5 us, launch and one
 // token's latency.
 #include "route.cuh"
 
@@ -59,9 +59,15 @@ __device__ __forceinline__ void sum_all(float (&v)[N], Group<W> &gr)
     }
 }
 
+// CTAs that an SM holds at once, by registers; the grid is as many (eight an
+// SM, 2.7 rounds of them, took 16.2 us instead of 13.9, four of 128 experts
+// are 8 % faster than three)
+template <int V, int J>
+constexpr int kGradResident = V >= 16 || J > 1 ? 2 : V >= 8 ? 3 : 4;
+
 // J: slots of a lane (k <= 32 W J).
 template <typename L, int V, int W, int C, int J>
-__global__ void __launch_bounds__(kGradThreads, V >= 16 || J > 1 ? 2 : 3)
+__global__ void __launch_bounds__(kGradThreads, kGradResident<V, J>)
     k_route_grad(const RouteGradArgs p)
 {
     constexpr int G = 32 * W;
@@ -289,10 +295,12 @@ extern "C" int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const
             constexpr int V = decltype(v)::value, W = decltype(w)::value, C = decltype(c)::value;
             using L = decltype(l);
             const int per = kGradWarps / W;
-            const int grid = std::min((T - 1) / per + 1, 8 * device_sm_count());
             // one slot a lane serves k up to 32 (or the CTA's 256 lanes)
-            auto kern = W > 1 || k <= 32 ? k_route_grad<L, V, W, C, 1>
-                                         : k_route_grad<L, V, W, C, W == 1 ? 8 : 1>;
+            constexpr int kMany = W == 1 ? 8 : 1;
+            const bool one = W > 1 || k <= 32;
+            auto kern = one ? k_route_grad<L, V, W, C, 1> : k_route_grad<L, V, W, C, kMany>;
+            const int resident = one ? kGradResident<V, 1> : kGradResident<V, kMany>;
+            const int grid = std::min((T - 1) / per + 1, resident * device_sm_count());
             return launch_pdl(kern, dim3(grid), dim3(kGradThreads),
                               size_t(per) * ((E + 3) & ~3) * 4, reinterpret_cast<cudaStream_t>(stream), a);
         });
