@@ -1,10 +1,12 @@
 // The router: logits -> top-k experts, weights, counts and the balance and z
 // losses (moe_route).  The scores and their ratios: route.cuh.
 //
-// Every token's row is read once into registers by one warp (E <= 512) or one
-// CTA (larger E); statistics, choice and weights come from there.  Counts and
-// probability sums are kept per CTA; k_route_final adds the CTAs' rows in
-// their order, so the losses are deterministic.
+// Every token's row is read once into registers by one warp (E <= 512), four
+// (E <= 2048) or one CTA; statistics, choice and weights come from there.
+// (8192 tokens of 1024 experts: 55 us with four warps, 215 with a CTA, whose
+// every reduction waits for 16 warps.)  Counts and probability sums are kept
+// per CTA; k_route_final adds the CTAs' rows in their order, so the losses
+// are deterministic.
 #include "route.cuh"
 
 namespace moe {
@@ -101,7 +103,7 @@ __device__ __forceinline__ uint32_t warp_threshold(uint32_t own, uint32_t kmax, 
 // experts: 12 for k = 10), each with its expert as one 64-bit number that
 // orders them (key, then the lower expert); each lane takes one and counts
 // how many are larger, which is its slot.  With more than 32 (ties, or one lane holding most),
-// k > 32, or a CTA per token: k rounds of the group's largest key, whose
+// k > 32, or more warps per token: k rounds of the group's largest key, whose
 // holder drops it and looks for its next best.
 //
 // Bound by instructions, not memory: some 500 a token at 128 experts (sigmoid,
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteResident<V>) k_route(cons
     constexpr int G = 32 * W;                 // threads of a group
     constexpr int kGroups = kRouteWarps / W;  // groups of the CTA
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint2 red[2][W];
+    __shared__ uint2 red[W > 1 ? kGroups : 1][2][W];
     __shared__ float s_sum[kRouteWarps];
     __shared__ float s_z[kGroups];
     __shared__ int s_live[kGroups];
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteResident<V>) k_route(cons
     uint64_t *sel_o = reinterpret_cast<uint64_t *>(ps);  // key, then ~expert
     int *sel_e = reinterpret_cast<int *>(sel_o + (p.k > 32 ? 0 : sel_slots(p.k)));
     float *sel_l = reinterpret_cast<float *>(sel_e + sel_slots(p.k));
-    Group<W> gr{red};
+    Group<W> gr{red[W > 1 ? g : 0]};
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
         cnt[e] = 0;
     if (threadIdx.x == 0)

@@ -183,19 +183,22 @@ __device__ __forceinline__ void store_row(const float (&d)[V], L *row, int lane,
 }
 
 // Reductions over the group of W warps that holds one token's row.  W > 1:
-// the group is the CTA; `red` is double-buffered so that one barrier per
-// reduction is enough.
+// the CTA's groups have a barrier each; `red` (the group's own) is
+// double-buffered so that one barrier per reduction is enough.
 template <int W>
 struct Group {
     uint2 (*red)[W];
     int buf = 0;
 
+    __device__ __forceinline__ int warp() const { return int(threadIdx.x >> 5) % W; }
+
     __device__ __forceinline__ void sync()
     {
         if constexpr (W == 1)
             __syncwarp();
-        else
-            __syncthreads();
+        else  // (barrier 0 is the CTA's)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + int(threadIdx.x) / (32 * W)), "n"(32 * W)
+                         : "memory");
     }
 
     // largest key of the group; e becomes the lowest e of those that have it
@@ -210,8 +213,8 @@ struct Group {
             em = __reduce_min_sync(kFull, key == km ? uint32_t(e) : 0xffffffffu);
         if constexpr (W > 1) {
             if ((threadIdx.x & 31) == 0)
-                red[buf][threadIdx.x >> 5] = make_uint2(km, em);
-            __syncthreads();
+                red[buf][warp()] = make_uint2(km, em);
+            sync();
             uint2 b = red[buf][0];
 #pragma unroll
             for (int i = 1; i < W; ++i) {
@@ -232,8 +235,8 @@ struct Group {
         uint32_t km = __reduce_max_sync(kFull, key);
         if constexpr (W > 1) {
             if ((threadIdx.x & 31) == 0)
-                red[buf][threadIdx.x >> 5].x = km;
-            __syncthreads();
+                red[buf][warp()].x = km;
+            sync();
 #pragma unroll
             for (int i = 0; i < W; ++i)
                 km = max(km, red[buf][i].x);
@@ -249,8 +252,8 @@ struct Group {
             v += __shfl_xor_sync(kFull, v, o);
         if constexpr (W > 1) {
             if ((threadIdx.x & 31) == 0)
-                red[buf][threadIdx.x >> 5].x = __float_as_uint(v);
-            __syncthreads();
+                red[buf][warp()].x = __float_as_uint(v);
+            sync();
             v = 0.0f;
 #pragma unroll
             for (int i = 0; i < W; ++i)
@@ -285,8 +288,8 @@ inline int check_sizes(int l_dtype, int T, int E, int k, int64_t ld, int score)
 }
 
 // Calls f<L, V, W, C>(): a warp per token up to 512 experts (V up to 16 a
-// lane), a CTA of `Warps` warps above; C elements per access where the
-// rows' length, distance and base allow it (`vec(C)`).
+// lane), four warps up to 2048, a CTA of `Warps` warps above; C elements per
+// access where the rows' length, distance and base allow it (`vec(C)`).
 template <int Warps, typename Vecs, typename F>
 auto by_shape(int dtype, int E, Vecs vec, F f)
 {
@@ -294,7 +297,7 @@ auto by_shape(int dtype, int E, Vecs vec, F f)
 #define MOE_ROUTE_CASE(L, V, W, C)                                                              \
     return f(L(), integral_constant<int, V>(), integral_constant<int, W>(),                     \
              integral_constant<int, C>())
-    constexpr int kV1 = 1024 / (32 * Warps), kV2 = MOE_MAX_EXPERTS / (32 * Warps);
+    constexpr int kV = MOE_MAX_EXPERTS / (32 * Warps);
     if (dtype == MOE_DT_F32) {
         if (E <= 32)
             MOE_ROUTE_CASE(float, 1, 1, 1);
@@ -314,8 +317,10 @@ auto by_shape(int dtype, int E, Vecs vec, F f)
         if (E <= 512)
             MOE_ROUTE_CASE(float, 16, 1, 1);
         if (E <= 1024)
-            MOE_ROUTE_CASE(float, kV1, Warps, 1);
-        MOE_ROUTE_CASE(float, kV2, Warps, 1);
+            MOE_ROUTE_CASE(float, 8, 4, 1);
+        if (E <= 2048)
+            MOE_ROUTE_CASE(float, 16, 4, 1);
+        MOE_ROUTE_CASE(float, kV, Warps, 1);
     }
     if (E <= 32)
         MOE_ROUTE_CASE(uint16_t, 1, 1, 1);
@@ -335,8 +340,10 @@ auto by_shape(int dtype, int E, Vecs vec, F f)
     if (E <= 512)
         MOE_ROUTE_CASE(uint16_t, 16, 1, 1);
     if (E <= 1024)
-        MOE_ROUTE_CASE(uint16_t, kV1, Warps, 1);
-    MOE_ROUTE_CASE(uint16_t, kV2, Warps, 1);
+        MOE_ROUTE_CASE(uint16_t, 8, 4, 1);
+    if (E <= 2048)
+        MOE_ROUTE_CASE(uint16_t, 16, 4, 1);
+    MOE_ROUTE_CASE(uint16_t, kV, Warps, 1);
 #undef MOE_ROUTE_CASE
 }
 

@@ -73,11 +73,11 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident<V, J>)
     constexpr int G = 32 * W;
     constexpr int kGroups = kGradWarps / W;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint2 red[2][W];
+    __shared__ uint2 red[W > 1 ? kGroups : 1][2][W];
     const int g = threadIdx.x / G, lane = threadIdx.x % G;
     const int E4 = (p.E + 3) & ~3;
     float *dsel = reinterpret_cast<float *>(smem) + size_t(g) * E4;  // by expert; zeros
-    Group<W> gr{red};
+    Group<W> gr{red[W > 1 ? g : 0]};
     for (int e = lane; e < p.E; e += G)
         dsel[e] = 0.0f;
     gr.sync();
@@ -295,9 +295,8 @@ extern "C" int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const
             constexpr int V = decltype(v)::value, W = decltype(w)::value, C = decltype(c)::value;
             using L = decltype(l);
             const int per = kGradWarps / W;
-            // one slot a lane serves k up to 32 (or the CTA's 256 lanes)
-            constexpr int kMany = W == 1 ? 8 : 1;
-            const bool one = W > 1 || k <= 32;
+            constexpr int kMany = (MOE_MAX_TOPK + 32 * W - 1) / (32 * W);
+            const bool one = k <= 32 * W;  // one slot a lane
             auto kern = one ? k_route_grad<L, V, W, C, 1> : k_route_grad<L, V, W, C, kMany>;
             const int resident = one ? kGradResident<V, 1> : kGradResident<V, kMany>;
             const int grid = std::min((T - 1) / per + 1, resident * device_sm_count());

@@ -99,6 +99,14 @@ def test_route_shapes(T, E, k, score):
     _check(T, E, k, score=score, norm=False, scale=2.5, closed=0.3, masked=0.3, seed=1, pad=3)
 
 
+@pytest.mark.parametrize("T,E,k", [(600, 1024, 8), (70, 1500, 200), (300, 2048, 140), (37, 2049, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_many_experts(T, E, k, score):
+    _check(T, E, k, score=score, masked=0.2, seed=4)
+    _check(T, E, k, score=score, norm=False, closed=0.3, dtype=torch.bfloat16, seed=5, pad=8)
+    _check(T, E, k, score=score, bias=True, scale=2.5, seed=6)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("norm", [True, False])
 def test_route_selection_bias(score, norm):
