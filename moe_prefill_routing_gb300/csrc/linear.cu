@@ -621,10 +621,10 @@ __global__ void __launch_bounds__(kLinThreads)
 // us, each lane storing its row from registers, 32 bytes at a time, 203 us,
 // where TMA stores took 168: both put 8 to 32 lines into an instruction.)
 //
-// Bound by the tensor cores: that product with GELU-tanh takes 157 - 161 us
-// (1.61 - 1.65 PFLOP/s, on several GPUs), without pre and activation 141 -
-// 150, its MMAs alone 133.  The rest is 184 MB of outputs, and the last of
-// ten rounds of tiles, a quarter full.
+// Bound by the tensor cores: that product with GELU-tanh takes 154 - 156 us
+// (1.67 - 1.69 PFLOP/s), without pre and activation 144 - 147, its MMAs alone
+// 133.  The rest is 184 MB of outputs, the last round of tiles and its
+// epilogue.
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
 //
@@ -651,7 +651,7 @@ struct PairCtrl {
 };
 
 struct PairArgs {
-    CUtensorMap a[2], b[2], out[2], pre;
+    CUtensorMap a[2], b[2], out[2], pre[2];
     LinArgs p[2];
     int tiles[2];       // 0 for an absent second product
     int bn;             // the larger of the two
@@ -1190,7 +1190,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     pair_cols(flags, mem.bias + h, pre, slot, h, v);
                 }
                 if (flags & kEpiPre)
-                    store_slot<uint16_t>(pre, &g.pre, p.pre, row, n0 + c, p.ldp, rows, cols,
+                    store_slot<uint16_t>(pre, &g.pre[w.which], p.pre, row, n0 + c, p.ldp, rows, cols,
                                          flags & kEpiVecPre);
                 if (flags & kEpiF32)
                     store_slot<float>(slot, &g.out[w.which], p.out, row, n0 + c, p.ldo, rows, cols,
@@ -1563,7 +1563,7 @@ struct Tiling {
     bool pair;
     int bn, split;
     int64_t tiles;
-    double tile_cycles;
+    double tile_cycles, cycles;  // of a tile, of the product
 };
 
 // What a tile of k_linear_pair takes per 64 of r, from times at bn = 64 ...
@@ -1573,18 +1573,31 @@ double pair_step(int bn, bool y_mn)
     return 200.0 + 1.65 * (2.0 * pair_b_bytes(bn, y_mn) / (LK * 2));
 }
 
-// A tile's epilogue (counted as 1500 cycles per 64 columns) hides behind the next
-// tile's MMAs, except the last one's; starting takes about 5000 cycles, and
-// joining the parts of a split tile about 8000.
+// A tile's epilogue hides behind the next tile's MMAs, except the last one's.
+// It is counted as 1500 cycles per 64 columns; it takes 2400 plain and 4200
+// with GELU-tanh and pre, but counted as 2400 the choice for short reductions
+// gets worse (4096 x 512 x 8192: 41.5 -> 69 us).  Starting takes about 5000
+// cycles, and joining the parts of a split tile about 8000.
+constexpr double kStartCycles = 5000.0, kJoinCycles = 8000.0, kEpiCycles = 1500.0;
 constexpr int kCutMaxBn = 160;  // three times as many columns fit tensor memory
+
+double epi_cycles(int bn)
+{
+    return kEpiCycles * ((bn + 63) / 64);
+}
+
+// A tile of one pair, unsplit, while others follow.
+double tile_cycles(const Product &q, int bn)
+{
+    return std::max(pair_step(bn, q.y_mn) * ((q.R + LK - 1) / LK), epi_cycles(bn));
+}
 
 Tiling choose_tiling(const Product &q, int sms, int max_bn)
 {
-    Tiling t{false, 0, 1, 0, 0.0};
+    Tiling t{false, 0, 1, 0, 0.0, 0.0};
     if (q.rows <= 128)
         return t;
     const int nk = (q.R + LK - 1) / LK, pairs = std::max(1, sms / 2);
-    double best = 0.0;
     for (int bn = max_bn; bn >= 64; bn -= 32) {
         const int64_t tiles =
             ((int64_t(q.rows) + 255) / 256) * ((int64_t(q.cols) + bn - 1) / bn);
@@ -1595,17 +1608,83 @@ Tiling choose_tiling(const Product &q, int sms, int max_bn)
             if (z > 1 && q.a.out_f32 && (nk + z - 1) / z > kChain)
                 continue;  // its chains are not cut further
             const double main = pair_step(bn, q.y_mn) * ((nk + z - 1) / z);
-            const double epi = 1500.0 * ((bn + 63) / 64);
             const int64_t waves = (tiles + pairs - 1) / pairs;
-            const double c = 5000.0 + main + (z > 1 ? 8000.0 : epi) +
-                             double(waves - 1) * std::max(main, epi);
-            if (!t.pair || c < best) {
-                t = Tiling{true, bn, z, tiles, std::max(main, epi)};
-                best = c;
-            }
+            const double c = kStartCycles + main + (z > 1 ? kJoinCycles : epi_cycles(bn)) +
+                             double(waves - 1) * tile_cycles(q, bn);
+            if (!t.pair || c < t.cycles)
+                t = Tiling{true, bn, z, tiles, tile_cycles(q, bn), c};
         }
     }
     return t;
+}
+
+// Tiles t0 of c0 cycles and then t1 of c1 on `pairs` pairs, as k_linear_pair
+// takes them: the cycles until the last is done, and the `shared` for it.
+double two_parts(int64_t t0, double c0, int64_t t1, double c1, int64_t pairs, int &shared)
+{
+    const int64_t per = t0 / pairs, extra = t0 % pairs, others = pairs - extra;
+    double best = 0.0;
+    for (int64_t s = 0; s <= (t1 + pairs - 1) / pairs; ++s) {
+        const int64_t rest = std::max<int64_t>(0, t1 - s * pairs);
+        const double more = extra ? (per + 1) * c0 + std::min(s, t1) * c1 : 0.0;
+        const double c = std::max(more, per * c0 + (s + (rest + others - 1) / others) * c1);
+        if (s == 0 || c < best) {
+            best = c;
+            shared = int(s);
+        }
+    }
+    return best;
+}
+
+// Columns of the product to leave to narrower tiles, so that its last round
+// is fuller and its last epilogue shorter; 0 if that gains nothing.  (4096 x
+// 2816 x 11264 with GELU-tanh and pre: 704 tiles of 256 columns are 9.3 rounds
+// of 76 pairs, 161 us; 656 and 96 of half the width end after 9.7, 155 us.
+// 4096 x 512 x 8192: 46.8 -> 41.5, 2048 x 10240 x 2560: 89.7 -> 85.4.)
+int64_t mixed_columns(const Product &q, int sms, const Tiling &t, Tiling &narrow)
+{
+    const int64_t pairs = std::max(1, sms / 2), n_mt = (int64_t(q.rows) + 255) / 256;
+    if (!t.pair || t.split != 1 || t.tiles <= pairs)
+        return 0;
+    const int64_t n_nt = (q.cols + t.bn - 1) / t.bn;
+    double best = t.cycles;
+    int64_t columns = 0;
+    // at most two rounds' worth of wide tiles are replaced
+    for (int64_t j = std::max<int64_t>(1, n_nt - 2 * pairs / n_mt - 1); j < n_nt; ++j)
+        for (int bn : {64, 96, 128, 192}) {
+            if (bn >= t.bn)
+                break;
+            const int64_t left = q.cols - j * t.bn;
+            const int64_t tiles = n_mt * ((left + bn - 1) / bn);
+            const double each = tile_cycles(q, bn);
+            int shared;
+            const double c = kStartCycles + epi_cycles(bn) +
+                             two_parts(n_mt * j, t.tile_cycles, tiles, each, pairs, shared);
+            if (c < best) {
+                best = c;
+                columns = left;
+                narrow = Tiling{true, bn, 1, tiles, each, c};
+            }
+        }
+    return columns;
+}
+
+// Columns [from, from + cols) of a product, `from` a multiple of 32.
+Product columns_of(const Product &q, int64_t from, int64_t cols)
+{
+    Product o = q;
+    const auto at = [&](const void *p, int64_t n) {
+        return p ? static_cast<uint8_t *>(const_cast<void *>(p)) + n : nullptr;
+    };
+    const int64_t size = q.a.out_f32 ? 4 : 2;
+    o.cols = int(cols);
+    (q.y_mn ? o.Y.cols : o.Y.rows) = cols;
+    o.Y.p = at(q.Y.p, from * 2 * (q.y_mn ? 1 : q.Y.ld));
+    o.a.bias = reinterpret_cast<const float *>(at(q.a.bias, from * 4));
+    o.a.residual = at(q.a.residual, from * size);
+    o.a.pre = at(q.a.pre, from * 2);
+    o.a.out = at(q.a.out, from * size);
+    return o;
 }
 
 constexpr int kSmallTmem = 256;
@@ -1692,7 +1771,7 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         if (e == cudaSuccess && a.vec_out && a.split == 1)
             e = out_map(&g.out[i], a.out, a.M, a.N, a.ldo, a.out_f32, a.f16);
         if (e == cudaSuccess && a.pre && a.vec_pre && a.split == 1)
-            e = out_map(&g.pre, a.pre, a.M, a.N, a.ldp, 0, a.f16);
+            e = out_map(&g.pre[i], a.pre, a.M, a.N, a.ldp, 0, a.f16);
         if (e != cudaSuccess)
             return e;
         g.slot = std::max(g.slot, a.out_f32 ? 4096u : 2048u);
@@ -1701,13 +1780,8 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
     int clusters = g.tiles[0];
     if (split == 1) {
         clusters = int(std::min<int64_t>(int64_t(g.tiles[0]) + g.tiles[1], pairs));
-        // the most of product 1's tiles that a pair with one more of product
-        // 0's takes: what evens out the pairs' times
-        const int extra = g.tiles[0] % clusters, others = clusters - extra;
-        const double lead = extra ? t[0].tile_cycles / std::max(1.0, t[1].tile_cycles) : 0.0;
-        const double each = (g.tiles[1] - lead * others) / clusters;
-        g.shared = extra ? std::max(0, int(each + 0.5))
-                         : (g.tiles[1] + clusters - 1) / clusters;
+        two_parts(g.tiles[0], t[0].tile_cycles, g.tiles[1], count == 2 ? t[1].tile_cycles : 0.0,
+                  clusters, g.shared);
     }
     const size_t smem = 1024 + size_t(kPairStages) * kPairSub * g.sub_bytes +
                         (split > 1 ? size_t(LM) * (g.bn + 4) * 4
@@ -1735,7 +1809,14 @@ cudaError_t launch_products(Product *q, int count, ColSums sums, cudaStream_t s)
     for (int i = 0; i < count; ++i)
         t[i] = choose_tiling(q[i], sms, f32 ? kCutMaxBn : 256);
     cudaError_t e = cudaSuccess;
-    if (count == 2 && t[0].pair && t[1].pair && t[0].split == 1 && t[1].split == 1) {
+    const int64_t narrow = count == 1 ? mixed_columns(q[0], sms, t[0], t[1]) : 0;
+    if (narrow) {
+        const int64_t wide = q[0].cols - narrow;
+        const Product parts[2] = {columns_of(q[0], 0, wide), columns_of(q[0], wide, narrow)};
+        t[0].tiles = (int64_t(q[0].rows) + 255) / 256 * (wide / t[0].bn);
+        e = launch_pairs(parts, t, 2, sums, s);
+        sums.db = nullptr;
+    } else if (count == 2 && t[0].pair && t[1].pair && t[0].split == 1 && t[1].split == 1) {
         e = launch_pairs(q, t, 2, sums, s);
         sums.db = nullptr;
     } else {

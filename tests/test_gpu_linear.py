@@ -119,6 +119,15 @@ def test_linear_256_wide_tiles_long_reduction():
     _check_linear(2304, 4104, 2304, "none", torch.bfloat16, torch.bfloat16, bias=False, res=False)
 
 
+@pytest.mark.parametrize("N,dtype,out", [
+    (3000, torch.bfloat16, torch.bfloat16), (3001, torch.float16, torch.float32),
+    (3001, torch.bfloat16, torch.bfloat16), (3000, torch.float16, torch.float32)])
+def test_linear_tiles_of_two_widths(N, dtype, out):
+    # just above a whole number of rounds of tiles: the last columns go to narrower ones
+    _check_linear(2321, 1032, N, "silu", dtype, out, pad=8)
+    _check_linear(2321, 1032, N, "none", dtype, out, bias=False, res=False, pre=False)
+
+
 def test_linear_adds_into_its_output():
     x = _rand(1, 40, 320).to("cuda", torch.bfloat16)
     W = _rand(2, 90, 320, amp=0.05).to("cuda", torch.bfloat16)
@@ -218,6 +227,17 @@ def test_linear_grad_large_tiles():
 def test_linear_grad_256_wide_tiles():
     _check_grad(2300, 2312, 2201, "gelu", torch.bfloat16, torch.bfloat16, torch.bfloat16, pad=8)
     _check_grad(1000, 4104, 2600, "none", torch.float16, torch.float16, torch.float32)
+
+
+def test_linear_grad_tiles_of_two_widths():
+    T, K, N = 2100, 2600, 264
+    x = _rand(0, T, K).to("cuda", torch.bfloat16)
+    W = _rand(1, N, K, amp=0.05).to("cuda", torch.bfloat16)
+    dy = _rand(2, T, N, amp=0.1).to("cuda", torch.bfloat16)
+    dx, _, db = B.linear_grad(x, W, dy, need=(True, False, True))
+    Wd, dyd = _f64(W), _f64(dy)
+    _within(dx, dyd @ Wd, 2.0 ** -20 * (np.abs(dyd) @ np.abs(Wd)), torch.bfloat16)
+    _within(db, dyd.sum(0), 2.0 ** -20 * np.abs(dyd).sum(0), torch.float32)
 
 
 def test_linear_grad_computes_what_is_asked():
