@@ -1574,16 +1574,18 @@ double pair_step(int bn, bool y_mn)
 }
 
 // A tile's epilogue hides behind the next tile's MMAs, except the last one's.
-// It is counted as 1500 cycles per 64 columns; it takes 2400 plain and 4200
-// with GELU-tanh and pre, but counted as 2400 the choice for short reductions
-// gets worse (4096 x 512 x 8192: 41.5 -> 69 us).  Starting takes about 5000
-// cycles, and joining the parts of a split tile about 8000.
-constexpr double kStartCycles = 5000.0, kJoinCycles = 8000.0, kEpiCycles = 1500.0;
+// It takes about 9700 cycles for 256 plain columns (17000 with GELU-tanh and
+// pre), of which a part does not depend on the columns.  (Counted as 1500 per
+// 64 columns, reductions of 128 and 256 took a third longer; as 2400, 4096 x
+// 512 x 8192 took 69 us instead of 42.)  Starting takes about 5000 cycles, and
+// joining the parts of a split tile about 8000.
+constexpr double kStartCycles = 5000.0, kJoinCycles = 8000.0;
+constexpr double kEpiStart = 2500.0, kEpiCycles = 1800.0;
 constexpr int kCutMaxBn = 160;  // three times as many columns fit tensor memory
 
 double epi_cycles(int bn)
 {
-    return kEpiCycles * ((bn + 63) / 64);
+    return kEpiStart + kEpiCycles * ((bn + 63) / 64);
 }
 
 // A tile of one pair, unsplit, while others follow.
