@@ -172,6 +172,7 @@ enum SmemSlot {
     kSlotDownMx4,
     kSlotLinear,
     kSlotLinearPair,
+    kSlotLinearPairWide,
     kSlotCount
 };
 

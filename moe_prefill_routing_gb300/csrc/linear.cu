@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kLinThreads)
 //
 // out[m * ldo + n] = sum_r A[m][r] B[n][r] in tiles of 256 (m) x bn (n): one
 // tcgen05.mma of a CTA pair per 16 of r, each CTA loading its 128 rows of A
-// and half the rows of B.  A stage of 64 r costs each SM 32 KB of loads
+// and half the rows of B.  A piece of 64 r costs each SM 32 KB of loads
 // (bn = 256) for 512 cycles of MMA; the same tile on one SM would load 48.
 // Pairs walk the tiles (persistent); two accumulators in tensor memory let
 // eight epilogue warps work on one tile while the MMAs fill the other.  An
@@ -621,9 +621,9 @@ __global__ void __launch_bounds__(kLinThreads)
 // us, each lane storing its row from registers, 32 bytes at a time, 203 us,
 // where TMA stores took 168: both put 8 to 32 lines into an instruction.)
 //
-// Bound by the tensor cores: that product with GELU-tanh takes 154 - 156 us
-// (1.67 - 1.69 PFLOP/s), without pre and activation 144 - 147, its MMAs alone
-// 133.  The rest is 184 MB of outputs, the last round of tiles and its
+// Bound by the tensor cores: that product with GELU-tanh takes 150 - 152 us
+// (1.72 PFLOP/s), without pre and activation 140 (1.85 PFLOP/s), its MMAs
+// alone 133.  The rest is 184 MB of outputs, the last round of tiles and its
 // epilogue.
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
@@ -637,13 +637,19 @@ constexpr int kPairParts = kPairEpiWarps / 4;  // warps that share 32 rows
 // more make the loop's code too long for the instruction caches: the product
 // above takes 166 us with 8, 161 with 16, 164 with 32 (on one GPU).
 constexpr int kCols = 16;
-constexpr int kPairSub = 2;     // 64-r halves of a stage
-constexpr int kPairStages = 3;
+constexpr int kPairRing = 6;    // pieces of 64 r of both operands in shared memory
+// A stage, which is loaded, awaited and released as one, has one piece where
+// tiles have kPairWide columns or more: the ring is refilled sooner (4096 x
+// 11264 x 2816: 153 -> 148 us, 4096 x 2816 x 11264: 153.5 -> 151.5).  Two
+// pieces halve the barriers for narrower tiles, whose MMAs take less time than
+// a barrier's round (160 columns, 2000 x 1024 x 3000: 15.0 us, 16.3 with one;
+// 64 columns, 300 x 2560 x 2560: 12.5, 15.2 with one).
+constexpr int kPairWide = 224;
 constexpr int kPairMaxSplit = 4;     // a cluster of eight CTAs
 
 struct PairCtrl {
-    uint64_t full[kPairStages];
-    uint64_t empty[kPairStages];
+    uint64_t full[kPairRing];
+    uint64_t empty[kPairRing];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint32_t tmem_base;
@@ -873,6 +879,8 @@ __device__ __noinline__ void add_chain(uint32_t acc, uint32_t sum, int c, int wi
     tmem_store_wait();
 }
 
+// SUB: pieces of a stage.
+template <int SUB>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ PairArgs g)
 {
@@ -886,9 +894,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t crank = cluster_ctarank();
     const uint32_t rank = crank & 1u, lead = crank & ~1u;  // place in the pair, its even CTA
     const int z = int(crank >> 1), Z = g.p[0].split;
-    constexpr int S = kPairStages;
+    constexpr int S = kPairRing / SUB;
     const uint32_t sub_bytes = g.sub_bytes;
-    uint8_t *stg = smem + S * kPairSub * sub_bytes;
+    uint8_t *stg = smem + kPairRing * sub_bytes;
     // two accumulators and, where chains are cut, the sum of the earlier ones
     const uint32_t tmem_need = uint32_t(g.bn) * (g.cut ? 3 : 2);
     const uint32_t tmem_cols = tmem_need <= 128 ? 128u : tmem_need <= 256 ? 256u : 512u;
@@ -968,20 +976,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int a_mn = p.a_mn, b_mn = p.b_mn, half = p.bn / 2;
             const uint32_t tx = 2 * (kLinATile + pair_b_bytes(p.bn, b_mn));
             const int m0 = w.m0 + int(rank) * LM, n0 = w.n0 + int(rank) * half;
-            for (int kb = w.nk0; kb < w.nk1; kb += kPairSub) {
+            for (int kb = w.nk0; kb < w.nk1; kb += SUB) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
                 if (!ok)
                     break;
                 if (one) {
-                    const int subs = min(kPairSub, w.nk1 - kb);
+                    const int subs = min(SUB, w.nk1 - kb);
                     if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
                         mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(subs) * tx);
                     const uint32_t fb = dsmem_addr(&ctl.full[stage], lead);
 #pragma unroll
-                    for (int h = 0; h < kPairSub; ++h) {
+                    for (int h = 0; h < SUB; ++h) {
                         if (h >= subs)
                             break;
-                        uint8_t *sa = smem + (stage * kPairSub + h) * sub_bytes;
+                        uint8_t *sa = smem + (stage * SUB + h) * sub_bytes;
                         uint8_t *sb = sa + kLinATile;
                         const int k0 = (kb + h) * LK;
                         if (a_mn) {  // 64 m x 64 r boxes, m contiguous
@@ -1040,7 +1048,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int chain = p.chain;
             uint32_t d = 0;
             int left = 0;  // steps to go in this chain
-            for (int kb = w.nk0; kb < w.nk1; kb += kPairSub) {
+            for (int kb = w.nk0; kb < w.nk1; kb += SUB) {
                 const bool start = left == 0;
                 if (start) {
                     ok = __all_sync(0xffffffffu,
@@ -1056,8 +1064,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tc_fence_after_sync();
                 if (one) {
 #pragma unroll
-                    for (int h = 0; h < kPairSub; ++h) {
-                        const uint32_t off = uint32_t(stage * kPairSub + h) * (sub_bytes >> 4);
+                    for (int h = 0; h < SUB; ++h) {
+                        const uint32_t off = uint32_t(stage * SUB + h) * (sub_bytes >> 4);
                         if (kb + h < w.nk1) {
 #pragma unroll
                             for (uint32_t kk = 0; kk < LK / 16; ++kk)
@@ -1072,8 +1080,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     stage = 0;
                     phase ^= 1u;
                 }
-                left -= kPairSub;
-                if (left <= 0 || kb + kPairSub >= w.nk1) {  // the chain is complete
+                left -= SUB;
+                if (left <= 0 || kb + SUB >= w.nk1) {  // the chain is complete
                     left = 0;
                     if (one)
                         tc_commit_pair(&ctl.acc_full[buf], uint16_t(3u << lead));
@@ -1785,11 +1793,14 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         two_parts(g.tiles[0], t[0].tile_cycles, g.tiles[1], count == 2 ? t[1].tile_cycles : 0.0,
                   clusters, g.shared);
     }
-    const size_t smem = 1024 + size_t(kPairStages) * kPairSub * g.sub_bytes +
+    const size_t smem = 1024 + size_t(kPairRing) * g.sub_bytes +
                         (split > 1 ? size_t(LM) * (g.bn + 4) * 4
                                    : size_t(kPairEpiWarps) * (2 * g.slot + 128));
-    const void *kern = reinterpret_cast<const void *>(k_linear_pair);
-    const cudaError_t e = ensure_smem_limit(kern, kSlotLinearPair, 226 * 1024);
+    const bool wide = g.bn >= kPairWide;
+    const void *kern = wide ? reinterpret_cast<const void *>(k_linear_pair<1>)
+                            : reinterpret_cast<const void *>(k_linear_pair<2>);
+    const cudaError_t e = ensure_smem_limit(
+        kern, wide ? kSlotLinearPairWide : kSlotLinearPair, 226 * 1024);
     if (e != cudaSuccess)
         return e;
     void *args[] = {&g};
