@@ -628,8 +628,9 @@ __global__ void __launch_bounds__(kLinThreads)
 //
 // split > 1: a cluster of `split` pairs shares one tile's reduction.
 //
-// A launch takes one product or two (dx and dW): two short launches would
-// each leave SMs idle in their last round and pay the start twice.
+// A launch takes one product or two: dx and dW, whose own launches would each
+// leave SMs idle in their last round and pay the start twice, or the wide and
+// the narrow tiles of one (mixed_columns).
 constexpr int kPairThreads = 320;  // producer, MMA, eight epilogue warps
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairParts = kPairEpiWarps / 4;  // warps that share 32 rows
@@ -932,7 +933,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
     // The pair's i-th tile: its product and its place there; false past the
     // last.  Tiles of a product are numbered in blocks of 16 m tiles, m
-    // fastest: the pairs running at one time share few rows of both operands.
+    // fastest: the pairs running at one time share few rows of both operands
+    // (the product above takes 151.5 us so, 155 with blocks of 8 or 11).
     const int pairs = int(gridDim.x) / (2 * Z), pair = int(blockIdx.x) / (2 * Z);
     struct Tile {
         int which, m0, n0, nk0, nk1;
