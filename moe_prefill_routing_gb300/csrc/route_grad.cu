@@ -15,7 +15,7 @@
 // memory.
 //
 // 32768 tokens x 256 experts, bf16: 13.9 us, 2.6 TB/s of the 35.7 MB it moves;
-// bound by instructions (370 a token, seven tenths of the issue slots; the rest
+// bound by instructions (320 a token, six tenths of the issue slots; the rest
 // waits for loads and reductions).  2048 x 512, fp32: 3.5 us, launch and one
 // token's latency.
 #include "route.cuh"
