@@ -540,8 +540,7 @@ MOE_API int moe_selftest_wait_limit(const void *xs, const void *Wg, const void *
  * T >= 0, N >= 1 (any), K a positive multiple of 8; ldx >= K a multiple of 8;
  * ldr, ldy >= N; T, K, N <= 2^31 - 512.  x and W 16-byte aligned, the others aligned
  * to their element.  residual may be y itself (same ldr and ldy): each element
- * is read before it is written, by the same thread.  No other operands may
- * overlap.  A fixed order of every sum: results are deterministic.
+ * is read before it is written.  No other operands may overlap.  A fixed order of every sum: results are deterministic.
  */
 MOE_API int moe_linear(const void *x, int64_t ldx, const void *W, const float *bias,
                        const void *residual, int64_t ldr, int dtype, int act, int T, int K,
