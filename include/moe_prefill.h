@@ -633,6 +633,16 @@ MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const ui
                            const float *dloss, int T, int E, int k, int score, int norm,
                            float scale, void *dlogits, int64_t ldd, moe_stream_t stream);
 
+/*
+ * moe_selftest_linear_plan -- the launches that moe_linear (what = 1) or the
+ * products of moe_linear_grad (2: dx, 4: dW, 6: both) would take on a GPU of
+ * `sms` SMs: plan[0] their number, plan[1] the most dynamic shared memory of
+ * a CTA, plan[2] the most CTAs.  f32: y (dW) is fp32.  Host arithmetic alone:
+ * needs no GPU.  For tests.
+ */
+MOE_API int moe_selftest_linear_plan(int T, int K, int N, int what, int f32, int sms,
+                                     int64_t *plan);
+
 /* Human-readable text of a return code. */
 MOE_API const char *moe_status_str(int code);
 

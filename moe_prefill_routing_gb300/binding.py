@@ -126,6 +126,7 @@ _SIGS = {
                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                  C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_int64,
                                  C.c_void_p]),
+    "moe_selftest_linear_plan": (C.c_int, [C.c_int] * 6 + [C.POINTER(C.c_int64)]),
     "moe_read_status": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
     "moe_selftest_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                           C.c_int, C.c_int, C.c_int, C.c_int64, C.c_void_p,
@@ -845,6 +846,18 @@ def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: 
     if rc:
         raise MoeError("moe_route_grad", rc)
     return dlogits
+
+
+def selftest_linear_plan(T: int, K: int, N: int, what=("y",), f32: bool = False,
+                         sms: int = 152) -> dict:
+    """The launches of ``linear`` (what = ("y",)) or of the products of
+    ``linear_grad`` (dx, dW or both) on a GPU of `sms` SMs: their number, the
+    most shared memory and CTAs of one.  Needs no GPU."""
+    plan = (C.c_int64 * 3)()
+    code = sum({"y": 1, "dx": 2, "dW": 4}[w] for w in what)
+    _check("moe_selftest_linear_plan",
+           lib().moe_selftest_linear_plan(T, K, N, code, f32, sms, plan))
+    return {"launches": plan[0], "smem": plan[1], "ctas": plan[2]}
 
 
 def selftest_wait_limit(xs, Wg, Wu, offsets, cap: int, status, cta: int = 0, H=None):

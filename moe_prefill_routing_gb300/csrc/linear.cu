@@ -1568,6 +1568,30 @@ struct Product {
     LinArgs a;
 };
 
+// Dynamic shared memory of a launch of k_linear_pair whose tiles take
+// `sub_bytes` per 64 r: the ring, and the epilogue's slots (4 KB where an
+// output is fp32) or the parts of a split tile.  A CTA has 227 KB at most, a
+// few hundred bytes of them static: tilings that need more than kPairSmem are
+// not chosen.
+constexpr size_t kPairSmem = 226 * 1024;
+
+uint32_t pair_sub_bytes(int bn, int b_mn)
+{
+    return kLinATile + pair_b_bytes(bn, b_mn);
+}
+
+uint32_t pair_slot(bool f32)
+{
+    return f32 ? 4096 : 2048;
+}
+
+size_t pair_smem(uint32_t sub_bytes, int bn, int split, bool f32)
+{
+    return 1024 + size_t(kPairRing) * sub_bytes +
+           (split > 1 ? size_t(LM) * (bn + 4) * 4
+                      : size_t(kPairEpiWarps) * (2 * pair_slot(f32) + 128));
+}
+
 // Tiling of a product, chosen by estimated SM cycles.
 struct Tiling {
     bool pair;
@@ -1591,7 +1615,10 @@ double pair_step(int bn, bool y_mn)
 // joining the parts of a split tile about 8000.
 constexpr double kStartCycles = 5000.0, kJoinCycles = 8000.0;
 constexpr double kEpiStart = 2500.0, kEpiCycles = 1800.0;
-constexpr int kCutMaxBn = 160;  // three times as many columns fit tensor memory
+// Three times as many columns fit tensor memory.  (Of a Y whose j is
+// contiguous, half of 160 columns is loaded as 128: shared memory holds no
+// more than 128 of those columns beside fp32 slots, see pair_smem.)
+constexpr int kCutMaxBn = 160;
 
 double epi_cycles(int bn)
 {
@@ -1604,13 +1631,16 @@ double tile_cycles(const Product &q, int bn)
     return std::max(pair_step(bn, q.y_mn) * ((q.R + LK - 1) / LK), epi_cycles(bn));
 }
 
-Tiling choose_tiling(const Product &q, int sms, int max_bn)
+// f32: an output of the launch is.
+Tiling choose_tiling(const Product &q, int sms, bool f32)
 {
     Tiling t{false, 0, 1, 0, 0.0, 0.0};
     if (q.rows <= 128)
         return t;
     const int nk = (q.R + LK - 1) / LK, pairs = std::max(1, sms / 2);
-    for (int bn = max_bn; bn >= 64; bn -= 32) {
+    for (int bn = f32 ? kCutMaxBn : 256; bn >= 64; bn -= 32) {
+        if (pair_smem(pair_sub_bytes(bn, q.y_mn), bn, 1, f32) > kPairSmem)
+            continue;
         const int64_t tiles =
             ((int64_t(q.rows) + 255) / 256) * ((int64_t(q.cols) + bn - 1) / bn);
         for (int z = 1; z <= kPairMaxSplit; z *= 2) {
@@ -1701,9 +1731,10 @@ Product columns_of(const Product &q, int64_t from, int64_t cols)
 
 constexpr int kSmallTmem = 256;
 
-cudaError_t launch_small(const Product &q, cudaStream_t s)
+// k_linear's arguments and shared memory for a product, and its CTAs.
+LinArgs small_args(const Product &q, int sms, int64_t &ctas, size_t &smem)
 {
-    const int sms = device_sm_count(), nk = (q.R + LK - 1) / LK;
+    const int nk = (q.R + LK - 1) / LK;
     LinArgs a = q.a;
     a.M = q.cols, a.N = q.rows, a.R = q.R;
     a.a_mn = q.y_mn, a.b_mn = q.x_mn;
@@ -1722,25 +1753,35 @@ cudaError_t launch_small(const Product &q, cudaStream_t s)
     const int steps = (nk + a.split - 1) / a.split;
     a.chain = !a.out_f32 ? std::max(steps, 1)
                          : std::max(kChain, (steps + kSmallTmem / a.bn - 1) / (kSmallTmem / a.bn));
-    if (tiles * a.split > INT_MAX)
-        return cudaErrorInvalidValue;
+    ctas = tiles * a.split;
     const uint32_t stage = kLinATile + lin_b_tile(a.bn, a.b_mn);
     // two CTAs an SM; the parts beside the ring, or in it at 128 columns
     const uint32_t parts = a.bn < LM ? uint32_t(LM) * (a.bn + 4) * 4 : 0;
     a.stages = std::min<int>(kLinMaxStages, (110 * 1024 - parts) / stage);
-    const size_t smem = 1024 + size_t(a.stages) * stage + parts;
+    smem = 1024 + size_t(a.stages) * stage + parts;
+    return a;
+}
+
+constexpr size_t kSmallSmem = 112 * 1024;
+
+cudaError_t launch_small(const Product &q, cudaStream_t s)
+{
+    int64_t ctas;
+    size_t smem;
+    LinArgs a = small_args(q, device_sm_count(), ctas, smem);
+    if (ctas > INT_MAX)
+        return cudaErrorInvalidValue;
     CUtensorMap ma, mb;
     cudaError_t e = lin_map(&ma, q.Y, q.y_mn ? LK : LM, a.f16);
     if (e == cudaSuccess)
         e = lin_map(&mb, q.X, q.x_mn ? LK : a.bn, a.f16);
     const void *kern = reinterpret_cast<const void *>(k_linear);
     if (e == cudaSuccess)
-        e = ensure_smem_limit(kern, kSlotLinear, 112 * 1024);
+        e = ensure_smem_limit(kern, kSlotLinear, kSmallSmem);
     if (e != cudaSuccess)
         return e;
     void *args[] = {&ma, &mb, &a};
-    return launch_clustered(kern, unsigned(tiles * a.split), unsigned(a.split), kLinThreads, smem, s,
-                            args);
+    return launch_clustered(kern, unsigned(ctas), unsigned(a.split), kLinThreads, smem, s, args);
 }
 
 struct ColSums {
@@ -1755,6 +1796,7 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
 {
     const int sms = device_sm_count(), pairs = std::max(1, sms / 2);
     PairArgs g = {};
+    bool f32 = false;
     g.part = sums.part, g.db = sums.db, g.chunks = sums.chunks, g.db_n = sums.n;
     for (int i = 0; i < count; ++i) {
         if (t[i].tiles > INT_MAX / 2)
@@ -1775,7 +1817,8 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         g.cut |= a.split == 1 && nk > a.chain;
         g.tiles[i] = int(t[i].tiles);
         g.bn = std::max(g.bn, a.bn);
-        g.sub_bytes = std::max(g.sub_bytes, kLinATile + pair_b_bytes(a.bn, a.b_mn));
+        g.sub_bytes = std::max(g.sub_bytes, pair_sub_bytes(a.bn, a.b_mn));
+        f32 |= a.out_f32 != 0;
         cudaError_t e = lin_map(&g.a[i], q[i].X, q[i].x_mn ? LK : LM, a.f16);
         if (e == cudaSuccess)
             e = lin_map(&g.b[i], q[i].Y, q[i].y_mn ? LK : a.bn / 2, a.f16);
@@ -1786,8 +1829,8 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
             e = out_map(&g.pre[i], a.pre, a.M, a.N, a.ldp, 0, a.f16);
         if (e != cudaSuccess)
             return e;
-        g.slot = std::max(g.slot, a.out_f32 ? 4096u : 2048u);
     }
+    g.slot = pair_slot(f32);
     const int split = t[0].split;
     int clusters = g.tiles[0];
     if (split == 1) {
@@ -1795,14 +1838,12 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         two_parts(g.tiles[0], t[0].tile_cycles, g.tiles[1], count == 2 ? t[1].tile_cycles : 0.0,
                   clusters, g.shared);
     }
-    const size_t smem = 1024 + size_t(kPairRing) * g.sub_bytes +
-                        (split > 1 ? size_t(LM) * (g.bn + 4) * 4
-                                   : size_t(kPairEpiWarps) * (2 * g.slot + 128));
+    const size_t smem = pair_smem(g.sub_bytes, g.bn, split, f32);
     const bool wide = g.bn >= kPairWide;
     const void *kern = wide ? reinterpret_cast<const void *>(k_linear_pair<1>)
                             : reinterpret_cast<const void *>(k_linear_pair<2>);
     const cudaError_t e = ensure_smem_limit(
-        kern, wide ? kSlotLinearPairWide : kSlotLinearPair, 226 * 1024);
+        kern, wide ? kSlotLinearPairWide : kSlotLinearPair, kPairSmem);
     if (e != cudaSuccess)
         return e;
     void *args[] = {&g};
@@ -1810,11 +1851,18 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
                             smem, s, args);
 }
 
-// The products (the one with the longer reduction first) and the column sums,
-// if any.
-cudaError_t launch_products(Product *q, int count, ColSums sums, cudaStream_t s)
+// One launch of k_linear_pair (`pair`) or k_linear.
+struct Launch {
+    bool pair;
+    int count;  // of products
+    Product q[2];
+    Tiling t[2];
+};
+
+// The launches that compute the products (the one with the longer reduction
+// first): their number, at most two.
+int plan_launches(Product *q, int count, int sms, Launch (&out)[2])
 {
-    const int sms = device_sm_count();
     if (count == 2 && q[1].R > q[0].R)
         std::swap(q[0], q[1]);
     Tiling t[2] = {};
@@ -1822,26 +1870,36 @@ cudaError_t launch_products(Product *q, int count, ColSums sums, cudaStream_t s)
     for (int i = 0; i < count; ++i)
         f32 |= q[i].a.out_f32 != 0;
     for (int i = 0; i < count; ++i)
-        t[i] = choose_tiling(q[i], sms, f32 ? kCutMaxBn : 256);
-    cudaError_t e = cudaSuccess;
+        t[i] = choose_tiling(q[i], sms, f32);
     const int64_t narrow = count == 1 ? mixed_columns(q[0], sms, t[0], t[1]) : 0;
     if (narrow) {
         const int64_t wide = q[0].cols - narrow;
-        const Product parts[2] = {columns_of(q[0], 0, wide), columns_of(q[0], wide, narrow)};
         t[0].tiles = (int64_t(q[0].rows) + 255) / 256 * (wide / t[0].bn);
-        e = launch_pairs(parts, t, 2, sums, s);
-        sums.db = nullptr;
-    } else if (count == 2 && t[0].pair && t[1].pair && t[0].split == 1 && t[1].split == 1) {
-        e = launch_pairs(q, t, 2, sums, s);
-        sums.db = nullptr;
-    } else {
-        for (int i = 0; i < count && e == cudaSuccess; ++i) {
-            if (t[i].pair) {
-                e = launch_pairs(q + i, t + i, 1, sums, s);
-                sums.db = nullptr;
-            } else {
-                e = launch_small(q[i], s);
-            }
+        out[0] = Launch{
+            true, 2, {columns_of(q[0], 0, wide), columns_of(q[0], wide, narrow)}, {t[0], t[1]}};
+        return 1;
+    }
+    if (count == 2 && t[0].pair && t[1].pair && t[0].split == 1 && t[1].split == 1) {
+        out[0] = Launch{true, 2, {q[0], q[1]}, {t[0], t[1]}};
+        return 1;
+    }
+    for (int i = 0; i < count; ++i)
+        out[i] = Launch{t[i].pair, 1, {q[i], {}}, {t[i], {}}};
+    return count;
+}
+
+// The products and the column sums, if any.
+cudaError_t launch_products(Product *q, int count, ColSums sums, cudaStream_t s)
+{
+    Launch l[2];
+    const int n = plan_launches(q, count, device_sm_count(), l);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n && e == cudaSuccess; ++i) {
+        if (l[i].pair) {
+            e = launch_pairs(l[i].q, l[i].t, l[i].count, sums, s);
+            sums.db = nullptr;
+        } else {
+            e = launch_small(l[i].q[0], s);
         }
     }
     if (e == cudaSuccess && sums.db)
@@ -2003,4 +2061,52 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     return launch_products(q, count, ColSums{part, db, chunks, N}, s) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+extern "C" int moe_selftest_linear_plan(int T, int K, int N, int what, int f32, int sms,
+                                        int64_t *plan)
+{
+    using namespace moe;
+    if (!plan)
+        return MOE_ERR_NULL;
+    if (!sizes_ok(T, K, N, MOE_ACT_NONE) || T == 0 || what < 1 || what > 6 || what == 3 ||
+        what == 5 || sms < 2)
+        return MOE_ERR_SHAPE;
+    Product q[2];
+    int count = 0;
+    LinArgs a = {};
+    a.out_f32 = f32 != 0;
+    if (what & 1)
+        q[count++] = Product{{nullptr, T, K, K}, {nullptr, N, K, K}, false, false, T, N, K, a};
+    if (what & 4)
+        q[count++] = Product{{nullptr, T, N, N}, {nullptr, T, K, K}, true, true, N, K, T, a};
+    a.out_f32 = 0;
+    if (what & 2)
+        q[count++] = Product{{nullptr, T, N, N}, {nullptr, N, K, K}, false, true, T, K, N, a};
+    Launch l[2];
+    plan[0] = plan_launches(q, count, sms, l);
+    plan[1] = plan[2] = 0;
+    for (int i = 0; i < plan[0]; ++i) {
+        size_t smem = 0;
+        int64_t ctas = 0;
+        if (l[i].pair) {
+            uint32_t sub = 0;
+            int bn = 0;
+            bool wide = false;
+            for (int j = 0; j < l[i].count; ++j) {
+                sub = std::max(sub, pair_sub_bytes(l[i].t[j].bn, l[i].q[j].y_mn));
+                bn = std::max(bn, l[i].t[j].bn);
+                wide |= l[i].q[j].a.out_f32 != 0;
+                ctas += 2 * l[i].t[j].split * l[i].t[j].tiles;
+            }
+            smem = pair_smem(sub, bn, l[i].t[0].split, wide);
+            if (l[i].t[0].split == 1)
+                ctas = std::min<int64_t>(ctas, sms / 2 * 2);
+        } else {
+            small_args(l[i].q[0], sms, ctas, smem);
+        }
+        plan[1] = std::max(plan[1], int64_t(smem));
+        plan[2] = std::max(plan[2], ctas);
+    }
+    return MOE_OK;
 }

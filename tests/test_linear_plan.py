@@ -1,0 +1,34 @@
+"""The choice of tiles of moe_linear and moe_linear_grad on the CPU, over the
+range of sizes, types and SM counts: what a launch asks of an SM has to fit."""
+import random
+
+import pytest
+
+from moe_prefill_routing_gb300 import binding as B
+from moe_prefill_routing_gb300 import build as build_mod
+
+SMEM = 227 * 1024  # of a CTA on sm_103a, its static shared memory included
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return B.lib()
+
+
+SIZES = [(2048, 2560, 512), (1024, 2560, 256), (512, 5120, 512), (4096, 2560, 1024),
+         (2048, 5120, 512), (4096, 5120, 512), (8192, 5120, 512), (1089, 3032, 875),
+         (2048, 7168, 256), (21, 912, 7602)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("what", [("y",), ("dx",), ("dW",), ("dx", "dW")])
+def test_every_launch_fits_shared_memory(lib, what, f32):
+    rng = random.Random(7)
+    span = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    sizes = SIZES + [(span(1, 200000), 8 * span(1, 4096), span(1, 40000)) for _ in range(4000)]
+    for sms in (132, 148, 152, 160):
+        for T, K, N in sizes:
+            p = B.selftest_linear_plan(T, K, N, what, f32, sms)
+            assert 1 <= p["launches"] <= 2
+            assert p["smem"] + 1024 <= SMEM, (T, K, N, sms, p)
