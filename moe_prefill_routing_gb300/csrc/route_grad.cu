@@ -128,11 +128,12 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident<V, J>)
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             e[j] = on ? id[j] : -1;
-            dj[j] = d[j];
             // the slot's logit (read again: this lane need not hold it)
             v[j] = uint32_t(e[j]) < uint32_t(p.E) ? to_f(row[e[j]], p.f16) : -INFINITY;
             if (!(v[j] < INFINITY))
                 v[j] = -INFINITY;
+            // a slot without weight may hold anything, and 0 times a NaN is one
+            dj[j] = v[j] > -INFINITY ? d[j] : 0.0f;
         }
         float own = -INFINITY;
 #pragma unroll

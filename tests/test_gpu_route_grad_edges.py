@@ -1,0 +1,42 @@
+"""moe_route_grad where slots have no weight, experts are closed, and the
+gradients handed to it are no numbers there."""
+import pytest
+import torch
+
+from moe_prefill_routing_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(E, k, dtype=torch.float32, T=37):
+    g = torch.Generator().manual_seed(E + k)
+    l = 2 * torch.randn(T, E, generator=g)
+    l[torch.rand(T, E, generator=g) < 0.2] = -float("inf")
+    l[3, k // 2:] = -float("inf")  # fewer open experts than slots
+    l[4] = -float("inf")
+    return l.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("E,k", [(8, 4), (64, 6), (200, 40), (512, 10), (700, 5), (3000, 40)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("norm", [True, False])
+def test_dw_of_slots_without_weight_is_not_looked_at(E, k, score, norm):
+    l = _case(E, k)
+    kw = dict(score=score, norm=norm)
+    r = B.route(l, k, **kw)
+    ids = r["ids"].clone()
+    ids[0, 1] = -1            # a slot that the caller dropped
+    ids[1, 0] = E + 7         # outside
+    ids[2, 2] = -5
+    closed = (l[6] == -float("inf")).nonzero()[0]
+    ids[6, 3] = closed.to(torch.int32)  # a closed expert
+    ok = (ids >= 0) & (ids < E)
+    ok &= l.gather(1, ids.clamp(0, E - 1).long()) > -float("inf")
+    assert int((~ok).sum()) > 4
+    dw = torch.randn(ids.shape, generator=torch.Generator().manual_seed(1)).cuda()
+    dloss = torch.tensor([0.7, -0.4], device="cuda")
+    want = B.route_grad(l, ids, r["counts"], dw=torch.where(ok, dw, 0.0), dloss=dloss, **kw)
+    assert bool(want.isfinite().all())
+    for poison in (float("nan"), float("inf"), -float("inf")):
+        got = B.route_grad(l, ids, r["counts"], dw=torch.where(ok, dw, poison), dloss=dloss, **kw)
+        assert torch.equal(got, want), poison
