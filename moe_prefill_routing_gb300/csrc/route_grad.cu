@@ -245,9 +245,18 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident<V, J>)
             }
         } else {  // s, ds and with them the gradient are 0 for closed experts
             const float z0 = zc - inv * base;
+            float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                l[i] = s[i] * (inv * cf[i] + z0) + ds[i];
+                o[i] = s[i] * (inv * cf[i] + z0) + ds[i];
+            if (!(fabsf(z0) < INFINITY)) {  // ... unless dloss or dw made 0 times infinity
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    o[i] = l[i] > -INFINITY ? o[i] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                l[i] = o[i];
         }
         store_row<L, V, C, G>(l, orow, lane, p.E, p.f16);
         gr.sync();

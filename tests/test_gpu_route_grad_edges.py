@@ -40,3 +40,24 @@ def test_dw_of_slots_without_weight_is_not_looked_at(E, k, score, norm):
     for poison in (float("nan"), float("inf"), -float("inf")):
         got = B.route_grad(l, ids, r["counts"], dw=torch.where(ok, dw, poison), dloss=dloss, **kw)
         assert torch.equal(got, want), poison
+
+
+@pytest.mark.parametrize("E,k,dtype", [(64, 6, torch.float32), (512, 10, torch.bfloat16),
+                                       (1500, 12, torch.float32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("norm", [True, False])
+def test_closed_experts_gradient_is_zero_whatever_comes_in(E, k, dtype, score, norm):
+    # an overflowed loss scale: infinities and NaN in dloss or in dw of a used slot
+    l = _case(E, k, dtype)
+    kw = dict(score=score, norm=norm)
+    r = B.route(l, k, **kw)
+    inf, nan = float("inf"), float("nan")
+    closed = l == -inf
+    dw = torch.ones(r["ids"].shape, device="cuda")
+    for a, b, c in ((inf, 1.0, 1.0), (1.0, -inf, 1.0), (nan, 1.0, 1.0), (1.0, 1.0, inf),
+                    (1.0, 1.0, nan), (3e38, 3e38, -3e38)):
+        dw[:, 0] = c
+        g = B.route_grad(l, r["ids"], r["counts"], dw=dw, dloss=torch.tensor([a, b], device="cuda"),
+                         **kw)
+        assert bool((g[closed] == 0).all()), (a, b, c)
+        assert not bool(g.isfinite().all()) or a == 3e38
