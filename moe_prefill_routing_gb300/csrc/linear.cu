@@ -111,13 +111,17 @@ __device__ __forceinline__ void dsmem_st4(uint32_t a, uint32_t x, uint32_t y, ui
 }
 
 // Phi(z) and e^(-z^2/2), Phi the normal distribution function, from
-// erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), x >= 0: formula
-// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions, off
-// by 1.5e-7 at most (Phi by half of that).  The library's erfc is more exact
-// than any output here needs and takes registers that the epilogue lacks.
+// erfc(x) = t P(t) e^(-x^2), t = 1 / (1 + 0.43 x), x >= 0.  P, of degree 7, was
+// fitted to e^(x^2) erfc(x) / t for the smallest relative error over
+// x = 0 ... 9.6 (8.5e-8; e^(-x^2) is below 2^-126 from there on), by least
+// squares whose weights grow where the error is largest.  A relative error,
+// because GELU's values for negative z are z Phi(z) itself: in fp32 Phi is off
+// by 1.5e-6 of itself down to z = -5 and 8e-6 at -13, most of it z^2's rounding
+// in the exponent.  (The library's erfc takes registers that the epilogue
+// lacks.)
 __device__ __forceinline__ float cdf_t(float z)  // 1 / t
 {
-    return 1.0f + 0.3275911f * 0.7071067811865476f * fabsf(z);
+    return 1.0f + 0.43f * 0.7071067811865476f * fabsf(z);
 }
 
 __device__ __forceinline__ float cdf_e(float z)  // log2 of e^(-z^2/2)
@@ -127,11 +131,14 @@ __device__ __forceinline__ float cdf_e(float z)  // log2 of e^(-z^2/2)
 
 __device__ __forceinline__ float cdf(float z, float t, float e)
 {
-    float q = 1.061405429f;
-    q = q * t - 1.453152027f;
-    q = q * t + 1.421413741f;
-    q = q * t - 0.284496736f;
-    q = q * t + 0.254829592f;
+    float q = 0.0736689789f;
+    q = q * t - 0.310215612f;
+    q = q * t + 0.383441133f;
+    q = q * t - 0.0854884358f;
+    q = q * t + 0.246721865f;
+    q = q * t + 0.204987442f;
+    q = q * t + 0.244369731f;
+    q = q * t + 0.242514975f;
     q = 0.5f * q * t * e;
     return z > 0.0f ? 1.0f - q : q;
 }
