@@ -245,18 +245,15 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident<V, J>)
             }
         } else {  // s, ds and with them the gradient are 0 for closed experts
             const float z0 = zc - inv * base;
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                o[i] = s[i] * (inv * cf[i] + z0) + ds[i];
-            if (!(fabsf(z0) < INFINITY)) {  // ... unless dloss or dw made 0 times infinity
+            if (fabsf(z0) < INFINITY) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    o[i] = l[i] > -INFINITY ? o[i] : 0.0f;
-            }
+                    l[i] = s[i] * (inv * cf[i] + z0) + ds[i];
+            } else {  // dloss or dw overflowed: no 0 times infinity for those
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                l[i] = o[i];
+                for (int i = 0; i < V; ++i)
+                    l[i] = s[i] > 0.0f ? s[i] * (inv * cf[i] + z0) + ds[i] : ds[i];
+            }
         }
         store_row<L, V, C, G>(l, orow, lane, p.E, p.f16);
         gr.sync();
