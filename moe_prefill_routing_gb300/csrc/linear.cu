@@ -40,12 +40,17 @@ constexpr int kLinMaxStages = 8;
 constexpr int kLinMaxSplit = 8;  // portable cluster size
 constexpr uint64_t kLinDrainNs = 200000000ull;
 
-// The tensor core adds each product of 16 r to its fp32 accumulator with
-// truncation, so a sum drifts by about 1.6e-8 of itself per addition (2.7e-6
-// measured for r = 2560).  That is nothing beside a 16-bit output's rounding;
-// an fp32 output's sums are cut into chains of kChain steps of 64 r (32
-// additions, 5e-7) that are added outside the tensor core.
-constexpr int kChain = 8;
+// The tensor core adds with truncation, so a sum of numbers of one sign drifts
+// by up to 2^-23 of itself per MMA of 16 r (measured: 2.4e-8 with bf16
+// operands, 7.7e-8 with fp16 ones, whose products have more bits).  Sums are cut
+// into chains of steps of 64 r, four MMAs each, that are added outside the
+// tensor core: of 8 steps for an fp32 output (8e-7 and 2.5e-6), and for 16-bit
+// outputs of as many as drift by a quarter of half a unit at most, 256 for
+// fp16 and 2048 for bf16.
+__host__ __device__ constexpr int chain_steps(bool f32, bool f16)
+{
+    return f32 ? 8 : f16 ? 256 : 2048;
+}
 
 struct LinArgs {
     const float *bias;
@@ -57,7 +62,7 @@ struct LinArgs {
     int M, N, R;     // k_linear: M = j, N = i; k_linear_pair: M = i, N = j
     int a_mn, b_mn;  // the operand's m (n) is contiguous, not its r
     int bn, stages, split, n_mt;
-    int chain;       // steps of 64 r that one accumulator sums, see kChain
+    int chain;       // steps of 64 r that one accumulator sums, see chain_steps
     int f16, out_f32, act;
     int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
     uint32_t flags;  // the epilogue's choices in one word, see EpiFlags
@@ -81,10 +86,14 @@ enum EpiFlags : uint32_t {
 struct LinCtrl {
     uint64_t full[kLinMaxStages];
     uint64_t empty[kLinMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
     uint64_t done;
     uint32_t tmem_base;
     int abort_flag;
 };
+
+constexpr int kSmallTmem = 256;  // columns of tensor memory of a CTA of k_linear
 
 __host__ __device__ __forceinline__ uint32_t lin_b_tile(int bn, int b_mn)
 {
@@ -378,6 +387,28 @@ __device__ __forceinline__ void lin_drain(uint64_t *bar, uint32_t parity)
             return;
 }
 
+// Adds (or, first, copies) an accumulator of bn columns to the sum of the
+// earlier chains; whole warp, its 32 lanes of tensor memory.  Not inlined: few
+// calls come here, and the others' code stays short.
+__device__ __noinline__ void add_small_chain(uint32_t acc, uint32_t sum, int bn, bool add)
+{
+#pragma unroll 1
+    for (int c = 0; c < bn; c += 16) {
+        uint32_t r[16], o[16];
+        tmem_ld_32x32b_x16(acc + uint32_t(c), r);
+        if (add)
+            tmem_ld_32x32b_x16(sum + uint32_t(c), o);
+        tmem_ld_wait();
+        if (add) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
+        }
+        tmem_store_32x32b_x16(sum + uint32_t(c), r);
+    }
+    tmem_store_wait();
+}
+
 // ---- few rows --------------------------------------------------------------------
 //
 // Tiles of 128 of Y's rows x bn of X's (16 ... 128), one CTA each, or `split`
@@ -388,6 +419,10 @@ __device__ __forceinline__ void lin_drain(uint64_t *bar, uint32_t parity)
 // first loads, joining the parts and writing: 16 x 10240 x 2560 with a
 // residual takes 13.2 us (52.9 MB, 4.0 TB/s, 6 without the fixed part);
 // 1 x 2560 x 512, 4.4 us.
+//
+// Chains (chain_steps) have an accumulator each where those fit the CTA's
+// tensor memory; more of them (fp32 outputs of 33 to 128 rows from R = 16384)
+// take turns on two, which the accumulator warps add up in a third.
 __global__ void __launch_bounds__(kLinThreads)
     k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const LinArgs p)
@@ -406,10 +441,12 @@ __global__ void __launch_bounds__(kLinThreads)
     const int m0 = (tile % p.n_mt) * LM, n0 = (tile / p.n_mt) * bn;
     const int nk = (p.R + LK - 1) / LK;
     const int kb0 = int(int64_t(nk) * z / p.split), kb1 = int(int64_t(nk) * (z + 1) / p.split);
-    // chains of p.chain steps, each in an accumulator of its own
-    const int accs = max(1, (kb1 - kb0 + p.chain - 1) / p.chain);
+    // chains of p.chain steps
+    const int chains = max(1, (kb1 - kb0 + p.chain - 1) / p.chain);
+    const bool turns = chains * bn > kSmallTmem;  // on two accumulators; a third has the sum
+    const int accs = turns ? 1 : chains;          // to add up at the end
     uint32_t tmem_cols = 32;
-    while (tmem_cols < uint32_t(accs * bn))
+    while (tmem_cols < uint32_t((turns ? 3 : chains) * bn))
         tmem_cols *= 2;
     volatile int *abort_flag = &ctl.abort_flag;
 
@@ -417,6 +454,10 @@ __global__ void __launch_bounds__(kLinThreads)
         for (int s = 0; s < S; ++s) {
             mbar_init(&ctl.full[s], 1);
             mbar_init(&ctl.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.acc_full[b], 1);
+            mbar_init(&ctl.acc_empty[b], 4);  // the accumulator warps
         }
         mbar_init(&ctl.done, 1);
         ctl.abort_flag = 0;
@@ -490,9 +531,16 @@ __global__ void __launch_bounds__(kLinThreads)
         const uint64_t da0 = p.a_mn ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
         const uint64_t db0 = p.b_mn ? smem_desc_sw128(sb, 8192, 1024) : smem_desc_sw128(sb, 16, 1024);
         const bool one = elect_one();
-        uint32_t d = tmem_base;
-        int left = p.chain;
+        uint32_t d = tmem_base, aphase = 0;
+        int left = p.chain, buf = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
+            if (turns && left == p.chain) {
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag)))
+                    break;
+                tc_fence_after_sync();
+                d = tmem_base + uint32_t(buf * bn);
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag)))
                 break;
             tc_fence_after_sync();
@@ -505,9 +553,18 @@ __global__ void __launch_bounds__(kLinThreads)
                                left != p.chain || kk != 0);
                 tc_commit(&ctl.empty[stage]);
             }
-            if (--left == 0) {
+            if (--left == 0 || kb + 1 == kb1) {
                 left = p.chain;
-                d += uint32_t(bn);
+                if (!turns) {
+                    d += uint32_t(bn);
+                } else {
+                    if (one)
+                        tc_commit(&ctl.acc_full[buf]);
+                    if (++buf == 2) {
+                        buf = 0;
+                        aphase ^= 1u;
+                    }
+                }
             }
             __syncwarp();
             if (++stage == S) {
@@ -536,6 +593,19 @@ __global__ void __launch_bounds__(kLinThreads)
         bias[i] = p.bias && i < left ? p.bias[at + i] : 0.0f;
     bool done = false;
     if (warp >= 2) {
+        const uint32_t lanes = tmem_base + (uint32_t(warp & 3) << 21);
+        for (int i = 0; turns && i < chains; ++i) {
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(&ctl.acc_full[i & 1], (i >> 1) & 1, abort_flag)))
+                break;
+            tc_fence_after_sync();
+            add_small_chain(lanes + uint32_t((i & 1) * bn), lanes + uint32_t(2 * bn), bn, i > 0);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl.acc_empty[i & 1]);
+        }
+        __syncwarp();
         done = mbar_wait(&ctl.done, 0, abort_flag);
         if (!done)  // stopped: the MMAs in flight still read shared and write tensor memory
             lin_drain(&ctl.done, 0);
@@ -548,7 +618,8 @@ __global__ void __launch_bounds__(kLinThreads)
     if (warp >= 2) {
         tc_fence_after_sync();
         const int m = (warp & 3) * 32 + int(lane);
-        const uint32_t t0 = tmem_base + (uint32_t(warp & 3) << 21);
+        const uint32_t t0 =
+            tmem_base + (uint32_t(warp & 3) << 21) + uint32_t(turns ? 2 * bn : 0);
         const uint32_t to = dsmem_addr(acc + (int(z) * slice + m % slice) * pitch, m / slice);
 #pragma unroll 1
         for (int c = 0; c < cols; c += 16) {
@@ -669,7 +740,7 @@ struct PairArgs {
     LinArgs p[2];
     int tiles[2];       // 0 for an absent second product
     int bn;             // the larger of the two
-    int cut;            // chains are cut (an fp32 output)
+    int cut;            // a sum is cut into chains, see chain_steps
     uint32_t sub_bytes; // of shared memory for 64 r of both operands
     uint32_t slot;      // bytes of one slot of an epilogue warp
     // Pair q of the grid's first takes tiles q, q + pairs, ... of product 0;
@@ -1627,6 +1698,11 @@ constexpr double kEpiStart = 2500.0, kEpiCycles = 1800.0;
 // more than 128 of those columns beside fp32 slots, see pair_smem.)
 constexpr int kCutMaxBn = 160;
 
+bool is_cut(const Product &q)
+{
+    return (q.R + LK - 1) / LK > chain_steps(q.a.out_f32, q.a.f16);
+}
+
 double epi_cycles(int bn)
 {
     return kEpiStart + kEpiCycles * ((bn + 63) / 64);
@@ -1638,14 +1714,14 @@ double tile_cycles(const Product &q, int bn)
     return std::max(pair_step(bn, q.y_mn) * ((q.R + LK - 1) / LK), epi_cycles(bn));
 }
 
-// f32: an output of the launch is.
-Tiling choose_tiling(const Product &q, int sms, bool f32)
+// f32: an output of the launch is; cut: a sum of the launch is, into chains.
+Tiling choose_tiling(const Product &q, int sms, bool f32, bool cut)
 {
     Tiling t{false, 0, 1, 0, 0.0, 0.0};
     if (q.rows <= 128)
         return t;
     const int nk = (q.R + LK - 1) / LK, pairs = std::max(1, sms / 2);
-    for (int bn = f32 ? kCutMaxBn : 256; bn >= 64; bn -= 32) {
+    for (int bn = f32 || cut ? kCutMaxBn : 256; bn >= 64; bn -= 32) {
         if (pair_smem(pair_sub_bytes(bn, q.y_mn), bn, 1, f32) > kPairSmem)
             continue;
         const int64_t tiles =
@@ -1654,7 +1730,7 @@ Tiling choose_tiling(const Product &q, int sms, bool f32)
             // a split tile needs room for the parts beside the ring
             if (z > 1 && (nk / z < 4 || tiles * z > pairs || (bn != 64 && bn != 128)))
                 break;
-            if (z > 1 && q.a.out_f32 && (nk + z - 1) / z > kChain)
+            if (z > 1 && (nk + z - 1) / z > chain_steps(q.a.out_f32, q.a.f16))
                 continue;  // its chains are not cut further
             const double main = pair_step(bn, q.y_mn) * ((nk + z - 1) / z);
             const int64_t waves = (tiles + pairs - 1) / pairs;
@@ -1736,8 +1812,6 @@ Product columns_of(const Product &q, int64_t from, int64_t cols)
     return o;
 }
 
-constexpr int kSmallTmem = 256;
-
 // k_linear's arguments and shared memory for a product, and its CTAs.
 LinArgs small_args(const Product &q, int sms, int64_t &ctas, size_t &smem)
 {
@@ -1745,21 +1819,21 @@ LinArgs small_args(const Product &q, int sms, int64_t &ctas, size_t &smem)
     LinArgs a = q.a;
     a.M = q.cols, a.N = q.rows, a.R = q.R;
     a.a_mn = q.y_mn, a.b_mn = q.x_mn;
-    a.bn = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 || a.out_f32 ? 64 : 128;
+    a.chain = chain_steps(a.out_f32, a.f16);
+    // (128 columns leave no room for a second chain)
+    a.bn = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 || nk > a.chain || a.out_f32 ? 64
+                                                                                            : 128;
     a.n_mt = (q.cols + LM - 1) / LM;
     const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.rows) + a.bn - 1) / a.bn);
     // split the reduction while the CTAs still fit at once and each has at
-    // least four stages, or until the chains of an fp32 output fit the 256
-    // columns of tensor memory that each of two CTAs has
-    const int fit = kSmallTmem / a.bn * kChain;
+    // least four stages, or until an fp32 output's chains have an accumulator
+    // each
+    const int fit = kSmallTmem / a.bn * a.chain;
     a.split = 1;
     while (a.split < kLinMaxSplit &&
            ((tiles * a.split * 2 <= 2 * sms && nk / (a.split * 2) >= 4) ||
             (a.out_f32 && nk > fit * a.split)))
         a.split *= 2;
-    const int steps = (nk + a.split - 1) / a.split;
-    a.chain = !a.out_f32 ? std::max(steps, 1)
-                         : std::max(kChain, (steps + kSmallTmem / a.bn - 1) / (kSmallTmem / a.bn));
     ctas = tiles * a.split;
     const uint32_t stage = kLinATile + lin_b_tile(a.bn, a.b_mn);
     // two CTAs an SM; the parts beside the ring, or in it at 128 columns
@@ -1819,9 +1893,8 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
                   (a.f16 ? kEpiF16 : 0) | (a.vec_out ? kEpiVecOut : 0) |
                   (a.vec_res ? kEpiVecRes : 0) | (a.vec_pre ? kEpiVecPre : 0) |
                   uint32_t(a.act) * kEpiAct;
-        const int nk = (a.R + LK - 1) / LK;
-        a.chain = a.out_f32 ? kChain : std::max(nk, 1);
-        g.cut |= a.split == 1 && nk > a.chain;
+        a.chain = chain_steps(a.out_f32, a.f16);
+        g.cut |= a.split == 1 && is_cut(q[i]);
         g.tiles[i] = int(t[i].tiles);
         g.bn = std::max(g.bn, a.bn);
         g.sub_bytes = std::max(g.sub_bytes, pair_sub_bytes(a.bn, a.b_mn));
@@ -1873,11 +1946,13 @@ int plan_launches(Product *q, int count, int sms, Launch (&out)[2])
     if (count == 2 && q[1].R > q[0].R)
         std::swap(q[0], q[1]);
     Tiling t[2] = {};
-    bool f32 = false;
-    for (int i = 0; i < count; ++i)
+    bool f32 = false, cut = false;
+    for (int i = 0; i < count; ++i) {
         f32 |= q[i].a.out_f32 != 0;
+        cut |= is_cut(q[i]);
+    }
     for (int i = 0; i < count; ++i)
-        t[i] = choose_tiling(q[i], sms, f32);
+        t[i] = choose_tiling(q[i], sms, f32, cut);
     const int64_t narrow = count == 1 ? mixed_columns(q[0], sms, t[0], t[1]) : 0;
     if (narrow) {
         const int64_t wide = q[0].cols - narrow;
