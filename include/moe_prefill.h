@@ -556,17 +556,25 @@ MOE_API int moe_linear(const void *x, int64_t ldx, const void *W, const float *b
  *   dW[n][i] = sum_t dP[t][n] x[t][i]
  *   db[n]    = sum_t dP[t][n]
  * The two products take dP as an operand of type dtype: unless it is dy
- * itself (act none, dy of type dtype) it is rounded to dtype once.  db is
- * summed from the fp32 values.  relu'(0) = 0.
+ * itself (act none, dy of type dtype) it is rounded to dtype once; for an fp32
+ * dW from an fp32 dy, dW takes it in two such pieces (what rounding leaves is
+ * the second one), off by 2^-16 (bf16) or 2^-22 (fp16) of itself at most.  With
+ * dtype fp16 and an fp32 dy, dP is scaled by a power of two that takes the
+ * largest finite |dy| to 2^13 ... 2^14 and the products by its reciprocal, so
+ * that no dy is too small or too large for fp16.  db is summed from the fp32
+ * values.  relu'(0) = 0.
  * in   x, W, pre as in moe_linear (pre may be NULL for MOE_ACT_NONE)
  * in   dy        dy_dtype [T, N], rows lddy elements apart (dtype or MOE_DT_F32)
  * out  dx        dtype [T, K] contiguous, or NULL
  * out  dW        dw_dtype [N, K] contiguous, or NULL (dtype or MOE_DT_F32)
  * out  db        fp32 [N], or NULL
- * ws             moe_linear_grad_workspace_bytes(T, N) bytes, 256-byte aligned
+ * ws             moe_linear_grad_workspace_bytes(T, N) bytes, enough for every
+ *                choice of types, or moe_linear_grad_workspace_bytes_for's
+ *                (half of it unless dy and dW are fp32); 256-byte aligned
  * With T = 0, dW and db are zero.  W may be NULL without dx, x without dW.
  */
 MOE_API size_t moe_linear_grad_workspace_bytes(int T, int N);
+MOE_API size_t moe_linear_grad_workspace_bytes_for(int T, int N, int dy_dtype, int dw_dtype);
 MOE_API int moe_linear_grad(const void *x, int64_t ldx, const void *W, const void *pre,
                             const void *dy, int64_t lddy, int dy_dtype, int dtype, int act, int T,
                             int K, int N, void *dx, void *dW, int dw_dtype, float *db, void *ws,
@@ -635,9 +643,9 @@ MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const ui
 
 /*
  * moe_selftest_linear_plan -- the launches that moe_linear (what = 1) or the
- * products of moe_linear_grad (2: dx, 4: dW, 6: both) would take on a GPU of
- * `sms` SMs: plan[0] their number, plan[1] the most dynamic shared memory of
- * a CTA, plan[2] the most CTAs.  f32: y (dW) is fp32.  Host arithmetic alone:
+ * products of moe_linear_grad (2: dx, 4: dW, 6: both; + 8: dy is fp32 as is
+ * dW) would take on a GPU of `sms` SMs: plan[0] their number, plan[1] the most
+ * dynamic shared memory of a CTA, plan[2] the most CTAs.  f32: y (dW) is fp32.  Host arithmetic alone:
  * needs no GPU.  For tests.
  */
 MOE_API int moe_selftest_linear_plan(int T, int K, int N, int what, int f32, int sms,

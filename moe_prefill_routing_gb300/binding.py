@@ -113,6 +113,7 @@ _SIGS = {
                              C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p,
                              C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p]),
     "moe_linear_grad_workspace_bytes": (C.c_size_t, [C.c_int] * 2),
+    "moe_linear_grad_workspace_bytes_for": (C.c_size_t, [C.c_int] * 4),
     "moe_linear_grad": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                   C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
                                   C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
@@ -695,8 +696,11 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
 
 
 @functools.lru_cache(maxsize=1024)
-def linear_grad_workspace_bytes(T: int, N: int) -> int:
-    return int((_lib or lib()).moe_linear_grad_workspace_bytes(T, N))
+def linear_grad_workspace_bytes(T: int, N: int, dy_dtype=torch.float32,
+                                dw_dtype=torch.float32) -> int:
+    """Of ``linear_grad``'s workspace; half of it unless dy and dW are float32."""
+    return int((_lib or lib()).moe_linear_grad_workspace_bytes_for(
+        T, N, _DTYPES.get(dy_dtype, -1), _DTYPES.get(dw_dtype, -1)))
 
 
 def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), dw_dtype=None,
@@ -706,7 +710,8 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
     ``pre`` is what ``linear`` left there (not needed for act "none").
     ``need`` says which of dx [T, K], dW [N, K] (``dw_dtype``: W's type or
     float32) and db fp32 [N] to compute; the others come back as None unless
-    they are passed in."""
+    they are passed in.  dx and a 16-bit dW see dy act'(pre) rounded to x's
+    type; a float32 dW from a float32 dy sees twice its bits."""
     T, K = x.shape
     N = W.shape[0]
     dt = x.dtype
@@ -739,7 +744,8 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
         db = torch.empty(N, dtype=torch.float32, device=dev)
         dbp = db.data_ptr()
     if ws is None:
-        ws = torch.empty(linear_grad_workspace_bytes(T, N), dtype=torch.uint8, device=dev)
+        ws = torch.empty(linear_grad_workspace_bytes(T, N, dy.dtype, dW.dtype if dWp else dt),
+                         dtype=torch.uint8, device=dev)
     else:
         _ptr(ws)
     rc = (_lib or lib()).moe_linear_grad(
@@ -854,7 +860,7 @@ def selftest_linear_plan(T: int, K: int, N: int, what=("y",), f32: bool = False,
     ``linear_grad`` (dx, dW or both) on a GPU of `sms` SMs: their number, the
     most shared memory and CTAs of one.  Needs no GPU."""
     plan = (C.c_int64 * 3)()
-    code = sum({"y": 1, "dx": 2, "dW": 4}[w] for w in what)
+    code = sum({"y": 1, "dx": 2, "dW": 4, "dy fp32": 8}[w] for w in what)
     _check("moe_selftest_linear_plan",
            lib().moe_selftest_linear_plan(T, K, N, code, f32, sms, plan))
     return {"launches": plan[0], "smem": plan[1], "ctas": plan[2]}

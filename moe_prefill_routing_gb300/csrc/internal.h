@@ -171,8 +171,9 @@ enum SmemSlot {
     kSlotGateUpMx4,
     kSlotDownMx4,
     kSlotLinear,
-    kSlotLinearPair,
-    kSlotLinearPairWide,
+    kSlotLinearExtra,
+    kSlotLinearPair,  // + 1 for wide tiles, + 2 with EXTRA
+    kSlotLinearPairEnd = kSlotLinearPair + 3,
     kSlotCount
 };
 

@@ -54,6 +54,7 @@ __host__ __device__ constexpr int chain_steps(bool f32, bool f16)
 
 struct LinArgs {
     const float *bias;
+    const float *mul;  // EXTRA kernels: the sums are multiplied by *mul (no bias then), or null
     const void *residual;
     void *pre;
     void *out;
@@ -62,6 +63,7 @@ struct LinArgs {
     int M, N, R;     // k_linear: M = j, N = i; k_linear_pair: M = i, N = j
     int a_mn, b_mn;  // the operand's m (n) is contiguous, not its r
     int bn, stages, split, n_mt;
+    int two;         // EXTRA kernels: X = X1 + X2, each summed over all r
     int chain;       // steps of 64 r that one accumulator sums, see chain_steps
     int f16, out_f32, act;
     int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
@@ -80,7 +82,8 @@ enum EpiFlags : uint32_t {
     kEpiVecOut = 32,
     kEpiVecRes = 64,
     kEpiVecPre = 128,
-    kEpiAct = 256,  // times the activation
+    kEpiMul = 256,
+    kEpiAct = 512,  // times the activation
 };
 
 struct LinCtrl {
@@ -423,9 +426,21 @@ __device__ __noinline__ void add_small_chain(uint32_t acc, uint32_t sum, int bn,
 // Chains (chain_steps) have an accumulator each where those fit the CTA's
 // tensor memory; more of them (fp32 outputs of 33 to 128 rows from R = 16384)
 // take turns on two, which the accumulator warps add up in a third.
+//
+// EXTRA: with the two pieces of X and the factor that gradients from an fp32 dy
+// may have (kernels of their own: both cost a call of 4.6 us 0.2).
+template <bool EXTRA>
+struct LinMaps {
+    CUtensorMap a, b;
+};
+template <>
+struct LinMaps<true> {
+    CUtensorMap a, b, b2;  // b2: the second piece of X, if any
+};
+
+template <bool EXTRA>
 __global__ void __launch_bounds__(kLinThreads)
-    k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-             const LinArgs p)
+    k_linear(const __grid_constant__ LinMaps<EXTRA> maps, const LinArgs p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -439,7 +454,7 @@ __global__ void __launch_bounds__(kLinThreads)
     const uint32_t z = cluster_ctarank();
     const int tile = int(blockIdx.x) / p.split;
     const int m0 = (tile % p.n_mt) * LM, n0 = (tile / p.n_mt) * bn;
-    const int nk = (p.R + LK - 1) / LK;
+    const int nk1 = (p.R + LK - 1) / LK, nk = nk1 << (EXTRA ? p.two : 0);  // of a piece, of all
     const int kb0 = int(int64_t(nk) * z / p.split), kb1 = int(int64_t(nk) * (z + 1) / p.split);
     // chains of p.chain steps
     const int chains = max(1, (kb1 - kb0 + p.chain - 1) / p.chain);
@@ -462,8 +477,8 @@ __global__ void __launch_bounds__(kLinThreads)
         mbar_init(&ctl.done, 1);
         ctl.abort_flag = 0;
         fence_mbar_init();
-        prefetch_tmap(&map_a);
-        prefetch_tmap(&map_b);
+        prefetch_tmap(&maps.a);
+        prefetch_tmap(&maps.b);
     }
     __syncwarp();
     cluster_arrive();
@@ -491,18 +506,22 @@ __global__ void __launch_bounds__(kLinThreads)
                 uint64_t *fb = &ctl.full[stage];
                 mbar_arrive_expect_tx(fb, stage_bytes);
                 uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
-                const int k0 = kb * LK;
+                const CUtensorMap *ma = &maps.a, *mb = &maps.b;
+                int k0 = kb * LK;
+                if constexpr (EXTRA)
+                    if (kb >= nk1)
+                        mb = &maps.b2, k0 -= nk1 * LK;
                 if (p.a_mn) {  // 64 m x 64 r boxes, m contiguous
-                    tma_load_2d(sa, &map_a, fb, m0, k0);
-                    tma_load_2d(sa + 8192, &map_a, fb, m0 + 64, k0);
+                    tma_load_2d(sa, ma, fb, m0, k0);
+                    tma_load_2d(sa + 8192, ma, fb, m0 + 64, k0);
                 } else {
-                    tma_load_2d(sa, &map_a, fb, k0, m0);
+                    tma_load_2d(sa, ma, fb, k0, m0);
                 }
                 if (p.b_mn) {
                     for (int c = 0; c < bn; c += 64)
-                        tma_load_2d(sb + c * (LK * 2), &map_b, fb, n0 + c, k0);
+                        tma_load_2d(sb + c * (LK * 2), mb, fb, n0 + c, k0);
                 } else {
-                    tma_load_2d(sb, &map_b, fb, k0, n0);
+                    tma_load_2d(sb, mb, fb, k0, n0);
                 }
             }
             __syncwarp();
@@ -666,6 +685,14 @@ __global__ void __launch_bounds__(kLinThreads)
                     }
                 }
             }
+            if (EXTRA && p.mul) {
+                const float mul = *p.mul;
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[i][j] *= mul;
+            }
             finish_rows<R>(p, v, n0 + n, by, cols - n, at, left);
         }
     };
@@ -752,6 +779,13 @@ struct PairArgs {
     float *db;
     int chunks, db_n;
 };
+
+struct PairArgsExtra : PairArgs {
+    CUtensorMap a2[2];  // the second piece of X, if any
+};
+
+template <bool EXTRA>
+using PairArgsOf = std::conditional_t<EXTRA, PairArgsExtra, PairArgs>;
 
 // What one CTA loads of B per 64 r.
 __host__ __device__ __forceinline__ uint32_t pair_b_bytes(int bn, int b_mn)
@@ -890,13 +924,20 @@ __device__ __forceinline__ void put16(uint8_t *slot, int h, const float (&v)[kCo
 }
 
 // The epilogue of 32 rows (lane = row) x kCols columns, from column h of the
-// slots on: bias (`bias`: theirs), pre, activation, residual (in `slot`),
-// output.
-__device__ __forceinline__ void pair_cols(uint32_t flags, const float *bias, uint8_t *pre,
-                                          uint8_t *slot, int h, float (&v)[kCols])
+// slots on: factor, bias (`bias`: theirs), pre, activation, residual (in
+// `slot`), output.
+template <bool EXTRA>
+__device__ __forceinline__ void pair_cols(uint32_t flags, const float *mul, const float *bias,
+                                          uint8_t *pre, uint8_t *slot, int h, float (&v)[kCols])
 {
     const int lane = threadIdx.x & 31;
     const int f16 = flags & kEpiF16;
+    if (EXTRA && (flags & kEpiMul)) {
+        const float m = *mul;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+            v[j] *= m;
+    }
     if (flags & kEpiBias) {
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
@@ -958,10 +999,10 @@ __device__ __noinline__ void add_chain(uint32_t acc, uint32_t sum, int c, int wi
     tmem_store_wait();
 }
 
-// SUB: pieces of a stage.
-template <int SUB>
+// SUB: pieces of a stage.  EXTRA: as k_linear's.
+template <int SUB, bool EXTRA>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    k_linear_pair(const __grid_constant__ PairArgs g)
+    k_linear_pair(const __grid_constant__ PairArgsOf<EXTRA> g)
 {
     extern __shared__ uint8_t smem_raw[];
     // the same offset in every CTA: dynamic shared memory starts at the same address
@@ -1038,7 +1079,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int b = t / block, tall = min(16, p.n_mt - 16 * b), u = t - b * block;
         o.n0 = u / tall * p.bn;
         o.m0 = (16 * b + u % tall) * (2 * LM);
-        const int nk = (p.R + LK - 1) / LK;
+        const int nk = (p.R + LK - 1) / LK << (EXTRA ? p.two : 0);
         o.nk0 = int(int64_t(nk) * z / Z);
         o.nk1 = int(int64_t(nk) * (z + 1) / Z);
         return true;
@@ -1052,7 +1093,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bool ok = true;
         for (int i = 0; ok && tile_at(i, w); ++i) {
             const LinArgs &p = g.p[w.which];
-            const CUtensorMap *map_a = &g.a[w.which], *map_b = &g.b[w.which];
+            const CUtensorMap *map_b = &g.b[w.which];
             const int a_mn = p.a_mn, b_mn = p.b_mn, half = p.bn / 2;
             const uint32_t tx = 2 * (kLinATile + pair_b_bytes(p.bn, b_mn));
             const int m0 = w.m0 + int(rank) * LM, n0 = w.n0 + int(rank) * half;
@@ -1071,7 +1112,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             break;
                         uint8_t *sa = smem + (stage * SUB + h) * sub_bytes;
                         uint8_t *sb = sa + kLinATile;
-                        const int k0 = (kb + h) * LK;
+                        const CUtensorMap *map_a = &g.a[w.which];
+                        int k0 = (kb + h) * LK;
+                        if constexpr (EXTRA) {
+                            const int k1 = (p.R + LK - 1) / LK * LK;  // of a piece
+                            if (k0 >= k1)
+                                map_a = &g.a2[w.which], k0 -= k1;
+                        }
                         if (a_mn) {  // 64 m x 64 r boxes, m contiguous
                             tma_load_2d_pair(sa, map_a, fb, m0, k0);
                             tma_load_2d_pair(sa + 8192, map_a, fb, m0 + 64, k0);
@@ -1275,7 +1322,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const int ahead = h + kCols < 32 ? c + h + kCols : next;
                     if (ahead < width)
                         tmem_ld_32x32b_x16(t0 + uint32_t(ahead), r);
-                    pair_cols(flags, mem.bias + h, pre, slot, h, v);
+                    pair_cols<EXTRA>(flags, p.mul, mem.bias + h, pre, slot, h, v);
                 }
                 if (flags & kEpiPre)
                     store_slot<uint16_t>(pre, &g.pre[w.which], p.pre, row, n0 + c, p.ldp, rows, cols,
@@ -1364,6 +1411,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     for (int j = 0; j < 4; ++j)
                         v[i][j] += bias[j];
                 }
+                if (EXTRA && p.mul) {
+                    const float mul = *p.mul;
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[i][j] *= mul;
+                }
                 finish_rows<kBatch>(p, v, int64_t(m0) + m, by, rows - m, n0 + n, left);
             }
         }
@@ -1390,7 +1445,10 @@ constexpr int kGradMaxChunks = 128;  // rows of partial column sums
 struct GradArgs {
     const void *dy, *pre;
     uint16_t *dp;     // null: not written
+    uint16_t *dp2;    // what dp's rounding leaves, rounded; null: not written
     float *part;      // [chunks][N] or null
+    const uint32_t *maxima;  // [kMaxima] of |dy| by k_dy_max: dp and dp2 are scaled; or null
+    float *unscale;          // receives 1 / scale
     int64_t lddy, lddp;
     int T, N, rows;   // rows per chunk
     int vec;          // 16-byte accesses of dy and pre are aligned
@@ -1447,6 +1505,54 @@ struct Eight {
     }
 };
 
+// fp32 gradients reach below fp16's range (losses that are means over many
+// tokens), so for fp16 operands dP is multiplied by a power of two that takes
+// the largest finite |dy| to 2^13 ... 2^14 (|act'| <= 1.13): what is 2^-27 of
+// the largest keeps all its bits, and products are multiplied by the
+// reciprocal in fp32.  k_dy_max gives each CTA's maximum, as the bits of a float.
+constexpr int kMaxima = 256;
+constexpr int kMaxThreads = 256;
+
+__global__ void __launch_bounds__(kMaxThreads)
+    k_dy_max(const float *dy, int64_t ld, int T, int N, int vec, uint32_t *maxima)
+{
+    __shared__ uint32_t red[kMaxThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    uint32_t m = 0;
+    auto take = [&](uint32_t v) {
+        v &= 0x7fffffffu;
+        m = max(m, v < 0x7f800000u ? v : 0u);
+    };
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(dy + t * ld);
+        int n = 0;
+        if (vec) {
+            n = N / 4 * 4;
+            for (int c = int(threadIdx.x) * 4; c < n; c += kMaxThreads * 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(row + c);
+                take(v.x), take(v.y), take(v.z), take(v.w);
+            }
+        }
+        for (int c = n + int(threadIdx.x); c < N; c += kMaxThreads)
+            take(row[c]);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kMaxThreads / 32; ++i)
+            m = max(m, red[i]);
+        maxima[blockIdx.x] = m;
+    }
+}
+
+__device__ __forceinline__ float pow2(int e)  // -126 <= e <= 127
+{
+    return __int_as_float((e + 127) << 23);
+}
+
 // dP = dy act'(pre), and the column sums of one chunk of rows.  A warp takes
 // every eighth row of the chunk, eight columns a lane, two rows' loads in
 // flight; the warps' sums are added in order.  Bound by memory: dy and pre
@@ -1455,15 +1561,35 @@ struct Eight {
 // taken (58 with the 16-bit type chosen at run time, 32 instructions).  Four
 // CTAs an SM with two rows in flight each; two CTAs with four rows took a
 // seventh longer.
+//
+// From an fp32 dy, dP may be written in two pieces (its value in 16 bits, and
+// what that leaves), for a product that is wanted in more than 16 bits.
 template <int ACT, bool F32, bool F16>
 __global__ void __launch_bounds__(kGradThreads, 4) k_act_grad(GradArgs p)
 {
     __shared__ float red[kGradGroups][kGradCols];
+    __shared__ uint32_t most;
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int c = blockIdx.x * kGradCols + lane * 8;
     const int left = min(8, p.N - c);
     pdl_wait();
     pdl_launch_dependents();
+    float scale = 1.0f;
+    if (F32 && F16 && p.maxima) {
+        if (threadIdx.x == 0)
+            most = 0;
+        __syncthreads();
+        static_assert(kMaxima == kGradThreads, "a maximum per thread");
+        const uint32_t m = __reduce_max_sync(0xffffffffu, p.maxima[threadIdx.x]);
+        if (lane == 0)
+            atomicMax(&most, m);
+        __syncthreads();
+        // (subnormal maxima count as 2^-126)
+        const int e = most ? min(13 - (max(int(most >> 23), 1) - 127), 126) : 0;
+        scale = pow2(e);
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+            *p.unscale = pow2(-e);
+    }
     const int64_t t0 = int64_t(blockIdx.y) * p.rows;
     const int64_t t1 = min(int64_t(p.T), t0 + p.rows);
     float s[8] = {};
@@ -1498,9 +1624,29 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_act_grad(GradArgs p)
                 for (int i = 0; i < 8; ++i)
                     s[i] += d[i];  // 0 past N
                 if (p.dp) {  // lddp is a multiple of 8: whole vectors, past N too
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (F32 && F16) {
+                            d[2 * i] *= scale;
+                            d[2 * i + 1] *= scale;
+                        }
+                        w[i] = pack16(d[2 * i], d[2 * i + 1], F16);
+                    }
                     *reinterpret_cast<uint4 *>(p.dp + r * p.lddp + c) =
-                        make_uint4(pack16(d[0], d[1], F16), pack16(d[2], d[3], F16),
-                                   pack16(d[4], d[5], F16), pack16(d[6], d[7], F16));
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                    if (F32 && p.dp2) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = unpack16(w[i], F16);
+                            // (0 beside an infinity, which is itself enough)
+                            const float a = d[2 * i] - f.x, b = d[2 * i + 1] - f.y;
+                            w[i] = pack16(fabsf(a) < INFINITY ? a : 0.0f,
+                                          fabsf(b) < INFINITY ? b : 0.0f, F16);
+                        }
+                        *reinterpret_cast<uint4 *>(p.dp2 + r * p.lddp + c) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
             }
         }
@@ -1638,12 +1784,17 @@ cudaError_t launch_clustered(const void *kern, unsigned grid, unsigned cluster, 
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
-// out[i][j] = sum_r X[i][r] Y[j][r], with a's epilogue fields.
+// out[i][j] = sum_r X[i][r] Y[j][r], with a's epilogue fields.  With a.two, X is
+// the sum of X and a matrix of the same shape at X2.
 struct Product {
     Operand X, Y;
     bool x_mn, y_mn;  // i (j) is contiguous, not r
     int rows, cols, R;
     LinArgs a;
+    const void *X2;
+
+    int steps() const { return (R + LK - 1) / LK << a.two; }  // of 64 r
+    Operand second() const { return {a.two ? X2 : X.p, X.rows, X.cols, X.ld}; }
 };
 
 // Dynamic shared memory of a launch of k_linear_pair whose tiles take
@@ -1700,7 +1851,7 @@ constexpr int kCutMaxBn = 160;
 
 bool is_cut(const Product &q)
 {
-    return (q.R + LK - 1) / LK > chain_steps(q.a.out_f32, q.a.f16);
+    return q.steps() > chain_steps(q.a.out_f32, q.a.f16);
 }
 
 double epi_cycles(int bn)
@@ -1711,7 +1862,7 @@ double epi_cycles(int bn)
 // A tile of one pair, unsplit, while others follow.
 double tile_cycles(const Product &q, int bn)
 {
-    return std::max(pair_step(bn, q.y_mn) * ((q.R + LK - 1) / LK), epi_cycles(bn));
+    return std::max(pair_step(bn, q.y_mn) * q.steps(), epi_cycles(bn));
 }
 
 // f32: an output of the launch is; cut: a sum of the launch is, into chains.
@@ -1720,7 +1871,7 @@ Tiling choose_tiling(const Product &q, int sms, bool f32, bool cut)
     Tiling t{false, 0, 1, 0, 0.0, 0.0};
     if (q.rows <= 128)
         return t;
-    const int nk = (q.R + LK - 1) / LK, pairs = std::max(1, sms / 2);
+    const int nk = q.steps(), pairs = std::max(1, sms / 2);
     for (int bn = f32 || cut ? kCutMaxBn : 256; bn >= 64; bn -= 32) {
         if (pair_smem(pair_sub_bytes(bn, q.y_mn), bn, 1, f32) > kPairSmem)
             continue;
@@ -1815,7 +1966,7 @@ Product columns_of(const Product &q, int64_t from, int64_t cols)
 // k_linear's arguments and shared memory for a product, and its CTAs.
 LinArgs small_args(const Product &q, int sms, int64_t &ctas, size_t &smem)
 {
-    const int nk = (q.R + LK - 1) / LK;
+    const int nk = q.steps();
     LinArgs a = q.a;
     a.M = q.cols, a.N = q.rows, a.R = q.R;
     a.a_mn = q.y_mn, a.b_mn = q.x_mn;
@@ -1852,16 +2003,24 @@ cudaError_t launch_small(const Product &q, cudaStream_t s)
     LinArgs a = small_args(q, device_sm_count(), ctas, smem);
     if (ctas > INT_MAX)
         return cudaErrorInvalidValue;
-    CUtensorMap ma, mb;
-    cudaError_t e = lin_map(&ma, q.Y, q.y_mn ? LK : LM, a.f16);
+    LinMaps<false> maps;
+    LinMaps<true> more;
+    cudaError_t e = lin_map(&maps.a, q.Y, q.y_mn ? LK : LM, a.f16);
     if (e == cudaSuccess)
-        e = lin_map(&mb, q.X, q.x_mn ? LK : a.bn, a.f16);
-    const void *kern = reinterpret_cast<const void *>(k_linear);
+        e = lin_map(&maps.b, q.X, q.x_mn ? LK : a.bn, a.f16);
+    const bool extra = a.two || a.mul;
+    const void *kern = extra ? reinterpret_cast<const void *>(k_linear<true>)
+                             : reinterpret_cast<const void *>(k_linear<false>);
+    if (extra) {
+        more.a = maps.a, more.b = more.b2 = maps.b;
+        if (e == cudaSuccess && a.two)
+            e = lin_map(&more.b2, q.second(), q.x_mn ? LK : a.bn, a.f16);
+    }
     if (e == cudaSuccess)
-        e = ensure_smem_limit(kern, kSlotLinear, kSmallSmem);
+        e = ensure_smem_limit(kern, extra ? kSlotLinearExtra : kSlotLinear, kSmallSmem);
     if (e != cudaSuccess)
         return e;
-    void *args[] = {&ma, &mb, &a};
+    void *args[] = {extra ? static_cast<void *>(&more) : &maps, &a};
     return launch_clustered(kern, unsigned(ctas), unsigned(a.split), kLinThreads, smem, s, args);
 }
 
@@ -1876,8 +2035,8 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
                          cudaStream_t s)
 {
     const int sms = device_sm_count(), pairs = std::max(1, sms / 2);
-    PairArgs g = {};
-    bool f32 = false;
+    PairArgsExtra g = {};  // (a launch without EXTRA takes its first part)
+    bool f32 = false, extra = false;
     g.part = sums.part, g.db = sums.db, g.chunks = sums.chunks, g.db_n = sums.n;
     for (int i = 0; i < count; ++i) {
         if (t[i].tiles > INT_MAX / 2)
@@ -1892,6 +2051,7 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
                   (a.residual ? kEpiResidual : 0) | (a.out_f32 ? kEpiF32 : 0) |
                   (a.f16 ? kEpiF16 : 0) | (a.vec_out ? kEpiVecOut : 0) |
                   (a.vec_res ? kEpiVecRes : 0) | (a.vec_pre ? kEpiVecPre : 0) |
+                  (a.mul ? kEpiMul : 0) |
                   uint32_t(a.act) * kEpiAct;
         a.chain = chain_steps(a.out_f32, a.f16);
         g.cut |= a.split == 1 && is_cut(q[i]);
@@ -1899,7 +2059,10 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         g.bn = std::max(g.bn, a.bn);
         g.sub_bytes = std::max(g.sub_bytes, pair_sub_bytes(a.bn, a.b_mn));
         f32 |= a.out_f32 != 0;
+        extra |= a.two || a.mul;
         cudaError_t e = lin_map(&g.a[i], q[i].X, q[i].x_mn ? LK : LM, a.f16);
+        if (e == cudaSuccess && a.two)
+            e = lin_map(&g.a2[i], q[i].second(), q[i].x_mn ? LK : LM, a.f16);
         if (e == cudaSuccess)
             e = lin_map(&g.b[i], q[i].Y, q[i].y_mn ? LK : a.bn / 2, a.f16);
         // outputs by TMA where their rows are aligned (a split tile's are not)
@@ -1920,13 +2083,14 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
     }
     const size_t smem = pair_smem(g.sub_bytes, g.bn, split, f32);
     const bool wide = g.bn >= kPairWide;
-    const void *kern = wide ? reinterpret_cast<const void *>(k_linear_pair<1>)
-                            : reinterpret_cast<const void *>(k_linear_pair<2>);
-    const cudaError_t e = ensure_smem_limit(
-        kern, wide ? kSlotLinearPairWide : kSlotLinearPair, kPairSmem);
+    const void *kern = extra ? wide ? reinterpret_cast<const void *>(k_linear_pair<1, true>)
+                                    : reinterpret_cast<const void *>(k_linear_pair<2, true>)
+                       : wide ? reinterpret_cast<const void *>(k_linear_pair<1, false>)
+                              : reinterpret_cast<const void *>(k_linear_pair<2, false>);
+    const cudaError_t e = ensure_smem_limit(kern, kSlotLinearPair + 2 * extra + wide, kPairSmem);
     if (e != cudaSuccess)
         return e;
-    void *args[] = {&g};
+    void *args[] = {extra ? static_cast<void *>(&g) : static_cast<PairArgs *>(&g)};
     return launch_clustered(kern, unsigned(clusters * 2 * split), unsigned(2 * split), kPairThreads,
                             smem, s, args);
 }
@@ -1943,7 +2107,7 @@ struct Launch {
 // first): their number, at most two.
 int plan_launches(Product *q, int count, int sms, Launch (&out)[2])
 {
-    if (count == 2 && q[1].R > q[0].R)
+    if (count == 2 && q[1].steps() > q[0].steps())
         std::swap(q[0], q[1]);
     Tiling t[2] = {};
     bool f32 = false, cut = false;
@@ -2056,13 +2220,37 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
                : MOE_ERR_CUDA;
 }
 
+namespace moe {
+namespace {
+
+// What moe_linear_grad's workspace holds: dP in 16 bits, the partial column
+// sums, the maxima and the factor of a scaled dP, and dP's second piece.
+struct GradLayout {
+    size_t part, maxima, unscale, dp2, total;
+
+    GradLayout(int T, int N, bool two)
+    {
+        const size_t ldp = (size_t(N) + 7) & ~size_t(7), dp = align256(size_t(T) * ldp * 2);
+        part = dp;
+        maxima = part + align256(size_t(kGradMaxChunks) * N * sizeof(float));
+        unscale = maxima + align256(kMaxima * sizeof(uint32_t));
+        dp2 = unscale + 256;
+        total = dp2 + (two ? dp : 0);
+    }
+};
+
+}  // namespace
+}  // namespace moe
+
 extern "C" size_t moe_linear_grad_workspace_bytes(int T, int N)
 {
-    if (!moe::sizes_ok(T, 8, N, MOE_ACT_NONE))
-        return 0;
-    const size_t ldp = (size_t(N) + 7) & ~size_t(7);
-    return moe::align256(size_t(T) * ldp * 2) +
-           moe::align256(size_t(moe::kGradMaxChunks) * N * sizeof(float));
+    return moe::sizes_ok(T, 8, N, MOE_ACT_NONE) ? moe::GradLayout(T, N, true).total : 0;
+}
+
+extern "C" size_t moe_linear_grad_workspace_bytes_for(int T, int N, int dy_dtype, int dw_dtype)
+{
+    const bool two = dy_dtype == MOE_DT_F32 && dw_dtype == MOE_DT_F32;
+    return moe::sizes_ok(T, 8, N, MOE_ACT_NONE) ? moe::GradLayout(T, N, two).total : 0;
 }
 
 extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const void *pre,
@@ -2079,7 +2267,9 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     if (!ws || (dx && !W) ||
         (T > 0 && (!dy || (dW && !x) || (act != MOE_ACT_NONE && !pre))))
         return MOE_ERR_NULL;
-    if (ws_bytes < moe_linear_grad_workspace_bytes(T, N))
+    const bool two = dW && dy_dtype == MOE_DT_F32 && dw_dtype == MOE_DT_F32;
+    const GradLayout layout(T, N, two);
+    if (ws_bytes < layout.total)
         return MOE_ERR_WORKSPACE;
     const int dysize = dy_dtype == MOE_DT_F32 ? 4 : 2, dwsize = dw_dtype == MOE_DT_F32 ? 4 : 2;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(pre, 2) || !aligned(dy, dysize) ||
@@ -2095,10 +2285,13 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
         return MOE_OK;
     }
     const int64_t ldp = (int64_t(N) + 7) & ~int64_t(7);
+    uint8_t *const base = static_cast<uint8_t *>(ws);
     uint16_t *dp = static_cast<uint16_t *>(ws);
-    float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) +
-                                            align256(size_t(T) * ldp * 2));
+    uint16_t *dp2 = two ? reinterpret_cast<uint16_t *>(base + layout.dp2) : nullptr;
+    float *part = reinterpret_cast<float *>(base + layout.part);
     const bool products = dx || dW;
+    const bool scaled = products && dtype == MOE_DT_F16 && dy_dtype == MOE_DT_F32;
+    float *unscale = scaled ? reinterpret_cast<float *>(base + layout.unscale) : nullptr;
     // dy is the products' operand as it is
     const bool direct =
         act == MOE_ACT_NONE && dy_dtype == dtype && lddy % 8 == 0 && aligned(dy, 16);
@@ -2107,7 +2300,16 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
         GradArgs g = {};
         g.dy = dy, g.pre = pre;
         g.dp = products && !direct ? dp : nullptr;
+        g.dp2 = dp2;
         g.part = db ? part : nullptr;
+        if (scaled) {
+            uint32_t *maxima = reinterpret_cast<uint32_t *>(base + layout.maxima);
+            if (launch_pdl(k_dy_max, dim3(kMaxima), dim3(kMaxThreads), 0, s,
+                           static_cast<const float *>(dy), lddy, T, N, vec16(dy, lddy, 4),
+                           maxima) != cudaSuccess)
+                return MOE_ERR_CUDA;
+            g.maxima = maxima, g.unscale = unscale;
+        }
         g.lddy = lddy, g.lddp = ldp;
         g.T = T, g.N = N;
         g.vec = vec16(dy, lddy, dysize) && (act == MOE_ACT_NONE || vec16(pre, N, 2));
@@ -2126,6 +2328,7 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
     a.status = status;
     a.f16 = dtype == MOE_DT_F16;
     a.act = MOE_ACT_NONE;
+    a.mul = unscale;
     a.ldo = K;
     Product q[2];
     int count = 0;
@@ -2138,7 +2341,8 @@ extern "C" int moe_linear_grad(const void *x, int64_t ldx, const void *W, const 
         a.out = dW;
         a.out_f32 = dw_dtype == MOE_DT_F32;
         a.vec_out = vec16(dW, K, dwsize);
-        q[count++] = Product{P, {x, T, K, ldx}, true, true, N, K, T, a};
+        a.two = two;
+        q[count++] = Product{P, {x, T, K, ldx}, true, true, N, K, T, a, dp2};
     }
     return launch_products(q, count, ColSums{part, db, chunks, N}, s) == cudaSuccess
                ? MOE_OK
@@ -2151,8 +2355,10 @@ extern "C" int moe_selftest_linear_plan(int T, int K, int N, int what, int f32, 
     using namespace moe;
     if (!plan)
         return MOE_ERR_NULL;
+    const bool two = what & 8;
+    what &= ~8;
     if (!sizes_ok(T, K, N, MOE_ACT_NONE) || T == 0 || what < 1 || what > 6 || what == 3 ||
-        what == 5 || sms < 2)
+        what == 5 || sms < 2 || (two && (!f32 || !(what & 4))))
         return MOE_ERR_SHAPE;
     Product q[2];
     int count = 0;
@@ -2160,9 +2366,10 @@ extern "C" int moe_selftest_linear_plan(int T, int K, int N, int what, int f32, 
     a.out_f32 = f32 != 0;
     if (what & 1)
         q[count++] = Product{{nullptr, T, K, K}, {nullptr, N, K, K}, false, false, T, N, K, a};
+    a.two = two;
     if (what & 4)
         q[count++] = Product{{nullptr, T, N, N}, {nullptr, T, K, K}, true, true, N, K, T, a};
-    a.out_f32 = 0;
+    a.two = a.out_f32 = 0;
     if (what & 2)
         q[count++] = Product{{nullptr, T, N, N}, {nullptr, N, K, K}, false, true, T, K, N, a};
     Launch l[2];

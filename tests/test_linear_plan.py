@@ -32,3 +32,13 @@ def test_every_launch_fits_shared_memory(lib, what, f32):
             p = B.selftest_linear_plan(T, K, N, what, f32, sms)
             assert 1 <= p["launches"] <= 2
             assert p["smem"] + 1024 <= SMEM, (T, K, N, sms, p)
+
+
+@pytest.mark.parametrize("what", [("dW", "dy fp32"), ("dx", "dW", "dy fp32")])
+def test_every_launch_of_a_dw_from_two_pieces_fits(lib, what):
+    rng = random.Random(8)
+    span = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    sizes = SIZES + [(span(1, 200000), 8 * span(1, 4096), span(1, 40000)) for _ in range(4000)]
+    for T, K, N in sizes:
+        p = B.selftest_linear_plan(T, K, N, what, True, 152)
+        assert 1 <= p["launches"] <= 2 and p["smem"] + 1024 <= SMEM, (T, K, N, p)
