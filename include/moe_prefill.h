@@ -37,9 +37,10 @@
  *  - Every call is asynchronous on `stream` (NULL = the legacy default
  *    stream) and returns once its kernels are enqueued.  The library never
  *    allocates device memory, never synchronises the host (except
- *    moe_read_status, on request) and keeps no per-call state (the one
- *    exception: moe_prefill_forward_host creates two copy streams per device
- *    on first use and a few events per call).  Kernels are chained with
+ *    moe_read_status and moe_take_status, on request) and keeps no per-call
+ *    state (the exceptions: moe_prefill_forward_host creates two copy streams
+ *    per device on first use and a few events per call, and each device has
+ *    the status word that moe_take_status reads).  Kernels are chained with
  *    programmatic dependent launch.
  *  - Flat entry i = t*k + j is token t's slot j.  An expert id of -1 marks a
  *    skipped slot: it gets no row, pos = -1 and adds nothing to y.
@@ -510,6 +511,14 @@ MOE_API int moe_prefill_forward_host(int n_chunks, const void *const *x_h,
 MOE_API int moe_read_status(const void *ws, moe_stream_t stream, uint32_t *status);
 
 /*
+ * moe_take_status -- the status bits of the current device's moe_linear and
+ * moe_linear_grad calls that had no status word and moe_route calls that had
+ * no workspace, on any stream, since they were last taken: copied to *status
+ * and cleared, synchronising `stream` (order it behind the calls asked about).
+ */
+MOE_API int moe_take_status(moe_stream_t stream, uint32_t *status);
+
+/*
  * moe_selftest_wait_limit -- failure-detection self-test of the GEMMs'
  * bounded waits.  Runs moe_ffn_gate_up on the given arguments with one
  * change: CTA `cta`'s first pipeline stage expects 16 bytes that never
@@ -535,7 +544,9 @@ MOE_API int moe_selftest_wait_limit(const void *xs, const void *Wg, const void *
  * in   residual  y_dtype [T, N], rows ldr elements apart, or NULL
  * out  pre       dtype [T, N] contiguous, or NULL
  * out  y         y_dtype [T, N], rows ldy elements apart
- * in   status    uint32* device word to OR MOE_STATUS_TIMEOUT into, or NULL
+ * in   status    uint32* device word to OR MOE_STATUS_TIMEOUT into (then tiles of
+ *                y are not written, or lack parts of their sums); NULL: the
+ *                device's own word, see moe_take_status
  * dtype is MOE_DT_BF16 or MOE_DT_F16, y_dtype that same type or MOE_DT_F32.
  * T >= 0, N >= 1 (any), K a positive multiple of 8; ldx >= K a multiple of 8;
  * ldr, ldy >= N; T, K, N <= 2^31 - 512.  x and W 16-byte aligned, the others aligned
@@ -612,7 +623,8 @@ MOE_API int moe_linear_grad(const void *x, int64_t ldx, const void *W, const voi
  * out  prob    fp32 [E] or NULL;  loss fp32 [2] or NULL
  * ws           moe_route_workspace_bytes(T, E) bytes, 256-byte aligned; its
  *              status word is set by every call (moe_read_status).  NULL, if
- *              counts, prob and loss are: then no status is kept
+ *              counts, prob and loss are: then the bits go to the device's own
+ *              word, see moe_take_status
  * T >= 0, 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E, MOE_MAX_TOPK), ld >= E,
  * T*k < 2^31.  All sums in a fixed order: results are deterministic.
  */
@@ -640,6 +652,15 @@ MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const ui
                            const int32_t *ids, const int32_t *counts, const float *dw,
                            const float *dloss, int T, int E, int k, int score, int norm,
                            float scale, void *dlogits, int64_t ldd, moe_stream_t stream);
+
+/*
+ * moe_selftest_linear_wait_limit -- the same of moe_linear (bf16, contiguous,
+ * no epilogue): the first stage of CTA `cta` (of more than 128 tokens: an even
+ * one) expects 16 bytes that never arrive.  status may be NULL.  For tests only.
+ */
+MOE_API int moe_selftest_linear_wait_limit(const void *x, const void *W, int T, int K, int N,
+                                           void *y, uint32_t *status, int cta,
+                                           moe_stream_t stream);
 
 /*
  * moe_selftest_linear_plan -- the launches that moe_linear (what = 1) or the

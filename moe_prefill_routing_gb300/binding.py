@@ -127,6 +127,9 @@ _SIGS = {
                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                  C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_int64,
                                  C.c_void_p]),
+    "moe_take_status": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
+    "moe_selftest_linear_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
+                                                 C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
     "moe_selftest_linear_plan": (C.c_int, [C.c_int] * 6 + [C.POINTER(C.c_int64)]),
     "moe_read_status": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
     "moe_selftest_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
@@ -658,7 +661,8 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
     [T, N] of ``out_dtype`` (x's type by default, or float32); the rows of x,
     residual and y may lie further apart than their length.  ``pre`` (an
     output, x's type, [T, N]) receives x W^T + bias for ``linear_grad``.
-    ``residual`` may be ``y``."""
+    ``residual`` may be ``y``.  ``status``: an int32 word to OR status bits into
+    (by default the device's own, see ``take_status``)."""
     T, K = x.shape
     N = W.shape[0]
     dt = x.dtype
@@ -772,7 +776,7 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
     ``layer_forward`` take) and, with ``stats``, counts int32 [E+1] (the
     last: tokens that take part), prob fp32 [E] and loss fp32 [2] (balance,
     z), and the workspace ``ws`` (status word at byte 0; without ``stats``
-    only if one is passed in, and no status is kept otherwise).  bias fp32 [E] is
+    only if one is passed in, and the bits go to ``take_status`` otherwise).  bias fp32 [E] is
     added to the scores for the choice alone; mask [T] (bool or uint8) is 0
     for padding.  ``out`` may hold some of the outputs."""
     T, E = logits.shape
@@ -854,6 +858,19 @@ def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: 
     return dlogits
 
 
+def selftest_linear_wait_limit(x, W, cta: int = 0, status=None):
+    """``linear(x, W)`` (bf16) with CTA `cta` made to wait for bytes that never
+    come: it stops after about 2 s and reports STATUS_TIMEOUT."""
+    T, K = x.shape
+    N = W.shape[0]
+    y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    with torch.cuda.device(x.device):
+        rc = lib().moe_selftest_linear_wait_limit(_ptr(x), _ptr(W), T, K, N, _ptr(y), _ptr(status),
+                                                  cta, _stream(x.device))
+    _check("moe_selftest_linear_wait_limit", rc)
+    return y
+
+
 def selftest_linear_plan(T: int, K: int, N: int, what=("y",), f32: bool = False,
                          sms: int = 152) -> dict:
     """The launches of ``linear`` (what = ("y",)) or of the products of
@@ -886,6 +903,17 @@ def read_status(ws) -> int:
     with torch.cuda.device(ws.device):
         rc = lib().moe_read_status(_ptr(ws), _stream(ws.device), C.byref(v))
     _check("moe_read_status", rc)
+    return int(v.value)
+
+
+def take_status(device=None) -> int:
+    """Status bits of the device's ``linear`` and ``linear_grad`` calls without
+    ``status`` and ``route`` calls without a workspace since the last call of
+    this (on the current stream, which it synchronises)."""
+    v = C.c_uint32(0)
+    with torch.cuda.device(device):
+        rc = lib().moe_take_status(_stream(), C.byref(v))
+    _check("moe_take_status", rc)
     return int(v.value)
 
 

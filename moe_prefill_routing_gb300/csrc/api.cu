@@ -17,6 +17,15 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 std::atomic<bool> g_smem_set[kMaxDevices][kSlotCount];
 
+__device__ uint32_t g_taken;
+
+// One exchange per word: a bit set meanwhile by another stream's kernel is in
+// this answer or in the next.
+__global__ void k_take_status(uint32_t *a, uint32_t *b)
+{
+    g_taken = atomicExch(a, 0u) | atomicExch(b, 0u);
+}
+
 }  // namespace
 
 int device_sm_count()
@@ -592,6 +601,24 @@ int moe_selftest_wait_limit(const void *xs, const void *Wg, const void *Wu,
         return MOE_ERR_SHAPE;
     return cuda_rc(moe::launch_ffn_gate_up(xs, Wg, Wu, offsets, E, d, f, cap, H, status,
                                            as_stream(stream), cta));
+}
+
+int moe_take_status(moe_stream_t stream, uint32_t *status)
+{
+    if (!status)
+        return MOE_ERR_NULL;
+    uint32_t *a = moe::linear_status_word(), *b = moe::route_status_word();
+    void *out = nullptr;
+    if (!a || !b || cudaGetSymbolAddress(&out, moe::g_taken) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    static std::mutex one_at_a_time;  // g_taken
+    const std::lock_guard<std::mutex> lock(one_at_a_time);
+    cudaStream_t s = as_stream(stream);
+    moe::k_take_status<<<1, 1, 0, s>>>(a, b);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(status, out, sizeof(uint32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return cuda_rc(cudaStreamSynchronize(s));
 }
 
 int moe_read_status(const void *ws, moe_stream_t stream, uint32_t *status)

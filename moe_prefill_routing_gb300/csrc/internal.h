@@ -132,6 +132,11 @@ int device_sm_count();
 // The driver's tensor-map encoder (null if the driver lacks it).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// The current device's words for status bits of calls that have no status word
+// of their own (null if CUDA fails).
+uint32_t *linear_status_word();
+uint32_t *route_status_word();
+
 // Raise a kernel's dynamic shared-memory limit once per device.
 cudaError_t ensure_smem_limit(const void *kernel, int slot, size_t bytes);
 

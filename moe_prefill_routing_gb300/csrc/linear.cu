@@ -64,6 +64,7 @@ struct LinArgs {
     int a_mn, b_mn;  // the operand's m (n) is contiguous, not its r
     int bn, stages, split, n_mt;
     int two;         // EXTRA kernels: X = X1 + X2, each summed over all r
+    int stall;       // EXTRA kernels, self-test: CTA stall - 1's first stage waits for 16 bytes
     int chain;       // steps of 64 r that one accumulator sums, see chain_steps
     int f16, out_f32, act;
     int vec_out, vec_res, vec_pre;  // rows and base are 16-byte aligned
@@ -85,6 +86,14 @@ enum EpiFlags : uint32_t {
     kEpiMul = 256,
     kEpiAct = 512,  // times the activation
 };
+
+// Status bits of calls without a status word, see moe_take_status.
+__device__ uint32_t g_status;
+
+__device__ __noinline__ void report_timeout(uint32_t *status)
+{
+    atomicOr(status ? status : &g_status, MOE_STATUS_TIMEOUT);
+}
 
 struct LinCtrl {
     uint64_t full[kLinMaxStages];
@@ -504,7 +513,8 @@ __global__ void __launch_bounds__(kLinThreads)
                 break;
             if (one) {
                 uint64_t *fb = &ctl.full[stage];
-                mbar_arrive_expect_tx(fb, stage_bytes);
+                const bool stall = EXTRA && p.stall == int(blockIdx.x) + 1 && kb == kb0;
+                mbar_arrive_expect_tx(fb, stage_bytes + (stall ? 16u : 0u));
                 uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
                 const CUtensorMap *ma = &maps.a, *mb = &maps.b;
                 int k0 = kb * LK;
@@ -532,10 +542,12 @@ __global__ void __launch_bounds__(kLinThreads)
                 phase ^= 1u;
             }
         }
-        if (!ok)  // stopped: let the copies already issued land
+        if (!ok) {  // stopped: let the copies already issued land
+            report_timeout(p.status);
             for (int s = 0; s < S; ++s)
                 if ((issued >> s) & 1u)
                     lin_drain(&ctl.full[s], (issued_par >> s) & 1u);
+        }
     } else if (warp == 1) {
         // the whole warp walks the loop and one lane issues, so that
         // descriptors and addresses stay warp-uniform
@@ -552,15 +564,18 @@ __global__ void __launch_bounds__(kLinThreads)
         const bool one = elect_one();
         uint32_t d = tmem_base, aphase = 0;
         int left = p.chain, buf = 0;
+        bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb) {
             if (turns && left == p.chain) {
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag)))
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
+                if (!ok)
                     break;
                 tc_fence_after_sync();
                 d = tmem_base + uint32_t(buf * bn);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag)))
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+            if (!ok)
                 break;
             tc_fence_after_sync();
             if (one) {
@@ -591,6 +606,8 @@ __global__ void __launch_bounds__(kLinThreads)
                 phase ^= 1u;
             }
         }
+        if (!ok)
+            report_timeout(p.status);
         if (one)
             tc_commit(&ctl.done);  // arrives once every MMA issued here has completed
     }
@@ -615,8 +632,10 @@ __global__ void __launch_bounds__(kLinThreads)
         const uint32_t lanes = tmem_base + (uint32_t(warp & 3) << 21);
         for (int i = 0; turns && i < chains; ++i) {
             if (!__all_sync(0xffffffffu,
-                            mbar_wait(&ctl.acc_full[i & 1], (i >> 1) & 1, abort_flag)))
+                            mbar_wait(&ctl.acc_full[i & 1], (i >> 1) & 1, abort_flag))) {
+                report_timeout(p.status);
                 break;
+            }
             tc_fence_after_sync();
             add_small_chain(lanes + uint32_t((i & 1) * bn), lanes + uint32_t(2 * bn), bn, i > 0);
             tc_fence_before_sync();
@@ -626,8 +645,10 @@ __global__ void __launch_bounds__(kLinThreads)
         }
         __syncwarp();
         done = mbar_wait(&ctl.done, 0, abort_flag);
-        if (!done)  // stopped: the MMAs in flight still read shared and write tensor memory
+        if (!done) {  // stopped: the MMAs in flight still read shared and write tensor memory
+            report_timeout(p.status);
             lin_drain(&ctl.done, 0);
+        }
         done = __all_sync(0xffffffffu, done) && kb1 > kb0;
     }
     __syncwarp();
@@ -707,8 +728,6 @@ __global__ void __launch_bounds__(kLinThreads)
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, tmem_cols);
     }
-    if (threadIdx.x == 0 && ctl.abort_flag && p.status)
-        atomicOr(p.status, MOE_STATUS_TIMEOUT);
 }
 
 // ---- large products: pairs of CTAs ---------------------------------------------
@@ -1103,8 +1122,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     break;
                 if (one) {
                     const int subs = min(SUB, w.nk1 - kb);
-                    if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
-                        mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(subs) * tx);
+                    if (rank == 0) {  // both CTAs' bytes complete on the even CTA's barrier
+                        const bool stall = EXTRA && p.stall && p.stall - 1 == int(blockIdx.x) &&
+                                           i == 0 && kb == w.nk0;
+                        mbar_arrive_expect_tx(&ctl.full[stage],
+                                              uint32_t(subs) * tx + (stall ? 16u : 0u));
+                    }
                     const uint32_t fb = dsmem_addr(&ctl.full[stage], lead);
 #pragma unroll
                     for (int h = 0; h < SUB; ++h) {
@@ -1425,8 +1448,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     }
     __syncthreads();
-    if (threadIdx.x == 0 && ctl.abort_flag && g.p[0].status)
-        atomicOr(g.p[0].status, MOE_STATUS_TIMEOUT);
+    if (threadIdx.x == 0 && ctl.abort_flag)
+        report_timeout(g.p[0].status);
+    __syncwarp();
     cluster_sync();  // the CTAs are done with each other's shared memory and barriers
     if (warp == 1) {
         tc_fence_after_sync();
@@ -2008,7 +2032,7 @@ cudaError_t launch_small(const Product &q, cudaStream_t s)
     cudaError_t e = lin_map(&maps.a, q.Y, q.y_mn ? LK : LM, a.f16);
     if (e == cudaSuccess)
         e = lin_map(&maps.b, q.X, q.x_mn ? LK : a.bn, a.f16);
-    const bool extra = a.two || a.mul;
+    const bool extra = a.two || a.mul || a.stall;
     const void *kern = extra ? reinterpret_cast<const void *>(k_linear<true>)
                              : reinterpret_cast<const void *>(k_linear<false>);
     if (extra) {
@@ -2059,7 +2083,7 @@ cudaError_t launch_pairs(const Product *q, const Tiling *t, int count, const Col
         g.bn = std::max(g.bn, a.bn);
         g.sub_bytes = std::max(g.sub_bytes, pair_sub_bytes(a.bn, a.b_mn));
         f32 |= a.out_f32 != 0;
-        extra |= a.two || a.mul;
+        extra |= a.two || a.mul || a.stall;
         cudaError_t e = lin_map(&g.a[i], q[i].X, q[i].x_mn ? LK : LM, a.f16);
         if (e == cudaSuccess && a.two)
             e = lin_map(&g.a2[i], q[i].second(), q[i].x_mn ? LK : LM, a.f16);
@@ -2186,12 +2210,20 @@ inline bool is16(int dtype)
 }  // namespace
 }  // namespace moe
 
-extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float *bias,
-                          const void *residual, int64_t ldr, int dtype, int act, int T, int K,
-                          int N, void *pre, void *y, int64_t ldy, int y_dtype, uint32_t *status,
-                          moe_stream_t stream)
+namespace moe {
+
+uint32_t *linear_status_word()
 {
-    using namespace moe;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? static_cast<uint32_t *>(p) : nullptr;
+}
+
+namespace {
+
+int linear(const void *x, int64_t ldx, const void *W, const float *bias, const void *residual,
+           int64_t ldr, int dtype, int act, int T, int K, int N, void *pre, void *y, int64_t ldy,
+           int y_dtype, uint32_t *status, int stall, moe_stream_t stream)
+{
     if (!is16(dtype) || (y_dtype != dtype && y_dtype != MOE_DT_F32))
         return MOE_ERR_DTYPE;
     if (!sizes_ok(T, K, N, act) || ldx < K || ldx % 8 != 0 || ldy < N || (residual && ldr < N))
@@ -2210,6 +2242,7 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
     a.pre = pre;
     a.out = y;
     a.status = status;
+    a.stall = stall;
     a.ldr = ldr, a.ldo = ldy, a.ldp = N;
     a.f16 = dtype == MOE_DT_F16, a.out_f32 = y_dtype == MOE_DT_F32, a.act = act;
     a.vec_out = vec16(y, ldy, ysize), a.vec_res = vec16(residual, ldr, ysize);
@@ -2218,6 +2251,28 @@ extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float
     return launch_products(&q, 1, ColSums{}, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_linear(const void *x, int64_t ldx, const void *W, const float *bias,
+                          const void *residual, int64_t ldr, int dtype, int act, int T, int K,
+                          int N, void *pre, void *y, int64_t ldy, int y_dtype, uint32_t *status,
+                          moe_stream_t stream)
+{
+    return moe::linear(x, ldx, W, bias, residual, ldr, dtype, act, T, K, N, pre, y, ldy, y_dtype,
+                       status, 0, stream);
+}
+
+extern "C" int moe_selftest_linear_wait_limit(const void *x, const void *W, int T, int K, int N,
+                                              void *y, uint32_t *status, int cta,
+                                              moe_stream_t stream)
+{
+    if (cta < 0 || cta == INT_MAX)
+        return MOE_ERR_SHAPE;
+    return moe::linear(x, K, W, nullptr, nullptr, 0, MOE_DT_BF16, MOE_ACT_NONE, T, K, N, nullptr, y,
+                       N, MOE_DT_BF16, status, cta + 1, stream);
 }
 
 namespace moe {

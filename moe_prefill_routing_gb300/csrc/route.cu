@@ -21,6 +21,9 @@ constexpr int kFinalCtas = 8;       // one cluster
 constexpr int kFinalThreads = 512;
 constexpr uint32_t kTaken = 0;  // key of an expert already chosen
 
+// Status bits of calls without a workspace, see moe_take_status.
+__device__ uint32_t g_status;
+
 // CTAs that an SM holds at once, by registers; the grid is as many
 template <int V>
 constexpr int kRouteResident = V >= 16 ? 1 : 2;
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kRouteThreads, kRouteResident<V>) k_route(cons
     }
 
     if (bad)
-        atomicOr(&s_flags, MOE_STATUS_BAD_LOGIT);
+        atomicOr(p.status ? &s_flags : &g_status, MOE_STATUS_BAD_LOGIT);
     if (lane == 0) {
         s_live[g] = live;
         s_z[g] = zsum;
@@ -528,6 +531,13 @@ inline size_t part_rows(int T)
 }
 
 }  // namespace
+
+uint32_t *route_status_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? static_cast<uint32_t *>(p) : nullptr;
+}
+
 }  // namespace moe
 
 extern "C" size_t moe_route_workspace_bytes(int T, int E)

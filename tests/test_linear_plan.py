@@ -42,3 +42,17 @@ def test_every_launch_of_a_dw_from_two_pieces_fits(lib, what):
     for T, K, N in sizes:
         p = B.selftest_linear_plan(T, K, N, what, True, 152)
         assert 1 <= p["launches"] <= 2 and p["smem"] + 1024 <= SMEM, (T, K, N, p)
+
+
+def test_status_calls_refuse(lib):
+    fake = 0x10000
+    assert lib.moe_take_status(None, None) == B.MOE_ERR_NULL
+    assert lib.moe_selftest_linear_wait_limit(fake, fake, 4, 64, 8, fake, None, -1, None) == (
+        B.MOE_ERR_SHAPE)
+    assert lib.moe_selftest_linear_wait_limit(fake, fake, 4, 60, 8, fake, None, 0, None) == (
+        B.MOE_ERR_SHAPE)
+    assert lib.moe_selftest_linear_plan(4, 64, 8, 1, 0, 152, None) == B.MOE_ERR_NULL
+    for what in (0, 3, 5, 7, 9, 16):
+        with pytest.raises(B.MoeError):
+            B._check("plan", lib.moe_selftest_linear_plan(4, 64, 8, what, 1, 152,
+                                                          (B.C.c_int64 * 3)()))
