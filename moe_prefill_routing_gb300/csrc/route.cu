@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p
     const int col = threadIdx.x % cols, row = threadIdx.x / cols;
     if (threadIdx.x == 0)
         s_flags = 0;
+    __syncwarp();  // the cluster's barriers are for whole warps
     cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
@@ -501,9 +502,11 @@ __global__ void __launch_bounds__(kFinalThreads) k_route_final(const RouteArgs p
         __syncthreads();
     }
     dot = cta_sum<kFinalThreads / 32>(dot, red_f);
+    __syncwarp();
     cluster_wait();  // every CTA has started, so its shared memory is there
     if (threadIdx.x == 0)
         dsmem_st(dsmem_addr(&s_dots[rank], 0), __float_as_int(dot));
+    __syncwarp();
     cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
         *p.status = s_flags;
