@@ -50,7 +50,10 @@ class MoeBlock:
         """One SGD step on Wr for balance * (balance loss) + z * (z loss) (and,
         with ``dw`` [T, k], the loss whose gradient with respect to the
         routing weights it is).  Returns (losses [2], dx): the losses before
-        the step and the gradient with respect to x."""
+        the step and the gradient with respect to x (0 where mask is)."""
+        if mask is not None:
+            # such a row may hold anything, and 0 times a NaN is one
+            x = torch.where(mask.bool()[:, None], x, 0.0)
         r = self.route(x, mask, stats=True)
         dloss = torch.tensor([balance, z], dtype=torch.float32, device=x.device)
         dlogits = B.route_grad(r["logits"], r["ids"], r["counts"], dw=dw, dloss=dloss, mask=mask,

@@ -1,0 +1,51 @@
+"""A training step of the block's router against the 64-bit gradient of its own
+logits, for both operand types and with the usual loss coefficients; what it
+does with padding rows, small steps and weights set in between; its status.
+
+Bounds.  dlogits are held to 1e-5 of the magnitudes they are sums of; an fp32
+dWr takes them in two 16-bit pieces (2^-16 of each at most) and sums in fp32
+(2^-20 of the magnitudes' sum)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import router as R
+
+from moe_prefill_routing_gb300 import binding as B
+from moe_prefill_routing_gb300.block import MoeBlock
+
+pytestmark = pytest.mark.gpu
+
+BF, F16 = torch.bfloat16, torch.float16
+
+
+def _rand(seed, *shape, amp=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return amp * torch.randn(*shape, generator=g)
+
+
+def _router(T, d, E, k, dtype, **kw):
+    x = (_rand(T, T, d) + 0.3).to("cuda", dtype)
+    return MoeBlock(None, _rand(E, E, d, amp=0.05).to("cuda", dtype), k, **kw), x
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_padding_rows_may_hold_anything(dtype):
+    T, d, E, k = 200, 128, 24, 3
+    mask = torch.ones(T, dtype=torch.bool, device="cuda")
+    mask[::7] = False
+    out = []
+    for fill in (0.0, float("nan"), float("inf"), 6e4):
+        block, x = _router(T, d, E, k, dtype)
+        x[~mask] = fill
+        keep = x.clone()
+        loss, dx = block.train_router(x, lr=1.0, mask=mask)
+        assert torch.equal(x.isnan(), keep.isnan()) and bool((dx[~mask] == 0).all())
+        out.append((loss, dx, block.Wr))
+    for o in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, out[0]))
+    assert bool(out[0][2].isfinite().all())
