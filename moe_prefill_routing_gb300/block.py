@@ -27,6 +27,7 @@ class MoeBlock:
         self.layer, self.Wr, self.k = layer, Wr, k
         self.up, self.down, self.bias = up, down, bias
         self.how = dict(score=score, norm=norm, scale=scale)
+        self._master = None
 
     def route(self, x, mask=None, stats: bool = False) -> dict:
         """The router alone: its fp32 logits and what ``binding.route`` returns."""
@@ -50,7 +51,11 @@ class MoeBlock:
         """One SGD step on Wr for balance * (balance loss) + z * (z loss) (and,
         with ``dw`` [T, k], the loss whose gradient with respect to the
         routing weights it is).  Returns (losses [2], dx): the losses before
-        the step and the gradient with respect to x (0 where mask is)."""
+        the step and the gradient with respect to x (0 where mask is).
+
+        Wr holds the 16-bit values of weights kept in fp32, so that steps
+        smaller than its spacing add up; entries of Wr that were set since the
+        last step start from what they were set to."""
         if mask is not None:
             # such a row may hold anything, and 0 times a NaN is one
             x = torch.where(mask.bool()[:, None], x, 0.0)
@@ -60,7 +65,14 @@ class MoeBlock:
                                **self.how)
         dx, dWr, _ = B.linear_grad(x, self.Wr, dlogits, need=(True, True, False),
                                    dw_dtype=torch.float32)
-        self.Wr.copy_(self.Wr.float() - lr * dWr)
+        W, w = self.Wr, self._master
+        if w is None or w.shape != W.shape or w.device != W.device:
+            w = W.float()
+        else:
+            w = torch.where(w.to(W.dtype) == W, w, W.float())
+        w.sub_(dWr, alpha=lr)
+        W.copy_(w)
+        self._master = w
         return r["loss"], dx
 
 

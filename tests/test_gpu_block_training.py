@@ -49,3 +49,32 @@ def test_padding_rows_may_hold_anything(dtype):
     for o in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(o, out[0]))
     assert bool(out[0][2].isfinite().all())
+
+
+def test_small_steps_add_up():
+    block, x = _router(400, 64, 16, 2, BF)
+    W0 = block.Wr.float()
+    block.train_router(x, lr=1.0)
+    step = (W0 - block._master).abs().max()  # the first step's largest entry
+    block, x = _router(400, 64, 16, 2, BF)
+    # steps of at most 1/64 of the least weights' spacing seen, a thousand of them
+    lr = float(2.0 ** -14 / 64 / step)
+    before = block.Wr.clone()
+    for _ in range(1000):
+        block.train_router(x, lr=lr)
+    moved = (block._master - W0).abs().max()
+    assert float(moved) > 5 * 2.0 ** -14
+    assert torch.equal(block.Wr, block._master.to(BF)) and not torch.equal(block.Wr, before)
+
+
+def test_weights_set_between_steps_count():
+    block, x = _router(100, 64, 16, 2, BF)
+    block.train_router(x, lr=0.3)
+    block.Wr[3:5] = 0.25                    # in place
+    want = block.Wr.clone()
+    block.train_router(x, lr=0.0)
+    assert torch.equal(block.Wr, want) and bool((block._master[3:5] == 0.25).all())
+    block.Wr = _rand(9, 20, 64).to("cuda", BF)  # another tensor
+    want = block.Wr.clone()
+    block.train_router(x, lr=0.0)
+    assert torch.equal(block.Wr, want) and tuple(block._master.shape) == (20, 64)
