@@ -47,11 +47,12 @@ class MoeBlock:
         return B.linear(h, self.down, residual=y.add_(x), y=y)
 
     def train_router(self, x, lr: float, balance: float = 1e-2, z: float = 1e-3, dw=None,
-                     mask=None):
+                     mask=None, grad_scale: float = 1.0):
         """One SGD step on Wr for balance * (balance loss) + z * (z loss) (and,
         with ``dw`` [T, k], the loss whose gradient with respect to the
         routing weights it is).  Returns (losses [2], dx): the losses before
-        the step and the gradient with respect to x (0 where mask is).
+        the step and the gradient with respect to x, times ``grad_scale`` (what
+        a 16-bit dx cannot hold otherwise; dx is 0 where mask is).
 
         Wr holds the 16-bit values of weights kept in fp32, so that steps
         smaller than its spacing add up; entries of Wr that were set since the
@@ -60,7 +61,11 @@ class MoeBlock:
             # such a row may hold anything, and 0 times a NaN is one
             x = torch.where(mask.bool()[:, None], x, 0.0)
         r = self.route(x, mask, stats=True)
-        dloss = torch.tensor([balance, z], dtype=torch.float32, device=x.device)
+        dloss = torch.empty(2, dtype=torch.float32, device=x.device)
+        dloss[0].fill_(balance * grad_scale)
+        dloss[1].fill_(z * grad_scale)
+        if dw is not None and grad_scale != 1.0:
+            dw = dw * grad_scale
         dlogits = B.route_grad(r["logits"], r["ids"], r["counts"], dw=dw, dloss=dloss, mask=mask,
                                **self.how)
         dx, dWr, _ = B.linear_grad(x, self.Wr, dlogits, need=(True, True, False),
@@ -70,7 +75,7 @@ class MoeBlock:
             w = W.float()
         else:
             w = torch.where(w.to(W.dtype) == W, w, W.float())
-        w.sub_(dWr, alpha=lr)
+        w.sub_(dWr, alpha=lr / grad_scale)
         W.copy_(w)
         self._master = w
         return r["loss"], dx

@@ -33,6 +33,44 @@ def _np(t):
     return t.detach().double().cpu().numpy()
 
 
+@pytest.mark.parametrize("T,d,E,k,dtype,kw", [
+    (300, 128, 32, 4, BF, {}), (300, 128, 32, 4, F16, dict(score="sigmoid", norm=False, scale=2.5)),
+    (1000, 264, 65, 6, F16, {}), (700, 72, 130, 8, BF, dict(score="sigmoid")),
+    (2048, 2560, 512, 10, BF, {}), (2048, 2560, 512, 10, F16, {})])
+def test_step_is_the_gradient(T, d, E, k, dtype, kw):
+    block, x = _router(T, d, E, k, dtype, **kw)
+    W0 = block.Wr.clone()
+    r = block.route(x, stats=True)
+    balance, z, lr, scale = 1e-2, 1e-3, 2.0 ** 10, 2.0 ** 12
+    dw = _rand(5, T, k, amp=1e-6)
+    loss, dx = block.train_router(x, lr=lr, dw=dw.cuda(), grad_scale=scale)
+    assert torch.equal(loss, r["loss"])
+    counts = r["counts"].cpu().numpy()
+    dl = R.route_grad(_np(r["logits"]), r["ids"].cpu().numpy(), counts, _np(dw),
+                      np.array([balance, z]), **block.how)
+    xd, Wd, n = _np(x), _np(W0), int(counts[E])
+    how = {**dict(scale=1.0), **kw}
+    mag = (how["scale"] * np.abs(_np(dw)).sum(1, keepdims=True)
+           + 2 * z * np.sqrt(float(loss[1]) + 100) / n
+           + balance * E * counts[:E].max() / (n * k) / n) * np.ones_like(dl)
+    off = 1e-5 * mag
+    dW = dl.T @ xd
+    got = (Wd - _np(block._master)) / lr
+    bound = (off + (2.0 ** -16 + 2.0 ** -20) * (np.abs(dl) + off)).T @ np.abs(xd)
+    bound += 2.0 ** -23 * (np.abs(Wd) + lr * np.abs(dW)) / lr  # the step itself, in fp32
+    err = np.abs(got - dW)
+    assert np.all(err <= bound), float(np.max(err / bound))
+    assert np.linalg.norm(err) < 1e-3 * np.linalg.norm(dW)
+    # Wr is those weights in 16 bits
+    assert torch.equal(block.Wr, block._master.to(dtype)) and not torch.equal(block.Wr, W0)
+    # dx: dlogits in one piece, half a unit of dx's type
+    half = torch.finfo(dtype).eps / 2
+    ref = scale * (dl @ Wd)
+    tol = scale * ((off + (half + 2.0 ** -20) * (np.abs(dl) + off)) @ np.abs(Wd))
+    small = torch.finfo(dtype).smallest_normal * half
+    assert np.all(np.abs(_np(dx) - ref) <= tol + half * (np.abs(ref) + tol) + small)
+
+
 @pytest.mark.parametrize("dtype", [BF, F16])
 def test_padding_rows_may_hold_anything(dtype):
     T, d, E, k = 200, 128, 24, 3
