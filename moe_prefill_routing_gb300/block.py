@@ -36,7 +36,19 @@ class MoeBlock:
         r["logits"] = logits
         return r
 
+    def status(self) -> int:
+        """Status bits (binding.STATUS_*) of the routed layer's last call and of
+        what the device's router and dense products reported since this was
+        last asked (binding.take_status); waits for the current stream."""
+        bits = B.take_status(self.Wr.device)
+        if self.layer is not None and self.layer._ws is not None:
+            bits |= B.read_status(self.layer._ws)
+        return bits
+
     def forward(self, x, mask=None):
+        """x [T, d] bf16 to [T, d]; rows with mask 0 are routed nowhere."""
+        if x.dtype != torch.bfloat16:
+            raise ValueError(f"x: the routed experts take bfloat16, got {x.dtype}")
         r = self.route(x, mask)
         y = self.layer.forward(x, r["ids"], r["w"])
         # the residual stream rides on the dense expert's down projection, or
@@ -102,6 +114,7 @@ def main():
             counts = block.route(x, stats=True)["counts"][:E]
             print(f"step {step:2d}: balance loss {float(loss[0]):.4f}  z loss {float(loss[1]):.3f}"
                   f"  tokens of the busiest expert {int(counts.max())} (mean {T * k // E})")
+    print("status bits", block.status())
 
 
 if __name__ == "__main__":

@@ -116,3 +116,18 @@ def test_weights_set_between_steps_count():
     want = block.Wr.clone()
     block.train_router(x, lr=0.0)
     assert torch.equal(block.Wr, want) and tuple(block._master.shape) == (20, 64)
+
+
+def test_status_and_types():
+    r = lambda *s: _rand(sum(s), *s, amp=0.05).to("cuda", BF)  # noqa: E731
+    block = MoeBlock(B.MoeLayer(r(16, 128, 64), r(16, 128, 64), r(16, 64, 128)), r(16, 128), 2,
+                     up=r(192, 128), down=r(128, 192))
+    x = r(40, 128)
+    block.status()
+    block.forward(x)
+    assert block.status() == 0
+    x[5, 7] = float("nan")
+    block.forward(x)
+    assert block.status() == B.STATUS_BAD_LOGIT and block.status() == 0
+    with pytest.raises(ValueError, match="bfloat16"):
+        block.forward(x.half())
