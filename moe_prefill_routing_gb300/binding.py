@@ -613,6 +613,7 @@ _16 = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _MASK = (torch.bool, torch.uint8)
+_WORD = (torch.int32, torch.uint32)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice  # of an initialised context: its tensors exist
 
@@ -647,6 +648,25 @@ def _ld(t, name: str, shape, dtypes, dev) -> int:
     if one != 1 and cols > 1:
         _refuse(t, name, shape, dtypes, dev)
     return step if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _status(t, dev):
+    """Address of a caller's status word, or None."""
+    if t is None:
+        return None
+    if t.dtype not in _WORD or t.numel() == 0 or t.device != dev:
+        raise ValueError(f"status: expected a 32-bit integer on {dev}, got {t.numel()} of "
+                         f"{t.dtype} on {t.device}")
+    return _ptr(t)
+
+
+def _ws(t, dev):
+    """Address of a caller's workspace and its bytes; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.device != dev:
+        raise ValueError(f"ws: on {t.device}, expected {dev}")
+    return _ptr(t), t.numel() * t.element_size()
 
 
 def _unknown(table: dict, key: str, what: str):
@@ -693,7 +713,8 @@ def linear(x, W, bias=None, residual=None, act: str = "none", out_dtype=None, pr
         None if bias is None else _flat(bias, "bias", (N,), _F32, dev), rp, ldr, _16[dt],
         ACTS[act] if act in ACTS else _unknown(ACTS, act, "act"), T, K, N,
         None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev), y.data_ptr(), ldy,
-        _DTYPES[y.dtype], None if status is None else _ptr(status), _raw_stream(dev.index))
+        _DTYPES[y.dtype], None if status is None else _status(status, dev),
+        _raw_stream(dev.index))
     if rc:
         raise MoeError("moe_linear", rc)
     return y
@@ -750,14 +771,12 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
     if ws is None:
         ws = torch.empty(linear_grad_workspace_bytes(T, N, dy.dtype, dW.dtype if dWp else dt),
                          dtype=torch.uint8, device=dev)
-    else:
-        _ptr(ws)
+    wsp, ws_bytes = _ws(ws, dev)
     rc = (_lib or lib()).moe_linear_grad(
         x.data_ptr(), ldx, wp, None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev),
         dy.data_ptr(), lddy, _DTYPES[dy.dtype], _16[dt],
         ACTS[act] if act in ACTS else _unknown(ACTS, act, "act"), T, K, N, dxp, dWp, dw_code, dbp,
-        ws.data_ptr(), ws.numel(), None if status is None else _ptr(status),
-        _raw_stream(dev.index))
+        wsp, ws_bytes, None if status is None else _status(status, dev), _raw_stream(dev.index))
     if rc:
         raise MoeError("moe_linear_grad", rc)
     return dx, dW, db
@@ -813,13 +832,13 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
             sp = output("loss", (2,), _F32)
     if ws is not None:
         o["ws"] = ws
+    wsp, ws_bytes = _ws(ws, dev)
     rc = (_lib or lib()).moe_route(
         logits.data_ptr(), ld, _DTYPES[logits.dtype],
         None if bias is None else _flat(bias, "bias", (E,), _F32, dev),
         None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, E, k,
         SCORES[score] if score in SCORES else _unknown(SCORES, score, "score"), norm, scale, ip,
-        wp, cp, pp, sp, None if ws is None else _ptr(ws), 0 if ws is None else ws.numel(),
-        _raw_stream(dev.index))
+        wp, cp, pp, sp, wsp, ws_bytes, _raw_stream(dev.index))
     if rc:
         raise MoeError("moe_route", rc)
     return o

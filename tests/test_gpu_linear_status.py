@@ -74,3 +74,23 @@ def test_route_without_a_workspace_reports_bad_logits(T):
     with torch.cuda.stream(s):
         B.route(l, 4, stats=False)
         assert B.take_status() == B.STATUS_BAD_LOGIT
+
+
+def test_words_and_workspaces_are_checked():
+    x, W = _rand(1, 20, 64), _rand(2, 24, 64)
+    dy, l = _rand(3, 20, 24), torch.zeros(20, 32, device="cuda")
+    cpu = torch.zeros(1, dtype=torch.int32)
+    for bad in (cpu, cpu.cuda().to(torch.int8), cpu.cuda()[:0]):
+        with pytest.raises(ValueError, match="status"):
+            B.linear(x, W, status=bad)
+        with pytest.raises(ValueError, match="status"):
+            B.linear_grad(x, W, dy, status=bad)
+    with pytest.raises(ValueError, match="ws"):
+        B.linear_grad(x, W, dy, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="ws"):
+        B.route(l, 2, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    # a workspace of another element type counts in bytes
+    n = B.linear_grad_workspace_bytes(20, 24, torch.bfloat16, torch.bfloat16)
+    B.linear_grad(x, W, dy, ws=torch.empty((n + 3) // 4, dtype=torch.int32, device="cuda"))
+    n = B.route_workspace_bytes(20, 32)
+    B.route(l, 2, ws=torch.empty((n + 3) // 4, dtype=torch.int32, device="cuda"))
