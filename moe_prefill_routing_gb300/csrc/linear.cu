@@ -517,10 +517,11 @@ __global__ void __launch_bounds__(kLinThreads)
                 mbar_arrive_expect_tx(fb, stage_bytes + (stall ? 16u : 0u));
                 uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kLinATile;
                 const CUtensorMap *ma = &maps.a, *mb = &maps.b;
-                int k0 = kb * LK;
+                int step = kb;
                 if constexpr (EXTRA)
-                    if (kb >= nk1)
-                        mb = &maps.b2, k0 -= nk1 * LK;
+                    if (step >= nk1)
+                        mb = &maps.b2, step -= nk1;
+                const int k0 = step * LK;
                 if (p.a_mn) {  // 64 m x 64 r boxes, m contiguous
                     tma_load_2d(sa, ma, fb, m0, k0);
                     tma_load_2d(sa + 8192, ma, fb, m0 + 64, k0);
@@ -1136,12 +1137,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         uint8_t *sa = smem + (stage * SUB + h) * sub_bytes;
                         uint8_t *sb = sa + kLinATile;
                         const CUtensorMap *map_a = &g.a[w.which];
-                        int k0 = (kb + h) * LK;
+                        int step = kb + h;
                         if constexpr (EXTRA) {
-                            const int k1 = (p.R + LK - 1) / LK * LK;  // of a piece
-                            if (k0 >= k1)
-                                map_a = &g.a2[w.which], k0 -= k1;
+                            const int nk1 = (p.R + LK - 1) / LK;  // of a piece
+                            if (step >= nk1)
+                                map_a = &g.a2[w.which], step -= nk1;
                         }
+                        const int k0 = step * LK;
                         if (a_mn) {  // 64 m x 64 r boxes, m contiguous
                             tma_load_2d_pair(sa, map_a, fb, m0, k0);
                             tma_load_2d_pair(sa + 8192, map_a, fb, m0 + 64, k0);
