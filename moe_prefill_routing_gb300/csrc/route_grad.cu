@@ -216,8 +216,12 @@ __global__ void __launch_bounds__(kGradThreads, kGradResident<V, J>)
         }
 #pragma unroll
         for (int j = 0; j < J; ++j)
-            if (v[j] > -INFINITY)
-                dsel[e[j]] = q[j] * mul * (dj[j] - mean);
+            if (v[j] > -INFINITY) {
+                // (a slot whose score is all of the sum has a constant weight:
+                // exactly 0, not what the reciprocal's rounding leaves of dw)
+                const bool alone = p.norm && q[j] == sums[kQ];
+                dsel[e[j]] = alone ? 0.0f : q[j] * mul * (dj[j] - mean);
+            }
         gr.sync();
         const float zc = gz * (m + __logf(sume)) * rcp_ftz(sume);
         float ds[V];

@@ -61,3 +61,22 @@ def test_closed_experts_gradient_is_zero_whatever_comes_in(E, k, dtype, score, n
                          **kw)
         assert bool((g[closed] == 0).all()), (a, b, c)
         assert not bool(g.isfinite().all()) or a == 3e38
+
+
+@pytest.mark.parametrize("E,k", [(14, 1), (200, 1), (512, 1), (900, 1), (40, 3), (2500, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_weight_that_is_alone_has_no_gradient(E, k, score):
+    # renormalised over itself it is `scale` whatever the logits: dw adds
+    # nothing, beside losses a million times smaller
+    l = torch.randn(300, E, generator=torch.Generator().manual_seed(E))
+    if k > 1:  # one open expert a token
+        keep = torch.randint(E, (300, 1), generator=torch.Generator().manual_seed(1))
+        l = torch.full_like(l, -float("inf")).scatter(1, keep, l.gather(1, keep))
+    l = l.cuda()
+    r = B.route(l, k, score=score, scale=2.5)
+    dw = torch.randn(300, k, generator=torch.Generator().manual_seed(2)).cuda()
+    dloss = torch.tensor([1e-4, 1e-6], device="cuda")
+    kw = dict(dloss=dloss, score=score, scale=2.5)
+    got = B.route_grad(l, r["ids"], r["counts"], dw=dw, **kw)
+    assert torch.equal(got, B.route_grad(l, r["ids"], r["counts"], **kw))
+    assert bool((B.route_grad(l, r["ids"], dw=dw, score=score, scale=2.5) == 0).all())
