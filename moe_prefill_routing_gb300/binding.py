@@ -651,9 +651,7 @@ def _ld(t, name: str, shape, dtypes, dev) -> int:
 
 
 def _status(t, dev):
-    """Address of a caller's status word, or None."""
-    if t is None:
-        return None
+    """Address of a caller's status word."""
     if t.dtype not in _WORD or t.numel() == 0 or t.device != dev:
         raise ValueError(f"status: expected a 32-bit integer on {dev}, got {t.numel()} of "
                          f"{t.dtype} on {t.device}")
@@ -661,9 +659,7 @@ def _status(t, dev):
 
 
 def _ws(t, dev):
-    """Address of a caller's workspace and its bytes; (None, 0) for None."""
-    if t is None:
-        return None, 0
+    """Address of a caller's workspace and its bytes."""
     if t.device != dev:
         raise ValueError(f"ws: on {t.device}, expected {dev}")
     return _ptr(t), t.numel() * t.element_size()
@@ -771,7 +767,9 @@ def linear_grad(x, W, dy, pre=None, act: str = "none", need=(True, True, True), 
     if ws is None:
         ws = torch.empty(linear_grad_workspace_bytes(T, N, dy.dtype, dW.dtype if dWp else dt),
                          dtype=torch.uint8, device=dev)
-    wsp, ws_bytes = _ws(ws, dev)
+        wsp, ws_bytes = ws.data_ptr(), ws.numel()
+    else:
+        wsp, ws_bytes = _ws(ws, dev)
     rc = (_lib or lib()).moe_linear_grad(
         x.data_ptr(), ldx, wp, None if pre is None else _flat(pre, "pre", (T, N), (dt,), dev),
         dy.data_ptr(), lddy, _DTYPES[dy.dtype], _16[dt],
@@ -804,8 +802,12 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return route(logits, k, bias, mask, score, norm, scale, stats, out, ws)
-    if ws is None and stats:
+    wsp, ws_bytes = None, 0
+    if ws is not None:
+        wsp, ws_bytes = _ws(ws, dev)
+    elif stats:
         ws = torch.empty(route_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+        wsp, ws_bytes = ws.data_ptr(), ws.numel()
     cp = pp = sp = None
     if out is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
@@ -832,7 +834,6 @@ def route(logits, k: int, bias=None, mask=None, score: str = "softmax", norm: bo
             sp = output("loss", (2,), _F32)
     if ws is not None:
         o["ws"] = ws
-    wsp, ws_bytes = _ws(ws, dev)
     rc = (_lib or lib()).moe_route(
         logits.data_ptr(), ld, _DTYPES[logits.dtype],
         None if bias is None else _flat(bias, "bias", (E,), _F32, dev),
