@@ -429,8 +429,8 @@ __device__ __noinline__ void add_small_chain(uint32_t acc, uint32_t sum, int bn,
 // all SMs together draw the memory's bandwidth.  Two CTAs fit an SM, 110 KB
 // of loads in flight each.  Bound by memory, and by a fixed 4 us of launch,
 // first loads, joining the parts and writing: 16 x 10240 x 2560 with a
-// residual takes 13.2 us (52.9 MB, 4.0 TB/s, 6 without the fixed part);
-// 1 x 2560 x 512, 4.4 us.
+// residual takes 14 us (52.9 MB, 3.8 TB/s, 5.3 without the fixed part);
+// 1 x 2560 x 512, 4.6 us.
 //
 // Chains (chain_steps) have an accumulator each where those fit the CTA's
 // tensor memory; more of them (fp32 outputs of 33 to 128 rows from R = 16384)
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kLinThreads)
 // us, each lane storing its row from registers, 32 bytes at a time, 203 us,
 // where TMA stores took 168: both put 8 to 32 lines into an instruction.)
 //
-// Bound by the tensor cores: that product with GELU-tanh takes 150 - 152 us
+// Bound by the tensor cores: that product with GELU-tanh takes 148 - 154 us
 // (1.72 PFLOP/s), without pre and activation 140 (1.85 PFLOP/s), its MMAs
 // alone 133.  The rest is 184 MB of outputs, the last round of tiles and its
 // epilogue.

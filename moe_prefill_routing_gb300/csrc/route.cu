@@ -111,10 +111,10 @@ __device__ __forceinline__ uint32_t warp_threshold(uint32_t own, uint32_t kmax, 
 //
 // Bound by instructions, not memory: some 500 a token at 128 experts (sigmoid,
 // bias, losses, k = 8), 1100 at 512 (softmax, losses, k = 10), with 70 % of
-// the issue slots taken.  With k_route_final 25.3 us for 32768 tokens x 128
-// experts (18.9 MB, 2.8 us of memory traffic), 9.2 us for 2048 x 512, of which
+// the issue slots taken.  With k_route_final 25.6 us for 32768 tokens x 128
+// experts (18.9 MB, 2.8 us of memory traffic), 9.0 us for 2048 x 512, of which
 // the launches, one token's chain of reductions and the final sums are most;
-// 2.4 us for one token.  (Two tokens a warp would halve the shuffles but
+// 2.5 us for one token.  (Two tokens a warp would halve the shuffles but
 // double the lane maxima's rounds, which one instruction each reduces.)
 template <typename L, int V, int W, int C, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads, kRouteResident<V>) k_route(const RouteArgs p)

@@ -14,10 +14,10 @@
 // once; the weights' part is k values a token, set out by expert in shared
 // memory.
 //
-// 32768 tokens x 256 experts, bf16: 13.9 us, 2.6 TB/s of the 35.7 MB it moves;
-// bound by instructions (320 a token, six tenths of the issue slots; the rest
-// waits for loads and reductions).  2048 x 512, fp32: 3.5 us, launch and one
-// token's latency.
+// 32768 tokens x 256 experts, bf16: 14.7 us, 2.4 TB/s of the 35.7 MB it moves;
+// bound by instructions (some 330 a token, six tenths of the issue slots; the
+// rest waits for loads and reductions).  2048 x 512, fp32: 3.7 us, launch and
+// one token's latency.
 #include "route.cuh"
 
 namespace moe {
