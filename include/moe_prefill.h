@@ -25,7 +25,10 @@
  * Beside the routed experts stand the operators that feed the layer and join
  * its result: moe_linear (router logits, dense projections, the residual
  * add) and moe_route (logits to ids, w, counts and the balance and z losses),
- * with their gradients moe_linear_grad and moe_route_grad.
+ * with their gradients moe_linear_grad and moe_route_grad; moe_block_norm (the
+ * norms before and after a block, its gate and the residual stream) with its
+ * gradient moe_block_norm_grad; and moe_linear_mxfp4, the dense projection on
+ * rows and weights in MXFP4 (moe_quantize_rows_mxfp4).
  *
  * Conventions shared by every call
  *  - Tensors are caller-owned DEVICE pointers, row-major and contiguous
@@ -88,6 +91,10 @@ typedef struct CUstream_st *moe_stream_t;
 #define MOE_ACT_SILU 2      /* z / (1 + e^-z) */
 #define MOE_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
 #define MOE_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+
+/* gate of moe_block_norm */
+#define MOE_GATE_PLAIN 0
+#define MOE_GATE_SIGMOID 1 /* 1 / (1 + e^-g) */
 
 /* score of moe_route */
 #define MOE_SCORE_SOFTMAX 0
@@ -511,9 +518,9 @@ MOE_API int moe_prefill_forward_host(int n_chunks, const void *const *x_h,
 MOE_API int moe_read_status(const void *ws, moe_stream_t stream, uint32_t *status);
 
 /*
- * moe_take_status -- the status bits of the current device's moe_linear and
- * moe_linear_grad calls that had no status word and moe_route calls that had
- * no workspace, on any stream, since they were last taken: copied to *status
+ * moe_take_status -- the status bits of the current device's moe_linear,
+ * moe_linear_grad and moe_linear_mxfp4 calls that had no status word and
+ * moe_route calls that had no workspace, on any stream, since they were last taken: copied to *status
  * and cleared, synchronising `stream` (order it behind the calls asked about).
  */
 MOE_API int moe_take_status(moe_stream_t stream, uint32_t *status);
@@ -652,6 +659,112 @@ MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const ui
                            const int32_t *ids, const int32_t *counts, const float *dw,
                            const float *dloss, int T, int E, int k, int score, int norm,
                            float scale, void *dlogits, int64_t ldd, moe_stream_t stream);
+
+/*
+ * moe_block_norm -- the norm after a block, its gate, the scaled residual add
+ * and the norm before the next block, in one pass.  Per row t,
+ * r(v) = (mean(v^2) + eps)^-1/2:
+ *
+ *   n     = r(o) o                     (post_norm != 0; else o)
+ *   xn[t] = alpha x + g n . post       (rounded to the stream's type)
+ *   h[t]  = r(xn) xn . pre             (of xn as rounded; rounded to the block's type)
+ *
+ * g is gate[t], 1 / (1 + e^-gate[t]) with MOE_GATE_SIGMOID, or 1 without gate;
+ * weights that are NULL (post) are 1.  Sums are fp32, so rows with values past
+ * about 3e18, whose squares leave its range, are not normalised.  Without o,
+ * xn is x itself (alpha is not looked at): h alone is written.
+ * in   x         x_dtype [T, d]  the residual stream, rows ldx elements apart
+ * in   o         b_dtype [T, d]  the block's output, rows ldo apart, or NULL (then
+ *                post, gate and xn are NULL too)
+ * in   pre       fp32 [d], or NULL: no h.  One of o and pre at least
+ * in   post      fp32 [d] or NULL;  gate fp32 [T] or NULL
+ * in   mask      uint8 [T] or NULL: rows with 0 are not read, and their xn and h are 0
+ * out  xn        x_dtype [T, d], rows ldxn apart; may be x itself (ldxn = ldx)
+ * out  h         b_dtype [T, d], rows ldh apart
+ * out  codes, scales   h (as rounded) in MXFP4, see moe_quantize_rows_mxfp4; or
+ *                both NULL.  h may be NULL with them.  d a multiple of 32 then
+ * x_dtype any MOE_DT_*; b_dtype the same, or a 16-bit type beside an fp32
+ * stream.  T >= 0, 1 <= d <= 16384.  Tensors aligned to their element, codes and
+ * scales to 16 bytes.  No other operands may overlap.  Deterministic.
+ */
+MOE_API int moe_block_norm(const void *x, int64_t ldx, int x_dtype, const void *o, int64_t ldo,
+                           int b_dtype, const float *pre, const float *post, const float *gate,
+                           const uint8_t *mask, int T, int d, int post_norm, int gate_act,
+                           float alpha, float eps, void *xn, int64_t ldxn, void *h, int64_t ldh,
+                           uint8_t *codes, uint8_t *scales, moe_stream_t stream);
+
+/*
+ * moe_block_norm_grad -- the gradients of moe_block_norm from dxn (what reaches
+ * the stream past the norm) and dh, the rounding of xn taken as the identity.
+ *
+ *   dS   = dxn + the gradient of h with respect to xn
+ *   dx   = alpha dS,  and through g n . post from dS: do, dgate, dpost;  dpre from dh
+ * in   xn        as moe_block_norm wrote it (x itself where there was no o); not
+ *                looked at without dh
+ * in   o, pre, post, gate, mask, post_norm, gate_act, alpha, eps  as given there
+ * in   dxn       x_dtype [T, d], rows lddxn apart, or NULL (zeros)
+ * in   dh        b_dtype [T, d], rows lddh apart, or NULL (zeros; there was no h).
+ *                One of dxn and dh at least
+ * out  dx        x_dtype [T, d], rows lddx apart; may be dxn itself (lddx = lddxn)
+ * out  d_o       b_dtype [T, d], rows lddo apart; NULL if o is; may be o or dh itself
+ * out  dpre, dpost  fp32 [d] or NULL;  dgate fp32 [T] or NULL
+ * ws             moe_block_norm_grad_workspace_bytes(T, d) bytes, 256-byte aligned;
+ *                may be NULL without dpre and dpost
+ * Rows with mask 0 are not read; their dx, do and dgate are 0.  All sums fp32 in
+ * a fixed order on one device: deterministic.  With T = 0 dpre and dpost are 0.
+ */
+MOE_API size_t moe_block_norm_grad_workspace_bytes(int T, int d);
+MOE_API int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, const void *o,
+                                int64_t ldo, int b_dtype, const float *pre, const float *post,
+                                const float *gate, const uint8_t *mask, const void *dxn,
+                                int64_t lddxn, const void *dh, int64_t lddh, int T, int d,
+                                int post_norm, int gate_act, float alpha, float eps, void *dx,
+                                int64_t lddx, void *d_o, int64_t lddo, float *dpre, float *dpost,
+                                float *dgate, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Rows in MXFP4 (the format of moe_quantize_mxfp4: E2M1 elements, a power-of-two
+ * scale 2^(S-127) for each 32 of them along the row), laid out for the tensor
+ * cores' 4-bit products:
+ *   codes   uint8 [rows, K/2]: element 2i in the low half of byte i
+ *   scales  uint8, moe_mxfp4_scale_bytes(rows, K) of them: S in tiles of 128
+ *           rows x 4 blocks, [ceil(rows/128), ceil(K/128), 512]; of a tile, row
+ *           32 q + l, block b at byte 16 l + 4 q + b
+ * both 16-byte aligned, K a positive multiple of 32.
+ *
+ * moe_quantize_rows_mxfp4 -- x dtype [rows, K] (any MOE_DT_*), rows ldx elements
+ * apart, aligned to its element, to codes and scales.  S and the codes as in
+ * moe_quantize_mxfp4; a block with a NaN or an infinity has S = 255 (NaN) and
+ * codes 0.  Scale bytes past the last row and block are written as 0.
+ *
+ * moe_dequantize_rows_mxfp4 -- y dtype [rows, K] (MOE_DT_BF16 or MOE_DT_F32,
+ * which hold the values exactly), rows ldy elements apart.
+ */
+MOE_API size_t moe_mxfp4_scale_bytes(int rows, int K);
+MOE_API int moe_quantize_rows_mxfp4(const void *x, int64_t ldx, int dtype, int rows, int K,
+                                    uint8_t *codes, uint8_t *scales, moe_stream_t stream);
+MOE_API int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scales, int rows, int K,
+                                      void *y, int64_t ldy, int dtype, moe_stream_t stream);
+
+/*
+ * moe_linear_mxfp4 -- moe_linear with both operands in MXFP4 (rows as above):
+ *
+ *   y[t][n] = act(sum_i x[t][i] W[n][i] + bias[n]) + residual[t][n]
+ *
+ * on the tensor cores' 4-bit path, sums in fp32, rounded once to y's type.
+ * in   x, x_scales   [T, K];  W, W_scales [N, K] (each output feature's weights a row)
+ * in   bias      fp32 [N] or NULL
+ * in   residual  y_dtype [T, N], rows ldr elements apart, or NULL; may be y itself
+ * out  y         y_dtype [T, N] (any MOE_DT_*), rows ldy elements apart
+ * in   status    as in moe_linear
+ * A row (or weight) with a NaN block makes its outputs NaN.  T >= 0, N >= 1, K a
+ * positive multiple of 32; T, K, N <= 2^31 - 512; ldr, ldy >= N.  codes and scales
+ * 16-byte aligned, the others to their element.  Deterministic.
+ */
+MOE_API int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W,
+                             const uint8_t *W_scales, const float *bias, const void *residual,
+                             int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy,
+                             int y_dtype, uint32_t *status, moe_stream_t stream);
 
 /*
  * moe_selftest_linear_wait_limit -- the same of moe_linear (bf16, contiguous,

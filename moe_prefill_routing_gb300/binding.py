@@ -28,6 +28,7 @@ STATUS_BAD_LOGIT = 16
 DT_BF16, DT_F16, DT_F32 = 0, 1, 2
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
+GATE_ACTS = {"none": 0, "sigmoid": 1}
 WS_FIELDS = ["status", "bcnt", "offsets", "counts", "srt_tok", "srt_w", "pos", "tile_expert",
              "xs", "H", "Ys", "total"]
 
@@ -127,6 +128,25 @@ _SIGS = {
                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                  C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_int64,
                                  C.c_void_p]),
+    "moe_block_norm": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int64, C.c_int,
+                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int,
+                                 C.c_int, C.c_int, C.c_float, C.c_float, C.c_void_p, C.c_int64,
+                                 C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "moe_block_norm_grad_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int]),
+    "moe_block_norm_grad": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int64,
+                                      C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                      C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
+                                      C.c_int, C.c_int, C.c_int, C.c_float, C.c_float, C.c_void_p,
+                                      C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "moe_mxfp4_scale_bytes": (C.c_size_t, [C.c_int, C.c_int]),
+    "moe_quantize_rows_mxfp4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int,
+                                          C.c_void_p, C.c_void_p, C.c_void_p]),
+    "moe_dequantize_rows_mxfp4": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p,
+                                            C.c_int64, C.c_int, C.c_void_p]),
+    "moe_linear_mxfp4": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                   C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int,
+                                   C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p]),
     "moe_take_status": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "moe_selftest_linear_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                                  C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
@@ -878,6 +898,298 @@ def route_grad(logits, ids, counts=None, dw=None, dloss=None, mask=None, score: 
     return dlogits
 
 
+# ---- block norms and MXFP4 rows ---------------------------------------------
+
+
+class Mxfp4Rows(NamedTuple):
+    """Rows in MXFP4 for ``linear_mxfp4``: codes uint8 [R, K/2] (E2M1, element
+    2i in the low half of byte i) and scales uint8 [ceil(R/128), ceil(K/128),
+    512] (bytes S of 2^(S-127), one for each 32 along K; of a tile, row 32 q + l,
+    block b at byte 16 l + 4 q + b)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], 2 * self.codes.shape[1]
+
+    @classmethod
+    def empty(cls, rows: int, K: int, device):
+        if K % 32 or K <= 0:
+            raise ValueError(f"MXFP4 rows: a positive multiple of 32, got {K}")
+        return cls(torch.empty((rows, K // 2), dtype=torch.uint8, device=device),
+                   torch.empty(((rows + 127) // 128, (K + 127) // 128, 512), dtype=torch.uint8,
+                               device=device))
+
+
+_U8 = (torch.uint8,)
+
+
+def _mx(q, name: str, shape, dev):
+    """Addresses of MXFP4 rows of the given shape on dev."""
+    R, K = shape
+    if K % 32 or K <= 0:
+        raise ValueError(f"{name}: rows of a positive multiple of 32, got {K}")
+    return (_flat(q.codes, name + ".codes", (R, K // 2), _U8, dev),
+            _flat(q.scales, name + ".scales", ((R + 127) // 128, (K + 127) // 128, 512), _U8, dev))
+
+
+def quantize_rows_mxfp4(x, out: Mxfp4Rows | None = None) -> Mxfp4Rows:
+    """moe_quantize_rows_mxfp4: rows x [R, K] (16-bit or float32, K a multiple of
+    32; they may lie further apart than their length) in MXFP4: activations, or a
+    dense weight [N, K] laid out once."""
+    R, K = x.shape
+    dev = x.device
+    ldx = _ld(x, "x", (R, K), _DTYPES, dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return quantize_rows_mxfp4(x, out)
+    if out is None:
+        out = Mxfp4Rows.empty(R, K, dev)
+        cp, sp = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        cp, sp = _mx(out, "out", (R, K), dev)
+    rc = (_lib or lib()).moe_quantize_rows_mxfp4(x.data_ptr(), ldx, _DTYPES[x.dtype], R, K, cp, sp,
+                                                 _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_quantize_rows_mxfp4", rc)
+    return out
+
+
+def dequantize_rows_mxfp4(q: Mxfp4Rows, dtype=torch.bfloat16, y=None):
+    """moe_dequantize_rows_mxfp4: what the rows stand for, [R, K] in bfloat16 or
+    float32 (exact in both)."""
+    R, K = q.shape
+    dev = q.codes.device
+    cp, sp = _mx(q, "q", (R, K), dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return dequantize_rows_mxfp4(q, dtype, y)
+    if y is None:
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise ValueError(f"dtype: unexpected dtype {dtype}")
+        y = torch.empty((R, K), dtype=dtype, device=dev)
+        ldy = K
+    else:
+        ldy = _ld(y, "y", (R, K), (torch.bfloat16, torch.float32), dev)
+    rc = (_lib or lib()).moe_dequantize_rows_mxfp4(cp, sp, R, K, y.data_ptr(), ldy,
+                                                   _DTYPES[y.dtype], _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_dequantize_rows_mxfp4", rc)
+    return y
+
+
+def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", out_dtype=None,
+                 y=None, x_rows: Mxfp4Rows | None = None, status=None):
+    """moe_linear_mxfp4: y = act(x W^T + bias) + residual, both operands in MXFP4.
+
+    x [T, K]: ``Mxfp4Rows``, or 16-bit or float32 rows, which are quantised first
+    (into ``x_rows`` if given).  W [N, K] from ``quantize_rows_mxfp4``.  bias fp32
+    [N], residual and y [T, N] of ``out_dtype`` (16-bit or float32; by default x's
+    type, bfloat16 for MXFP4 rows); their rows may lie further apart than their
+    length.  ``residual`` may be ``y``; ``status`` as in ``linear``."""
+    T, K = x.shape
+    N = W.codes.shape[0]
+    rows = isinstance(x, Mxfp4Rows)
+    dev = W.codes.device
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return linear_mxfp4(x, W, bias, residual, act, out_dtype, y, x_rows, status)
+    wp, wsp = _mx(W, "W", (N, K), dev)
+    code = ACTS[act] if act in ACTS else _unknown(ACTS, act, "act")
+    if y is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16 if rows else x.dtype
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out_dtype: unexpected dtype {out_dtype}")
+        y = torch.empty((T, N), dtype=out_dtype, device=dev)
+        ldy = N
+    elif out_dtype is not None and y.dtype != out_dtype:
+        raise ValueError(f"y: expected {out_dtype}, got {y.dtype}")
+    else:
+        ldy = _ld(y, "y", (T, N), _DTYPES, dev)
+    rp, ldr = None, 0
+    if residual is not None:
+        ldr = _ld(residual, "residual", (T, N), (y.dtype,), dev)
+        rp = residual.data_ptr()
+    bp = None if bias is None else _flat(bias, "bias", (N,), _F32, dev)
+    stp = None if status is None else _status(status, dev)
+    if not rows:
+        if x.device != dev:
+            _refuse(x, "x", (T, K), _DTYPES, dev)
+        x = quantize_rows_mxfp4(x, x_rows)
+        xp, xsp = x.codes.data_ptr(), x.scales.data_ptr()
+    else:
+        xp, xsp = _mx(x, "x", (T, K), dev)
+    rc = (_lib or lib()).moe_linear_mxfp4(xp, xsp, wp, wsp, bp, rp, ldr, code, T, K, N,
+                                          y.data_ptr(), ldy, _DTYPES[y.dtype], stp,
+                                          _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_linear_mxfp4", rc)
+    return y
+
+
+def _block_types(stream) -> tuple:
+    """Types of a block's rows beside a residual stream of the given one."""
+    return tuple(_DTYPES) if stream is torch.float32 else (stream,)
+
+
+def block_norm(x, o=None, pre=None, post=None, gate=None, mask=None, post_norm: bool = True,
+               gate_act: str = "none", alpha: float = 1.0, eps: float = 1e-6, h_dtype=None,
+               mxfp4: bool = False, xn=None, h=None, mx: Mxfp4Rows | None = None) -> dict:
+    """moe_block_norm: xn = alpha x + g norm(o) . post and h = norm(xn) . pre.
+
+    x [T, d] is the residual stream (16-bit or float32), o [T, d] the output of
+    the block before (x's type, or a 16-bit one beside a float32 stream) or None;
+    norm(v) = v / sqrt(mean(v^2) + eps), of o only with ``post_norm``.  pre and
+    post are fp32 [d] (post None: ones; pre None: no h), gate fp32 [T] the gate of
+    each token, through a sigmoid with gate_act "sigmoid".  Rows with mask 0 (bool
+    or uint8 [T]) are not read and come out as 0.  Returns xn (x itself without
+    o), h of o's type (``h_dtype``, or x's, without o) and, with ``mxfp4``, mx:
+    the rows of h in MXFP4.  xn, h and mx may be passed in; xn may be x."""
+    T, d = x.shape
+    dev = x.device
+    xt = x.dtype
+    ldx = _ld(x, "x", (T, d), _DTYPES, dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return block_norm(x, o, pre, post, gate, mask, post_norm, gate_act, alpha, eps,
+                              h_dtype, mxfp4, xn, h, mx)
+    op, ldo, xnp, ldxn, hp, ldh, cp, sp = None, 0, None, 0, None, 0, None, None
+    out = {}
+    if o is not None:
+        ldo = _ld(o, "o", (T, d), _block_types(xt), dev)
+        op = o.data_ptr()
+        bt = o.dtype
+        if h_dtype is not None and h_dtype is not bt:
+            raise ValueError(f"h_dtype: expected {bt}, got {h_dtype}")
+        if xn is None:
+            xn = torch.empty((T, d), dtype=xt, device=dev)
+            ldxn = d
+        else:
+            ldxn = _ld(xn, "xn", (T, d), (xt,), dev)
+        xnp = xn.data_ptr()
+        out["xn"] = xn
+    else:
+        if post is not None or gate is not None or xn is not None:
+            raise ValueError("post, gate and xn come with o")
+        bt = h_dtype or (h.dtype if h is not None else xt)
+        if bt not in _block_types(xt):
+            raise ValueError(f"h_dtype: {bt} beside a stream of {xt}")
+        out["xn"] = x
+    if pre is not None:
+        if h is None:
+            h = torch.empty((T, d), dtype=bt, device=dev)
+            ldh = d
+        else:
+            ldh = _ld(h, "h", (T, d), (bt,), dev)
+        hp = h.data_ptr()
+        out["h"] = h
+        if mx is not None:
+            cp, sp = _mx(mx, "mx", (T, d), dev)
+        elif mxfp4:
+            mx = Mxfp4Rows.empty(T, d, dev)
+            cp, sp = mx.codes.data_ptr(), mx.scales.data_ptr()
+        if mx is not None:
+            out["mx"] = mx
+    elif h is not None or mxfp4 or mx is not None:
+        raise ValueError("h and its MXFP4 rows come with pre")
+    rc = (_lib or lib()).moe_block_norm(
+        x.data_ptr(), ldx, _DTYPES[xt], op, ldo, _DTYPES[bt],
+        None if pre is None else _flat(pre, "pre", (d,), _F32, dev),
+        None if post is None else _flat(post, "post", (d,), _F32, dev),
+        None if gate is None else _flat(gate, "gate", (T,), _F32, dev),
+        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, d, bool(post_norm),
+        GATE_ACTS[gate_act] if gate_act in GATE_ACTS else _unknown(GATE_ACTS, gate_act, "gate_act"),
+        alpha, eps, xnp, ldxn, hp, ldh, cp, sp, _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_block_norm", rc)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def block_norm_grad_workspace_bytes(T: int, d: int) -> int:
+    return int((_lib or lib()).moe_block_norm_grad_workspace_bytes(T, d))
+
+
+def block_norm_grad(xn, o=None, dxn=None, dh=None, pre=None, post=None, gate=None, mask=None,
+                    post_norm: bool = True, gate_act: str = "none", alpha: float = 1.0,
+                    eps: float = 1e-6, weights: bool = True, dx=None, do=None, ws=None) -> dict:
+    """moe_block_norm_grad: the gradients of ``block_norm`` from dxn [T, d] (xn's
+    type; what reaches the stream past the norm) and dh [T, d] (h's type), either
+    of which may be None.
+
+    xn, o and the rest as ``block_norm`` returned and took them (xn: x where there
+    was no o).  Returns dx and, where the inputs were, do, dgate fp32 [T], and with
+    ``weights`` dpre and dpost fp32 [d].  dx and do may be passed in; dx may be
+    dxn."""
+    T, d = xn.shape
+    dev = xn.device
+    xt = xn.dtype
+    ldxn = _ld(xn, "xn", (T, d), _DTYPES, dev)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return block_norm_grad(xn, o, dxn, dh, pre, post, gate, mask, post_norm, gate_act,
+                                   alpha, eps, weights, dx, do, ws)
+    if dxn is None and dh is None:
+        raise ValueError("one of dxn and dh at least")
+    if dh is not None and pre is None:
+        raise ValueError("dh comes with pre")
+    if o is None and (post is not None or gate is not None or do is not None):
+        raise ValueError("post, gate and do come with o")
+    bt = o.dtype if o is not None else dh.dtype if dh is not None else xt
+    op, ldo, dop, lddo, lddxn, lddh = None, 0, None, 0, 0, 0
+    out = {}
+    if dxn is not None:
+        lddxn = _ld(dxn, "dxn", (T, d), (xt,), dev)
+    if dh is not None:
+        lddh = _ld(dh, "dh", (T, d), (bt,) if o is not None else _block_types(xt), dev)
+    if dx is None:
+        dx = torch.empty((T, d), dtype=xt, device=dev)
+        lddx = d
+    else:
+        lddx = _ld(dx, "dx", (T, d), (xt,), dev)
+    out["dx"] = dx
+    dgate = dpre = dpost = None
+    if o is not None:
+        ldo = _ld(o, "o", (T, d), _block_types(xt), dev)
+        op = o.data_ptr()
+        if do is None:
+            do = torch.empty((T, d), dtype=bt, device=dev)
+            lddo = d
+        else:
+            lddo = _ld(do, "do", (T, d), (bt,), dev)
+        dop = do.data_ptr()
+        out["do"] = do
+        if gate is not None:
+            out["dgate"] = dgate = torch.empty(T, dtype=torch.float32, device=dev)
+        if post is not None and weights:
+            out["dpost"] = dpost = torch.empty(d, dtype=torch.float32, device=dev)
+    if dh is not None and weights:
+        out["dpre"] = dpre = torch.empty(d, dtype=torch.float32, device=dev)
+    wsp, ws_bytes = None, 0
+    if ws is not None:
+        wsp, ws_bytes = _ws(ws, dev)
+    elif dpre is not None or dpost is not None:
+        ws = torch.empty(block_norm_grad_workspace_bytes(T, d), dtype=torch.uint8, device=dev)
+        wsp, ws_bytes = ws.data_ptr(), ws.numel()
+    rc = (_lib or lib()).moe_block_norm_grad(
+        xn.data_ptr(), ldxn, _DTYPES[xt], op, ldo, _DTYPES[bt],
+        None if pre is None else _flat(pre, "pre", (d,), _F32, dev),
+        None if post is None else _flat(post, "post", (d,), _F32, dev),
+        None if gate is None else _flat(gate, "gate", (T,), _F32, dev),
+        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev),
+        None if dxn is None else dxn.data_ptr(), lddxn, None if dh is None else dh.data_ptr(), lddh,
+        T, d, bool(post_norm),
+        GATE_ACTS[gate_act] if gate_act in GATE_ACTS else _unknown(GATE_ACTS, gate_act, "gate_act"),
+        alpha, eps, dx.data_ptr(), lddx, dop, lddo,
+        None if dpre is None else dpre.data_ptr(), None if dpost is None else dpost.data_ptr(),
+        None if dgate is None else dgate.data_ptr(), wsp, ws_bytes, _raw_stream(dev.index))
+    if rc:
+        raise MoeError("moe_block_norm_grad", rc)
+    return out
+
+
 def selftest_linear_wait_limit(x, W, cta: int = 0, status=None):
     """``linear(x, W)`` (bf16) with CTA `cta` made to wait for bytes that never
     come: it stops after about 2 s and reports STATUS_TIMEOUT."""
@@ -927,8 +1239,8 @@ def read_status(ws) -> int:
 
 
 def take_status(device=None) -> int:
-    """Status bits of the device's ``linear`` and ``linear_grad`` calls without
-    ``status`` and ``route`` calls without a workspace since the last call of
+    """Status bits of the device's ``linear``, ``linear_grad`` and ``linear_mxfp4``
+    calls without ``status`` and ``route`` calls without a workspace since the last call of
     this (on the current stream, which it synchronises)."""
     v = C.c_uint32(0)
     with torch.cuda.device(device):

@@ -21,9 +21,9 @@ __device__ uint32_t g_taken;
 
 // One exchange per word: a bit set meanwhile by another stream's kernel is in
 // this answer or in the next.
-__global__ void k_take_status(uint32_t *a, uint32_t *b)
+__global__ void k_take_status(uint32_t *a, uint32_t *b, uint32_t *c)
 {
-    g_taken = atomicExch(a, 0u) | atomicExch(b, 0u);
+    g_taken = atomicExch(a, 0u) | atomicExch(b, 0u) | atomicExch(c, 0u);
 }
 
 }  // namespace
@@ -608,13 +608,14 @@ int moe_take_status(moe_stream_t stream, uint32_t *status)
     if (!status)
         return MOE_ERR_NULL;
     uint32_t *a = moe::linear_status_word(), *b = moe::route_status_word();
+    uint32_t *c = moe::linear_mx_status_word();
     void *out = nullptr;
-    if (!a || !b || cudaGetSymbolAddress(&out, moe::g_taken) != cudaSuccess)
+    if (!a || !b || !c || cudaGetSymbolAddress(&out, moe::g_taken) != cudaSuccess)
         return MOE_ERR_CUDA;
     static std::mutex one_at_a_time;  // g_taken
     const std::lock_guard<std::mutex> lock(one_at_a_time);
     cudaStream_t s = as_stream(stream);
-    moe::k_take_status<<<1, 1, 0, s>>>(a, b);
+    moe::k_take_status<<<1, 1, 0, s>>>(a, b, c);
     if (cudaGetLastError() != cudaSuccess ||
         cudaMemcpyAsync(status, out, sizeof(uint32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess)
         return MOE_ERR_CUDA;

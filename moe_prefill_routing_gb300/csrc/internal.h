@@ -135,6 +135,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // The current device's words for status bits of calls that have no status word
 // of their own (null if CUDA fails).
 uint32_t *linear_status_word();
+uint32_t *linear_mx_status_word();
 uint32_t *route_status_word();
 
 // Raise a kernel's dynamic shared-memory limit once per device.
@@ -179,6 +180,7 @@ enum SmemSlot {
     kSlotLinearExtra,
     kSlotLinearPair,  // + 1 for wide tiles, + 2 with EXTRA
     kSlotLinearPairEnd = kSlotLinearPair + 3,
+    kSlotLinearMx,
     kSlotCount
 };
 

@@ -1,0 +1,443 @@
+// The dense product with both operands in MXFP4 (moe_linear_mxfp4) on the
+// tensor cores' 4-bit path: tcgen05.mma.kind::mxf4, which multiplies E2M1 codes
+// and applies the blocks' power-of-two scales itself.  Codes come by TMA with
+// the 128-byte swizzle (a row of 128 bytes is 256 of K), scale tiles as they
+// are; tcgen05.cp puts the scales into tensor memory beside the accumulators.
+//
+//   y[t][n] = act(sum_i x[t][i] W[n][i] + bias[n]) + residual[t][n]
+#include "../../include/moe_prefill.h"
+#include "internal.h"
+#include "linear_epilogue.cuh"
+#include "mx_rows.cuh"
+#include "ptx.cuh"
+
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+constexpr int MM = 128;                     // rows of a CTA's operand A
+constexpr int MK = 256;                     // of K per stage: one 128-byte row
+constexpr int kMxThreads = 192;             // producer, MMA, four accumulator warps
+constexpr uint32_t kMxATile = MM * MK / 2;  // 16 KB
+constexpr uint32_t kMxScales = 2 * kMxTileBytes;  // of 128 rows per stage
+constexpr int kMxMaxStages = 8;
+constexpr int kMxMaxSplit = 8;  // portable cluster size
+constexpr int kMxScaleCols = 16;  // of tensor memory: two tiles of A's and two of B's scales
+
+// Stages of 256 of K, four MMAs each, that one accumulator sums; sums of more
+// are cut into chains that are added outside the tensor core, which adds with
+// truncation (see linear.cu, whose numbers of MMAs these are).
+__host__ __device__ constexpr int mx_chain(bool f32, bool f16)
+{
+    return f32 ? 8 : f16 ? 256 : 2048;
+}
+
+struct MxArgs : EpiArgs {
+    uint32_t *status;
+    const uint8_t *a_scales, *b_scales;
+    int M, N, K, k_tiles;
+    int bn, stages, split, n_mt;
+    int chain;
+};
+
+// Status bits of calls without a status word, see moe_take_status.
+__device__ uint32_t g_status;
+
+__device__ __noinline__ void report_timeout(uint32_t *status)
+{
+    atomicOr(status ? status : &g_status, MOE_STATUS_TIMEOUT);
+}
+
+struct MxCtrl {
+    uint64_t full[kMxMaxStages];
+    uint64_t empty[kMxMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct MxMaps {
+    CUtensorMap a, b;
+};
+
+__host__ __device__ __forceinline__ uint32_t mx_stage_bytes(int bn)
+{
+    return kMxATile + uint32_t(bn) * (MK / 2) + 2 * kMxScales;
+}
+
+// Columns of tensor memory: the accumulator, or two of them and the sum where
+// a sum is cut into chains; then the scales.
+__host__ __device__ __forceinline__ uint32_t mx_columns(int bn, bool cut)
+{
+    const uint32_t need = uint32_t(bn) * (cut ? 3 : 1) + kMxScaleCols;
+    uint32_t cols = 32;
+    while (cols < need)
+        cols *= 2;
+    return cols;
+}
+
+// Tiles of 128 of W's rows (A) x bn of x's (16 ... 128), one CTA each, or `split`
+// CTAs of a cluster that share the reduction and join their parts through
+// distributed shared memory, each finishing 128 / split of the tile's features.
+__global__ void __launch_bounds__(kMxThreads)
+    k_linear_mx(const __grid_constant__ MxMaps maps, const MxArgs p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    __shared__ MxCtrl ctl;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const int bn = p.bn, S = p.stages;
+    const uint32_t b_bytes = uint32_t(bn) * (MK / 2), stage_bytes = mx_stage_bytes(bn);
+    const uint32_t z = cluster_ctarank();
+    const int tile = int(blockIdx.x) / p.split;
+    const int m0 = (tile % p.n_mt) * MM, n0 = (tile / p.n_mt) * bn;
+    const int nk = (p.K + MK - 1) / MK;
+    const int kb0 = int(int64_t(nk) * z / p.split), kb1 = int(int64_t(nk) * (z + 1) / p.split);
+    const int chains = (kb1 - kb0 + p.chain - 1) / p.chain;
+    // the same in every CTA of the launch
+    const bool cut = (nk + p.split - 1) / p.split > p.chain;
+    const uint32_t tmem_cols = mx_columns(bn, cut);
+    volatile int *abort_flag = &ctl.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.acc_full[b], 1);
+            mbar_init(&ctl.acc_empty[b], 4);  // the accumulator warps
+        }
+        mbar_init(&ctl.done, 1);
+        ctl.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&maps.a);
+        prefetch_tmap(&maps.b);
+    }
+    __syncwarp();
+    cluster_arrive();
+    if (warp == 1) {
+        tmem_alloc(&ctl.tmem_base, tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = ctl.tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, issued_par = 0;
+        const bool one = elect_one();
+        bool ok = true;
+        const int64_t a_at = int64_t(m0 / 128) * p.k_tiles, b_at = int64_t(n0 / 128) * p.k_tiles;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
+            if (!ok)
+                break;
+            if (one) {
+                uint64_t *fb = &ctl.full[stage];
+                const uint32_t tiles = uint32_t(min(2, p.k_tiles - 2 * kb)) * kMxTileBytes;
+                mbar_arrive_expect_tx(fb, kMxATile + b_bytes + 2 * tiles);
+                uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kMxATile, *ss = sb + b_bytes;
+                tma_load_2d(sa, &maps.a, fb, kb * (MK / 2), m0);
+                tma_load_2d(sb, &maps.b, fb, kb * (MK / 2), n0);
+                bulk_load(ss, p.a_scales + (a_at + 2 * kb) * kMxTileBytes, tiles, fb);
+                bulk_load(ss + kMxScales, p.b_scales + (b_at + 2 * kb) * kMxTileBytes, tiles, fb);
+            }
+            __syncwarp();
+            issued |= 1u << stage;
+            issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {  // stopped: let the copies already issued land
+            report_timeout(p.status);
+            for (int s = 0; s < S; ++s)
+                if ((issued >> s) & 1u)
+                    lin_drain(&ctl.full[s], (issued_par >> s) & 1u);
+        }
+    } else if (warp == 1) {
+        // the whole warp walks the loop and one lane issues
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint32_t sa = smem_u32(smem), sb = sa + kMxATile, ss = sb + b_bytes;
+        const uint64_t da0 = smem_desc_sw128(sa, 16, 1024), db0 = smem_desc_sw128(sb, 16, 1024);
+        const uint64_t ds0 = smem_desc_rows16(ss);
+        const uint32_t scales = tmem_base + tmem_cols - kMxScaleCols;
+        const bool one = elect_one();
+        uint32_t d = tmem_base, aphase = 0;
+        int left = p.chain, buf = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (cut && left == p.chain) {
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                d = tmem_base + uint32_t(buf * bn);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            if (one) {
+                const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
+                const int rest = p.K - kb * MK;
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i)
+                    if (rest > int(i) * 128) {
+                        tc_copy_32x128b(scales + 4 * i, ds0 + off + i * (kMxTileBytes >> 4));
+                        tc_copy_32x128b(scales + 8 + 4 * i,
+                                        ds0 + off + ((kMxScales + i * kMxTileBytes) >> 4));
+                    }
+#pragma unroll
+                for (uint32_t kk = 0; kk < 4; ++kk)
+                    if (rest > int(kk) * 64)
+                        tc_mma_mxf4(d, da0 + off + kk * 2, db0 + off + kk * 2,
+                                    idesc_mxf4(MM, uint32_t(bn), kk & 1), scales + 4 * (kk >> 1),
+                                    scales + 8 + 4 * (kk >> 1), left != p.chain || kk != 0);
+                tc_commit(&ctl.empty[stage]);
+            }
+            if (--left == 0 || kb + 1 == kb1) {
+                left = p.chain;
+                if (cut) {
+                    if (one)
+                        tc_commit(&ctl.acc_full[buf]);
+                    if (++buf == 2) {
+                        buf = 0;
+                        aphase ^= 1u;
+                    }
+                }
+            }
+            __syncwarp();
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok)
+            report_timeout(p.status);
+        if (one)
+            tc_commit(&ctl.done);  // arrives once everything issued here has completed
+    }
+    // CTA z of the cluster finishes 128 / Z of the tile's m: every CTA sends it
+    // its sums of those, and it adds them in rank order.  They go beside the
+    // ring, which may still be in use there, or (128 columns) into the ring
+    // once every CTA is done with it.
+    const bool beside = bn < MM;
+    float *acc = reinterpret_cast<float *>(smem + (beside ? S * stage_bytes : 0u));
+    const int slice = MM / p.split, pitch = bn + 4;  // acc: [Z][128 / Z][pitch]
+    const int cols = min(bn, p.N - n0);
+    // what a thread finishes: four neighbouring m, always the same, of every `by`-th n
+    const int quads = slice / 4, by = kMxThreads / quads;
+    const int mq = int(threadIdx.x) % quads * 4, at = m0 + int(z) * slice + mq;
+    const int left = min(4, p.M - at);
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bias[i] = p.bias && i < left ? p.bias[at + i] : 0.0f;
+    bool done = false;
+    if (warp >= 2) {
+        const uint32_t lanes = tmem_base + (uint32_t(warp & 3) << 21);
+        for (int i = 0; cut && i < chains; ++i) {
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(&ctl.acc_full[i & 1], (i >> 1) & 1, abort_flag))) {
+                report_timeout(p.status);
+                break;
+            }
+            tc_fence_after_sync();
+            add_small_chain(lanes + uint32_t((i & 1) * bn), lanes + uint32_t(2 * bn), bn, i > 0);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl.acc_empty[i & 1]);
+        }
+        __syncwarp();
+        done = mbar_wait(&ctl.done, 0, abort_flag);
+        if (!done) {  // stopped: the MMAs in flight still read shared and write tensor memory
+            report_timeout(p.status);
+            lin_drain(&ctl.done, 0);
+        }
+        done = __all_sync(0xffffffffu, done) && kb1 > kb0;
+    }
+    __syncwarp();
+    cluster_wait();  // every CTA of the cluster has started
+    if (!beside)
+        cluster_sync();
+    if (warp >= 2) {
+        tc_fence_after_sync();
+        const int m = (warp & 3) * 32 + int(lane);
+        const uint32_t t0 = tmem_base + (uint32_t(warp & 3) << 21) + uint32_t(cut ? 2 * bn : 0);
+        const uint32_t to = dsmem_addr(acc + (int(z) * slice + m % slice) * pitch, m / slice);
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+            uint32_t r[16] = {};
+            if (done) {
+                tmem_ld_32x32b_x16(t0 + uint32_t(c), r);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                dsmem_st4(to + uint32_t(c + j) * 4, r[j], r[j + 1], r[j + 2], r[j + 3]);
+        }
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    cluster_sync();
+    auto finish = [&](auto count) {
+        constexpr int R = decltype(count)::value;
+#pragma unroll 1
+        for (int n = int(threadIdx.x) / quads; n < cols; n += R * by) {
+            float v[R][4];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = bias[j];
+                if (i == 0 || n + i * by < cols) {
+                    const float *a = acc + mq * pitch + n + i * by;
+                    for (int r = 0; r < p.split; ++r, a += slice * pitch) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[i][j] += a[j * pitch];
+                    }
+                }
+            }
+            finish_rows<R>(p, v, n0 + n, by, cols - n, at, left);
+        }
+    };
+    if (left > 0) {
+        if (cols <= by)
+            finish(std::integral_constant<int, 1>());
+        else
+            finish(std::integral_constant<int, 4>());
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, tmem_cols);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------
+
+// Codes [rows, K / 2]: boxes of 128 bytes x box_rows rows with the 128-byte swizzle.
+cudaError_t mx_map(CUtensorMap *m, const uint8_t *codes, int64_t rows, int K, int box_rows)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cuuint64_t(K) / 2, cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(K) / 2};
+    const cuuint32_t box[2] = {MK / 2, cuuint32_t(box_rows)}, estr[2] = {1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct MxProduct {
+    const uint8_t *x, *x_scales, *W, *W_scales;
+    int T, K, N;
+    EpiArgs epi;
+    uint32_t *status;
+};
+
+constexpr size_t kMxLoneSmem = 226 * 1024;  // of a CTA that takes all of an SM's tensor memory
+
+cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
+{
+    const int sms = device_sm_count(), nk = (q.K + MK - 1) / MK;
+    MxArgs a = {};
+    static_cast<EpiArgs &>(a) = q.epi;
+    a.status = q.status;
+    a.a_scales = q.W_scales, a.b_scales = q.x_scales;
+    a.M = q.N, a.N = q.T, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
+    a.bn = q.T <= 16 ? 16 : q.T <= 32 ? 32 : q.T <= 64 ? 64 : 128;
+    a.chain = mx_chain(a.out_f32, a.f16);
+    a.n_mt = (q.N + MM - 1) / MM;
+    const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.T) + a.bn - 1) / a.bn);
+    // split the reduction while the CTAs still fit at once and each has two stages
+    a.split = 1;
+    while (a.split < kMxMaxSplit && tiles * a.split * 2 <= 2 * sms && nk / (a.split * 2) >= 2)
+        a.split *= 2;
+    if (tiles * a.split > INT_MAX)
+        return cudaErrorInvalidValue;
+    const uint32_t stage = mx_stage_bytes(a.bn);
+    const uint32_t parts = a.bn < MM ? uint32_t(MM) * (a.bn + 4) * 4 : 0;
+    a.stages = std::min<int>(kMxMaxStages, (110 * 1024 - parts) / stage);
+    size_t smem = 1024 + std::max<size_t>(size_t(a.stages) * stage + parts,
+                                          a.bn < MM ? 0 : size_t(MM) * (a.bn + 4) * 4);
+    // Two CTAs share an SM's 512 columns of tensor memory.  One that takes them
+    // all must be alone there, be the other of its own cluster or of another
+    // kernel's: two clusters that each wait for tensor memory the other holds
+    // would wait for ever.
+    if (mx_columns(a.bn, (nk + a.split - 1) / a.split > a.chain) > 256)
+        smem = kMxLoneSmem;
+    MxMaps maps;
+    cudaError_t e = mx_map(&maps.a, q.W, q.N, q.K, MM);
+    if (e == cudaSuccess)
+        e = mx_map(&maps.b, q.x, q.T, q.K, a.bn);
+    const void *kern = reinterpret_cast<const void *>(k_linear_mx);
+    if (e == cudaSuccess)
+        e = ensure_smem_limit(kern, kSlotLinearMx, kMxLoneSmem);
+    if (e != cudaSuccess)
+        return e;
+    void *args[] = {&maps, &a};
+    return launch_clustered(kern, unsigned(tiles * a.split), unsigned(a.split), kMxThreads, smem, s,
+                            args);
+}
+
+}  // namespace
+
+uint32_t *linear_mx_status_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_status) == cudaSuccess ? static_cast<uint32_t *>(p) : nullptr;
+}
+
+}  // namespace moe
+
+extern "C" int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W,
+                                const uint8_t *W_scales, const float *bias, const void *residual,
+                                int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy,
+                                int y_dtype, uint32_t *status, moe_stream_t stream)
+{
+    using namespace moe;
+    constexpr int kMost = INT_MAX - 511;
+    if (y_dtype != MOE_DT_BF16 && y_dtype != MOE_DT_F16 && y_dtype != MOE_DT_F32)
+        return MOE_ERR_DTYPE;
+    if (T < 0 || T > kMost || K < 32 || K > kMost || K % 32 != 0 || N < 1 || N > kMost ||
+        act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH || ldy < N || (residual && ldr < N))
+        return MOE_ERR_SHAPE;
+    if (!W || !W_scales || (T > 0 && (!x || !x_scales || !y)))
+        return MOE_ERR_NULL;
+    const int size = dtype_size(y_dtype);
+    if (!aligned(x, 16) || !aligned(x_scales, 16) || !aligned(W, 16) || !aligned(W_scales, 16) ||
+        !aligned(bias, 4) || !aligned(residual, size) || !aligned(y, size) || !aligned(status, 4))
+        return MOE_ERR_ALIGN;
+    if (T == 0)
+        return MOE_OK;
+    EpiArgs e = {};
+    e.bias = bias, e.residual = residual, e.out = y;
+    e.ldr = ldr, e.ldo = ldy;
+    e.f16 = y_dtype == MOE_DT_F16, e.out_f32 = y_dtype == MOE_DT_F32, e.act = act;
+    e.vec_out = vec16(y, ldy, size), e.vec_res = vec16(residual, ldr, size);
+    const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status};
+    return launch_mx_small(q, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+                                                                                     : MOE_ERR_CUDA;
+}

@@ -1,0 +1,202 @@
+// Rows to MXFP4 and back (moe_quantize_rows_mxfp4, moe_dequantize_rows_mxfp4).
+// The format: mx_rows.cuh.
+//
+// Both are bound by memory.  A thread has eight elements, sixteen lanes a scale
+// tile's 128 of one row; a warp takes pieces of 128 two at a time, four such
+// steps' loads in flight.
+#include "../../include/moe_prefill.h"
+#include "internal.h"
+#include "mx_rows.cuh"
+#include "ptx.cuh"
+
+#include <algorithm>
+#include <climits>
+
+namespace moe {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kPieces = kRowThreads / 16;  // of 128 elements, of a CTA at a time
+constexpr int kAhead = 4;
+constexpr int kRowCtas = 8;  // an SM
+
+struct MxRowsArgs {
+    const void *x;  // rows to quantise, or null
+    void *y;        // rows to write
+    int64_t ld;
+    uint8_t *codes, *scales;
+    int64_t rows, all_rows;  // all_rows: of the scale tiles
+    int K, k_tiles, vec;
+};
+
+// Walks pieces (row, tile along K) with one division at the start.
+struct Piece {
+    int64_t row;
+    int kt;
+
+    __device__ Piece(int64_t i, int k_tiles) : row(i / k_tiles), kt(int(i % k_tiles)) {}
+
+    __device__ __forceinline__ void advance(int64_t rows, int tiles, int k_tiles)
+    {
+        row += rows;
+        kt += tiles;
+        if (kt >= k_tiles) {
+            kt -= k_tiles;
+            ++row;
+        }
+    }
+};
+
+template <typename E>
+__global__ void __launch_bounds__(kRowThreads, 4) k_quant_rows(const MxRowsArgs p)
+{
+    const int lane = threadIdx.x & 15;
+    const int64_t step = int64_t(gridDim.x) * kPieces;
+    const int64_t step_rows = step / p.k_tiles;
+    const int step_tiles = int(step % p.k_tiles);
+    Piece at(int64_t(blockIdx.x) * kPieces + (threadIdx.x >> 4), p.k_tiles);
+    pdl_wait();
+    pdl_launch_dependents();
+    // (both halves of a warp walk on while one of them has rows left)
+    while (__any_sync(0xffffffffu, at.row < p.all_rows)) {
+        Oct<E> in[kAhead];
+        Piece of[kAhead] = {at, at, at, at};
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            of[u] = at;
+            const int c = at.kt * 128 + lane * 8;
+            in[u].load(static_cast<const E *>(p.x) + (at.row < p.rows ? at.row * p.ld + c : 0),
+                       at.row < p.rows ? p.K - c : 0, p.vec);
+            at.advance(step_rows, step_tiles, p.k_tiles);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            float v[8];
+            in[u].to(v);
+            const uint32_t byte = mx_scale_byte(max_of_block(max_bits8(v)));
+            const uint32_t word = word_of_tile(byte);
+            const int c = of[u].kt * 128 + lane * 8;
+            if (of[u].row < p.rows && c < p.K)
+                *reinterpret_cast<uint32_t *>(p.codes + of[u].row * (p.K / 2) + c / 2) =
+                    mx_encode8(v, byte);
+            if (lane == 0 && of[u].row < p.all_rows)
+                *mx_scale_word(p.scales, of[u].row, of[u].kt, p.k_tiles) = word;
+        }
+    }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArgs p)
+{
+    const int lane = threadIdx.x & 15;
+    const int64_t step = int64_t(gridDim.x) * kPieces;
+    const int64_t step_rows = step / p.k_tiles;
+    const int step_tiles = int(step % p.k_tiles);
+    Piece at(int64_t(blockIdx.x) * kPieces + (threadIdx.x >> 4), p.k_tiles);
+    pdl_wait();
+    pdl_launch_dependents();
+    while (at.row < p.rows) {
+        uint32_t code[kAhead], word[kAhead];
+        Piece of[kAhead] = {at, at, at, at};
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            of[u] = at;
+            const int c = at.kt * 128 + lane * 8;
+            code[u] = word[u] = 0;
+            if (at.row < p.rows && c < p.K) {
+                code[u] = __ldcs(
+                    reinterpret_cast<const uint32_t *>(p.codes + at.row * (p.K / 2) + c / 2));
+                word[u] = *mx_scale_word(p.scales, at.row, at.kt, p.k_tiles);
+            }
+            at.advance(step_rows, step_tiles, p.k_tiles);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = of[u].kt * 128 + lane * 8;
+            if (of[u].row >= p.rows || c >= p.K)
+                continue;
+            float v[8];
+            mx_decode8(code[u], (word[u] >> (8 * (lane >> 2))) & 0xffu, v);
+            Oct<E> out;
+            out.from(v);
+            out.store(static_cast<E *>(p.y) + of[u].row * p.ld + c, p.K - c, p.vec);
+        }
+    }
+}
+
+cudaError_t launch(void (*kern)(MxRowsArgs), const MxRowsArgs &a, int64_t rows, cudaStream_t s)
+{
+    const int64_t pieces = rows * a.k_tiles;
+    const int64_t ctas = std::min<int64_t>((pieces + kPieces - 1) / kPieces,
+                                           int64_t(device_sm_count()) * kRowCtas);
+    return launch_pdl(kern, dim3(unsigned(ctas)), dim3(kRowThreads), 0, s, a);
+}
+
+inline bool aligned(const void *p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+int check(const void *x, int64_t ld, int dtype, int rows, int K, const uint8_t *codes,
+          const uint8_t *scales)
+{
+    if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16 && dtype != MOE_DT_F32)
+        return MOE_ERR_DTYPE;
+    if (rows < 0 || rows > INT_MAX - 511 || K < 32 || K % 32 != 0 || K > INT_MAX - 511 || ld < K)
+        return MOE_ERR_SHAPE;
+    if (rows > 0 && (!x || !codes || !scales))
+        return MOE_ERR_NULL;
+    if (!aligned(x, dtype_size(dtype)) || !aligned(codes, 16) || !aligned(scales, 16))
+        return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" size_t moe_mxfp4_scale_bytes(int rows, int K)
+{
+    return rows < 0 || K < 32 || K % 32 != 0 ? 0 : size_t(moe::mx_scale_bytes(rows, K));
+}
+
+extern "C" int moe_quantize_rows_mxfp4(const void *x, int64_t ldx, int dtype, int rows, int K,
+                                       uint8_t *codes, uint8_t *scales, moe_stream_t stream)
+{
+    using namespace moe;
+    const int rc = check(x, ldx, dtype, rows, K, codes, scales);
+    if (rc != MOE_OK || rows == 0)
+        return rc;
+    MxRowsArgs a = {};
+    a.x = x, a.ld = ldx, a.codes = codes, a.scales = scales;
+    a.rows = rows, a.all_rows = (int64_t(rows) + 127) / 128 * 128;
+    a.K = K, a.k_tiles = mx_k_tiles(K);
+    a.vec = rows_vec(x, ldx, dtype_size(dtype));
+    const auto kern = dtype == MOE_DT_F32   ? k_quant_rows<float>
+                      : dtype == MOE_DT_F16 ? k_quant_rows<__half>
+                                            : k_quant_rows<__nv_bfloat16>;
+    return launch(kern, a, a.all_rows, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+extern "C" int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scales, int rows,
+                                         int K, void *y, int64_t ldy, int dtype,
+                                         moe_stream_t stream)
+{
+    using namespace moe;
+    if (dtype == MOE_DT_F16)  // does not hold every scale
+        return MOE_ERR_DTYPE;
+    const int rc = check(y, ldy, dtype, rows, K, codes, scales);
+    if (rc != MOE_OK || rows == 0)
+        return rc;
+    MxRowsArgs a = {};
+    a.y = y, a.ld = ldy;
+    a.codes = const_cast<uint8_t *>(codes), a.scales = const_cast<uint8_t *>(scales);
+    a.rows = a.all_rows = rows;
+    a.K = K, a.k_tiles = mx_k_tiles(K);
+    a.vec = rows_vec(y, ldy, dtype_size(dtype));
+    const auto kern = dtype == MOE_DT_F32 ? k_dequant_rows<float> : k_dequant_rows<__nv_bfloat16>;
+    return launch(kern, a, rows, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}

@@ -1,0 +1,196 @@
+// Rows in MXFP4 (OCP Microscaling: 4-bit E2M1 elements, one power-of-two scale
+// for each 32 along the row) in the layout that tcgen05.mma.kind::mxf4 reads,
+// and rows of 16-bit or fp32 elements eight at a time.
+//
+// Codes [rows, K / 2]: element 2i in the low half of byte i.  Scales: byte S of
+// 2^(S - 127), in tiles of 128 rows x 4 blocks (128 of K) of 512 bytes,
+// [ceil(rows / 128), ceil(K / 128), 512]: of a tile, row 32 q + l, block b at
+// byte 16 l + 4 q + b, so that one tcgen05.cp (32 lanes x 16 bytes) brings a
+// tile into the four columns of tensor memory where the MMA looks for it.
+// What lies past the last row or block is 0.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kMxTileBytes = 512;
+
+__host__ __device__ __forceinline__ int mx_k_tiles(int K)
+{
+    return (K + 127) / 128;
+}
+
+inline int64_t mx_scale_bytes(int64_t rows, int K)
+{
+    return (rows + 127) / 128 * mx_k_tiles(K) * kMxTileBytes;
+}
+
+// Where the four scale bytes of row t, tile kt along K, are (a 32-bit word).
+__device__ __forceinline__ uint32_t *mx_scale_word(uint8_t *scales, int64_t t, int kt, int k_tiles)
+{
+    return reinterpret_cast<uint32_t *>(scales + ((t >> 7) * k_tiles + kt) * kMxTileBytes +
+                                        (t & 31) * 16 + ((t >> 5) & 3) * 4);
+}
+
+// The scale byte of a block whose largest |v| has these bits:
+// floor(log2 max) - 2 (2: the exponent of E2M1's largest value, 6 = 1.5 x 2^2),
+// at least -127; 255 (NaN) where an element is a NaN or an infinity.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t max_bits)
+{
+    const int f = int(max_bits >> 23);
+    return f == 255 ? 255u : uint32_t(max(f - 2, 0));
+}
+
+// Eight elements (v 2^-x, x = byte - 127) to codes: nearest, ties to the even
+// code, past 6 saturated, the sign kept; 0 for a block without a finite scale.
+__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t byte)
+{
+    if (byte == 255u)
+        return 0u;
+    const float r = __uint_as_float((254u - byte) << 23);  // byte <= 252: 2^-125 at least
+    uint32_t w;
+    asm("{\n"
+        ".reg .b8 a, b, c, d;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        "mov.b32 %0, {a, b, c, d};\n"
+        "}\n"
+        : "=r"(w)
+        : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r), "f"(v[4] * r),
+          "f"(v[5] * r), "f"(v[6] * r), "f"(v[7] * r));
+    return w;
+}
+
+// What eight codes and their scale byte stand for (exact in bf16 and fp32).
+__device__ __forceinline__ void mx_decode8(uint32_t w, uint32_t byte, float (&v)[8])
+{
+    uint32_t h[4];
+    asm("{\n"
+        ".reg .b8 a, b, c, d;\n"
+        "mov.b32 {a, b, c, d}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n"
+        "}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+    // 2^-127 is subnormal; 255 stands for NaN
+    const float s = byte == 0u     ? __uint_as_float(1u << 22)
+                    : byte == 255u ? __uint_as_float(0x7fc00000u)
+                                   : __uint_as_float(byte << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x * s;
+        v[2 * i + 1] = f.y * s;
+    }
+}
+
+// The largest of four neighbouring lanes' values (a block of 32: eight a lane).
+__device__ __forceinline__ uint32_t max_of_block(uint32_t m)
+{
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// The four scale bytes of sixteen neighbouring lanes as a word (in every lane).
+__device__ __forceinline__ uint32_t word_of_tile(uint32_t byte)
+{
+    uint32_t w = byte << (8 * ((threadIdx.x >> 2) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    return w | __shfl_xor_sync(0xffffffffu, w, 8);
+}
+
+// The bits of the largest |v| of a lane's eight.
+__device__ __forceinline__ uint32_t max_bits8(const float (&v)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+
+// ---- eight neighbouring elements of a row ----------------------------------------
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_float(float v, float &o) { o = v; }
+__device__ __forceinline__ void from_float(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_float(float v, __half &o) { o = __float2half_rn(v); }
+
+// As they are stored.
+template <typename E>
+struct alignas(16) Oct {
+    E e[8];
+
+    // The first n exist (the others are 0); vec: 16-byte accesses are aligned.
+    __device__ __forceinline__ void load(const E *p, int n, bool vec)
+    {
+        constexpr int kQ = sizeof(E) == 4 ? 2 : 1;
+        if (vec && n >= 8) {
+            uint4 q[kQ];
+#pragma unroll
+            for (int i = 0; i < kQ; ++i)
+                q[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            memcpy(e, q, sizeof(e));
+        } else {
+            E zero;
+            from_float(0.0f, zero);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                e[i] = i < n ? p[i] : zero;
+        }
+    }
+
+    __device__ __forceinline__ void store(E *p, int n, bool vec) const
+    {
+        constexpr int kQ = sizeof(E) == 4 ? 2 : 1;
+        if (vec && n >= 8) {
+            uint4 q[kQ];
+            memcpy(q, e, sizeof(e));
+#pragma unroll
+            for (int i = 0; i < kQ; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = q[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n)
+                    p[i] = e[i];
+        }
+    }
+
+    __device__ __forceinline__ void to(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = to_float(e[i]);
+    }
+
+    __device__ __forceinline__ void from(const float (&v)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            from_float(v[i], e[i]);
+    }
+};
+
+// Whether 16-byte pieces of rows `ld` elements apart are aligned accesses.
+inline bool rows_vec(const void *p, int64_t ld, int size)
+{
+    return ld * size % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+inline int dtype_size(int dtype)
+{
+    return dtype == 2 ? 4 : 2;  // MOE_DT_F32, or a 16-bit type
+}
+
+}  // namespace moe

@@ -241,6 +241,17 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
+// `bytes` contiguous bytes (both addresses and the size multiples of 16).
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // ---- TMA stores (shared -> global, bulk groups) -------------------------------
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int32_t c0,
@@ -360,6 +371,34 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         "}\n" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// D[tmem] (+)= A[smem] x B[smem]^T with both operands in MXFP4 (E2M1 codes, two
+// a byte, and a power-of-two scale for each 32 along K), fp32 accumulator,
+// K = 64 per instruction.  The scales are in tensor memory: of a row 32 q + l,
+// lane l of each of the four lane quadrants, column q from the given address
+// on, two neighbouring bytes of it (which two: the instruction descriptor).
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t a_scales, uint32_t b_scales,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows of 16 bytes of shared memory to lanes 0 - 31 of each of the four
+// quadrants of tensor memory, four columns.
+__device__ __forceinline__ void tc_copy_32x128b(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
 }
 
 // The same operations for a pair of CTAs (cta_group::2).  One MMA of M = 256:
@@ -525,6 +564,24 @@ __host__ __device__ __forceinline__ constexpr uint32_t idesc_bf16_f32(uint32_t M
 __host__ __device__ __forceinline__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N)
 {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Instruction descriptor of tcgen05.mma.kind::mxf4, K = 64: bits 7-9 and 10-12
+// the formats (1 = E2M1), bit 23 the scales' type (1 = a power of two), bits
+// 4-5 and 29-30 which bytes of a column hold B's and A's scales (0: the low
+// two, 2: the high two); the rest as above.
+__host__ __device__ __forceinline__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N,
+                                                                  uint32_t half)
+{
+    return (1u << 7) | (1u << 10) | (1u << 23) | ((N >> 3) << 17) | ((M >> 7) << 27) |
+           (half << 5) | (half << 30);
+}
+
+// Shared-memory descriptor of 32 contiguous rows of 16 bytes, not swizzled
+// (8-row groups 128 bytes apart), for tc_copy_32x128b.
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (8ull << 32) | (1ull << 46);
 }
 
 }  // namespace moe
