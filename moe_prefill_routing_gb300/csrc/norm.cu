@@ -20,6 +20,7 @@
 #include "ptx.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -28,6 +29,7 @@ namespace {
 
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxD = kNormMaxThreads * 8 * 4;
+constexpr int kNormStages = 3;      // rows of a ring
 constexpr int kNormGradCtas = 608;  // at most: rows of partial column sums
 constexpr int kSumThreads = 256;
 
@@ -57,10 +59,10 @@ struct NormGradArgs {
     float alpha, eps;
 };
 
-// Sums of N values over the CTA's threads, in every thread; one barrier, two
-// sets of words in turn.
+// Sums of N <= 4 values over the CTA's threads, in every thread; one barrier,
+// two sets of words in turn.
 struct BlockSum {
-    float (*red)[3][kNormMaxThreads / 32];
+    float4 (*red)[kNormMaxThreads / 32];
     int turn;
 
     template <int N>
@@ -74,74 +76,216 @@ struct BlockSum {
         const int warps = int(blockDim.x) >> 5;
         if (warps == 1)
             return;
-        if ((threadIdx.x & 31) == 0) {
+        if ((threadIdx.x & 31) == 0)
+            red[turn][threadIdx.x >> 5] = make_float4(v[0], N > 1 ? v[N > 1] : 0.0f,
+                                                      N > 2 ? v[N > 2 ? 2 : 0] : 0.0f, 0.0f);
+        __syncthreads();
+        // every warp adds the warps' sums (16 at most) across its lanes
+        const int lane = int(threadIdx.x) & 31;
+        const float4 s = lane < warps ? red[turn][lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        v[0] = s.x;
+        if (N > 1)
+            v[N > 1] = s.y;
+        if (N > 2)
+            v[N > 2 ? 2 : 0] = s.z;
+#pragma unroll
+        for (int o = 8; o; o >>= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                red[turn][i][threadIdx.x >> 5] = v[i];
-        }
-        __syncthreads();
+                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float s = 0.0f;
-            for (int w = 0; w < warps; ++w)
-                s += red[turn][i][w];
-            v[i] = s;
-        }
+        for (int i = 0; i < N; ++i)
+            v[i] = __shfl_sync(0xffffffffu, v[i], 0);
         turn ^= 1;
     }
 };
 
-__device__ __forceinline__ float gate_of(const float *gate, int sigmoid, int64_t t)
+__device__ __forceinline__ float gate_of(float g, bool some, int sigmoid)
 {
-    if (!gate)
-        return 1.0f;
-    const float g = gate[t];
-    return sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
+    return !some ? 1.0f : sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
 }
 
-// Eight weights of a row of d (1 where there are none), 0 past its end.
-__device__ __forceinline__ void load_weights(float (&w)[8], const float *p, int c, int d)
-{
+// Rows of a tensor of [rows, d].  RING: cp.async brings them ahead of their use
+// into slots of shared memory of the thread that reads them, so that what is in
+// flight takes neither barriers nor registers (16-byte pieces are aligned then,
+// and d a multiple of 8).  Otherwise they are read when they are used.  A tensor
+// that is not there reads as zeros.
+template <typename E, int R, bool RING>
+struct Rows {
+    static constexpr int kPieces = sizeof(E) == 4 ? 2 : 1;  // of 16 bytes: eight elements
+    const E *p;
+    int64_t ld;
+    int d, vec;
+    uint4 *slots;  // [stage][kPieces][threads]
+
+    __device__ __forceinline__ Rows(const void *tensor, int64_t ld_, int d_, int vec_,
+                                    uint8_t *&smem)
+        : p(static_cast<const E *>(tensor)), ld(ld_), d(d_), vec(vec_),
+          slots(reinterpret_cast<uint4 *>(smem))
+    {
+        static_assert(!RING || R == 1, "longer rows do not fit");
+        if (RING) {
+            const int G = int(blockDim.x), t = int(threadIdx.x);
+            smem += kNormStages * kPieces * G * 16;
+            if (!p || t * 8 >= d)  // never fetched
+                for (int i = 0; i < kNormStages * kPieces; ++i)
+                    slots[i * G + t] = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    __device__ __forceinline__ void fetch(int64_t row, int stage) const
+    {
+        const int G = int(blockDim.x), t = int(threadIdx.x);
+        if (RING && p && t * 8 < d) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i] = c + i >= d ? 0.0f : p ? p[c + i] : 1.0f;
+            for (int q = 0; q < kPieces; ++q)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(slots + (stage * kPieces + q) * G + t)),
+                             "l"(reinterpret_cast<const uint4 *>(p + row * ld) + t * kPieces + q)
+                             : "memory");
+        }
+    }
+
+    __device__ __forceinline__ Oct<E> read(int64_t row, int stage, int r) const
+    {
+        const int G = int(blockDim.x), t = int(threadIdx.x), c = (t + r * G) * 8;
+        Oct<E> o;
+        if (RING) {
+            uint4 v[kPieces];
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q)
+                v[q] = slots[(stage * kPieces + q) * G + t];
+            memcpy(o.e, v, sizeof(o.e));
+        } else {
+            o.load(p + (p ? row * ld + c : 0), p ? d - c : 0, vec);
+        }
+        return o;
+    }
+};
+
+// A thread's eight elements of a row to memory.
+template <bool RING, typename E>
+__device__ __forceinline__ void put(void *p, int64_t ld, int64_t row, int c, int d, int vec,
+                                    const Oct<E> &o)
+{
+    if (!RING || c < d)
+        o.store(static_cast<E *>(p) + row * ld + c, RING ? 8 : d - c, RING || vec);
 }
 
-template <typename S, typename B, int R>
+// Weights of a row (1 where there are none, 0 past its end): in registers where
+// a thread has eight, in shared memory where it has more.
+template <int R>
+struct Weights {
+    float w[R == 1 ? 8 : 1];
+    float4 *slots;
+
+    __device__ __forceinline__ void load(const float *p, int d, uint8_t *&smem)
+    {
+        const int G = int(blockDim.x), t = int(threadIdx.x);
+        slots = reinterpret_cast<float4 *>(smem);
+        if (R > 1)
+            smem += R * 2 * G * 16;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (t + r * G) * 8;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = c + i >= d ? 0.0f : p ? p[c + i] : 1.0f;
+            if (R == 1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[R == 1 ? i : 0] = v[i];
+            } else {
+                slots[(2 * r) * G + t] = make_float4(v[0], v[1], v[2], v[3]);
+                slots[(2 * r + 1) * G + t] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void get(int r, float (&v)[8]) const
+    {
+        if (R == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = w[R == 1 ? i : 0];
+        } else {
+            const int G = int(blockDim.x), t = int(threadIdx.x);
+            const float4 a = slots[(2 * r) * G + t], b = slots[(2 * r + 1) * G + t];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+    }
+};
+
+__device__ __forceinline__ void async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Until only the latest kNormStages - 1 groups are on their way.
+__device__ __forceinline__ void async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kNormStages - 1) : "memory");
+}
+
+template <typename S, typename B, int R, bool RING>
 __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p)
 {
-    __shared__ float red[2][3][kNormMaxThreads / 32];
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ float4 red[2][kNormMaxThreads / 32];
     BlockSum sum{red, 0};
     const int G = int(blockDim.x);
     const float inv_d = 1.0f / float(p.d);
+    uint8_t *smem = smem_raw;
+    const Rows<S, R, RING> xs(p.x, p.ldx, p.d, p.vec_x, smem);
+    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, smem);
     pdl_wait();
     pdl_launch_dependents();
-    float pre[R][8], post[R][8];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = (int(threadIdx.x) + r * G) * 8;
-        load_weights(pre[r], p.pre, c, p.d);
-        load_weights(post[r], p.post, c, p.d);
-    }
-    const int rows = p.codes ? (p.T + 127) / 128 * 128 : p.T;
-    for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
-        const bool live = t < p.T && (!p.mask || p.mask[t]);
+    const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T, step = gridDim.x;
+    auto is_live = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
+    // the rows of the next two turns are on their way while one is worked on
+    int64_t ahead = blockIdx.x;
+    int in = 0;
+    auto fetch = [&](bool live) {
+        if (live) {
+            xs.fetch(ahead, in);
+            os.fetch(ahead, in);
+        }
+        async_commit();
+        ahead += step;
+        if (++in == kNormStages)
+            in = 0;
+    };
+    bool live = is_live(blockIdx.x);
+    fetch(live);
+    bool next = is_live(ahead);
+    float gate = p.gate && live ? p.gate[blockIdx.x] : 0.0f;
+    fetch(next);
+    Weights<R> pre, post;
+    pre.load(p.pre, p.d, smem);
+    post.load(p.post, p.d, smem);
+    bool coming = is_live(ahead);
+    int out = 0;
+    for (int64_t t = blockIdx.x; t < rows; t += step) {
+        const bool third = coming;
+        fetch(third);
+        coming = is_live(ahead);
+        const float g = gate_of(gate, p.gate, p.sigmoid);
+        gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
+        async_wait();
         float v[R][8];
         if (live) {
             Oct<S> x[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int c = (int(threadIdx.x) + r * G) * 8;
-                x[r].load(static_cast<const S *>(p.x) + t * p.ldx + c, p.d - c, p.vec_x);
-            }
+            for (int r = 0; r < R; ++r)
+                x[r] = xs.read(t, out, r);
             if (p.o) {
                 Oct<B> o[R];
-                float k = gate_of(p.gate, p.sigmoid, t);
+                float k = g;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int c = (int(threadIdx.x) + r * G) * 8;
-                    o[r].load(static_cast<const B *>(p.o) + t * p.ldo + c, p.d - c, p.vec_o);
-                }
+                for (int r = 0; r < R; ++r)
+                    o[r] = os.read(t, out, r);
                 if (p.post_norm) {
                     float s[1] = {0.0f};
 #pragma unroll
@@ -159,14 +303,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const int c = (int(threadIdx.x) + r * G) * 8;
-                    float f[8];
+                    float f[8], w[8];
                     o[r].to(f);
                     x[r].to(v[r]);
+                    post.get(r, w);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[r][i] = p.alpha * v[r][i] + f[i] * (k * post[r][i]);
+                        v[r][i] = p.alpha * v[r][i] + f[i] * (k * w[i]);
                     x[r].from(v[r]);
-                    x[r].store(static_cast<S *>(p.xn) + t * p.ldxn + c, p.d - c, p.vec_xn);
+                    put<RING>(p.xn, p.ldxn, t, c, p.d, p.vec_xn, x[r]);
                 }
             }
 #pragma unroll
@@ -178,70 +323,180 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[r][i] = 0.0f;
-                const int c = (int(threadIdx.x) + r * G) * 8;
                 if (p.o && t < p.T) {
                     Oct<S> zero;
                     zero.from(v[r]);
-                    zero.store(static_cast<S *>(p.xn) + t * p.ldxn + c, p.d - c, p.vec_xn);
+                    put<RING>(p.xn, p.ldxn, t, (int(threadIdx.x) + r * G) * 8, p.d, p.vec_xn, zero);
                 }
             }
         }
-        if (!p.pre)
-            continue;
-        float k = 0.0f;
-        if (live) {
-            float s[1] = {0.0f};
+        if (p.pre) {
+            float k = 0.0f;
+            if (live) {
+                float s[1] = {0.0f};
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        s[0] += v[r][i] * v[r][i];
+                s[0] *= inv_d;
+                sum(s);
+                k = rsqrtf(s[0] + p.eps);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (int(threadIdx.x) + r * G) * 8;
+                float w[8];
+                pre.get(r, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    s[0] += v[r][i] * v[r][i];
-            s[0] *= inv_d;
-            sum(s);
-            k = rsqrtf(s[0] + p.eps);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int c = (int(threadIdx.x) + r * G) * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[r][i] = live ? v[r][i] * k * pre[r][i] : 0.0f;
-            Oct<B> h;
-            h.from(v[r]);
-            if (p.h && t < p.T)
-                h.store(static_cast<B *>(p.h) + t * p.ldh + c, p.d - c, p.vec_h);
-            if (p.codes) {
-                h.to(v[r]);  // codes of h as it is stored
-                const uint32_t byte = mx_scale_byte(max_of_block(max_bits8(v[r])));
-                const uint32_t word = word_of_tile(byte);
-                if (t < p.T && c < p.d)
-                    *reinterpret_cast<uint32_t *>(p.codes + t * (p.d / 2) + c / 2) =
-                        mx_encode8(v[r], byte);
-                if ((threadIdx.x & 15) == 0 && c < p.k_tiles * 128)
-                    *mx_scale_word(p.scales, t, c / 128, p.k_tiles) = word;
+                    v[r][i] = live ? v[r][i] * k * w[i] : 0.0f;
+                Oct<B> h;
+                h.from(v[r]);
+                if (p.h && t < p.T)
+                    put<RING>(p.h, p.ldh, t, c, p.d, p.vec_h, h);
+                if (p.codes) {
+                    h.to(v[r]);  // codes of h as it is stored
+                    const uint32_t byte = mx_scale_byte(max_of_block(max_bits8(v[r])));
+                    const uint32_t word = word_of_tile(byte);
+                    if (t < p.T && c < p.d)
+                        *reinterpret_cast<uint32_t *>(p.codes + t * (p.d / 2) + c / 2) =
+                            mx_encode8(v[r], byte);
+                    if ((threadIdx.x & 15) == 0 && c < p.k_tiles * 128)
+                        *mx_scale_word(p.scales, t, c / 128, p.k_tiles) = word;
+                }
             }
         }
+        live = next;
+        next = third;
+        if (++out == kNormStages)
+            out = 0;
     }
 }
 
-template <typename S, typename B, int R>
-__global__ void __launch_bounds__(kNormMaxThreads) k_block_norm_grad(const NormGradArgs p)
+template <typename S, typename B, int R, bool RING>
+__global__ void __maxnreg__(R == 1 ? 80 : 128) k_block_norm_grad(const NormGradArgs p)
 {
-    __shared__ float red[2][3][kNormMaxThreads / 32];
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ float4 red[2][kNormMaxThreads / 32];
     BlockSum sum{red, 0};
     const int G = int(blockDim.x);
     const float inv_d = 1.0f / float(p.d);
+    uint8_t *smem = smem_raw;
+    const Rows<S, R, RING> xns(p.dh ? p.xn : nullptr, p.ldxn, p.d, p.vec_xn, smem);
+    const Rows<S, R, RING> dxns(p.dxn, p.lddxn, p.d, p.vec_dxn, smem);
+    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, smem);
+    const Rows<B, R, RING> dhs(p.dh, p.lddh, p.d, p.vec_dh, smem);
     pdl_wait();
     pdl_launch_dependents();
-    float pre[R][8], post[R][8], dpre[R][8] = {}, dpost[R][8] = {};
+    const int64_t step = gridDim.x;
+    auto is_live = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
+    int64_t ahead = blockIdx.x;
+    int in = 0;
+    auto fetch = [&](bool live) {
+        if (live) {
+            xns.fetch(ahead, in);
+            dxns.fetch(ahead, in);
+            os.fetch(ahead, in);
+            dhs.fetch(ahead, in);
+        }
+        async_commit();
+        ahead += step;
+        if (++in == kNormStages)
+            in = 0;
+    };
+    bool live = is_live(blockIdx.x);
+    fetch(live);
+    bool next = is_live(ahead);
+    float gate = p.gate && live ? p.gate[blockIdx.x] : 0.0f;
+    fetch(next);
+    Weights<R> pre, post;
+    pre.load(p.pre, p.d, smem);
+    post.load(p.post, p.d, smem);
+    float dpre[R][8] = {}, dpost[R][8] = {};
+    bool coming = is_live(ahead);
+    int out = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += step) {
+        const bool third = coming;
+        fetch(third);
+        coming = is_live(ahead);
+        const float g = gate_of(gate, p.gate, p.sigmoid);
+        gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
+        async_wait();
+        if (live) {
+            Oct<B> o[R], dh[R];
+            Oct<S> xn[R], ds[R];  // (ds: dxn as it came)
+            float s[3] = {};      // xn^2, a xn, o^2
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = (int(threadIdx.x) + r * G) * 8;
-        load_weights(pre[r], p.pre, c, p.d);
-        load_weights(post[r], p.post, c, p.d);
-    }
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        if (p.mask && !p.mask[t]) {
+            for (int r = 0; r < R; ++r) {
+                float x[8], h[8], f[8], w[8];
+                xn[r] = xns.read(t, out, r);
+                dh[r] = dhs.read(t, out, r);
+                o[r] = os.read(t, out, r);
+                ds[r] = dxns.read(t, out, r);
+                xn[r].to(x);
+                dh[r].to(h);
+                o[r].to(f);
+                pre.get(r, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[0] += x[i] * x[i];
+                    s[1] += h[i] * w[i] * x[i];
+                    s[2] += f[i] * f[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                s[i] *= inv_d;
+            sum(s);
+            const float r2 = p.dh ? rsqrtf(s[0] + p.eps) : 0.0f;
+            const float r1 = p.post_norm ? rsqrtf(s[2] + p.eps) : 1.0f;
+            const float c2 = r2 * r2 * r2 * s[1];
+            float q[1] = {0.0f}, d[R][8];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (int(threadIdx.x) + r * G) * 8;
+                float x[8], h[8], f[8], w[8], v[8];
+                xn[r].to(x);
+                dh[r].to(h);
+                o[r].to(f);
+                ds[r].to(d[r]);
+                pre.get(r, w);
+                post.get(r, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dpre[r][i] += h[i] * (x[i] * r2);
+                    d[r][i] += r2 * (h[i] * w[i]) - c2 * x[i];
+                    q[0] += d[r][i] * (v[i] * f[i]);
+                    x[i] = p.alpha * d[r][i];
+                }
+                Oct<S> dx;
+                dx.from(x);
+                put<RING>(p.dx, p.lddx, t, c, p.d, p.vec_dx, dx);
+            }
+            if (p.o) {
+                if (p.post_norm || p.dgate)
+                    sum(q);
+                if (p.dgate && threadIdx.x == 0)
+                    p.dgate[t] = r1 * q[0] * (p.sigmoid ? g * (1.0f - g) : 1.0f);
+                const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q[0] * inv_d)) : 0.0f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int c = (int(threadIdx.x) + r * G) * 8;
+                    float f[8], v[8];
+                    o[r].to(f);
+                    post.get(r, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float e = k * d[r][i];
+                        dpost[r][i] += e * f[i];
+                        f[i] = e * v[i] - c1 * f[i];
+                    }
+                    o[r].from(f);
+                    put<RING>(p.d_o, p.lddo, t, c, p.d, p.vec_do, o[r]);
+                }
+            }
+        } else {
             float zero[8] = {};
             Oct<S> zs;
             Oct<B> zb;
@@ -250,92 +505,17 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm_grad(const NormG
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int c = (int(threadIdx.x) + r * G) * 8;
-                zs.store(static_cast<S *>(p.dx) + t * p.lddx + c, p.d - c, p.vec_dx);
+                put<RING>(p.dx, p.lddx, t, c, p.d, p.vec_dx, zs);
                 if (p.o)
-                    zb.store(static_cast<B *>(p.d_o) + t * p.lddo + c, p.d - c, p.vec_do);
+                    put<RING>(p.d_o, p.lddo, t, c, p.d, p.vec_do, zb);
             }
             if (p.dgate && threadIdx.x == 0)
                 p.dgate[t] = 0.0f;
-            continue;
         }
-        float ds[R][8];
-        Oct<B> o[R], dh[R];
-        Oct<S> xn[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int c = (int(threadIdx.x) + r * G) * 8;
-            Oct<S> in;
-            in.load(static_cast<const S *>(p.dxn) + (p.dxn ? t * p.lddxn + c : 0),
-                    p.dxn ? p.d - c : 0, p.vec_dxn);
-            in.to(ds[r]);
-            dh[r].load(static_cast<const B *>(p.dh) + (p.dh ? t * p.lddh + c : 0),
-                       p.dh ? p.d - c : 0, p.vec_dh);
-            xn[r].load(static_cast<const S *>(p.xn) + t * p.ldxn + c, p.dh ? p.d - c : 0, p.vec_xn);
-            o[r].load(static_cast<const B *>(p.o) + (p.o ? t * p.ldo + c : 0), p.o ? p.d - c : 0,
-                      p.vec_o);
-        }
-        const float g = p.o ? gate_of(p.gate, p.sigmoid, t) : 1.0f;
-        float s[3] = {};  // xn^2, a xn, o^2
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float x[8], h[8], f[8];
-            xn[r].to(x);
-            dh[r].to(h);
-            o[r].to(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s[0] += x[i] * x[i];
-                s[1] += h[i] * pre[r][i] * x[i];
-                s[2] += f[i] * f[i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            s[i] *= inv_d;
-        sum(s);
-        const float r2 = p.dh ? rsqrtf(s[0] + p.eps) : 0.0f;
-        const float r1 = p.post_norm ? rsqrtf(s[2] + p.eps) : 1.0f;
-        const float c2 = r2 * r2 * r2 * s[1];
-        float q[1] = {0.0f};
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int c = (int(threadIdx.x) + r * G) * 8;
-            float x[8], h[8], f[8];
-            xn[r].to(x);
-            dh[r].to(h);
-            o[r].to(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dpre[r][i] += h[i] * (x[i] * r2);
-                ds[r][i] += r2 * (h[i] * pre[r][i]) - c2 * x[i];
-                q[0] += ds[r][i] * (post[r][i] * f[i]);
-                x[i] = p.alpha * ds[r][i];
-            }
-            Oct<S> out;
-            out.from(x);
-            out.store(static_cast<S *>(p.dx) + t * p.lddx + c, p.d - c, p.vec_dx);
-        }
-        if (!p.o)
-            continue;
-        if (p.post_norm || p.dgate)
-            sum(q);
-        if (p.dgate && threadIdx.x == 0)
-            p.dgate[t] = r1 * q[0] * (p.sigmoid ? g * (1.0f - g) : 1.0f);
-        const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q[0] * inv_d)) : 0.0f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int c = (int(threadIdx.x) + r * G) * 8;
-            float f[8];
-            o[r].to(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float e = k * ds[r][i];
-                dpost[r][i] += e * f[i];
-                f[i] = e * post[r][i] - c1 * f[i];
-            }
-            o[r].from(f);
-            o[r].store(static_cast<B *>(p.d_o) + t * p.lddo + c, p.d - c, p.vec_do);
-        }
+        live = next;
+        next = third;
+        if (++out == kNormStages)
+            out = 0;
     }
     if (!p.part)
         return;
@@ -386,6 +566,9 @@ __global__ void __launch_bounds__(kSumThreads)
 
 // ---- host ---------------------------------------------------------------------
 
+constexpr size_t kNormSmem = 200 * 1024;  // the most dynamic shared memory of a CTA: fp32 rows' ring
+static_assert(kNormStages * kNormMaxThreads * 16 * 8 <= kNormSmem, "");
+
 struct Shape {
     int threads, r;
 };
@@ -398,15 +581,19 @@ Shape norm_shape(int d, bool whole)
     return {((chunks + r - 1) / r + 31) / 32 * 32, r};
 }
 
+// f(S, B, R, RING) of the types, the rounds and whether a ring can be used.
 template <typename F>
-cudaError_t with_types(int s, int b, int r, F f)
+cudaError_t with_types(int s, int b, int r, bool ring, F f)
 {
     const auto with_r = [&](auto sv, auto bv) {
         using S = decltype(sv);
         using B = decltype(bv);
-        return r == 1   ? f(S(), B(), std::integral_constant<int, 1>())
-               : r == 2 ? f(S(), B(), std::integral_constant<int, 2>())
-                        : f(S(), B(), std::integral_constant<int, 4>());
+        using Yes = std::true_type;
+        using No = std::false_type;
+        return r == 1   ? ring ? f(S(), B(), std::integral_constant<int, 1>(), Yes())
+                               : f(S(), B(), std::integral_constant<int, 1>(), No())
+               : r == 2 ? f(S(), B(), std::integral_constant<int, 2>(), No())
+                        : f(S(), B(), std::integral_constant<int, 4>(), No());
     };
     if (s == MOE_DT_BF16)
         return with_r(__nv_bfloat16(), __nv_bfloat16());
@@ -415,6 +602,35 @@ cudaError_t with_types(int s, int b, int r, F f)
     return b == MOE_DT_BF16  ? with_r(float(), __nv_bfloat16())
            : b == MOE_DT_F16 ? with_r(float(), __half())
                              : with_r(float(), float());
+}
+
+// Launches a norm kernel on as many CTAs as the device holds at once (what it
+// holds is asked once per kernel, number of warps and device).
+template <auto KERN, typename Args>
+cudaError_t launch_norm(const Args &a, Shape sh, size_t ring_bytes, int64_t rows, int most,
+                        int &ctas, cudaStream_t s)
+{
+    constexpr int kDevices = 16;
+    static std::atomic<int> per_sm[kDevices][kNormMaxThreads / 32 + 1];
+    const size_t smem = ring_bytes + (sh.r > 1 ? size_t(2) * sh.r * 2 * sh.threads * 16 : 0);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    int held = dev < kDevices ? per_sm[dev][sh.threads / 32].load(std::memory_order_acquire) : 0;
+    if (!held) {
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(KERN),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, KERN, sh.threads, smem);
+        if (e != cudaSuccess)
+            return e;
+        held = std::max(held, 1);
+        if (dev < kDevices)
+            per_sm[dev][sh.threads / 32].store(held, std::memory_order_release);
+    }
+    ctas = int(std::min<int64_t>({int64_t(held) * device_sm_count(), rows, most}));
+    return launch_pdl(KERN, dim3(ctas), dim3(sh.threads), smem, s, a);
 }
 
 inline bool aligned(const void *p, uintptr_t a)
@@ -427,17 +643,6 @@ inline bool types_ok(int s, int b)
 {
     return s >= MOE_DT_BF16 && s <= MOE_DT_F32 && b >= MOE_DT_BF16 && b <= MOE_DT_F32 &&
            (s == b || s == MOE_DT_F32);
-}
-
-// CTAs of a launch over T rows: as many as the device holds at once.
-template <typename K>
-int norm_ctas(K kern, int threads, int64_t rows, int most)
-{
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess)
-        per_sm = 1;
-    const int64_t ctas = int64_t(std::max(1, per_sm)) * device_sm_count();
-    return int(std::min<int64_t>({ctas, rows, most}));
 }
 
 }  // namespace
@@ -478,10 +683,14 @@ extern "C" int moe_block_norm(const void *x, int64_t ldx, int x_dtype, const voi
     a.alpha = alpha, a.eps = eps;
     const Shape sh = norm_shape(d, codes != nullptr);
     const int64_t rows = codes ? (int64_t(T) + 127) / 128 * 128 : T;
-    const cudaError_t e = with_types(x_dtype, b_dtype, sh.r, [&](auto s, auto b, auto r) {
-        const auto kern = k_block_norm<decltype(s), decltype(b), decltype(r)::value>;
-        return launch_pdl(kern, dim3(norm_ctas(kern, sh.threads, rows, INT_MAX)),
-                          dim3(sh.threads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+    const bool ring = d % 8 == 0 && a.vec_x && (!o || (a.vec_o && a.vec_xn)) && (!h || a.vec_h);
+    const size_t bytes = ring ? size_t(kNormStages) * sh.threads * 8 * (xs + bs) : 0;
+    int ctas = 0;
+    const cudaError_t e = with_types(x_dtype, b_dtype, sh.r, ring, [&](auto s, auto b, auto r, auto g) {
+        constexpr auto kern =
+            k_block_norm<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
+        return launch_norm<kern>(a, sh, decltype(g)::value ? bytes : 0, rows, INT_MAX, ctas,
+                                 reinterpret_cast<cudaStream_t>(stream));
     });
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -541,11 +750,15 @@ extern "C" int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, co
     a.vec_dx = rows_vec(dx, lddx, xs), a.vec_do = rows_vec(d_o, lddo, bs);
     a.alpha = o ? alpha : 1.0f, a.eps = eps;
     const Shape sh = norm_shape(d, false);
+    const bool ring = d % 8 == 0 && (!dh || (a.vec_xn && a.vec_dh)) && (!dxn || a.vec_dxn) &&
+                      a.vec_dx && (!o || (a.vec_o && a.vec_do));
+    const size_t bytes = ring ? size_t(kNormStages) * sh.threads * 16 * (xs + bs) : 0;
     int ctas = 0;
-    cudaError_t e = with_types(x_dtype, b_dtype, sh.r, [&](auto s, auto b, auto r) {
-        const auto kern = k_block_norm_grad<decltype(s), decltype(b), decltype(r)::value>;
-        ctas = norm_ctas(kern, sh.threads, T, kNormGradCtas);
-        return launch_pdl(kern, dim3(ctas), dim3(sh.threads), 0, stm, a);
+    cudaError_t e = with_types(x_dtype, b_dtype, sh.r, ring, [&](auto s, auto b, auto r, auto g) {
+        constexpr auto kern =
+            k_block_norm_grad<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
+        return launch_norm<kern>(a, sh, decltype(g)::value ? bytes : 0, T, kNormGradCtas, ctas,
+                                 stm);
     });
     if (e == cudaSuccess && sums)
         e = launch_pdl(k_norm_col_sum, dim3((2 * d + 31) / 32), dim3(kSumThreads), 0, stm,
