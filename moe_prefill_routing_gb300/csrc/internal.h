@@ -181,6 +181,7 @@ enum SmemSlot {
     kSlotLinearPair,  // + 1 for wide tiles, + 2 with EXTRA
     kSlotLinearPairEnd = kSlotLinearPair + 3,
     kSlotLinearMx,
+    kSlotLinearMxPair,
     kSlotCount
 };
 

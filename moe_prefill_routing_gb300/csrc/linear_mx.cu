@@ -29,10 +29,12 @@ constexpr int kMxScaleCols = 16;  // of tensor memory: two tiles of A's and two 
 
 // Stages of 256 of K, four MMAs each, that one accumulator sums; sums of more
 // are cut into chains that are added outside the tensor core, which adds with
-// truncation (see linear.cu, whose numbers of MMAs these are).
+// truncation: sums of one sign over blocks of very different scales came out
+// 1.4e-7 of themselves low after 16 stages, so 6e-7 after 64.  16-bit outputs may
+// drift by a quarter of half a unit (see linear.cu).
 __host__ __device__ constexpr int mx_chain(bool f32, bool f16)
 {
-    return f32 ? 8 : f16 ? 256 : 2048;
+    return f32 ? 64 : f16 ? 256 : 2048;
 }
 
 struct MxArgs : EpiArgs {
@@ -332,6 +334,306 @@ __global__ void __launch_bounds__(kMxThreads)
     }
 }
 
+// ---- many rows: pairs of CTAs ---------------------------------------------------
+//
+// Tiles of 256 of x's rows (A) x bn of W's (B), one tcgen05.mma of a CTA pair per
+// 64 of K: each CTA loads its 128 rows of A and half the rows of B, the scales of
+// its own rows of A and those of all rows of B.  Pairs walk the tiles
+// (persistent); two accumulators let twelve epilogue warps work on one tile
+// while the MMAs fill the other.  192 columns are the most: two accumulators of
+// 256 would leave no tensor memory for the scales.
+constexpr int kMxEpiWarps = 12;
+constexpr int kMxParts = kMxEpiWarps / 4;  // warps that share 32 rows
+constexpr int kMxPairThreads = 64 + 32 * kMxEpiWarps;
+constexpr uint32_t kMxSlots = 4096;  // bytes of an epilogue warp's slots: two of 16 bits or one of fp32
+constexpr int kMxPairScaleCols = 24;  // A's two tiles, B's two of two; two such sets in turn
+
+struct MxPairCtrl {
+    uint64_t full[kMxMaxStages];
+    uint64_t empty[kMxMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct MxPairArgs {
+    CUtensorMap a, b, a_scales, b_scales, out;
+    MxArgs p;  // M: x's rows, N: W's
+    int tiles, stages;
+    uint32_t stage_bytes;
+};
+
+// Tiles of 128 rows' scales that bn of B's rows lie in (tiles of 192 start in the
+// middle of one every other time).
+__host__ __device__ __forceinline__ int mx_b_tiles(int bn)
+{
+    return bn > 128 ? 2 : 1;
+}
+
+// What one CTA loads per stage.
+__host__ __device__ __forceinline__ uint32_t mx_pair_stage(int bn)
+{
+    return kMxATile + uint32_t(bn / 2) * (MK / 2) + (1 + mx_b_tiles(bn)) * kMxScales;
+}
+
+__global__ void __launch_bounds__(kMxPairThreads, 1)
+    k_linear_mx_pair(const __grid_constant__ MxPairArgs g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    // the same offset in both CTAs: dynamic shared memory starts at the same address
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    __shared__ MxPairCtrl ctl;
+    const MxArgs &p = g.p;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int bn = p.bn, half = bn / 2, S = g.stages;
+    const uint32_t stage_bytes = g.stage_bytes;
+    uint8_t *stg = smem + S * stage_bytes;
+    volatile int *abort_flag = &ctl.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.acc_full[b], 1);
+            mbar_init(&ctl.acc_empty[b], 2 * kMxEpiWarps);  // both CTAs' warps
+        }
+        ctl.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&g.a);
+        prefetch_tmap(&g.b);
+        prefetch_tmap(&g.a_scales);
+        prefetch_tmap(&g.b_scales);
+    }
+    __syncwarp();
+    cluster_arrive();
+    if (warp == 1)
+        tmem_alloc_pair(&ctl.tmem_base, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_wait();  // the other CTA's barriers are initialised
+    tc_fence_after_sync();
+    const uint32_t tmem_base = ctl.tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int pairs = int(gridDim.x) / 2, pair = int(blockIdx.x) / 2;
+    const int nk = (p.K + MK - 1) / MK;
+    // tile t: blocks of 16 m tiles, m fastest, so that the pairs running at one
+    // time share few rows of both operands
+    const int block = 16 * ((p.N + bn - 1) / bn);
+    auto place = [&](int t, int &m0, int &n0) {
+        const int b = t / block, tall = min(16, p.n_mt - 16 * b), u = t - b * block;
+        n0 = u / tall * bn;
+        m0 = (16 * b + u % tall) * (2 * MM) + int(rank) * MM;
+    };
+    int m0, n0;
+
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        const bool one = elect_one();
+        bool ok = true;
+        for (int t = pair; ok && t < g.tiles; t += pairs) {
+            place(t, m0, n0);
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
+                if (!ok)
+                    break;
+                if (one) {
+                    if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
+                        mbar_arrive_expect_tx(&ctl.full[stage], 2 * stage_bytes);
+                    const uint32_t fb = dsmem_addr(&ctl.full[stage], 0);
+                    uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kMxATile;
+                    uint8_t *ss = sb + half * (MK / 2);
+                    tma_load_2d_pair(sa, &g.a, fb, kb * (MK / 2), m0);
+                    tma_load_2d_pair(sb, &g.b, fb, kb * (MK / 2), n0 + int(rank) * half);
+                    tma_load_3d_pair(ss, &g.a_scales, fb, 0, 2 * kb, m0 / 128);
+                    tma_load_3d_pair(ss + kMxScales, &g.b_scales, fb, 0, 2 * kb, n0 / 128);
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every stage released: this CTA's copies have landed and been read
+        for (int i = 0; ok && i < S; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {  // stopped: copies in flight take microseconds; give them a millisecond
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000u) {
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // the whole warp walks the loop and one lane issues
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, aphase = 0, set = 0;
+        const uint32_t sa = smem_u32(smem), sb = sa + kMxATile, ss = sb + half * (MK / 2);
+        const uint64_t da0 = smem_desc_sw128(sa, 16, 1024), db0 = smem_desc_sw128(sb, 16, 1024);
+        const uint64_t ds0 = smem_desc_rows16(ss);
+        const uint32_t idesc = idesc_mxf4(2 * MM, uint32_t(bn), 0);
+        constexpr uint32_t kTile = kMxTileBytes >> 4;
+        const bool one = elect_one();
+        bool ok = true;
+        for (int t = pair; ok && t < g.tiles; t += pairs) {
+            place(t, m0, n0);
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
+            if (!ok)
+                break;
+            const uint32_t d = tmem_base + uint32_t(buf * bn);
+            const uint32_t b_col = uint32_t(n0 % 128) / 32;
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                if (one) {
+                    const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
+                    const uint32_t sca = tmem_base + 512 - 2 * kMxPairScaleCols + set, scb = sca + 8;
+                    const int rest = p.K - kb * MK;
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i) {  // tiles of 128 of K
+                        if (rest <= int(i) * 128)
+                            break;
+                        tc_copy_32x128b_pair(sca + 4 * i, ds0 + off + i * kTile);
+                        tc_copy_32x128b_pair(scb + 8 * i, ds0 + off + (2 + i) * kTile);
+                        if (bn > 128)
+                            tc_copy_32x128b_pair(scb + 8 * i + 4, ds0 + off + (4 + i) * kTile);
+                    }
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 4; ++kk)
+                        if (rest > int(kk) * 64)
+                            tc_mma_mxf4_pair(d, da0 + off + kk * 2, db0 + off + kk * 2,
+                                             idesc | (kk & 1) << 5 | (kk & 1) << 30,
+                                             sca + 4 * (kk >> 1), scb + 8 * (kk >> 1) + b_col,
+                                             kb != 0 || kk != 0);
+                    tc_commit_pair(&ctl.empty[stage], 3);
+                }
+                __syncwarp();
+                set ^= uint32_t(kMxPairScaleCols);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok && one)
+                tc_commit_pair(&ctl.acc_full[buf], 3);
+            __syncwarp();
+            if (++buf == 2) {
+                buf = 0;
+                aphase ^= 1u;
+            }
+        }
+        // (the epilogue warps of both CTAs wait for every accumulator, so the
+        // MMAs are done when the cluster meets below)
+    } else if (warp >= 2) {
+        const int q = warp & 3, part = (warp - 2) >> 2;  // lane quadrant; which 32 columns
+        const uint32_t flags = p.flags;
+        const bool f32 = flags & kEpiF32;
+        // an fp32 slot takes both's room: the one slot is used every time
+        EpiMemory mem{stg + uint32_t(warp - 2) * kMxSlots, f32 ? 0u : kMxSlots / 2,
+                      reinterpret_cast<float *>(stg + kMxEpiWarps * kMxSlots) + (warp - 2) * 32, 0,
+                      f32};
+        const uint32_t lanes = tmem_base + (uint32_t(q * 32) << 16);
+        int buf = 0;
+        uint32_t aphase = 0;
+        for (int t = pair; t < g.tiles; t += pairs) {
+            place(t, m0, n0);
+            const int64_t row = int64_t(m0) + q * 32;
+            const int rows = int(min(int64_t(32), p.M - row)), width = min(bn, p.N - n0);
+            const float *bias_at = flags & kEpiBias ? p.bias + n0 + lane : nullptr;
+            auto bias_of = [&](int c) {
+                return bias_at && c + int(lane) < width ? bias_at[c] : 0.0f;
+            };
+            float bias = bias_of(part * 32);
+            const uint32_t t0 = lanes + uint32_t(buf * bn);
+            uint32_t r[kCols];
+            const bool some = rows > 0 && part * 32 < width;
+            bool ok = true;
+#pragma unroll 1
+            for (int c = part * 32; c == part * 32 || c < width; c += 32 * kMxParts) {
+                const int cols = min(32, width - c);
+                // (a tile's first may follow one that was taken and not stored)
+                mem.strict = f32 || c == part * 32;
+                uint8_t *slot = mem.take();
+                if ((flags & kEpiResidual) && some) {
+                    const int64_t at = row * p.ldr + n0 + c;
+                    if (f32)
+                        load_slot<float>(slot, p.residual, at, p.ldr, rows, cols,
+                                         flags & kEpiVecRes);
+                    else
+                        load_slot<uint16_t>(slot, p.residual, at, p.ldr, rows, cols,
+                                            flags & kEpiVecRes);
+                }
+                if (flags & kEpiBias)
+                    mem.bias[lane] = bias;
+                __syncwarp();
+                if (c == part * 32) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
+                    if (!ok || !some)
+                        break;
+                    tc_fence_after_sync();
+                    tmem_ld_32x32b_x16(t0 + uint32_t(c), r);
+                }
+                const int next = c + 32 * kMxParts;
+                if (next < width)
+                    bias = bias_of(next);
+#pragma unroll 1
+                for (int h = 0; h < 32; h += kCols) {
+                    float v[kCols];
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        v[j] = __uint_as_float(r[j]);
+                    const int ahead = h + kCols < 32 ? c + h + kCols : next;
+                    if (ahead < width)
+                        tmem_ld_32x32b_x16(t0 + uint32_t(ahead), r);
+                    pair_cols<false>(flags, nullptr, mem.bias + h, slot, slot, h, v);
+                }
+                if (f32)
+                    store_slot<float>(slot, &g.out, p.out, row, n0 + c, p.ldo, rows, cols,
+                                      flags & kEpiVecOut);
+                else
+                    store_slot<uint16_t>(slot, &g.out, p.out, row, n0 + c, p.ldo, rows, cols,
+                                         flags & kEpiVecOut);
+            }
+            if (!ok)
+                break;
+            tc_fence_before_sync();  // this accumulator has been read
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster_relaxed(dsmem_addr(&ctl.acc_empty[buf], 0));
+            if (++buf == 2) {
+                buf = 0;
+                aphase ^= 1u;
+            }
+        }
+        if (lane == 0)
+            bulk_wait<0>();  // every store written before the CTA (and its memory) goes
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && ctl.abort_flag)
+        report_timeout(p.status);
+    __syncwarp();
+    cluster_sync();  // the CTAs are done with each other's shared memory and barriers
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
 // ---- host ---------------------------------------------------------------------
 
 // Codes [rows, K / 2]: boxes of 128 bytes x box_rows rows with the 128-byte swizzle.
@@ -346,6 +648,24 @@ cudaError_t mx_map(CUtensorMap *m, const uint8_t *codes, int64_t rows, int K, in
     const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes),
                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Scale tiles [row_tiles, k_tiles, 512]: boxes of the two tiles of a stage of
+// `box_rows` neighbouring tiles of 128 rows.
+cudaError_t mx_scale_map(CUtensorMap *m, const uint8_t *scales, int64_t rows, int K, int box_rows)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode)
+        return cudaErrorNotSupported;
+    const cuuint64_t kt = cuuint64_t(mx_k_tiles(K));
+    const cuuint64_t dims[3] = {kMxTileBytes / 4, kt, cuuint64_t((rows + 127) / 128)};
+    const cuuint64_t strides[2] = {kMxTileBytes, kt * kMxTileBytes};
+    const cuuint32_t box[3] = {kMxTileBytes / 4, 2, cuuint32_t(box_rows)}, estr[3] = {1, 1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(scales),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -402,6 +722,70 @@ cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
                             args);
 }
 
+// Columns of a tile of k_linear_mx_pair: those with the least estimated time.
+int mx_pair_columns(const MxProduct &q, int pairs)
+{
+    const int nk = (q.K + MK - 1) / MK;
+    int best = 0;
+    double least = 0.0;
+    for (int bn : {192, 128, 64}) {
+        const int64_t tiles = ((int64_t(q.T) + 255) / 256) * ((int64_t(q.N) + bn - 1) / bn);
+        const double main = double(nk) * (150.0 + 1.4 * bn), epi = 1500.0 + 25.0 * bn;
+        const double c = double((tiles + pairs - 1) / pairs) * std::max(main, epi) + main + epi;
+        if (!best || c < least) {
+            best = bn;
+            least = c;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
+{
+    const int pairs = std::max(1, device_sm_count() / 2);
+    MxPairArgs g = {};
+    MxArgs &a = g.p;
+    static_cast<EpiArgs &>(a) = q.epi;
+    a.status = q.status;
+    a.M = q.T, a.N = q.N, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
+    a.bn = mx_pair_columns(q, pairs);
+    a.n_mt = int((int64_t(q.T) + 2 * MM - 1) / (2 * MM));
+    a.flags = (a.bias ? kEpiBias : 0) | (a.residual ? kEpiResidual : 0) |
+              (a.out_f32 ? kEpiF32 : 0) | (a.f16 ? kEpiF16 : 0) | (a.vec_out ? kEpiVecOut : 0) |
+              (a.vec_res ? kEpiVecRes : 0) | uint32_t(a.act) * kEpiAct;
+    const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.N) + a.bn - 1) / a.bn);
+    if (tiles > INT_MAX / 2)
+        return cudaErrorInvalidValue;
+    g.tiles = int(tiles);
+    g.stage_bytes = mx_pair_stage(a.bn);
+    const size_t epi = size_t(kMxEpiWarps) * (kMxSlots + 128);
+    g.stages = std::min<int>(kMxMaxStages, int((kMxLoneSmem - 1024 - epi) / g.stage_bytes));
+    cudaError_t e = mx_map(&g.a, q.x, q.T, q.K, MM);
+    if (e == cudaSuccess)
+        e = mx_map(&g.b, q.W, q.N, q.K, a.bn / 2);
+    if (e == cudaSuccess)
+        e = mx_scale_map(&g.a_scales, q.x_scales, q.T, q.K, 1);
+    if (e == cudaSuccess)
+        e = mx_scale_map(&g.b_scales, q.W_scales, q.N, q.K, mx_b_tiles(a.bn));
+    if (e == cudaSuccess && a.vec_out)
+        e = out_map(&g.out, a.out, a.M, a.N, a.ldo, a.out_f32, a.f16);
+    const void *kern = reinterpret_cast<const void *>(k_linear_mx_pair);
+    if (e == cudaSuccess)
+        e = ensure_smem_limit(kern, kSlotLinearMxPair, kMxLoneSmem);
+    if (e != cudaSuccess)
+        return e;
+    void *args[] = {&g};
+    return launch_clustered(kern, unsigned(2 * std::min<int64_t>(tiles, pairs)), 2, kMxPairThreads,
+                            kMxLoneSmem, s, args);
+}
+
+cudaError_t launch_mx(const MxProduct &q, cudaStream_t s)
+{
+    // (the pairs' sums are not cut)
+    const bool cut = (q.K + MK - 1) / MK > mx_chain(q.epi.out_f32, q.epi.f16);
+    return q.T > 128 && !cut ? launch_mx_pair(q, s) : launch_mx_small(q, s);
+}
+
 }  // namespace
 
 uint32_t *linear_mx_status_word()
@@ -438,6 +822,6 @@ extern "C" int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const
     e.f16 = y_dtype == MOE_DT_F16, e.out_f32 = y_dtype == MOE_DT_F32, e.act = act;
     e.vec_out = vec16(y, ldy, size), e.vec_res = vec16(residual, ldr, size);
     const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status};
-    return launch_mx_small(q, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
-                                                                                     : MOE_ERR_CUDA;
+    return launch_mx(q, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+                                                                               : MOE_ERR_CUDA;
 }
