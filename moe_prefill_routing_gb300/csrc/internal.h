@@ -181,7 +181,8 @@ enum SmemSlot {
     kSlotLinearPair,  // + 1 for wide tiles, + 2 with EXTRA
     kSlotLinearPairEnd = kSlotLinearPair + 3,
     kSlotLinearMx,
-    kSlotLinearMxPair,
+    kSlotLinearMxPair,  // + 3 per activation, + 1 for fp16, + 2 for fp32
+    kSlotLinearMxPairEnd = kSlotLinearMxPair + 14,
     kSlotCount
 };
 

@@ -339,18 +339,23 @@ __global__ void __launch_bounds__(kMxThreads)
 // Tiles of 256 of x's rows (A) x bn of W's (B), one tcgen05.mma of a CTA pair per
 // 64 of K: each CTA loads its 128 rows of A and half the rows of B, the scales of
 // its own rows of A and those of all rows of B.  Pairs walk the tiles
-// (persistent); two accumulators let twelve epilogue warps work on one tile
-// while the MMAs fill the other.  192 columns are the most: two accumulators of
-// 256 would leave no tensor memory for the scales.
-constexpr int kMxEpiWarps = 12;
-constexpr int kMxParts = kMxEpiWarps / 4;  // warps that share 32 rows
+// (persistent); two accumulators let the epilogue warps work on one tile while
+// the MMAs fill the other.  192 columns are the most: two accumulators of 256
+// would leave no tensor memory for the scales.
+//
+// A stage has two pieces of 256 of K: a stage's barriers take the issuing warp
+// about 400 cycles whatever it multiplies, the MMAs of a piece of 192 columns 384.
+constexpr int kMxSub = 2;        // pieces of a stage
+constexpr int kMxPairStages = 4; // at most
+constexpr int kMxEpiCols = 64;   // of an epilogue warp (32 rows), all in registers at once
+constexpr int kMxEpiWarps = 12;  // at most: 192 columns
 constexpr int kMxPairThreads = 64 + 32 * kMxEpiWarps;
-constexpr uint32_t kMxSlots = 4096;  // bytes of an epilogue warp's slots: two of 16 bits or one of fp32
-constexpr int kMxPairScaleCols = 24;  // A's two tiles, B's two of two; two such sets in turn
+constexpr uint32_t kMxSlot = 2048;  // of an epilogue warp: 32 rows of 64 bytes
+constexpr int kMxPieceCols = 24;    // of tensor memory: A's two scale tiles, B's two of two
 
 struct MxPairCtrl {
-    uint64_t full[kMxMaxStages];
-    uint64_t empty[kMxMaxStages];
+    uint64_t full[kMxPairStages];
+    uint64_t empty[kMxPairStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint32_t tmem_base;
@@ -361,7 +366,7 @@ struct MxPairArgs {
     CUtensorMap a, b, a_scales, b_scales, out;
     MxArgs p;  // M: x's rows, N: W's
     int tiles, stages;
-    uint32_t stage_bytes;
+    uint32_t piece_bytes;
 };
 
 // Tiles of 128 rows' scales that bn of B's rows lie in (tiles of 192 start in the
@@ -371,12 +376,89 @@ __host__ __device__ __forceinline__ int mx_b_tiles(int bn)
     return bn > 128 ? 2 : 1;
 }
 
-// What one CTA loads per stage.
-__host__ __device__ __forceinline__ uint32_t mx_pair_stage(int bn)
+// What one CTA loads per piece.
+__host__ __device__ __forceinline__ uint32_t mx_pair_piece(int bn)
 {
     return kMxATile + uint32_t(bn / 2) * (MK / 2) + (1 + mx_b_tiles(bn)) * kMxScales;
 }
 
+// A slot's 16-byte piece c of row r, as the 64-byte swizzle of a TMA copy has it.
+__device__ __forceinline__ uint4 *mx_slot_at(uint8_t *slot, int r, int c)
+{
+    return reinterpret_cast<uint4 *>(slot) + r * 4 + (c ^ ((r >> 1) & 3));
+}
+
+// Element by element, where 16-byte pieces are not aligned or do not exist whole.
+template <bool STORE, typename E>
+__device__ __noinline__ void mx_move_by_element(uint8_t *slot, E *p, int64_t ld, int rows, int cols)
+{
+    constexpr int kPer = 16 / int(sizeof(E));
+    const int lane = threadIdx.x & 31;
+    if (lane < cols)
+#pragma unroll 16
+        for (int r = 0; r < rows; ++r) {
+            E *at = reinterpret_cast<E *>(mx_slot_at(slot, r, lane / kPer)) + lane % kPer;
+            if (STORE)
+                p[int64_t(r) * ld + lane] = *at;
+            else
+                *at = p[int64_t(r) * ld + lane];
+        }
+}
+
+// The epilogue's blocks: 32 rows (lane = row) x 64 bytes of the output.
+template <typename E>
+struct MxBlock {
+    static constexpr int kColumns = 64 / int(sizeof(E));
+    static constexpr bool kF32 = sizeof(E) == 4;
+    static constexpr int kF16 = std::is_same<E, __half>::value;
+
+    // The residual's block on its way: lane's pieces of rows lane / 4 + 8 i.
+    static __device__ __forceinline__ void ask(uint4 (&q)[4], const E *p, int64_t ld, int rows)
+    {
+        const int lane = threadIdx.x & 31;
+        const E *at = p + (lane >> 2) * ld + (lane & 3) * (16 / int(sizeof(E)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((lane >> 2) + 8 * i < rows)
+                q[i] = *reinterpret_cast<const uint4 *>(at + 8 * i * ld);
+    }
+
+    static __device__ __forceinline__ void add(const uint8_t *slot, float *v)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 q = *mx_slot_at(const_cast<uint8_t *>(slot), lane, c);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (kF32) {
+                    v[4 * c + j] += __uint_as_float(w[j]);
+                } else {
+                    const float2 f = unpack16(w[j], kF16);
+                    v[8 * c + 2 * j] += f.x;
+                    v[8 * c + 2 * j + 1] += f.y;
+                }
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void put(uint8_t *slot, const float *v)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = kF32 ? __float_as_uint(v[4 * c + j])
+                            : pack16(v[8 * c + 2 * j], v[8 * c + 2 * j + 1], kF16);
+            *mx_slot_at(slot, lane, c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+};
+
+template <int ACT, typename E>
 __global__ void __launch_bounds__(kMxPairThreads, 1)
     k_linear_mx_pair(const __grid_constant__ MxPairArgs g)
 {
@@ -390,8 +472,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int bn = p.bn, half = bn / 2, S = g.stages;
-    const uint32_t stage_bytes = g.stage_bytes;
-    uint8_t *stg = smem + S * stage_bytes;
+    const uint32_t piece_bytes = g.piece_bytes;
+    uint8_t *stg = smem + S * kMxSub * piece_bytes;
     volatile int *abort_flag = &ctl.abort_flag;
 
     if (threadIdx.x == 0) {
@@ -401,7 +483,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl.acc_full[b], 1);
-            mbar_init(&ctl.acc_empty[b], 2 * kMxEpiWarps);  // both CTAs' warps
+            mbar_init(&ctl.acc_empty[b], 2 * 4 * (bn / kMxEpiCols));  // both CTAs' warps
         }
         ctl.abort_flag = 0;
         fence_mbar_init();
@@ -441,20 +523,27 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         bool ok = true;
         for (int t = pair; ok && t < g.tiles; t += pairs) {
             place(t, m0, n0);
-            for (int kb = 0; kb < nk; ++kb) {
+            for (int kb = 0; kb < nk; kb += kMxSub) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
                 if (!ok)
                     break;
                 if (one) {
+                    const int subs = min(kMxSub, nk - kb);
                     if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
-                        mbar_arrive_expect_tx(&ctl.full[stage], 2 * stage_bytes);
+                        mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(subs) * 2 * piece_bytes);
                     const uint32_t fb = dsmem_addr(&ctl.full[stage], 0);
-                    uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kMxATile;
-                    uint8_t *ss = sb + half * (MK / 2);
-                    tma_load_2d_pair(sa, &g.a, fb, kb * (MK / 2), m0);
-                    tma_load_2d_pair(sb, &g.b, fb, kb * (MK / 2), n0 + int(rank) * half);
-                    tma_load_3d_pair(ss, &g.a_scales, fb, 0, 2 * kb, m0 / 128);
-                    tma_load_3d_pair(ss + kMxScales, &g.b_scales, fb, 0, 2 * kb, n0 / 128);
+#pragma unroll
+                    for (int h = 0; h < kMxSub; ++h) {
+                        if (h >= subs)
+                            break;
+                        uint8_t *sa = smem + (stage * kMxSub + h) * piece_bytes;
+                        uint8_t *sb = sa + kMxATile, *ss = sb + half * (MK / 2);
+                        const int k = kb + h;
+                        tma_load_2d_pair(sa, &g.a, fb, k * (MK / 2), m0);
+                        tma_load_2d_pair(sb, &g.b, fb, k * (MK / 2), n0 + int(rank) * half);
+                        tma_load_3d_pair(ss, &g.a_scales, fb, 0, 2 * k, m0 / 128);
+                        tma_load_3d_pair(ss + kMxScales, &g.b_scales, fb, 0, 2 * k, n0 / 128);
+                    }
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -479,11 +568,12 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     } else if (warp == 1 && rank == 0) {
         // the whole warp walks the loop and one lane issues
         int stage = 0, buf = 0;
-        uint32_t phase = 0, aphase = 0, set = 0;
+        uint32_t phase = 0, aphase = 0;
         const uint32_t sa = smem_u32(smem), sb = sa + kMxATile, ss = sb + half * (MK / 2);
         const uint64_t da0 = smem_desc_sw128(sa, 16, 1024), db0 = smem_desc_sw128(sb, 16, 1024);
         const uint64_t ds0 = smem_desc_rows16(ss);
         const uint32_t idesc = idesc_mxf4(2 * MM, uint32_t(bn), 0);
+        const uint32_t scales = tmem_base + 512 - kMxSub * kMxPieceCols;
         constexpr uint32_t kTile = kMxTileBytes >> 4;
         const bool one = elect_one();
         bool ok = true;
@@ -494,35 +584,43 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                 break;
             const uint32_t d = tmem_base + uint32_t(buf * bn);
             const uint32_t b_col = uint32_t(n0 % 128) / 32;
-            for (int kb = 0; kb < nk; ++kb) {
+            for (int kb = 0; kb < nk; kb += kMxSub) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
                 if (!ok)
                     break;
                 tc_fence_after_sync();
                 if (one) {
-                    const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
-                    const uint32_t sca = tmem_base + 512 - 2 * kMxPairScaleCols + set, scb = sca + 8;
-                    const int rest = p.K - kb * MK;
 #pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {  // tiles of 128 of K
-                        if (rest <= int(i) * 128)
-                            break;
-                        tc_copy_32x128b_pair(sca + 4 * i, ds0 + off + i * kTile);
-                        tc_copy_32x128b_pair(scb + 8 * i, ds0 + off + (2 + i) * kTile);
-                        if (bn > 128)
-                            tc_copy_32x128b_pair(scb + 8 * i + 4, ds0 + off + (4 + i) * kTile);
+                    for (int h = 0; h < kMxSub; ++h) {
+                        const uint32_t off = uint32_t(stage * kMxSub + h) * (piece_bytes >> 4);
+                        const uint32_t sca = scales + uint32_t(h * kMxPieceCols), scb = sca + 8;
+                        const int rest = p.K - (kb + h) * MK;
+#pragma unroll
+                        for (uint32_t i = 0; i < 2; ++i)  // tiles of 128 of K
+                            if (rest > int(i) * 128) {
+                                tc_copy_32x128b_pair(sca + 4 * i, ds0 + (off + i * kTile));
+                                tc_copy_32x128b_pair(scb + 8 * i, ds0 + (off + (2 + i) * kTile));
+                                if (bn > 128)
+                                    tc_copy_32x128b_pair(scb + 8 * i + 4,
+                                                         ds0 + (off + (4 + i) * kTile));
+                            }
                     }
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 4; ++kk)
-                        if (rest > int(kk) * 64)
-                            tc_mma_mxf4_pair(d, da0 + off + kk * 2, db0 + off + kk * 2,
-                                             idesc | (kk & 1) << 5 | (kk & 1) << 30,
-                                             sca + 4 * (kk >> 1), scb + 8 * (kk >> 1) + b_col,
-                                             kb != 0 || kk != 0);
+                    for (int h = 0; h < kMxSub; ++h) {
+                        const uint32_t off = uint32_t(stage * kMxSub + h) * (piece_bytes >> 4);
+                        const uint32_t sca = scales + uint32_t(h * kMxPieceCols), scb = sca + 8;
+                        const int rest = p.K - (kb + h) * MK;
+#pragma unroll
+                        for (uint32_t kk = 0; kk < 4; ++kk)
+                            if (rest > int(kk) * 64)
+                                tc_mma_mxf4_pair(d, da0 + (off + kk * 2), db0 + (off + kk * 2),
+                                                 idesc | (kk & 1) << 5 | (kk & 1) << 30,
+                                                 sca + 4 * (kk >> 1), scb + 8 * (kk >> 1) + b_col,
+                                                 kb != 0 || h != 0 || kk != 0);
+                    }
                     tc_commit_pair(&ctl.empty[stage], 3);
                 }
                 __syncwarp();
-                set ^= uint32_t(kMxPairScaleCols);
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1u;
@@ -538,79 +636,46 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         }
         // (the epilogue warps of both CTAs wait for every accumulator, so the
         // MMAs are done when the cluster meets below)
-    } else if (warp >= 2) {
-        const int q = warp & 3, part = (warp - 2) >> 2;  // lane quadrant; which 32 columns
-        const uint32_t flags = p.flags;
-        const bool f32 = flags & kEpiF32;
-        // an fp32 slot takes both's room: the one slot is used every time
-        EpiMemory mem{stg + uint32_t(warp - 2) * kMxSlots, f32 ? 0u : kMxSlots / 2,
-                      reinterpret_cast<float *>(stg + kMxEpiWarps * kMxSlots) + (warp - 2) * 32, 0,
-                      f32};
-        const uint32_t lanes = tmem_base + (uint32_t(q * 32) << 16);
+    } else if (warp >= 2 && (warp - 2) >> 2 < bn / kMxEpiCols) {
+        // A warp takes its 64 columns into registers at once and gives the
+        // accumulator back; then block after block: bias, activation, residual, one
+        // slot of shared memory, one TMA store.  (With 16 columns at a time and the
+        // accumulator kept till the end, 4096 x 256 x 11264 took 33 us.)
+        using Block = MxBlock<E>;
+        constexpr int C = Block::kColumns, kBlocks = kMxEpiCols / C;
+        const int q = warp & 3, part = (warp - 2) >> 2;  // lane quadrant; which 64 columns
+        uint8_t *slot = stg + uint32_t(warp - 2) * kMxSlot;
+        float *bias = reinterpret_cast<float *>(stg + kMxEpiWarps * kMxSlot) +
+                      (warp - 2) * kMxEpiCols;
+        const uint32_t lanes =
+            tmem_base + (uint32_t(q * 32) << 16) + uint32_t(part * kMxEpiCols);
+        const bool vec_res = p.residual && p.vec_res, any_res = p.residual;
         int buf = 0;
         uint32_t aphase = 0;
         for (int t = pair; t < g.tiles; t += pairs) {
             place(t, m0, n0);
             const int64_t row = int64_t(m0) + q * 32;
-            const int rows = int(min(int64_t(32), p.M - row)), width = min(bn, p.N - n0);
-            const float *bias_at = flags & kEpiBias ? p.bias + n0 + lane : nullptr;
-            auto bias_of = [&](int c) {
-                return bias_at && c + int(lane) < width ? bias_at[c] : 0.0f;
-            };
-            float bias = bias_of(part * 32);
-            const uint32_t t0 = lanes + uint32_t(buf * bn);
-            uint32_t r[kCols];
-            const bool some = rows > 0 && part * 32 < width;
-            bool ok = true;
-#pragma unroll 1
-            for (int c = part * 32; c == part * 32 || c < width; c += 32 * kMxParts) {
-                const int cols = min(32, width - c);
-                // (a tile's first may follow one that was taken and not stored)
-                mem.strict = f32 || c == part * 32;
-                uint8_t *slot = mem.take();
-                if ((flags & kEpiResidual) && some) {
-                    const int64_t at = row * p.ldr + n0 + c;
-                    if (f32)
-                        load_slot<float>(slot, p.residual, at, p.ldr, rows, cols,
-                                         flags & kEpiVecRes);
-                    else
-                        load_slot<uint16_t>(slot, p.residual, at, p.ldr, rows, cols,
-                                            flags & kEpiVecRes);
-                }
-                if (flags & kEpiBias)
-                    mem.bias[lane] = bias;
+            const int rows = int(min(int64_t(32), p.M - row));
+            const int col = n0 + part * kMxEpiCols, width = min(kMxEpiCols, p.N - col);
+            const E *res = static_cast<const E *>(p.residual) + (any_res ? row * p.ldr + col : 0);
+            E *out = static_cast<E *>(p.out) + row * p.ldo + col;
+            uint4 ahead[4] = {};
+            if (vec_res && width >= C)
+                Block::ask(ahead, res, p.ldr, rows);
+            if (p.bias) {
                 __syncwarp();
-                if (c == part * 32) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[buf], aphase, abort_flag));
-                    if (!ok || !some)
-                        break;
-                    tc_fence_after_sync();
-                    tmem_ld_32x32b_x16(t0 + uint32_t(c), r);
-                }
-                const int next = c + 32 * kMxParts;
-                if (next < width)
-                    bias = bias_of(next);
-#pragma unroll 1
-                for (int h = 0; h < 32; h += kCols) {
-                    float v[kCols];
-                    tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        v[j] = __uint_as_float(r[j]);
-                    const int ahead = h + kCols < 32 ? c + h + kCols : next;
-                    if (ahead < width)
-                        tmem_ld_32x32b_x16(t0 + uint32_t(ahead), r);
-                    pair_cols<false>(flags, nullptr, mem.bias + h, slot, slot, h, v);
-                }
-                if (f32)
-                    store_slot<float>(slot, &g.out, p.out, row, n0 + c, p.ldo, rows, cols,
-                                      flags & kEpiVecOut);
-                else
-                    store_slot<uint16_t>(slot, &g.out, p.out, row, n0 + c, p.ldo, rows, cols,
-                                         flags & kEpiVecOut);
+                for (int i = 0; i < kMxEpiCols; i += 32)
+                    bias[i + lane] = i + int(lane) < width ? p.bias[col + i + int(lane)] : 0.0f;
+                __syncwarp();
             }
-            if (!ok)
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[buf], aphase, abort_flag)))
                 break;
+            tc_fence_after_sync();
+            uint32_t r0[32], r1[32];
+            tmem_ld_32x32b_x32(lanes + uint32_t(buf * bn), r0);
+            tmem_ld_32x32b_x32(lanes + uint32_t(buf * bn) + 32, r1);
+            tmem_ld_wait();
             tc_fence_before_sync();  // this accumulator has been read
             __syncwarp();
             if (lane == 0)
@@ -618,6 +683,64 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             if (++buf == 2) {
                 buf = 0;
                 aphase ^= 1u;
+            }
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int cols = min(C, width - b * C);
+                if (rows <= 0 || cols <= 0)
+                    break;
+                float v[C];
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    v[j] = __uint_as_float(b * C + j < 32 ? r0[(b * C + j) & 31]
+                                                          : r1[(b * C + j) & 31]);
+                if (p.bias) {
+#pragma unroll
+                    for (int j = 0; j < C; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(bias + b * C + j);
+                        v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < C; j += 16) {
+                    float w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = v[j + i];
+                    act_all<ACT>(w);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        v[j + i] = w[i];
+                }
+                if (lane == 0)
+                    bulk_wait_read<0>();  // the last store is done with the slot
+                __syncwarp();
+                if (any_res) {
+                    if (vec_res && cols == C) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *mx_slot_at(slot, int(lane >> 2) + 8 * i, int(lane & 3)) = ahead[i];
+                        if (b + 1 < kBlocks && width >= (b + 2) * C)
+                            Block::ask(ahead, res + (b + 1) * C, p.ldr, rows);
+                    } else {
+                        mx_move_by_element<false>(slot, const_cast<E *>(res) + b * C, p.ldr, rows,
+                                                  cols);
+                    }
+                    __syncwarp();
+                    Block::add(slot, v);
+                }
+                Block::put(slot, v);
+                if (p.vec_out) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&g.out, slot, col + b * C, int(row));
+                        bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+                    mx_move_by_element<true>(slot, out + b * C, p.ldo, rows, cols);
+                }
             }
         }
         if (lane == 0)
@@ -631,6 +754,32 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+using MxPairKernel = void (*)(MxPairArgs);
+
+template <int ACT>
+MxPairKernel mx_pair_kernel(bool f32, bool f16)
+{
+    return f32   ? k_linear_mx_pair<ACT, float>
+           : f16 ? k_linear_mx_pair<ACT, __half>
+                 : k_linear_mx_pair<ACT, __nv_bfloat16>;
+}
+
+MxPairKernel mx_pair_kernel(int act, bool f32, bool f16)
+{
+    switch (act) {
+    case MOE_ACT_RELU:
+        return mx_pair_kernel<MOE_ACT_RELU>(f32, f16);
+    case MOE_ACT_SILU:
+        return mx_pair_kernel<MOE_ACT_SILU>(f32, f16);
+    case MOE_ACT_GELU:
+        return mx_pair_kernel<MOE_ACT_GELU>(f32, f16);
+    case MOE_ACT_GELU_TANH:
+        return mx_pair_kernel<MOE_ACT_GELU_TANH>(f32, f16);
+    default:
+        return mx_pair_kernel<MOE_ACT_NONE>(f32, f16);
     }
 }
 
@@ -667,6 +816,27 @@ cudaError_t mx_scale_map(CUtensorMap *m, const uint8_t *scales, int64_t rows, in
                               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Outputs [M, N], written in blocks of 32 rows x 64 bytes from a slot.
+cudaError_t mx_out_map(CUtensorMap *m, const MxArgs &a)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode)
+        return cudaErrorNotSupported;
+    const int size = a.out_f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {cuuint64_t(a.N), cuuint64_t(a.M)};
+    const cuuint64_t strides[1] = {cuuint64_t(a.ldo) * size};
+    const cuuint32_t box[2] = {cuuint32_t(64 / size), 32}, estr[2] = {1, 1};
+    const CUresult r =
+        encode(m,
+               a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+               : a.f16   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               2, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -750,16 +920,14 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
     a.M = q.T, a.N = q.N, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
     a.bn = mx_pair_columns(q, pairs);
     a.n_mt = int((int64_t(q.T) + 2 * MM - 1) / (2 * MM));
-    a.flags = (a.bias ? kEpiBias : 0) | (a.residual ? kEpiResidual : 0) |
-              (a.out_f32 ? kEpiF32 : 0) | (a.f16 ? kEpiF16 : 0) | (a.vec_out ? kEpiVecOut : 0) |
-              (a.vec_res ? kEpiVecRes : 0) | uint32_t(a.act) * kEpiAct;
     const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.N) + a.bn - 1) / a.bn);
     if (tiles > INT_MAX / 2)
         return cudaErrorInvalidValue;
     g.tiles = int(tiles);
-    g.stage_bytes = mx_pair_stage(a.bn);
-    const size_t epi = size_t(kMxEpiWarps) * (kMxSlots + 128);
-    g.stages = std::min<int>(kMxMaxStages, int((kMxLoneSmem - 1024 - epi) / g.stage_bytes));
+    g.piece_bytes = mx_pair_piece(a.bn);
+    const size_t epi = size_t(kMxEpiWarps) * (kMxSlot + kMxEpiCols * 4);
+    g.stages = std::min<int>(kMxPairStages,
+                             int((kMxLoneSmem - 1024 - epi) / (kMxSub * g.piece_bytes)));
     cudaError_t e = mx_map(&g.a, q.x, q.T, q.K, MM);
     if (e == cudaSuccess)
         e = mx_map(&g.b, q.W, q.N, q.K, a.bn / 2);
@@ -768,10 +936,12 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
     if (e == cudaSuccess)
         e = mx_scale_map(&g.b_scales, q.W_scales, q.N, q.K, mx_b_tiles(a.bn));
     if (e == cudaSuccess && a.vec_out)
-        e = out_map(&g.out, a.out, a.M, a.N, a.ldo, a.out_f32, a.f16);
-    const void *kern = reinterpret_cast<const void *>(k_linear_mx_pair);
+        e = mx_out_map(&g.out, a);
+    const void *kern =
+        reinterpret_cast<const void *>(mx_pair_kernel(a.act, a.out_f32, a.f16));
     if (e == cudaSuccess)
-        e = ensure_smem_limit(kern, kSlotLinearMxPair, kMxLoneSmem);
+        e = ensure_smem_limit(kern, kSlotLinearMxPair + 3 * a.act + (a.out_f32 ? 2 : a.f16),
+                              kMxLoneSmem);
     if (e != cudaSuccess)
         return e;
     void *args[] = {&g};
