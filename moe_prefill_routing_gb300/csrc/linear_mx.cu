@@ -343,10 +343,11 @@ __global__ void __launch_bounds__(kMxThreads)
 // the MMAs fill the other.  192 columns are the most: two accumulators of 256
 // would leave no tensor memory for the scales.
 //
-// A stage has two pieces of 256 of K: a stage's barriers take the issuing warp
-// about 400 cycles whatever it multiplies, the MMAs of a piece of 192 columns 384.
-constexpr int kMxSub = 2;        // pieces of a stage
-constexpr int kMxPairStages = 4; // at most
+// What bounds the ring is a stage's round trip, about 2000 cycles from its
+// release to its next data's arrival: the more stages it is spread over, the
+// better (192 columns: six; with five 4096 x 11264 x 11264 took 172 us, with three
+// of twice the size 155 us).
+constexpr int kMxPairStages = 8;  // at most
 constexpr int kMxEpiCols = 64;   // of an epilogue warp (32 rows), all in registers at once
 constexpr int kMxEpiWarps = 12;  // at most: 192 columns
 constexpr int kMxPairThreads = 64 + 32 * kMxEpiWarps;
@@ -366,7 +367,7 @@ struct MxPairArgs {
     CUtensorMap a, b, a_scales, b_scales, out;
     MxArgs p;  // M: x's rows, N: W's
     int tiles, stages;
-    uint32_t piece_bytes;
+    uint32_t stage_bytes;
 };
 
 // Tiles of 128 rows' scales that bn of B's rows lie in (tiles of 192 start in the
@@ -376,8 +377,8 @@ __host__ __device__ __forceinline__ int mx_b_tiles(int bn)
     return bn > 128 ? 2 : 1;
 }
 
-// What one CTA loads per piece.
-__host__ __device__ __forceinline__ uint32_t mx_pair_piece(int bn)
+// What one CTA loads per stage.
+__host__ __device__ __forceinline__ uint32_t mx_pair_stage(int bn)
 {
     return kMxATile + uint32_t(bn / 2) * (MK / 2) + (1 + mx_b_tiles(bn)) * kMxScales;
 }
@@ -472,8 +473,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int bn = p.bn, half = bn / 2, S = g.stages;
-    const uint32_t piece_bytes = g.piece_bytes;
-    uint8_t *stg = smem + S * kMxSub * piece_bytes;
+    const uint32_t stage_bytes = g.stage_bytes;
+    uint8_t *stg = smem + S * stage_bytes;
     volatile int *abort_flag = &ctl.abort_flag;
 
     if (threadIdx.x == 0) {
@@ -523,27 +524,20 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         bool ok = true;
         for (int t = pair; ok && t < g.tiles; t += pairs) {
             place(t, m0, n0);
-            for (int kb = 0; kb < nk; kb += kMxSub) {
+            for (int kb = 0; kb < nk; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[stage], phase ^ 1u, abort_flag));
                 if (!ok)
                     break;
                 if (one) {
-                    const int subs = min(kMxSub, nk - kb);
                     if (rank == 0)  // both CTAs' bytes complete on the even CTA's barrier
-                        mbar_arrive_expect_tx(&ctl.full[stage], uint32_t(subs) * 2 * piece_bytes);
+                        mbar_arrive_expect_tx(&ctl.full[stage], 2 * stage_bytes);
                     const uint32_t fb = dsmem_addr(&ctl.full[stage], 0);
-#pragma unroll
-                    for (int h = 0; h < kMxSub; ++h) {
-                        if (h >= subs)
-                            break;
-                        uint8_t *sa = smem + (stage * kMxSub + h) * piece_bytes;
-                        uint8_t *sb = sa + kMxATile, *ss = sb + half * (MK / 2);
-                        const int k = kb + h;
-                        tma_load_2d_pair(sa, &g.a, fb, k * (MK / 2), m0);
-                        tma_load_2d_pair(sb, &g.b, fb, k * (MK / 2), n0 + int(rank) * half);
-                        tma_load_3d_pair(ss, &g.a_scales, fb, 0, 2 * k, m0 / 128);
-                        tma_load_3d_pair(ss + kMxScales, &g.b_scales, fb, 0, 2 * k, n0 / 128);
-                    }
+                    uint8_t *sa = smem + stage * stage_bytes;
+                    uint8_t *sb = sa + kMxATile, *ss = sb + half * (MK / 2);
+                    tma_load_2d_pair(sa, &g.a, fb, kb * (MK / 2), m0);
+                    tma_load_2d_pair(sb, &g.b, fb, kb * (MK / 2), n0 + int(rank) * half);
+                    tma_load_3d_pair(ss, &g.a_scales, fb, 0, 2 * kb, m0 / 128);
+                    tma_load_3d_pair(ss + kMxScales, &g.b_scales, fb, 0, 2 * kb, n0 / 128);
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -566,74 +560,71 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             }
         }
     } else if (warp == 1 && rank == 0) {
-        // the whole warp walks the loop and one lane issues
+        // The whole warp walks the loop and one lane issues, without a branch: what
+        // lies past the end of K in the last stage is zeros, codes and scales.  (A
+        // test for each MMA made 4096 x 11264 x 11264 162 us instead of 133, without
+        // its epilogue.)
         int stage = 0, buf = 0;
-        uint32_t phase = 0, aphase = 0;
+        uint32_t phase = 0, aphase = 0, set = 0;
         const uint32_t sa = smem_u32(smem), sb = sa + kMxATile, ss = sb + half * (MK / 2);
         const uint64_t da0 = smem_desc_sw128(sa, 16, 1024), db0 = smem_desc_sw128(sb, 16, 1024);
         const uint64_t ds0 = smem_desc_rows16(ss);
         const uint32_t idesc = idesc_mxf4(2 * MM, uint32_t(bn), 0);
-        const uint32_t scales = tmem_base + 512 - kMxSub * kMxPieceCols;
+        const uint32_t scales = tmem_base + 512 - 2 * kMxPieceCols;  // two sets
         constexpr uint32_t kTile = kMxTileBytes >> 4;
         const bool one = elect_one();
-        bool ok = true;
-        for (int t = pair; ok && t < g.tiles; t += pairs) {
-            place(t, m0, n0);
-            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
-            if (!ok)
-                break;
-            const uint32_t d = tmem_base + uint32_t(buf * bn);
-            const uint32_t b_col = uint32_t(n0 % 128) / 32;
-            for (int kb = 0; kb < nk; kb += kMxSub) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+        const auto walk = [&](auto wide) {  // more than 128 columns
+            bool ok = true;
+            for (int t = pair; ok && t < g.tiles; t += pairs) {
+                place(t, m0, n0);
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
                 if (!ok)
                     break;
-                tc_fence_after_sync();
-                if (one) {
-#pragma unroll
-                    for (int h = 0; h < kMxSub; ++h) {
-                        const uint32_t off = uint32_t(stage * kMxSub + h) * (piece_bytes >> 4);
-                        const uint32_t sca = scales + uint32_t(h * kMxPieceCols), scb = sca + 8;
-                        const int rest = p.K - (kb + h) * MK;
-#pragma unroll
-                        for (uint32_t i = 0; i < 2; ++i)  // tiles of 128 of K
-                            if (rest > int(i) * 128) {
-                                tc_copy_32x128b_pair(sca + 4 * i, ds0 + (off + i * kTile));
-                                tc_copy_32x128b_pair(scb + 8 * i, ds0 + (off + (2 + i) * kTile));
-                                if (bn > 128)
-                                    tc_copy_32x128b_pair(scb + 8 * i + 4,
-                                                         ds0 + (off + (4 + i) * kTile));
-                            }
-                    }
-#pragma unroll
-                    for (int h = 0; h < kMxSub; ++h) {
-                        const uint32_t off = uint32_t(stage * kMxSub + h) * (piece_bytes >> 4);
-                        const uint32_t sca = scales + uint32_t(h * kMxPieceCols), scb = sca + 8;
-                        const int rest = p.K - (kb + h) * MK;
-#pragma unroll
+                const uint32_t d = tmem_base + uint32_t(buf * bn);
+                const uint32_t b_col = uint32_t(n0 % 128) / 32;
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    if (one) {
+                        const uint32_t off = uint32_t(stage) * (stage_bytes >> 4);
+                        const uint32_t at = scales + set;
+                        tc_copy_32x128b_pair(at, ds0 + off);
+                        tc_copy_32x128b_pair(at + 4, ds0 + (off + kTile));
+                        tc_copy_32x128b_pair(at + 8, ds0 + (off + 2 * kTile));
+                        tc_copy_32x128b_pair(at + 16, ds0 + (off + 3 * kTile));
+                        if constexpr (decltype(wide)::value) {
+                            tc_copy_32x128b_pair(at + 12, ds0 + (off + 4 * kTile));
+                            tc_copy_32x128b_pair(at + 20, ds0 + (off + 5 * kTile));
+                        }
+    #pragma unroll
                         for (uint32_t kk = 0; kk < 4; ++kk)
-                            if (rest > int(kk) * 64)
-                                tc_mma_mxf4_pair(d, da0 + (off + kk * 2), db0 + (off + kk * 2),
-                                                 idesc | (kk & 1) << 5 | (kk & 1) << 30,
-                                                 sca + 4 * (kk >> 1), scb + 8 * (kk >> 1) + b_col,
-                                                 kb != 0 || h != 0 || kk != 0);
+                            tc_mma_mxf4_pair(d, da0 + (off + 2 * kk), db0 + (off + 2 * kk),
+                                             idesc | (kk & 1) << 5 | (kk & 1) << 30, at + 4 * (kk >> 1),
+                                             at + 8 + 8 * (kk >> 1) + b_col, kb != 0 || kk != 0);
+                        tc_commit_pair(&ctl.empty[stage], 3);
                     }
-                    tc_commit_pair(&ctl.empty[stage], 3);
+                    __syncwarp();
+                    set ^= uint32_t(kMxPieceCols);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+                if (ok && one)
+                    tc_commit_pair(&ctl.acc_full[buf], 3);
                 __syncwarp();
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
+                if (++buf == 2) {
+                    buf = 0;
+                    aphase ^= 1u;
                 }
             }
-            if (ok && one)
-                tc_commit_pair(&ctl.acc_full[buf], 3);
-            __syncwarp();
-            if (++buf == 2) {
-                buf = 0;
-                aphase ^= 1u;
-            }
-        }
+        };
+        if (bn > 128)
+            walk(std::true_type());
+        else
+            walk(std::false_type());
         // (the epilogue warps of both CTAs wait for every accumulator, so the
         // MMAs are done when the cluster meets below)
     } else if (warp >= 2 && (warp - 2) >> 2 < bn / kMxEpiCols) {
@@ -892,7 +883,10 @@ cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
                             args);
 }
 
-// Columns of a tile of k_linear_mx_pair: those with the least estimated time.
+// Columns of a tile of k_linear_mx_pair: those with the least estimated time, in
+// cycles, from times at 64 ... 192.  (One round of 40 stages takes 11.7, 11.8 and
+// 12.3 us with 64, 128 and 192, 4096 x 10240 x 2560 in 9, 5 and 3 rounds 79, 48 and
+// 35; of two stages, which the epilogue bounds, 4096 x 512 x 2560 13.0, 10.0 and 8.6.)
 int mx_pair_columns(const MxProduct &q, int pairs)
 {
     const int nk = (q.K + MK - 1) / MK;
@@ -900,8 +894,9 @@ int mx_pair_columns(const MxProduct &q, int pairs)
     double least = 0.0;
     for (int bn : {192, 128, 64}) {
         const int64_t tiles = ((int64_t(q.T) + 255) / 256) * ((int64_t(q.N) + bn - 1) / bn);
-        const double main = double(nk) * (150.0 + 1.4 * bn), epi = 1500.0 + 25.0 * bn;
-        const double c = double((tiles + pairs - 1) / pairs) * std::max(main, epi) + main + epi;
+        const double main = nk * (370.0 + 0.65 * bn), epi = 1300.0 + 12.5 * bn;
+        const double c =
+            double((tiles + pairs - 1) / pairs) * std::max(main, epi) + std::min(main, epi);
         if (!best || c < least) {
             best = bn;
             least = c;
@@ -924,10 +919,9 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
     if (tiles > INT_MAX / 2)
         return cudaErrorInvalidValue;
     g.tiles = int(tiles);
-    g.piece_bytes = mx_pair_piece(a.bn);
+    g.stage_bytes = mx_pair_stage(a.bn);
     const size_t epi = size_t(kMxEpiWarps) * (kMxSlot + kMxEpiCols * 4);
-    g.stages = std::min<int>(kMxPairStages,
-                             int((kMxLoneSmem - 1024 - epi) / (kMxSub * g.piece_bytes)));
+    g.stages = std::min<int>(kMxPairStages, int((kMxLoneSmem - 1024 - epi) / g.stage_bytes));
     cudaError_t e = mx_map(&g.a, q.x, q.T, q.K, MM);
     if (e == cudaSuccess)
         e = mx_map(&g.b, q.W, q.N, q.K, a.bn / 2);

@@ -184,6 +184,13 @@ def test_residual_in_place_and_rows_left_alone():
             assert torch.equal(r[T:], keep[T:]) and torch.equal(r[:, 72:], keep[:, 72:])
 
 
+@pytest.mark.parametrize("T", [129, 143, 144, 145, 271, 272])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_residual_of_a_few_rows_of_a_tile(T, out):
+    """Warps whose 32 rows end in their first or second half."""
+    _check(T, 128, 200, out=out, bias=False)
+
+
 def test_the_same_bits_every_time():
     x, W = _rows(_rand(1, 1000, 2560)), _rows(_rand(2, 700, 2560))
     y = B.linear_mxfp4(x, W, out_dtype=F32)
