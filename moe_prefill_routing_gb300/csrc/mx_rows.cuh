@@ -14,6 +14,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace moe {
 
 constexpr int kMxTileBytes = 512;
@@ -119,66 +121,94 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&v)[8])
 
 // ---- eight neighbouring elements of a row ----------------------------------------
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ void from_float(float v, float &o) { o = v; }
-__device__ __forceinline__ void from_float(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void from_float(float v, __half &o) { o = __float2half_rn(v); }
-
-// As they are stored.
+// As they are stored, in 32-bit words (two 16-bit elements a word).
 template <typename E>
 struct alignas(16) Oct {
-    E e[8];
+    static constexpr int kWords = 2 * int(sizeof(E));
+    uint32_t w[kWords];
 
     // The first n exist (the others are 0); vec: 16-byte accesses are aligned.
     __device__ __forceinline__ void load(const E *p, int n, bool vec)
     {
-        constexpr int kQ = sizeof(E) == 4 ? 2 : 1;
         if (vec && n >= 8) {
-            uint4 q[kQ];
 #pragma unroll
-            for (int i = 0; i < kQ; ++i)
-                q[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-            memcpy(e, q, sizeof(e));
+            for (int i = 0; i < kWords / 4; ++i)
+                set(i, __ldcs(reinterpret_cast<const uint4 *>(p) + i));
         } else {
-            E zero;
-            from_float(0.0f, zero);
+            using Bits = std::conditional_t<sizeof(E) == 4, uint32_t, uint16_t>;
+            const Bits *q = reinterpret_cast<const Bits *>(p);
+            uint32_t e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                e[i] = i < n ? p[i] : zero;
+                e[i] = i < n ? uint32_t(q[i]) : 0u;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = sizeof(E) == 4 ? e[i % 8] : e[2 * i % 8] | e[(2 * i + 1) % 8] << 16;
         }
+    }
+
+    __device__ __forceinline__ void set(int i, uint4 q)
+    {
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
 
     __device__ __forceinline__ void store(E *p, int n, bool vec) const
     {
-        constexpr int kQ = sizeof(E) == 4 ? 2 : 1;
         if (vec && n >= 8) {
-            uint4 q[kQ];
-            memcpy(q, e, sizeof(e));
 #pragma unroll
-            for (int i = 0; i < kQ; ++i)
-                reinterpret_cast<uint4 *>(p)[i] = q[i];
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         } else {
+            using Bits = std::conditional_t<sizeof(E) == 4, uint32_t, uint16_t>;
+            Bits *q = reinterpret_cast<Bits *>(p);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i < n)
-                    p[i] = e[i];
+                    q[i] = Bits(sizeof(E) == 4 ? w[i % kWords]
+                                               : w[i / 2 % kWords] >> (16 * (i & 1)));
         }
     }
 
     __device__ __forceinline__ void to(float (&v)[8]) const
     {
+        if constexpr (sizeof(E) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = to_float(e[i]);
+            for (int i = 0; i < 8; ++i)
+                v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            }
+        }
     }
 
     __device__ __forceinline__ void from(const float (&v)[8])
     {
+        if constexpr (sizeof(E) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            from_float(v[i], e[i]);
+            for (int i = 0; i < 8; ++i)
+                w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                } else {
+                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+        }
     }
 };
 

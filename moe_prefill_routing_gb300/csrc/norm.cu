@@ -151,11 +151,9 @@ struct Rows {
         const int G = int(blockDim.x), t = int(threadIdx.x), c = (t + r * G) * 8;
         Oct<E> o;
         if (RING) {
-            uint4 v[kPieces];
 #pragma unroll
             for (int q = 0; q < kPieces; ++q)
-                v[q] = slots[(stage * kPieces + q) * G + t];
-            memcpy(o.e, v, sizeof(o.e));
+                o.set(q, slots[(stage * kPieces + q) * G + t]);
         } else {
             o.load(p + (p ? row * ld + c : 0), p ? d - c : 0, vec);
         }
