@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxD = kNormMaxThreads * 8 * 4;
-constexpr int kNormStages = 3;      // rows of a ring
+constexpr int kNormStages = 2;      // rows of a ring: one in use, one on its way
 constexpr int kNormGradCtas = 608;  // at most: rows of partial column sums
 constexpr int kSumThreads = 256;
 
@@ -41,7 +41,7 @@ struct NormArgs {
     uint8_t *codes, *scales;
     int64_t ldx, ldo, ldxn, ldh;
     int T, d;
-    int post_norm, sigmoid, k_tiles;
+    int post_norm, sigmoid, k_tiles, warps, ring_bytes;  // of a group
     int vec_x, vec_o, vec_xn, vec_h;
     float alpha, eps;
 };
@@ -54,15 +54,37 @@ struct NormGradArgs {
     float *dgate, *part;  // part: [CTAs][2][d], dpre's and dpost's
     int64_t ldxn, ldo, lddxn, lddh, lddx, lddo;
     int T, d;
-    int post_norm, sigmoid;
+    int post_norm, sigmoid, warps, ring_bytes;  // of a group
     int vec_xn, vec_o, vec_dxn, vec_dh, vec_dx, vec_do;
     float alpha, eps;
 };
 
-// Sums of N <= 4 values over the CTA's threads, in every thread; one barrier,
-// two sets of words in turn.
-struct BlockSum {
-    float4 (*red)[kNormMaxThreads / 32];
+// The threads of a CTA that have one row: CTAs take several rows side by side
+// where rows are short.
+struct Group {
+    int id, t, size, warps, count;  // t: the thread's place in it; count: groups of the CTA
+
+    __device__ __forceinline__ Group(int warps_) : size(32 * warps_), warps(warps_)
+    {
+        id = int(threadIdx.x) / size;
+        t = int(threadIdx.x) - id * size;
+        count = int(blockDim.x) / size;
+    }
+
+    __device__ __forceinline__ void sync() const
+    {
+        if (count == 1)
+            __syncthreads();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(size) : "memory");
+    }
+};
+
+// Sums of N <= 3 values over a group, in every thread; one barrier, two sets of
+// words in turn.
+struct GroupSum {
+    const Group &gr;
+    float4 *red;  // the group's [2][warps]
     int turn;
 
     template <int N>
@@ -73,16 +95,16 @@ struct BlockSum {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        const int warps = int(blockDim.x) >> 5;
-        if (warps == 1)
+        if (gr.warps == 1)
             return;
-        if ((threadIdx.x & 31) == 0)
-            red[turn][threadIdx.x >> 5] = make_float4(v[0], N > 1 ? v[N > 1] : 0.0f,
-                                                      N > 2 ? v[N > 2 ? 2 : 0] : 0.0f, 0.0f);
-        __syncthreads();
-        // every warp adds the warps' sums (16 at most) across its lanes
         const int lane = int(threadIdx.x) & 31;
-        const float4 s = lane < warps ? red[turn][lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 *const words = red + (turn ? gr.warps : 0);
+        if (lane == 0)
+            words[gr.t >> 5] = make_float4(v[0], N > 1 ? v[N > 1] : 0.0f,
+                                           N > 2 ? v[N > 2 ? 2 : 0] : 0.0f, 0.0f);
+        gr.sync();
+        // every warp adds the warps' sums (16 at most) across its lanes
+        const float4 s = lane < gr.warps ? words[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         v[0] = s.x;
         if (N > 1)
             v[N > 1] = s.y;
@@ -115,45 +137,51 @@ struct Rows {
     static constexpr int kPieces = sizeof(E) == 4 ? 2 : 1;  // of 16 bytes: eight elements
     const E *p;
     int64_t ld;
-    int d, vec;
-    uint4 *slots;  // [stage][kPieces][threads]
+    int d, vec, G, t;  // G, t: the group's threads, and which this one is
+    uint4 *slots;      // the thread's: [stage][R][kPieces], G apart
 
     __device__ __forceinline__ Rows(const void *tensor, int64_t ld_, int d_, int vec_,
-                                    uint8_t *&smem)
-        : p(static_cast<const E *>(tensor)), ld(ld_), d(d_), vec(vec_),
-          slots(reinterpret_cast<uint4 *>(smem))
+                                    const Group &gr, uint8_t *&smem)
+        : p(static_cast<const E *>(tensor)), ld(ld_), d(d_), vec(vec_), G(gr.size), t(gr.t),
+          slots(reinterpret_cast<uint4 *>(smem) + gr.t)
     {
-        static_assert(!RING || R == 1, "longer rows do not fit");
         if (RING) {
-            const int G = int(blockDim.x), t = int(threadIdx.x);
-            smem += kNormStages * kPieces * G * 16;
-            if (!p || t * 8 >= d)  // never fetched
-                for (int i = 0; i < kNormStages * kPieces; ++i)
-                    slots[i * G + t] = make_uint4(0, 0, 0, 0);
+            smem += kNormStages * R * kPieces * G * 16;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (!p || (t + r * G) * 8 >= d)  // never fetched
+                    for (int i = 0; i < kNormStages; ++i)
+#pragma unroll
+                        for (int q = 0; q < kPieces; ++q)
+                            slots[((i * R + r) * kPieces + q) * G] = make_uint4(0, 0, 0, 0);
         }
     }
 
     __device__ __forceinline__ void fetch(int64_t row, int stage) const
     {
-        const int G = int(blockDim.x), t = int(threadIdx.x);
-        if (RING && p && t * 8 < d) {
+        if (!RING || !p)
+            return;
+        const uint4 *from = reinterpret_cast<const uint4 *>(p + row * ld) + t * kPieces;
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(slots + (stage * kPieces + q) * G + t)),
-                             "l"(reinterpret_cast<const uint4 *>(p + row * ld) + t * kPieces + q)
-                             : "memory");
-        }
+        for (int r = 0; r < R; ++r)
+            if ((t + r * G) * 8 < d) {
+#pragma unroll
+                for (int q = 0; q < kPieces; ++q)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(
+                                     slots + ((stage * R + r) * kPieces + q) * G)),
+                                 "l"(from + r * G * kPieces + q)
+                                 : "memory");
+            }
     }
 
     __device__ __forceinline__ Oct<E> read(int64_t row, int stage, int r) const
     {
-        const int G = int(blockDim.x), t = int(threadIdx.x), c = (t + r * G) * 8;
+        const int c = (t + r * G) * 8;
         Oct<E> o;
         if (RING) {
 #pragma unroll
             for (int q = 0; q < kPieces; ++q)
-                o.set(q, slots[(stage * kPieces + q) * G + t]);
+                o.set(q, slots[((stage * R + r) * kPieces + q) * G]);
         } else {
             o.load(p + (p ? row * ld + c : 0), p ? d - c : 0, vec);
         }
@@ -171,32 +199,37 @@ __device__ __forceinline__ void put(void *p, int64_t ld, int64_t row, int c, int
 }
 
 // Weights of a row (1 where there are none, 0 past its end): in registers where
-// a thread has eight, in shared memory where it has more.
+// a thread has eight, in shared memory (of the whole CTA) where it has more.
 template <int R>
 struct Weights {
     float w[R == 1 ? 8 : 1];
-    float4 *slots;
+    const float4 *slots;
+    int G;
 
-    __device__ __forceinline__ void load(const float *p, int d, uint8_t *&smem)
+    // (to be used after a barrier of the CTA)
+    __device__ __forceinline__ void load(const float *p, int d, const Group &gr, uint8_t *&smem)
     {
-        const int G = int(blockDim.x), t = int(threadIdx.x);
-        slots = reinterpret_cast<float4 *>(smem);
+        G = gr.size;
+        float4 *mine = reinterpret_cast<float4 *>(smem) + gr.t;
+        slots = mine;
         if (R > 1)
             smem += R * 2 * G * 16;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int c = (t + r * G) * 8;
+            const int c = (gr.t + r * G) * 8;
             float v[8];
+            if (R == 1 || gr.id == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = c + i >= d ? 0.0f : p ? p[c + i] : 1.0f;
+                for (int i = 0; i < 8; ++i)
+                    v[i] = c + i >= d ? 0.0f : p ? p[c + i] : 1.0f;
+            }
             if (R == 1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     w[R == 1 ? i : 0] = v[i];
-            } else {
-                slots[(2 * r) * G + t] = make_float4(v[0], v[1], v[2], v[3]);
-                slots[(2 * r + 1) * G + t] = make_float4(v[4], v[5], v[6], v[7]);
+            } else if (gr.id == 0) {
+                mine[(2 * r) * G] = make_float4(v[0], v[1], v[2], v[3]);
+                mine[(2 * r + 1) * G] = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
     }
@@ -208,8 +241,7 @@ struct Weights {
             for (int i = 0; i < 8; ++i)
                 v[i] = w[R == 1 ? i : 0];
         } else {
-            const int G = int(blockDim.x), t = int(threadIdx.x);
-            const float4 a = slots[(2 * r) * G + t], b = slots[(2 * r + 1) * G + t];
+            const float4 a = slots[(2 * r) * G], b = slots[(2 * r + 1) * G];
             v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
             v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         }
@@ -221,29 +253,30 @@ __device__ __forceinline__ void async_commit()
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Until only the latest kNormStages - 1 groups are on their way.
+// Until only the latest group is on its way.
 __device__ __forceinline__ void async_wait()
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kNormStages - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(1) : "memory");
 }
 
 template <typename S, typename B, int R, bool RING>
 __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ float4 red[2][kNormMaxThreads / 32];
-    BlockSum sum{red, 0};
-    const int G = int(blockDim.x);
+    __shared__ float4 red[2 * kNormMaxThreads / 32];
+    const Group gr(p.warps);
+    GroupSum sum{gr, red + 2 * gr.id * gr.warps, 0};
+    const int G = gr.size;
     const float inv_d = 1.0f / float(p.d);
-    uint8_t *smem = smem_raw;
-    const Rows<S, R, RING> xs(p.x, p.ldx, p.d, p.vec_x, smem);
-    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, smem);
+    uint8_t *smem = smem_raw + gr.id * p.ring_bytes;  // a ring for each group, then the weights
+    const Rows<S, R, RING> xs(p.x, p.ldx, p.d, p.vec_x, gr, smem);
+    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T, step = gridDim.x;
+    const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T, step = int64_t(gridDim.x) * gr.count, first = int64_t(blockIdx.x) * gr.count + gr.id;
     auto is_live = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
-    // the rows of the next two turns are on their way while one is worked on
-    int64_t ahead = blockIdx.x;
+    // the next turn's row is on its way while one is worked on
+    int64_t ahead = first;
     int in = 0;
     auto fetch = [&](bool live) {
         if (live) {
@@ -252,23 +285,22 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
         }
         async_commit();
         ahead += step;
-        if (++in == kNormStages)
-            in = 0;
+        in ^= 1;
     };
-    bool live = is_live(blockIdx.x);
+    bool live = is_live(first);
     fetch(live);
     bool next = is_live(ahead);
-    float gate = p.gate && live ? p.gate[blockIdx.x] : 0.0f;
-    fetch(next);
+    float gate = p.gate && live ? p.gate[first] : 0.0f;
     Weights<R> pre, post;
-    pre.load(p.pre, p.d, smem);
-    post.load(p.post, p.d, smem);
-    bool coming = is_live(ahead);
+    smem = smem_raw + gr.count * p.ring_bytes;
+    pre.load(p.pre, p.d, gr, smem);
+    post.load(p.post, p.d, gr, smem);
+    if (R > 1)
+        __syncthreads();
     int out = 0;
-    for (int64_t t = blockIdx.x; t < rows; t += step) {
-        const bool third = coming;
-        fetch(third);
-        coming = is_live(ahead);
+    for (int64_t t = first; t < rows; t += step) {
+        fetch(next);
+        const bool coming = is_live(ahead);
         const float g = gate_of(gate, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
@@ -300,7 +332,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const int c = (int(threadIdx.x) + r * G) * 8;
+                    const int c = (gr.t + r * G) * 8;
                     float f[8], w[8];
                     o[r].to(f);
                     x[r].to(v[r]);
@@ -324,7 +356,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                 if (p.o && t < p.T) {
                     Oct<S> zero;
                     zero.from(v[r]);
-                    put<RING>(p.xn, p.ldxn, t, (int(threadIdx.x) + r * G) * 8, p.d, p.vec_xn, zero);
+                    put<RING>(p.xn, p.ldxn, t, (gr.t + r * G) * 8, p.d, p.vec_xn, zero);
                 }
             }
         }
@@ -343,7 +375,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int c = (int(threadIdx.x) + r * G) * 8;
+                const int c = (gr.t + r * G) * 8;
                 float w[8];
                 pre.get(r, w);
 #pragma unroll
@@ -360,36 +392,37 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                     if (t < p.T && c < p.d)
                         *reinterpret_cast<uint32_t *>(p.codes + t * (p.d / 2) + c / 2) =
                             mx_encode8(v[r], byte);
-                    if ((threadIdx.x & 15) == 0 && c < p.k_tiles * 128)
+                    if ((gr.t & 15) == 0 && c < p.k_tiles * 128)
                         *mx_scale_word(p.scales, t, c / 128, p.k_tiles) = word;
                 }
             }
         }
         live = next;
-        next = third;
-        if (++out == kNormStages)
-            out = 0;
+        next = coming;
+        out ^= 1;
     }
 }
 
 template <typename S, typename B, int R, bool RING>
-__global__ void __maxnreg__(R == 1 ? 80 : 128) k_block_norm_grad(const NormGradArgs p)
+__global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradArgs p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ float4 red[2][kNormMaxThreads / 32];
-    BlockSum sum{red, 0};
-    const int G = int(blockDim.x);
+    __shared__ float4 red[2 * kNormMaxThreads / 32];
+    const Group gr(p.warps);
+    GroupSum sum{gr, red + 2 * gr.id * gr.warps, 0};
+    const int G = gr.size;
     const float inv_d = 1.0f / float(p.d);
-    uint8_t *smem = smem_raw;
-    const Rows<S, R, RING> xns(p.dh ? p.xn : nullptr, p.ldxn, p.d, p.vec_xn, smem);
-    const Rows<S, R, RING> dxns(p.dxn, p.lddxn, p.d, p.vec_dxn, smem);
-    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, smem);
-    const Rows<B, R, RING> dhs(p.dh, p.lddh, p.d, p.vec_dh, smem);
+    uint8_t *smem = smem_raw + gr.id * p.ring_bytes;  // a ring for each group, then the weights
+    const Rows<S, R, RING> xns(p.dh ? p.xn : nullptr, p.ldxn, p.d, p.vec_xn, gr, smem);
+    const Rows<S, R, RING> dxns(p.dxn, p.lddxn, p.d, p.vec_dxn, gr, smem);
+    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
+    const Rows<B, R, RING> dhs(p.dh, p.lddh, p.d, p.vec_dh, gr, smem);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t step = gridDim.x;
+    const int64_t step = int64_t(gridDim.x) * gr.count;
+    const int64_t first = int64_t(blockIdx.x) * gr.count + gr.id;
     auto is_live = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
-    int64_t ahead = blockIdx.x;
+    int64_t ahead = first;
     int in = 0;
     auto fetch = [&](bool live) {
         if (live) {
@@ -400,24 +433,23 @@ __global__ void __maxnreg__(R == 1 ? 80 : 128) k_block_norm_grad(const NormGradA
         }
         async_commit();
         ahead += step;
-        if (++in == kNormStages)
-            in = 0;
+        in ^= 1;
     };
-    bool live = is_live(blockIdx.x);
+    bool live = is_live(first);
     fetch(live);
     bool next = is_live(ahead);
-    float gate = p.gate && live ? p.gate[blockIdx.x] : 0.0f;
-    fetch(next);
+    float gate = p.gate && live ? p.gate[first] : 0.0f;
     Weights<R> pre, post;
-    pre.load(p.pre, p.d, smem);
-    post.load(p.post, p.d, smem);
+    smem = smem_raw + gr.count * p.ring_bytes;
+    pre.load(p.pre, p.d, gr, smem);
+    post.load(p.post, p.d, gr, smem);
+    if (R > 1)
+        __syncthreads();
     float dpre[R][8] = {}, dpost[R][8] = {};
-    bool coming = is_live(ahead);
     int out = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += step) {
-        const bool third = coming;
-        fetch(third);
-        coming = is_live(ahead);
+    for (int64_t t = first; t < p.T; t += step) {
+        fetch(next);
+        const bool coming = is_live(ahead);
         const float g = gate_of(gate, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
@@ -453,7 +485,7 @@ __global__ void __maxnreg__(R == 1 ? 80 : 128) k_block_norm_grad(const NormGradA
             float q[1] = {0.0f}, d[R][8];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int c = (int(threadIdx.x) + r * G) * 8;
+                const int c = (gr.t + r * G) * 8;
                 float x[8], h[8], f[8], w[8], v[8];
                 xn[r].to(x);
                 dh[r].to(h);
@@ -475,12 +507,12 @@ __global__ void __maxnreg__(R == 1 ? 80 : 128) k_block_norm_grad(const NormGradA
             if (p.o) {
                 if (p.post_norm || p.dgate)
                     sum(q);
-                if (p.dgate && threadIdx.x == 0)
+                if (p.dgate && gr.t == 0)
                     p.dgate[t] = r1 * q[0] * (p.sigmoid ? g * (1.0f - g) : 1.0f);
                 const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q[0] * inv_d)) : 0.0f;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const int c = (int(threadIdx.x) + r * G) * 8;
+                    const int c = (gr.t + r * G) * 8;
                     float f[8], v[8];
                     o[r].to(f);
                     post.get(r, v);
@@ -502,31 +534,56 @@ __global__ void __maxnreg__(R == 1 ? 80 : 128) k_block_norm_grad(const NormGradA
             zb.from(zero);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int c = (int(threadIdx.x) + r * G) * 8;
+                const int c = (gr.t + r * G) * 8;
                 put<RING>(p.dx, p.lddx, t, c, p.d, p.vec_dx, zs);
                 if (p.o)
                     put<RING>(p.d_o, p.lddo, t, c, p.d, p.vec_do, zb);
             }
-            if (p.dgate && threadIdx.x == 0)
+            if (p.dgate && gr.t == 0)
                 p.dgate[t] = 0.0f;
         }
         live = next;
-        next = third;
-        if (++out == kNormStages)
-            out = 0;
+        next = coming;
+        out ^= 1;
     }
     if (!p.part)
         return;
     float *part = p.part + int64_t(blockIdx.x) * 2 * p.d;
+    if (gr.count == 1) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = (int(threadIdx.x) + r * G) * 8;
+        for (int r = 0; r < R; ++r) {
+            const int c = (gr.t + r * G) * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < p.d) {
-                part[c + i] = dpre[r][i];
-                part[p.d + c + i] = dpost[r][i];
-            }
+            for (int i = 0; i < 8; ++i)
+                if (c + i < p.d) {
+                    part[c + i] = dpre[r][i];
+                    part[p.d + c + i] = dpost[r][i];
+                }
+        }
+        return;
+    }
+    // the groups' sums, in order, through the rings' memory (of 2 R 8 G floats a
+    // group, see norm_shape)
+    float *all = reinterpret_cast<float *>(smem_raw);
+    const int words = 2 * R * 8 * G;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            all[gr.id * words + (r * 8 + i) * G + gr.t] = dpre[r][i];
+            all[gr.id * words + ((R + r) * 8 + i) * G + gr.t] = dpost[r][i];
+        }
+    __syncthreads();
+    for (int j = int(threadIdx.x); j < words; j += int(blockDim.x)) {
+        float v = 0.0f;
+        for (int k = 0; k < gr.count; ++k)
+            v += all[k * words + j];
+        const int which = j / (R * 8 * G), r = j / (8 * G) % R, i = j / G % 8;
+        const int c = (j % G + r * G) * 8 + i;
+        if (c < p.d)
+            part[which * p.d + c] = v;
     }
 }
 
@@ -564,19 +621,40 @@ __global__ void __launch_bounds__(kSumThreads)
 
 // ---- host ---------------------------------------------------------------------
 
-constexpr size_t kNormSmem = 200 * 1024;  // the most dynamic shared memory of a CTA: fp32 rows' ring
-static_assert(kNormStages * kNormMaxThreads * 16 * 8 <= kNormSmem, "");
+constexpr size_t kNormSmem = 200 * 1024;  // the most dynamic shared memory of a CTA
 
+// How a launch lays rows out.
 struct Shape {
-    int threads, r;
+    int warps, r, groups;  // of a row; rounds of eight elements a thread; rows side by side
+    bool ring;
+    size_t ring_bytes, smem;  // of a group, of a CTA
+
+    int threads() const { return 32 * warps * groups; }
 };
 
-// Threads and rounds of a row of d elements (`whole`: up to a multiple of 128).
-Shape norm_shape(int d, bool whole)
+// A thread has eight elements of rows that a warp can hold so, else 16 (its share
+// of a row's sums and addresses costs about as much as eight elements do), or
+// 32 past 8192; eight too where the rows do not go round the SMs, and only a
+// row's time counts.  `whole`: rows up to a multiple of 128; `bytes`: of a row's
+// element in all tensors that are read; `sums`: column sums are kept.
+Shape norm_shape(int64_t rows, int d, bool whole, bool vec, int bytes, bool sums)
 {
     const int chunks = whole ? mx_k_tiles(d) * 16 : (d + 7) / 8;
-    const int r = chunks <= kNormMaxThreads ? 1 : chunks <= 2 * kNormMaxThreads ? 2 : 4;
-    return {((chunks + r - 1) / r + 31) / 32 * 32, r};
+    Shape s;
+    s.r = chunks <= (rows > device_sm_count() ? 32 : kNormMaxThreads) ? 1
+          : chunks <= 2 * kNormMaxThreads                             ? 2
+                                                                      : 4;
+    s.warps = ((chunks + s.r - 1) / s.r + 31) / 32;
+    s.groups = std::max(1, 8 / s.warps);
+    const size_t weights = s.r > 1 ? size_t(4) * s.r * 32 * s.warps * 16 : 0;
+    s.ring_bytes = size_t(kNormStages) * s.r * 8 * bytes * 32 * s.warps;
+    s.ring = vec && s.r <= 2 && s.groups * s.ring_bytes + weights <= kNormSmem;
+    if (!s.ring)
+        s.ring_bytes = 0;
+    if (sums && s.groups > 1)  // the groups' sums pass through the rings' memory
+        s.ring_bytes = std::max(s.ring_bytes, size_t(2) * s.r * 8 * 32 * s.warps * 4);
+    s.smem = s.groups * s.ring_bytes + weights;
+    return s;
 }
 
 // f(S, B, R, RING) of the types, the rounds and whether a ring can be used.
@@ -590,7 +668,8 @@ cudaError_t with_types(int s, int b, int r, bool ring, F f)
         using No = std::false_type;
         return r == 1   ? ring ? f(S(), B(), std::integral_constant<int, 1>(), Yes())
                                : f(S(), B(), std::integral_constant<int, 1>(), No())
-               : r == 2 ? f(S(), B(), std::integral_constant<int, 2>(), No())
+               : r == 2 ? ring ? f(S(), B(), std::integral_constant<int, 2>(), Yes())
+                               : f(S(), B(), std::integral_constant<int, 2>(), No())
                         : f(S(), B(), std::integral_constant<int, 4>(), No());
     };
     if (s == MOE_DT_BF16)
@@ -605,30 +684,30 @@ cudaError_t with_types(int s, int b, int r, bool ring, F f)
 // Launches a norm kernel on as many CTAs as the device holds at once (what it
 // holds is asked once per kernel, number of warps and device).
 template <auto KERN, typename Args>
-cudaError_t launch_norm(const Args &a, Shape sh, size_t ring_bytes, int64_t rows, int most,
-                        int &ctas, cudaStream_t s)
+cudaError_t launch_norm(Args &a, const Shape &sh, int64_t rows, int most, int &ctas, cudaStream_t s)
 {
     constexpr int kDevices = 16;
     static std::atomic<int> per_sm[kDevices][kNormMaxThreads / 32 + 1];
-    const size_t smem = ring_bytes + (sh.r > 1 ? size_t(2) * sh.r * 2 * sh.threads * 16 : 0);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    int held = dev < kDevices ? per_sm[dev][sh.threads / 32].load(std::memory_order_acquire) : 0;
+    int held = dev < kDevices ? per_sm[dev][sh.warps].load(std::memory_order_acquire) : 0;
     if (!held) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(KERN),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, KERN, sh.threads, smem);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, KERN, sh.threads(), sh.smem);
         if (e != cudaSuccess)
             return e;
         held = std::max(held, 1);
         if (dev < kDevices)
-            per_sm[dev][sh.threads / 32].store(held, std::memory_order_release);
+            per_sm[dev][sh.warps].store(held, std::memory_order_release);
     }
-    ctas = int(std::min<int64_t>({int64_t(held) * device_sm_count(), rows, most}));
-    return launch_pdl(KERN, dim3(ctas), dim3(sh.threads), smem, s, a);
+    a.warps = sh.warps, a.ring_bytes = int(sh.ring_bytes);
+    ctas = int(std::min<int64_t>(
+        {int64_t(held) * device_sm_count(), (rows + sh.groups - 1) / sh.groups, most}));
+    return launch_pdl(KERN, dim3(ctas), dim3(sh.threads()), sh.smem, s, a);
 }
 
 inline bool aligned(const void *p, uintptr_t a)
@@ -679,17 +758,17 @@ extern "C" int moe_block_norm(const void *x, int64_t ldx, int x_dtype, const voi
     a.vec_x = rows_vec(x, ldx, xs), a.vec_o = rows_vec(o, ldo, bs);
     a.vec_xn = rows_vec(xn, ldxn, xs), a.vec_h = rows_vec(h, ldh, bs);
     a.alpha = alpha, a.eps = eps;
-    const Shape sh = norm_shape(d, codes != nullptr);
+    const bool vec = d % 8 == 0 && a.vec_x && (!o || (a.vec_o && a.vec_xn)) && (!h || a.vec_h);
+    const Shape sh = norm_shape(T, d, codes != nullptr, vec, xs + bs, false);
     const int64_t rows = codes ? (int64_t(T) + 127) / 128 * 128 : T;
-    const bool ring = d % 8 == 0 && a.vec_x && (!o || (a.vec_o && a.vec_xn)) && (!h || a.vec_h);
-    const size_t bytes = ring ? size_t(kNormStages) * sh.threads * 8 * (xs + bs) : 0;
     int ctas = 0;
-    const cudaError_t e = with_types(x_dtype, b_dtype, sh.r, ring, [&](auto s, auto b, auto r, auto g) {
-        constexpr auto kern =
-            k_block_norm<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
-        return launch_norm<kern>(a, sh, decltype(g)::value ? bytes : 0, rows, INT_MAX, ctas,
-                                 reinterpret_cast<cudaStream_t>(stream));
-    });
+    const cudaError_t e =
+        with_types(x_dtype, b_dtype, sh.r, sh.ring, [&](auto s, auto b, auto r, auto g) {
+            constexpr auto kern =
+                k_block_norm<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
+            return launch_norm<kern>(a, sh, rows, INT_MAX, ctas,
+                                     reinterpret_cast<cudaStream_t>(stream));
+        });
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -747,17 +826,16 @@ extern "C" int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, co
     a.vec_dxn = rows_vec(dxn, lddxn, xs), a.vec_dh = rows_vec(dh, lddh, bs);
     a.vec_dx = rows_vec(dx, lddx, xs), a.vec_do = rows_vec(d_o, lddo, bs);
     a.alpha = o ? alpha : 1.0f, a.eps = eps;
-    const Shape sh = norm_shape(d, false);
-    const bool ring = d % 8 == 0 && (!dh || (a.vec_xn && a.vec_dh)) && (!dxn || a.vec_dxn) &&
-                      a.vec_dx && (!o || (a.vec_o && a.vec_do));
-    const size_t bytes = ring ? size_t(kNormStages) * sh.threads * 16 * (xs + bs) : 0;
+    const bool vec = d % 8 == 0 && (!dh || (a.vec_xn && a.vec_dh)) && (!dxn || a.vec_dxn) &&
+                     a.vec_dx && (!o || (a.vec_o && a.vec_do));
+    const Shape sh = norm_shape(T, d, false, vec, 2 * (xs + bs), sums);
     int ctas = 0;
-    cudaError_t e = with_types(x_dtype, b_dtype, sh.r, ring, [&](auto s, auto b, auto r, auto g) {
-        constexpr auto kern =
-            k_block_norm_grad<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
-        return launch_norm<kern>(a, sh, decltype(g)::value ? bytes : 0, T, kNormGradCtas, ctas,
-                                 stm);
-    });
+    cudaError_t e =
+        with_types(x_dtype, b_dtype, sh.r, sh.ring, [&](auto s, auto b, auto r, auto g) {
+            constexpr auto kern =
+                k_block_norm_grad<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
+            return launch_norm<kern>(a, sh, T, kNormGradCtas, ctas, stm);
+        });
     if (e == cudaSuccess && sums)
         e = launch_pdl(k_norm_col_sum, dim3((2 * d + 31) / 32), dim3(kSumThreads), 0, stm,
                        static_cast<const float *>(ws), ctas, d, dpre, dpost);
