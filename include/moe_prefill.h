@@ -757,6 +757,9 @@ MOE_API int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scale
  * in   residual  y_dtype [T, N], rows ldr elements apart, or NULL; may be y itself
  * out  y         y_dtype [T, N] (any MOE_DT_*), rows ldy elements apart
  * in   status    as in moe_linear
+ * moe_linear_rows_mxfp4 -- the same for rows x dtype [T, K] (any MOE_DT_*, rows ldx
+ * elements apart, as in moe_quantize_rows_mxfp4), which it quantises first, into
+ * ws: moe_linear_rows_mxfp4_workspace_bytes(T, K) bytes, 256-byte aligned.
  * A row (or weight) with a NaN block makes its outputs NaN.  T >= 0, N >= 1, K a
  * positive multiple of 32; T, K, N <= 2^31 - 512; ldr, ldy >= N.  codes and scales
  * 16-byte aligned, the others to their element.  Deterministic.
@@ -765,6 +768,12 @@ MOE_API int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const ui
                              const uint8_t *W_scales, const float *bias, const void *residual,
                              int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy,
                              int y_dtype, uint32_t *status, moe_stream_t stream);
+MOE_API size_t moe_linear_rows_mxfp4_workspace_bytes(int T, int K);
+MOE_API int moe_linear_rows_mxfp4(const void *x, int64_t ldx, int x_dtype, const uint8_t *W,
+                                  const uint8_t *W_scales, const float *bias,
+                                  const void *residual, int64_t ldr, int act, int T, int K, int N,
+                                  void *y, int64_t ldy, int y_dtype, void *ws, size_t ws_bytes,
+                                  uint32_t *status, moe_stream_t stream);
 
 /*
  * moe_selftest_linear_wait_limit -- the same of moe_linear (bf16, contiguous,

@@ -147,6 +147,11 @@ _SIGS = {
     "moe_linear_mxfp4": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int,
                                    C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p]),
+    "moe_linear_rows_mxfp4_workspace_bytes": (C.c_size_t, [C.c_int] * 2),
+    "moe_linear_rows_mxfp4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_void_p, C.c_int64, C.c_int, C.c_int,
+                                        C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int,
+                                        C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
     "moe_take_status": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "moe_selftest_linear_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                                  C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
@@ -928,10 +933,23 @@ _U8 = (torch.uint8,)
 def _mx(q, name: str, shape, dev):
     """Addresses of MXFP4 rows of the given shape on dev."""
     R, K = shape
+    c, s = q
     if K % 32 or K <= 0:
         raise ValueError(f"{name}: rows of a positive multiple of 32, got {K}")
-    return (_flat(q.codes, name + ".codes", (R, K // 2), _U8, dev),
-            _flat(q.scales, name + ".scales", ((R + 127) // 128, (K + 127) // 128, 512), _U8, dev))
+    if (c.dtype is not torch.uint8 or c.device != dev or c.shape != (R, K // 2)
+            or not c.is_contiguous() or not c.is_cuda):
+        _refuse(c, name + ".codes", (R, K // 2), _U8, dev)
+    tiles = ((R + 127) // 128, (K + 127) // 128, 512)
+    if s.dtype is not torch.uint8 or s.device != dev or s.shape != tiles or not s.is_contiguous():
+        _refuse(s, name + ".scales", tiles, _U8, dev)
+    return c.data_ptr(), s.data_ptr()
+
+
+def _beside(t, name: str, shape, dtype, dev) -> int:
+    """As ``_ld``, for a tensor of one type beside another on dev."""
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _refuse(t, name, shape, (dtype,), dev)
+    return shape[1] if t.is_contiguous() else _ld(t, name, shape, (dtype,), dev)
 
 
 def quantize_rows_mxfp4(x, out: Mxfp4Rows | None = None) -> Mxfp4Rows:
@@ -945,8 +963,8 @@ def quantize_rows_mxfp4(x, out: Mxfp4Rows | None = None) -> Mxfp4Rows:
         with torch.cuda.device(dev):
             return quantize_rows_mxfp4(x, out)
     if out is None:
-        out = Mxfp4Rows.empty(R, K, dev)
-        cp, sp = out.codes.data_ptr(), out.scales.data_ptr()
+        out = c, s = Mxfp4Rows.empty(R, K, dev)
+        cp, sp = c.data_ptr(), s.data_ptr()
     else:
         cp, sp = _mx(out, "out", (R, K), dev)
     rc = (_lib or lib()).moe_quantize_rows_mxfp4(x.data_ptr(), ldx, _DTYPES[x.dtype], R, K, cp, sp,
@@ -979,28 +997,38 @@ def dequantize_rows_mxfp4(q: Mxfp4Rows, dtype=torch.bfloat16, y=None):
     return y
 
 
+@functools.lru_cache(maxsize=1024)
+def linear_rows_mxfp4_workspace_bytes(T: int, K: int) -> int:
+    """Of ``linear_mxfp4`` for rows that it quantises."""
+    return int((_lib or lib()).moe_linear_rows_mxfp4_workspace_bytes(T, K))
+
+
 def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", out_dtype=None,
-                 y=None, x_rows: Mxfp4Rows | None = None, status=None):
+                 y=None, ws=None, status=None):
     """moe_linear_mxfp4: y = act(x W^T + bias) + residual, both operands in MXFP4.
 
     x [T, K]: ``Mxfp4Rows``, or 16-bit or float32 rows, which are quantised first
-    (into ``x_rows`` if given).  W [N, K] from ``quantize_rows_mxfp4``.  bias fp32
-    [N], residual and y [T, N] of ``out_dtype`` (16-bit or float32; by default x's
-    type, bfloat16 for MXFP4 rows); their rows may lie further apart than their
-    length.  ``residual`` may be ``y``; ``status`` as in ``linear``."""
+    (moe_linear_rows_mxfp4, into ``ws`` if given).  W [N, K] from
+    ``quantize_rows_mxfp4``.  bias fp32 [N], residual and y [T, N] of ``out_dtype``
+    (16-bit or float32; by default x's type, bfloat16 for MXFP4 rows); their rows
+    may lie further apart than their length.  ``residual`` may be ``y``;
+    ``status`` as in ``linear``."""
     T, K = x.shape
-    N = W.codes.shape[0]
-    rows = isinstance(x, Mxfp4Rows)
     dev = W.codes.device
+    N = W.codes.shape[0]
     if dev.index != _current_device():
         with torch.cuda.device(dev):
-            return linear_mxfp4(x, W, bias, residual, act, out_dtype, y, x_rows, status)
+            return linear_mxfp4(x, W, bias, residual, act, out_dtype, y, ws, status)
     wp, wsp = _mx(W, "W", (N, K), dev)
-    code = ACTS[act] if act in ACTS else _unknown(ACTS, act, "act")
+    rows = isinstance(x, Mxfp4Rows)
+    if rows:
+        xp, xsp = _mx(x, "x", (T, K), dev)
+    else:
+        ldx = _ld(x, "x", (T, K), _DTYPES, dev)
     if y is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16 if rows else x.dtype
-        if out_dtype not in _DTYPES:
+        elif out_dtype not in _DTYPES:
             raise ValueError(f"out_dtype: unexpected dtype {out_dtype}")
         y = torch.empty((T, N), dtype=out_dtype, device=dev)
         ldy = N
@@ -1013,19 +1041,24 @@ def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", o
         ldr = _ld(residual, "residual", (T, N), (y.dtype,), dev)
         rp = residual.data_ptr()
     bp = None if bias is None else _flat(bias, "bias", (N,), _F32, dev)
+    code = ACTS[act] if act in ACTS else _unknown(ACTS, act, "act")
     stp = None if status is None else _status(status, dev)
-    if not rows:
-        if x.device != dev:
-            _refuse(x, "x", (T, K), _DTYPES, dev)
-        x = quantize_rows_mxfp4(x, x_rows)
-        xp, xsp = x.codes.data_ptr(), x.scales.data_ptr()
+    if rows:
+        rc = (_lib or lib()).moe_linear_mxfp4(xp, xsp, wp, wsp, bp, rp, ldr, code, T, K, N,
+                                              y.data_ptr(), ldy, _DTYPES[y.dtype], stp,
+                                              _raw_stream(dev.index))
     else:
-        xp, xsp = _mx(x, "x", (T, K), dev)
-    rc = (_lib or lib()).moe_linear_mxfp4(xp, xsp, wp, wsp, bp, rp, ldr, code, T, K, N,
-                                          y.data_ptr(), ldy, _DTYPES[y.dtype], stp,
-                                          _raw_stream(dev.index))
+        if ws is None:
+            ws = torch.empty(linear_rows_mxfp4_workspace_bytes(T, K), dtype=torch.uint8, device=dev)
+            qp, ws_bytes = ws.data_ptr(), ws.numel()
+        else:
+            qp, ws_bytes = _ws(ws, dev)
+        rc = (_lib or lib()).moe_linear_rows_mxfp4(x.data_ptr(), ldx, _DTYPES[x.dtype], wp, wsp, bp,
+                                                   rp, ldr, code, T, K, N, y.data_ptr(), ldy,
+                                                   _DTYPES[y.dtype], qp, ws_bytes, stp,
+                                                   _raw_stream(dev.index))
     if rc:
-        raise MoeError("moe_linear_mxfp4", rc)
+        raise MoeError("moe_linear_mxfp4" if rows else "moe_linear_rows_mxfp4", rc)
     return y
 
 
@@ -1047,51 +1080,52 @@ def block_norm(x, o=None, pre=None, post=None, gate=None, mask=None, post_norm: 
     or uint8 [T]) are not read and come out as 0.  Returns xn (x itself without
     o), h of o's type (``h_dtype``, or x's, without o) and, with ``mxfp4``, mx:
     the rows of h in MXFP4.  xn, h and mx may be passed in; xn may be x."""
-    T, d = x.shape
+    shape = T, d = x.shape
     dev = x.device
     xt = x.dtype
-    ldx = _ld(x, "x", (T, d), _DTYPES, dev)
+    ldx = _ld(x, "x", shape, _DTYPES, dev)
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return block_norm(x, o, pre, post, gate, mask, post_norm, gate_act, alpha, eps,
                               h_dtype, mxfp4, xn, h, mx)
-    op, ldo, xnp, ldxn, hp, ldh, cp, sp = None, 0, None, 0, None, 0, None, None
-    out = {}
+    op = xnp = hp = cp = sp = None
+    ldo = ldxn = ldh = 0
     if o is not None:
-        ldo = _ld(o, "o", (T, d), _block_types(xt), dev)
-        op = o.data_ptr()
         bt = o.dtype
+        if bt is not xt and bt not in _block_types(xt):
+            _refuse(o, "o", shape, _block_types(xt), dev)
         if h_dtype is not None and h_dtype is not bt:
             raise ValueError(f"h_dtype: expected {bt}, got {h_dtype}")
+        ldo = _beside(o, "o", shape, bt, dev)
+        op = o.data_ptr()
         if xn is None:
-            xn = torch.empty((T, d), dtype=xt, device=dev)
+            xn = torch.empty(shape, dtype=xt, device=dev)
             ldxn = d
         else:
-            ldxn = _ld(xn, "xn", (T, d), (xt,), dev)
+            ldxn = _beside(xn, "xn", shape, xt, dev)
         xnp = xn.data_ptr()
-        out["xn"] = xn
+        out = {"xn": xn}
     else:
         if post is not None or gate is not None or xn is not None:
             raise ValueError("post, gate and xn come with o")
         bt = h_dtype or (h.dtype if h is not None else xt)
         if bt not in _block_types(xt):
             raise ValueError(f"h_dtype: {bt} beside a stream of {xt}")
-        out["xn"] = x
+        out = {"xn": x}
     if pre is not None:
         if h is None:
-            h = torch.empty((T, d), dtype=bt, device=dev)
+            h = torch.empty(shape, dtype=bt, device=dev)
             ldh = d
         else:
-            ldh = _ld(h, "h", (T, d), (bt,), dev)
+            ldh = _beside(h, "h", shape, bt, dev)
         hp = h.data_ptr()
         out["h"] = h
         if mx is not None:
-            cp, sp = _mx(mx, "mx", (T, d), dev)
-        elif mxfp4:
-            mx = Mxfp4Rows.empty(T, d, dev)
-            cp, sp = mx.codes.data_ptr(), mx.scales.data_ptr()
-        if mx is not None:
+            cp, sp = _mx(mx, "mx", shape, dev)
             out["mx"] = mx
+        elif mxfp4:
+            out["mx"] = c, s = Mxfp4Rows.empty(T, d, dev)
+            cp, sp = c.data_ptr(), s.data_ptr()
     elif h is not None or mxfp4 or mx is not None:
         raise ValueError("h and its MXFP4 rows come with pre")
     rc = (_lib or lib()).moe_block_norm(
@@ -1099,7 +1133,7 @@ def block_norm(x, o=None, pre=None, post=None, gate=None, mask=None, post_norm: 
         None if pre is None else _flat(pre, "pre", (d,), _F32, dev),
         None if post is None else _flat(post, "post", (d,), _F32, dev),
         None if gate is None else _flat(gate, "gate", (T,), _F32, dev),
-        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, d, bool(post_norm),
+        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), T, d, post_norm,
         GATE_ACTS[gate_act] if gate_act in GATE_ACTS else _unknown(GATE_ACTS, gate_act, "gate_act"),
         alpha, eps, xnp, ldxn, hp, ldh, cp, sp, _raw_stream(dev.index))
     if rc:
@@ -1123,10 +1157,10 @@ def block_norm_grad(xn, o=None, dxn=None, dh=None, pre=None, post=None, gate=Non
     was no o).  Returns dx and, where the inputs were, do, dgate fp32 [T], and with
     ``weights`` dpre and dpost fp32 [d].  dx and do may be passed in; dx may be
     dxn."""
-    T, d = xn.shape
+    shape = T, d = xn.shape
     dev = xn.device
     xt = xn.dtype
-    ldxn = _ld(xn, "xn", (T, d), _DTYPES, dev)
+    ldxn = _ld(xn, "xn", shape, _DTYPES, dev)
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return block_norm_grad(xn, o, dxn, dh, pre, post, gate, mask, post_norm, gate_act,
@@ -1137,40 +1171,46 @@ def block_norm_grad(xn, o=None, dxn=None, dh=None, pre=None, post=None, gate=Non
         raise ValueError("dh comes with pre")
     if o is None and (post is not None or gate is not None or do is not None):
         raise ValueError("post, gate and do come with o")
-    bt = o.dtype if o is not None else dh.dtype if dh is not None else xt
-    op, ldo, dop, lddo, lddxn, lddh = None, 0, None, 0, 0, 0
-    out = {}
+    first = o if o is not None else dh
+    bt = xt if first is None else first.dtype
+    if bt is not xt and bt not in _block_types(xt):
+        _refuse(first, "dh" if o is None else "o", shape, _block_types(xt), dev)
+    op = dop = dxnp = dhp = dgp = dprep = dpostp = wsp = None
+    ldo = lddo = lddxn = lddh = ws_bytes = 0
     if dxn is not None:
-        lddxn = _ld(dxn, "dxn", (T, d), (xt,), dev)
+        lddxn = _beside(dxn, "dxn", shape, xt, dev)
+        dxnp = dxn.data_ptr()
     if dh is not None:
-        lddh = _ld(dh, "dh", (T, d), (bt,) if o is not None else _block_types(xt), dev)
+        lddh = _beside(dh, "dh", shape, bt, dev)
+        dhp = dh.data_ptr()
     if dx is None:
-        dx = torch.empty((T, d), dtype=xt, device=dev)
+        dx = torch.empty(shape, dtype=xt, device=dev)
         lddx = d
     else:
-        lddx = _ld(dx, "dx", (T, d), (xt,), dev)
-    out["dx"] = dx
-    dgate = dpre = dpost = None
+        lddx = _beside(dx, "dx", shape, xt, dev)
+    out = {"dx": dx}
     if o is not None:
-        ldo = _ld(o, "o", (T, d), _block_types(xt), dev)
+        ldo = _beside(o, "o", shape, bt, dev)
         op = o.data_ptr()
         if do is None:
-            do = torch.empty((T, d), dtype=bt, device=dev)
+            do = torch.empty(shape, dtype=bt, device=dev)
             lddo = d
         else:
-            lddo = _ld(do, "do", (T, d), (bt,), dev)
+            lddo = _beside(do, "do", shape, bt, dev)
         dop = do.data_ptr()
         out["do"] = do
         if gate is not None:
             out["dgate"] = dgate = torch.empty(T, dtype=torch.float32, device=dev)
+            dgp = dgate.data_ptr()
         if post is not None and weights:
             out["dpost"] = dpost = torch.empty(d, dtype=torch.float32, device=dev)
+            dpostp = dpost.data_ptr()
     if dh is not None and weights:
         out["dpre"] = dpre = torch.empty(d, dtype=torch.float32, device=dev)
-    wsp, ws_bytes = None, 0
+        dprep = dpre.data_ptr()
     if ws is not None:
         wsp, ws_bytes = _ws(ws, dev)
-    elif dpre is not None or dpost is not None:
+    elif dprep or dpostp:
         ws = torch.empty(block_norm_grad_workspace_bytes(T, d), dtype=torch.uint8, device=dev)
         wsp, ws_bytes = ws.data_ptr(), ws.numel()
     rc = (_lib or lib()).moe_block_norm_grad(
@@ -1178,13 +1218,11 @@ def block_norm_grad(xn, o=None, dxn=None, dh=None, pre=None, post=None, gate=Non
         None if pre is None else _flat(pre, "pre", (d,), _F32, dev),
         None if post is None else _flat(post, "post", (d,), _F32, dev),
         None if gate is None else _flat(gate, "gate", (T,), _F32, dev),
-        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev),
-        None if dxn is None else dxn.data_ptr(), lddxn, None if dh is None else dh.data_ptr(), lddh,
-        T, d, bool(post_norm),
+        None if mask is None else _flat(mask, "mask", (T,), _MASK, dev), dxnp, lddxn, dhp, lddh, T,
+        d, post_norm,
         GATE_ACTS[gate_act] if gate_act in GATE_ACTS else _unknown(GATE_ACTS, gate_act, "gate_act"),
-        alpha, eps, dx.data_ptr(), lddx, dop, lddo,
-        None if dpre is None else dpre.data_ptr(), None if dpost is None else dpost.data_ptr(),
-        None if dgate is None else dgate.data_ptr(), wsp, ws_bytes, _raw_stream(dev.index))
+        alpha, eps, dx.data_ptr(), lddx, dop, lddo, dprep, dpostp, dgp, wsp, ws_bytes,
+        _raw_stream(dev.index))
     if rc:
         raise MoeError("moe_block_norm_grad", rc)
     return out

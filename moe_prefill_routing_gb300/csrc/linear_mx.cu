@@ -960,32 +960,101 @@ uint32_t *linear_mx_status_word()
 
 }  // namespace moe
 
-extern "C" int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W,
-                                const uint8_t *W_scales, const float *bias, const void *residual,
-                                int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy,
-                                int y_dtype, uint32_t *status, moe_stream_t stream)
+namespace moe {
+namespace {
+
+constexpr int kMost = INT_MAX - 511;
+
+// What both entry points check of a product, x's operands apart.
+int mx_check(const uint8_t *W, const uint8_t *W_scales, const float *bias, const void *residual,
+             int64_t ldr, int act, int T, int K, int N, const void *y, int64_t ldy, int y_dtype,
+             const uint32_t *status)
 {
-    using namespace moe;
-    constexpr int kMost = INT_MAX - 511;
     if (y_dtype != MOE_DT_BF16 && y_dtype != MOE_DT_F16 && y_dtype != MOE_DT_F32)
         return MOE_ERR_DTYPE;
     if (T < 0 || T > kMost || K < 32 || K > kMost || K % 32 != 0 || N < 1 || N > kMost ||
         act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH || ldy < N || (residual && ldr < N))
         return MOE_ERR_SHAPE;
-    if (!W || !W_scales || (T > 0 && (!x || !x_scales || !y)))
+    if (!W || !W_scales || (T > 0 && !y))
         return MOE_ERR_NULL;
     const int size = dtype_size(y_dtype);
-    if (!aligned(x, 16) || !aligned(x_scales, 16) || !aligned(W, 16) || !aligned(W_scales, 16) ||
-        !aligned(bias, 4) || !aligned(residual, size) || !aligned(y, size) || !aligned(status, 4))
-        return MOE_ERR_ALIGN;
-    if (T == 0)
-        return MOE_OK;
+    return aligned(W, 16) && aligned(W_scales, 16) && aligned(bias, 4) && aligned(residual, size) &&
+                   aligned(y, size) && aligned(status, 4)
+               ? MOE_OK
+               : MOE_ERR_ALIGN;
+}
+
+int mx_linear(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W, const uint8_t *W_scales,
+              const float *bias, const void *residual, int64_t ldr, int act, int T, int K, int N,
+              void *y, int64_t ldy, int y_dtype, uint32_t *status, cudaStream_t s)
+{
+    const int size = dtype_size(y_dtype);
     EpiArgs e = {};
     e.bias = bias, e.residual = residual, e.out = y;
     e.ldr = ldr, e.ldo = ldy;
     e.f16 = y_dtype == MOE_DT_F16, e.out_f32 = y_dtype == MOE_DT_F32, e.act = act;
     e.vec_out = vec16(y, ldy, size), e.vec_res = vec16(residual, ldr, size);
     const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status};
-    return launch_mx(q, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
-                                                                               : MOE_ERR_CUDA;
+    return launch_mx(q, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Where moe_linear_rows_mxfp4's workspace holds the scales.
+inline size_t mx_codes_bytes(int T, int K)
+{
+    return align256(size_t(T) * (K / 2));
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W,
+                                const uint8_t *W_scales, const float *bias, const void *residual,
+                                int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy,
+                                int y_dtype, uint32_t *status, moe_stream_t stream)
+{
+    using namespace moe;
+    const int rc =
+        mx_check(W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype, status);
+    if (rc != MOE_OK)
+        return rc;
+    if (T > 0 && (!x || !x_scales))
+        return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(x_scales, 16))
+        return MOE_ERR_ALIGN;
+    if (T == 0)
+        return MOE_OK;
+    return mx_linear(x, x_scales, W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype,
+                     status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t moe_linear_rows_mxfp4_workspace_bytes(int T, int K)
+{
+    using namespace moe;
+    if (T < 0 || T > kMost || K < 32 || K > kMost || K % 32 != 0)
+        return 0;
+    return std::max<size_t>(256, mx_codes_bytes(T, K) + align256(size_t(mx_scale_bytes(T, K))));
+}
+
+extern "C" int moe_linear_rows_mxfp4(const void *x, int64_t ldx, int x_dtype, const uint8_t *W,
+                                     const uint8_t *W_scales, const float *bias,
+                                     const void *residual, int64_t ldr, int act, int T, int K,
+                                     int N, void *y, int64_t ldy, int y_dtype, void *ws,
+                                     size_t ws_bytes, uint32_t *status, moe_stream_t stream)
+{
+    using namespace moe;
+    int rc = mx_check(W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype, status);
+    if (rc != MOE_OK)
+        return rc;
+    if (!ws)
+        return MOE_ERR_NULL;
+    if (ws_bytes < moe_linear_rows_mxfp4_workspace_bytes(T, K))
+        return MOE_ERR_WORKSPACE;
+    if (!aligned(ws, 256))
+        return MOE_ERR_ALIGN;
+    uint8_t *codes = static_cast<uint8_t *>(ws), *scales = codes + mx_codes_bytes(T, K);
+    rc = moe_quantize_rows_mxfp4(x, ldx, x_dtype, T, K, codes, scales, stream);
+    if (rc != MOE_OK || T == 0)
+        return rc;
+    return mx_linear(codes, scales, W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype,
+                     status, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,9 +1,10 @@
 // Rows to MXFP4 and back (moe_quantize_rows_mxfp4, moe_dequantize_rows_mxfp4).
 // The format: mx_rows.cuh.
 //
-// Both are bound by memory.  A thread has eight elements, sixteen lanes a scale
-// tile's 128 of one row; a warp takes pieces of 128 two at a time, four such
-// steps' loads in flight.
+// Both are bound by memory.  Quantising, a thread has sixteen elements and eight
+// lanes a scale tile's 128 of one row (with eight elements a thread, twice the
+// lanes per block, instructions bound it: 4096 x 11264 bf16 31 us); reading back,
+// a thread has eight, whose 16 bytes of output then lie side by side.
 #include "../../include/moe_prefill.h"
 #include "internal.h"
 #include "mx_rows.cuh"
@@ -16,9 +17,9 @@ namespace moe {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kPieces = kRowThreads / 16;  // of 128 elements, of a CTA at a time
-constexpr int kAhead = 4;
-constexpr int kRowCtas = 8;  // an SM
+constexpr int kQuantLanes = 8, kReadLanes = 16;  // of 128 elements
+constexpr int kQuantAhead = 2, kReadAhead = 4;   // pieces of 128 a thread has in flight
+constexpr int kRowCtas = 8;                      // an SM
 
 struct MxRowsArgs {
     const void *x;  // rows to quantise, or null
@@ -50,35 +51,42 @@ struct Piece {
 template <typename E>
 __global__ void __launch_bounds__(kRowThreads, 4) k_quant_rows(const MxRowsArgs p)
 {
-    const int lane = threadIdx.x & 15;
+    constexpr int kPieces = kRowThreads / kQuantLanes;
+    const int lane = threadIdx.x % kQuantLanes;
     const int64_t step = int64_t(gridDim.x) * kPieces;
     const int64_t step_rows = step / p.k_tiles;
     const int step_tiles = int(step % p.k_tiles);
-    Piece at(int64_t(blockIdx.x) * kPieces + (threadIdx.x >> 4), p.k_tiles);
+    Piece at(int64_t(blockIdx.x) * kPieces + threadIdx.x / kQuantLanes, p.k_tiles);
     pdl_wait();
     pdl_launch_dependents();
-    // (both halves of a warp walk on while one of them has rows left)
+    // (all of a warp's pieces walk on while one of them has rows left)
     while (__any_sync(0xffffffffu, at.row < p.all_rows)) {
-        Oct<E> in[kAhead];
-        Piece of[kAhead] = {at, at, at, at};
+        Oct<E> in[kQuantAhead][2];
+        Piece of[kQuantAhead] = {at, at};
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kQuantAhead; ++u) {
             of[u] = at;
-            const int c = at.kt * 128 + lane * 8;
-            in[u].load(static_cast<const E *>(p.x) + (at.row < p.rows ? at.row * p.ld + c : 0),
-                       at.row < p.rows ? p.K - c : 0, p.vec);
+            const int c = at.kt * 128 + lane * 16, left = at.row < p.rows ? p.K - c : 0;
+            const E *x = static_cast<const E *>(p.x) + (left > 0 ? at.row * p.ld + c : 0);
+            in[u][0].load(x, left, p.vec);
+            in[u][1].load(x + 8, left - 8, p.vec);
             at.advance(step_rows, step_tiles, p.k_tiles);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            float v[8];
-            in[u].to(v);
-            const uint32_t byte = mx_scale_byte(max_of_block(max_bits8(v)));
-            const uint32_t word = word_of_tile(byte);
-            const int c = of[u].kt * 128 + lane * 8;
-            if (of[u].row < p.rows && c < p.K)
-                *reinterpret_cast<uint32_t *>(p.codes + of[u].row * (p.K / 2) + c / 2) =
-                    mx_encode8(v, byte);
+        for (int u = 0; u < kQuantAhead; ++u) {
+            const uint32_t byte = mx_scale_byte(
+                max_of_lanes<2>(max(in[u][0].max_bits(), in[u][1].max_bits())));
+            const uint32_t word = word_of_tile<2>(byte);
+            const int c = of[u].kt * 128 + lane * 16;
+            if (of[u].row < p.rows && c < p.K) {
+                float v[8];
+                uint2 codes;
+                in[u][0].to(v);
+                codes.x = mx_encode8(v, byte);
+                in[u][1].to(v);
+                codes.y = mx_encode8(v, byte);
+                *reinterpret_cast<uint2 *>(p.codes + of[u].row * (p.K / 2) + c / 2) = codes;
+            }
             if (lane == 0 && of[u].row < p.all_rows)
                 *mx_scale_word(p.scales, of[u].row, of[u].kt, p.k_tiles) = word;
         }
@@ -88,18 +96,19 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_quant_rows(const MxRowsArgs 
 template <typename E>
 __global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArgs p)
 {
-    const int lane = threadIdx.x & 15;
+    constexpr int kPieces = kRowThreads / kReadLanes;
+    const int lane = threadIdx.x % kReadLanes;
     const int64_t step = int64_t(gridDim.x) * kPieces;
     const int64_t step_rows = step / p.k_tiles;
     const int step_tiles = int(step % p.k_tiles);
-    Piece at(int64_t(blockIdx.x) * kPieces + (threadIdx.x >> 4), p.k_tiles);
+    Piece at(int64_t(blockIdx.x) * kPieces + threadIdx.x / kReadLanes, p.k_tiles);
     pdl_wait();
     pdl_launch_dependents();
     while (at.row < p.rows) {
-        uint32_t code[kAhead], word[kAhead];
-        Piece of[kAhead] = {at, at, at, at};
+        uint32_t code[kReadAhead], word[kReadAhead];
+        Piece of[kReadAhead] = {at, at, at, at};
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kReadAhead; ++u) {
             of[u] = at;
             const int c = at.kt * 128 + lane * 8;
             code[u] = word[u] = 0;
@@ -111,7 +120,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArg
             at.advance(step_rows, step_tiles, p.k_tiles);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kReadAhead; ++u) {
             const int c = of[u].kt * 128 + lane * 8;
             if (of[u].row >= p.rows || c >= p.K)
                 continue;
@@ -124,10 +133,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArg
     }
 }
 
-cudaError_t launch(void (*kern)(MxRowsArgs), const MxRowsArgs &a, int64_t rows, cudaStream_t s)
+// `lanes` of a piece of 128 elements.
+cudaError_t launch(void (*kern)(MxRowsArgs), const MxRowsArgs &a, int64_t rows, int lanes,
+                   cudaStream_t s)
 {
-    const int64_t pieces = rows * a.k_tiles;
-    const int64_t ctas = std::min<int64_t>((pieces + kPieces - 1) / kPieces,
+    const int64_t pieces = rows * a.k_tiles, of_cta = kRowThreads / lanes;
+    const int64_t ctas = std::min<int64_t>((pieces + of_cta - 1) / of_cta,
                                            int64_t(device_sm_count()) * kRowCtas);
     return launch_pdl(kern, dim3(unsigned(ctas)), dim3(kRowThreads), 0, s, a);
 }
@@ -174,7 +185,7 @@ extern "C" int moe_quantize_rows_mxfp4(const void *x, int64_t ldx, int dtype, in
     const auto kern = dtype == MOE_DT_F32   ? k_quant_rows<float>
                       : dtype == MOE_DT_F16 ? k_quant_rows<__half>
                                             : k_quant_rows<__nv_bfloat16>;
-    return launch(kern, a, a.all_rows, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch(kern, a, a.all_rows, kQuantLanes, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -196,7 +207,7 @@ extern "C" int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *sc
     a.K = K, a.k_tiles = mx_k_tiles(K);
     a.vec = rows_vec(y, ldy, dtype_size(dtype));
     const auto kern = dtype == MOE_DT_F32 ? k_dequant_rows<float> : k_dequant_rows<__nv_bfloat16>;
-    return launch(kern, a, rows, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch(kern, a, rows, kReadLanes, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }

@@ -94,29 +94,24 @@ __device__ __forceinline__ void mx_decode8(uint32_t w, uint32_t byte, float (&v)
     }
 }
 
-// The largest of four neighbouring lanes' values (a block of 32: eight a lane).
-__device__ __forceinline__ uint32_t max_of_block(uint32_t m)
+// The largest of L neighbouring lanes' values.
+template <int L>
+__device__ __forceinline__ uint32_t max_of_lanes(uint32_t m)
 {
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+    for (int o = 1; o < L; o *= 2)
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
 }
 
-// The four scale bytes of sixteen neighbouring lanes as a word (in every lane).
+// The scale bytes of a tile's four blocks, of L lanes each, as a word (in every
+// lane).
+template <int L>
 __device__ __forceinline__ uint32_t word_of_tile(uint32_t byte)
 {
-    uint32_t w = byte << (8 * ((threadIdx.x >> 2) & 3));
-    w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    return w | __shfl_xor_sync(0xffffffffu, w, 8);
-}
-
-// The bits of the largest |v| of a lane's eight.
-__device__ __forceinline__ uint32_t max_bits8(const float (&v)[8])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
+    uint32_t w = byte << (8 * (threadIdx.x / L % 4));
+    w |= __shfl_xor_sync(0xffffffffu, w, L);
+    return w | __shfl_xor_sync(0xffffffffu, w, 2 * L);
 }
 
 // ---- eight neighbouring elements of a row ----------------------------------------
@@ -152,13 +147,17 @@ struct alignas(16) Oct {
         w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
 
+    __device__ __forceinline__ uint4 get(int i) const
+    {
+        return make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+
     __device__ __forceinline__ void store(E *p, int n, bool vec) const
     {
         if (vec && n >= 8) {
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i)
-                reinterpret_cast<uint4 *>(p)[i] =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                reinterpret_cast<uint4 *>(p)[i] = get(i);
         } else {
             using Bits = std::conditional_t<sizeof(E) == 4, uint32_t, uint16_t>;
             Bits *q = reinterpret_cast<Bits *>(p);
@@ -167,6 +166,29 @@ struct alignas(16) Oct {
                 if (i < n)
                     q[i] = Bits(sizeof(E) == 4 ? w[i % kWords]
                                                : w[i / 2 % kWords] >> (16 * (i & 1)));
+        }
+    }
+
+    // The bits, as a float, of the largest |v|; of a NaN or an infinity if there
+    // is one.
+    __device__ __forceinline__ uint32_t max_bits() const
+    {
+        if constexpr (sizeof(E) == 4) {
+            uint32_t m = w[0] & 0x7fffffffu;
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+            uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+            if constexpr (std::is_same<E, __nv_bfloat16>::value)
+                return m << 16;
+            else
+                return __float_as_uint(__half2float(__ushort_as_half(uint16_t(m))));
         }
     }
 

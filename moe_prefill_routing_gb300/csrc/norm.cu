@@ -128,22 +128,27 @@ __device__ __forceinline__ float gate_of(float g, bool some, int sigmoid)
 }
 
 // Rows of a tensor of [rows, d].  RING: cp.async brings them ahead of their use
-// into slots of shared memory of the thread that reads them, so that what is in
-// flight takes neither barriers nor registers (16-byte pieces are aligned then,
-// and d a multiple of 8).  Otherwise they are read when they are used.  A tensor
-// that is not there reads as zeros.
+// into slots of shared memory of the thread (fp32: the warp) that reads them, so
+// that what is in flight takes neither barriers nor registers (16-byte pieces are
+// aligned then, and d a multiple of 8).  Otherwise they are read when they are
+// used.  A tensor that is not there reads as zeros.
+//
+// Eight fp32 are two 16-byte pieces; copied by the thread that uses them, every
+// instruction would touch half of each 32-byte sector of memory.  A warp copies
+// (and, through a slot that has been read, writes) neighbouring pieces with
+// neighbouring lanes instead: 32768 rows x 2816 of an fp32 stream 210 -> 185 us.
 template <typename E, int R, bool RING>
 struct Rows {
     static constexpr int kPieces = sizeof(E) == 4 ? 2 : 1;  // of 16 bytes: eight elements
     const E *p;
     int64_t ld;
     int d, vec, G, t;  // G, t: the group's threads, and which this one is
-    uint4 *slots;      // the thread's: [stage][R][kPieces], G apart
+    uint4 *slots;      // [stage][R][G][kPieces], from the warp's first on
 
     __device__ __forceinline__ Rows(const void *tensor, int64_t ld_, int d_, int vec_,
                                     const Group &gr, uint8_t *&smem)
         : p(static_cast<const E *>(tensor)), ld(ld_), d(d_), vec(vec_), G(gr.size), t(gr.t),
-          slots(reinterpret_cast<uint4 *>(smem) + gr.t)
+          slots(reinterpret_cast<uint4 *>(smem) + (gr.t & ~31) * kPieces)
     {
         if (RING) {
             smem += kNormStages * R * kPieces * G * 16;
@@ -153,50 +158,84 @@ struct Rows {
                     for (int i = 0; i < kNormStages; ++i)
 #pragma unroll
                         for (int q = 0; q < kPieces; ++q)
-                            slots[((i * R + r) * kPieces + q) * G] = make_uint4(0, 0, 0, 0);
+                            *mine(i, r, q) = make_uint4(0, 0, 0, 0);
+            __syncwarp();
         }
+    }
+
+    // The thread's q-th piece (fp32: lanes 4 - 7 of eight take theirs in the other
+    // order, which keeps eight lanes' banks apart).
+    __device__ __forceinline__ uint4 *mine(int stage, int r, int q) const
+    {
+        return slots + (stage * R + r) * G * kPieces + (t & 31) * kPieces +
+               (kPieces == 2 ? q ^ ((t >> 2) & 1) : 0);
     }
 
     __device__ __forceinline__ void fetch(int64_t row, int stage) const
     {
         if (!RING || !p)
             return;
-        const uint4 *from = reinterpret_cast<const uint4 *>(p + row * ld) + t * kPieces;
+        if (kPieces == 2)
+            __syncwarp();  // the slot's last row has been read by every lane
+        const int w = (t & ~31) * kPieces + (t & 31);
+        const uint4 *from = reinterpret_cast<const uint4 *>(p + row * ld) + w;
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if ((t + r * G) * 8 < d) {
 #pragma unroll
-                for (int q = 0; q < kPieces; ++q)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(
-                                     slots + ((stage * R + r) * kPieces + q) * G)),
-                                 "l"(from + r * G * kPieces + q)
+            for (int q = 0; q < kPieces; ++q)
+                if ((w + 32 * q + r * G * kPieces) * (8 / kPieces) < d)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     smem_u32(slots + (stage * R + r) * G * kPieces + 32 * q +
+                                              (t & 31))),
+                                 "l"(from + r * G * kPieces + 32 * q)
                                  : "memory");
-            }
     }
 
+    // After async_wait.
     __device__ __forceinline__ Oct<E> read(int64_t row, int stage, int r) const
     {
         const int c = (t + r * G) * 8;
         Oct<E> o;
-        if (RING) {
-#pragma unroll
-            for (int q = 0; q < kPieces; ++q)
-                o.set(q, slots[((stage * R + r) * kPieces + q) * G]);
+        if (RING && kPieces == 2) {
+            const uint4 a = *mine(stage, r, 0), b = *mine(stage, r, 1);
+            const bool other = (t >> 2) & 1;
+            o.set(0, other ? b : a);
+            o.set(kPieces - 1, other ? a : b);
+        } else if (RING) {
+            o.set(0, *mine(stage, r, 0));
         } else {
             o.load(p + (p ? row * ld + c : 0), p ? d - c : 0, vec);
         }
         return o;
     }
-};
 
-// A thread's eight elements of a row to memory.
-template <bool RING, typename E>
-__device__ __forceinline__ void put(void *p, int64_t ld, int64_t row, int c, int d, int vec,
-                                    const Oct<E> &o)
-{
-    if (!RING || c < d)
-        o.store(static_cast<E *>(p) + row * ld + c, RING ? 8 : d - c, RING || vec);
-}
+    // The thread's eight elements of a row of another tensor of [rows, d]; fp32
+    // through slots whose row has been read.
+    __device__ __forceinline__ void put(void *to, int64_t to_ld, int64_t row, int stage, int r,
+                                        int to_vec, const Oct<E> &o) const
+    {
+        const int c = (t + r * G) * 8;
+        E *out = static_cast<E *>(to) + row * to_ld;
+        if (RING && kPieces == 2) {
+            __syncwarp();
+            if (c < d) {
+                const bool other = (t >> 2) & 1;
+                const uint4 a = o.get(0), b = o.get(kPieces - 1);
+                *mine(stage, r, 0) = other ? b : a;
+                *mine(stage, r, 1) = other ? a : b;
+            }
+            __syncwarp();
+            const int w = (t & ~31) * kPieces + (t & 31) + r * G * kPieces;
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q)
+                if ((w + 32 * q) * 4 < d)
+                    reinterpret_cast<uint4 *>(out)[w + 32 * q] =
+                        slots[(stage * R + r) * G * kPieces + 32 * q + (t & 31)];
+        } else if (!RING || c < d) {
+            o.store(out + c, RING ? 8 : d - c, RING || to_vec);
+        }
+    }
+};
 
 // Weights of a row (1 where there are none, 0 past its end): in registers where
 // a thread has eight, in shared memory (of the whole CTA) where it has more.
@@ -260,7 +299,8 @@ __device__ __forceinline__ void async_wait()
 }
 
 template <typename S, typename B, int R, bool RING>
-__global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p)
+__global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 128)
+    k_block_norm(const NormArgs p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ float4 red[2 * kNormMaxThreads / 32];
@@ -274,11 +314,13 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
     pdl_wait();
     pdl_launch_dependents();
     const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T, step = int64_t(gridDim.x) * gr.count, first = int64_t(blockIdx.x) * gr.count + gr.id;
-    auto is_live = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
+    // nonzero for a row that takes part; as it is loaded, so that nothing waits for
+    // it before it is used (a row later)
+    auto is_live = [&](int64_t t) -> uint32_t { return t >= p.T ? 0u : !p.mask ? 1u : p.mask[t]; };
     // the next turn's row is on its way while one is worked on
     int64_t ahead = first;
     int in = 0;
-    auto fetch = [&](bool live) {
+    auto fetch = [&](uint32_t live) {
         if (live) {
             xs.fetch(ahead, in);
             os.fetch(ahead, in);
@@ -287,9 +329,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
         ahead += step;
         in ^= 1;
     };
-    bool live = is_live(first);
+    uint32_t live = is_live(first);
     fetch(live);
-    bool next = is_live(ahead);
+    uint32_t next = is_live(ahead);
     float gate = p.gate && live ? p.gate[first] : 0.0f;
     Weights<R> pre, post;
     smem = smem_raw + gr.count * p.ring_bytes;
@@ -300,10 +342,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
     int out = 0;
     for (int64_t t = first; t < rows; t += step) {
         fetch(next);
-        const bool coming = is_live(ahead);
+        const uint32_t coming = is_live(ahead);
         const float g = gate_of(gate, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
+        if (RING && (sizeof(S) == 4 || sizeof(B) == 4))
+            __syncwarp();  // other lanes' copies
         float v[R][8];
         if (live) {
             Oct<S> x[R];
@@ -332,7 +376,6 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const int c = (gr.t + r * G) * 8;
                     float f[8], w[8];
                     o[r].to(f);
                     x[r].to(v[r]);
@@ -341,7 +384,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                     for (int i = 0; i < 8; ++i)
                         v[r][i] = p.alpha * v[r][i] + f[i] * (k * w[i]);
                     x[r].from(v[r]);
-                    put<RING>(p.xn, p.ldxn, t, c, p.d, p.vec_xn, x[r]);
+                    xs.put(p.xn, p.ldxn, t, out, r, p.vec_xn, x[r]);
                 }
             }
 #pragma unroll
@@ -356,7 +399,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                 if (p.o && t < p.T) {
                     Oct<S> zero;
                     zero.from(v[r]);
-                    put<RING>(p.xn, p.ldxn, t, (gr.t + r * G) * 8, p.d, p.vec_xn, zero);
+                    xs.put(p.xn, p.ldxn, t, out, r, p.vec_xn, zero);
                 }
             }
         }
@@ -384,11 +427,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_block_norm(const NormArgs p
                 Oct<B> h;
                 h.from(v[r]);
                 if (p.h && t < p.T)
-                    put<RING>(p.h, p.ldh, t, c, p.d, p.vec_h, h);
+                    os.put(p.h, p.ldh, t, out, r, p.vec_h, h);
                 if (p.codes) {
                     h.to(v[r]);  // codes of h as it is stored
-                    const uint32_t byte = mx_scale_byte(max_of_block(max_bits8(v[r])));
-                    const uint32_t word = word_of_tile(byte);
+                    const uint32_t byte = mx_scale_byte(max_of_lanes<4>(h.max_bits()));
+                    const uint32_t word = word_of_tile<4>(byte);
                     if (t < p.T && c < p.d)
                         *reinterpret_cast<uint32_t *>(p.codes + t * (p.d / 2) + c / 2) =
                             mx_encode8(v[r], byte);
@@ -417,14 +460,18 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     const Rows<S, R, RING> dxns(p.dxn, p.lddxn, p.d, p.vec_dxn, gr, smem);
     const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
     const Rows<B, R, RING> dhs(p.dh, p.lddh, p.d, p.vec_dh, gr, smem);
+    // (the slots of a tensor that is not there stay zeros)
+    const Rows<S, R, RING> &spare = p.dxn ? dxns : xns;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t step = int64_t(gridDim.x) * gr.count;
     const int64_t first = int64_t(blockIdx.x) * gr.count + gr.id;
-    auto is_live = [&](int64_t t) { return t < p.T && (!p.mask || p.mask[t]); };
+    // nonzero for a row that takes part; as it is loaded, so that nothing waits for
+    // it before it is used (a row later)
+    auto is_live = [&](int64_t t) -> uint32_t { return t >= p.T ? 0u : !p.mask ? 1u : p.mask[t]; };
     int64_t ahead = first;
     int in = 0;
-    auto fetch = [&](bool live) {
+    auto fetch = [&](uint32_t live) {
         if (live) {
             xns.fetch(ahead, in);
             dxns.fetch(ahead, in);
@@ -435,9 +482,9 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
         ahead += step;
         in ^= 1;
     };
-    bool live = is_live(first);
+    uint32_t live = is_live(first);
     fetch(live);
-    bool next = is_live(ahead);
+    uint32_t next = is_live(ahead);
     float gate = p.gate && live ? p.gate[first] : 0.0f;
     Weights<R> pre, post;
     smem = smem_raw + gr.count * p.ring_bytes;
@@ -449,10 +496,12 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     int out = 0;
     for (int64_t t = first; t < p.T; t += step) {
         fetch(next);
-        const bool coming = is_live(ahead);
+        const uint32_t coming = is_live(ahead);
         const float g = gate_of(gate, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
+        if (RING && (sizeof(S) == 4 || sizeof(B) == 4))
+            __syncwarp();  // other lanes' copies
         if (live) {
             Oct<B> o[R], dh[R];
             Oct<S> xn[R], ds[R];  // (ds: dxn as it came)
@@ -485,7 +534,6 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
             float q[1] = {0.0f}, d[R][8];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int c = (gr.t + r * G) * 8;
                 float x[8], h[8], f[8], w[8], v[8];
                 xn[r].to(x);
                 dh[r].to(h);
@@ -502,7 +550,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
                 }
                 Oct<S> dx;
                 dx.from(x);
-                put<RING>(p.dx, p.lddx, t, c, p.d, p.vec_dx, dx);
+                spare.put(p.dx, p.lddx, t, out, r, p.vec_dx, dx);
             }
             if (p.o) {
                 if (p.post_norm || p.dgate)
@@ -512,7 +560,6 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
                 const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q[0] * inv_d)) : 0.0f;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const int c = (gr.t + r * G) * 8;
                     float f[8], v[8];
                     o[r].to(f);
                     post.get(r, v);
@@ -523,7 +570,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
                         f[i] = e * v[i] - c1 * f[i];
                     }
                     o[r].from(f);
-                    put<RING>(p.d_o, p.lddo, t, c, p.d, p.vec_do, o[r]);
+                    os.put(p.d_o, p.lddo, t, out, r, p.vec_do, o[r]);
                 }
             }
         } else {
@@ -534,10 +581,9 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
             zb.from(zero);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int c = (gr.t + r * G) * 8;
-                put<RING>(p.dx, p.lddx, t, c, p.d, p.vec_dx, zs);
+                spare.put(p.dx, p.lddx, t, out, r, p.vec_dx, zs);
                 if (p.o)
-                    put<RING>(p.d_o, p.lddo, t, c, p.d, p.vec_do, zb);
+                    os.put(p.d_o, p.lddo, t, out, r, p.vec_do, zb);
             }
             if (p.dgate && gr.t == 0)
                 p.dgate[t] = 0.0f;

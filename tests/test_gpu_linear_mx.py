@@ -143,10 +143,15 @@ def test_rows_quantised_by_the_call():
     for T in (1, 20, 300):
         for dtype in (BF, F16, F32):
             x = _wide(_rand(2, T, 640), 8, dtype)
-            q = B.Mxfp4Rows.empty(T, 640, "cuda")
-            y = B.linear_mxfp4(x, W, act="silu", x_rows=q)
+            y = B.linear_mxfp4(x, W, act="silu")
             assert y.dtype == dtype
+            q = B.quantize_rows_mxfp4(x)
             assert torch.equal(y, B.linear_mxfp4(q, W, act="silu", out_dtype=dtype))
+            ws = torch.empty(B.linear_rows_mxfp4_workspace_bytes(T, 640), dtype=torch.uint8,
+                             device="cuda")
+            assert torch.equal(y, B.linear_mxfp4(x, W, act="silu", ws=ws))
+            with pytest.raises(B.MoeError):
+                B.linear_mxfp4(x, W, ws=ws[:-1])
 
 
 def test_extreme_scales():
