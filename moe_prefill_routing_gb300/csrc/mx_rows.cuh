@@ -114,6 +114,48 @@ __device__ __forceinline__ uint32_t word_of_tile(uint32_t byte)
     return w | __shfl_xor_sync(0xffffffffu, w, 2 * L);
 }
 
+// ---- two fp32 values that one instruction works on ---------------------------------
+
+using Two = unsigned long long;
+
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+
+__device__ __forceinline__ Two both(float a)
+{
+    return two(a, a);
+}
+
+__device__ __forceinline__ void apart(Two v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ float sum_of(Two v)
+{
+    float a, b;
+    apart(v, a, b);
+    return a + b;
+}
+
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    Two v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+
 // ---- eight neighbouring elements of a row ----------------------------------------
 
 // As they are stored, in 32-bit words (two 16-bit elements a word).
@@ -211,6 +253,24 @@ struct alignas(16) Oct {
                 }
             }
         }
+    }
+
+    __device__ __forceinline__ void to(Two (&v)[4]) const
+    {
+        float f[8];
+        to(f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = two(f[2 * i], f[2 * i + 1]);
+    }
+
+    __device__ __forceinline__ void from(const Two (&v)[4])
+    {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            apart(v[i], f[2 * i], f[2 * i + 1]);
+        from(f);
     }
 
     __device__ __forceinline__ void from(const float (&v)[8])

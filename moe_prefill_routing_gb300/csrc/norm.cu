@@ -4,7 +4,7 @@
 // Per row, with r(v) = (mean(v^2) + eps)^-1/2:
 //   xn = alpha x + g r(o) (o . post),   h = xn r(xn) . pre
 // and from dxn and dh, with a = dh . pre, r1 = r(o), r2 = r(xn):
-//   dS = dxn + r2 a - r2^3 mean(a . xn) xn
+//   dS = dxn + r2 a - c2 xn,   c2 = r2^3 mean(a . xn)
 //   dx = alpha dS,   q = sum(dS . post . o),   dg = r1 q
 //   do = g r1 dS . post - r1^2 (g r1 q / d) o
 //   dpost = sum over rows of g r1 dS . o,   dpre = sum over rows of r2 dh . xn
@@ -80,45 +80,72 @@ struct Group {
     }
 };
 
-// Sums of N <= 3 values over a group, in every thread; one barrier, two sets of
-// words in turn.
+// Sums over a group, in every thread; one barrier, two sets of words in turn.
 struct GroupSum {
     const Group &gr;
-    float4 *red;  // the group's [2][warps]
+    float *red;  // the group's [2][warps][8]
     int turn;
 
-    template <int N>
-    __device__ __forceinline__ void operator()(float (&v)[N])
+    __device__ __forceinline__ float *words()
+    {
+        turn ^= 1;
+        return red + (turn ? 8 * gr.warps : 0);
+    }
+
+    __device__ __forceinline__ float one(float v)
     {
 #pragma unroll
         for (int o = 16; o; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            v += __shfl_xor_sync(0xffffffffu, v, o);
         if (gr.warps == 1)
-            return;
+            return v;
         const int lane = int(threadIdx.x) & 31;
-        float4 *const words = red + (turn ? gr.warps : 0);
+        float *const w = words();
         if (lane == 0)
-            words[gr.t >> 5] = make_float4(v[0], N > 1 ? v[N > 1] : 0.0f,
-                                           N > 2 ? v[N > 2 ? 2 : 0] : 0.0f, 0.0f);
+            w[gr.t >> 5] = v;
         gr.sync();
         // every warp adds the warps' sums (16 at most) across its lanes
-        const float4 s = lane < gr.warps ? words[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        v[0] = s.x;
-        if (N > 1)
-            v[N > 1] = s.y;
-        if (N > 2)
-            v[N > 2 ? 2 : 0] = s.z;
+        v = lane < gr.warps ? w[lane] : 0.0f;
 #pragma unroll
         for (int o = 8; o; o >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+        return __shfl_sync(0xffffffffu, v, 0);
+    }
+
+    // Eight values, of which the first N are wanted: lanes pass on the half of the
+    // values that they do not keep, so that four lanes have one each in the end.
+    template <int N>
+    __device__ __forceinline__ void eight(float (&v)[8])
+    {
+        const int lane = int(threadIdx.x) & 31;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int n = 4; n; n >>= 1) {
+            const bool upper = lane & (4 * n);
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = upper ? v[i + n] : v[i], pass = upper ? v[i] : v[i + n];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, pass, 4 * n);
+            }
+        }
+        float s = v[0];  // of value lane / 4
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        if (gr.warps > 1) {
+            float *const w = words();
+            if ((lane & 3) == 0)
+                w[(gr.t >> 5) * 8 + (lane >> 2)] = s;
+            gr.sync();
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kNormMaxThreads / 32; i += 4)
+                if (i + (lane & 3) < gr.warps)
+                    s += w[(i + (lane & 3)) * 8 + (lane >> 2)];
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            v[i] = __shfl_sync(0xffffffffu, v[i], 0);
-        turn ^= 1;
+            v[i] = __shfl_sync(0xffffffffu, s, 4 * i);
     }
 };
 
@@ -237,12 +264,38 @@ struct Rows {
     }
 };
 
+// A thread's part of a row that is looked at more than once: read from a ring's
+// slot each time (registers are what limits the rows that an SM works on), kept
+// in registers without one.
+template <typename E, int R, bool RING>
+struct Part {
+    const Rows<E, R, RING> &rows;
+    Oct<E> kept[RING ? 1 : R];
+
+    __device__ __forceinline__ Part(const Rows<E, R, RING> &rows_, int64_t row) : rows(rows_)
+    {
+        if (!RING) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                kept[RING ? 0 : r] = rows.read(row, 0, r);
+        }
+    }
+
+    __device__ __forceinline__ void get(int stage, int r, Two (&v)[4]) const
+    {
+        if (RING)
+            rows.read(0, stage, r).to(v);
+        else
+            kept[RING ? 0 : r].to(v);
+    }
+};
+
 // Weights of a row (1 where there are none, 0 past its end): in registers where
 // a thread has eight, in shared memory (of the whole CTA) where it has more.
 template <int R>
 struct Weights {
-    float w[R == 1 ? 8 : 1];
-    const float4 *slots;
+    Two w[R == 1 ? 4 : 1];
+    const ulonglong2 *slots;
     int G;
 
     // (to be used after a barrier of the CTA)
@@ -250,7 +303,7 @@ struct Weights {
     {
         G = gr.size;
         float4 *mine = reinterpret_cast<float4 *>(smem) + gr.t;
-        slots = mine;
+        slots = reinterpret_cast<const ulonglong2 *>(mine);
         if (R > 1)
             smem += R * 2 * G * 16;
 #pragma unroll
@@ -264,8 +317,8 @@ struct Weights {
             }
             if (R == 1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[R == 1 ? i : 0] = v[i];
+                for (int i = 0; i < 4; ++i)
+                    w[R == 1 ? i : 0] = two(v[2 * i], v[2 * i + 1]);
             } else if (gr.id == 0) {
                 mine[(2 * r) * G] = make_float4(v[0], v[1], v[2], v[3]);
                 mine[(2 * r + 1) * G] = make_float4(v[4], v[5], v[6], v[7]);
@@ -273,16 +326,15 @@ struct Weights {
         }
     }
 
-    __device__ __forceinline__ void get(int r, float (&v)[8]) const
+    __device__ __forceinline__ void get(int r, Two (&v)[4]) const
     {
         if (R == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
                 v[i] = w[R == 1 ? i : 0];
         } else {
-            const float4 a = slots[(2 * r) * G], b = slots[(2 * r + 1) * G];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            const ulonglong2 a = slots[(2 * r) * G], b = slots[(2 * r + 1) * G];
+            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
         }
     }
 };
@@ -303,9 +355,9 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
     k_block_norm(const NormArgs p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ float4 red[2 * kNormMaxThreads / 32];
+    __shared__ float red[2 * 8 * kNormMaxThreads / 32];
     const Group gr(p.warps);
-    GroupSum sum{gr, red + 2 * gr.id * gr.warps, 0};
+    GroupSum sum{gr, red + 2 * 8 * gr.id * gr.warps, 0};
     const int G = gr.size;
     const float inv_d = 1.0f / float(p.d);
     uint8_t *smem = smem_raw + gr.id * p.ring_bytes;  // a ring for each group, then the weights
@@ -313,7 +365,9 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
     const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T, step = int64_t(gridDim.x) * gr.count, first = int64_t(blockIdx.x) * gr.count + gr.id;
+    const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T;
+    const int64_t step = int64_t(gridDim.x) * gr.count;
+    const int64_t first = int64_t(blockIdx.x) * gr.count + gr.id;
     // nonzero for a row that takes part; as it is loaded, so that nothing waits for
     // it before it is used (a row later)
     auto is_live = [&](int64_t t) -> uint32_t { return t >= p.T ? 0u : !p.mask ? 1u : p.mask[t]; };
@@ -348,54 +402,49 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
         async_wait();
         if (RING && (sizeof(S) == 4 || sizeof(B) == 4))
             __syncwarp();  // other lanes' copies
-        float v[R][8];
+        Two v[R][4];
         if (live) {
-            Oct<S> x[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r] = xs.read(t, out, r);
+            const Part<S, R, RING> x(xs, t);
             if (p.o) {
-                Oct<B> o[R];
+                const Part<B, R, RING> o(os, t);
                 float k = g;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    o[r] = os.read(t, out, r);
                 if (p.post_norm) {
-                    float s[1] = {0.0f};
+                    Two squares = 0;
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        float f[8];
-                        o[r].to(f);
+                        Two f[4];
+                        o.get(out, r, f);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            s[0] += f[i] * f[i];
+                        for (int i = 0; i < 4; ++i)
+                            squares = fma(f[i], f[i], squares);
                     }
-                    s[0] *= inv_d;
-                    sum(s);
-                    k *= rsqrtf(s[0] + p.eps);
+                    k *= rsqrtf(sum.one(sum_of(squares) * inv_d) + p.eps);
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float f[8], w[8];
-                    o[r].to(f);
-                    x[r].to(v[r]);
+                    Two f[4], w[4];
+                    o.get(out, r, f);
+                    x.get(out, r, v[r]);
                     post.get(r, w);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[r][i] = p.alpha * v[r][i] + f[i] * (k * w[i]);
-                    x[r].from(v[r]);
-                    xs.put(p.xn, p.ldxn, t, out, r, p.vec_xn, x[r]);
+                    for (int i = 0; i < 4; ++i)
+                        v[r][i] = fma(both(p.alpha), v[r][i], mul(f[i], mul(both(k), w[i])));
+                    Oct<S> xn;
+                    xn.from(v[r]);
+                    xs.put(p.xn, p.ldxn, t, out, r, p.vec_xn, xn);
+                    xn.to(v[r]);  // the stream as it is stored
                 }
-            }
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                x[r].to(v[r]);  // the stream as it is stored
+                for (int r = 0; r < R; ++r)
+                    x.get(out, r, v[r]);
+            }
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[r][i] = 0.0f;
+                for (int i = 0; i < 4; ++i)
+                    v[r][i] = 0;
                 if (p.o && t < p.T) {
                     Oct<S> zero;
                     zero.from(v[r]);
@@ -404,37 +453,38 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
             }
         }
         if (p.pre) {
-            float k = 0.0f;
             if (live) {
-                float s[1] = {0.0f};
+                Two squares = 0;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        s[0] += v[r][i] * v[r][i];
-                s[0] *= inv_d;
-                sum(s);
-                k = rsqrtf(s[0] + p.eps);
+                    for (int i = 0; i < 4; ++i)
+                        squares = fma(v[r][i], v[r][i], squares);
+                const float k = rsqrtf(sum.one(sum_of(squares) * inv_d) + p.eps);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    Two w[4];
+                    pre.get(r, w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[r][i] = mul(mul(v[r][i], both(k)), w[i]);
+                }
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int c = (gr.t + r * G) * 8;
-                float w[8];
-                pre.get(r, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[r][i] = live ? v[r][i] * k * w[i] : 0.0f;
                 Oct<B> h;
                 h.from(v[r]);
                 if (p.h && t < p.T)
                     os.put(p.h, p.ldh, t, out, r, p.vec_h, h);
                 if (p.codes) {
-                    h.to(v[r]);  // codes of h as it is stored
+                    float f[8];
+                    h.to(f);  // codes of h as it is stored
                     const uint32_t byte = mx_scale_byte(max_of_lanes<4>(h.max_bits()));
                     const uint32_t word = word_of_tile<4>(byte);
                     if (t < p.T && c < p.d)
                         *reinterpret_cast<uint32_t *>(p.codes + t * (p.d / 2) + c / 2) =
-                            mx_encode8(v[r], byte);
+                            mx_encode8(f, byte);
                     if ((gr.t & 15) == 0 && c < p.k_tiles * 128)
                         *mx_scale_word(p.scales, t, c / 128, p.k_tiles) = word;
                 }
@@ -450,9 +500,9 @@ template <typename S, typename B, int R, bool RING>
 __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradArgs p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ float4 red[2 * kNormMaxThreads / 32];
+    __shared__ float red[2 * 8 * kNormMaxThreads / 32];
     const Group gr(p.warps);
-    GroupSum sum{gr, red + 2 * gr.id * gr.warps, 0};
+    GroupSum sum{gr, red + 2 * 8 * gr.id * gr.warps, 0};
     const int G = gr.size;
     const float inv_d = 1.0f / float(p.d);
     uint8_t *smem = smem_raw + gr.id * p.ring_bytes;  // a ring for each group, then the weights
@@ -492,7 +542,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     post.load(p.post, p.d, gr, smem);
     if (R > 1)
         __syncthreads();
-    float dpre[R][8] = {}, dpost[R][8] = {};
+    Two dpre[R][4] = {}, dpost[R][4] = {};
     int out = 0;
     for (int64_t t = first; t < p.T; t += step) {
         fetch(next);
@@ -503,74 +553,65 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
         if (RING && (sizeof(S) == 4 || sizeof(B) == 4))
             __syncwarp();  // other lanes' copies
         if (live) {
-            Oct<B> o[R], dh[R];
-            Oct<S> xn[R], ds[R];  // (ds: dxn as it came)
-            float s[3] = {};      // xn^2, a xn, o^2
+            const Part<S, R, RING> xn(xns, t), dxn(dxns, t);
+            const Part<B, R, RING> dh(dhs, t), o(os, t);
+            // of the means and of q, whose dS is made of three terms, all at once
+            Two xx = 0, ax = 0, oo = 0, dq = 0, aq = 0, xq = 0;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float x[8], h[8], f[8], w[8];
-                xn[r] = xns.read(t, out, r);
-                dh[r] = dhs.read(t, out, r);
-                o[r] = os.read(t, out, r);
-                ds[r] = dxns.read(t, out, r);
-                xn[r].to(x);
-                dh[r].to(h);
-                o[r].to(f);
-                pre.get(r, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[0] += x[i] * x[i];
-                    s[1] += h[i] * w[i] * x[i];
-                    s[2] += f[i] * f[i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                s[i] *= inv_d;
-            sum(s);
-            const float r2 = p.dh ? rsqrtf(s[0] + p.eps) : 0.0f;
-            const float r1 = p.post_norm ? rsqrtf(s[2] + p.eps) : 1.0f;
-            const float c2 = r2 * r2 * r2 * s[1];
-            float q[1] = {0.0f}, d[R][8];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float x[8], h[8], f[8], w[8], v[8];
-                xn[r].to(x);
-                dh[r].to(h);
-                o[r].to(f);
-                ds[r].to(d[r]);
+                Two x[4], h[4], f[4], d[4], w[4], v[4];
+                xn.get(out, r, x);
+                dh.get(out, r, h);
+                o.get(out, r, f);
+                dxn.get(out, r, d);
                 pre.get(r, w);
                 post.get(r, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dpre[r][i] += h[i] * (x[i] * r2);
-                    d[r][i] += r2 * (h[i] * w[i]) - c2 * x[i];
-                    q[0] += d[r][i] * (v[i] * f[i]);
-                    x[i] = p.alpha * d[r][i];
+                for (int i = 0; i < 4; ++i) {
+                    const Two a = mul(h[i], w[i]), u = mul(v[i], f[i]);
+                    xx = fma(x[i], x[i], xx);
+                    ax = fma(a, x[i], ax);
+                    oo = fma(f[i], f[i], oo);
+                    dq = fma(d[i], u, dq);
+                    aq = fma(a, u, aq);
+                    xq = fma(x[i], u, xq);
+                }
+            }
+            float s[8] = {sum_of(xx) * inv_d, sum_of(ax) * inv_d, sum_of(oo) * inv_d,
+                          sum_of(dq), sum_of(aq), sum_of(xq)};
+            sum.eight<6>(s);
+            const float r2 = p.dh ? rsqrtf(s[0] + p.eps) : 0.0f;
+            const float r1 = p.post_norm ? rsqrtf(s[2] + p.eps) : 1.0f;
+            const float c2 = r2 * r2 * r2 * s[1];
+            const float q = s[3] + r2 * s[4] - c2 * s[5];
+            if (p.dgate && gr.t == 0)
+                p.dgate[t] = r1 * q * (p.sigmoid ? g * (1.0f - g) : 1.0f);
+            const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q * inv_d)) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                Two x[4], h[4], f[4], d[4], w[4], v[4];
+                xn.get(out, r, x);
+                dh.get(out, r, h);
+                o.get(out, r, f);
+                dxn.get(out, r, d);
+                pre.get(r, w);
+                post.get(r, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dpre[r][i] = fma(h[i], mul(x[i], both(r2)), dpre[r][i]);
+                    d[i] = fma(both(r2), mul(h[i], w[i]), fma(both(-c2), x[i], d[i]));
+                    const Two e = mul(both(k), d[i]);
+                    dpost[r][i] = fma(e, f[i], dpost[r][i]);
+                    f[i] = fma(e, v[i], mul(both(-c1), f[i]));
+                    d[i] = mul(both(p.alpha), d[i]);
                 }
                 Oct<S> dx;
-                dx.from(x);
+                dx.from(d);
                 spare.put(p.dx, p.lddx, t, out, r, p.vec_dx, dx);
-            }
-            if (p.o) {
-                if (p.post_norm || p.dgate)
-                    sum(q);
-                if (p.dgate && gr.t == 0)
-                    p.dgate[t] = r1 * q[0] * (p.sigmoid ? g * (1.0f - g) : 1.0f);
-                const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q[0] * inv_d)) : 0.0f;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float f[8], v[8];
-                    o[r].to(f);
-                    post.get(r, v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float e = k * d[r][i];
-                        dpost[r][i] += e * f[i];
-                        f[i] = e * v[i] - c1 * f[i];
-                    }
-                    o[r].from(f);
-                    os.put(p.d_o, p.lddo, t, out, r, p.vec_do, o[r]);
+                if (p.o) {
+                    Oct<B> d_o;
+                    d_o.from(f);
+                    os.put(p.d_o, p.lddo, t, out, r, p.vec_do, d_o);
                 }
             }
         } else {
@@ -595,17 +636,24 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     if (!p.part)
         return;
     float *part = p.part + int64_t(blockIdx.x) * 2 * p.d;
+    const auto each = [&](auto f) {  // f(which, r, i, value)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float a, b;
+                apart(dpre[r][i / 2], a, b);
+                f(0, r, i, a), f(0, r, i + 1, b);
+                apart(dpost[r][i / 2], a, b);
+                f(1, r, i, a), f(1, r, i + 1, b);
+            }
+    };
     if (gr.count == 1) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int c = (gr.t + r * G) * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < p.d) {
-                    part[c + i] = dpre[r][i];
-                    part[p.d + c + i] = dpost[r][i];
-                }
-        }
+        each([&](int which, int r, int i, float v) {
+            const int c = (gr.t + r * G) * 8 + i;
+            if (c < p.d)
+                part[which * p.d + c] = v;
+        });
         return;
     }
     // the groups' sums, in order, through the rings' memory (of 2 R 8 G floats a
@@ -614,13 +662,9 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     const int words = 2 * R * 8 * G;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            all[gr.id * words + (r * 8 + i) * G + gr.t] = dpre[r][i];
-            all[gr.id * words + ((R + r) * 8 + i) * G + gr.t] = dpost[r][i];
-        }
+    each([&](int which, int r, int i, float v) {
+        all[gr.id * words + ((which * R + r) * 8 + i) * G + gr.t] = v;
+    });
     __syncthreads();
     for (int j = int(threadIdx.x); j < words; j += int(blockDim.x)) {
         float v = 0.0f;
