@@ -31,7 +31,7 @@ constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxD = kNormMaxThreads * 8 * 4;
 constexpr int kNormStages = 2;      // rows of a ring: one in use, one on its way
 constexpr int kNormGradCtas = 608;  // at most: rows of partial column sums
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 1024;
 
 struct NormArgs {
     const void *x, *o;
@@ -649,11 +649,26 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
             }
     };
     if (gr.count == 1) {
-        each([&](int which, int r, int i, float v) {
-            const int c = (gr.t + r * G) * 8 + i;
-            if (c < p.d)
-                part[which * p.d + c] = v;
-        });
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int c = (gr.t + r * G) * 8;
+            if (p.d % 8 == 0) {
+                if (c < p.d) {
+                    ulonglong2 *a = reinterpret_cast<ulonglong2 *>(part + c);
+                    ulonglong2 *b = reinterpret_cast<ulonglong2 *>(part + p.d + c);
+                    a[0] = make_ulonglong2(dpre[r][0], dpre[r][1]);
+                    a[1] = make_ulonglong2(dpre[r][2], dpre[r][3]);
+                    b[0] = make_ulonglong2(dpost[r][0], dpost[r][1]);
+                    b[1] = make_ulonglong2(dpost[r][2], dpost[r][3]);
+                }
+            }
+        }
+        if (p.d % 8 != 0)
+            each([&](int which, int r, int i, float v) {
+                const int c = (gr.t + r * G) * 8 + i;
+                if (c < p.d)
+                    part[which * p.d + c] = v;
+            });
         return;
     }
     // the groups' sums, in order, through the rings' memory (of 2 R 8 G floats a
@@ -677,34 +692,39 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     }
 }
 
-// The CTAs' column sums: a CTA takes 32 columns of the 2 d, its warps every
-// eighth row, added in order.
+// The CTAs' column sums: a CTA takes 32 columns of the 2 d, its 32 warps every
+// 32nd row (all of a warp's 19 rows at most are on their way at once; with eight
+// warps the rows' latencies added up: 2048 x 2560 25.6 us), added in order.
 __global__ void __launch_bounds__(kSumThreads)
     k_norm_col_sum(const float *part, int rows, int d, float *dpre, float *dpost)
 {
     constexpr int kWarps = kSumThreads / 32;
-    __shared__ float red[kWarps][32];
+    __shared__ float red[kWarps][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     pdl_wait();
     pdl_launch_dependents();
     float v = 0.0f;
     if (c < 2 * d) {
-#pragma unroll 8
-        for (int i = g; i < rows; i += kWarps)
-            v += part[int64_t(i) * 2 * d + c];
+#pragma unroll
+        for (int i = 0; i < (kNormGradCtas + kWarps - 1) / kWarps; ++i)
+            if (g + i * kWarps < rows)
+                v += part[int64_t(g + i * kWarps) * 2 * d + c];
     }
     red[g][lane] = v;
     __syncthreads();
-    if (g == 0 && c < 2 * d) {
+    // warp g adds column g across its lanes
+    v = red[lane][g];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i)
-            v += red[i][lane];
-        if (c < d) {
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int column = blockIdx.x * 32 + g;
+    if (lane == 0 && column < 2 * d) {
+        if (column < d) {
             if (dpre)
-                dpre[c] = v;
+                dpre[column] = v;
         } else if (dpost) {
-            dpost[c - d] = v;
+            dpost[column - d] = v;
         }
     }
 }
