@@ -1,11 +1,13 @@
-"""A whole mixture-of-experts block on the library: router, routed experts, a
-dense expert beside them and the residual; and a training step of the router.
+"""A whole mixture-of-experts block on the library: norms, router, routed
+experts, a dense expert beside them and the residual; and a training step of the
+router.
 
     python -m moe_prefill_routing_gb300.block      # needs a GB300
 
 ``MoeBlock.forward`` is what a model runs per layer (a prefill chunk or a few
-decoded tokens); ``MoeBlock.train_router`` takes one gradient step that
-balances the experts, the experts' weights fixed.
+decoded tokens), ``run_blocks`` several layers, the norms between two of them in
+one pass; ``MoeBlock.train_router`` takes one gradient step that balances the
+experts, the experts' weights fixed.
 """
 from __future__ import annotations
 
@@ -15,17 +17,29 @@ from . import binding as B
 
 
 class MoeBlock:
-    """out = x + experts(x) + down(gelu(up(x))), the experts chosen by a router.
+    """out = x + f(x), f(h) = experts(h) + down(gelu(up(h))), the experts chosen by
+    a router; or, with norms,
+
+        out = alpha x + sigmoid(gate . h) * norm(f(h)) . post,   h = norm(x) . pre
 
     Wr [E, d] are the router's weights and ``layer`` a binding.MoeLayer over
-    the E experts; ``up`` [h, d] and ``down`` [d, h] the dense expert, or None.
-    ``score``, ``norm``, ``scale`` and the per-expert selection ``bias`` are
-    moe_route's."""
+    the E experts; ``up`` [h, d] and ``down`` [d, h] the dense expert, or None:
+    bfloat16, or both in MXFP4 (binding.quantize_rows_mxfp4), whose rows then are
+    too.  ``pre`` and ``post`` are fp32 [d] weights of the norms (binding.block_norm;
+    post None: f is not normalised), ``gate`` bfloat16 [1, d] or None (no gate);
+    post, gate and an ``alpha`` of not 1 come with ``pre``.  ``score``, ``norm``,
+    ``scale`` and the per-expert selection ``bias`` are moe_route's."""
 
     def __init__(self, layer: B.MoeLayer, Wr, k: int, up=None, down=None, bias=None,
-                 score: str = "softmax", norm: bool = True, scale: float = 1.0):
+                 score: str = "softmax", norm: bool = True, scale: float = 1.0, pre=None,
+                 post=None, gate=None, alpha: float = 1.0, eps: float = 1e-6):
+        if pre is None and (post is not None or gate is not None or alpha != 1.0):
+            raise ValueError("post, gate and alpha come with pre")
+        if isinstance(up, B.Mxfp4Rows) != isinstance(down, B.Mxfp4Rows):
+            raise ValueError("the dense expert is in MXFP4 as a whole or not at all")
         self.layer, self.Wr, self.k = layer, Wr, k
         self.up, self.down, self.bias = up, down, bias
+        self.pre, self.post, self.gate, self.alpha, self.eps = pre, post, gate, alpha, eps
         self.how = dict(score=score, norm=norm, scale=scale)
         self._master = None
 
@@ -45,18 +59,46 @@ class MoeBlock:
             bits |= B.read_status(self.layer._ws)
         return bits
 
+    def _dense(self, h, rows, y):
+        """y + down(gelu(up(h))), into y; ``rows``: h, or its MXFP4 rows."""
+        if isinstance(self.up, B.Mxfp4Rows):
+            hid = B.linear_mxfp4(rows, self.up, act="gelu_tanh")
+            return B.linear_mxfp4(hid, self.down, residual=y, y=y)
+        return B.linear(B.linear(h, self.up, act="gelu_tanh"), self.down, residual=y, y=y)
+
+    def _before(self) -> dict:
+        """What block_norm takes of the norm before this block."""
+        return dict(pre=self.pre, eps=self.eps, mxfp4=isinstance(self.up, B.Mxfp4Rows))
+
+    def _inside(self, n: dict, mask):
+        """f(h) and the tokens' gates, of what block_norm returned."""
+        h = n["h"]
+        r = self.route(h, mask)
+        y = self.layer.forward(h, r["ids"], r["w"])
+        if self.up is not None:
+            y = self._dense(h, n.get("mx", h), y)
+        if self.gate is None:
+            return y, None
+        return y, B.linear(h, self.gate, out_dtype=torch.float32).view(-1)
+
+    def _after(self, o, g) -> dict:
+        """What block_norm takes of the norm, gate and residual after this block."""
+        return dict(o=o, post=self.post, post_norm=self.post is not None, gate=g,
+                    gate_act="sigmoid", alpha=self.alpha, eps=self.eps)
+
     def forward(self, x, mask=None):
-        """x [T, d] bf16 to [T, d]; rows with mask 0 are routed nowhere."""
+        """x [T, d] to [T, d], bf16 (with norms, or float32); rows with mask 0 are
+        routed nowhere (with norms they are not read, and come out as 0)."""
+        if self.pre is not None:
+            return run_blocks([self], x, mask)
         if x.dtype != torch.bfloat16:
             raise ValueError(f"x: the routed experts take bfloat16, got {x.dtype}")
         r = self.route(x, mask)
         y = self.layer.forward(x, r["ids"], r["w"])
         # the residual stream rides on the dense expert's down projection, or
         # is added to the experts' sum as it is
-        if self.up is None:
-            return y.add_(x)
-        h = B.linear(x, self.up, act="gelu_tanh")
-        return B.linear(h, self.down, residual=y.add_(x), y=y)
+        y.add_(x)
+        return y if self.up is None else self._dense(x, x, y)
 
     def train_router(self, x, lr: float, balance: float = 1e-2, z: float = 1e-3, dw=None,
                      mask=None, grad_scale: float = 1.0):
@@ -66,10 +108,16 @@ class MoeBlock:
         the step and the gradient with respect to x, times ``grad_scale`` (what
         a 16-bit dx cannot hold otherwise; dx is 0 where mask is).
 
+        With norms x is the residual stream, and dx goes through the norm before
+        the router (whose weights stay as they are).
+
         Wr holds the 16-bit values of weights kept in fp32, so that steps
         smaller than its spacing add up; entries of Wr that were set since the
         last step start from what they were set to."""
-        if mask is not None:
+        stream = x
+        if self.pre is not None:
+            x = B.block_norm(x, pre=self.pre, mask=mask, eps=self.eps, h_dtype=self.Wr.dtype)["h"]
+        elif mask is not None:
             # such a row may hold anything, and 0 times a NaN is one
             x = torch.where(mask.bool()[:, None], x, 0.0)
         r = self.route(x, mask, stats=True)
@@ -90,7 +138,30 @@ class MoeBlock:
         w.sub_(dWr, alpha=lr / grad_scale)
         W.copy_(w)
         self._master = w
+        if self.pre is not None:
+            dx = B.block_norm_grad(stream, dh=dx, pre=self.pre, mask=mask, eps=self.eps,
+                                   weights=False)["dx"]
         return r["loss"], dx
+
+
+def run_blocks(blocks, x, mask=None):
+    """x [T, d] through blocks with norms, one after another: the norm after a
+    block, its gate, the residual and the norm before the next block are one pass.
+    x is bfloat16 or float32 and is left as it is; mask as in MoeBlock.forward."""
+    blocks = list(blocks)
+    if any(b.pre is None for b in blocks) or len({b.eps for b in blocks}) > 1:
+        raise ValueError("blocks: all with norms, and of one eps")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x: bfloat16 or float32, got {x.dtype}")
+    n = own = None  # own: the stream's buffer once it is not the caller's
+    for b in blocks:
+        if n is None:
+            n = B.block_norm(x, mask=mask, h_dtype=torch.bfloat16, **b._before())
+        else:
+            n = B.block_norm(x, mask=mask, xn=own, **{**last, **b._before()})
+            x = own = n["xn"]
+        last = b._after(*b._inside(n, mask))
+    return x if n is None else B.block_norm(x, mask=mask, xn=own, **last)["xn"]
 
 
 def main():
@@ -114,6 +185,11 @@ def main():
             counts = block.route(x, stats=True)["counts"][:E]
             print(f"step {step:2d}: balance loss {float(loss[0]):.4f}  z loss {float(loss[1]):.3f}"
                   f"  tokens of the busiest expert {int(counts.max())} (mean {T * k // E})")
+    # three blocks in a row: norms, a gate, the dense expert in MXFP4
+    norm = torch.rand(d, device=dev) + 0.5
+    dense = dict(up=B.quantize_rows_mxfp4(block.up), down=B.quantize_rows_mxfp4(block.down))
+    normed = MoeBlock(layer, Wr, k, **dense, pre=norm, post=norm, gate=randn(1, d, amp=0.1))
+    print("three blocks with norms", tuple(run_blocks([normed] * 3, x).shape))
     print("status bits", block.status())
 
 
