@@ -759,7 +759,9 @@ MOE_API int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scale
  * in   status    as in moe_linear
  * moe_linear_rows_mxfp4 -- the same for rows x dtype [T, K] (any MOE_DT_*, rows ldx
  * elements apart, as in moe_quantize_rows_mxfp4), which it quantises first, into
- * ws: moe_linear_rows_mxfp4_workspace_bytes(T, K) bytes, 256-byte aligned.
+ * ws: moe_linear_rows_mxfp4_workspace_bytes(T, K, N) bytes, 256-byte aligned.
+ * That is 0 on the current device for a few rows that the product's kernel
+ * quantises itself (to the same codes); ws may be NULL then.
  * A row (or weight) with a NaN block makes its outputs NaN.  T >= 0, N >= 1, K a
  * positive multiple of 32; T, K, N <= 2^31 - 512; ldr, ldy >= N.  codes and scales
  * 16-byte aligned, the others to their element.  Deterministic.
@@ -768,7 +770,7 @@ MOE_API int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const ui
                              const uint8_t *W_scales, const float *bias, const void *residual,
                              int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy,
                              int y_dtype, uint32_t *status, moe_stream_t stream);
-MOE_API size_t moe_linear_rows_mxfp4_workspace_bytes(int T, int K);
+MOE_API size_t moe_linear_rows_mxfp4_workspace_bytes(int T, int K, int N);
 MOE_API int moe_linear_rows_mxfp4(const void *x, int64_t ldx, int x_dtype, const uint8_t *W,
                                   const uint8_t *W_scales, const float *bias,
                                   const void *residual, int64_t ldr, int act, int T, int K, int N,

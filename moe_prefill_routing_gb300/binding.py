@@ -147,7 +147,7 @@ _SIGS = {
     "moe_linear_mxfp4": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int,
                                    C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p]),
-    "moe_linear_rows_mxfp4_workspace_bytes": (C.c_size_t, [C.c_int] * 2),
+    "moe_linear_rows_mxfp4_workspace_bytes": (C.c_size_t, [C.c_int] * 3),
     "moe_linear_rows_mxfp4": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p,
                                         C.c_void_p, C.c_void_p, C.c_int64, C.c_int, C.c_int,
                                         C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int,
@@ -998,9 +998,9 @@ def dequantize_rows_mxfp4(q: Mxfp4Rows, dtype=torch.bfloat16, y=None):
 
 
 @functools.lru_cache(maxsize=1024)
-def linear_rows_mxfp4_workspace_bytes(T: int, K: int) -> int:
-    """Of ``linear_mxfp4`` for rows that it quantises."""
-    return int((_lib or lib()).moe_linear_rows_mxfp4_workspace_bytes(T, K))
+def linear_rows_mxfp4_workspace_bytes(T: int, K: int, N: int) -> int:
+    """Of ``linear_mxfp4`` for rows that it quantises: 0 for a few of them."""
+    return int((_lib or lib()).moe_linear_rows_mxfp4_workspace_bytes(T, K, N))
 
 
 def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", out_dtype=None,
@@ -1048,11 +1048,14 @@ def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", o
                                               y.data_ptr(), ldy, _DTYPES[y.dtype], stp,
                                               _raw_stream(dev.index))
     else:
-        if ws is None:
-            ws = torch.empty(linear_rows_mxfp4_workspace_bytes(T, K), dtype=torch.uint8, device=dev)
-            qp, ws_bytes = ws.data_ptr(), ws.numel()
-        else:
+        qp, ws_bytes = None, 0
+        if ws is not None:
             qp, ws_bytes = _ws(ws, dev)
+        else:
+            ws_bytes = linear_rows_mxfp4_workspace_bytes(T, K, N)
+            if ws_bytes:
+                ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+                qp = ws.data_ptr()
         rc = (_lib or lib()).moe_linear_rows_mxfp4(x.data_ptr(), ldx, _DTYPES[x.dtype], wp, wsp, bp,
                                                    rp, ldr, code, T, K, N, y.data_ptr(), ldy,
                                                    _DTYPES[y.dtype], qp, ws_bytes, stp,

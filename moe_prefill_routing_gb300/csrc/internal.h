@@ -180,7 +180,8 @@ enum SmemSlot {
     kSlotLinearExtra,
     kSlotLinearPair,  // + 1 for wide tiles, + 2 with EXTRA
     kSlotLinearPairEnd = kSlotLinearPair + 3,
-    kSlotLinearMx,
+    kSlotLinearMx,  // + 1 for rows that the kernel quantises
+    kSlotLinearMxEnd = kSlotLinearMx + 1,
     kSlotLinearMxPair,  // + 3 per activation, + 1 for fp16, + 2 for fp32
     kSlotLinearMxPairEnd = kSlotLinearMxPair + 14,
     kSlotCount

@@ -25,6 +25,8 @@ constexpr uint32_t kMxATile = MM * MK / 2;  // 16 KB
 constexpr uint32_t kMxScales = 2 * kMxTileBytes;  // of 128 rows per stage
 constexpr int kMxMaxStages = 8;
 constexpr int kMxMaxSplit = 8;  // portable cluster size
+// Rows that the kernel quantises itself: at most so many, of so many stages a CTA.
+constexpr int kMxQuantRows = 16, kMxQuantStages = 8;
 constexpr int kMxScaleCols = 16;  // of tensor memory: two tiles of A's and two of B's scales
 
 // Stages of 256 of K, four MMAs each, that one accumulator sums; sums of more
@@ -43,6 +45,11 @@ struct MxArgs : EpiArgs {
     int M, N, K, k_tiles;
     int bn, stages, split, n_mt;
     int chain;
+    // QUANT kernels: x as it is, its type (MOE_DT_*) and whether 16-byte accesses
+    // are aligned
+    const void *rows;
+    int64_t ld;
+    int type, vec;
 };
 
 // Status bits of calls without a status word, see moe_take_status.
@@ -59,6 +66,7 @@ struct MxCtrl {
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint64_t done;
+    uint64_t rows_full[kMxQuantStages];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -67,9 +75,42 @@ struct MxMaps {
     CUtensorMap a, b;
 };
 
-__host__ __device__ __forceinline__ uint32_t mx_stage_bytes(int bn)
+__host__ __device__ __forceinline__ uint32_t mx_stage_bytes(int bn, bool quant)
 {
-    return kMxATile + uint32_t(bn) * (MK / 2) + 2 * kMxScales;
+    return kMxATile + kMxScales + (quant ? 0 : uint32_t(bn) * (MK / 2) + kMxScales);
+}
+
+// What a CTA of a QUANT kernel holds of x: codes and scales of its stages.
+__host__ __device__ __forceinline__ uint32_t mx_rows_bytes(int stages)
+{
+    return uint32_t(stages) * (kMxQuantRows * (MK / 2) + kMxScales);
+}
+
+// A block of 32 elements of row t, from column c on, to a stage's B tile and scales.
+template <typename E>
+__device__ __forceinline__ void mx_quant_block(const MxArgs &p, int t, int c, uint8_t *tile,
+                                               uint8_t *scales, int block)
+{
+    Oct<E> in[4];
+    const E *x = static_cast<const E *>(p.rows) + int64_t(t) * p.ld + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        in[i].load(x + 8 * i, p.K - c, p.vec);  // a whole block or nothing
+    uint32_t m = in[0].max_bits();
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        m = max(m, in[i].max_bits());
+    const uint32_t byte = mx_scale_byte(m);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[8];
+        in[i].to(v);
+        w[i] = mx_encode8(v, byte);
+    }
+    // a block is one 16-byte piece of the row's 128 bytes, in their swizzle
+    reinterpret_cast<uint4 *>(tile)[t * 8 + (block ^ (t & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+    scales[(block >> 2) * kMxTileBytes + t * 16 + (block & 3)] = uint8_t(byte);
 }
 
 // Columns of tensor memory: the accumulator, or two of them and the sum where
@@ -86,6 +127,11 @@ __host__ __device__ __forceinline__ uint32_t mx_columns(int bn, bool cut)
 // Tiles of 128 of W's rows (A) x bn of x's (16 ... 128), one CTA each, or `split`
 // CTAs of a cluster that share the reduction and join their parts through
 // distributed shared memory, each finishing 128 / split of the tile's features.
+//
+// QUANT: the accumulator warps, which have nothing to do yet, quantise the CTA's
+// part of a few rows while the weights are on their way (one launch, and no memory
+// for the codes).
+template <bool QUANT>
 __global__ void __launch_bounds__(kMxThreads)
     k_linear_mx(const __grid_constant__ MxMaps maps, const MxArgs p)
 {
@@ -96,15 +142,17 @@ __global__ void __launch_bounds__(kMxThreads)
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
     const int bn = p.bn, S = p.stages;
-    const uint32_t b_bytes = uint32_t(bn) * (MK / 2), stage_bytes = mx_stage_bytes(bn);
+    const uint32_t b_bytes = QUANT ? 0u : uint32_t(bn) * (MK / 2);
+    const uint32_t stage_bytes = mx_stage_bytes(bn, QUANT);
     const uint32_t z = cluster_ctarank();
     const int tile = int(blockIdx.x) / p.split;
     const int m0 = (tile % p.n_mt) * MM, n0 = (tile / p.n_mt) * bn;
     const int nk = (p.K + MK - 1) / MK;
     const int kb0 = int(int64_t(nk) * z / p.split), kb1 = int(int64_t(nk) * (z + 1) / p.split);
     const int chains = (kb1 - kb0 + p.chain - 1) / p.chain;
-    // the same in every CTA of the launch
-    const bool cut = (nk + p.split - 1) / p.split > p.chain;
+    // the same in every CTA of the launch: the most stages of one
+    const int most = (nk + p.split - 1) / p.split;
+    const bool cut = most > p.chain;
     const uint32_t tmem_cols = mx_columns(bn, cut);
     volatile int *abort_flag = &ctl.abort_flag;
 
@@ -118,10 +166,14 @@ __global__ void __launch_bounds__(kMxThreads)
             mbar_init(&ctl.acc_empty[b], 4);  // the accumulator warps
         }
         mbar_init(&ctl.done, 1);
+        if (QUANT)
+            for (int s = 0; s < kMxQuantStages; ++s)
+                mbar_init(&ctl.rows_full[s], 4);  // the accumulator warps
         ctl.abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.a);
-        prefetch_tmap(&maps.b);
+        if (!QUANT)
+            prefetch_tmap(&maps.b);
     }
     __syncwarp();
     cluster_arrive();
@@ -133,6 +185,9 @@ __global__ void __launch_bounds__(kMxThreads)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = ctl.tmem_base;
+    // QUANT: behind the ring, the tiles of x and then their scales
+    uint8_t *x_tiles = smem + S * stage_bytes;
+    uint8_t *x_scales = x_tiles + (kb1 - kb0) * (kMxQuantRows * (MK / 2));
     pdl_wait();
     pdl_launch_dependents();
 
@@ -149,12 +204,15 @@ __global__ void __launch_bounds__(kMxThreads)
             if (one) {
                 uint64_t *fb = &ctl.full[stage];
                 const uint32_t tiles = uint32_t(min(2, p.k_tiles - 2 * kb)) * kMxTileBytes;
-                mbar_arrive_expect_tx(fb, kMxATile + b_bytes + 2 * tiles);
+                mbar_arrive_expect_tx(fb, kMxATile + b_bytes + (QUANT ? 1 : 2) * tiles);
                 uint8_t *sa = smem + stage * stage_bytes, *sb = sa + kMxATile, *ss = sb + b_bytes;
                 tma_load_2d(sa, &maps.a, fb, kb * (MK / 2), m0);
-                tma_load_2d(sb, &maps.b, fb, kb * (MK / 2), n0);
                 bulk_load(ss, p.a_scales + (a_at + 2 * kb) * kMxTileBytes, tiles, fb);
-                bulk_load(ss + kMxScales, p.b_scales + (b_at + 2 * kb) * kMxTileBytes, tiles, fb);
+                if (!QUANT) {
+                    tma_load_2d(sb, &maps.b, fb, kb * (MK / 2), n0);
+                    bulk_load(ss + kMxScales, p.b_scales + (b_at + 2 * kb) * kMxTileBytes, tiles,
+                              fb);
+                }
             }
             __syncwarp();
             issued |= 1u << stage;
@@ -175,8 +233,10 @@ __global__ void __launch_bounds__(kMxThreads)
         int stage = 0;
         uint32_t phase = 0;
         const uint32_t sa = smem_u32(smem), sb = sa + kMxATile, ss = sb + b_bytes;
-        const uint64_t da0 = smem_desc_sw128(sa, 16, 1024), db0 = smem_desc_sw128(sb, 16, 1024);
+        const uint64_t da0 = smem_desc_sw128(sa, 16, 1024);
+        const uint64_t db0 = smem_desc_sw128(QUANT ? smem_u32(x_tiles) : sb, 16, 1024);
         const uint64_t ds0 = smem_desc_rows16(ss);
+        const uint64_t dx0 = smem_desc_rows16(QUANT ? smem_u32(x_scales) : ss + kMxScales);
         const uint32_t scales = tmem_base + tmem_cols - kMxScaleCols;
         const bool one = elect_one();
         uint32_t d = tmem_base, aphase = 0;
@@ -192,23 +252,28 @@ __global__ void __launch_bounds__(kMxThreads)
                 d = tmem_base + uint32_t(buf * bn);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
+            if (QUANT && ok)
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.rows_full[kb - kb0], 0, abort_flag));
             if (!ok)
                 break;
             tc_fence_after_sync();
             if (one) {
-                const uint64_t off = uint64_t(uint32_t(stage) * (stage_bytes >> 4));
+                const uint32_t off = uint32_t(stage) * (stage_bytes >> 4);
+                const uint32_t x_at = uint32_t(kb - kb0);  // QUANT: its tile of x
+                const uint32_t b_off = QUANT ? x_at * (kMxQuantRows * (MK / 2) >> 4) : off;
+                const uint32_t x_off = QUANT ? x_at * (kMxScales >> 4) : off;
                 const int rest = p.K - kb * MK;
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i)
                     if (rest > int(i) * 128) {
-                        tc_copy_32x128b(scales + 4 * i, ds0 + off + i * (kMxTileBytes >> 4));
+                        tc_copy_32x128b(scales + 4 * i, ds0 + (off + i * (kMxTileBytes >> 4)));
                         tc_copy_32x128b(scales + 8 + 4 * i,
-                                        ds0 + off + ((kMxScales + i * kMxTileBytes) >> 4));
+                                        dx0 + (x_off + i * (kMxTileBytes >> 4)));
                     }
 #pragma unroll
                 for (uint32_t kk = 0; kk < 4; ++kk)
                     if (rest > int(kk) * 64)
-                        tc_mma_mxf4(d, da0 + off + kk * 2, db0 + off + kk * 2,
+                        tc_mma_mxf4(d, da0 + (off + kk * 2), db0 + (b_off + kk * 2),
                                     idesc_mxf4(MM, uint32_t(bn), kk & 1), scales + 4 * (kk >> 1),
                                     scales + 8 + 4 * (kk >> 1), left != p.chain || kk != 0);
                 tc_commit(&ctl.empty[stage]);
@@ -240,7 +305,8 @@ __global__ void __launch_bounds__(kMxThreads)
     // ring, which may still be in use there, or (128 columns) into the ring
     // once every CTA is done with it.
     const bool beside = bn < MM;
-    float *acc = reinterpret_cast<float *>(smem + (beside ? S * stage_bytes : 0u));
+    float *acc = reinterpret_cast<float *>(
+        smem + (beside ? S * stage_bytes + (QUANT ? mx_rows_bytes(most) : 0u) : 0u));
     const int slice = MM / p.split, pitch = bn + 4;  // acc: [Z][128 / Z][pitch]
     const int cols = min(bn, p.N - n0);
     // what a thread finishes: four neighbouring m, always the same, of every `by`-th n
@@ -252,6 +318,26 @@ __global__ void __launch_bounds__(kMxThreads)
     for (int i = 0; i < 4; ++i)
         bias[i] = p.bias && i < left ? p.bias[at + i] : 0.0f;
     bool done = false;
+    if (QUANT && warp >= 2) {
+        // a thread has a block of 32: eight to a row and stage
+        for (int kb = kb0; kb < kb1; ++kb) {
+            uint8_t *tile = x_tiles + (kb - kb0) * (kMxQuantRows * (MK / 2));
+            uint8_t *tile_scales = x_scales + (kb - kb0) * kMxScales;
+            for (int i = int(threadIdx.x) - 64; i < p.N * 8; i += 128) {
+                const int t = i >> 3, block = i & 7, c = kb * MK + block * 32;
+                if (p.type == MOE_DT_F32)
+                    mx_quant_block<float>(p, t, c, tile, tile_scales, block);
+                else if (p.type == MOE_DT_F16)
+                    mx_quant_block<__half>(p, t, c, tile, tile_scales, block);
+                else
+                    mx_quant_block<__nv_bfloat16>(p, t, c, tile, tile_scales, block);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl.rows_full[kb - kb0]);
+        }
+    }
     if (warp >= 2) {
         const uint32_t lanes = tmem_base + (uint32_t(warp & 3) << 21);
         for (int i = 0; cut && i < chains; ++i) {
@@ -836,30 +922,59 @@ struct MxProduct {
     int T, K, N;
     EpiArgs epi;
     uint32_t *status;
+    // in place of x: rows to quantise (k_linear_mx alone)
+    const void *rows;
+    int64_t ld;
+    int type;
 };
 
 constexpr size_t kMxLoneSmem = 226 * 1024;  // of a CTA that takes all of an SM's tensor memory
 
+// Columns, tiles and split of k_linear_mx.
+struct MxSmall {
+    int bn, n_mt, split;
+    int64_t tiles;
+
+    MxSmall(int T, int K, int N, int sms)
+    {
+        const int nk = (K + MK - 1) / MK;
+        bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+        n_mt = int((int64_t(N) + MM - 1) / MM);
+        tiles = int64_t(n_mt) * ((int64_t(T) + bn - 1) / bn);
+        // split the reduction while the CTAs still fit at once and each has two stages
+        split = 1;
+        while (split < kMxMaxSplit && tiles * split * 2 <= 2 * sms && nk / (split * 2) >= 2)
+            split *= 2;
+    }
+
+    // Whether the kernel quantises x itself: its CTAs hold their part of x beside
+    // the ring, and a few rows take them no longer than the weights' first stages.
+    bool quantises(int T, int K) const
+    {
+        const int nk = (K + MK - 1) / MK;
+        return T <= kMxQuantRows && (nk + split - 1) / split <= kMxQuantStages;
+    }
+};
+
 cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
 {
-    const int sms = device_sm_count(), nk = (q.K + MK - 1) / MK;
+    const int nk = (q.K + MK - 1) / MK;
+    const MxSmall l(q.T, q.K, q.N, device_sm_count());
+    const bool quant = q.rows != nullptr;
     MxArgs a = {};
     static_cast<EpiArgs &>(a) = q.epi;
     a.status = q.status;
     a.a_scales = q.W_scales, a.b_scales = q.x_scales;
+    a.rows = q.rows, a.ld = q.ld, a.type = q.type;
+    a.vec = quant && rows_vec(q.rows, q.ld, dtype_size(q.type));
     a.M = q.N, a.N = q.T, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
-    a.bn = q.T <= 16 ? 16 : q.T <= 32 ? 32 : q.T <= 64 ? 64 : 128;
     a.chain = mx_chain(a.out_f32, a.f16);
-    a.n_mt = (q.N + MM - 1) / MM;
-    const int64_t tiles = int64_t(a.n_mt) * ((int64_t(q.T) + a.bn - 1) / a.bn);
-    // split the reduction while the CTAs still fit at once and each has two stages
-    a.split = 1;
-    while (a.split < kMxMaxSplit && tiles * a.split * 2 <= 2 * sms && nk / (a.split * 2) >= 2)
-        a.split *= 2;
-    if (tiles * a.split > INT_MAX)
+    a.bn = l.bn, a.n_mt = l.n_mt, a.split = l.split;
+    if (l.tiles * a.split > INT_MAX)
         return cudaErrorInvalidValue;
-    const uint32_t stage = mx_stage_bytes(a.bn);
-    const uint32_t parts = a.bn < MM ? uint32_t(MM) * (a.bn + 4) * 4 : 0;
+    const uint32_t stage = mx_stage_bytes(a.bn, quant);
+    const uint32_t parts = (a.bn < MM ? uint32_t(MM) * (a.bn + 4) * 4 : 0) +
+                           (quant ? mx_rows_bytes((nk + a.split - 1) / a.split) : 0);
     a.stages = std::min<int>(kMxMaxStages, (110 * 1024 - parts) / stage);
     size_t smem = 1024 + std::max<size_t>(size_t(a.stages) * stage + parts,
                                           a.bn < MM ? 0 : size_t(MM) * (a.bn + 4) * 4);
@@ -869,18 +984,19 @@ cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
     // would wait for ever.
     if (mx_columns(a.bn, (nk + a.split - 1) / a.split > a.chain) > 256)
         smem = kMxLoneSmem;
-    MxMaps maps;
+    MxMaps maps = {};
     cudaError_t e = mx_map(&maps.a, q.W, q.N, q.K, MM);
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !quant)
         e = mx_map(&maps.b, q.x, q.T, q.K, a.bn);
-    const void *kern = reinterpret_cast<const void *>(k_linear_mx);
+    const void *kern = quant ? reinterpret_cast<const void *>(k_linear_mx<true>)
+                             : reinterpret_cast<const void *>(k_linear_mx<false>);
     if (e == cudaSuccess)
-        e = ensure_smem_limit(kern, kSlotLinearMx, kMxLoneSmem);
+        e = ensure_smem_limit(kern, kSlotLinearMx + quant, kMxLoneSmem);
     if (e != cudaSuccess)
         return e;
     void *args[] = {&maps, &a};
-    return launch_clustered(kern, unsigned(tiles * a.split), unsigned(a.split), kMxThreads, smem, s,
-                            args);
+    return launch_clustered(kern, unsigned(l.tiles * a.split), unsigned(a.split), kMxThreads, smem,
+                            s, args);
 }
 
 // Columns of a tile of k_linear_mx_pair: those with the least estimated time, in
@@ -984,9 +1100,10 @@ int mx_check(const uint8_t *W, const uint8_t *W_scales, const float *bias, const
                : MOE_ERR_ALIGN;
 }
 
-int mx_linear(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W, const uint8_t *W_scales,
-              const float *bias, const void *residual, int64_t ldr, int act, int T, int K, int N,
-              void *y, int64_t ldy, int y_dtype, uint32_t *status, cudaStream_t s)
+int mx_linear(const uint8_t *x, const uint8_t *x_scales, const void *rows, int64_t ld, int type,
+              const uint8_t *W, const uint8_t *W_scales, const float *bias, const void *residual,
+              int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy, int y_dtype,
+              uint32_t *status, cudaStream_t s)
 {
     const int size = dtype_size(y_dtype);
     EpiArgs e = {};
@@ -994,7 +1111,7 @@ int mx_linear(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W, const
     e.ldr = ldr, e.ldo = ldy;
     e.f16 = y_dtype == MOE_DT_F16, e.out_f32 = y_dtype == MOE_DT_F32, e.act = act;
     e.vec_out = vec16(y, ldy, size), e.vec_res = vec16(residual, ldr, size);
-    const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status};
+    const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status, rows, ld, type};
     return launch_mx(q, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1023,16 +1140,17 @@ extern "C" int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const
         return MOE_ERR_ALIGN;
     if (T == 0)
         return MOE_OK;
-    return mx_linear(x, x_scales, W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype,
-                     status, reinterpret_cast<cudaStream_t>(stream));
+    return mx_linear(x, x_scales, nullptr, 0, 0, W, W_scales, bias, residual, ldr, act, T, K, N, y,
+                     ldy, y_dtype, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t moe_linear_rows_mxfp4_workspace_bytes(int T, int K)
+extern "C" size_t moe_linear_rows_mxfp4_workspace_bytes(int T, int K, int N)
 {
     using namespace moe;
-    if (T < 0 || T > kMost || K < 32 || K > kMost || K % 32 != 0)
+    if (T <= 0 || T > kMost || K < 32 || K > kMost || K % 32 != 0 || N < 1 || N > kMost ||
+        MxSmall(T, K, N, device_sm_count()).quantises(T, K))
         return 0;
-    return std::max<size_t>(256, mx_codes_bytes(T, K) + align256(size_t(mx_scale_bytes(T, K))));
+    return mx_codes_bytes(T, K) + align256(size_t(mx_scale_bytes(T, K)));
 }
 
 extern "C" int moe_linear_rows_mxfp4(const void *x, int64_t ldx, int x_dtype, const uint8_t *W,
@@ -1042,19 +1160,29 @@ extern "C" int moe_linear_rows_mxfp4(const void *x, int64_t ldx, int x_dtype, co
                                      size_t ws_bytes, uint32_t *status, moe_stream_t stream)
 {
     using namespace moe;
-    int rc = mx_check(W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype, status);
+    if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16 && x_dtype != MOE_DT_F32)
+        return MOE_ERR_DTYPE;
+    const int rc = mx_check(W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype, status);
     if (rc != MOE_OK)
         return rc;
-    if (!ws)
+    const size_t need = moe_linear_rows_mxfp4_workspace_bytes(T, K, N);
+    if (ldx < K)
+        return MOE_ERR_SHAPE;
+    if ((T > 0 && !x) || (need && !ws))
         return MOE_ERR_NULL;
-    if (ws_bytes < moe_linear_rows_mxfp4_workspace_bytes(T, K))
+    if (ws_bytes < need)
         return MOE_ERR_WORKSPACE;
-    if (!aligned(ws, 256))
+    if (!aligned(x, dtype_size(x_dtype)) || (need && !aligned(ws, 256)))
         return MOE_ERR_ALIGN;
+    if (T == 0)
+        return MOE_OK;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!need)
+        return mx_linear(nullptr, nullptr, x, ldx, x_dtype, W, W_scales, bias, residual, ldr, act,
+                         T, K, N, y, ldy, y_dtype, status, s);
     uint8_t *codes = static_cast<uint8_t *>(ws), *scales = codes + mx_codes_bytes(T, K);
-    rc = moe_quantize_rows_mxfp4(x, ldx, x_dtype, T, K, codes, scales, stream);
-    if (rc != MOE_OK || T == 0)
-        return rc;
-    return mx_linear(codes, scales, W, W_scales, bias, residual, ldr, act, T, K, N, y, ldy, y_dtype,
-                     status, reinterpret_cast<cudaStream_t>(stream));
+    const int quantised = moe_quantize_rows_mxfp4(x, ldx, x_dtype, T, K, codes, scales, stream);
+    return quantised != MOE_OK ? quantised
+                               : mx_linear(codes, scales, nullptr, 0, 0, W, W_scales, bias, residual,
+                                           ldr, act, T, K, N, y, ldy, y_dtype, status, s);
 }

@@ -138,20 +138,54 @@ def test_every_block_has_its_own_scale():
         assert np.array_equal(_f64(y), want)
 
 
-def test_rows_quantised_by_the_call():
-    W = _rows(_rand(1, 300, 640, amp=0.05))
-    for T in (1, 20, 300):
-        for dtype in (BF, F16, F32):
-            x = _wide(_rand(2, T, 640), 8, dtype)
-            y = B.linear_mxfp4(x, W, act="silu")
-            assert y.dtype == dtype
-            q = B.quantize_rows_mxfp4(x)
-            assert torch.equal(y, B.linear_mxfp4(q, W, act="silu", out_dtype=dtype))
-            ws = torch.empty(B.linear_rows_mxfp4_workspace_bytes(T, 640), dtype=torch.uint8,
-                             device="cuda")
-            assert torch.equal(y, B.linear_mxfp4(x, W, act="silu", ws=ws))
+@pytest.mark.parametrize("T", [1, 2, 7, 15, 16, 17, 40, 300])
+@pytest.mark.parametrize("K", [32, 96, 640, 2560, 2816])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_rows_quantised_by_the_call(T, K, dtype):
+    """Bit for bit what the product of the quantised rows is, whichever kernel
+    quantises them, with NaN and infinite values too."""
+    W = _rows(_rand(1, 300, K, amp=0.05))
+    for pad in (0, 3, 8):
+        x = _wide(_rand(2, T, K) * torch.exp(3 * _rand(3, T, K // 32)).repeat_interleave(32, 1), pad,
+                  dtype)
+        x[0, 5] = 0.0
+        if T > 2:
+            x[1, K - 1] = float("nan")
+            x[2, 3] = float("inf")
+        y = B.linear_mxfp4(x, W, act="relu", out_dtype=dtype)
+        assert y.dtype == dtype
+        q = B.quantize_rows_mxfp4(x)
+        want = B.linear_mxfp4(q, W, act="relu", out_dtype=dtype)
+        assert torch.equal(y.isnan(), want.isnan())
+        assert torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0))
+        need = B.linear_rows_mxfp4_workspace_bytes(T, K, 300)
+        assert (need == 0) == (T <= 16)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            again = B.linear_mxfp4(x, W, act="relu", out_dtype=dtype, ws=ws)
+            assert torch.equal(again.nan_to_num(7.0), want.nan_to_num(7.0))
             with pytest.raises(B.MoeError):
                 B.linear_mxfp4(x, W, ws=ws[:-1])
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 2560, 10240), (16, 10240, 2560), (16, 11264, 11264),
+                                   (3, 65536, 40), (16, 2048, 20000), (1, 11264, 2816)])
+def test_few_rows_of_large_products(T, K, N):
+    """Among them products whose rows are too long for the kernel to quantise."""
+    x = _rand(1, T, K).to("cuda", BF)
+    W = B.quantize_rows_mxfp4((_rand(2, 64, K, amp=K ** -0.5)).cuda())
+    many = B.Mxfp4Rows(W.codes.repeat((N + 63) // 64, 1)[:N].contiguous(), None)
+    scales = W.scales.view(1, -1, 32, 4, 4)[:, :, :, :2].repeat(1, 1, 1, 2, 1)  # rows 64 ... are 0 ...
+    scales = scales.reshape(1, -1, 512).repeat((N + 127) // 128, 1, 1).contiguous()
+    many = B.Mxfp4Rows(many.codes, scales)
+    res = _rand(3, T, N).cuda()
+    y = B.linear_mxfp4(x, many, residual=res, out_dtype=F32)
+    q = B.quantize_rows_mxfp4(x)
+    assert torch.equal(y, B.linear_mxfp4(q, many, residual=res, out_dtype=F32))
+    xd, Wd = _values(q), _values(W)
+    ref = np.tile(xd @ Wd.T, (1, (N + 63) // 64))[:, :N] + _f64(res)
+    size = np.tile(np.abs(xd) @ np.abs(Wd).T, (1, (N + 63) // 64))[:, :N]
+    _within(y, ref, 2.0 ** -19 * size + 2.0 ** -23 * np.abs(_f64(res)))
 
 
 def test_extreme_scales():

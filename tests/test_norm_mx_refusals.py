@@ -145,15 +145,17 @@ def test_linear(lib, kw, rc):
 
 ROWS = ("x ldx x_dtype W Ws bias residual ldr act T K N y ldy y_dtype ws ws_bytes status "
         "stream").split()
-ROWS_OK = dict(LIN_OK, ldx=64, x_dtype=0, ws=FAKE, ws_bytes=BIG)
+ROWS_OK = dict(LIN_OK, ldx=64, x_dtype=0, T=20, ws=FAKE, ws_bytes=BIG)
 
 
 @pytest.mark.parametrize("kw,rc", [
     (dict(y_dtype=3), "DTYPE"), (dict(x_dtype=3), "DTYPE"), (dict(T=-1), "SHAPE"),
     (dict(K=48), "SHAPE"), (dict(N=0), "SHAPE"), (dict(ldx=63), "SHAPE"), (dict(ldy=9), "SHAPE"),
     (dict(x=None), "NULL"), (dict(W=None), "NULL"), (dict(y=None), "NULL"), (dict(ws=None), "NULL"),
-    (dict(ws_bytes=256 + 511), "WORKSPACE"), (dict(ws=FAKE + 128), "ALIGN"),
-    (dict(x=FAKE + 1), "ALIGN"), (dict(W=FAKE + 8), "ALIGN"), (dict(T=0, x=None, y=None), None)])
+    (dict(T=4, x=None, ws=None), "NULL"), (dict(T=4, x=FAKE + 1), "ALIGN"), (dict(T=4, ldx=63), "SHAPE"),
+    (dict(ws_bytes=768 + 511), "WORKSPACE"), (dict(ws=FAKE + 128), "ALIGN"),
+    (dict(x=FAKE + 1), "ALIGN"), (dict(W=FAKE + 8), "ALIGN"),
+    (dict(T=0, x=None, y=None, ws=None, ws_bytes=0), None)])
 def test_linear_of_rows(lib, kw, rc):
     want = B.MOE_OK if rc is None else getattr(B, "MOE_ERR_" + rc)
     assert _call(lib.moe_linear_rows_mxfp4, ROWS, ROWS_OK, **kw) == want
@@ -161,8 +163,11 @@ def test_linear_of_rows(lib, kw, rc):
 
 def test_linear_of_rows_workspace(lib):
     f = lib.moe_linear_rows_mxfp4_workspace_bytes
-    assert f(4, 64) == 256 + 512 and f(0, 64) == 256 and f(4, 48) == 0 and f(-1, 64) == 0
-    assert f(1000, 2560) == 1000 * 1280 + 8 * 20 * 512
+    assert f(20, 64, 10) == 768 + 512 and f(0, 64, 10) == 0 and f(20, 48, 10) == 0
+    assert f(-1, 64, 10) == 0 and f(20, 64, 0) == 0
+    assert f(4, 64, 10) == 0  # quantised by the product's kernel
+    assert f(16, 1 << 20, 10) == 16 * (1 << 19) + 8192 * 512  # too long for it
+    assert f(1000, 2560, 10) == 1000 * 1280 + 8 * 20 * 512
 
 
 def test_the_binding_refuses_tensors_that_are_not_on_a_gpu():
