@@ -730,12 +730,14 @@ MOE_API int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, const
  *   scales  uint8, moe_mxfp4_scale_bytes(rows, K) of them: S in tiles of 128
  *           rows x 4 blocks, [ceil(rows/128), ceil(K/128), 512]; of a tile, row
  *           32 q + l, block b at byte 16 l + 4 q + b
- * both 16-byte aligned, K a positive multiple of 32.
+ * both 16-byte aligned, K a positive multiple of 32.  The scale bytes of blocks past
+ * the last (of the last tile along K) are 0, as these calls write them; those of
+ * rows past the last may be anything.
  *
  * moe_quantize_rows_mxfp4 -- x dtype [rows, K] (any MOE_DT_*), rows ldx elements
  * apart, aligned to its element, to codes and scales.  S and the codes as in
  * moe_quantize_mxfp4; a block with a NaN or an infinity has S = 255 (NaN) and
- * codes 0.  Scale bytes past the last row and block are written as 0.
+ * codes 0.  Scale bytes past the last row are written as 0 too.
  *
  * moe_dequantize_rows_mxfp4 -- y dtype [rows, K] (MOE_DT_BF16 or MOE_DT_F32,
  * which hold the values exactly), rows ldy elements apart.
@@ -764,7 +766,8 @@ MOE_API int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scale
  * quantises itself (to the same codes); ws may be NULL then.
  * A row (or weight) with a NaN block makes its outputs NaN.  T >= 0, N >= 1, K a
  * positive multiple of 32; T, K, N <= 2^31 - 512; ldr, ldy >= N.  codes and scales
- * 16-byte aligned, the others to their element.  Deterministic.
+ * 16-byte aligned, the others to their element.  No operands but residual and y
+ * may overlap.  Deterministic.
  */
 MOE_API int moe_linear_mxfp4(const uint8_t *x, const uint8_t *x_scales, const uint8_t *W,
                              const uint8_t *W_scales, const float *bias, const void *residual,

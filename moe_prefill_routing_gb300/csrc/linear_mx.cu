@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(kMxThreads)
 // better (192 columns: six; with five 4096 x 11264 x 11264 took 172 us, with three
 // of twice the size 155 us).
 constexpr int kMxPairStages = 8;  // at most
-constexpr int kMxEpiCols = 64;   // of an epilogue warp (32 rows), all in registers at once
-constexpr int kMxEpiWarps = 12;  // at most: 192 columns
+constexpr int kMxEpiCols = 64;    // of an epilogue warp (32 rows), all in registers at once
+constexpr int kMxEpiWarps = 12;   // at most: 192 columns
 constexpr int kMxPairThreads = 64 + 32 * kMxEpiWarps;
 constexpr uint32_t kMxSlot = 2048;  // of an epilogue warp: 32 rows of 64 bytes
 constexpr int kMxPieceCols = 24;    // of tensor memory: A's two scale tiles, B's two of two
@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             bool ok = true;
             for (int t = pair; ok && t < g.tiles; t += pairs) {
                 place(t, m0, n0);
-                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
                 if (!ok)
                     break;
                 const uint32_t d = tmem_base + uint32_t(buf * bn);
@@ -684,11 +685,12 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                             tc_copy_32x128b_pair(at + 12, ds0 + (off + 4 * kTile));
                             tc_copy_32x128b_pair(at + 20, ds0 + (off + 5 * kTile));
                         }
-    #pragma unroll
+#pragma unroll
                         for (uint32_t kk = 0; kk < 4; ++kk)
                             tc_mma_mxf4_pair(d, da0 + (off + 2 * kk), db0 + (off + 2 * kk),
-                                             idesc | (kk & 1) << 5 | (kk & 1) << 30, at + 4 * (kk >> 1),
-                                             at + 8 + 8 * (kk >> 1) + b_col, kb != 0 || kk != 0);
+                                             idesc | (kk & 1) << 5 | (kk & 1) << 30,
+                                             at + 4 * (kk >> 1), at + 8 + 8 * (kk >> 1) + b_col,
+                                             kb != 0 || kk != 0);
                         tc_commit_pair(&ctl.empty[stage], 3);
                     }
                     __syncwarp();

@@ -170,6 +170,36 @@ def test_in_place_and_rows_left_alone():
     assert (h[50:] == 7).all() and (big[50:] == 7).all() and (big[:, 640:] == 7).all()
 
 
+@pytest.mark.parametrize("S,Bt", [(BF, BF), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("d", [40, 520, 9000])
+def test_rows_that_start_anywhere(S, Bt, d):
+    v = _inputs(20, d, S, Bt)
+    how = {n: v[n] for n in ("pre", "post", "gate")}
+    want = B.block_norm(v["x"], v["o"], **how)
+    gx, gh = _rand(7, 20, d).to("cuda", S), _rand(8, 20, d).to("cuda", Bt)
+    grads = B.block_norm_grad(want["xn"], v["o"], dxn=gx, dh=gh, **how)
+    moved = lambda t, at: torch.cat((torch.full((20, at), 3.0, dtype=t.dtype, device="cuda"), t),  # noqa: E731
+                                    1)[:, at:]
+    for at in (1, 3):
+        x, o = moved(v["x"], at), moved(v["o"], at)
+        xn, h = moved(torch.zeros_like(x), at), moved(torch.zeros_like(o), at)
+        B.block_norm(x, o, **how, xn=xn, h=h)
+        # (sums in another order: 2^-18 of the norm and a rounding to either side)
+        for a, b in ((xn, want["xn"]), (h, want["h"])):
+            assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -17 + torch.finfo(a.dtype).eps,
+                                  atol=2.0 ** -17)
+        dx, do = moved(torch.zeros_like(x), at), moved(torch.zeros_like(o), at)
+        got = B.block_norm_grad(moved(want["xn"], at), o, dxn=moved(gx, at), dh=moved(gh, at), **how,
+                                dx=dx, do=do)
+        ref, size = D.grads(_f64(want["xn"]), _f64(v["o"]), _f64(gx), _f64(gh), _f64(v["pre"]),
+                            _f64(v["post"]), _f64(v["gate"]))
+        for n in ref:
+            _within(got[n], ref[n], 2.0 ** -16 * size[n], n)
+            _within(grads[n], ref[n], 2.0 ** -16 * size[n], n)
+        for t in (xn, h, dx, do):
+            assert (t._base[:, :at] == 3).all()
+
+
 def test_no_rows():
     v = _inputs(0, 64, BF, BF)
     r = B.block_norm(**v, mxfp4=True)

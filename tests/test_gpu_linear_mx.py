@@ -210,6 +210,37 @@ def test_a_nan_block_stays_in_its_row():
         assert torch.equal(y[keep], clean[keep])
 
 
+def test_a_nan_block_of_a_weight_stays_in_its_column():
+    x, W = _rand(1, 300, 320), _rand(2, 300, 320)
+    bad = W.clone()
+    bad[7, 300] = float("nan")
+    bad[250, 0] = -float("inf")
+    keep = [n for n in range(300) if n not in (7, 250)]
+    for T in (5, 100, 300):
+        clean = B.linear_mxfp4(_rows(x[:T]), _rows(W), out_dtype=F32)
+        y = B.linear_mxfp4(_rows(x[:T]), _rows(bad), out_dtype=F32)
+        assert torch.isnan(y[:, [7, 250]]).all() and torch.equal(y[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_many_chains(T, out):
+    """More of K than one accumulator sums of an fp32 output."""
+    _check(T, 16640, 130, out=out)
+    _check(T, 40000, 20, out=out, bias=False, res=False)
+
+
+@pytest.mark.parametrize("T", [9, 200])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_rows_that_start_anywhere(T, out):
+    x = _rand(1, T, 321).to("cuda", BF)[:, 1:]
+    W = _rows(_rand(2, 72, 320))
+    r, y = _rand(3, T, 75).to("cuda", out)[:, 1:73], torch.zeros(T, 75, dtype=out, device="cuda")
+    B.linear_mxfp4(x, W, residual=r, y=y[:, 3:])
+    want = B.linear_mxfp4(x.contiguous(), W, residual=r.contiguous(), out_dtype=out)
+    assert torch.equal(y[:, 3:], want) and not y[:, :3].any()
+
+
 def test_residual_in_place_and_rows_left_alone():
     x, W = _rand(1, 200, 320), _rows(_rand(2, 72, 320))
     for T in (5, 200):

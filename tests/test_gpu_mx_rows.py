@@ -55,6 +55,17 @@ def test_rows_of_a_wider_tensor(dtype, pad):
     assert torch.equal(y[:, :320].isnan(), want.isnan()) and (y[:, 320:] == 5).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_rows_that_start_anywhere(dtype):
+    w = _rows(3, 70, 352, dtype, spread=1.0)
+    for at in (1, 2, 5):
+        q = _check(w[:, at:at + 320])
+        y = torch.full((70, 352), 5.0, dtype=F32, device="cuda")
+        B.dequantize_rows_mxfp4(q, y=y[:, at:at + 320])
+        assert torch.equal(y[:, at:at + 320], B.dequantize_rows_mxfp4(q, F32))
+        assert (y[:, :at] == 5).all() and (y[:, at + 320:] == 5).all()
+
+
 def test_every_tie_and_its_neighbours():
     points = torch.tensor([0.0, 0.25, 0.5, 0.75, 1.0, 1.25, 1.5, 1.75, 2.0, 2.5, 3.0, 3.5, 4.0, 5.0,
                            6.0, 7.0])
