@@ -1061,11 +1061,28 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
                             kMxLoneSmem, s, args);
 }
 
+// Which kernel.  Pairs of CTAs waste most of their 256 rows on a few, but a tile
+// takes them 2.3 us and 0.22 for each stage of its whole reduction however few
+// its rows are, where k_linear_mx splits the reduction eight ways at best and
+// joins the parts in 3 to 10 us that grow with the rows.  Measured (us, k_linear_mx
+// and pairs): 64 rows x 2560 x 10240 10.0 and 7.6, x 10240 x 2560 9.4 and 11.2, x
+// 11264 x 11264 (split by two) 23.0 and 17.3, x 512 x 2560 8.1 and 4.0; 128 x 10240
+// x 2560 14.5 and 11.5; 32 x 2560 x 2560 5.1 and 6.6, x 512 x 2560 6.2 and 4.0.
+bool mx_takes_pairs(const MxProduct &q)
+{
+    const int nk = (q.K + MK - 1) / MK;
+    if (nk > mx_chain(q.epi.out_f32, q.epi.f16))  // the pairs' sums are not cut
+        return false;
+    if (q.T > 64)
+        return true;
+    if (q.T > 32)
+        return nk <= 20 || MxSmall(q.T, q.K, q.N, device_sm_count()).split < kMxMaxSplit;
+    return q.T > kMxQuantRows && nk <= 4;
+}
+
 cudaError_t launch_mx(const MxProduct &q, cudaStream_t s)
 {
-    // (the pairs' sums are not cut)
-    const bool cut = (q.K + MK - 1) / MK > mx_chain(q.epi.out_f32, q.epi.f16);
-    return q.T > 128 && !cut ? launch_mx_pair(q, s) : launch_mx_small(q, s);
+    return mx_takes_pairs(q) ? launch_mx_pair(q, s) : launch_mx_small(q, s);
 }
 
 }  // namespace

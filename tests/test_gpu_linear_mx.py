@@ -82,7 +82,7 @@ def _check(T, K, N, act="none", out=BF, bias=True, res=True, pad=0, seed=0, sums
 
 
 @pytest.mark.parametrize("T,K,N", [
-    (1, 32, 1), (1, 64, 8), (1, 96, 130), (2, 128, 3), (7, 160, 16), (15, 256, 127), (16, 288, 128),
+    (1, 32, 1), (1, 64, 8), (20, 96, 40), (31, 1024, 70), (40, 10240, 300), (64, 5376, 64), (1, 96, 130), (2, 128, 3), (7, 160, 16), (15, 256, 127), (16, 288, 128),
     (17, 512, 129), (32, 544, 100), (33, 1024, 300), (64, 1056, 64), (65, 2560, 200),
     (127, 800, 256), (128, 2560, 520), (1, 2560, 1024), (16, 10240, 256), (1, 11264, 40)])
 @pytest.mark.parametrize("out", [BF, F32])
