@@ -475,21 +475,19 @@ __device__ __forceinline__ uint4 *mx_slot_at(uint8_t *slot, int r, int c)
     return reinterpret_cast<uint4 *>(slot) + r * 4 + (c ^ ((r >> 1) & 3));
 }
 
-// Element by element, where 16-byte pieces are not aligned or do not exist whole.
-template <bool STORE, typename E>
-__device__ __noinline__ void mx_move_by_element(uint8_t *slot, E *p, int64_t ld, int rows, int cols)
+// A slot's columns to memory element by element, where 16-byte pieces are not
+// aligned.
+template <typename E>
+__device__ __noinline__ void mx_store_by_element(uint8_t *slot, E *p, int64_t ld, int rows,
+                                                 int cols)
 {
     constexpr int kPer = 16 / int(sizeof(E));
     const int lane = threadIdx.x & 31;
     if (lane < cols)
 #pragma unroll 16
-        for (int r = 0; r < rows; ++r) {
-            E *at = reinterpret_cast<E *>(mx_slot_at(slot, r, lane / kPer)) + lane % kPer;
-            if (STORE)
-                p[int64_t(r) * ld + lane] = *at;
-            else
-                *at = p[int64_t(r) * ld + lane];
-        }
+        for (int r = 0; r < rows; ++r)
+            p[int64_t(r) * ld + lane] =
+                reinterpret_cast<E *>(mx_slot_at(slot, r, lane / kPer))[lane % kPer];
 }
 
 // The epilogue's blocks: 32 rows (lane = row) x 64 bytes of the output.
@@ -499,15 +497,66 @@ struct MxBlock {
     static constexpr bool kF32 = sizeof(E) == 4;
     static constexpr int kF16 = std::is_same<E, __half>::value;
 
-    // The residual's block on its way: lane's pieces of rows lane / 4 + 8 i.
-    static __device__ __forceinline__ void ask(uint4 (&q)[4], const E *p, int64_t ld, int rows)
+    // The residual's block on its way, and into the slot: 16-byte pieces of rows
+    // lane / 4 + 8 i where they are aligned and exist whole (`vec`); else, just as
+    // many words, 16-bit elements of column `lane` of rows 2 i and 2 i + 1, or fp32
+    // ones of column lane % 16 of row 2 i + lane / 16.
+    static __device__ __forceinline__ void ask(uint4 (&q)[4], const E *p, int64_t ld, int rows,
+                                               int cols, bool vec)
     {
         const int lane = threadIdx.x & 31;
-        const E *at = p + (lane >> 2) * ld + (lane & 3) * (16 / int(sizeof(E)));
+        if (vec && cols >= kColumns) {
+            const E *at = p + (lane >> 2) * ld + (lane & 3) * (16 / int(sizeof(E)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((lane >> 2) + 8 * i < rows)
+                    q[i] = *reinterpret_cast<const uint4 *>(at + 8 * i * ld);
+            return;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (kF32) {
+                const int r = 2 * i + (lane >> 4), c = lane & 15;
+                w[i] = r < rows && c < cols
+                           ? __float_as_uint(reinterpret_cast<const float *>(p)[r * ld + c])
+                           : 0u;
+            } else {
+                const uint16_t *at = reinterpret_cast<const uint16_t *>(p) + 2 * i * ld + lane;
+                const uint32_t a = lane < cols && 2 * i < rows ? at[0] : 0u;
+                const uint32_t b = lane < cols && 2 * i + 1 < rows ? at[ld] : 0u;
+                w[i] = a | b << 16;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if ((lane >> 2) + 8 * i < rows)
-                q[i] = *reinterpret_cast<const uint4 *>(at + 8 * i * ld);
+            q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+
+    static __device__ __forceinline__ void place(uint8_t *slot, const uint4 (&q)[4], int cols,
+                                                 bool vec)
+    {
+        const int lane = threadIdx.x & 31;
+        if (vec && cols >= kColumns) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *mx_slot_at(slot, (lane >> 2) + 8 * i, lane & 3) = q[i];
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint4 v = q[i / 4];
+            const uint32_t w = i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
+            if constexpr (kF32) {
+                reinterpret_cast<uint32_t *>(
+                    mx_slot_at(slot, 2 * i + (lane >> 4), (lane & 15) / 4))[lane & 3] = w;
+            } else {
+                reinterpret_cast<uint16_t *>(mx_slot_at(slot, 2 * i, lane / 8))[lane & 7] =
+                    uint16_t(w);
+                reinterpret_cast<uint16_t *>(mx_slot_at(slot, 2 * i + 1, lane / 8))[lane & 7] =
+                    uint16_t(w >> 16);
+            }
+        }
     }
 
     static __device__ __forceinline__ void add(const uint8_t *slot, float *v)
@@ -728,7 +777,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                       (warp - 2) * kMxEpiCols;
         const uint32_t lanes =
             tmem_base + (uint32_t(q * 32) << 16) + uint32_t(part * kMxEpiCols);
-        const bool vec_res = p.residual && p.vec_res, any_res = p.residual;
+        const bool any_res = p.residual, vec_res = p.vec_res;
         int buf = 0;
         uint32_t aphase = 0;
         for (int t = pair; t < g.tiles; t += pairs) {
@@ -739,8 +788,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             const E *res = static_cast<const E *>(p.residual) + (any_res ? row * p.ldr + col : 0);
             E *out = static_cast<E *>(p.out) + row * p.ldo + col;
             uint4 ahead[4] = {};
-            if (vec_res && width >= C)
-                Block::ask(ahead, res, p.ldr, rows);
+            if (any_res)
+                Block::ask(ahead, res, p.ldr, rows, width, vec_res);
             if (p.bias) {
                 __syncwarp();
 #pragma unroll
@@ -795,16 +844,10 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                     bulk_wait_read<0>();  // the last store is done with the slot
                 __syncwarp();
                 if (any_res) {
-                    if (vec_res && cols == C) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *mx_slot_at(slot, int(lane >> 2) + 8 * i, int(lane & 3)) = ahead[i];
-                        if (b + 1 < kBlocks && width >= (b + 2) * C)
-                            Block::ask(ahead, res + (b + 1) * C, p.ldr, rows);
-                    } else {
-                        mx_move_by_element<false>(slot, const_cast<E *>(res) + b * C, p.ldr, rows,
-                                                  cols);
-                    }
+                    Block::place(slot, ahead, cols, vec_res);
+                    if (b + 1 < kBlocks)
+                        Block::ask(ahead, res + (b + 1) * C, p.ldr, rows, width - (b + 1) * C,
+                                   vec_res);
                     __syncwarp();
                     Block::add(slot, v);
                 }
@@ -818,7 +861,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                     }
                 } else {
                     __syncwarp();
-                    mx_move_by_element<true>(slot, out + b * C, p.ldo, rows, cols);
+                    mx_store_by_element(slot, out + b * C, p.ldo, rows, cols);
                 }
             }
         }
