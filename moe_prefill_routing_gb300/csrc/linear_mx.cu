@@ -128,9 +128,12 @@ __host__ __device__ __forceinline__ uint32_t mx_columns(int bn, bool cut)
 // CTAs of a cluster that share the reduction and join their parts through
 // distributed shared memory, each finishing 128 / split of the tile's features.
 //
+// What bounds it is latency: a launch's start, the first weights, the join.  One
+// row x 2560 x 10240 takes 5.5 us (13.9 MB, 2.5 TB/s), 16 x 10240 x 2560 8.5.
+//
 // QUANT: the accumulator warps, which have nothing to do yet, quantise the CTA's
 // part of a few rows while the weights are on their way (one launch, and no memory
-// for the codes).
+// for the codes): the first of these with GELU 8.3 -> 7.2 us.
 template <bool QUANT>
 __global__ void __launch_bounds__(kMxThreads)
     k_linear_mx(const __grid_constant__ MxMaps maps, const MxArgs p)
@@ -429,16 +432,17 @@ __global__ void __launch_bounds__(kMxThreads)
 // the MMAs fill the other.  192 columns are the most: two accumulators of 256
 // would leave no tensor memory for the scales.
 //
-// What bounds the ring is a stage's round trip, about 2000 cycles from its
-// release to its next data's arrival: the more stages it is spread over, the
-// better (192 columns: six; with five 4096 x 11264 x 11264 took 172 us, with three
-// of twice the size 155 us).
+// A stage's round trip, from its release to its next data's arrival, takes 1.14 us
+// however little is loaded, so it is spread over many stages (192 columns: six; 4096
+// x 11264 x 11264 217, 175, 151 and 142 us with three to six).  With six, what
+// bounds a long reduction are the MMAs of 64 of K (140 us, 7.4 PFLOP/s; 116 without
+// loads and epilogue, 126 without the epilogue), a short one the loads and stores:
+// 4096 x 2816 x 11264 51 us (5.1 PFLOP/s), 45 without MMAs, 39 without stores.
 constexpr int kMxPairStages = 8;  // at most
 constexpr int kMxEpiCols = 64;    // of an epilogue warp (32 rows), all in registers at once
 constexpr int kMxEpiWarps = 12;   // at most: 192 columns
 constexpr int kMxPairThreads = 64 + 32 * kMxEpiWarps;
 constexpr uint32_t kMxSlot = 2048;  // of an epilogue warp: 32 rows of 64 bytes
-constexpr int kMxPieceCols = 24;    // of tensor memory: A's two scale tiles, B's two of two
 
 struct MxPairCtrl {
     uint64_t full[kMxPairStages];
@@ -457,8 +461,10 @@ struct MxPairArgs {
 };
 
 // Tiles of 128 rows' scales that bn of B's rows lie in (tiles of 192 start in the
-// middle of one every other time).
-__host__ __device__ __forceinline__ int mx_b_tiles(int bn)
+// middle of one every other time).  Widths are multiples of 64: with 224, whose
+// scales start at an odd column of tensor memory every other time, the MMA ended in
+// a misaligned-address error.
+__host__ __device__ constexpr int mx_b_tiles(int bn)
 {
     return bn > 128 ? 2 : 1;
 }
@@ -695,73 +701,72 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             }
         }
     } else if (warp == 1 && rank == 0) {
-        // The whole warp walks the loop and one lane issues, without a branch: what
-        // lies past the end of K in the last stage is zeros, codes and scales.  (A
-        // test for each MMA made 4096 x 11264 x 11264 162 us instead of 133, without
-        // its epilogue.)
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, aphase = 0, set = 0;
+        // One lane walks and issues, without a branch: what lies past the end of K in
+        // the last stage is zeros, codes and scales.  Its turn takes 0.18 us, a stage's
+        // MMAs of 192 columns 0.20 (9.5 PFLOP/s), so every step of it counts: a test
+        // for each MMA made 4096 x 11264 x 11264 162 us instead of 133 without its
+        // epilogue, a walk of the whole warp 142.8 instead of 140.4 with it.
         const uint32_t sa = smem_u32(smem), sb = sa + kMxATile, ss = sb + half * (MK / 2);
         const uint64_t da0 = smem_desc_sw128(sa, 16, 1024), db0 = smem_desc_sw128(sb, 16, 1024);
         const uint64_t ds0 = smem_desc_rows16(ss);
         const uint32_t idesc = idesc_mxf4(2 * MM, uint32_t(bn), 0);
-        const uint32_t scales = tmem_base + 512 - 2 * kMxPieceCols;  // two sets
-        constexpr uint32_t kTile = kMxTileBytes >> 4;
-        const bool one = elect_one();
-        const auto walk = [&](auto wide) {  // more than 128 columns
-            bool ok = true;
-            for (int t = pair; ok && t < g.tiles; t += pairs) {
+        const auto walk = [&](auto count) {
+            constexpr uint32_t kB = decltype(count)::value;  // scale tiles of B
+            // of tensor memory, twice: A's two scale tiles, then B's two of kB
+            constexpr uint32_t kSet = 8 + 8 * kB, kTile = kMxTileBytes >> 4;
+            const uint32_t scales = tmem_base + 512 - 2 * kSet;
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, aphase = 0, set = 0;
+            for (int t = pair; t < g.tiles; t += pairs) {
                 place(t, m0, n0);
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag));
-                if (!ok)
-                    break;
+                if (!mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag))
+                    return;
                 const uint32_t d = tmem_base + uint32_t(buf * bn);
                 const uint32_t b_col = uint32_t(n0 % 128) / 32;
                 for (int kb = 0; kb < nk; ++kb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[stage], phase, abort_flag));
-                    if (!ok)
-                        break;
+                    if (!mbar_wait(&ctl.full[stage], phase, abort_flag))
+                        return;
                     tc_fence_after_sync();
-                    if (one) {
-                        const uint32_t off = uint32_t(stage) * (stage_bytes >> 4);
-                        const uint32_t at = scales + set;
-                        tc_copy_32x128b_pair(at, ds0 + off);
-                        tc_copy_32x128b_pair(at + 4, ds0 + (off + kTile));
-                        tc_copy_32x128b_pair(at + 8, ds0 + (off + 2 * kTile));
-                        tc_copy_32x128b_pair(at + 16, ds0 + (off + 3 * kTile));
-                        if constexpr (decltype(wide)::value) {
-                            tc_copy_32x128b_pair(at + 12, ds0 + (off + 4 * kTile));
-                            tc_copy_32x128b_pair(at + 20, ds0 + (off + 5 * kTile));
-                        }
-#pragma unroll
-                        for (uint32_t kk = 0; kk < 4; ++kk)
-                            tc_mma_mxf4_pair(d, da0 + (off + 2 * kk), db0 + (off + 2 * kk),
-                                             idesc | (kk & 1) << 5 | (kk & 1) << 30,
-                                             at + 4 * (kk >> 1), at + 8 + 8 * (kk >> 1) + b_col,
-                                             kb != 0 || kk != 0);
-                        tc_commit_pair(&ctl.empty[stage], 3);
-                    }
-                    __syncwarp();
-                    set ^= uint32_t(kMxPieceCols);
+                    const uint32_t off = uint32_t(stage) * (stage_bytes >> 4);
+                    uint64_t *const released = &ctl.empty[stage];
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    const uint32_t at = scales + set;
+                    set ^= kSet;
+                    tc_copy_32x128b_pair(at, smem_desc_at(ds0, off));
+                    tc_copy_32x128b_pair(at + 4, smem_desc_at(ds0, off + kTile));
+#pragma unroll
+                    for (uint32_t i = 0; i < kB; ++i) {
+                        tc_copy_32x128b_pair(at + 8 + 4 * i,
+                                             smem_desc_at(ds0, off + (2 + 2 * i) * kTile));
+                        tc_copy_32x128b_pair(at + 8 + 4 * (kB + i),
+                                             smem_desc_at(ds0, off + (3 + 2 * i) * kTile));
+                    }
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 4; ++kk)
+                        tc_mma_mxf4_pair(d, smem_desc_at(da0, off + 2 * kk),
+                                         smem_desc_at(db0, off + 2 * kk),
+                                         idesc | (kk & 1) << 5 | (kk & 1) << 30,
+                                         at + 4 * (kk >> 1), at + 8 + 4 * kB * (kk >> 1) + b_col,
+                                         kb != 0 || kk != 0);
+                    tc_commit_pair(released, 3);
                 }
-                if (ok && one)
-                    tc_commit_pair(&ctl.acc_full[buf], 3);
-                __syncwarp();
+                tc_commit_pair(&ctl.acc_full[buf], 3);
                 if (++buf == 2) {
                     buf = 0;
                     aphase ^= 1u;
                 }
             }
         };
-        if (bn > 128)
-            walk(std::true_type());
-        else
-            walk(std::false_type());
+        if (elect_one()) {
+            if (mx_b_tiles(bn) == 2)
+                walk(std::integral_constant<uint32_t, 2>());
+            else
+                walk(std::integral_constant<uint32_t, 1>());
+        }
+        __syncwarp();
         // (the epilogue warps of both CTAs wait for every accumulator, so the
         // MMAs are done when the cluster meets below)
     } else if (warp >= 2 && (warp - 2) >> 2 < bn / kMxEpiCols) {

@@ -1,10 +1,12 @@
 // Rows to MXFP4 and back (moe_quantize_rows_mxfp4, moe_dequantize_rows_mxfp4).
 // The format: mx_rows.cuh.
 //
-// Both are bound by memory.  Quantising, a thread has sixteen elements and eight
-// lanes a scale tile's 128 of one row (with eight elements a thread, twice the
-// lanes per block, instructions bound it: 4096 x 11264 bf16 31 us); reading back,
-// a thread has eight, whose 16 bytes of output then lie side by side.
+// 4096 x 11264 bf16 takes 22.9 us (117 MB, 5.1 TB/s) and back 23.3 (the same
+// bytes); what bounds them is memory, and instructions (67 % of the issue slots,
+// quantising).  Quantising, a thread has sixteen elements and eight lanes a scale
+// tile's 128 of one row (with eight elements a thread, twice the lanes per block,
+// instructions alone bound it: 31 us); reading back, a thread has eight, whose 16
+// bytes of output then lie side by side.
 #include "../../include/moe_prefill.h"
 #include "internal.h"
 #include "mx_rows.cuh"

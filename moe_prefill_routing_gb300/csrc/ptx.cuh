@@ -618,4 +618,11 @@ __device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr)
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (8ull << 32) | (1ull << 46);
 }
 
+// A shared-memory descriptor's `pieces` of 16 bytes further on (the address, in its
+// low word, does not carry out of its 14 bits).
+__device__ __forceinline__ uint64_t smem_desc_at(uint64_t desc, uint32_t pieces)
+{
+    return (desc & 0xffffffff00000000ull) | (static_cast<uint32_t>(desc) + pieces);
+}
+
 }  // namespace moe
