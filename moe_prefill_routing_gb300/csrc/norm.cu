@@ -160,58 +160,121 @@ __device__ __forceinline__ float gate_of(float g, bool some, int sigmoid)
     return !some ? 1.0f : sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
 }
 
-// Rows of a tensor of [rows, d].  RING: cp.async brings them ahead of their use
-// into slots of shared memory of the thread (fp32: the warp) that reads them, so
-// that what is in flight takes neither barriers nor registers (16-byte pieces are
-// aligned then, and d a multiple of 8).  Otherwise they are read when they are
-// used.  A tensor that is not there reads as zeros.
+// How a kernel reads rows.
+enum Mode {
+    kDirect,   // where they are used
+    kRing,     // ahead of their use; 16-byte pieces of rows are aligned, d a multiple of 8
+    kShifted,  // ahead of their use, rows that start and end anywhere
+};
+
+// Rows of a tensor of [rows, d].  In a ring, cp.async brings them ahead of their use
+// into slots of shared memory of the thread (fp32, kShifted: the warp) that reads
+// them, so that what is in flight takes neither barriers nor registers.  A tensor
+// that is not there reads as zeros.
 //
 // Eight fp32 are two 16-byte pieces; copied by the thread that uses them, every
 // instruction would touch half of each 32-byte sector of memory.  A warp copies
 // (and, through a slot that has been read, writes) neighbouring pieces with
 // neighbouring lanes instead: 32768 rows x 2816 of an fp32 stream 210 -> 185 us (169
 // with later changes).
-template <typename E, int R, bool RING>
+//
+// kShifted: what is brought are the aligned 16-byte pieces of memory that a row lies
+// in, one more to a warp than its elements fill, which the warp then shifts into
+// place; results leave through a slot, neighbouring words by neighbouring lanes.
+// (Element by element from the thread that uses them, 32768 x 2815 bf16 took 490 us
+// instead of 251, its gradients 1113 instead of 512; 1.9 and 2.3 times the aligned
+// 2816's, from the instructions of the way through the slots.)
+template <typename E, int R, int MODE>
 struct Rows {
     static constexpr int kPieces = sizeof(E) == 4 ? 2 : 1;  // of 16 bytes: eight elements
+    static constexpr int kWarp = 32 * kPieces + (MODE == kShifted);  // a warp's of a round
     const E *p;
     int64_t ld;
     int d, vec, G, t;  // G, t: the group's threads, and which this one is
-    uint4 *slots;      // [stage][R][G][kPieces], from the warp's first on
+    uint4 *slots;      // [stage][R][warps][kWarp], from the warp's first on
 
     __device__ __forceinline__ Rows(const void *tensor, int64_t ld_, int d_, int vec_,
                                     const Group &gr, uint8_t *&smem)
         : p(static_cast<const E *>(tensor)), ld(ld_), d(d_), vec(vec_), G(gr.size), t(gr.t),
-          slots(reinterpret_cast<uint4 *>(smem) + (gr.t & ~31) * kPieces)
+          slots(reinterpret_cast<uint4 *>(smem) + (gr.t >> 5) * kWarp)
     {
-        if (RING) {
-            smem += kNormStages * R * kPieces * G * 16;
+        if (MODE == kDirect)
+            return;
+        smem += kNormStages * R * gr.warps * kWarp * 16;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (!p || (t + r * G) * 8 >= d)  // never fetched
-                    for (int i = 0; i < kNormStages; ++i)
+        for (int r = 0; r < R; ++r)
+            for (int i = 0; i < kNormStages; ++i) {
+                if (MODE == kShifted) {
+                    for (int j = t & 31; !p && j < kWarp; j += 32)
+                        at(i, r)[j] = make_uint4(0, 0, 0, 0);
+                } else if (!p || (t + r * G) * 8 >= d) {  // never fetched
 #pragma unroll
-                        for (int q = 0; q < kPieces; ++q)
-                            *mine(i, r, q) = make_uint4(0, 0, 0, 0);
-            __syncwarp();
-        }
+                    for (int q = 0; q < kPieces; ++q)
+                        *mine(i, r, q) = make_uint4(0, 0, 0, 0);
+                }
+            }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ uint4 *at(int stage, int r) const
+    {
+        return slots + (stage * R + r) * (G >> 5) * kWarp;
     }
 
     // The thread's q-th piece (fp32: lanes 4 - 7 of eight take theirs in the other
     // order, which keeps eight lanes' banks apart).
     __device__ __forceinline__ uint4 *mine(int stage, int r, int q) const
     {
-        return slots + (stage * R + r) * G * kPieces + (t & 31) * kPieces +
-               (kPieces == 2 ? q ^ ((t >> 2) & 1) : 0);
+        return at(stage, r) + (t & 31) * kPieces + (kPieces == 2 ? q ^ ((t >> 2) & 1) : 0);
+    }
+
+    // The words of the warp's 256 elements, from the lane's first on.
+    __device__ __forceinline__ uint32_t *words(int stage, int r) const
+    {
+        return reinterpret_cast<uint32_t *>(at(stage, r)) + (t & 31);
+    }
+
+    // kShifted: a row's bytes before its first element in its first piece.
+    __device__ __forceinline__ int shift(int64_t row) const
+    {
+        return int(reinterpret_cast<uintptr_t>(p + row * ld) & 15);
     }
 
     __device__ __forceinline__ void fetch(int64_t row, int stage) const
     {
-        if (!RING || !p)
+        if (MODE == kDirect || !p)
             return;
-        if (kPieces == 2)
+        if (MODE == kShifted || kPieces == 2)
             __syncwarp();  // the slot's last row has been read by every lane
-        const int w = (t & ~31) * kPieces + (t & 31);
+        const int lane = t & 31, w = (t & ~31) * kPieces + lane;
+        if (MODE == kShifted) {
+            const int before = shift(row), total = before + d * int(sizeof(E));
+            const uint8_t *const from = reinterpret_cast<const uint8_t *>(p + row * ld) - before;
+            // (nothing before the tensor is read)
+            const int early = int(max(reinterpret_cast<const uint8_t *>(p) - from, ptrdiff_t(0)));
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int q = 0; q <= kPieces; ++q) {
+                    const int c = (w + 32 * q + r * G * kPieces) * 16;  // of the row's bytes
+                    const int n = min(max(total - c, 0), 16);           // those past it: zeros
+                    uint4 *const to = at(stage, r) + 32 * q + lane;
+                    if (q == kPieces && lane)
+                        continue;
+                    if (early && c == 0) {
+                        *to = make_uint4(0, 0, 0, 0);
+                        for (int b = early; b < n; b += int(sizeof(E)))
+                            reinterpret_cast<E *>(to)[b / int(sizeof(E))] =
+                                reinterpret_cast<const E *>(from)[b / int(sizeof(E))];
+                    } else {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         smem_u32(to)),
+                                     "l"(n ? from + c : from + 16), "r"(n)
+                                     : "memory");
+                    }
+                }
+            return;
+        }
         const uint4 *from = reinterpret_cast<const uint4 *>(p + row * ld) + w;
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -219,23 +282,74 @@ struct Rows {
             for (int q = 0; q < kPieces; ++q)
                 if ((w + 32 * q + r * G * kPieces) * (8 / kPieces) < d)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     smem_u32(slots + (stage * R + r) * G * kPieces + 32 * q +
-                                              (t & 31))),
+                                     smem_u32(at(stage, r) + 32 * q + lane)),
                                  "l"(from + r * G * kPieces + 32 * q)
                                  : "memory");
     }
 
-    // After async_wait.
+    // kShifted, after async_wait and a barrier of the warp: the row's elements to
+    // where `mine` finds them.
+    __device__ __forceinline__ void settle(int64_t row, int stage) const
+    {
+        if (MODE != kShifted || !p)
+            return;
+        const int before = shift(row);
+        if (!before)
+            return;
+        if (kPieces == 1) {
+            uint32_t w[R][8];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint4 a = mine(stage, r, 0)[0], b = mine(stage, r, 0)[1];
+                w[r][0] = a.x, w[r][1] = a.y, w[r][2] = a.z, w[r][3] = a.w;
+                w[r][4] = b.x, w[r][5] = b.y, w[r][6] = b.z, w[r][7] = b.w;
+            }
+            __syncwarp();
+            if (before & 8) {
+#pragma unroll
+                for (int i = 0; i < R * 6; ++i)
+                    w[i / 6][i % 6] = w[i / 6][i % 6 + 2];
+            }
+            if (before & 4) {
+#pragma unroll
+                for (int i = 0; i < R * 5; ++i)
+                    w[i / 5][i % 5] = w[i / 5][i % 5 + 1];
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[r][i] = __funnelshift_r(w[r][i], w[r][i + 1], (before & 2) * 8);
+                *mine(stage, r, 0) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
+            }
+        } else {
+            uint32_t w[R][8];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[r][i] = words(stage, r)[32 * i + (before >> 2)];
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    words(stage, r)[32 * i] = w[r][i];
+            __syncwarp();
+        }
+    }
+
+    // After async_wait (and settle).
     __device__ __forceinline__ Oct<E> read(int64_t row, int stage, int r) const
     {
         const int c = (t + r * G) * 8;
         Oct<E> o;
-        if (RING && kPieces == 2) {
+        if (MODE != kDirect && kPieces == 2) {
             const uint4 a = *mine(stage, r, 0), b = *mine(stage, r, 1);
             const bool other = (t >> 2) & 1;
             o.set(0, other ? b : a);
             o.set(kPieces - 1, other ? a : b);
-        } else if (RING) {
+        } else if (MODE != kDirect) {
             o.set(0, *mine(stage, r, 0));
         } else {
             o.load(p + (p ? row * ld + c : 0), p ? d - c : 0, vec);
@@ -243,30 +357,60 @@ struct Rows {
         return o;
     }
 
-    // The thread's eight elements of a row of another tensor of [rows, d]; fp32
-    // through slots whose row has been read.
+    // The thread's eight elements of a row of another tensor of [rows, d]; fp32 and
+    // kShifted through slots whose row has been read.
     __device__ __forceinline__ void put(void *to, int64_t to_ld, int64_t row, int stage, int r,
                                         int to_vec, const Oct<E> &o) const
     {
-        const int c = (t + r * G) * 8;
+        const int lane = t & 31, c = (t + r * G) * 8;
         E *out = static_cast<E *>(to) + row * to_ld;
-        if (RING && kPieces == 2) {
-            __syncwarp();
-            if (c < d) {
-                const bool other = (t >> 2) & 1;
-                const uint4 a = o.get(0), b = o.get(kPieces - 1);
-                *mine(stage, r, 0) = other ? b : a;
+        if (MODE == kDirect || (MODE == kRing && kPieces == 1)) {
+            if (MODE == kDirect || c < d)
+                o.store(out + c, MODE == kRing ? 8 : d - c, MODE == kRing || to_vec);
+            return;
+        }
+        __syncwarp();
+        if (MODE == kShifted || c < d) {
+            const bool other = kPieces == 2 && ((t >> 2) & 1);
+            const uint4 a = o.get(0), b = o.get(kPieces - 1);
+            *mine(stage, r, 0) = other ? b : a;
+            if (kPieces == 2)
                 *mine(stage, r, 1) = other ? a : b;
-            }
-            __syncwarp();
-            const int w = (t & ~31) * kPieces + (t & 31) + r * G * kPieces;
+        }
+        __syncwarp();
+        if (MODE == kRing) {
+            const int w = (t & ~31) * kPieces + lane + r * G * kPieces;
 #pragma unroll
             for (int q = 0; q < kPieces; ++q)
                 if ((w + 32 * q) * 4 < d)
-                    reinterpret_cast<uint4 *>(out)[w + 32 * q] =
-                        slots[(stage * R + r) * G * kPieces + 32 * q + (t & 31)];
-        } else if (!RING || c < d) {
-            o.store(out + c, RING ? 8 : d - c, RING || to_vec);
+                    reinterpret_cast<uint4 *>(out)[w + 32 * q] = at(stage, r)[32 * q + lane];
+            return;
+        }
+        const int n = min(d - (c - lane * 8), 256);  // of the warp's elements
+        if (kPieces == 2) {
+            uint32_t *const first = reinterpret_cast<uint32_t *>(out) + (c - lane * 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (lane + 32 * i < n)
+                    first[lane + 32 * i] = words(stage, r)[32 * i];
+        } else {
+            // words where they are aligned: from the second element on where the first
+            // one lies in the upper half of a word
+            uint16_t *const first = reinterpret_cast<uint16_t *>(out) + (c - lane * 8);
+            const int odd = int(reinterpret_cast<uintptr_t>(first) >> 1 & 1);
+            const uint32_t *const a = words(stage, r);
+            if (odd && lane == 0 && n > 0)
+                first[0] = uint16_t(a[0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = 2 * (lane + 32 * i) + odd;
+                const uint32_t v =
+                    odd ? __funnelshift_r(a[32 * i], a[32 * i + 1], 16) : a[32 * i];
+                if (e + 1 < n)
+                    *reinterpret_cast<uint32_t *>(first + e) = v;
+                else if (e < n)
+                    first[e] = uint16_t(v);
+            }
         }
     }
 };
@@ -274,26 +418,26 @@ struct Rows {
 // A thread's part of a row that is looked at more than once: read from a ring's
 // slot each time (registers are what limits the rows that an SM works on), kept
 // in registers without one.
-template <typename E, int R, bool RING>
+template <typename E, int R, int MODE>
 struct Part {
-    const Rows<E, R, RING> &rows;
-    Oct<E> kept[RING ? 1 : R];
+    const Rows<E, R, MODE> &rows;
+    Oct<E> kept[MODE == kDirect ? R : 1];
 
-    __device__ __forceinline__ Part(const Rows<E, R, RING> &rows_, int64_t row) : rows(rows_)
+    __device__ __forceinline__ Part(const Rows<E, R, MODE> &rows_, int64_t row) : rows(rows_)
     {
-        if (!RING) {
+        if (MODE == kDirect) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                kept[RING ? 0 : r] = rows.read(row, 0, r);
+                kept[MODE == kDirect ? r : 0] = rows.read(row, 0, r);
         }
     }
 
     __device__ __forceinline__ void get(int stage, int r, Two (&v)[4]) const
     {
-        if (RING)
-            rows.read(0, stage, r).to(v);
+        if (MODE == kDirect)
+            kept[MODE == kDirect ? r : 0].to(v);
         else
-            kept[RING ? 0 : r].to(v);
+            rows.read(0, stage, r).to(v);
     }
 };
 
@@ -357,7 +501,7 @@ __device__ __forceinline__ void async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(1) : "memory");
 }
 
-template <typename S, typename B, int R, bool RING>
+template <typename S, typename B, int R, int MODE>
 __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 128)
     k_block_norm(const NormArgs p)
 {
@@ -368,8 +512,8 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
     const int G = gr.size;
     const float inv_d = 1.0f / float(p.d);
     uint8_t *smem = smem_raw + gr.id * p.ring_bytes;  // a ring for each group, then the weights
-    const Rows<S, R, RING> xs(p.x, p.ldx, p.d, p.vec_x, gr, smem);
-    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
+    const Rows<S, R, MODE> xs(p.x, p.ldx, p.d, p.vec_x, gr, smem);
+    const Rows<B, R, MODE> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t rows = p.codes ? (int64_t(p.T) + 127) / 128 * 128 : p.T;
@@ -407,13 +551,15 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
         const float g = gate_of(gate, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
-        if (RING && (sizeof(S) == 4 || sizeof(B) == 4))
+        if (MODE == kShifted || (MODE == kRing && (sizeof(S) == 4 || sizeof(B) == 4)))
             __syncwarp();  // other lanes' copies
         Two v[R][4];
         if (live) {
-            const Part<S, R, RING> x(xs, t);
+            xs.settle(t, out);
+            os.settle(t, out);
+            const Part<S, R, MODE> x(xs, t);
             if (p.o) {
-                const Part<B, R, RING> o(os, t);
+                const Part<B, R, MODE> o(os, t);
                 float k = g;
                 if (p.post_norm) {
                     Two squares = 0;
@@ -503,7 +649,7 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
     }
 }
 
-template <typename S, typename B, int R, bool RING>
+template <typename S, typename B, int R, int MODE>
 __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradArgs p)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -513,12 +659,12 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     const int G = gr.size;
     const float inv_d = 1.0f / float(p.d);
     uint8_t *smem = smem_raw + gr.id * p.ring_bytes;  // a ring for each group, then the weights
-    const Rows<S, R, RING> xns(p.dh ? p.xn : nullptr, p.ldxn, p.d, p.vec_xn, gr, smem);
-    const Rows<S, R, RING> dxns(p.dxn, p.lddxn, p.d, p.vec_dxn, gr, smem);
-    const Rows<B, R, RING> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
-    const Rows<B, R, RING> dhs(p.dh, p.lddh, p.d, p.vec_dh, gr, smem);
+    const Rows<S, R, MODE> xns(p.dh ? p.xn : nullptr, p.ldxn, p.d, p.vec_xn, gr, smem);
+    const Rows<S, R, MODE> dxns(p.dxn, p.lddxn, p.d, p.vec_dxn, gr, smem);
+    const Rows<B, R, MODE> os(p.o, p.ldo, p.d, p.vec_o, gr, smem);
+    const Rows<B, R, MODE> dhs(p.dh, p.lddh, p.d, p.vec_dh, gr, smem);
     // (the slots of a tensor that is not there stay zeros)
-    const Rows<S, R, RING> &spare = p.dxn ? dxns : xns;
+    const Rows<S, R, MODE> &spare = p.dxn ? dxns : xns;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t step = int64_t(gridDim.x) * gr.count;
@@ -557,11 +703,15 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
         const float g = gate_of(gate, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
-        if (RING && (sizeof(S) == 4 || sizeof(B) == 4))
+        if (MODE == kShifted || (MODE == kRing && (sizeof(S) == 4 || sizeof(B) == 4)))
             __syncwarp();  // other lanes' copies
         if (live) {
-            const Part<S, R, RING> xn(xns, t), dxn(dxns, t);
-            const Part<B, R, RING> dh(dhs, t), o(os, t);
+            xns.settle(t, out);
+            dxns.settle(t, out);
+            os.settle(t, out);
+            dhs.settle(t, out);
+            const Part<S, R, MODE> xn(xns, t), dxn(dxns, t);
+            const Part<B, R, MODE> dh(dhs, t), o(os, t);
             // of the means and of q, whose dS is made of three terms, all at once
             Two xx = 0, ax = 0, oo = 0, dq = 0, aq = 0, xq = 0;
 #pragma unroll
@@ -743,7 +893,7 @@ constexpr size_t kNormSmem = 200 * 1024;  // the most dynamic shared memory of a
 // How a launch lays rows out.
 struct Shape {
     int warps, r, groups;  // of a row; rounds of eight elements a thread; rows side by side
-    bool ring;
+    int mode;
     size_t ring_bytes, smem;  // of a group, of a CTA
 
     int threads() const { return 32 * warps * groups; }
@@ -752,21 +902,32 @@ struct Shape {
 // A thread has eight elements of rows that a warp can hold so, else 16 (its share
 // of a row's sums and addresses costs about as much as eight elements do), or
 // 32 past 8192; eight too where the rows do not go round the SMs, and only a
-// row's time counts.  `whole`: rows up to a multiple of 128; `bytes`: of a row's
-// element in all tensors that are read; `sums`: column sums are kept.
-Shape norm_shape(int64_t rows, int d, bool whole, bool vec, int bytes, bool sums)
+// row's time counts, and where rows that are not aligned would leave an SM one CTA
+// (gradients of 32768 x 2815 fp32 864 -> 654 us, of 16384 x 4095 with an fp32 stream
+// 484 -> 385; aligned ones, whose CTAs wait less, are faster with 16: 32768 x 2816
+// with an fp32 stream 257 us, 460 with eight).  `whole`: rows up to a multiple of
+// 128; `bytes`: of a row's element in all `tensors` that are read; `sums`: column
+// sums are kept.
+Shape norm_shape(int64_t rows, int d, bool whole, bool vec, int tensors, int bytes, bool sums)
 {
     const int chunks = whole ? mx_k_tiles(d) * 16 : (d + 7) / 8;
     Shape s;
-    s.r = chunks <= (rows > device_sm_count() ? 32 : kNormMaxThreads) ? 1
-          : chunks <= 2 * kNormMaxThreads                             ? 2
-                                                                      : 4;
-    s.warps = ((chunks + s.r - 1) / s.r + 31) / 32;
-    s.groups = std::max(1, 8 / s.warps);
-    const size_t weights = s.r > 1 ? size_t(4) * s.r * 32 * s.warps * 16 : 0;
-    s.ring_bytes = size_t(kNormStages) * s.r * 8 * bytes * 32 * s.warps;
-    s.ring = vec && s.r <= 2 && s.groups * s.ring_bytes + weights <= kNormSmem;
-    if (!s.ring)
+    size_t weights = 0;
+    const auto lay = [&](int r) {
+        s.r = r;
+        s.warps = ((chunks + r - 1) / r + 31) / 32;
+        s.groups = std::max(1, 8 / s.warps);
+        weights = r > 1 ? size_t(4) * r * 32 * s.warps * 16 : 0;
+        s.ring_bytes = size_t(kNormStages) * r * s.warps * (32 * 8 * bytes + (vec ? 0 : tensors) * 16);
+        s.smem = s.groups * s.ring_bytes + weights;
+    };
+    lay(chunks <= (rows > device_sm_count() ? 32 : kNormMaxThreads) ? 1
+        : chunks <= 2 * kNormMaxThreads                             ? 2
+                                                                    : 4);
+    if (!vec && chunks <= kNormMaxThreads && s.smem > kNormSmem / 2)
+        lay(1);
+    s.mode = s.r > 2 || s.smem > kNormSmem ? kDirect : vec ? kRing : kShifted;
+    if (s.mode == kDirect)
         s.ring_bytes = 0;
     if (sums && s.groups > 1)  // the groups' sums pass through the rings' memory
         s.ring_bytes = std::max(s.ring_bytes, size_t(2) * s.r * 8 * 32 * s.warps * 4);
@@ -774,20 +935,25 @@ Shape norm_shape(int64_t rows, int d, bool whole, bool vec, int bytes, bool sums
     return s;
 }
 
-// f(S, B, R, RING) of the types, the rounds and whether a ring can be used.
-template <typename F>
-cudaError_t with_types(int s, int b, int r, bool ring, F f)
+// f(S, B, R, MODE) of the types, the rounds and how rows are read.  One round always
+// fits a ring, and so do two of 8 bytes an element or fewer (`wide`: of more).
+template <bool WIDE, typename F>
+cudaError_t with_types(int s, int b, int r, int mode, F f)
 {
     const auto with_r = [&](auto sv, auto bv) {
         using S = decltype(sv);
         using B = decltype(bv);
-        using Yes = std::true_type;
-        using No = std::false_type;
-        return r == 1   ? ring ? f(S(), B(), std::integral_constant<int, 1>(), Yes())
-                               : f(S(), B(), std::integral_constant<int, 1>(), No())
-               : r == 2 ? ring ? f(S(), B(), std::integral_constant<int, 2>(), Yes())
-                               : f(S(), B(), std::integral_constant<int, 2>(), No())
-                        : f(S(), B(), std::integral_constant<int, 4>(), No());
+        const auto with_mode = [&](auto rv) {
+            if constexpr (WIDE && sizeof(S) == 4 && decltype(rv)::value == 2)
+                if (mode == kDirect)
+                    return f(S(), B(), rv, std::integral_constant<int, kDirect>());
+            return mode == kRing ? f(S(), B(), rv, std::integral_constant<int, kRing>())
+                                 : f(S(), B(), rv, std::integral_constant<int, kShifted>());
+        };
+        return r == 1   ? with_mode(std::integral_constant<int, 1>())
+               : r == 2 ? with_mode(std::integral_constant<int, 2>())
+                        : f(S(), B(), std::integral_constant<int, 4>(),
+                            std::integral_constant<int, kDirect>());
     };
     if (s == MOE_DT_BF16)
         return with_r(__nv_bfloat16(), __nv_bfloat16());
@@ -876,11 +1042,11 @@ extern "C" int moe_block_norm(const void *x, int64_t ldx, int x_dtype, const voi
     a.vec_xn = rows_vec(xn, ldxn, xs), a.vec_h = rows_vec(h, ldh, bs);
     a.alpha = alpha, a.eps = eps;
     const bool vec = d % 8 == 0 && a.vec_x && (!o || (a.vec_o && a.vec_xn)) && (!h || a.vec_h);
-    const Shape sh = norm_shape(T, d, codes != nullptr, vec, xs + bs, false);
+    const Shape sh = norm_shape(T, d, codes != nullptr, vec, 2, xs + bs, false);
     const int64_t rows = codes ? (int64_t(T) + 127) / 128 * 128 : T;
     int ctas = 0;
     const cudaError_t e =
-        with_types(x_dtype, b_dtype, sh.r, sh.ring, [&](auto s, auto b, auto r, auto g) {
+        with_types<false>(x_dtype, b_dtype, sh.r, sh.mode, [&](auto s, auto b, auto r, auto g) {
             constexpr auto kern =
                 k_block_norm<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
             return launch_norm<kern>(a, sh, rows, INT_MAX, ctas,
@@ -945,10 +1111,10 @@ extern "C" int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, co
     a.alpha = o ? alpha : 1.0f, a.eps = eps;
     const bool vec = d % 8 == 0 && (!dh || (a.vec_xn && a.vec_dh)) && (!dxn || a.vec_dxn) &&
                      a.vec_dx && (!o || (a.vec_o && a.vec_do));
-    const Shape sh = norm_shape(T, d, false, vec, 2 * (xs + bs), sums);
+    const Shape sh = norm_shape(T, d, false, vec, 4, 2 * (xs + bs), sums);
     int ctas = 0;
     cudaError_t e =
-        with_types(x_dtype, b_dtype, sh.r, sh.ring, [&](auto s, auto b, auto r, auto g) {
+        with_types<true>(x_dtype, b_dtype, sh.r, sh.mode, [&](auto s, auto b, auto r, auto g) {
             constexpr auto kern =
                 k_block_norm_grad<decltype(s), decltype(b), decltype(r)::value, decltype(g)::value>;
             return launch_norm<kern>(a, sh, T, kNormGradCtas, ctas, stm);

@@ -200,6 +200,38 @@ def test_rows_that_start_anywhere(S, Bt, d):
             assert (t._base[:, :at] == 3).all()
 
 
+@pytest.mark.parametrize("S,Bt", TYPES)
+@pytest.mark.parametrize("T,d", [(40, 1), (40, 3), (33, 5), (20, 13), (9, 255), (200, 263), (7, 1030),
+                                 (300, 2815), (3, 4097)])
+def test_rows_without_a_gap_at_any_offset(S, Bt, T, d):
+    """Rows of odd length one behind the other, in the middle of memory that holds NaN, at every
+    element's offset into 16 bytes: a value from beside a row would show."""
+    def at(t, i):
+        big = torch.full((T * d + 40,), float("nan"), dtype=t.dtype, device="cuda")
+        v = big[8 + i:8 + i + T * d].view(T, d)
+        v.copy_(t)
+        return v
+
+    v = _inputs(T, d, S, Bt, mask=T > 30)
+    rest = {n: v[n] for n in ("pre", "post", "gate", "mask")}
+    gx, gh = _rand(7, T, d).to("cuda", S), _rand(8, T, d).to("cuda", Bt)
+    for i in range(16 // torch.finfo(Bt).bits * 8 if d < 300 else 1, 0, -1):
+        j, k = (3 * i) % 8, (5 * i + 1) % 8
+        x, o, xn, h = at(v["x"], i), at(v["o"], j), at(v["x"], k), at(v["o"], i)
+        r = _check({**rest, "x": x, "o": o}, gate_act="sigmoid", alpha=0.5, xn=xn, h=h)
+        dx, do = at(v["x"], j), at(v["o"], k)
+        got = B.block_norm_grad(xn, o, dxn=at(gx, k), dh=at(gh, j), gate_act="sigmoid", alpha=0.5,
+                                dx=dx, do=do, **rest)
+        ref, size = D.grads(_f64(r["xn"]), _f64(o), _f64(gx), _f64(gh), _f64(v["pre"]),
+                            _f64(v["post"]), _f64(v["gate"]), _f64(v["mask"]), gate_act="sigmoid",
+                            alpha=0.5)
+        for n in ref:
+            _within(got[n], ref[n], 2.0 ** -16 * size[n], n)
+        for t in (xn, h, dx, do):
+            left = t._base.isnan()
+            assert left.sum() == 40 and not t.isnan().any()
+
+
 def test_no_rows():
     v = _inputs(0, 64, BF, BF)
     r = B.block_norm(**v, mxfp4=True)
