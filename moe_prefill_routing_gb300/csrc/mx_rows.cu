@@ -1,12 +1,12 @@
 // Rows to MXFP4 and back (moe_quantize_rows_mxfp4, moe_dequantize_rows_mxfp4).
 // The format: mx_rows.cuh.
 //
-// 4096 x 11264 bf16 takes 22.9 us (117 MB, 5.1 TB/s) and back 23.3 (the same
-// bytes); what bounds them is memory, and instructions (67 % of the issue slots,
-// quantising).  Quantising, a thread has sixteen elements and eight lanes a scale
-// tile's 128 of one row (with eight elements a thread, twice the lanes per block,
-// instructions alone bound it: 31 us); reading back, a thread has eight, whose 16
-// bytes of output then lie side by side.
+// 4096 x 11264 bf16 takes 22.2 us (117 MB, 5.3 TB/s) and back 23.0, 8192 x 16384
+// 59 either way.  What bounds them is memory (to write zeros to the 92 MB takes 23.3
+// us, to the 268 MB 66.7) and, quantising, instructions (67 % of the issue slots):
+// there a thread has sixteen elements and eight lanes a scale tile's 128 of one row
+// (with eight elements a thread, twice the lanes per block, 31 us).  Reading back, a
+// thread has eight, whose 16 bytes of output then lie side by side.
 #include "../../include/moe_prefill.h"
 #include "internal.h"
 #include "mx_rows.cuh"
@@ -21,7 +21,9 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kQuantLanes = 8, kReadLanes = 16;  // of 128 elements
 constexpr int kQuantAhead = 2, kReadAhead = 4;   // pieces of 128 a thread has in flight
-constexpr int kRowCtas = 8;                      // an SM
+// CTAs an SM at most (quantising 4096 x 11264 and 8192 x 16384: 22.2 and 59.1 us; 8
+// CTAs 23.1 and 61.2, 32 CTAs 23.3 and 57.6).
+constexpr int kRowCtas = 16;
 
 struct MxRowsArgs {
     const void *x;  // rows to quantise, or null
