@@ -1,8 +1,8 @@
 // Rows to MXFP4 and back (moe_quantize_rows_mxfp4, moe_dequantize_rows_mxfp4).
 // The format: mx_rows.cuh.
 //
-// 4096 x 11264 bf16 takes 22.2 us (117 MB, 5.3 TB/s) and back 23.0, 8192 x 16384
-// 59 either way.  What bounds them is memory (to write zeros to the 92 MB takes 23.3
+// 4096 x 11264 bf16 takes 21.3 us (117 MB, 5.5 TB/s) and back 22.2, 8192 x 16384
+// 58 and 59.  What bounds them is memory (to write zeros to the 92 MB takes 23.3
 // us, to the 268 MB 66.7) and, quantising, instructions (67 % of the issue slots):
 // there a thread has sixteen elements and eight lanes a scale tile's 128 of one row
 // (with eight elements a thread, twice the lanes per block, 31 us).  Reading back, a
@@ -21,9 +21,10 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kQuantLanes = 8, kReadLanes = 16;  // of 128 elements
 constexpr int kQuantAhead = 2, kReadAhead = 4;   // pieces of 128 a thread has in flight
-// CTAs an SM at most (quantising 4096 x 11264 and 8192 x 16384: 22.2 and 59.1 us; 8
-// CTAs 23.1 and 61.2, 32 CTAs 23.3 and 57.6).
-constexpr int kRowCtas = 16;
+// CTAs that an SM holds; twice as many are launched where each of their threads has
+// a full turn of pieces (quantising 4096 x 11264 21.3 us, with 8 an SM 22.5, with 16
+// 22.0; 2048 x 2560 3.4 us, with 10 an SM 5.0).
+constexpr int kRowCtas = 5;
 
 struct MxRowsArgs {
     const void *x;  // rows to quantise, or null
@@ -137,13 +138,15 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArg
     }
 }
 
-// `lanes` of a piece of 128 elements.
-cudaError_t launch(void (*kern)(MxRowsArgs), const MxRowsArgs &a, int64_t rows, int lanes,
+// `lanes` of a piece of 128 elements, `ahead` of which a thread has in flight.
+cudaError_t launch(void (*kern)(MxRowsArgs), const MxRowsArgs &a, int64_t rows, int lanes, int ahead,
                    cudaStream_t s)
 {
     const int64_t pieces = rows * a.k_tiles, of_cta = kRowThreads / lanes;
-    const int64_t ctas = std::min<int64_t>((pieces + of_cta - 1) / of_cta,
-                                           int64_t(device_sm_count()) * kRowCtas);
+    const int64_t held = int64_t(device_sm_count()) * kRowCtas;
+    const auto ctas_of = [&](int64_t n) { return (pieces + n - 1) / n; };
+    const int64_t ctas =
+        std::min(ctas_of(of_cta), std::clamp(ctas_of(of_cta * ahead), held, 2 * held));
     return launch_pdl(kern, dim3(unsigned(ctas)), dim3(kRowThreads), 0, s, a);
 }
 
@@ -189,7 +192,8 @@ extern "C" int moe_quantize_rows_mxfp4(const void *x, int64_t ldx, int dtype, in
     const auto kern = dtype == MOE_DT_F32   ? k_quant_rows<float>
                       : dtype == MOE_DT_F16 ? k_quant_rows<__half>
                                             : k_quant_rows<__nv_bfloat16>;
-    return launch(kern, a, a.all_rows, kQuantLanes, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch(kern, a, a.all_rows, kQuantLanes, kQuantAhead,
+                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -211,7 +215,8 @@ extern "C" int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *sc
     a.K = K, a.k_tiles = mx_k_tiles(K);
     a.vec = rows_vec(y, ldy, dtype_size(dtype));
     const auto kern = dtype == MOE_DT_F32 ? k_dequant_rows<float> : k_dequant_rows<__nv_bfloat16>;
-    return launch(kern, a, rows, kReadLanes, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch(kern, a, rows, kReadLanes, kReadAhead, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
