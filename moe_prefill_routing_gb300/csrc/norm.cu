@@ -926,7 +926,12 @@ Shape norm_shape(int64_t rows, int d, bool whole, bool vec, int tensors, int byt
                                                                     : 4);
     if (!vec && chunks <= kNormMaxThreads && s.smem > kNormSmem / 2)
         lay(1);
-    s.mode = s.r > 2 || s.smem > kNormSmem ? kDirect : vec ? kRing : kShifted;
+    // (rows that are not aligned gain nothing from the way through the slots where
+    // they fill half a warp, and two tensors' loads are few: norm of 100000 x 101 bf16
+    // 56 us, kShifted 73; of 50000 x 191 50 and 38)
+    s.mode = s.r > 2 || s.smem > kNormSmem || (!vec && tensors == 2 && chunks <= 16) ? kDirect
+             : vec                                                                  ? kRing
+                                                                                    : kShifted;
     if (s.mode == kDirect)
         s.ring_bytes = 0;
     if (sums && s.groups > 1)  // the groups' sums pass through the rings' memory
@@ -935,16 +940,18 @@ Shape norm_shape(int64_t rows, int d, bool whole, bool vec, int tensors, int byt
     return s;
 }
 
-// f(S, B, R, MODE) of the types, the rounds and how rows are read.  One round always
-// fits a ring, and so do two of 8 bytes an element or fewer (`wide`: of more).
-template <bool WIDE, typename F>
+// f(S, B, R, MODE) of the types, the rounds and how rows are read.  Of the gradient's
+// four tensors one round always goes through a ring, and two do unless they have
+// more than 8 bytes an element; of the norm's two, two rounds always do.
+template <bool GRAD, typename F>
 cudaError_t with_types(int s, int b, int r, int mode, F f)
 {
     const auto with_r = [&](auto sv, auto bv) {
         using S = decltype(sv);
         using B = decltype(bv);
         const auto with_mode = [&](auto rv) {
-            if constexpr (WIDE && sizeof(S) == 4 && decltype(rv)::value == 2)
+            if constexpr (GRAD ? sizeof(S) == 4 && decltype(rv)::value == 2
+                               : decltype(rv)::value == 1)
                 if (mode == kDirect)
                     return f(S(), B(), rv, std::integral_constant<int, kDirect>());
             return mode == kRing ? f(S(), B(), rv, std::integral_constant<int, kRing>())
