@@ -429,18 +429,18 @@ __global__ void __launch_bounds__(kMxThreads)
 // 64 of K: each CTA loads its 128 rows of A and half the rows of B, the scales of
 // its own rows of A and those of all rows of B.  Pairs walk the tiles
 // (persistent); two accumulators let the epilogue warps work on one tile while
-// the MMAs fill the other.  192 columns are the most: two accumulators of 256
-// would leave no tensor memory for the scales.
+// the MMAs fill the other.
 //
 // A stage's round trip, from its release to its next data's arrival, takes 1.14 us
 // however little is loaded, so it is spread over many stages (192 columns: six; 4096
-// x 11264 x 11264 217, 175, 151 and 142 us with three to six).  With six, what
-// bounds a long reduction are the MMAs of 64 of K (140 us, 7.4 PFLOP/s; 116 without
-// loads and epilogue, 126 without the epilogue), a short one the loads and stores:
-// 4096 x 2816 x 11264 51 us (5.1 PFLOP/s), 45 without MMAs, 39 without stores.
+// x 11264 x 11264 217, 175, 151 and 142 us with three to six).  What bounds a long
+// reduction are that and the MMAs of 64 of K (137 us with 256 columns and five stages,
+// 7.6 PFLOP/s; with 192 140, 126 without the epilogue, 116 without loads either), a
+// short one the loads and stores: 4096 x 2816 x 11264 46.4 us (5.6 PFLOP/s); with 192
+// columns 51, 45 without MMAs, 39 without stores.
 constexpr int kMxPairStages = 8;  // at most
 constexpr int kMxEpiCols = 64;    // of an epilogue warp (32 rows), all in registers at once
-constexpr int kMxEpiWarps = 12;   // at most: 192 columns
+constexpr int kMxEpiWarps = 12;   // at most: 192 columns (256 go round)
 constexpr int kMxPairThreads = 64 + 32 * kMxEpiWarps;
 constexpr uint32_t kMxSlot = 2048;  // of an epilogue warp: 32 rows of 64 bytes
 
@@ -449,6 +449,7 @@ struct MxPairCtrl {
     uint64_t empty[kMxPairStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
+    uint64_t shared_read[2];  // the columns that the other accumulator shares
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -467,6 +468,16 @@ struct MxPairArgs {
 __host__ __device__ constexpr int mx_b_tiles(int bn)
 {
     return bn > 128 ? 2 : 1;
+}
+
+// Columns between the two accumulators.  Two of 256 and the scales do not fit the
+// 512 columns: they share 48, the first one's last, which the epilogue takes out
+// first.
+constexpr int kMxAccStep = 208;
+
+__host__ __device__ constexpr int mx_acc_step(int bn)
+{
+    return bn < kMxAccStep ? bn : kMxAccStep;
 }
 
 // What one CTA loads per stage.
@@ -600,7 +611,8 @@ struct MxBlock {
     }
 };
 
-template <int ACT, typename E>
+// WIDE: tiles of 256 columns.
+template <int ACT, typename E, bool WIDE>
 __global__ void __launch_bounds__(kMxPairThreads, 1)
     k_linear_mx_pair(const __grid_constant__ MxPairArgs g)
 {
@@ -613,7 +625,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int bn = p.bn, half = bn / 2, S = g.stages;
+    const int bn = WIDE ? 256 : p.bn, half = bn / 2, S = g.stages;
     const uint32_t stage_bytes = g.stage_bytes;
     uint8_t *stg = smem + S * stage_bytes;
     volatile int *abort_flag = &ctl.abort_flag;
@@ -626,6 +638,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl.acc_full[b], 1);
             mbar_init(&ctl.acc_empty[b], 2 * 4 * (bn / kMxEpiCols));  // both CTAs' warps
+            mbar_init(&ctl.shared_read[b], 2 * 4);
         }
         ctl.abort_flag = 0;
         fence_mbar_init();
@@ -721,7 +734,12 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                 place(t, m0, n0);
                 if (!mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag))
                     return;
-                const uint32_t d = tmem_base + uint32_t(buf * bn);
+                // the other accumulator's shared columns: it was filled a tile ago
+                if (WIDE && t != pair &&
+                    !mbar_wait(&ctl.shared_read[buf ^ 1], buf ? aphase : aphase ^ 1u, abort_flag))
+                    return;
+                tc_fence_after_sync();
+                const uint32_t d = tmem_base + uint32_t(buf * mx_acc_step(bn));
                 const uint32_t b_col = uint32_t(n0 % 128) / 32;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(&ctl.full[stage], phase, abort_flag))
@@ -769,7 +787,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         __syncwarp();
         // (the epilogue warps of both CTAs wait for every accumulator, so the
         // MMAs are done when the cluster meets below)
-    } else if (warp >= 2 && (warp - 2) >> 2 < bn / kMxEpiCols) {
+    } else if (warp >= 2 && (warp - 2) >> 2 < bn / kMxEpiCols) {  // (12 warps at most)
         // A warp takes its 64 columns into registers at once and gives the
         // accumulator back; then block after block: bias, activation, residual, one
         // slot of shared memory, one TMA store.  (With 16 columns at a time and the
@@ -780,16 +798,20 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         uint8_t *slot = stg + uint32_t(warp - 2) * kMxSlot;
         float *bias = reinterpret_cast<float *>(stg + kMxEpiWarps * kMxSlot) +
                       (warp - 2) * kMxEpiCols;
-        const uint32_t lanes =
-            tmem_base + (uint32_t(q * 32) << 16) + uint32_t(part * kMxEpiCols);
+        const uint32_t lanes = tmem_base + (uint32_t(q * 32) << 16);
         const bool any_res = p.residual, vec_res = p.vec_res;
-        int buf = 0;
+        // WIDE: four parts for the three warps of a quadrant, whose roles go round: the
+        // one that has had the longest rest takes the shared columns (0), the next but
+        // one (2) two parts.
+        int buf = 0, role = (part + 2) % 3;
         uint32_t aphase = 0;
-        for (int t = pair; t < g.tiles; t += pairs) {
+        bool more = false;  // the second of two parts
+        for (int t = pair; t < g.tiles;) {
             place(t, m0, n0);
+            const int c0 = (WIDE ? (role + more + (buf ? 0 : 3)) & 3 : part) * kMxEpiCols;
             const int64_t row = int64_t(m0) + q * 32;
             const int rows = int(min(int64_t(32), p.M - row));
-            const int col = n0 + part * kMxEpiCols, width = min(kMxEpiCols, p.N - col);
+            const int col = n0 + c0, width = min(kMxEpiCols, p.N - col);
             const E *res = static_cast<const E *>(p.residual) + (any_res ? row * p.ldr + col : 0);
             E *out = static_cast<E *>(p.out) + row * p.ldo + col;
             uint4 ahead[4] = {};
@@ -806,16 +828,25 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                 break;
             tc_fence_after_sync();
             uint32_t r0[32], r1[32];
-            tmem_ld_32x32b_x32(lanes + uint32_t(buf * bn), r0);
-            tmem_ld_32x32b_x32(lanes + uint32_t(buf * bn) + 32, r1);
+            const uint32_t from = lanes + uint32_t(buf * mx_acc_step(bn) + c0);
+            tmem_ld_32x32b_x32(from, r0);
+            tmem_ld_32x32b_x32(from + 32, r1);
             tmem_ld_wait();
-            tc_fence_before_sync();  // this accumulator has been read
+            tc_fence_before_sync();  // these columns have been read
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive_cluster_relaxed(dsmem_addr(&ctl.acc_empty[buf], 0));
-            if (++buf == 2) {
-                buf = 0;
-                aphase ^= 1u;
+                if (WIDE && role == 0)
+                    mbar_arrive_cluster_relaxed(dsmem_addr(&ctl.shared_read[buf], 0));
+            }
+            more = WIDE && role == 2 && !more;
+            if (!more) {
+                t += pairs;
+                role = role ? role - 1 : 2;
+                if (++buf == 2) {
+                    buf = 0;
+                    aphase ^= 1u;
+                }
             }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
@@ -886,27 +917,28 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
 
 using MxPairKernel = void (*)(MxPairArgs);
 
-template <int ACT>
+template <int ACT, bool WIDE>
 MxPairKernel mx_pair_kernel(bool f32, bool f16)
 {
-    return f32   ? k_linear_mx_pair<ACT, float>
-           : f16 ? k_linear_mx_pair<ACT, __half>
-                 : k_linear_mx_pair<ACT, __nv_bfloat16>;
+    return f32   ? k_linear_mx_pair<ACT, float, WIDE>
+           : f16 ? k_linear_mx_pair<ACT, __half, WIDE>
+                 : k_linear_mx_pair<ACT, __nv_bfloat16, WIDE>;
 }
 
+template <bool WIDE>
 MxPairKernel mx_pair_kernel(int act, bool f32, bool f16)
 {
     switch (act) {
     case MOE_ACT_RELU:
-        return mx_pair_kernel<MOE_ACT_RELU>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_RELU, WIDE>(f32, f16);
     case MOE_ACT_SILU:
-        return mx_pair_kernel<MOE_ACT_SILU>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_SILU, WIDE>(f32, f16);
     case MOE_ACT_GELU:
-        return mx_pair_kernel<MOE_ACT_GELU>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_GELU, WIDE>(f32, f16);
     case MOE_ACT_GELU_TANH:
-        return mx_pair_kernel<MOE_ACT_GELU_TANH>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_GELU_TANH, WIDE>(f32, f16);
     default:
-        return mx_pair_kernel<MOE_ACT_NONE>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_NONE, WIDE>(f32, f16);
     }
 }
 
@@ -1050,21 +1082,26 @@ cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
 }
 
 // Columns of a tile of k_linear_mx_pair: those with the least estimated time, in
-// cycles, from times at 64 ... 192.  (One round of 40 stages takes 11.7, 11.8 and
-// 12.3 us with 64, 128 and 192, 4096 x 10240 x 2560 in 9, 5 and 3 rounds 79, 48 and
-// 35; of two stages, which the epilogue bounds, 4096 x 512 x 2560 13.0, 10.0 and 8.6.)
+// cycles, of a round of tiles and of the last tile's epilogue, by times at 64 ... 256.
+// (4096 x 10240 x 2560 in 9, 5, 3 and 3 rounds 79, 48, 34 and 42 us, x 512 x 2560 13.0,
+// 10.0, 9.0 and 9.8; with 192 and 256 columns 4096 x 2816 x 11264 51.2 and 47.8, x 11264
+// x 11264 141 and 138, 8192 x 4096 x 4096 48.7 and 44.7.)
 int mx_pair_columns(const MxProduct &q, int pairs)
 {
+    constexpr struct {
+        int bn;
+        double round, stage;
+    } kTimes[] = {{256, 2260, 540}, {192, 1800, 435}, {128, 1320, 390}, {64, 1050, 376}};
     const int nk = (q.K + MK - 1) / MK;
+    const double part = (q.epi.residual ? 3500 : 1000) * (q.epi.out_f32 ? 2 : 1);
     int best = 0;
     double least = 0.0;
-    for (int bn : {192, 128, 64}) {
-        const int64_t tiles = ((int64_t(q.T) + 255) / 256) * ((int64_t(q.N) + bn - 1) / bn);
-        const double main = nk * (370.0 + 0.65 * bn), epi = 1300.0 + 12.5 * bn;
-        const double c =
-            double((tiles + pairs - 1) / pairs) * std::max(main, epi) + std::min(main, epi);
+    for (const auto &w : kTimes) {
+        const int64_t tiles = ((int64_t(q.T) + 255) / 256) * ((int64_t(q.N) + w.bn - 1) / w.bn);
+        const double c = double((tiles + pairs - 1) / pairs) * (w.round + nk * w.stage) +
+                         part * (w.bn > 192 ? 2 : 1);
         if (!best || c < least) {
-            best = bn;
+            best = w.bn;
             least = c;
         }
     }
@@ -1097,10 +1134,13 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
         e = mx_scale_map(&g.b_scales, q.W_scales, q.N, q.K, mx_b_tiles(a.bn));
     if (e == cudaSuccess && a.vec_out)
         e = mx_out_map(&g.out, a);
+    const bool wide = a.bn == 256;
     const void *kern =
-        reinterpret_cast<const void *>(mx_pair_kernel(a.act, a.out_f32, a.f16));
+        reinterpret_cast<const void *>(wide ? mx_pair_kernel<true>(a.act, a.out_f32, a.f16)
+                                            : mx_pair_kernel<false>(a.act, a.out_f32, a.f16));
     if (e == cudaSuccess)
-        e = ensure_smem_limit(kern, kSlotLinearMxPair + 3 * a.act + (a.out_f32 ? 2 : a.f16),
+        e = ensure_smem_limit(kern,
+                              kSlotLinearMxPair + 6 * a.act + 3 * wide + (a.out_f32 ? 2 : a.f16),
                               kMxLoneSmem);
     if (e != cudaSuccess)
         return e;

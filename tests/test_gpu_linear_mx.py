@@ -98,6 +98,18 @@ def test_many_rows(T, K, N, out):
     _check(T, K, N, out=out, pad=8 if N % 8 == 0 else 3)
 
 
+@pytest.mark.parametrize("out", [BF, F16, F32])
+@pytest.mark.parametrize("act", ["none", "gelu_tanh"])
+def test_wide_tiles_several_a_pair(out, act):
+    """Three rounds of tiles of 256 columns: accumulators that share columns, in turn."""
+    _check(2049, 512, 5900, act=act, out=out, res=False)
+
+
+@pytest.mark.parametrize("K,out,pad", [(2560, BF, 8), (2560, F16, 3), (11264, F32, 0), (11264, F32, 1)])
+def test_wide_tiles_with_a_residual(K, out, pad):
+    _check(1000, K, 4850, out=out, pad=pad)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T", [5, 40, 300])
 @pytest.mark.parametrize("out", [BF, F16, F32])
