@@ -131,6 +131,29 @@ def test_mxfp4_rows_of_h(d, S, Bt):
     _check(_inputs(7, d, S, Bt, o=False, mask=True), mxfp4=True, h_dtype=Bt)
 
 
+@pytest.mark.parametrize("S,Bt", TYPES)
+@pytest.mark.parametrize("T,d", [(50, 96), (50, 416), (200, 2592), (3, 8224)])
+def test_mxfp4_rows_of_h_from_unaligned_rows(T, d, S, Bt):
+    _check(_inputs(T, d, S, Bt, mask=True, pad=3), gate_act="sigmoid", alpha=0.5, mxfp4=True)
+    v = _inputs(T, d, S, Bt, o=False, pad=1)
+    _check(v, mxfp4=True)
+
+
+def test_in_place_on_unaligned_rows():
+    for S, T, d in ((BF, 400, 263), (F32, 300, 1001), (F16, 50, 99)):
+        v = _inputs(T, d, S, S, mask=True, gate=False, pad=2)
+        want = _check(v)
+        gx, gh = _wide(_rand(5, T, d), 1, S), _wide(_rand(6, T, d), 4, S)
+        how = {n: v[n] for n in ("pre", "post", "mask")}
+        ref = B.block_norm_grad(want["xn"], v["o"], dxn=gx, dh=gh, **how)
+        x, o = v["x"].clone(), v["o"].clone()
+        r = B.block_norm(**{**v, "x": x}, xn=x)
+        assert r["xn"] is x and torch.equal(x, want["xn"]) and torch.equal(r["h"], want["h"])
+        got = B.block_norm_grad(want["xn"], o, dxn=gx, dh=gh, **how, dx=gx, do=o)
+        for n in ref:
+            assert torch.equal(got[n], ref[n]), n
+
+
 def test_rows_of_zeros_and_of_one_value():
     v = _inputs(6, 512, BF, BF)
     v["x"][0] = 0
