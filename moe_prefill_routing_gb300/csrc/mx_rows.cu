@@ -1,7 +1,7 @@
 // Rows to MXFP4 and back (moe_quantize_rows_mxfp4, moe_dequantize_rows_mxfp4).
 // The format: mx_rows.cuh.
 //
-// 4096 x 11264 bf16 takes 21.3 us (117 MB, 5.5 TB/s) and back 22.2, 8192 x 16384
+// 4096 x 11264 bf16 takes 21.3 us (117 MB, 5.5 TB/s) and back 21.7, 8192 x 16384
 // 58 and 59.  What bounds them is memory (to write zeros to the 92 MB takes 23.3
 // us, to the 268 MB 66.7) and, quantising, instructions (67 % of the issue slots):
 // there a thread has sixteen elements and eight lanes a scale tile's 128 of one row
@@ -98,9 +98,50 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_quant_rows(const MxRowsArgs 
     }
 }
 
+// 128 elements of a row, eight from each of 16 lanes (of `mask`), n of which exist:
+// through `slot`, neighbouring words by neighbouring lanes.  For 16-bit rows that are
+// not aligned (element by element, 4096 x 11264 took 131 us instead of 34) and fp32
+// ones, whose 16-byte pieces would fill half a sector an instruction (48 instead of 39).
 template <typename E>
+__device__ __forceinline__ void put_piece(E *to, int n, const Oct<E> &o, uint32_t *slot,
+                                          uint32_t mask)
+{
+    const int lane = threadIdx.x % kReadLanes;
+    __syncwarp(mask);  // the slot has been read
+#pragma unroll
+    for (int i = 0; i < Oct<E>::kWords / 4; ++i)
+        reinterpret_cast<uint4 *>(slot)[lane * (Oct<E>::kWords / 4) + i] = o.get(i);
+    __syncwarp(mask);
+    if constexpr (sizeof(E) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane + 16 * i < n)
+                reinterpret_cast<uint32_t *>(to)[lane + 16 * i] = slot[lane + 16 * i];
+    } else {
+        // from the second element on where the first lies in the upper half of a word
+        uint16_t *const first = reinterpret_cast<uint16_t *>(to);
+        const int odd = int(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+        if (odd && lane == 0)
+            first[0] = uint16_t(slot[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int w = lane + 16 * i, e = 2 * w + odd;
+            const uint32_t v = odd ? __funnelshift_r(slot[w], slot[w + 1], 16) : slot[w];
+            if (e + 1 < n)
+                *reinterpret_cast<uint32_t *>(first + e) = v;
+            else if (e < n)
+                first[e] = uint16_t(v);
+        }
+    }
+}
+
+template <typename E, bool VEC>
 __global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArgs p)
 {
+    constexpr int kSlot = VEC ? 4 : kReadLanes * Oct<E>::kWords + 4;  // of a piece, and a word more
+    __shared__ __align__(16) uint32_t slots[kRowThreads / kReadLanes * kSlot];
+    uint32_t *const slot = slots + threadIdx.x / kReadLanes * kSlot;
+    const uint32_t mask = 0xffffu << (threadIdx.x & 16);
     constexpr int kPieces = kRowThreads / kReadLanes;
     const int lane = threadIdx.x % kReadLanes;
     const int64_t step = int64_t(gridDim.x) * kPieces;
@@ -127,13 +168,17 @@ __global__ void __launch_bounds__(kRowThreads, 4) k_dequant_rows(const MxRowsArg
 #pragma unroll
         for (int u = 0; u < kReadAhead; ++u) {
             const int c = of[u].kt * 128 + lane * 8;
-            if (of[u].row >= p.rows || c >= p.K)
+            if (of[u].row >= p.rows || (VEC && c >= p.K))
                 continue;
             float v[8];
             mx_decode8(code[u], (word[u] >> (8 * (lane >> 2))) & 0xffu, v);
             Oct<E> out;
             out.from(v);
-            out.store(static_cast<E *>(p.y) + of[u].row * p.ld + c, p.K - c, p.vec);
+            E *const y = static_cast<E *>(p.y) + of[u].row * p.ld;
+            if (VEC)
+                out.store(y + c, 8, true);
+            else
+                put_piece(y + of[u].kt * 128, min(p.K - of[u].kt * 128, 128), out, slot, mask);
         }
     }
 }
@@ -214,7 +259,9 @@ extern "C" int moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *sc
     a.rows = a.all_rows = rows;
     a.K = K, a.k_tiles = mx_k_tiles(K);
     a.vec = rows_vec(y, ldy, dtype_size(dtype));
-    const auto kern = dtype == MOE_DT_F32 ? k_dequant_rows<float> : k_dequant_rows<__nv_bfloat16>;
+    const auto kern = dtype == MOE_DT_F32 ? k_dequant_rows<float, false>
+                      : a.vec             ? k_dequant_rows<__nv_bfloat16, true>
+                                          : k_dequant_rows<__nv_bfloat16, false>;
     return launch(kern, a, rows, kReadLanes, kReadAhead, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? MOE_OK

@@ -66,6 +66,20 @@ def test_rows_that_start_anywhere(dtype):
         assert (y[:, :at] == 5).all() and (y[:, at + 320:] == 5).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R,K", [(1, 32), (5, 96), (130, 160), (33, 2816), (700, 4128)])
+def test_read_back_at_any_offset(R, K, dtype):
+    q = _check(_rows(4, R, K, BF, spread=1.0))
+    want = B.dequantize_rows_mxfp4(q, dtype)
+    for at, pad in ((1, 0), (0, 1), (3, 4), (2, 0)):
+        big = torch.full((R * (K + pad) + 16,), 5.0, dtype=dtype, device="cuda")
+        y = big[at:at + R * (K + pad)].view(R, K + pad)[:, :K]
+        B.dequantize_rows_mxfp4(q, y=y)
+        assert torch.equal(y, want)
+        y.fill_(5.0)
+        assert (big == 5).all()
+
+
 def test_every_tie_and_its_neighbours():
     points = torch.tensor([0.0, 0.25, 0.5, 0.75, 1.0, 1.25, 1.5, 1.75, 2.0, 2.5, 3.0, 3.5, 4.0, 5.0,
                            6.0, 7.0])
