@@ -1083,9 +1083,9 @@ cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
 
 // Columns of a tile of k_linear_mx_pair: those with the least estimated time, in
 // cycles, of a round of tiles and of the last tile's epilogue, by times at 64 ... 256.
-// (4096 x 10240 x 2560 in 9, 5, 3 and 3 rounds 79, 48, 34 and 42 us, x 512 x 2560 13.0,
-// 10.0, 9.0 and 9.8; with 192 and 256 columns 4096 x 2816 x 11264 51.2 and 47.8, x 11264
-// x 11264 141 and 138, 8192 x 4096 x 4096 48.7 and 44.7.)
+// (4096 x 10240 x 2560 in 9, 5, 3 and 3 rounds 76, 46, 34 and 41 us, x 512 x 2560 12.5,
+// 9.5, 8.4 and 9.1; with 192 and 256 columns 4096 x 2816 x 11264 50.9 and 46.4, x 11264
+// x 11264 141 and 137, 8192 x 4096 x 4096 48.4 and 44.0.)
 int mx_pair_columns(const MxProduct &q, int pairs)
 {
     constexpr struct {
