@@ -671,7 +671,8 @@ MOE_API int moe_route_grad(const void *logits, int64_t ld, int l_dtype, const ui
  *
  * g is gate[t], 1 / (1 + e^-gate[t]) with MOE_GATE_SIGMOID, or 1 without gate;
  * weights that are NULL (post) are 1.  Sums are fp32, so rows with values past
- * about 3e18, whose squares leave its range, are not normalised.  Without o,
+ * about 3e18, whose squares leave its range, are not normalised, and with an eps
+ * below 1e-36 those of rows below about 1e-17 lose digits.  Without o,
  * xn is x itself (alpha is not looked at): h alone is written.
  * in   x         x_dtype [T, d]  the residual stream, rows ldx elements apart
  * in   o         b_dtype [T, d]  the block's output, rows ldo apart, or NULL (then
@@ -711,7 +712,9 @@ MOE_API int moe_block_norm(const void *x, int64_t ldx, int x_dtype, const void *
  * ws             moe_block_norm_grad_workspace_bytes(T, d) bytes, 256-byte aligned;
  *                may be NULL without dpre and dpost
  * Rows with mask 0 are not read; their dx, do and dgate are 0.  All sums fp32 in
- * a fixed order on one device: deterministic.  With T = 0 dpre and dpost are 0.
+ * a fixed order on one device: deterministic.  Values in moe_block_norm's range, and
+ * products of them (o times post among them) and of a gradient in fp32's.  With
+ * T = 0 dpre and dpost are 0.
  */
 MOE_API size_t moe_block_norm_grad_workspace_bytes(int T, int d);
 MOE_API int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, const void *o,

@@ -4,16 +4,19 @@
 // Per row, with r(v) = (mean(v^2) + eps)^-1/2:
 //   xn = alpha x + g r(o) (o . post),   h = xn r(xn) . pre
 // and from dxn and dh, with a = dh . pre, r1 = r(o), r2 = r(xn):
-//   dS = dxn + r2 a - c2 xn,   c2 = r2^3 mean(a . xn)
-//   dx = alpha dS,   q = sum(dS . post . o),   dg = r1 q
-//   do = g r1 dS . post - r1^2 (g r1 q / d) o
+//   dS = dxn + r2 (a - c2 r2 xn),   c2 = r2 mean(a . xn)
+//   dx = alpha dS,   q = mean(dS . post . o),   dg = d r1 q
+//   do = g r1 dS . post - r1^2 q (g r1 o)
 //   dpost = sum over rows of g r1 dS . o,   dpre = sum over rows of r2 dh . xn
+// in which r1 and r2 multiply one value each time and never one another: r2^3 of a row
+// around 2^45 is subnormal, of one around 2^-43 infinite.
 //
 // Each tensor crosses memory once: a group of warps takes a row at a time, a thread
 // eight neighbouring elements of it (1, 2 or 4 times), kept in registers or its
 // slots between the sums, while the next row is on its way.  All sums are fp32 in a
 // fixed order; a thread's part of a mean is divided by d before the parts are
-// added, so that it does not overflow sooner than a thread's 8 to 32 squares do.
+// added, so that it does not overflow sooner than a thread's 8 to 32 squares (or
+// products) do.
 //
 // 32768 rows x 2816: bf16 125 us (738 MB, 5.9 TB/s), with MXFP4 rows 167, an fp32
 // stream 169 (6.55 TB/s); gradients 218 (1.1 GB, 5.1 TB/s) and, of an fp32 stream,
@@ -712,7 +715,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
             dhs.settle(t, out);
             const Part<S, R, MODE> xn(xns, t), dxn(dxns, t);
             const Part<B, R, MODE> dh(dhs, t), o(os, t);
-            // of the means and of q, whose dS is made of three terms, all at once
+            // the means (q's dS is made of three terms) all at once
             Two xx = 0, ax = 0, oo = 0, dq = 0, aq = 0, xq = 0;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -735,15 +738,15 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
                 }
             }
             float s[8] = {sum_of(xx) * inv_d, sum_of(ax) * inv_d, sum_of(oo) * inv_d,
-                          sum_of(dq), sum_of(aq), sum_of(xq)};
+                          sum_of(dq) * inv_d, sum_of(aq) * inv_d, sum_of(xq) * inv_d};
             sum.eight<6>(s);
             const float r2 = p.dh ? rsqrtf(s[0] + p.eps) : 0.0f;
             const float r1 = p.post_norm ? rsqrtf(s[2] + p.eps) : 1.0f;
-            const float c2 = r2 * r2 * r2 * s[1];
-            const float q = s[3] + r2 * s[4] - c2 * s[5];
+            const float c2 = r2 * s[1];
+            const float q = s[3] + r2 * (s[4] - c2 * (r2 * s[5]));
             if (p.dgate && gr.t == 0)
-                p.dgate[t] = r1 * q * (p.sigmoid ? g * (1.0f - g) : 1.0f);
-            const float k = g * r1, c1 = p.post_norm ? r1 * r1 * (k * (q * inv_d)) : 0.0f;
+                p.dgate[t] = r1 * q * float(p.d) * (p.sigmoid ? g * (1.0f - g) : 1.0f);
+            const float k = g * r1, c1 = p.post_norm ? r1 * (r1 * q) : 0.0f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 Two x[4], h[4], f[4], d[4], w[4], v[4];
@@ -755,11 +758,12 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
                 post.get(r, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    dpre[r][i] = fma(h[i], mul(x[i], both(r2)), dpre[r][i]);
-                    d[i] = fma(both(r2), mul(h[i], w[i]), fma(both(-c2), x[i], d[i]));
-                    const Two e = mul(both(k), d[i]);
-                    dpost[r][i] = fma(e, f[i], dpost[r][i]);
-                    f[i] = fma(e, v[i], mul(both(-c1), f[i]));
+                    x[i] = mul(x[i], both(r2));
+                    f[i] = mul(f[i], both(k));
+                    dpre[r][i] = fma(h[i], x[i], dpre[r][i]);
+                    d[i] = fma(both(r2), fma(both(-c2), x[i], mul(h[i], w[i])), d[i]);
+                    dpost[r][i] = fma(d[i], f[i], dpost[r][i]);
+                    f[i] = fma(both(k), mul(d[i], v[i]), mul(both(-c1), f[i]));
                     d[i] = mul(both(p.alpha), d[i]);
                 }
                 Oct<S> dx;
