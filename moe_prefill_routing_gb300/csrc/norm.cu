@@ -163,6 +163,12 @@ __device__ __forceinline__ float gate_of(float g, bool some, int sigmoid)
     return !some ? 1.0f : sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
 }
 
+// Its slope: of a sigmoid s(g) s(-g), as 1 - s(g) has no digits left past g = 17.
+__device__ __forceinline__ float gate_slope(float g, int sigmoid)
+{
+    return sigmoid ? 1.0f / ((1.0f + expf(-g)) * (1.0f + expf(g))) : 1.0f;
+}
+
 // How a kernel reads rows.
 enum Mode {
     kDirect,   // where they are used
@@ -703,7 +709,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
     for (int64_t t = first; t < p.T; t += step) {
         fetch(next);
         const uint32_t coming = is_live(ahead);
-        const float g = gate_of(gate, p.gate, p.sigmoid);
+        const float raw = gate, g = gate_of(raw, p.gate, p.sigmoid);
         gate = p.gate && t + step < p.T ? p.gate[t + step] : 0.0f;
         async_wait();
         if (MODE == kShifted || (MODE == kRing && (sizeof(S) == 4 || sizeof(B) == 4)))
@@ -745,7 +751,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
             const float c2 = r2 * s[1];
             const float q = s[3] + r2 * (s[4] - c2 * (r2 * s[5]));
             if (p.dgate && gr.t == 0)
-                p.dgate[t] = r1 * q * float(p.d) * (p.sigmoid ? g * (1.0f - g) : 1.0f);
+                p.dgate[t] = r1 * q * float(p.d) * gate_slope(raw, p.sigmoid);
             const float k = g * r1, c1 = p.post_norm ? r1 * (r1 * q) : 0.0f;
 #pragma unroll
             for (int r = 0; r < R; ++r) {

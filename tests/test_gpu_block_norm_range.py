@@ -1,4 +1,5 @@
-"""Gradients of moe_block_norm where its values are large or small.
+"""Gradients of moe_block_norm where its values are large or small, or a gate
+is far from 0.
 
 Bounds as in test_gpu_block_norm.py, of which these are further cases: 2^-16 of the
 magnitudes that a value is made of.  Rows are scaled by a power of two that leaves
@@ -64,3 +65,22 @@ def test_gradients_of_large_rows_of_one_sign():
         g = torch.Generator().manual_seed(20 + i)
         v[n] = (2.0 ** 59 * (1 + 3 * torch.rand(4, 2560, generator=g))).cuda()
     _check(v, _rand(91, 4, 2560).cuda(), alpha=1.0)
+
+
+@pytest.mark.parametrize("S,Bt", [(BF, BF), (F32, F32)])
+@pytest.mark.parametrize("d", [64, 2560])
+def test_gradient_of_a_sigmoid_far_from_its_middle(S, Bt, d):
+    """Its slope is 1/(1 + e^-g) 1/(1 + e^g), each within 2^-21 of itself."""
+    at = torch.tensor([-80.0, -30, -17, -9, -4, -1, 0, 1, 4, 9, 17, 30, 80])
+    v = _inputs(len(at), d, S, Bt)
+    v["gate"] = at.cuda()
+    r = B.block_norm(**v, gate_act="sigmoid")
+    gx = _rand(92, len(at), d).to("cuda", S)
+    how = {n: v[n] for n in ("o", "post", "gate")}
+    got = B.block_norm_grad(r["xn"], dxn=gx, gate_act="sigmoid", **how)["dgate"]
+    # a plain gate's gradient, times the slope
+    ref, size = D.grads(_f64(r["xn"]), _f64(v["o"]), _f64(gx), None, None, _f64(v["post"]),
+                        np.ones(len(at)))
+    g = at.double().numpy()
+    slope = 1 / (1 + np.exp(-g)) / (1 + np.exp(g))
+    _within(got, ref["dgate"] * slope, (2.0 ** -16 + 2.0 ** -20) * size["dgate"] * slope, "dgate")
