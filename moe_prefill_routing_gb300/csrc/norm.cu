@@ -642,7 +642,9 @@ __global__ void __maxnreg__(R == 1 ? 64 : R == 2 ? (sizeof(S) == 4 ? 80 : 88) : 
                 if (p.codes) {
                     float f[8];
                     h.to(f);  // codes of h as it is stored
-                    const uint32_t byte = mx_scale_byte(max_of_lanes<4>(h.max_bits()));
+                    // (0 past the row's end, where a norm of NaN makes NaN of zeros too)
+                    const uint32_t top = max_of_lanes<4>(h.max_bits());
+                    const uint32_t byte = c < p.d ? mx_scale_byte(top) : 0u;
                     const uint32_t word = word_of_tile<4>(byte);
                     if (t < p.T && c < p.d)
                         *reinterpret_cast<uint32_t *>(p.codes + t * (p.d / 2) + c / 2) =
