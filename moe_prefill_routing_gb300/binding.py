@@ -997,10 +997,16 @@ def dequantize_rows_mxfp4(q: Mxfp4Rows, dtype=torch.bfloat16, y=None):
     return y
 
 
-@functools.lru_cache(maxsize=1024)
 def linear_rows_mxfp4_workspace_bytes(T: int, K: int, N: int) -> int:
-    """Of ``linear_mxfp4`` for rows that it quantises: 0 for a few of them."""
+    """Of ``linear_mxfp4`` for rows that it quantises, on the current device: 0 for
+    a few of them."""
     return int((_lib or lib()).moe_linear_rows_mxfp4_workspace_bytes(T, K, N))
+
+
+@functools.lru_cache(maxsize=1024)
+def _rows_workspace(device: int, T: int, K: int, N: int) -> int:
+    """The same, kept: ``device`` is the current one, whose SMs the answer goes by."""
+    return linear_rows_mxfp4_workspace_bytes(T, K, N)
 
 
 def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", out_dtype=None,
@@ -1052,7 +1058,7 @@ def linear_mxfp4(x, W: Mxfp4Rows, bias=None, residual=None, act: str = "none", o
         if ws is not None:
             qp, ws_bytes = _ws(ws, dev)
         else:
-            ws_bytes = linear_rows_mxfp4_workspace_bytes(T, K, N)
+            ws_bytes = _rows_workspace(dev.index, T, K, N)
             if ws_bytes:
                 ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
                 qp = ws.data_ptr()
