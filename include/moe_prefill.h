@@ -793,6 +793,16 @@ MOE_API int moe_selftest_linear_wait_limit(const void *x, const void *W, int T, 
                                            moe_stream_t stream);
 
 /*
+ * moe_selftest_linear_mxfp4_wait_limit -- the same of moe_linear_mxfp4 (contiguous
+ * y, no epilogue) or, without x_scales, of moe_linear_rows_mxfp4 for bf16 rows that
+ * need no workspace.  cta even where pairs of CTAs take the call.  For tests only.
+ */
+MOE_API int moe_selftest_linear_mxfp4_wait_limit(const void *x, const uint8_t *x_scales,
+                                                 const uint8_t *W, const uint8_t *W_scales, int T,
+                                                 int K, int N, void *y, int y_dtype,
+                                                 uint32_t *status, int cta, moe_stream_t stream);
+
+/*
  * moe_selftest_linear_plan -- the launches that moe_linear (what = 1) or the
  * products of moe_linear_grad (2: dx, 4: dW, 6: both; + 8: dy is fp32 as is
  * dW) would take on a GPU of `sms` SMs: plan[0] their number, plan[1] the most

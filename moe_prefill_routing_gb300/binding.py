@@ -155,6 +155,9 @@ _SIGS = {
     "moe_take_status": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "moe_selftest_linear_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                                  C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
+    "moe_selftest_linear_mxfp4_wait_limit": (
+        C.c_int, [C.c_void_p] * 4 + [C.c_int] * 3 + [C.c_void_p, C.c_int, C.c_void_p, C.c_int,
+                                                     C.c_void_p]),
     "moe_selftest_linear_plan": (C.c_int, [C.c_int] * 6 + [C.POINTER(C.c_int64)]),
     "moe_read_status": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
     "moe_selftest_wait_limit": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
@@ -1247,6 +1250,23 @@ def selftest_linear_wait_limit(x, W, cta: int = 0, status=None):
         rc = lib().moe_selftest_linear_wait_limit(_ptr(x), _ptr(W), T, K, N, _ptr(y), _ptr(status),
                                                   cta, _stream(x.device))
     _check("moe_selftest_linear_wait_limit", rc)
+    return y
+
+
+def selftest_linear_mxfp4_wait_limit(x, W: Mxfp4Rows, cta: int = 0, out_dtype=torch.bfloat16,
+                                     status=None):
+    """The same of ``linear_mxfp4(x, W)``; x ``Mxfp4Rows``, or a few bfloat16 rows."""
+    T, K = x.shape
+    N = W.shape[0]
+    dev = W.codes.device
+    xp, xsp = _mx(x, "x", (T, K), dev) if isinstance(x, Mxfp4Rows) else (
+        _flat(x, "x", (T, K), (torch.bfloat16,), dev), None)
+    y = torch.zeros((T, N), dtype=out_dtype, device=dev)
+    with torch.cuda.device(dev):
+        rc = lib().moe_selftest_linear_mxfp4_wait_limit(
+            xp, xsp, *_mx(W, "W", (N, K), dev), T, K, N, _ptr(y), _DTYPES[out_dtype], _ptr(status),
+            cta, _stream(dev))
+    _check("moe_selftest_linear_mxfp4_wait_limit", rc)
     return y
 
 

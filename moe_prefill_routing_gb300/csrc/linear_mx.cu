@@ -45,6 +45,7 @@ struct MxArgs : EpiArgs {
     int M, N, K, k_tiles;
     int bn, stages, split, n_mt;
     int chain;
+    int stall;  // self-test: CTA stall - 1's first stage waits for 16 bytes
     // QUANT kernels: x as it is, its type (MOE_DT_*) and whether 16-byte accesses
     // are aligned
     const void *rows;
@@ -172,6 +173,8 @@ __global__ void __launch_bounds__(kMxThreads)
         if (QUANT)
             for (int s = 0; s < kMxQuantStages; ++s)
                 mbar_init(&ctl.rows_full[s], 4);  // the accumulator warps
+        if (p.stall == int(blockIdx.x) + 1)
+            mbar_expect_tx(&ctl.full[0], 16);
         ctl.abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.a);
@@ -640,6 +643,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             mbar_init(&ctl.acc_empty[b], 2 * 4 * (bn / kMxEpiCols));  // both CTAs' warps
             mbar_init(&ctl.shared_read[b], 2 * 4);
         }
+        if (p.stall == int(blockIdx.x) + 1)
+            mbar_expect_tx(&ctl.full[0], 16);
         ctl.abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&g.a);
@@ -1008,6 +1013,7 @@ struct MxProduct {
     const void *rows;
     int64_t ld;
     int type;
+    int stall;  // MxArgs::stall
 };
 
 constexpr size_t kMxLoneSmem = 226 * 1024;  // of a CTA that takes all of an SM's tensor memory
@@ -1050,7 +1056,7 @@ cudaError_t launch_mx_small(const MxProduct &q, cudaStream_t s)
     a.rows = q.rows, a.ld = q.ld, a.type = q.type;
     a.vec = quant && rows_vec(q.rows, q.ld, dtype_size(q.type));
     a.M = q.N, a.N = q.T, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
-    a.chain = mx_chain(a.out_f32, a.f16);
+    a.chain = mx_chain(a.out_f32, a.f16), a.stall = q.stall;
     a.bn = l.bn, a.n_mt = l.n_mt, a.split = l.split;
     if (l.tiles * a.split > INT_MAX)
         return cudaErrorInvalidValue;
@@ -1114,7 +1120,7 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
     MxPairArgs g = {};
     MxArgs &a = g.p;
     static_cast<EpiArgs &>(a) = q.epi;
-    a.status = q.status;
+    a.status = q.status, a.stall = q.stall;
     a.M = q.T, a.N = q.N, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
     a.bn = mx_pair_columns(q, pairs);
     a.n_mt = int((int64_t(q.T) + 2 * MM - 1) / (2 * MM));
@@ -1210,7 +1216,7 @@ int mx_check(const uint8_t *W, const uint8_t *W_scales, const float *bias, const
 int mx_linear(const uint8_t *x, const uint8_t *x_scales, const void *rows, int64_t ld, int type,
               const uint8_t *W, const uint8_t *W_scales, const float *bias, const void *residual,
               int64_t ldr, int act, int T, int K, int N, void *y, int64_t ldy, int y_dtype,
-              uint32_t *status, cudaStream_t s)
+              uint32_t *status, cudaStream_t s, int stall = 0)
 {
     const int size = dtype_size(y_dtype);
     EpiArgs e = {};
@@ -1218,7 +1224,7 @@ int mx_linear(const uint8_t *x, const uint8_t *x_scales, const void *rows, int64
     e.ldr = ldr, e.ldo = ldy;
     e.f16 = y_dtype == MOE_DT_F16, e.out_f32 = y_dtype == MOE_DT_F32, e.act = act;
     e.vec_out = vec16(y, ldy, size), e.vec_res = vec16(residual, ldr, size);
-    const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status, rows, ld, type};
+    const MxProduct q{x, x_scales, W, W_scales, T, K, N, e, status, rows, ld, type, stall};
     return launch_mx(q, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1292,4 +1298,29 @@ extern "C" int moe_linear_rows_mxfp4(const void *x, int64_t ldx, int x_dtype, co
     return quantised != MOE_OK ? quantised
                                : mx_linear(codes, scales, nullptr, 0, 0, W, W_scales, bias, residual,
                                            ldr, act, T, K, N, y, ldy, y_dtype, status, s);
+}
+
+extern "C" int moe_selftest_linear_mxfp4_wait_limit(const void *x, const uint8_t *x_scales,
+                                                    const uint8_t *W, const uint8_t *W_scales,
+                                                    int T, int K, int N, void *y, int y_dtype,
+                                                    uint32_t *status, int cta, moe_stream_t stream)
+{
+    using namespace moe;
+    const int rc = mx_check(W, W_scales, nullptr, nullptr, 0, MOE_ACT_NONE, T, K, N, y, N, y_dtype,
+                            status);
+    if (rc != MOE_OK)
+        return rc;
+    if (T == 0 || cta < 0 || cta == INT_MAX ||
+        (!x_scales && moe_linear_rows_mxfp4_workspace_bytes(T, K, N)))
+        return MOE_ERR_SHAPE;
+    if (!x)
+        return MOE_ERR_NULL;
+    if (!aligned(x, x_scales ? 16 : 2) || !aligned(x_scales, 16))
+        return MOE_ERR_ALIGN;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return x_scales ? mx_linear(static_cast<const uint8_t *>(x), x_scales, nullptr, 0, 0, W,
+                                W_scales, nullptr, nullptr, 0, MOE_ACT_NONE, T, K, N, y, N, y_dtype,
+                                status, s, cta + 1)
+                    : mx_linear(nullptr, nullptr, x, K, MOE_DT_BF16, W, W_scales, nullptr, nullptr,
+                                0, MOE_ACT_NONE, T, K, N, y, N, y_dtype, status, s, cta + 1);
 }
