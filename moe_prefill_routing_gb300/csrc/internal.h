@@ -182,8 +182,9 @@ enum SmemSlot {
     kSlotLinearPairEnd = kSlotLinearPair + 3,
     kSlotLinearMx,  // + 1 for rows that the kernel quantises
     kSlotLinearMxEnd = kSlotLinearMx + 1,
-    kSlotLinearMxPair,  // + 6 per activation, + 3 for 256 columns, + 1 for fp16, + 2 for fp32
-    kSlotLinearMxPairEnd = kSlotLinearMxPair + 29,
+    // + 7 per activation, + 3 for 256 columns, + 1 for fp16, + 2 for fp32; + 6: cut sums
+    kSlotLinearMxPair,
+    kSlotLinearMxPairEnd = kSlotLinearMxPair + 34,
     kSlotCount
 };
 

@@ -31,12 +31,13 @@ constexpr int kMxScaleCols = 16;  // of tensor memory: two tiles of A's and two 
 
 // Stages of 256 of K, four MMAs each, that one accumulator sums; sums of more
 // are cut into chains that are added outside the tensor core, which adds with
-// truncation: sums of one sign over blocks of very different scales came out
-// 1.4e-7 of themselves low after 16 stages, so 6e-7 after 64.  16-bit outputs may
-// drift by a quarter of half a unit (see linear.cu).
+// truncation: a sum of one sign loses up to 2^-23 of itself in an MMA (measured over
+// blocks of very different scales: 2.4e-8, so 6.2e-6 after 64 stages and 1.5e-6 after
+// 16; blocks of like scales lose nothing, as their products have few bits).  16-bit
+// outputs may drift by a quarter of half a unit (see linear.cu).
 __host__ __device__ constexpr int mx_chain(bool f32, bool f16)
 {
-    return f32 ? 64 : f16 ? 256 : 2048;
+    return f32 ? 16 : f16 ? 256 : 2048;
 }
 
 struct MxArgs : EpiArgs {
@@ -432,7 +433,8 @@ __global__ void __launch_bounds__(kMxThreads)
 // 64 of K: each CTA loads its 128 rows of A and half the rows of B, the scales of
 // its own rows of A and those of all rows of B.  Pairs walk the tiles
 // (persistent); two accumulators let the epilogue warps work on one tile while
-// the MMAs fill the other.
+// the MMAs fill the other.  Sums that are cut (fp32 outputs) take them chain after
+// chain, and the epilogue warps add the chains up in registers.
 //
 // A stage's round trip, from its release to its next data's arrival, takes 1.14 us
 // however little is loaded, so it is spread over many stages (192 columns: six; 4096
@@ -614,11 +616,39 @@ struct MxBlock {
     }
 };
 
-// WIDE: tiles of 256 columns.
-template <int ACT, typename E, bool WIDE>
+// An epilogue warp's 64 columns of an accumulator, or (ADD) their sum with what it has,
+// eight at a time (with sixteen more registers spill: 4096 x 11264 x 2816 fp32 with a
+// residual 60.8 us instead of 57.4; uncut it would take 55.1).
+template <bool ADD>
+__device__ __forceinline__ void mx_take_columns(uint32_t from, uint32_t (&r0)[32],
+                                                uint32_t (&r1)[32])
+{
+    if (!ADD) {
+        tmem_ld_32x32b_x32(from, r0);
+        tmem_ld_32x32b_x32(from + 32, r1);
+        tmem_ld_wait();
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < kMxEpiCols; c += 8) {
+        uint32_t r[8];
+        tmem_ld_32x32b_x8(from + uint32_t(c), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t &sum = c < 32 ? r0[(c + j) & 31] : r1[(c + j) & 31];
+            sum = __float_as_uint(__uint_as_float(sum) + __uint_as_float(r[j]));
+        }
+    }
+}
+
+enum MxTiles { kNarrow, kCut, kWide };  // kCut: sums are cut into chains; kWide: 256 columns
+
+template <int ACT, typename E, MxTiles TILES>
 __global__ void __launch_bounds__(kMxPairThreads, 1)
     k_linear_mx_pair(const __grid_constant__ MxPairArgs g)
 {
+    constexpr bool WIDE = TILES == kWide, CUT = TILES == kCut;
     extern __shared__ uint8_t smem_raw[];
     // the same offset in both CTAs: dynamic shared memory starts at the same address
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -737,50 +767,57 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             uint32_t phase = 0, aphase = 0, set = 0;
             for (int t = pair; t < g.tiles; t += pairs) {
                 place(t, m0, n0);
-                if (!mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag))
-                    return;
-                // the other accumulator's shared columns: it was filled a tile ago
-                if (WIDE && t != pair &&
-                    !mbar_wait(&ctl.shared_read[buf ^ 1], buf ? aphase : aphase ^ 1u, abort_flag))
-                    return;
-                tc_fence_after_sync();
-                const uint32_t d = tmem_base + uint32_t(buf * mx_acc_step(bn));
-                const uint32_t b_col = uint32_t(n0 % 128) / 32;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait(&ctl.full[stage], phase, abort_flag))
+                int kb = 0;
+                do {  // a chain
+                    const int last = CUT ? min(kb + p.chain, nk) : nk;
+                    uint32_t some = 0;
+                    if (!mbar_wait(&ctl.acc_empty[buf], aphase ^ 1u, abort_flag))
+                        return;
+                    // the other accumulator's shared columns: it was filled a tile ago
+                    if (WIDE && t != pair &&
+                        !mbar_wait(&ctl.shared_read[buf ^ 1], buf ? aphase : aphase ^ 1u,
+                                   abort_flag))
                         return;
                     tc_fence_after_sync();
-                    const uint32_t off = uint32_t(stage) * (stage_bytes >> 4);
-                    uint64_t *const released = &ctl.empty[stage];
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    const uint32_t at = scales + set;
-                    set ^= kSet;
-                    tc_copy_32x128b_pair(at, smem_desc_at(ds0, off));
-                    tc_copy_32x128b_pair(at + 4, smem_desc_at(ds0, off + kTile));
+                    const uint32_t d = tmem_base + uint32_t(buf * mx_acc_step(bn));
+                    const uint32_t b_scales = 8 + uint32_t(n0 % 128) / 32;
+                    for (; kb < last; ++kb) {
+                        if (!mbar_wait(&ctl.full[stage], phase, abort_flag))
+                            return;
+                        tc_fence_after_sync();
+                        const uint32_t off = uint32_t(stage) * (stage_bytes >> 4);
+                        uint64_t *const released = &ctl.empty[stage];
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        const uint32_t at = scales + set;
+                        set ^= kSet;
+                        tc_copy_32x128b_pair(at, smem_desc_at(ds0, off));
+                        tc_copy_32x128b_pair(at + 4, smem_desc_at(ds0, off + kTile));
 #pragma unroll
-                    for (uint32_t i = 0; i < kB; ++i) {
-                        tc_copy_32x128b_pair(at + 8 + 4 * i,
-                                             smem_desc_at(ds0, off + (2 + 2 * i) * kTile));
-                        tc_copy_32x128b_pair(at + 8 + 4 * (kB + i),
-                                             smem_desc_at(ds0, off + (3 + 2 * i) * kTile));
-                    }
+                        for (uint32_t i = 0; i < kB; ++i) {
+                            tc_copy_32x128b_pair(at + 8 + 4 * i,
+                                                 smem_desc_at(ds0, off + (2 + 2 * i) * kTile));
+                            tc_copy_32x128b_pair(at + 8 + 4 * (kB + i),
+                                                 smem_desc_at(ds0, off + (3 + 2 * i) * kTile));
+                        }
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 4; ++kk)
-                        tc_mma_mxf4_pair(d, smem_desc_at(da0, off + 2 * kk),
-                                         smem_desc_at(db0, off + 2 * kk),
-                                         idesc | (kk & 1) << 5 | (kk & 1) << 30,
-                                         at + 4 * (kk >> 1), at + 8 + 4 * kB * (kk >> 1) + b_col,
-                                         kb != 0 || kk != 0);
-                    tc_commit_pair(released, 3);
-                }
-                tc_commit_pair(&ctl.acc_full[buf], 3);
-                if (++buf == 2) {
-                    buf = 0;
-                    aphase ^= 1u;
-                }
+                        for (uint32_t kk = 0; kk < 4; ++kk)
+                            tc_mma_mxf4_pair(d, smem_desc_at(da0, off + 2 * kk),
+                                             smem_desc_at(db0, off + 2 * kk),
+                                             idesc | (kk & 1) << 5 | (kk & 1) << 30,
+                                             at + 4 * (kk >> 1), at + b_scales + 4 * kB * (kk >> 1),
+                                             kk != 0 ? 1u : some);
+                        tc_commit_pair(released, 3);
+                        some = 1;
+                    }
+                    tc_commit_pair(&ctl.acc_full[buf], 3);
+                    if (++buf == 2) {
+                        buf = 0;
+                        aphase ^= 1u;
+                    }
+                } while (CUT && kb < nk);
             }
         };
         if (elect_one()) {
@@ -817,6 +854,29 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             const int64_t row = int64_t(m0) + q * 32;
             const int rows = int(min(int64_t(32), p.M - row));
             const int col = n0 + c0, width = min(kMxEpiCols, p.N - col);
+            uint32_t r0[32], r1[32];
+            if constexpr (CUT) {  // all chains but the last
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    r0[i] = r1[i] = 0u;
+                int chains = (nk - 1) / p.chain;
+                for (; chains > 0; --chains) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[buf], aphase, abort_flag)))
+                        break;
+                    tc_fence_after_sync();
+                    mx_take_columns<true>(lanes + uint32_t(buf * mx_acc_step(bn) + c0), r0, r1);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster_relaxed(dsmem_addr(&ctl.acc_empty[buf], 0));
+                    if (++buf == 2) {
+                        buf = 0;
+                        aphase ^= 1u;
+                    }
+                }
+                if (chains > 0)
+                    break;
+            }
             const E *res = static_cast<const E *>(p.residual) + (any_res ? row * p.ldr + col : 0);
             E *out = static_cast<E *>(p.out) + row * p.ldo + col;
             uint4 ahead[4] = {};
@@ -832,11 +892,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(&ctl.acc_full[buf], aphase, abort_flag)))
                 break;
             tc_fence_after_sync();
-            uint32_t r0[32], r1[32];
-            const uint32_t from = lanes + uint32_t(buf * mx_acc_step(bn) + c0);
-            tmem_ld_32x32b_x32(from, r0);
-            tmem_ld_32x32b_x32(from + 32, r1);
-            tmem_ld_wait();
+            mx_take_columns<CUT>(lanes + uint32_t(buf * mx_acc_step(bn) + c0), r0, r1);
             tc_fence_before_sync();  // these columns have been read
             __syncwarp();
             if (lane == 0) {
@@ -922,28 +978,31 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
 
 using MxPairKernel = void (*)(MxPairArgs);
 
-template <int ACT, bool WIDE>
+template <int ACT, MxTiles TILES>
 MxPairKernel mx_pair_kernel(bool f32, bool f16)
 {
-    return f32   ? k_linear_mx_pair<ACT, float, WIDE>
-           : f16 ? k_linear_mx_pair<ACT, __half, WIDE>
-                 : k_linear_mx_pair<ACT, __nv_bfloat16, WIDE>;
+    if constexpr (TILES == kCut)
+        return k_linear_mx_pair<ACT, float, kCut>;
+    else
+        return f32   ? k_linear_mx_pair<ACT, float, TILES>
+               : f16 ? k_linear_mx_pair<ACT, __half, TILES>
+                     : k_linear_mx_pair<ACT, __nv_bfloat16, TILES>;
 }
 
-template <bool WIDE>
+template <MxTiles TILES>
 MxPairKernel mx_pair_kernel(int act, bool f32, bool f16)
 {
     switch (act) {
     case MOE_ACT_RELU:
-        return mx_pair_kernel<MOE_ACT_RELU, WIDE>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_RELU, TILES>(f32, f16);
     case MOE_ACT_SILU:
-        return mx_pair_kernel<MOE_ACT_SILU, WIDE>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_SILU, TILES>(f32, f16);
     case MOE_ACT_GELU:
-        return mx_pair_kernel<MOE_ACT_GELU, WIDE>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_GELU, TILES>(f32, f16);
     case MOE_ACT_GELU_TANH:
-        return mx_pair_kernel<MOE_ACT_GELU_TANH, WIDE>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_GELU_TANH, TILES>(f32, f16);
     default:
-        return mx_pair_kernel<MOE_ACT_NONE, WIDE>(f32, f16);
+        return mx_pair_kernel<MOE_ACT_NONE, TILES>(f32, f16);
     }
 }
 
@@ -1099,10 +1158,13 @@ int mx_pair_columns(const MxProduct &q, int pairs)
         double round, stage;
     } kTimes[] = {{256, 2260, 540}, {192, 1800, 435}, {128, 1320, 390}, {64, 1050, 376}};
     const int nk = (q.K + MK - 1) / MK;
+    const bool cut = nk > mx_chain(q.epi.out_f32, q.epi.f16);
     const double part = (q.epi.residual ? 3500 : 1000) * (q.epi.out_f32 ? 2 : 1);
     int best = 0;
     double least = 0.0;
     for (const auto &w : kTimes) {
+        if (cut && w.bn == 256)
+            continue;
         const int64_t tiles = ((int64_t(q.T) + 255) / 256) * ((int64_t(q.N) + w.bn - 1) / w.bn);
         const double c = double((tiles + pairs - 1) / pairs) * (w.round + nk * w.stage) +
                          part * (w.bn > 192 ? 2 : 1);
@@ -1121,6 +1183,7 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
     MxArgs &a = g.p;
     static_cast<EpiArgs &>(a) = q.epi;
     a.status = q.status, a.stall = q.stall;
+    a.chain = mx_chain(a.out_f32, a.f16);
     a.M = q.T, a.N = q.N, a.K = q.K, a.k_tiles = mx_k_tiles(q.K);
     a.bn = mx_pair_columns(q, pairs);
     a.n_mt = int((int64_t(q.T) + 2 * MM - 1) / (2 * MM));
@@ -1140,13 +1203,15 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
         e = mx_scale_map(&g.b_scales, q.W_scales, q.N, q.K, mx_b_tiles(a.bn));
     if (e == cudaSuccess && a.vec_out)
         e = mx_out_map(&g.out, a);
-    const bool wide = a.bn == 256;
-    const void *kern =
-        reinterpret_cast<const void *>(wide ? mx_pair_kernel<true>(a.act, a.out_f32, a.f16)
-                                            : mx_pair_kernel<false>(a.act, a.out_f32, a.f16));
+    const MxTiles how = a.bn == 256 ? kWide : (q.K + MK - 1) / MK > a.chain ? kCut : kNarrow;
+    const auto kern = reinterpret_cast<const void *>(
+        how == kWide  ? mx_pair_kernel<kWide>(a.act, a.out_f32, a.f16)
+        : how == kCut ? mx_pair_kernel<kCut>(a.act, a.out_f32, a.f16)
+                      : mx_pair_kernel<kNarrow>(a.act, a.out_f32, a.f16));
     if (e == cudaSuccess)
         e = ensure_smem_limit(kern,
-                              kSlotLinearMxPair + 6 * a.act + 3 * wide + (a.out_f32 ? 2 : a.f16),
+                              kSlotLinearMxPair + 7 * a.act +
+                                  (how == kCut ? 6 : 3 * (how == kWide) + (a.out_f32 ? 2 : a.f16)),
                               kMxLoneSmem);
     if (e != cudaSuccess)
         return e;
@@ -1165,7 +1230,7 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
 bool mx_takes_pairs(const MxProduct &q)
 {
     const int nk = (q.K + MK - 1) / MK;
-    if (nk > mx_chain(q.epi.out_f32, q.epi.f16))  // the pairs' sums are not cut
+    if (!q.epi.out_f32 && nk > mx_chain(false, q.epi.f16))  // the pairs cut fp32 sums alone
         return false;
     if (q.T > 64)
         return true;
