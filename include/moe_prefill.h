@@ -743,7 +743,8 @@ MOE_API int moe_block_norm_grad(const void *xn, int64_t ldxn, int x_dtype, const
  * codes 0.  Scale bytes past the last row are written as 0 too.
  *
  * moe_dequantize_rows_mxfp4 -- y dtype [rows, K] (MOE_DT_BF16 or MOE_DT_F32,
- * which hold the values exactly), rows ldy elements apart.
+ * which hold the values exactly, but for those of S = 253 and 254 that are 2^128 or
+ * more and become infinite; the calls above write no such S), rows ldy elements apart.
  */
 MOE_API size_t moe_mxfp4_scale_bytes(int rows, int K);
 MOE_API int moe_quantize_rows_mxfp4(const void *x, int64_t ldx, int dtype, int rows, int K,
