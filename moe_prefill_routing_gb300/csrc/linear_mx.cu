@@ -1224,7 +1224,7 @@ cudaError_t launch_mx_pair(const MxProduct &q, cudaStream_t s)
 // takes them 2.3 us and 0.22 for each stage of its whole reduction however few
 // its rows are, where k_linear_mx splits the reduction eight ways at best and
 // joins the parts in 3 to 10 us that grow with the rows.  Measured (us, k_linear_mx
-// and pairs): 64 rows x 2560 x 10240 10.0 and 7.6, x 10240 x 2560 9.4 and 11.2, x
+// and pairs): 64 rows x 2560 x 10240 10.0 and 7.5 - 8.3, x 10240 x 2560 9.4 and 11.2, x
 // 11264 x 11264 (split by two) 23.0 and 17.3, x 512 x 2560 8.1 and 4.0; 128 x 10240
 // x 2560 14.5 and 11.5; 32 x 2560 x 2560 5.1 and 6.6, x 512 x 2560 6.2 and 4.0.
 bool mx_takes_pairs(const MxProduct &q)

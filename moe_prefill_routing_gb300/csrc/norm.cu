@@ -18,11 +18,13 @@
 // added, so that it does not overflow sooner than a thread's 8 to 32 squares (or
 // products) do.
 //
-// 32768 rows x 2816: bf16 125 us (738 MB, 5.9 TB/s), with MXFP4 rows 167, an fp32
-// stream 169 (6.55 TB/s); gradients 218 (1.1 GB, 5.1 TB/s) and, of an fp32 stream,
-// 256 (6.5 TB/s).  What bounds the 16-bit forms are instructions and their
+// 32768 rows x 2816: bf16 123 us (738 MB, 6.0 TB/s), with MXFP4 rows 165, an fp32
+// stream 168 (6.6 TB/s); gradients 217 (1.1 GB, 5.1 TB/s) and, of an fp32 stream,
+// 255 (6.5 TB/s).  What bounds the 16-bit forms are instructions and their
 // latencies: 60 % of the issue slots, in the gradients with 12 warps an SM.  2048 x
-// 2560: 10.5 us, with MXFP4 rows 13.8, gradients 20.9.
+// 2560 from memory: 12.8 us, with MXFP4 rows 15.3, gradients 21.2.  Rows too wide for
+// a ring are read where they are used: gradients of 16384 x 7168 with an fp32 stream
+// 567 us (3.7 TB/s), of 4096 x 16384 bf16 353 (2.3 TB/s).
 #include "../../include/moe_prefill.h"
 #include "internal.h"
 #include "mx_rows.cuh"
@@ -191,7 +193,7 @@ enum Mode {
 // in, one more to a warp than its elements fill, which the warp then shifts into
 // place; results leave through a slot, neighbouring words by neighbouring lanes.
 // (Element by element from the thread that uses them, 32768 x 2815 bf16 took 490 us
-// instead of 251, its gradients 1113 instead of 512; 1.9 and 2.3 times the aligned
+// instead of 248, its gradients 1113 instead of 519; 2.0 and 2.4 times the aligned
 // 2816's, from the instructions of the way through the slots.)
 template <typename E, int R, int MODE>
 struct Rows {
@@ -783,7 +785,7 @@ __global__ void __maxnreg__(R == 1 ? 96 : 128) k_block_norm_grad(const NormGradA
                 }
             }
             // (here, as the row's stores need not wait for the slope: 16384 x 7168 with an
-            // fp32 stream 573 us, ahead of them 640)
+            // fp32 stream 567 us, ahead of them 640)
             if (p.dgate && gr.t == 0)
                 p.dgate[t] = dgate * gate_slope(raw, p.sigmoid);
         } else {
