@@ -520,8 +520,9 @@ MOE_API int moe_read_status(const void *ws, moe_stream_t stream, uint32_t *statu
 /*
  * moe_take_status -- the status bits of the current device's moe_linear,
  * moe_linear_grad and moe_linear_mxfp4 calls that had no status word and
- * moe_route calls that had no workspace, on any stream, since they were last taken: copied to *status
- * and cleared, synchronising `stream` (order it behind the calls asked about).
+ * moe_route calls that had no workspace, on any stream, since they were last
+ * taken: copied to *status and cleared, synchronising `stream` (order it behind
+ * the calls asked about).
  */
 MOE_API int moe_take_status(moe_stream_t stream, uint32_t *status);
 
